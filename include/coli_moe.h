@@ -422,6 +422,133 @@ COLI_API coli_status coli_debug_fail_copies(int32_t n);
  * d_records. */
 COLI_API coli_status coli_debug_read_log(uint32_t* d_count, void* d_records, int32_t capacity);
 
+/* ------------------------------------------------------------ MXFP4 experts
+ * Microscaled 4-bit floating point, the format gfx950's matrix instructions
+ * multiply directly. A row of K values (K a positive multiple of 32) is K/2
+ * bytes of E2M1 codes (1 sign, 2 exponent and 1 mantissa bit: 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6; column 2i in bits 0-3 of byte i, 2i+1 in bits 4-7) and K/32
+ * bytes of scales, one per 32 columns: code c stands for 2^(c - 127), 255 for
+ * NaN. Rows of codes and of scales follow each other without gaps. Code
+ * buffers are 16-byte aligned, scale buffers need no alignment.
+ * The calls below are stateless, allocate nothing, use no workspace and may be
+ * captured into a HIP graph. Where a buffer is both read and written the
+ * comment says so; other buffers of a call must not overlap. */
+#define COLI_F32 0
+#define COLI_BF16 1
+#define COLI_F16 2
+#define COLI_MXFP4 3   /* as an output type of coli_mxfp4_swiglu */
+
+/* Quantise d_x [rows][cols] of type dtype (COLI_F32, COLI_BF16 or COLI_F16; row
+ * r starts ld elements after row r-1, ld >= cols) to d_q [rows][cols/2] and d_s
+ * [rows][cols/32]: the scale of a block is 2^(floor(log2(max |x|)) - 2), its
+ * code clamped to at least 0; values are x / scale rounded half to even to
+ * E2M1, saturated at +-6, signs kept (of zeros too). A block that holds an
+ * infinity or a NaN gets scale code 255 and codes 0: it reads back as NaN. */
+COLI_API coli_status coli_quantize_mxfp4(const void* d_x, int32_t dtype, int64_t rows, int64_t cols,
+                                         int64_t ld, uint8_t* d_q, uint8_t* d_s, void* stream);
+
+/* The values of d_q, d_s as d_x [rows][cols] (row stride ld): exact in f32 and
+ * bf16, rounded half to even (to infinity above its range) in f16. */
+COLI_API coli_status coli_dequantize_mxfp4(const uint8_t* d_q, const uint8_t* d_s, int64_t rows,
+                                           int64_t cols, void* d_x, int32_t dtype, int64_t ld,
+                                           void* stream);
+
+/* An expert in MXFP4 as one buffer (which the expert cache can place like any
+ * other blob): offsets (bytes) of the gate/up codes, down codes, gate/up
+ * scales, down scales, and the buffer's size. Gate and up rows are interleaved
+ * in blocks of 16 rows, as in the int4 blob: row r of gate is row 32 (r / 16) + r %
+ * 16 of the [2 inter][hidden] matrix, row r of up 16 rows later. group, topp,
+ * wbits and routed_scale of the shape are not used. Host-only arithmetic. */
+COLI_API coli_status coli_mxfp4_blob_layout(const coli_moe_shape* shape, size_t off[4],
+                                            size_t* blob_bytes);
+
+/* Quantise one expert's three matrices of type dtype (gate/up [inter][hidden],
+ * down [hidden][inter], without gaps) into such a buffer (16-byte aligned). */
+COLI_API coli_status coli_quantize_mxfp4_expert(const coli_moe_shape* shape, const void* d_gate,
+                                                const void* d_up, const void* d_down, int32_t dtype,
+                                                void* d_blob, void* stream);
+
+/* Grouped product: d_y[r][n] = sum_k a[r][k] w[n][k], n < N, for MXFP4 rows d_a
+ * [rows][K/2], d_as [rows][K/32] and the MXFP4 matrix w [N][K] of the row's
+ * expert. d_offsets [E+1] (device, ascending, as coli_moe_union gives it): rows
+ * d_offsets[e] .. d_offsets[e+1]-1 belong to expert e; rows from d_offsets[E] on
+ * are neither read nor written. d_offsets NULL: E is 1 and has every row.
+ * d_blob_table [E] (device): per expert the buffer that holds its matrix, codes
+ * at q_off (a multiple of 16, as the buffer's address) and scales at s_off.
+ * Entries of experts without rows are not read. d_y: type dtype (f32, bf16 or
+ * f16), row stride ld >= N. Products are exact, sums f32, the result rounded
+ * once; a row's result does not depend on the other rows' values. E <= 1024. */
+COLI_API coli_status coli_mxfp4_matmul(const uint8_t* d_a, const uint8_t* d_as, int32_t rows, int32_t K,
+                                       const int32_t* d_offsets, int32_t E,
+                                       const void* const* d_blob_table, size_t q_off, size_t s_off,
+                                       int32_t N, void* d_y, int32_t dtype, int64_t ld, void* stream);
+
+/* The gate/up product with SwiGLU, arguments as coli_mxfp4_matmul: with the
+ * expert's interleaved [2 inter][K] matrix, h[r][i] = silu(gate_i . a_r) *
+ * (up_i . a_r), i < inter (a positive multiple of 32). dtype f32, bf16 or f16:
+ * d_h [rows][ld], d_hs NULL. COLI_MXFP4: the f32 h is quantised in the same
+ * launch as coli_quantize_mxfp4 does, d_h [rows][inter/2] codes and d_hs
+ * [rows][inter/32] scales (ld is ignored): the input of the down product. */
+COLI_API coli_status coli_mxfp4_swiglu(const uint8_t* d_a, const uint8_t* d_as, int32_t rows, int32_t K,
+                                       const int32_t* d_offsets, int32_t E,
+                                       const void* const* d_blob_table, size_t q_off, size_t s_off,
+                                       int32_t inter, void* d_h, uint8_t* d_hs, int32_t dtype,
+                                       int64_t ld, void* stream);
+
+/* ------------------------------------------------------- token permutation
+ * The T tokens' rows in the experts' order and back, with gradients. d_inv [T][k]
+ * holds each assignment's row in that order; values outside [0, T*k) (-1 from
+ * coli_moe_union_inverse) mark slots without a row. No two slots may have the
+ * same row. Row buffers have T*k rows; rows that no slot has are neither read
+ * nor written. Every row stride is in elements and at least H. 1 <= k <= 1024,
+ * T*k < 2^31, H positive. Sums run in slot order in f32. */
+
+/* coli_moe_union that also writes the inverse of d_perm: d_inv [T][k], d_inv[a]
+ * = p where d_perm[p] = a, -1 where the entry belongs to no expert. The same
+ * arguments, limits and workspace otherwise; at most 1024 assignments take one
+ * launch. */
+COLI_API coli_status coli_moe_union_inverse(const int32_t* d_idx, int32_t T, int32_t k, int32_t E,
+                                            int32_t* d_counts, int32_t* d_offsets, int32_t* d_perm,
+                                            int32_t* d_unique, int32_t* d_n_unique, int32_t* d_inv,
+                                            void* d_ws, size_t ws_bytes, void* stream);
+
+/* d_rows[d_inv[t][j]] = d_x[t], d_x [T][H] and d_rows of type dtype, bit for bit. */
+COLI_API coli_status coli_moe_dispatch(const void* d_x, int32_t dtype, int32_t T, int32_t k, int32_t H,
+                                       int64_t ld_x, const int32_t* d_inv, void* d_rows,
+                                       int64_t ld_rows, void* stream);
+
+/* The same into MXFP4 rows d_q [T*k][H/2], d_s [T*k][H/32], each token quantised
+ * as by coli_quantize_mxfp4 (H a multiple of 32). */
+COLI_API coli_status coli_moe_dispatch_mxfp4(const void* d_x, int32_t dtype, int32_t T, int32_t k,
+                                             int32_t H, int64_t ld_x, const int32_t* d_inv,
+                                             uint8_t* d_q, uint8_t* d_s, void* stream);
+
+/* Gradient of coli_moe_dispatch: d_dx[t] = sum_j d_g[d_inv[t][j]] (0 for a token
+ * without rows). d_g has type g_dtype, d_dx type dtype. */
+COLI_API coli_status coli_moe_dispatch_bwd(const void* d_g, int32_t g_dtype, int64_t ld_g, int32_t T,
+                                           int32_t k, int32_t H, const int32_t* d_inv, void* d_dx,
+                                           int32_t dtype, int64_t ld_dx, void* stream);
+
+/* d_y[t] = d_shared[t] + scale * sum_j d_w[t][j] d_rows[d_inv[t][j]]. d_rows has
+ * type rows_dtype; d_shared (nullable: nothing is added) and d_y have type
+ * dtype, and may be the same buffer with the same stride. d_w [T][k] f32; the
+ * weight of a slot without a row is not used. scale must be finite. */
+COLI_API coli_status coli_moe_combine(const void* d_rows, int32_t rows_dtype, int64_t ld_rows,
+                                      int32_t T, int32_t k, int32_t H, const int32_t* d_inv,
+                                      const float* d_w, const void* d_shared, int64_t ld_shared,
+                                      float scale, void* d_y, int32_t dtype, int64_t ld_y,
+                                      void* stream);
+
+/* Gradients of coli_moe_combine for the output gradient d_dy [T][H] of type
+ * dy_dtype (which is also d_shared's gradient): d_drows[d_inv[t][j]] = scale *
+ * d_w[t][j] * d_dy[t] in the rows' type, and d_dw[t][j] = scale * <d_dy[t],
+ * d_rows[d_inv[t][j]]> (0 for a slot without a row). */
+COLI_API coli_status coli_moe_combine_bwd(const void* d_dy, int32_t dy_dtype, int64_t ld_dy,
+                                          const void* d_rows, int32_t rows_dtype, int64_t ld_rows,
+                                          int32_t T, int32_t k, int32_t H, const int32_t* d_inv,
+                                          const float* d_w, float scale, void* d_drows,
+                                          int64_t ld_drows, float* d_dw, void* stream);
+
 /* ---------------------------------------------------------- kernel timing
  * Optional HIP-event timing of the library's main kernels, recorded on the
  * stream each kernel runs on. coli_profile_enable(n) pre-creates n event

@@ -18,6 +18,7 @@ SO_PATH = os.path.join(HERE, "libcoli_moe.so")
 
 COLI_OK, COLI_EINVAL, COLI_EUNSUPPORTED, COLI_EHIP, COLI_ENOMEM, COLI_EBUSY = 0, -1, -2, -3, -4, -5
 PATH_AUTO, PATH_GEMV, PATH_MFMA = 0, 1, 2
+F32, BF16, F16, MXFP4 = 0, 1, 2, 3
 
 EXPORTED = [
     "coli_last_error", "coli_version", "coli_expert_blob_layout", "coli_quantize_int4",
@@ -33,6 +34,10 @@ EXPORTED = [
     "coli_moe_lookahead", "coli_debug_fail_copies", "coli_debug_read_log",
     "coli_profile_enable", "coli_profile_clear",
     "coli_profile_summary", "coli_profile_rerun", "coli_read_probe",
+    "coli_quantize_mxfp4", "coli_dequantize_mxfp4", "coli_mxfp4_blob_layout",
+    "coli_quantize_mxfp4_expert", "coli_mxfp4_matmul", "coli_mxfp4_swiglu",
+    "coli_moe_union_inverse", "coli_moe_dispatch", "coli_moe_dispatch_mxfp4",
+    "coli_moe_dispatch_bwd", "coli_moe_combine", "coli_moe_combine_bwd",
 ]
 
 
@@ -124,6 +129,22 @@ def lib():
             L.coli_profile_summary.argtypes = [ctypes.c_char_p, P(i64), P(ctypes.c_double)]
             L.coli_profile_rerun.argtypes = [P(Shape), i32, vp, vp, i32, vp, sz, vp]
             L.coli_read_probe.argtypes = [vp, sz, i32, i32, i32, vp, sz, vp]
+            L.coli_quantize_mxfp4.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
+            L.coli_dequantize_mxfp4.argtypes = [vp, vp, i64, i64, vp, i32, i64, vp]
+            L.coli_mxfp4_blob_layout.argtypes = [P(Shape), P(sz), P(sz)]
+            L.coli_quantize_mxfp4_expert.argtypes = [P(Shape), vp, vp, vp, i32, vp, vp]
+            L.coli_mxfp4_matmul.argtypes = [vp, vp, i32, i32, vp, i32, vp, sz, sz, i32, vp, i32, i64,
+                                            vp]
+            L.coli_mxfp4_swiglu.argtypes = [vp, vp, i32, i32, vp, i32, vp, sz, sz, i32, vp, vp, i32,
+                                            i64, vp]
+            L.coli_moe_union_inverse.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+            L.coli_moe_dispatch.argtypes = [vp, i32, i32, i32, i32, i64, vp, vp, i64, vp]
+            L.coli_moe_dispatch_mxfp4.argtypes = [vp, i32, i32, i32, i32, i64, vp, vp, vp, vp]
+            L.coli_moe_dispatch_bwd.argtypes = [vp, i32, i64, i32, i32, i32, vp, vp, i32, i64, vp]
+            L.coli_moe_combine.argtypes = [vp, i32, i64, i32, i32, i32, vp, vp, vp, i64, f32, vp, i32,
+                                           i64, vp]
+            L.coli_moe_combine_bwd.argtypes = [vp, i32, i64, vp, i32, i64, i32, i32, i32, vp, vp, f32,
+                                               vp, i64, vp, vp]
             _lib = L
     return _lib
 
@@ -458,6 +479,279 @@ def read_probe(src, pattern: int, row_bytes: int, rows_per_wg: int, sink, stream
     n = src.numel() if nbytes is None else nbytes
     _check(lib().coli_read_probe(_ptr(src), n, pattern, row_bytes, rows_per_wg, _ptr(sink),
                                  sink.numel() * sink.element_size(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- MXFP4 experts and token permutation
+def _dtype_code(dtype) -> int:
+    import torch
+    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(dtype)
+    if code is None:
+        raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+    return code
+
+
+def _rows(t, name, rows=None, cols=None, dtype=None):
+    """(type code, row stride) of a 2-d device tensor whose columns follow each
+    other; `rows` is a least number of rows, `cols` and `dtype` must be met."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-d with contiguous columns")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if (rows is not None and t.shape[0] < rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {cols})")
+    ld = t.stride(0)
+    if t.shape[0] <= 1:
+        ld = max(ld, t.shape[1])
+    elif ld < t.shape[1]:
+        raise ValueError(f"{name} has rows that overlap")
+    return _dtype_code(t.dtype), ld
+
+
+def _mx(q, s, name):
+    """(rows, cols) of an MXFP4 pair: codes uint8 [rows][cols/2], scales uint8 [rows][cols/32]."""
+    import torch
+    _need(q, torch.uint8, f"{name} codes")
+    _need(s, torch.uint8, f"{name} scales")
+    if q.dim() != 2 or s.dim() != 2 or s.shape[0] != q.shape[0] or q.shape[1] != 16 * s.shape[1]:
+        raise ValueError(f"{name}: codes {tuple(q.shape)} and scales {tuple(s.shape)} do not match")
+    return q.shape[0], 2 * q.shape[1]
+
+
+def _mx_out(q, s, rows, cols, device, name):
+    import torch
+    if cols % 32:
+        raise ValueError(f"{name}: the columns of MXFP4 rows must be a multiple of 32, got {cols}")
+    if q is None:
+        q = torch.empty((rows, cols // 2), dtype=torch.uint8, device=device)
+    if s is None:
+        s = torch.empty((rows, cols // 32), dtype=torch.uint8, device=device)
+    if _mx(q, s, name) != (rows, cols):
+        raise ValueError(f"{name}: codes must have shape ({rows}, {cols // 2})")
+    return q, s
+
+
+def _enqueue(tensors, stream, fn, *args):
+    """fn(*args, stream) on the tensors' device, on its current stream unless one is given."""
+    import torch
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: one device is needed")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream.cuda_stream)
+    if rc != COLI_OK:
+        _check(rc)
+
+
+def quantize_mxfp4(x, q=None, s=None, stream=None):
+    """Rows x [rows][cols] (float32, bfloat16 or float16) -> (codes uint8
+    [rows][cols/2], scales uint8 [rows][cols/32])."""
+    code, ld = _rows(x, "x")
+    rows, cols = x.shape
+    q, s = _mx_out(q, s, rows, cols, x.device, "quantize_mxfp4")
+    _enqueue((x, q, s), stream, lib().coli_quantize_mxfp4, x.data_ptr(), code, rows, cols, ld,
+             q.data_ptr(), s.data_ptr())
+    return q, s
+
+
+def dequantize_mxfp4(q, s, dtype=None, out=None, stream=None):
+    """The values of MXFP4 rows, in `out`'s type, else `dtype` (default float32)."""
+    import torch
+    rows, cols = _mx(q, s, "dequantize_mxfp4")
+    if out is None:
+        out = torch.empty((rows, cols), dtype=dtype or torch.float32, device=q.device)
+    code, ld = _rows(out, "out", rows, cols, dtype)
+    _enqueue((q, s, out), stream, lib().coli_dequantize_mxfp4, q.data_ptr(), s.data_ptr(), rows, cols,
+             out.data_ptr(), code, ld)
+    return out
+
+
+def mxfp4_blob_layout(shape: MoEShape):
+    """(offsets of the gate/up codes, down codes, gate/up scales, down scales; blob bytes)."""
+    off = (ctypes.c_size_t * 4)()
+    nb = ctypes.c_size_t()
+    _check(lib().coli_mxfp4_blob_layout(ctypes.byref(shape.c()), off, ctypes.byref(nb)))
+    return list(off), nb.value
+
+
+def quantize_mxfp4_expert(shape: MoEShape, gate, up, down, blob=None, stream=None):
+    """One expert's gate/up [inter][hidden] and down [hidden][inter] into an MXFP4 blob."""
+    import torch
+    H, I = shape.hidden, shape.inter
+    nbytes = mxfp4_blob_layout(shape)[1]
+    for t, n, want in ((gate, "gate", (I, H)), (up, "up", (I, H)), (down, "down", (H, I))):
+        _need(t, gate.dtype, n)
+        if tuple(t.shape) != want:
+            raise ValueError(f"{n} must have shape {want}")
+    if blob is None:
+        blob = torch.empty(nbytes, dtype=torch.uint8, device=gate.device)
+    _need(blob, torch.uint8, "blob")
+    if blob.numel() < nbytes:
+        raise ValueError(f"blob must hold {nbytes} bytes")
+    _enqueue((gate, up, down, blob), stream, lib().coli_quantize_mxfp4_expert, ctypes.byref(shape.c()),
+             gate.data_ptr(), up.data_ptr(), down.data_ptr(), _dtype_code(gate.dtype), blob.data_ptr())
+    return blob
+
+
+def _groups(table, offsets):
+    import torch
+    _need(table, torch.int64, "table")
+    _need(offsets, torch.int32, "offsets")
+    if offsets is not None and offsets.numel() != table.numel() + 1:
+        raise ValueError("offsets must hold one more value than the table")
+    return table.numel(), None if offsets is None else offsets.data_ptr()
+
+
+def mxfp4_matmul(a, a_s, table, n, q_off=0, s_off=0, offsets=None, dtype=None, out=None, stream=None):
+    """out[r] = W_e(r) a[r] for MXFP4 rows (a, a_s) sorted by expert. table: device
+    array (int64) of pointers to the experts' buffers, each with an MXFP4
+    [n][K] matrix: codes at q_off, scales at s_off. offsets [E + 1] as union
+    gives it (None: one matrix for every row). out in `dtype` (default float32)."""
+    import torch
+    rows, K = _mx(a, a_s, "a")
+    E, off = _groups(table, offsets)
+    if out is None:
+        out = torch.empty((rows, n), dtype=dtype or torch.float32, device=a.device)
+    code, ld = _rows(out, "out", rows, n, dtype)
+    _enqueue((a, a_s, table, offsets, out), stream, lib().coli_mxfp4_matmul, a.data_ptr(),
+             a_s.data_ptr(), rows, K, off, E, table.data_ptr(), q_off, s_off, n, out.data_ptr(), code, ld)
+    return out
+
+
+def mxfp4_swiglu(a, a_s, table, inter, q_off=0, s_off=0, offsets=None, dtype=None, out=None,
+                 stream=None):
+    """h[r] = silu(G_e(r) a[r]) * (U_e(r) a[r]), arguments as mxfp4_matmul with the
+    interleaved [2 inter][K] gate/up matrix. dtype "mxfp4" (or out a (codes,
+    scales) pair): h as MXFP4 rows, returned as that pair."""
+    import torch
+    rows, K = _mx(a, a_s, "a")
+    E, off = _groups(table, offsets)
+    if dtype == "mxfp4" or isinstance(out, (tuple, list)):
+        q, s = _mx_out(*(out or (None, None)), rows, inter, a.device, "mxfp4_swiglu")
+        out, h, hs, code, ld = (q, s), q, s.data_ptr(), MXFP4, inter
+    else:
+        if out is None:
+            out = torch.empty((rows, inter), dtype=dtype or torch.float32, device=a.device)
+        code, ld = _rows(out, "out", rows, inter, dtype)
+        h, hs, s = out, None, None
+    _enqueue((a, a_s, table, offsets, h, s), stream, lib().coli_mxfp4_swiglu, a.data_ptr(),
+             a_s.data_ptr(), rows, K, off, E, table.data_ptr(), q_off, s_off, inter, h.data_ptr(), hs,
+             code, ld)
+    return out
+
+
+def union_inverse(idx, E, stream=None):
+    """union, with each assignment's place in the experts' order: (counts, offsets,
+    perm, unique, n_unique, inv [T][k])."""
+    import torch
+    _need(idx, torch.int32, "idx")
+    T, k = idx.shape
+    n = T * k
+    nb = ctypes.c_size_t()
+    _check(lib().coli_moe_union_workspace_size(T, k, E, ctypes.byref(nb)))
+    buf = torch.empty(3 * E + 2 + 2 * n + (nb.value + 3) // 4, dtype=torch.int32, device=idx.device)
+    counts, offsets, perm, unique, n_unique, inv, ws = buf.split(
+        (E, E + 1, n, E, 1, n, (nb.value + 3) // 4))
+    base = buf.data_ptr()
+    at = [base + 4 * i for i in (0, E, 2 * E + 1, 2 * E + 1 + n, 3 * E + 1 + n, 3 * E + 2 + n,
+                                 3 * E + 2 + 2 * n)]
+    _enqueue((idx, buf), stream, lib().coli_moe_union_inverse, idx.data_ptr(), T, k, E, *at[:6], at[6],
+             nb.value)
+    return counts, offsets, perm, unique, n_unique, inv.view(T, k)
+
+
+def _slots(inv, w=None):
+    import torch
+    _need(inv, torch.int32, "inv")
+    _need(w, torch.float32, "w")
+    if inv.dim() != 2 or (w is not None and w.shape != inv.shape):
+        raise ValueError("inv must be [T][k], and w of the same shape")
+    return inv.shape
+
+
+def dispatch(x, inv, out=None, stream=None):
+    """out[inv[t, j]] = x[t]: the tokens' rows in the experts' order (rows of no
+    slot are left as they are)."""
+    import torch
+    T, k = _slots(inv)
+    code, ld = _rows(x, "x", T)
+    H = x.shape[1]
+    if out is None:
+        out = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
+    ld_out = _rows(out, "out", T * k, H, x.dtype)[1]
+    _enqueue((x, inv, out), stream, lib().coli_moe_dispatch, x.data_ptr(), code, T, k, H, ld,
+             inv.data_ptr(), out.data_ptr(), ld_out)
+    return out
+
+
+def dispatch_mxfp4(x, inv, q=None, s=None, stream=None):
+    """dispatch with the rows quantised on the way: (codes, scales) of T*k MXFP4 rows."""
+    T, k = _slots(inv)
+    code, ld = _rows(x, "x", T)
+    H = x.shape[1]
+    q, s = _mx_out(q, s, T * k, H, x.device, "dispatch_mxfp4")
+    _enqueue((x, inv, q, s), stream, lib().coli_moe_dispatch_mxfp4, x.data_ptr(), code, T, k, H, ld,
+             inv.data_ptr(), q.data_ptr(), s.data_ptr())
+    return q, s
+
+
+def dispatch_bwd(grad, inv, dtype=None, out=None, stream=None):
+    """dispatch's gradient: out[t] = sum_j grad[inv[t, j]], in `dtype` (default grad's)."""
+    import torch
+    T, k = _slots(inv)
+    g_code, ld_g = _rows(grad, "grad", T * k)
+    H = grad.shape[1]
+    if out is None:
+        out = torch.empty((T, H), dtype=dtype or grad.dtype, device=grad.device)
+    code, ld = _rows(out, "out", T, H, dtype)
+    _enqueue((grad, inv, out), stream, lib().coli_moe_dispatch_bwd, grad.data_ptr(), g_code, ld_g, T, k,
+             H, inv.data_ptr(), out.data_ptr(), code, ld)
+    return out
+
+
+def combine(rows, inv, w, shared=None, scale=1.0, dtype=None, out=None, stream=None):
+    """out[t] = shared[t] + scale * sum_j w[t, j] * rows[inv[t, j]], in `dtype`
+    (default: shared's type, else the rows'). out may be shared."""
+    import torch
+    T, k = _slots(inv, w)
+    r_code, ld_r = _rows(rows, "rows", T * k)
+    H = rows.shape[1]
+    if out is None:
+        out = torch.empty((T, H), dtype=dtype or (rows if shared is None else shared).dtype,
+                          device=rows.device)
+    code, ld = _rows(out, "out", T, H, dtype)
+    ld_s = ld if shared is None else _rows(shared, "shared", T, H, out.dtype)[1]
+    _enqueue((rows, inv, w, shared, out), stream, lib().coli_moe_combine, rows.data_ptr(), r_code, ld_r,
+             T, k, H, inv.data_ptr(), w.data_ptr(), None if shared is None else shared.data_ptr(), ld_s,
+             scale, out.data_ptr(), code, ld)
+    return out
+
+
+def combine_bwd(grad, rows, inv, w, scale=1.0, rows_grad=None, w_grad=None, stream=None):
+    """combine's gradients for the output gradient `grad` (which is shared's own
+    gradient): (rows_grad in the rows' type and order, w_grad [T][k])."""
+    import torch
+    T, k = _slots(inv, w)
+    r_code, ld_r = _rows(rows, "rows", T * k)
+    H = rows.shape[1]
+    g_code, ld_g = _rows(grad, "grad", T, H)
+    if rows_grad is None:
+        rows_grad = torch.empty_like(rows, memory_format=torch.contiguous_format)
+    if w_grad is None:
+        w_grad = torch.empty_like(w)
+    _slots(inv, w_grad)
+    ld_rg = _rows(rows_grad, "rows_grad", T * k, H, rows.dtype)[1]
+    _enqueue((grad, rows, inv, w, rows_grad, w_grad), stream, lib().coli_moe_combine_bwd,
+             grad.data_ptr(), g_code, ld_g, rows.data_ptr(), r_code, ld_r, T, k, H, inv.data_ptr(),
+             w.data_ptr(), scale, rows_grad.data_ptr(), ld_rg, w_grad.data_ptr())
+    return rows_grad, w_grad
 
 
 class ExpertCache:

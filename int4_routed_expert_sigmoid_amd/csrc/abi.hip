@@ -2,6 +2,7 @@
 // sequence of each call (include/coli_moe.h documents every entry point).
 #include <algorithm>
 #include <exception>
+#include <initializer_list>
 #include <mutex>
 #include <new>
 #include <string>
@@ -9,6 +10,7 @@
 #include "common.h"
 #include "gemm.h"
 #include "layer.h"
+#include "mxfp4.h"
 #include "quant.h"
 
 namespace coli {
@@ -390,6 +392,235 @@ coli_status coli_moe_lookahead(const coli_moe_shape* shape, const float* d_x, in
     if (!d_ws || ws_bytes < W.bytes) return fail(COLI_ENOMEM, "lookahead: workspace too small");
     return run_lookahead(shape, d_x, T, d_logits, d_router_w, d_bias, cache, layer, h_started,
                          (uint8_t*)d_ws, W, (hipStream_t)stream);
+    COLI_GUARD_END
+}
+
+// ------------------------------------------------------------ MXFP4 experts
+static bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+static coli_status check_mx_rows(const char* what, int64_t rows, int64_t cols, int32_t dtype, int64_t ld) {
+    if (rows < 0 || cols <= 0 || cols % kMxBlock)
+        return fail(COLI_EINVAL, std::string(what) + ": rows >= 0, cols a positive multiple of 32");
+    if (!elem_dtype(dtype)) return fail(COLI_EUNSUPPORTED, std::string(what) + ": dtype must be f32, bf16 or f16");
+    if (ld < cols) return fail(COLI_EINVAL, std::string(what) + ": ld below cols");
+    if (rows > 0 && (ld > (int64_t(1) << 56) / rows || cols > (int64_t(1) << 56) / rows))
+        return fail(COLI_EUNSUPPORTED, std::string(what) + ": too large");
+    return COLI_OK;
+}
+
+coli_status coli_quantize_mxfp4(const void* d_x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
+                                uint8_t* d_q, uint8_t* d_s, void* stream) {
+    COLI_GUARD_BEGIN
+    coli_status st = check_mx_rows("quantize_mxfp4", rows, cols, dtype, ld);
+    if (st) return st;
+    if (rows == 0) return COLI_OK;
+    if (!d_x || !d_q || !d_s) return fail(COLI_EINVAL, "quantize_mxfp4: NULL pointer");
+    if (!aligned16(d_q)) return fail(COLI_EINVAL, "quantize_mxfp4: codes must be 16-byte aligned");
+    return launch_quantize_mxfp4(d_x, dtype, rows, cols, ld, d_q, d_s, -1, (hipStream_t)stream);
+    COLI_GUARD_END
+}
+
+coli_status coli_dequantize_mxfp4(const uint8_t* d_q, const uint8_t* d_s, int64_t rows, int64_t cols,
+                                  void* d_x, int32_t dtype, int64_t ld, void* stream) {
+    COLI_GUARD_BEGIN
+    coli_status st = check_mx_rows("dequantize_mxfp4", rows, cols, dtype, ld);
+    if (st) return st;
+    if (rows == 0) return COLI_OK;
+    if (!d_x || !d_q || !d_s) return fail(COLI_EINVAL, "dequantize_mxfp4: NULL pointer");
+    if (!aligned16(d_q)) return fail(COLI_EINVAL, "dequantize_mxfp4: codes must be 16-byte aligned");
+    return launch_dequantize_mxfp4(d_q, d_s, rows, cols, d_x, dtype, ld, (hipStream_t)stream);
+    COLI_GUARD_END
+}
+
+struct MxBlobLayout {
+    size_t gu_q, down_q, gu_s, down_s, bytes;
+};
+
+static MxBlobLayout mx_blob_layout(size_t H, size_t I) {
+    MxBlobLayout L;
+    L.gu_q = 0;
+    L.down_q = align256(L.gu_q + 2 * I * (H / 2));
+    L.gu_s = align256(L.down_q + H * (I / 2));
+    L.down_s = align256(L.gu_s + 2 * I * (H / kMxBlock));
+    L.bytes = align256(L.down_s + H * (I / kMxBlock));
+    return L;
+}
+
+coli_status coli_mxfp4_blob_layout(const coli_moe_shape* shape, size_t off[4], size_t* blob_bytes) {
+    COLI_GUARD_BEGIN
+    coli_status st = check_shape(shape);
+    if (st) return st;
+    if (!off || !blob_bytes) return fail(COLI_EINVAL, "off or blob_bytes is NULL");
+    const MxBlobLayout L = mx_blob_layout(shape->hidden, shape->inter);
+    off[0] = L.gu_q; off[1] = L.down_q; off[2] = L.gu_s; off[3] = L.down_s;
+    *blob_bytes = L.bytes;
+    return COLI_OK;
+    COLI_GUARD_END
+}
+
+coli_status coli_quantize_mxfp4_expert(const coli_moe_shape* shape, const void* d_gate, const void* d_up,
+                                       const void* d_down, int32_t dtype, void* d_blob, void* stream) {
+    COLI_GUARD_BEGIN
+    coli_status st = check_shape(shape);
+    if (st) return st;
+    if (!elem_dtype(dtype)) return fail(COLI_EUNSUPPORTED, "quantize_mxfp4_expert: dtype must be f32, bf16 or f16");
+    if (!d_gate || !d_up || !d_down || !d_blob) return fail(COLI_EINVAL, "quantize_mxfp4_expert: NULL pointer");
+    if (!aligned16(d_blob)) return fail(COLI_EINVAL, "quantize_mxfp4_expert: the blob must be 16-byte aligned");
+    const int64_t H = shape->hidden, I = shape->inter;
+    const MxBlobLayout L = mx_blob_layout(H, I);
+    uint8_t* b = (uint8_t*)d_blob;
+    hipStream_t s = (hipStream_t)stream;
+    if ((st = launch_quantize_mxfp4(d_gate, dtype, I, H, H, b + L.gu_q, b + L.gu_s, 0, s))) return st;
+    if ((st = launch_quantize_mxfp4(d_up, dtype, I, H, H, b + L.gu_q, b + L.gu_s, kGuBlock, s))) return st;
+    return launch_quantize_mxfp4(d_down, dtype, H, I, I, b + L.down_q, b + L.down_s, -1, s);
+    COLI_GUARD_END
+}
+
+static coli_status mx_product(const char* what, const uint8_t* d_a, const uint8_t* d_as, int32_t rows,
+                              int32_t K, const int32_t* d_offsets, int32_t E,
+                              const void* const* d_blob_table, size_t q_off, size_t s_off, int64_t N,
+                              bool swiglu, void* d_y, uint8_t* d_ys, int32_t dtype, int64_t ld,
+                              void* stream) {
+    const std::string w(what);
+    const int64_t n_out = swiglu ? N / 2 : N;
+    if (rows < 0 || K <= 0 || K % kMxBlock) return fail(COLI_EINVAL, w + ": rows >= 0, K a positive multiple of 32");
+    if (n_out <= 0 || (swiglu && n_out % kMxBlock))
+        return fail(COLI_EINVAL, w + (swiglu ? ": inter must be a positive multiple of 32" : ": N must be positive"));
+    if (N > INT32_MAX - 4096) return fail(COLI_EUNSUPPORTED, w + ": matrix too large");
+    if (E < 1) return fail(COLI_EINVAL, w + ": E must be at least 1");
+    if (E > 1024) return fail(COLI_EUNSUPPORTED, w + ": E must be at most 1024");
+    if (!d_offsets && E != 1) return fail(COLI_EINVAL, w + ": without offsets E must be 1");
+    const bool mx = swiglu && dtype == COLI_MXFP4;
+    if (!mx && !elem_dtype(dtype)) return fail(COLI_EUNSUPPORTED, w + ": output type not supported");
+    if (!mx && ld < n_out) return fail(COLI_EINVAL, w + ": ld below the output's columns");
+    if (!mx && ld > (int64_t(1) << 56) / std::max(1, rows)) return fail(COLI_EUNSUPPORTED, w + ": ld too large");
+    if (q_off % 16) return fail(COLI_EINVAL, w + ": q_off must be a multiple of 16");
+    if (rows == 0) return COLI_OK;
+    if (!d_a || !d_as || !d_blob_table || !d_y || (mx && !d_ys)) return fail(COLI_EINVAL, w + ": NULL pointer");
+    if (!aligned16(d_a) || (mx && !aligned16(d_y))) return fail(COLI_EINVAL, w + ": codes must be 16-byte aligned");
+    MxGemmArgs a;
+    a.a = d_a; a.as = d_as; a.offsets = d_offsets; a.table = d_blob_table;
+    a.q_off = q_off; a.s_off = s_off; a.y = d_y; a.ys = d_ys; a.ld = ld;
+    a.rows = rows; a.K = K; a.E = E; a.N = (int32_t)N;
+    return launch_mxfp4_gemm(a, swiglu, dtype, (hipStream_t)stream);
+}
+
+coli_status coli_mxfp4_matmul(const uint8_t* d_a, const uint8_t* d_as, int32_t rows, int32_t K,
+                              const int32_t* d_offsets, int32_t E, const void* const* d_blob_table,
+                              size_t q_off, size_t s_off, int32_t N, void* d_y, int32_t dtype,
+                              int64_t ld, void* stream) {
+    COLI_GUARD_BEGIN
+    return mx_product("mxfp4_matmul", d_a, d_as, rows, K, d_offsets, E, d_blob_table, q_off, s_off, N,
+                      false, d_y, nullptr, dtype, ld, stream);
+    COLI_GUARD_END
+}
+
+coli_status coli_mxfp4_swiglu(const uint8_t* d_a, const uint8_t* d_as, int32_t rows, int32_t K,
+                              const int32_t* d_offsets, int32_t E, const void* const* d_blob_table,
+                              size_t q_off, size_t s_off, int32_t inter, void* d_h, uint8_t* d_hs,
+                              int32_t dtype, int64_t ld, void* stream) {
+    COLI_GUARD_BEGIN
+    return mx_product("mxfp4_swiglu", d_a, d_as, rows, K, d_offsets, E, d_blob_table, q_off, s_off,
+                      2 * (int64_t)inter, true, d_h, d_hs, dtype, ld, stream);
+    COLI_GUARD_END
+}
+
+// ------------------------------------------------------- token permutation
+coli_status coli_moe_union_inverse(const int32_t* d_idx, int32_t T, int32_t k, int32_t E, int32_t* d_counts,
+                                   int32_t* d_offsets, int32_t* d_perm, int32_t* d_unique,
+                                   int32_t* d_n_unique, int32_t* d_inv, void* d_ws, size_t ws_bytes,
+                                   void* stream) {
+    COLI_GUARD_BEGIN
+    if (T < 0 || k <= 0 || E <= 0) return fail(COLI_EINVAL, "union_inverse: bad sizes");
+    if (E > 1024) return fail(COLI_EUNSUPPORTED, "union_inverse: E <= 1024");
+    if ((int64_t)T * k > (1 << 26)) return fail(COLI_EUNSUPPORTED, "union_inverse: T*k too large");
+    if (!d_counts || !d_offsets || !d_unique || !d_n_unique || (T > 0 && (!d_idx || !d_perm || !d_inv)))
+        return fail(COLI_EINVAL, "union_inverse: NULL pointer");
+    if (ws_bytes < union_ws_bytes(T, k, E) || !d_ws) return fail(COLI_ENOMEM, "union_inverse: workspace too small");
+    return launch_union(d_idx, T, k, E, d_counts, d_offsets, d_perm, d_unique, d_n_unique, d_ws,
+                        (hipStream_t)stream, d_inv);
+    COLI_GUARD_END
+}
+
+static coli_status check_permute(const char* what, int32_t T, int32_t k, int32_t H, int32_t dtype,
+                                 int32_t dtype2, std::initializer_list<int64_t> lds) {
+    const std::string w(what);
+    if (T < 0 || k <= 0 || H <= 0) return fail(COLI_EINVAL, w + ": need T >= 0, k > 0, H > 0");
+    if (k > 1024 || (int64_t)T * k > INT32_MAX) return fail(COLI_EUNSUPPORTED, w + ": k <= 1024 and T*k < 2^31");
+    if (H > (1 << 28)) return fail(COLI_EUNSUPPORTED, w + ": H <= 2^28");
+    if (!elem_dtype(dtype) || !elem_dtype(dtype2)) return fail(COLI_EUNSUPPORTED, w + ": dtype must be f32, bf16 or f16");
+    for (int64_t ld : lds) {
+        if (ld < H) return fail(COLI_EINVAL, w + ": row stride below H");
+        if (ld > int64_t(1) << 28) return fail(COLI_EUNSUPPORTED, w + ": row stride above 2^28");
+    }
+    return COLI_OK;
+}
+
+coli_status coli_moe_dispatch(const void* d_x, int32_t dtype, int32_t T, int32_t k, int32_t H, int64_t ld_x,
+                              const int32_t* d_inv, void* d_rows, int64_t ld_rows, void* stream) {
+    COLI_GUARD_BEGIN
+    coli_status st = check_permute("dispatch", T, k, H, dtype, dtype, {ld_x, ld_rows});
+    if (st || T == 0) return st;
+    if (!d_x || !d_inv || !d_rows) return fail(COLI_EINVAL, "dispatch: NULL pointer");
+    return launch_dispatch(d_x, dtype, T, k, H, ld_x, d_inv, d_rows, ld_rows, (hipStream_t)stream);
+    COLI_GUARD_END
+}
+
+coli_status coli_moe_dispatch_mxfp4(const void* d_x, int32_t dtype, int32_t T, int32_t k, int32_t H,
+                                    int64_t ld_x, const int32_t* d_inv, uint8_t* d_q, uint8_t* d_s,
+                                    void* stream) {
+    COLI_GUARD_BEGIN
+    coli_status st = check_permute("dispatch_mxfp4", T, k, H, dtype, dtype, {ld_x});
+    if (st) return st;
+    if (H % kMxBlock) return fail(COLI_EINVAL, "dispatch_mxfp4: H must be a multiple of 32");
+    if (T == 0) return COLI_OK;
+    if (!d_x || !d_inv || !d_q || !d_s) return fail(COLI_EINVAL, "dispatch_mxfp4: NULL pointer");
+    if (!aligned16(d_q)) return fail(COLI_EINVAL, "dispatch_mxfp4: codes must be 16-byte aligned");
+    return launch_dispatch_mxfp4(d_x, dtype, T, k, H, ld_x, d_inv, d_q, d_s, (hipStream_t)stream);
+    COLI_GUARD_END
+}
+
+coli_status coli_moe_dispatch_bwd(const void* d_g, int32_t g_dtype, int64_t ld_g, int32_t T, int32_t k,
+                                  int32_t H, const int32_t* d_inv, void* d_dx, int32_t dtype,
+                                  int64_t ld_dx, void* stream) {
+    COLI_GUARD_BEGIN
+    coli_status st = check_permute("dispatch_bwd", T, k, H, g_dtype, dtype, {ld_g, ld_dx});
+    if (st || T == 0) return st;
+    if (!d_g || !d_inv || !d_dx) return fail(COLI_EINVAL, "dispatch_bwd: NULL pointer");
+    return launch_dispatch_bwd(d_g, g_dtype, ld_g, T, k, H, d_inv, d_dx, dtype, ld_dx, (hipStream_t)stream);
+    COLI_GUARD_END
+}
+
+static bool finite_scale(float s) { return s == s && s <= 3.4e38f && s >= -3.4e38f; }
+
+coli_status coli_moe_combine(const void* d_rows, int32_t rows_dtype, int64_t ld_rows, int32_t T, int32_t k,
+                             int32_t H, const int32_t* d_inv, const float* d_w, const void* d_shared,
+                             int64_t ld_shared, float scale, void* d_y, int32_t dtype, int64_t ld_y,
+                             void* stream) {
+    COLI_GUARD_BEGIN
+    coli_status st = check_permute("combine", T, k, H, rows_dtype, dtype,
+                                   {ld_rows, ld_y, d_shared ? ld_shared : ld_y});
+    if (st) return st;
+    if (!finite_scale(scale)) return fail(COLI_EINVAL, "combine: scale must be finite");
+    if (T == 0) return COLI_OK;
+    if (!d_rows || !d_inv || !d_w || !d_y) return fail(COLI_EINVAL, "combine: NULL pointer");
+    return launch_combine_rows(d_rows, rows_dtype, ld_rows, T, k, H, d_inv, d_w, d_shared, ld_shared, scale,
+                               d_y, dtype, ld_y, (hipStream_t)stream);
+    COLI_GUARD_END
+}
+
+coli_status coli_moe_combine_bwd(const void* d_dy, int32_t dy_dtype, int64_t ld_dy, const void* d_rows,
+                                 int32_t rows_dtype, int64_t ld_rows, int32_t T, int32_t k, int32_t H,
+                                 const int32_t* d_inv, const float* d_w, float scale, void* d_drows,
+                                 int64_t ld_drows, float* d_dw, void* stream) {
+    COLI_GUARD_BEGIN
+    coli_status st = check_permute("combine_bwd", T, k, H, dy_dtype, rows_dtype, {ld_dy, ld_rows, ld_drows});
+    if (st) return st;
+    if (!finite_scale(scale)) return fail(COLI_EINVAL, "combine_bwd: scale must be finite");
+    if (T == 0) return COLI_OK;
+    if (!d_dy || !d_rows || !d_inv || !d_w || !d_drows || !d_dw) return fail(COLI_EINVAL, "combine_bwd: NULL pointer");
+    return launch_combine_bwd(d_dy, dy_dtype, ld_dy, d_rows, rows_dtype, ld_rows, T, k, H, d_inv, d_w, scale,
+                              d_drows, ld_drows, d_dw, (hipStream_t)stream);
     COLI_GUARD_END
 }
 

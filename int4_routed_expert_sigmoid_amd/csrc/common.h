@@ -666,7 +666,7 @@ coli_status launch_route(const float* logits, const float* bias, int32_t T, int3
 size_t union_ws_bytes(int32_t T, int32_t k, int32_t E);
 coli_status launch_union(const int32_t* idx, int32_t T, int32_t k, int32_t E, int32_t* counts,
                          int32_t* offsets, int32_t* perm, int32_t* unique, int32_t* n_unique,
-                         void* ws, hipStream_t stream);
+                         void* ws, hipStream_t stream, int32_t* inv = nullptr);
 // Work list from a union: items [max_items], *n_items, rows_tok/rows_out
 // [T*k + T]. With a shared blob, item 0 is the shared expert over all T
 // tokens (output rows T*k + t). `phase_mask` (nullable, [E]) keeps only

@@ -23,6 +23,8 @@ namespace {
 constexpr int kUnionThreads = 1024;
 constexpr int kSlab = kUnionThreads;           // assignments per slab
 constexpr int kSlabWaves = kSlab / 64;
+// Experts whose per-wave counts and the scan's 16 words fit 64 KiB of LDS.
+constexpr int kSmallExperts = 65536 / (4 * kSlabWaves) - 16;
 
 __device__ __forceinline__ int block_exclusive_scan(int v, int* sh, int* total) {
     // Hillis-Steele over 1024 threads; sh has 1024 ints.
@@ -121,11 +123,88 @@ __global__ __launch_bounds__(kUnionThreads) void union_scan_kernel(
 __global__ __launch_bounds__(kUnionThreads) void union_scatter_kernel(
     const int32_t* __restrict__ idx, int n, int E, const int32_t* __restrict__ slab_cnt,
     const int32_t* __restrict__ rank, const int32_t* __restrict__ offsets,
-    int32_t* __restrict__ perm) {
+    int32_t* __restrict__ perm, int32_t* __restrict__ inv /* [n] or nullptr */) {
     const int a = blockIdx.x * kSlab + threadIdx.x;
     const int e = valid_expert(idx, a, n, E);
-    if (e < 0) return;
-    perm[offsets[e] + slab_cnt[(int64_t)blockIdx.x * E + e] + rank[a]] = a;
+    if (e < 0) {
+        if (inv != nullptr && a < n) inv[a] = -1;
+        return;
+    }
+    const int at = offsets[e] + slab_cnt[(int64_t)blockIdx.x * E + e] + rank[a];
+    perm[at] = a;
+    if (inv != nullptr) inv[a] = at;
+}
+
+// All three passes and the inverse for at most one slab, in one workgroup: the
+// counts stay in LDS, and one scan over the experts carries both the counts
+// (low half) and the number of experts used (high half; both at most 1024).
+// Dynamic LDS: kSlabWaves * E ints.
+__global__ __launch_bounds__(kUnionThreads) void union_small_kernel(
+    const int32_t* __restrict__ idx, int n, int E, int32_t* __restrict__ counts,
+    int32_t* __restrict__ offsets, int32_t* __restrict__ perm, int32_t* __restrict__ unique,
+    int32_t* __restrict__ n_unique, int32_t* __restrict__ inv) {
+    extern __shared__ int s_cnt[];               // [wave][E]: counts, then exclusive prefixes
+    __shared__ int s_wave[kSlabWaves];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int e = valid_expert(idx, t, n, E);
+    for (int i = t; i < kSlabWaves * E; i += kUnionThreads) s_cnt[i] = 0;
+    __syncthreads();
+    int r = 0;
+    unsigned long long active = __ballot(e >= 0);
+    while (active) {
+        const int leader = __ffsll((long long)active) - 1;
+        const int v = __shfl(e, leader);
+        const unsigned long long m = __ballot(e == v) & active;
+        if (e == v) r = __popcll(m & ((1ull << lane) - 1ull));
+        if (lane == leader) s_cnt[wave * E + v] = __popcll(m);
+        active &= ~m;
+    }
+    __syncthreads();
+    int cnt = 0;
+    if (t < E) {
+#pragma unroll
+        for (int w = 0; w < kSlabWaves; ++w) {
+            const int v = s_cnt[w * E + t];
+            s_cnt[w * E + t] = cnt;
+            cnt += v;
+        }
+        counts[t] = cnt;
+    }
+    const int own = cnt | (cnt > 0 ? 1 << 16 : 0);
+    int incl = own;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 63) s_wave[wave] = incl;
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kSlabWaves; ++w) {
+        before += w < wave ? s_wave[w] : 0;
+        total += s_wave[w];
+    }
+    const int excl = before + incl - own;
+    if (t < E) {
+        const int off = excl & 0xffff;
+        offsets[t] = off;
+#pragma unroll
+        for (int w = 0; w < kSlabWaves; ++w) s_cnt[w * E + t] += off;
+        if (cnt > 0) unique[excl >> 16] = t;
+    }
+    if (t == 0) {
+        offsets[E] = total & 0xffff;
+        *n_unique = total >> 16;
+    }
+    __syncthreads();
+    if (e >= 0) {
+        const int at = s_cnt[wave * E + e] + r;
+        perm[at] = t;
+        inv[t] = at;
+    } else if (t < n) {
+        inv[t] = -1;
+    }
 }
 
 // Work list for the FFN kernels: optional shared expert first, then the
@@ -203,8 +282,15 @@ size_t union_ws_bytes(int32_t T, int32_t k, int32_t E) {
 
 coli_status launch_union(const int32_t* idx, int32_t T, int32_t k, int32_t E, int32_t* counts,
                          int32_t* offsets, int32_t* perm, int32_t* unique, int32_t* n_unique,
-                         void* ws, hipStream_t stream) {
+                         void* ws, hipStream_t stream, int32_t* inv) {
     const int n = T * k;
+    if (inv != nullptr && n <= kSlab && E <= kSmallExperts) {
+        launch(union_small_kernel, dim3(1), dim3(kUnionThreads),
+               (size_t)kSlabWaves * E * 4, stream, idx, n, E, counts, offsets, perm, unique,
+               n_unique, inv);
+        COLI_CHECK_LAUNCH("union small kernel launch");
+        return COLI_OK;
+    }
     const int S = (n + kSlab - 1) / kSlab;
     int32_t* slab_cnt = (int32_t*)ws;
     int32_t* rank = (int32_t*)((char*)ws + align256((size_t)S * E * 4));
@@ -218,7 +304,7 @@ coli_status launch_union(const int32_t* idx, int32_t T, int32_t k, int32_t E, in
     COLI_CHECK_LAUNCH("union scan kernel launch");
     if (S > 0) {
         launch(union_scatter_kernel, dim3(S), dim3(kUnionThreads), 0, stream, idx, n, E, slab_cnt,
-               rank, offsets, perm);
+               rank, offsets, perm, inv);
         COLI_CHECK_LAUNCH("union scatter kernel launch");
     }
     return COLI_OK;
