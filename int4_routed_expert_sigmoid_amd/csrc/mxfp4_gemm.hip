@@ -101,6 +101,13 @@ __device__ __forceinline__ bool find_unit(const int32_t* offsets, int E, int R, 
 struct __attribute__((packed, aligned(1))) Bytes16 {
     uint32_t w[4];
 };
+// Blob pointers come from a table in memory: without the address space their
+// loads would be generic ones, which also count as LDS accesses.
+typedef __attribute__((address_space(1))) const uint8_t global_u8;
+typedef __attribute__((address_space(1))) const Bytes16 global_bytes16;
+
+__device__ __forceinline__ u32x4 load16(const uint8_t* p) { return *(global_u32x4*)(p); }
+__device__ __forceinline__ uint32_t load1(const uint8_t* p) { return *(global_u8*)(p); }
 
 __device__ __forceinline__ f32x4 mx_mfma(const u32x4& w, uint32_t ws, const u32x4& a, uint32_t as,
                                          f32x4 c) {
@@ -177,13 +184,13 @@ __global__ __launch_bounds__(64 * KS) void mx_few_rows_kernel(MxGemmArgs a, int 
         const int b = s * 4 + g;
         const bool in = b < KB;              // the last step may have fewer than 4 blocks
         const int bc = in ? b : KB - 1;
-        u32x4 av = *(const u32x4*)(ap + bc * 16);
-        const uint32_t as = asp[bc];
+        u32x4 av = load16(ap + bc * 16);
+        const uint32_t as = load1(asp + bc);
         if (!in) av = u32x4{0, 0, 0, 0};
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
-            u32x4 wv = *(const u32x4*)(wp[f] + bc * 16);
-            const uint32_t ws = wsp[f][bc];
+            u32x4 wv = load16(wp[f] + bc * 16);
+            const uint32_t ws = load1(wsp[f] + bc);
             if (!in) wv = u32x4{0, 0, 0, 0};
             acc[f] = mx_mfma(wv, in ? ws : 0u, av, in ? as : 0u, acc[f]);
         }
@@ -225,6 +232,179 @@ __global__ __launch_bounds__(64 * KS) void mx_few_rows_kernel(MxGemmArgs a, int 
     }
 }
 
+// ------------------------------------------------------------ many rows
+// Workgroup: 4 waves, each 64 matrix rows (4 fragments) by MT fragments of 16
+// rows. The matrix is the operand that has to come from HBM: each wave loads
+// its own rows straight into the instruction's registers, one step's registers
+// refilled for the next chunk as soon as the step has used them, so that nearly
+// a chunk (16 KB a wave) is on the way all the time without a barrier. The rows
+// are shared by the waves and come (from L2) over LDS, two chunks deep, and so
+// do the scale bytes of both sides, which a wave then reads one per lane.
+constexpr int kChunkSteps = 4;
+constexpr int kChunkBlocks = 4 * kChunkSteps;          // 16 blocks: 512 columns
+constexpr int kWaveFrags = 4;
+constexpr int kTileWaves = 4;
+constexpr int kTileRows = kTileWaves * kWaveFrags * kFrag;   // 256 matrix rows
+
+// Position of 16-byte unit b of row r in the LDS chunk: the units of a row
+// are permuted by its number, so that the 16 rows that a load reads at one
+// column fall into different banks.
+__device__ __forceinline__ int lds_unit(int r, int b) { return r * kChunkBlocks + (b ^ (r & 15)); }
+
+template <int MT>
+struct TileLds {
+    u32x4 code[2][MT * kFrag * kChunkBlocks];
+    u32x4 scale[2][MT * kFrag];                // a row's 16 scale bytes
+    u32x4 w_scale[2][kTileRows];
+};
+
+// The scale bytes of blocks b0 .. b0 + 15 of a row in two steps, so that the
+// load can be on the way while other work runs: the 16 bytes from b0 on, or the
+// row's last 16 where fewer are left (no byte outside the row is touched; KB >=
+// 16), and then their shift into place, which leaves 0 (2^-127) for blocks from KB
+// on; their codes are 0 on one side of the product.
+__device__ __forceinline__ u32x4 load_scales16(const uint8_t* row, int b0, int KB) {
+    global_bytes16* v = (global_bytes16*)(row + min(b0, KB - 16));
+    return u32x4{v->w[0], v->w[1], v->w[2], v->w[3]};
+}
+
+__device__ __forceinline__ u32x4 place_scales16(const u32x4& v, int b0, int KB) {
+    const int sh = 8 * (b0 + 16 - KB);               // uniform
+    if (sh <= 0) return v;
+    const uint64_t lo = v.x | (uint64_t)v.y << 32, hi = v.z | (uint64_t)v.w << 32;
+    const uint64_t l = sh < 64 ? lo >> sh | hi << (64 - sh) : hi >> (sh - 64);
+    const uint64_t h = sh < 64 ? hi >> sh : 0;
+    return u32x4{(uint32_t)l, (uint32_t)(l >> 32), (uint32_t)h, (uint32_t)(h >> 32)};
+}
+
+// Everything above this point happens before everything below it: memory
+// accesses by the clobber, the instructions that feed `acc` (which the compiler
+// would otherwise collect at the end of the loop, with all their operands
+// live) by the operands. No instruction of its own.
+template <int N>
+__device__ __forceinline__ void hold(f32x4 (&acc)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(acc[i])::"memory");
+}
+
+template <typename Out, bool SWIGLU, int MT>
+__global__ __launch_bounds__(64 * kTileWaves, MT <= 4 ? 2 : 1) void mx_tile_kernel(MxGemmArgs a, int NT) {
+    constexpr int BM = MT * kFrag;
+    constexpr int kThreads = 64 * kTileWaves;
+    constexpr int kStage = BM * kChunkBlocks / kThreads;      // 16-byte units a thread stages
+    __shared__ TileLds<MT> lds;
+    Unit u;
+    if (!find_unit(a.offsets, a.E, a.rows, BM, NT, &u)) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+    const uint8_t* blob = (const uint8_t*)a.table[u.e];
+    const int KB = a.K / kMxBlock, chunks = (KB + kChunkBlocks - 1) / kChunkBlocks;
+    const uint32_t row_bytes = KB * 16;
+    const int n_tile = u.nt * kTileRows, n_wave = n_tile + wave * kWaveFrags * kFrag;
+    // bases are uniform, lanes add 32-bit offsets
+    const uint8_t* w_base = blob + a.q_off + (int64_t)n_tile * row_bytes;
+    const uint8_t* ws_row = blob + a.s_off + (int64_t)min(n_tile + tid, a.N - 1) * KB;
+    const uint8_t* a_base = a.a + (int64_t)u.m0 * row_bytes;
+    const uint8_t* as_row = a.as + (int64_t)(u.m0 + min(tid, u.rows - 1)) * KB;
+    uint32_t w_off[kWaveFrags], s_off[kStage];
+#pragma unroll
+    for (int f = 0; f < kWaveFrags; ++f)
+        w_off[f] = (uint32_t)(min(n_wave + f * kFrag + r, a.N - 1) - n_tile) * row_bytes;
+#pragma unroll
+    for (int i = 0; i < kStage; ++i)
+        s_off[i] = (uint32_t)min((tid + i * kThreads) / kChunkBlocks, u.rows - 1) * row_bytes;
+
+    u32x4 stage[kStage], stage_s, stage_ws;
+    auto stage_load = [&](int c) {
+        const int b = c * kChunkBlocks + tid % kChunkBlocks, bc = min(b, KB - 1) * 16;
+#pragma unroll
+        for (int i = 0; i < kStage; ++i) stage[i] = load16(a_base + (s_off[i] + bc));
+        stage_ws = load_scales16(ws_row, c * kChunkBlocks, KB);
+        stage_s = load_scales16(as_row, c * kChunkBlocks, KB);
+    };
+    auto stage_store = [&](int c, int buf) {
+        const bool in = c * kChunkBlocks + tid % kChunkBlocks < KB;
+#pragma unroll
+        for (int i = 0; i < kStage; ++i) {
+            const int x = tid + i * kThreads;
+            lds.code[buf][lds_unit(x / kChunkBlocks, x % kChunkBlocks)] = in ? stage[i] : u32x4{0, 0, 0, 0};
+        }
+        lds.w_scale[buf][tid] = place_scales16(stage_ws, c * kChunkBlocks, KB);
+        if (tid < BM) lds.scale[buf][tid] = place_scales16(stage_s, c * kChunkBlocks, KB);
+    };
+
+    u32x4 w[kChunkSteps][kWaveFrags];
+    auto w_load = [&](int c, int s) {
+        const uint32_t b = min(c * kChunkBlocks + s * 4 + g, KB - 1) * 16;
+#pragma unroll
+        for (int f = 0; f < kWaveFrags; ++f) w[s][f] = load16(w_base + (w_off[f] + b));
+    };
+
+    f32x4 acc[kWaveFrags][MT];
+#pragma unroll
+    for (int f = 0; f < kWaveFrags; ++f)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[f][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    stage_load(0);
+#pragma unroll
+    for (int s = 0; s < kChunkSteps; ++s) w_load(0, s);
+    stage_store(0, 0);
+    __syncthreads();
+    for (int c = 0; c < chunks; ++c) {
+        const int buf = c & 1, next = min(c + 1, chunks - 1);
+        const uint8_t* as_b = (const uint8_t*)lds.scale[buf] + r * 16 + g;
+        const uint8_t* ws_b = (const uint8_t*)lds.w_scale[buf] + (wave * kWaveFrags * kFrag + r) * 16 + g;
+        stage_load(next);
+#pragma unroll
+        for (int s = 0; s < kChunkSteps; ++s) {
+            u32x4 av[MT];
+            uint32_t as[MT], ws[kWaveFrags];
+#pragma unroll
+            for (int f = 0; f < kWaveFrags; ++f) ws[f] = ws_b[f * kFrag * 16 + s * 4];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                as[i] = as_b[i * kFrag * 16 + s * 4];
+                av[i] = lds.code[buf][lds_unit(i * kFrag + r, s * 4 + g)];
+            }
+#pragma unroll
+            for (int f = 0; f < kWaveFrags; ++f)
+#pragma unroll
+                for (int i = 0; i < MT; ++i) acc[f][i] = mx_mfma(w[s][f], ws[f], av[i], as[i], acc[f][i]);
+#pragma unroll
+            for (int f = 0; f < kWaveFrags; ++f) hold(acc[f]);
+            w_load(next, s);
+            sched_fence();
+        }
+        stage_store(next, buf ^ 1);
+        __syncthreads();
+    }
+    // outputs
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const bool live = i * kFrag + r < u.rows;
+        const int m = u.m0 + i * kFrag + r;
+        if constexpr (!SWIGLU) {
+#pragma unroll
+            for (int f = 0; f < kWaveFrags; ++f)
+                if (live) store4<Out>(a, m, n_wave + f * kFrag + 4 * g, a.N, acc[f][i]);
+        } else {
+            f32x4 h[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) h[p][x] = silu_mul(acc[2 * p][i][x], acc[2 * p + 1][i][x]);
+            const int n0 = n_wave / 2;
+            if constexpr (std::is_same<Out, MxOut>::value) {
+                store_mx(a, m, n0, a.N / 2, live && n0 < a.N / 2, h[0], h[1]);
+            } else {
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    if (live) store4<Out>(a, m, n0 + p * kFrag + 4 * g, a.N / 2, h[p]);
+            }
+        }
+    }
+}
+
 // Units of a launch at most: the rows fill rows / BM stretches, and each expert
 // with rows may add one that is not full.
 coli_status grid_of(const MxGemmArgs& a, int BM, int NT, int threads, uint32_t* grid) {
@@ -246,13 +426,32 @@ coli_status few_rows(const MxGemmArgs& a, hipStream_t stream) {
     return COLI_OK;
 }
 
+template <typename Out, bool SWIGLU, int MT>
+coli_status tiles(const MxGemmArgs& a, hipStream_t stream) {
+    const int NT = (a.N + kTileRows - 1) / kTileRows;
+    uint32_t grid;
+    if (coli_status st = grid_of(a, MT * kFrag, NT, 64 * kTileWaves, &grid)) return st;
+    launch(mx_tile_kernel<Out, SWIGLU, MT>, dim3(grid), dim3(64 * kTileWaves), 0, stream, a, NT);
+    COLI_CHECK_LAUNCH("mxfp4 product kernel launch");
+    return COLI_OK;
+}
+
+template <typename Out, bool SWIGLU>
+coli_status product(const MxGemmArgs& a, hipStream_t stream) {
+    constexpr bool mx = std::is_same<Out, MxOut>::value;
+    const double per = (double)a.rows / (a.offsets ? std::min(a.E, a.rows) : 1);
+    if (per <= 8 || a.K < kChunkBlocks * kMxBlock) return few_rows<Out, SWIGLU, mx ? 4 : SWIGLU ? 2 : 1, 4>(a, stream);
+    if (per <= 128) return tiles<Out, SWIGLU, 4>(a, stream);
+    return tiles<Out, SWIGLU, 8>(a, stream);
+}
+
 }  // namespace
 
 coli_status launch_mxfp4_gemm(const MxGemmArgs& a, bool swiglu, int32_t dtype, hipStream_t stream) {
-    if (swiglu && dtype == COLI_MXFP4) return few_rows<MxOut, true, 4, 4>(a, stream);
+    if (swiglu && dtype == COLI_MXFP4) return product<MxOut, true>(a, stream);
     return with_elem(dtype, [&](auto e) -> coli_status {
         using T = decltype(e);
-        return swiglu ? few_rows<T, true, 2, 4>(a, stream) : few_rows<T, false, 1, 4>(a, stream);
+        return swiglu ? product<T, true>(a, stream) : product<T, false>(a, stream);
     });
 }
 
