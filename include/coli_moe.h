@@ -475,9 +475,10 @@ COLI_API coli_status coli_quantize_mxfp4_expert(const coli_moe_shape* shape, con
  * are neither read nor written. d_offsets NULL: E is 1 and has every row.
  * d_blob_table [E] (device): per expert the buffer that holds its matrix, codes
  * at q_off (a multiple of 16, as the buffer's address) and scales at s_off.
- * Entries of experts without rows are not read. d_y: type dtype (f32, bf16 or
+ * The buffers of experts without rows are not read. d_y: type dtype (f32, bf16 or
  * f16), row stride ld >= N. Products are exact, sums f32, the result rounded
- * once; a row's result does not depend on the other rows' values. E <= 1024. */
+ * once; a row's result does not depend on the other rows' values. E <= 1024, K <=
+ * 2^22. */
 COLI_API coli_status coli_mxfp4_matmul(const uint8_t* d_a, const uint8_t* d_as, int32_t rows, int32_t K,
                                        const int32_t* d_offsets, int32_t E,
                                        const void* const* d_blob_table, size_t q_off, size_t s_off,

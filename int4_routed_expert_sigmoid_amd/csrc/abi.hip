@@ -486,6 +486,7 @@ static coli_status mx_product(const char* what, const uint8_t* d_a, const uint8_
     if (rows < 0 || K <= 0 || K % kMxBlock) return fail(COLI_EINVAL, w + ": rows >= 0, K a positive multiple of 32");
     if (n_out <= 0 || (swiglu && n_out % kMxBlock))
         return fail(COLI_EINVAL, w + (swiglu ? ": inter must be a positive multiple of 32" : ": N must be positive"));
+    if (K > (1 << 22)) return fail(COLI_EUNSUPPORTED, w + ": K must be at most 2^22");
     if (N > INT32_MAX - 4096) return fail(COLI_EUNSUPPORTED, w + ": matrix too large");
     if (E < 1) return fail(COLI_EINVAL, w + ": E must be at least 1");
     if (E > 1024) return fail(COLI_EUNSUPPORTED, w + ": E must be at most 1024");

@@ -29,68 +29,100 @@ struct MxOut {};
 // ------------------------------------------------------------ work units
 // Unit `w` of the launch: an expert, a stretch of its rows and a stretch of the
 // matrix' rows. Every wave finds its unit from the offsets by itself (a scan
-// over at most 1024 counts, 16 a lane), so a product is one launch without a
-// workspace. Consecutive workgroups run on different XCDs; each XCD is given
-// one contiguous eighth of the units, ordered by expert, matrix rows, rows, so
-// that units that read the same matrix rows follow each other behind one L2.
+// over at most 1024 counts), so a product is one launch without a workspace. Up
+// to 256 experts a lane's four offsets and blob pointers are loaded together:
+// the search costs one memory latency. Consecutive workgroups run on different
+// XCDs; each XCD is given one contiguous eighth of the units, ordered by
+// expert, matrix rows, rows, so that units that read the same matrix rows
+// follow each other behind one L2.
 struct Unit {
-    int e, m0, rows, nt;         // rows [m0, m0 + rows) (rows <= BM), n tile
+    const uint8_t* blob;
+    int m0, rows, nt;            // rows [m0, m0 + rows) (rows <= BM), n tile
 };
 
-__device__ __forceinline__ bool find_unit(const int32_t* offsets, int E, int R, int BM, int NT,
-                                          Unit* out) {
-    const int lane = threadIdx.x & 63;
+constexpr int kLaneExperts = 4;
+
+// First row and row count of experts e0 .. e0 + 3, clamped to the R rows; 0 rows
+// from expert E on.
+__device__ __forceinline__ void expert_rows(const int32_t* offsets, int e0, int E, int R,
+                                            int (&lo)[kLaneExperts], int (&n)[kLaneExperts]) {
+    int o[kLaneExperts + 1];
+#pragma unroll
+    for (int c = 0; c <= kLaneExperts; ++c) o[c] = offsets[min(e0 + c, E)];
+#pragma unroll
+    for (int c = 0; c < kLaneExperts; ++c) {
+        lo[c] = min(max(o[c], 0), R);
+        n[c] = min(max(o[c + 1], lo[c]), R) - lo[c];
+    }
+}
+
+template <int BM>
+__device__ __forceinline__ bool find_unit(const MxGemmArgs& a, int NT, Unit* out) {
+    const int lane = threadIdx.x & 63, E = a.E, R = a.rows;
     const uint32_t xcd = blockIdx.x % kXcds, at = blockIdx.x / kXcds;
-    if (offsets == nullptr) {
+    if (a.offsets == nullptr) {
         const uint32_t mt = (R + BM - 1) / BM, total = mt * NT, per = (total + kXcds - 1) / kXcds;
         const uint32_t w = xcd * per + at;
         if (at >= per || w >= total) return false;
-        out->e = 0;
+        out->blob = (const uint8_t*)a.table[0];
         out->nt = w / mt;
         out->m0 = (w % mt) * BM;
         out->rows = min(BM, R - out->m0);
         return true;
     }
-    const int C = (E + 63) / 64;             // experts of a lane
+    const int groups = (E + 64 * kLaneExperts - 1) / (64 * kLaneExperts);   // of 4 experts a lane
+    const int e0 = lane * groups * kLaneExperts;
+    int lo[kLaneExperts], n[kLaneExperts];
     uint32_t tiles = 0;
-    for (int c = 0; c < C; ++c) {
-        const int e = lane * C + c;
-        if (e >= E) break;
-        const int lo = min(max(offsets[e], 0), R), hi = min(max(offsets[e + 1], lo), R);
-        tiles += (hi - lo + BM - 1) / BM;
+    for (int c = groups - 1; c >= 0; --c) {                  // ends with the lane's first group loaded
+        expert_rows(a.offsets, e0 + c * kLaneExperts, E, R, lo, n);
+#pragma unroll
+        for (int i = 0; i < kLaneExperts; ++i) tiles += (n[i] + BM - 1) / BM;
     }
+    const uint8_t* ptr[kLaneExperts];
+#pragma unroll
+    for (int i = 0; i < kLaneExperts; ++i) ptr[i] = (const uint8_t*)a.table[min(e0 + i, E - 1)];
     uint32_t incl = tiles;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
         const uint32_t v = __shfl_up(incl, o);
         if (lane >= o) incl += v;
     }
-    const uint32_t total = __shfl(incl, 63) * NT, per = (total + kXcds - 1) / kXcds;
+    const uint32_t total = __builtin_amdgcn_readlane(incl, 63) * NT, per = (total + kXcds - 1) / kXcds;
     const uint32_t w = xcd * per + at;
     if (at >= per || w >= total) return false;
     const uint32_t first = (incl - tiles) * NT;
     const unsigned long long has = __ballot(w >= first && w < incl * NT);
-    if (has == 0) return false;              // offsets that are not ascending
+    if (has == 0) return false;                              // offsets that are not ascending
     const int owner = __ffsll(has) - 1;
-    Unit u = {0, 0, 0, 0};
+    Unit u = {nullptr, 0, 0, 0};
     if (lane == owner) {
         uint32_t rest = w - first;
-        for (int c = 0; c < C; ++c) {
-            const int e = lane * C + c;
-            if (e >= E) break;
-            const int lo = min(max(offsets[e], 0), R), hi = min(max(offsets[e + 1], lo), R);
-            const uint32_t mt = (hi - lo + BM - 1) / BM;
-            if (rest < mt * NT) {
-                u.e = e;
-                u.nt = rest / mt;
-                u.m0 = lo + (int)(rest % mt) * BM;
-                u.rows = min(BM, hi - u.m0);
-                break;
+        for (int c = 0; c < groups; ++c) {
+            if (c > 0) {
+                expert_rows(a.offsets, e0 + c * kLaneExperts, E, R, lo, n);
+#pragma unroll
+                for (int i = 0; i < kLaneExperts; ++i)
+                    ptr[i] = (const uint8_t*)a.table[min(e0 + c * kLaneExperts + i, E - 1)];
             }
-            rest -= mt * NT;
+#pragma unroll
+            for (int i = 0; i < kLaneExperts; ++i) {
+                const uint32_t mt = (n[i] + BM - 1) / BM;
+                if (u.rows == 0 && rest < mt * NT) {
+                    u.blob = ptr[i];
+                    u.nt = rest / mt;
+                    u.m0 = (int)(rest % mt) * BM;
+                    u.rows = min(BM, n[i] - u.m0);
+                    u.m0 += lo[i];
+                }
+                rest -= u.rows == 0 ? mt * NT : 0;
+            }
         }
     }
-    out->e = __builtin_amdgcn_readlane(u.e, owner);
+    const uint64_t b = (uint64_t)u.blob;
+    const uint32_t b_lo = __builtin_amdgcn_readlane((uint32_t)b, owner);
+    const uint32_t b_hi = __builtin_amdgcn_readlane((uint32_t)(b >> 32), owner);
+    out->blob = (const uint8_t*)((uint64_t)b_hi << 32 | b_lo);
     out->m0 = __builtin_amdgcn_readlane(u.m0, owner);
     out->rows = __builtin_amdgcn_readlane(u.rows, owner);
     out->nt = __builtin_amdgcn_readlane(u.nt, owner);
@@ -107,6 +139,8 @@ typedef __attribute__((address_space(1))) const uint8_t global_u8;
 typedef __attribute__((address_space(1))) const Bytes16 global_bytes16;
 
 __device__ __forceinline__ u32x4 load16(const uint8_t* p) { return *(global_u32x4*)(p); }
+// Matrix rows that one workgroup alone reads: kept out of the caches.
+__device__ __forceinline__ u32x4 load16_once(const uint8_t* p) { return __builtin_nontemporal_load((global_u32x4*)(p)); }
 __device__ __forceinline__ uint32_t load1(const uint8_t* p) { return *(global_u8*)(p); }
 
 __device__ __forceinline__ f32x4 mx_mfma(const u32x4& w, uint32_t ws, const u32x4& a, uint32_t as,
@@ -115,6 +149,39 @@ __device__ __forceinline__ f32x4 mx_mfma(const u32x4& w, uint32_t ws, const u32x
     const i32x8 A = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
     // 4: E2M1 operands; the scale is the low byte of its register
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(W, A, c, 4, 4, 0, (int)ws, 0, (int)as);
+}
+
+// Columns go through the kernels in chunks of 512: 4 steps, 16 blocks.
+constexpr int kChunkSteps = 4;
+constexpr int kChunkBlocks = 4 * kChunkSteps;          // 16 blocks: 512 columns
+
+// The scale bytes of blocks b0 .. b0 + 15 of a row in two steps, so that the
+// load can be on the way while other work runs: the 16 bytes from b0 on, or the
+// row's last 16 where fewer are left (no byte outside the row is touched; KB >=
+// 16), and then their shift into place, which leaves 0 (2^-127) for blocks from KB
+// on; their codes are 0 on one side of the product.
+__device__ __forceinline__ u32x4 load_scales16(const uint8_t* row, int b0, int KB) {
+    global_bytes16* v = (global_bytes16*)(row + min(b0, KB - 16));
+    return u32x4{v->w[0], v->w[1], v->w[2], v->w[3]};
+}
+
+__device__ __forceinline__ u32x4 place_scales16(const u32x4& v, int b0, int KB) {
+    const int sh = 8 * (b0 + 16 - KB);               // uniform
+    if (sh <= 0) return v;
+    const uint64_t lo = v.x | (uint64_t)v.y << 32, hi = v.z | (uint64_t)v.w << 32;
+    const uint64_t l = sh < 64 ? lo >> sh | hi << (64 - sh) : hi >> (sh - 64);
+    const uint64_t h = sh < 64 ? hi >> sh : 0;
+    return u32x4{(uint32_t)l, (uint32_t)(l >> 32), (uint32_t)h, (uint32_t)(h >> 32)};
+}
+
+// Everything above this point happens before everything below it: memory
+// accesses by the clobber, the instructions that feed `acc` (which the compiler
+// would otherwise collect at the end of the loop, with all their operands
+// live) by the operands. No instruction of its own.
+template <int N>
+__device__ __forceinline__ void hold(f32x4 (&acc)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(acc[i])::"memory");
 }
 
 // ------------------------------------------------------------ epilogues
@@ -154,45 +221,78 @@ __device__ __forceinline__ void store_mx(const MxGemmArgs& a, int m, int n0, int
 }
 
 // ------------------------------------------------------------ few rows
-// Workgroup: NF fragments of 16 matrix rows by up to 16 rows; the columns are
-// split over its KS waves in stretches of whole steps, so that even one row of
-// one expert has KS waves a fragment set on the way, and the partial sums meet
-// in LDS in wave order.
-template <typename Out, bool SWIGLU, int NF, int KS>
+// Workgroup: NF fragments of 16 matrix rows by up to 16 rows. Its KS waves take
+// chunks of the columns in turn, so that even one row of one expert has KS
+// waves a fragment set on the way, and the partial sums meet in LDS in wave
+// order. Everything goes straight into the instruction's registers; a step's
+// registers are refilled for the wave's next chunk as soon as the step has
+// used them. Whole chunks only (TAIL false) or any number of columns.
+template <typename Out, bool SWIGLU, int NF, int KS, bool TAIL>
 __global__ __launch_bounds__(64 * KS) void mx_few_rows_kernel(MxGemmArgs a, int NT) {
     __shared__ f32x4 part[KS][NF][64];
     Unit u;
-    if (!find_unit(a.offsets, a.E, a.rows, kFrag, NT, &u)) return;
+    if (!find_unit<kFrag>(a, NT, &u)) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-    const uint8_t* blob = (const uint8_t*)a.table[u.e];
-    const int KB = a.K / kMxBlock, steps = (KB + 3) / 4;
-    const int m = u.m0 + min(r, u.rows - 1);
-    const uint8_t* ap = a.a + (int64_t)m * (a.K / 2);
-    const uint8_t* asp = a.as + (int64_t)m * KB;
-    const uint8_t *wp[NF], *wsp[NF];
+    const int KB = a.K / kMxBlock, chunks = (KB + kChunkBlocks - 1) / kChunkBlocks;
+    const uint32_t row_bytes = KB * 16;
+    const int n_tile = u.nt * NF * kFrag;
+    const uint8_t* w_base = u.blob + a.q_off + (int64_t)n_tile * row_bytes;
+    const uint8_t* ws_base = u.blob + a.s_off + (int64_t)n_tile * KB;
+    const uint8_t* a_base = a.a + (int64_t)u.m0 * row_bytes;
+    const uint8_t* as_base = a.as + (int64_t)u.m0 * KB;
+    const int mr = min(r, u.rows - 1);
+    int nr[NF];
 #pragma unroll
-    for (int f = 0; f < NF; ++f) {
-        const int64_t n = min((u.nt * NF + f) * kFrag + r, a.N - 1);
-        wp[f] = blob + a.q_off + n * (a.K / 2);
-        wsp[f] = blob + a.s_off + n * KB;
-    }
+    for (int f = 0; f < NF; ++f) nr[f] = min(f * kFrag + r, a.N - 1 - n_tile);
+
+    u32x4 w[kChunkSteps][NF], av[kChunkSteps], ws[NF], as;
+    auto load_step = [&](int c, int s) {
+        int b = c * kChunkBlocks + s * 4 + g;
+        if (TAIL) b = min(b, KB - 1);
+        av[s] = load16(a_base + (mr * row_bytes + b * 16));
+#pragma unroll
+        for (int f = 0; f < NF; ++f) w[s][f] = load16_once(w_base + (nr[f] * row_bytes + b * 16));
+    };
+    // a lane's scale byte of step s: byte g of word s
+    auto load_scales = [&](int c) {
+        if (!TAIL) {
+            as = load_scales16(as_base + mr * (uint32_t)KB, c * kChunkBlocks, KB);
+#pragma unroll
+            for (int f = 0; f < NF; ++f) ws[f] = load_scales16(ws_base + nr[f] * (uint32_t)KB, c * kChunkBlocks, KB);
+            return;
+        }
+#pragma unroll
+        for (int s = 0; s < kChunkSteps; ++s) {
+            const int b = min(c * kChunkBlocks + s * 4 + g, KB - 1);
+            as[s] = load1(as_base + (mr * (uint32_t)KB + b));
+#pragma unroll
+            for (int f = 0; f < NF; ++f) ws[f][s] = load1(ws_base + (nr[f] * (uint32_t)KB + b));
+        }
+    };
     f32x4 acc[NF];
 #pragma unroll
     for (int f = 0; f < NF; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int s0 = (int)((int64_t)steps * wave / KS), s1 = (int)((int64_t)steps * (wave + 1) / KS);
-    for (int s = s0; s < s1; ++s) {
-        const int b = s * 4 + g;
-        const bool in = b < KB;              // the last step may have fewer than 4 blocks
-        const int bc = in ? b : KB - 1;
-        u32x4 av = load16(ap + bc * 16);
-        const uint32_t as = load1(asp + bc);
-        if (!in) av = u32x4{0, 0, 0, 0};
+    if (wave < chunks) {
+        load_scales(wave);
 #pragma unroll
-        for (int f = 0; f < NF; ++f) {
-            u32x4 wv = load16(wp[f] + bc * 16);
-            const uint32_t ws = load1(wsp[f] + bc);
-            if (!in) wv = u32x4{0, 0, 0, 0};
-            acc[f] = mx_mfma(wv, in ? ws : 0u, av, in ? as : 0u, acc[f]);
+        for (int s = 0; s < kChunkSteps; ++s) load_step(wave, s);
+    }
+    for (int c = wave; c < chunks; c += KS) {
+        const bool more = c + KS < chunks;
+        u32x4 as_c = as, ws_c[NF];
+#pragma unroll
+        for (int f = 0; f < NF; ++f) ws_c[f] = ws[f];
+        if (more) load_scales(c + KS);
+#pragma unroll
+        for (int s = 0; s < kChunkSteps; ++s) {
+            // a block from KB on has codes 0 on one side and the row's last scale on both
+            u32x4 x = av[s];
+            if (TAIL && c * kChunkBlocks + s * 4 + g >= KB) x = u32x4{0, 0, 0, 0};
+            const int sh = TAIL ? 0 : 8 * g;
+#pragma unroll
+            for (int f = 0; f < NF; ++f) acc[f] = mx_mfma(w[s][f], ws_c[f][s] >> sh, x, as_c[s] >> sh, acc[f]);
+            hold(acc);
+            if (more) load_step(c + KS, s);
         }
     }
 #pragma unroll
@@ -240,8 +340,6 @@ __global__ __launch_bounds__(64 * KS) void mx_few_rows_kernel(MxGemmArgs a, int 
 // a chunk (16 KB a wave) is on the way all the time without a barrier. The rows
 // are shared by the waves and come (from L2) over LDS, two chunks deep, and so
 // do the scale bytes of both sides, which a wave then reads one per lane.
-constexpr int kChunkSteps = 4;
-constexpr int kChunkBlocks = 4 * kChunkSteps;          // 16 blocks: 512 columns
 constexpr int kWaveFrags = 4;
 constexpr int kTileWaves = 4;
 constexpr int kTileRows = kTileWaves * kWaveFrags * kFrag;   // 256 matrix rows
@@ -258,35 +356,6 @@ struct TileLds {
     u32x4 w_scale[2][kTileRows];
 };
 
-// The scale bytes of blocks b0 .. b0 + 15 of a row in two steps, so that the
-// load can be on the way while other work runs: the 16 bytes from b0 on, or the
-// row's last 16 where fewer are left (no byte outside the row is touched; KB >=
-// 16), and then their shift into place, which leaves 0 (2^-127) for blocks from KB
-// on; their codes are 0 on one side of the product.
-__device__ __forceinline__ u32x4 load_scales16(const uint8_t* row, int b0, int KB) {
-    global_bytes16* v = (global_bytes16*)(row + min(b0, KB - 16));
-    return u32x4{v->w[0], v->w[1], v->w[2], v->w[3]};
-}
-
-__device__ __forceinline__ u32x4 place_scales16(const u32x4& v, int b0, int KB) {
-    const int sh = 8 * (b0 + 16 - KB);               // uniform
-    if (sh <= 0) return v;
-    const uint64_t lo = v.x | (uint64_t)v.y << 32, hi = v.z | (uint64_t)v.w << 32;
-    const uint64_t l = sh < 64 ? lo >> sh | hi << (64 - sh) : hi >> (sh - 64);
-    const uint64_t h = sh < 64 ? hi >> sh : 0;
-    return u32x4{(uint32_t)l, (uint32_t)(l >> 32), (uint32_t)h, (uint32_t)(h >> 32)};
-}
-
-// Everything above this point happens before everything below it: memory
-// accesses by the clobber, the instructions that feed `acc` (which the compiler
-// would otherwise collect at the end of the loop, with all their operands
-// live) by the operands. No instruction of its own.
-template <int N>
-__device__ __forceinline__ void hold(f32x4 (&acc)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(acc[i])::"memory");
-}
-
 template <typename Out, bool SWIGLU, int MT>
 __global__ __launch_bounds__(64 * kTileWaves, MT <= 4 ? 2 : 1) void mx_tile_kernel(MxGemmArgs a, int NT) {
     constexpr int BM = MT * kFrag;
@@ -294,15 +363,14 @@ __global__ __launch_bounds__(64 * kTileWaves, MT <= 4 ? 2 : 1) void mx_tile_kern
     constexpr int kStage = BM * kChunkBlocks / kThreads;      // 16-byte units a thread stages
     __shared__ TileLds<MT> lds;
     Unit u;
-    if (!find_unit(a.offsets, a.E, a.rows, BM, NT, &u)) return;
+    if (!find_unit<BM>(a, NT, &u)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
-    const uint8_t* blob = (const uint8_t*)a.table[u.e];
     const int KB = a.K / kMxBlock, chunks = (KB + kChunkBlocks - 1) / kChunkBlocks;
     const uint32_t row_bytes = KB * 16;
     const int n_tile = u.nt * kTileRows, n_wave = n_tile + wave * kWaveFrags * kFrag;
     // bases are uniform, lanes add 32-bit offsets
-    const uint8_t* w_base = blob + a.q_off + (int64_t)n_tile * row_bytes;
-    const uint8_t* ws_row = blob + a.s_off + (int64_t)min(n_tile + tid, a.N - 1) * KB;
+    const uint8_t* w_base = u.blob + a.q_off + (int64_t)n_tile * row_bytes;
+    const uint8_t* ws_row = u.blob + a.s_off + (int64_t)min(n_tile + tid, a.N - 1) * KB;
     const uint8_t* a_base = a.a + (int64_t)u.m0 * row_bytes;
     const uint8_t* as_row = a.as + (int64_t)(u.m0 + min(tid, u.rows - 1)) * KB;
     uint32_t w_off[kWaveFrags], s_off[kStage];
@@ -421,7 +489,10 @@ coli_status few_rows(const MxGemmArgs& a, hipStream_t stream) {
     const int NT = (a.N + NF * kFrag - 1) / (NF * kFrag);
     uint32_t grid;
     if (coli_status st = grid_of(a, kFrag, NT, 64 * KS, &grid)) return st;
-    launch(mx_few_rows_kernel<Out, SWIGLU, NF, KS>, dim3(grid), dim3(64 * KS), 0, stream, a, NT);
+    if (a.K % (kChunkBlocks * kMxBlock) == 0)
+        launch(mx_few_rows_kernel<Out, SWIGLU, NF, KS, false>, dim3(grid), dim3(64 * KS), 0, stream, a, NT);
+    else
+        launch(mx_few_rows_kernel<Out, SWIGLU, NF, KS, true>, dim3(grid), dim3(64 * KS), 0, stream, a, NT);
     COLI_CHECK_LAUNCH("mxfp4 product kernel launch");
     return COLI_OK;
 }
@@ -440,7 +511,7 @@ template <typename Out, bool SWIGLU>
 coli_status product(const MxGemmArgs& a, hipStream_t stream) {
     constexpr bool mx = std::is_same<Out, MxOut>::value;
     const double per = (double)a.rows / (a.offsets ? std::min(a.E, a.rows) : 1);
-    if (per <= 8 || a.K < kChunkBlocks * kMxBlock) return few_rows<Out, SWIGLU, mx ? 4 : SWIGLU ? 2 : 1, 4>(a, stream);
+    if (per <= 8 || a.K < kChunkBlocks * kMxBlock) return few_rows<Out, SWIGLU, mx ? 4 : 2, 4>(a, stream);
     if (per <= 128) return tiles<Out, SWIGLU, 4>(a, stream);
     return tiles<Out, SWIGLU, 8>(a, stream);
 }

@@ -55,6 +55,7 @@ def test_product_refusals(L):
 
     for f in (mm, sw):
         assert f(rows=-1) == EINVAL and f(K=48) == EINVAL and f(K=0) == EINVAL
+        assert f(K=(1 << 22) + 32) == EUNSUP
         assert f(n=0) == EINVAL and f(E=0) == EINVAL and f(E=1025) == EUNSUP
         assert f(off=None) == EINVAL                            # several experts need offsets
         assert f(ld=7) == EINVAL and f(dt=4) == EUNSUP and f(dt=-1) == EUNSUP
