@@ -484,10 +484,13 @@ def read_probe(src, pattern: int, row_bytes: int, rows_per_wg: int, sink, stream
 # ---------------------------------------------------------------- MXFP4 experts and token permutation
 def _dtype_code(dtype) -> int:
     import torch
-    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(dtype)
-    if code is None:
-        raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
-    return code
+    if dtype == torch.bfloat16:
+        return BF16
+    if dtype == torch.float32:
+        return F32
+    if dtype == torch.float16:
+        return F16
+    raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
 
 
 def _rows(t, name, rows=None, cols=None, dtype=None):
@@ -495,17 +498,20 @@ def _rows(t, name, rows=None, cols=None, dtype=None):
     other; `rows` is a least number of rows, `cols` and `dtype` must be met."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be 2-d with contiguous columns")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-d")
+    n, m = t.shape
+    ld, step = t.stride()
+    if step != 1 and m > 1:
+        raise ValueError(f"{name} must have contiguous columns")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if (rows is not None and t.shape[0] < rows) or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {cols})")
-    ld = t.stride(0)
-    if t.shape[0] <= 1:
-        ld = max(ld, t.shape[1])
-    elif ld < t.shape[1]:
-        raise ValueError(f"{name} has rows that overlap")
+    if (rows is not None and n < rows) or (cols is not None and m != cols):
+        raise ValueError(f"{name} has shape {(n, m)}, expected ({rows}, {cols})")
+    if ld < m:
+        if n > 1:
+            raise ValueError(f"{name} has rows that overlap")
+        ld = m
     return _dtype_code(t.dtype), ld
 
 
@@ -514,38 +520,44 @@ def _mx(q, s, name):
     import torch
     _need(q, torch.uint8, f"{name} codes")
     _need(s, torch.uint8, f"{name} scales")
-    if q.dim() != 2 or s.dim() != 2 or s.shape[0] != q.shape[0] or q.shape[1] != 16 * s.shape[1]:
-        raise ValueError(f"{name}: codes {tuple(q.shape)} and scales {tuple(s.shape)} do not match")
-    return q.shape[0], 2 * q.shape[1]
+    if q.dim() == 2 and s.dim() == 2:
+        rows, half = q.shape
+        if s.shape == (rows, half // 16) and half % 16 == 0:
+            return rows, 2 * half
+    raise ValueError(f"{name}: codes {tuple(q.shape)} and scales {tuple(s.shape)} do not match")
 
 
-def _mx_out(q, s, rows, cols, device, name):
+def _mx_out(q, s, rows, cols, like, name):
     import torch
     if cols % 32:
         raise ValueError(f"{name}: the columns of MXFP4 rows must be a multiple of 32, got {cols}")
+    if q is None and s is None:
+        return (like.new_empty((rows, cols // 2), dtype=torch.uint8),
+                like.new_empty((rows, cols // 32), dtype=torch.uint8))
     if q is None:
-        q = torch.empty((rows, cols // 2), dtype=torch.uint8, device=device)
+        q = like.new_empty((rows, cols // 2), dtype=torch.uint8)
     if s is None:
-        s = torch.empty((rows, cols // 32), dtype=torch.uint8, device=device)
+        s = like.new_empty((rows, cols // 32), dtype=torch.uint8)
     if _mx(q, s, name) != (rows, cols):
         raise ValueError(f"{name}: codes must have shape ({rows}, {cols // 2})")
     return q, s
 
 
 def _enqueue(tensors, stream, fn, *args):
-    """fn(*args, stream) on the tensors' device, on its current stream unless one is given."""
+    """The library's call `fn`(*args, stream) on the tensors' device, on its current stream unless
+    one is given. (The raw current stream costs 0.2 us of host time, a Stream object 2.)"""
     import torch
-    dev = tensors[0].device
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: one device is needed")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, stream.cuda_stream)
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on devices {dev} and {t.get_device()}: one device is needed")
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    call = getattr(_lib or lib(), fn)
+    if dev == torch.cuda.current_device():
+        rc = call(*args, raw)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, stream.cuda_stream)
+            rc = call(*args, raw)
     if rc != COLI_OK:
         _check(rc)
 
@@ -555,8 +567,8 @@ def quantize_mxfp4(x, q=None, s=None, stream=None):
     [rows][cols/2], scales uint8 [rows][cols/32])."""
     code, ld = _rows(x, "x")
     rows, cols = x.shape
-    q, s = _mx_out(q, s, rows, cols, x.device, "quantize_mxfp4")
-    _enqueue((x, q, s), stream, lib().coli_quantize_mxfp4, x.data_ptr(), code, rows, cols, ld,
+    q, s = _mx_out(q, s, rows, cols, x, "quantize_mxfp4")
+    _enqueue((x, q, s), stream, "coli_quantize_mxfp4", x.data_ptr(), code, rows, cols, ld,
              q.data_ptr(), s.data_ptr())
     return q, s
 
@@ -566,9 +578,9 @@ def dequantize_mxfp4(q, s, dtype=None, out=None, stream=None):
     import torch
     rows, cols = _mx(q, s, "dequantize_mxfp4")
     if out is None:
-        out = torch.empty((rows, cols), dtype=dtype or torch.float32, device=q.device)
+        out = q.new_empty((rows, cols), dtype=dtype or torch.float32)
     code, ld = _rows(out, "out", rows, cols, dtype)
-    _enqueue((q, s, out), stream, lib().coli_dequantize_mxfp4, q.data_ptr(), s.data_ptr(), rows, cols,
+    _enqueue((q, s, out), stream, "coli_dequantize_mxfp4", q.data_ptr(), s.data_ptr(), rows, cols,
              out.data_ptr(), code, ld)
     return out
 
@@ -595,7 +607,7 @@ def quantize_mxfp4_expert(shape: MoEShape, gate, up, down, blob=None, stream=Non
     _need(blob, torch.uint8, "blob")
     if blob.numel() < nbytes:
         raise ValueError(f"blob must hold {nbytes} bytes")
-    _enqueue((gate, up, down, blob), stream, lib().coli_quantize_mxfp4_expert, ctypes.byref(shape.c()),
+    _enqueue((gate, up, down, blob), stream, "coli_quantize_mxfp4_expert", ctypes.byref(shape.c()),
              gate.data_ptr(), up.data_ptr(), down.data_ptr(), _dtype_code(gate.dtype), blob.data_ptr())
     return blob
 
@@ -620,7 +632,7 @@ def mxfp4_matmul(a, a_s, table, n, q_off=0, s_off=0, offsets=None, dtype=None, o
     if out is None:
         out = torch.empty((rows, n), dtype=dtype or torch.float32, device=a.device)
     code, ld = _rows(out, "out", rows, n, dtype)
-    _enqueue((a, a_s, table, offsets, out), stream, lib().coli_mxfp4_matmul, a.data_ptr(),
+    _enqueue((a, a_s, table, offsets, out), stream, "coli_mxfp4_matmul", a.data_ptr(),
              a_s.data_ptr(), rows, K, off, E, table.data_ptr(), q_off, s_off, n, out.data_ptr(), code, ld)
     return out
 
@@ -634,14 +646,14 @@ def mxfp4_swiglu(a, a_s, table, inter, q_off=0, s_off=0, offsets=None, dtype=Non
     rows, K = _mx(a, a_s, "a")
     E, off = _groups(table, offsets)
     if dtype == "mxfp4" or isinstance(out, (tuple, list)):
-        q, s = _mx_out(*(out or (None, None)), rows, inter, a.device, "mxfp4_swiglu")
+        q, s = _mx_out(*(out or (None, None)), rows, inter, a, "mxfp4_swiglu")
         out, h, hs, code, ld = (q, s), q, s.data_ptr(), MXFP4, inter
     else:
         if out is None:
             out = torch.empty((rows, inter), dtype=dtype or torch.float32, device=a.device)
         code, ld = _rows(out, "out", rows, inter, dtype)
         h, hs, s = out, None, None
-    _enqueue((a, a_s, table, offsets, h, s), stream, lib().coli_mxfp4_swiglu, a.data_ptr(),
+    _enqueue((a, a_s, table, offsets, h, s), stream, "coli_mxfp4_swiglu", a.data_ptr(),
              a_s.data_ptr(), rows, K, off, E, table.data_ptr(), q_off, s_off, inter, h.data_ptr(), hs,
              code, ld)
     return out
@@ -662,7 +674,7 @@ def union_inverse(idx, E, stream=None):
     base = buf.data_ptr()
     at = [base + 4 * i for i in (0, E, 2 * E + 1, 2 * E + 1 + n, 3 * E + 1 + n, 3 * E + 2 + n,
                                  3 * E + 2 + 2 * n)]
-    _enqueue((idx, buf), stream, lib().coli_moe_union_inverse, idx.data_ptr(), T, k, E, *at[:6], at[6],
+    _enqueue((idx, buf), stream, "coli_moe_union_inverse", idx.data_ptr(), T, k, E, *at[:6], at[6],
              nb.value)
     return counts, offsets, perm, unique, n_unique, inv.view(T, k)
 
@@ -686,7 +698,7 @@ def dispatch(x, inv, out=None, stream=None):
     if out is None:
         out = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
     ld_out = _rows(out, "out", T * k, H, x.dtype)[1]
-    _enqueue((x, inv, out), stream, lib().coli_moe_dispatch, x.data_ptr(), code, T, k, H, ld,
+    _enqueue((x, inv, out), stream, "coli_moe_dispatch", x.data_ptr(), code, T, k, H, ld,
              inv.data_ptr(), out.data_ptr(), ld_out)
     return out
 
@@ -696,8 +708,8 @@ def dispatch_mxfp4(x, inv, q=None, s=None, stream=None):
     T, k = _slots(inv)
     code, ld = _rows(x, "x", T)
     H = x.shape[1]
-    q, s = _mx_out(q, s, T * k, H, x.device, "dispatch_mxfp4")
-    _enqueue((x, inv, q, s), stream, lib().coli_moe_dispatch_mxfp4, x.data_ptr(), code, T, k, H, ld,
+    q, s = _mx_out(q, s, T * k, H, x, "dispatch_mxfp4")
+    _enqueue((x, inv, q, s), stream, "coli_moe_dispatch_mxfp4", x.data_ptr(), code, T, k, H, ld,
              inv.data_ptr(), q.data_ptr(), s.data_ptr())
     return q, s
 
@@ -711,7 +723,7 @@ def dispatch_bwd(grad, inv, dtype=None, out=None, stream=None):
     if out is None:
         out = torch.empty((T, H), dtype=dtype or grad.dtype, device=grad.device)
     code, ld = _rows(out, "out", T, H, dtype)
-    _enqueue((grad, inv, out), stream, lib().coli_moe_dispatch_bwd, grad.data_ptr(), g_code, ld_g, T, k,
+    _enqueue((grad, inv, out), stream, "coli_moe_dispatch_bwd", grad.data_ptr(), g_code, ld_g, T, k,
              H, inv.data_ptr(), out.data_ptr(), code, ld)
     return out
 
@@ -728,7 +740,7 @@ def combine(rows, inv, w, shared=None, scale=1.0, dtype=None, out=None, stream=N
                           device=rows.device)
     code, ld = _rows(out, "out", T, H, dtype)
     ld_s = ld if shared is None else _rows(shared, "shared", T, H, out.dtype)[1]
-    _enqueue((rows, inv, w, shared, out), stream, lib().coli_moe_combine, rows.data_ptr(), r_code, ld_r,
+    _enqueue((rows, inv, w, shared, out), stream, "coli_moe_combine", rows.data_ptr(), r_code, ld_r,
              T, k, H, inv.data_ptr(), w.data_ptr(), None if shared is None else shared.data_ptr(), ld_s,
              scale, out.data_ptr(), code, ld)
     return out
@@ -748,7 +760,7 @@ def combine_bwd(grad, rows, inv, w, scale=1.0, rows_grad=None, w_grad=None, stre
         w_grad = torch.empty_like(w)
     _slots(inv, w_grad)
     ld_rg = _rows(rows_grad, "rows_grad", T * k, H, rows.dtype)[1]
-    _enqueue((grad, rows, inv, w, rows_grad, w_grad), stream, lib().coli_moe_combine_bwd,
+    _enqueue((grad, rows, inv, w, rows_grad, w_grad), stream, "coli_moe_combine_bwd",
              grad.data_ptr(), g_code, ld_g, rows.data_ptr(), r_code, ld_r, T, k, H, inv.data_ptr(),
              w.data_ptr(), scale, rows_grad.data_ptr(), ld_rg, w_grad.data_ptr())
     return rows_grad, w_grad

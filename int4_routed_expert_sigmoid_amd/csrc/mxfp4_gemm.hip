@@ -139,8 +139,6 @@ typedef __attribute__((address_space(1))) const uint8_t global_u8;
 typedef __attribute__((address_space(1))) const Bytes16 global_bytes16;
 
 __device__ __forceinline__ u32x4 load16(const uint8_t* p) { return *(global_u32x4*)(p); }
-// Matrix rows that one workgroup alone reads: kept out of the caches.
-__device__ __forceinline__ u32x4 load16_once(const uint8_t* p) { return __builtin_nontemporal_load((global_u32x4*)(p)); }
 __device__ __forceinline__ uint32_t load1(const uint8_t* p) { return *(global_u8*)(p); }
 
 __device__ __forceinline__ f32x4 mx_mfma(const u32x4& w, uint32_t ws, const u32x4& a, uint32_t as,
@@ -155,23 +153,10 @@ __device__ __forceinline__ f32x4 mx_mfma(const u32x4& w, uint32_t ws, const u32x
 constexpr int kChunkSteps = 4;
 constexpr int kChunkBlocks = 4 * kChunkSteps;          // 16 blocks: 512 columns
 
-// The scale bytes of blocks b0 .. b0 + 15 of a row in two steps, so that the
-// load can be on the way while other work runs: the 16 bytes from b0 on, or the
-// row's last 16 where fewer are left (no byte outside the row is touched; KB >=
-// 16), and then their shift into place, which leaves 0 (2^-127) for blocks from KB
-// on; their codes are 0 on one side of the product.
-__device__ __forceinline__ u32x4 load_scales16(const uint8_t* row, int b0, int KB) {
-    global_bytes16* v = (global_bytes16*)(row + min(b0, KB - 16));
+// Blocks b0 .. b0 + 15 of a row, all inside it.
+__device__ __forceinline__ u32x4 load_scales16(const uint8_t* row, int b0) {
+    global_bytes16* v = (global_bytes16*)(row + b0);
     return u32x4{v->w[0], v->w[1], v->w[2], v->w[3]};
-}
-
-__device__ __forceinline__ u32x4 place_scales16(const u32x4& v, int b0, int KB) {
-    const int sh = 8 * (b0 + 16 - KB);               // uniform
-    if (sh <= 0) return v;
-    const uint64_t lo = v.x | (uint64_t)v.y << 32, hi = v.z | (uint64_t)v.w << 32;
-    const uint64_t l = sh < 64 ? lo >> sh | hi << (64 - sh) : hi >> (sh - 64);
-    const uint64_t h = sh < 64 ? hi >> sh : 0;
-    return u32x4{(uint32_t)l, (uint32_t)(l >> 32), (uint32_t)h, (uint32_t)(h >> 32)};
 }
 
 // Everything above this point happens before everything below it: memory
@@ -224,9 +209,13 @@ __device__ __forceinline__ void store_mx(const MxGemmArgs& a, int m, int n0, int
 // Workgroup: NF fragments of 16 matrix rows by up to 16 rows. Its KS waves take
 // chunks of the columns in turn, so that even one row of one expert has KS
 // waves a fragment set on the way, and the partial sums meet in LDS in wave
-// order. Everything goes straight into the instruction's registers; a step's
-// registers are refilled for the wave's next chunk as soon as the step has
-// used them. Whole chunks only (TAIL false) or any number of columns.
+// order. Everything goes straight into the instruction's registers; those of two
+// steps, 128 bytes or one cache line of every row, are refilled together for
+// the wave's next chunk as soon as they are used. (Refilled step by step, the
+// second half of a line came after the line had left the caches: 1.33 times the
+// matrix' bytes from HBM, and 26-29 us in place of 22.6 for the SwiGLU of 8 rows
+// of 8 experts, K 6144, inter 2048.) Whole chunks only (TAIL false) or any number
+// of columns.
 template <typename Out, bool SWIGLU, int NF, int KS, bool TAIL>
 __global__ __launch_bounds__(64 * KS) void mx_few_rows_kernel(MxGemmArgs a, int NT) {
     __shared__ f32x4 part[KS][NF][64];
@@ -246,19 +235,23 @@ __global__ __launch_bounds__(64 * KS) void mx_few_rows_kernel(MxGemmArgs a, int 
     for (int f = 0; f < NF; ++f) nr[f] = min(f * kFrag + r, a.N - 1 - n_tile);
 
     u32x4 w[kChunkSteps][NF], av[kChunkSteps], ws[NF], as;
-    auto load_step = [&](int c, int s) {
-        int b = c * kChunkBlocks + s * 4 + g;
-        if (TAIL) b = min(b, KB - 1);
-        av[s] = load16(a_base + (mr * row_bytes + b * 16));
+    auto load_pair = [&](int c, int s) {
+        int b0 = c * kChunkBlocks + s * 4 + g, b1 = b0 + 4;
+        if (TAIL) b0 = min(b0, KB - 1), b1 = min(b1, KB - 1);
 #pragma unroll
-        for (int f = 0; f < NF; ++f) w[s][f] = load16_once(w_base + (nr[f] * row_bytes + b * 16));
+        for (int f = 0; f < NF; ++f) {
+            w[s][f] = load16(w_base + (nr[f] * row_bytes + b0 * 16));
+            w[s + 1][f] = load16(w_base + (nr[f] * row_bytes + b1 * 16));
+        }
+        av[s] = load16(a_base + (mr * row_bytes + b0 * 16));
+        av[s + 1] = load16(a_base + (mr * row_bytes + b1 * 16));
     };
     // a lane's scale byte of step s: byte g of word s
     auto load_scales = [&](int c) {
         if (!TAIL) {
-            as = load_scales16(as_base + mr * (uint32_t)KB, c * kChunkBlocks, KB);
+            as = load_scales16(as_base + mr * (uint32_t)KB, c * kChunkBlocks);
 #pragma unroll
-            for (int f = 0; f < NF; ++f) ws[f] = load_scales16(ws_base + nr[f] * (uint32_t)KB, c * kChunkBlocks, KB);
+            for (int f = 0; f < NF; ++f) ws[f] = load_scales16(ws_base + nr[f] * (uint32_t)KB, c * kChunkBlocks);
             return;
         }
 #pragma unroll
@@ -274,8 +267,8 @@ __global__ __launch_bounds__(64 * KS) void mx_few_rows_kernel(MxGemmArgs a, int 
     for (int f = 0; f < NF; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (wave < chunks) {
         load_scales(wave);
-#pragma unroll
-        for (int s = 0; s < kChunkSteps; ++s) load_step(wave, s);
+        load_pair(wave, 0);
+        load_pair(wave, 2);
     }
     for (int c = wave; c < chunks; c += KS) {
         const bool more = c + KS < chunks;
@@ -292,7 +285,7 @@ __global__ __launch_bounds__(64 * KS) void mx_few_rows_kernel(MxGemmArgs a, int 
 #pragma unroll
             for (int f = 0; f < NF; ++f) acc[f] = mx_mfma(w[s][f], ws_c[f][s] >> sh, x, as_c[s] >> sh, acc[f]);
             hold(acc);
-            if (more) load_step(c + KS, s);
+            if (more && s % 2 == 1) load_pair(c + KS, s - 1);
         }
     }
 #pragma unroll
@@ -340,137 +333,197 @@ __global__ __launch_bounds__(64 * KS) void mx_few_rows_kernel(MxGemmArgs a, int 
 // a chunk (16 KB a wave) is on the way all the time without a barrier. The rows
 // are shared by the waves and come (from L2) over LDS, two chunks deep, and so
 // do the scale bytes of both sides, which a wave then reads one per lane.
-constexpr int kWaveFrags = 4;
-constexpr int kTileWaves = 4;
-constexpr int kTileRows = kTileWaves * kWaveFrags * kFrag;   // 256 matrix rows
 
-// Position of 16-byte unit b of row r in the LDS chunk: the units of a row
-// are permuted by its number, so that the 16 rows that a load reads at one
+// Position of 16-byte unit b of row r in an LDS chunk of U units a row: the units
+// of a row are permuted by its number, so that the rows that a load reads at one
 // column fall into different banks.
-__device__ __forceinline__ int lds_unit(int r, int b) { return r * kChunkBlocks + (b ^ (r & 15)); }
+template <int U>
+__device__ __forceinline__ int lds_unit(int r, int b) { return r * U + (b ^ (r & (U - 1))); }
 
-template <int MT>
-struct TileLds {
-    u32x4 code[2][MT * kFrag * kChunkBlocks];
-    u32x4 scale[2][MT * kFrag];                // a row's 16 scale bytes
-    u32x4 w_scale[2][kTileRows];
+// BYTES (8 or 16) scale bytes.
+template <int BYTES>
+struct Scales {
+    uint32_t w[BYTES / 4];
 };
 
-template <typename Out, bool SWIGLU, int MT>
-__global__ __launch_bounds__(64 * kTileWaves, MT <= 4 ? 2 : 1) void mx_tile_kernel(MxGemmArgs a, int NT) {
-    constexpr int BM = MT * kFrag;
-    constexpr int kThreads = 64 * kTileWaves;
-    constexpr int kStage = BM * kChunkBlocks / kThreads;      // 16-byte units a thread stages
-    __shared__ TileLds<MT> lds;
-    Unit u;
-    if (!find_unit<BM>(a, NT, &u)) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
-    const int KB = a.K / kMxBlock, chunks = (KB + kChunkBlocks - 1) / kChunkBlocks;
-    const uint32_t row_bytes = KB * 16;
-    const int n_tile = u.nt * kTileRows, n_wave = n_tile + wave * kWaveFrags * kFrag;
-    // bases are uniform, lanes add 32-bit offsets
-    const uint8_t* w_base = u.blob + a.q_off + (int64_t)n_tile * row_bytes;
-    const uint8_t* ws_row = u.blob + a.s_off + (int64_t)min(n_tile + tid, a.N - 1) * KB;
-    const uint8_t* a_base = a.a + (int64_t)u.m0 * row_bytes;
-    const uint8_t* as_row = a.as + (int64_t)(u.m0 + min(tid, u.rows - 1)) * KB;
-    uint32_t w_off[kWaveFrags], s_off[kStage];
-#pragma unroll
-    for (int f = 0; f < kWaveFrags; ++f)
-        w_off[f] = (uint32_t)(min(n_wave + f * kFrag + r, a.N - 1) - n_tile) * row_bytes;
-#pragma unroll
-    for (int i = 0; i < kStage; ++i)
-        s_off[i] = (uint32_t)min((tid + i * kThreads) / kChunkBlocks, u.rows - 1) * row_bytes;
+// The scale bytes of blocks b0 .. b0 + BYTES - 1 of a row in two steps, so that the
+// load can be on the way while other work runs: the bytes from b0 on, or the row's
+// last BYTES where fewer are left (no byte outside the row is touched; KB >= 16),
+// and then their shift into place, which leaves 0 (2^-127) for blocks from KB on;
+// their codes are 0 on one side of the product.
+template <int BYTES>
+__device__ __forceinline__ Scales<BYTES> load_scales(const uint8_t* row, int b0, int KB) {
+    typedef __attribute__((address_space(1))) const Pack<uint8_t, BYTES> G;
+    G* p = (G*)(row + min(b0, KB - BYTES));
+    Scales<BYTES> v;
+    __builtin_memcpy(&v, p, BYTES);
+    return v;
+}
 
-    u32x4 stage[kStage], stage_s, stage_ws;
-    auto stage_load = [&](int c) {
-        const int b = c * kChunkBlocks + tid % kChunkBlocks, bc = min(b, KB - 1) * 16;
-#pragma unroll
-        for (int i = 0; i < kStage; ++i) stage[i] = load16(a_base + (s_off[i] + bc));
-        stage_ws = load_scales16(ws_row, c * kChunkBlocks, KB);
-        stage_s = load_scales16(as_row, c * kChunkBlocks, KB);
-    };
-    auto stage_store = [&](int c, int buf) {
-        const bool in = c * kChunkBlocks + tid % kChunkBlocks < KB;
-#pragma unroll
-        for (int i = 0; i < kStage; ++i) {
-            const int x = tid + i * kThreads;
-            lds.code[buf][lds_unit(x / kChunkBlocks, x % kChunkBlocks)] = in ? stage[i] : u32x4{0, 0, 0, 0};
-        }
-        lds.w_scale[buf][tid] = place_scales16(stage_ws, c * kChunkBlocks, KB);
-        if (tid < BM) lds.scale[buf][tid] = place_scales16(stage_s, c * kChunkBlocks, KB);
-    };
+template <int BYTES>
+__device__ __forceinline__ Scales<BYTES> place_scales(const Scales<BYTES>& v, int b0, int KB) {
+    const int sh = 8 * (b0 + BYTES - KB);            // uniform
+    if (sh <= 0) return v;
+    uint64_t lo = v.w[0] | (uint64_t)v.w[1] << 32, hi = 0;
+    if constexpr (BYTES == 16) hi = v.w[2] | (uint64_t)v.w[3] << 32;
+    const uint64_t l = sh < 64 ? lo >> sh | (hi << 1) << (63 - sh) : hi >> (sh - 64);
+    const uint64_t h = sh < 64 ? hi >> sh : 0;
+    Scales<BYTES> o;
+    o.w[0] = (uint32_t)l;
+    o.w[1] = (uint32_t)(l >> 32);
+    if constexpr (BYTES == 16) o.w[2] = (uint32_t)h, o.w[3] = (uint32_t)(h >> 32);
+    return o;
+}
 
-    u32x4 w[kChunkSteps][kWaveFrags];
-    auto w_load = [&](int c, int s) {
-        const uint32_t b = min(c * kChunkBlocks + s * 4 + g, KB - 1) * 16;
-#pragma unroll
-        for (int f = 0; f < kWaveFrags; ++f) w[s][f] = load16(w_base + (w_off[f] + b));
-    };
+template <int BM, int BN, int CS>
+struct TileLds {
+    u32x4 code[2][BM * 4 * CS];
+    Scales<4 * CS> scale[2][BM], w_scale[2][BN];
+};
 
-    f32x4 acc[kWaveFrags][MT];
-#pragma unroll
-    for (int f = 0; f < kWaveFrags; ++f)
-#pragma unroll
-        for (int i = 0; i < MT; ++i) acc[f][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+// WM x WN waves, each MT fragments of rows by NF fragments of matrix rows;
+// chunks of CS steps.
+template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int CS>
+struct Tile {
+    static constexpr int BM = WM * MT * kFrag, BN = WN * NF * kFrag, kThreads = 64 * WM * WN;
+    static constexpr int U = 4 * CS;                          // 16-byte units of a row's chunk
+    static_assert(BM <= kThreads && BN <= kThreads, "a thread stages one row's scales");
+    typedef TileLds<BM, BN, CS> Lds;
 
-    stage_load(0);
+    // L: the fragments of a wave that hold rows (all MT unless WM is 1).
+    template <int L>
+    static __device__ __forceinline__ void run(const MxGemmArgs& a, const Unit& u, Lds& lds) {
+        constexpr int LM = WM * L * kFrag;
+        constexpr int kStage = LM * U / kThreads;             // 16-byte units a thread stages
+        static_assert(LM * U % kThreads == 0, "whole units for every thread");
+        const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+        const int wn = (tid >> 6) % WN, wm = (tid >> 6) / WN;
+        const int KB = a.K / kMxBlock, chunks = (KB + U - 1) / U;
+        const uint32_t row_bytes = KB * 16;
+        const int n_tile = u.nt * BN, n_wave = n_tile + wn * NF * kFrag;
+        // bases are uniform, lanes add 32-bit offsets
+        const uint8_t* w_base = u.blob + a.q_off + (int64_t)n_tile * row_bytes;
+        const uint8_t* ws_row = u.blob + a.s_off + (int64_t)min(n_tile + tid, a.N - 1) * KB;
+        const uint8_t* a_base = a.a + (int64_t)u.m0 * row_bytes;
+        const uint8_t* as_row = a.as + (int64_t)(u.m0 + min(tid, u.rows - 1)) * KB;
+        uint32_t w_off[NF], s_off[kStage];
 #pragma unroll
-    for (int s = 0; s < kChunkSteps; ++s) w_load(0, s);
-    stage_store(0, 0);
-    __syncthreads();
-    for (int c = 0; c < chunks; ++c) {
-        const int buf = c & 1, next = min(c + 1, chunks - 1);
-        const uint8_t* as_b = (const uint8_t*)lds.scale[buf] + r * 16 + g;
-        const uint8_t* ws_b = (const uint8_t*)lds.w_scale[buf] + (wave * kWaveFrags * kFrag + r) * 16 + g;
-        stage_load(next);
+        for (int f = 0; f < NF; ++f)
+            w_off[f] = (uint32_t)(min(n_wave + f * kFrag + r, a.N - 1) - n_tile) * row_bytes;
 #pragma unroll
-        for (int s = 0; s < kChunkSteps; ++s) {
-            u32x4 av[MT];
-            uint32_t as[MT], ws[kWaveFrags];
+        for (int i = 0; i < kStage; ++i)
+            s_off[i] = (uint32_t)min((tid + i * kThreads) / U, u.rows - 1) * row_bytes;
+
+        u32x4 stage[kStage];
+        Scales<U> stage_s, stage_ws;
+        auto stage_load = [&](int c) {
+            const uint32_t b = min(c * U + tid % U, KB - 1) * 16;
 #pragma unroll
-            for (int f = 0; f < kWaveFrags; ++f) ws[f] = ws_b[f * kFrag * 16 + s * 4];
+            for (int i = 0; i < kStage; ++i) stage[i] = load16(a_base + (s_off[i] + b));
+            stage_ws = load_scales<U>(ws_row, c * U, KB);
+            stage_s = load_scales<U>(as_row, c * U, KB);
+        };
+        auto stage_store = [&](int c, int buf) {
+            const bool in = c * U + tid % U < KB;
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                as[i] = as_b[i * kFrag * 16 + s * 4];
-                av[i] = lds.code[buf][lds_unit(i * kFrag + r, s * 4 + g)];
+            for (int i = 0; i < kStage; ++i) {
+                const int x = tid + i * kThreads;
+                lds.code[buf][lds_unit<U>(x / U, x % U)] = in ? stage[i] : u32x4{0, 0, 0, 0};
             }
+            if (tid < BN) lds.w_scale[buf][tid] = place_scales<U>(stage_ws, c * U, KB);
+            if (tid < LM) lds.scale[buf][tid] = place_scales<U>(stage_s, c * U, KB);
+        };
+
+        u32x4 w[CS][NF];
+        auto w_pair = [&](int c, int s) {                     // steps s and s + 1: a cache line of every row
+            const int b = c * U + s * 4 + g;
+            const uint32_t b0 = min(b, KB - 1) * 16, b1 = min(b + 4, KB - 1) * 16;
 #pragma unroll
-            for (int f = 0; f < kWaveFrags; ++f)
+            for (int f = 0; f < NF; ++f) {
+                w[s][f] = load16(w_base + (w_off[f] + b0));
+                w[s + 1][f] = load16(w_base + (w_off[f] + b1));
+            }
+        };
+
+        f32x4 acc[NF][L];
 #pragma unroll
-                for (int i = 0; i < MT; ++i) acc[f][i] = mx_mfma(w[s][f], ws[f], av[i], as[i], acc[f][i]);
+        for (int f = 0; f < NF; ++f)
 #pragma unroll
-            for (int f = 0; f < kWaveFrags; ++f) hold(acc[f]);
-            w_load(next, s);
-            sched_fence();
-        }
-        stage_store(next, buf ^ 1);
+            for (int i = 0; i < L; ++i) acc[f][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+        stage_load(0);
+#pragma unroll
+        for (int s = 0; s < CS; s += 2) w_pair(0, s);
+        stage_store(0, 0);
         __syncthreads();
-    }
-    // outputs
+        const int m_wave = wm * L * kFrag + r;
+        for (int c = 0; c < chunks; ++c) {
+            const int buf = c & 1, next = min(c + 1, chunks - 1);
+            const uint8_t* as_b = (const uint8_t*)lds.scale[buf] + m_wave * U + g;
+            const uint8_t* ws_b = (const uint8_t*)lds.w_scale[buf] + (wn * NF * kFrag + r) * U + g;
+            stage_load(next);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const bool live = i * kFrag + r < u.rows;
-        const int m = u.m0 + i * kFrag + r;
-        if constexpr (!SWIGLU) {
+            for (int s = 0; s < CS; ++s) {
+                u32x4 av[L];
+                uint32_t as[L], ws[NF];
 #pragma unroll
-            for (int f = 0; f < kWaveFrags; ++f)
-                if (live) store4<Out>(a, m, n_wave + f * kFrag + 4 * g, a.N, acc[f][i]);
-        } else {
-            f32x4 h[2];
+                for (int f = 0; f < NF; ++f) ws[f] = ws_b[f * kFrag * U + s * 4];
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
+                for (int i = 0; i < L; ++i) {
+                    as[i] = as_b[i * kFrag * U + s * 4];
+                    av[i] = lds.code[buf][lds_unit<U>(m_wave + i * kFrag, s * 4 + g)];
+                }
 #pragma unroll
-                for (int x = 0; x < 4; ++x) h[p][x] = silu_mul(acc[2 * p][i][x], acc[2 * p + 1][i][x]);
-            const int n0 = n_wave / 2;
-            if constexpr (std::is_same<Out, MxOut>::value) {
-                store_mx(a, m, n0, a.N / 2, live && n0 < a.N / 2, h[0], h[1]);
+                for (int f = 0; f < NF; ++f)
+#pragma unroll
+                    for (int i = 0; i < L; ++i) acc[f][i] = mx_mfma(w[s][f], ws[f], av[i], as[i], acc[f][i]);
+#pragma unroll
+                for (int f = 0; f < NF; ++f) hold(acc[f]);
+                if (s % 2 == 1) w_pair(next, s - 1);
+                sched_fence();
+            }
+            stage_store(next, buf ^ 1);
+            __syncthreads();
+        }
+        // outputs
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            const bool live = m_wave + i * kFrag < u.rows;
+            const int m = u.m0 + m_wave + i * kFrag;
+            if constexpr (!SWIGLU) {
+#pragma unroll
+                for (int f = 0; f < NF; ++f)
+                    if (live) store4<Out>(a, m, n_wave + f * kFrag + 4 * g, a.N, acc[f][i]);
             } else {
+                f32x4 h[NF / 2];
 #pragma unroll
-                for (int p = 0; p < 2; ++p)
-                    if (live) store4<Out>(a, m, n0 + p * kFrag + 4 * g, a.N / 2, h[p]);
+                for (int p = 0; p < NF / 2; ++p)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) h[p][x] = silu_mul(acc[2 * p][i][x], acc[2 * p + 1][i][x]);
+                const int n0 = n_wave / 2;
+                if constexpr (std::is_same<Out, MxOut>::value) {
+                    static_assert(NF == 4, "a wave holds one block of h");
+                    store_mx(a, m, n0, a.N / 2, live && n0 < a.N / 2, h[0], h[1]);
+                } else {
+#pragma unroll
+                    for (int p = 0; p < NF / 2; ++p)
+                        if (live) store4<Out>(a, m, n0 + p * kFrag + 4 * g, a.N / 2, h[p]);
+                }
             }
         }
     }
+};
+
+template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int CS>
+__global__ __launch_bounds__(64 * WM * WN, 2) void mx_tile_kernel(MxGemmArgs a, int NT) {
+    typedef Tile<Out, SWIGLU, MT, NF, WM, WN, CS> T;
+    __shared__ typename T::Lds lds;
+    Unit u;
+    if (!find_unit<T::BM>(a, NT, &u)) return;
+    if constexpr (WM == 1 && MT >= 8) {
+        if (u.rows <= T::BM / 2) return T::template run<MT / 2>(a, u, lds);
+    }
+    T::template run<MT>(a, u, lds);
 }
 
 // Units of a launch at most: the rows fill rows / BM stretches, and each expert
@@ -497,12 +550,13 @@ coli_status few_rows(const MxGemmArgs& a, hipStream_t stream) {
     return COLI_OK;
 }
 
-template <typename Out, bool SWIGLU, int MT>
+template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int CS>
 coli_status tiles(const MxGemmArgs& a, hipStream_t stream) {
-    const int NT = (a.N + kTileRows - 1) / kTileRows;
+    typedef Tile<Out, SWIGLU, MT, NF, WM, WN, CS> T;
+    const int NT = (a.N + T::BN - 1) / T::BN;
     uint32_t grid;
-    if (coli_status st = grid_of(a, MT * kFrag, NT, 64 * kTileWaves, &grid)) return st;
-    launch(mx_tile_kernel<Out, SWIGLU, MT>, dim3(grid), dim3(64 * kTileWaves), 0, stream, a, NT);
+    if (coli_status st = grid_of(a, T::BM, NT, T::kThreads, &grid)) return st;
+    launch(mx_tile_kernel<Out, SWIGLU, MT, NF, WM, WN, CS>, dim3(grid), dim3(T::kThreads), 0, stream, a, NT);
     COLI_CHECK_LAUNCH("mxfp4 product kernel launch");
     return COLI_OK;
 }
@@ -511,9 +565,19 @@ template <typename Out, bool SWIGLU>
 coli_status product(const MxGemmArgs& a, hipStream_t stream) {
     constexpr bool mx = std::is_same<Out, MxOut>::value;
     const double per = (double)a.rows / (a.offsets ? std::min(a.E, a.rows) : 1);
-    if (per <= 8 || a.K < kChunkBlocks * kMxBlock) return few_rows<Out, SWIGLU, mx ? 4 : 2, 4>(a, stream);
-    if (per <= 128) return tiles<Out, SWIGLU, 4>(a, stream);
-    return tiles<Out, SWIGLU, 8>(a, stream);
+    if (per <= 8 || a.K < kChunkBlocks * kMxBlock) {
+        // a wave takes at least two chunks where there are that many: 11.4 us with 2
+        // waves against 13.3 with 4 for 8 rows of 8 experts at K 2048, N 6144 (4
+        // chunks), 22.6 with 4 against 23.7 with 2 at K 6144, inter 2048 (12)
+        if (a.K >= 8 * kChunkBlocks * kMxBlock) return few_rows<Out, SWIGLU, mx ? 4 : 2, 4>(a, stream);
+        return few_rows<Out, SWIGLU, mx ? 4 : 2, 2>(a, stream);
+    }
+    // 64-row tiles read the matrix once for the rows of most experts up to here:
+    // 637 against 710 us for 4072 rows over 256 experts (K 6144, inter 2048), 884
+    // against 833 us for 16384
+    if (per <= 32) return tiles<Out, SWIGLU, 4, 4, 1, 4, 4>(a, stream);
+    if constexpr (mx) return tiles<Out, SWIGLU, 8, 4, 1, 4, 2>(a, stream);
+    else return tiles<Out, SWIGLU, 8, 2, 1, 8, 4>(a, stream);
 }
 
 }  // namespace

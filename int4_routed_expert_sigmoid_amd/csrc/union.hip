@@ -4,14 +4,17 @@
 //
 // Three passes over slabs of 1024 assignments, deterministic throughout:
 //  1. per slab (one workgroup, 16 waves of 64): lanes holding the same expert
-//     are found with ballots (one round per distinct expert in the wave),
-//     which gives each assignment its rank among equal experts of its wave and
-//     the wave's per-expert count; an exclusive scan over the 16 waves (in
-//     order) turns that into the rank inside the slab and the slab's count;
+//     are found with one ballot per bit of the expert number, which gives each
+//     assignment its rank among equal experts of its wave and the wave's
+//     per-expert count; an exclusive scan over the 16 waves (in order) turns
+//     that into the rank inside the slab and the slab's count;
 //  2. one workgroup: per expert, an exclusive scan of the slab counts (in slab
 //     order), the expert's total, then offsets (exclusive scan over experts)
 //     and the unique list;
 //  3. per slab: perm[offsets[e] + slab_prefix[s][e] + rank] = a.
+// Up to kFusedSlabs slabs every workgroup of the third pass does the second for
+// itself (S loads a thread, which cost less than the launch between them); one
+// slab alone, where the inverse is wanted too, takes one launch.
 // The result is the stable counting sort of the assignments by expert.
 #include <algorithm>
 
@@ -23,8 +26,9 @@ namespace {
 constexpr int kUnionThreads = 1024;
 constexpr int kSlab = kUnionThreads;           // assignments per slab
 constexpr int kSlabWaves = kSlab / 64;
-// Experts whose per-wave counts and the scan's 16 words fit 64 KiB of LDS.
+// Experts whose per-wave counts and the scan's 16 sums fit 64 KiB of LDS.
 constexpr int kSmallExperts = 65536 / (4 * kSlabWaves) - 16;
+constexpr int kFusedSlabs = 64;
 
 __device__ __forceinline__ int block_exclusive_scan(int v, int* sh, int* total) {
     // Hillis-Steele over 1024 threads; sh has 1024 ints.
@@ -48,9 +52,42 @@ __device__ __forceinline__ int valid_expert(const int32_t* idx, int a, int n, in
     return (e >= 0 && e < E) ? e : -1;           // out-of-range entries are skipped
 }
 
+// The lanes of the wave that hold the same expert (bits: of the largest expert
+// number); 0 for a lane without one.
+__device__ __forceinline__ unsigned long long same_expert(int e, int bits) {
+    unsigned long long m = __ballot(e >= 0);
+    for (int b = 0; b < bits; ++b) {
+        const unsigned long long on = __ballot((e >> b) & 1);
+        m &= (e >> b) & 1 ? on : ~on;
+    }
+    return e >= 0 ? m : 0;
+}
+
+// Exclusive scan over the workgroup of counts (low half) and flags (high half):
+// within the waves by shuffles, over the 16 waves in order.
+__device__ __forceinline__ uint64_t block_scan2(uint64_t own, uint64_t* s_wave, uint64_t* total) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint64_t incl = own;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const uint64_t v = __shfl_up((unsigned long long)incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 63) s_wave[wave] = incl;
+    __syncthreads();
+    uint64_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kSlabWaves; ++w) {
+        before += w < wave ? s_wave[w] : 0;
+        all += s_wave[w];
+    }
+    *total = all;
+    return before + incl - own;
+}
+
 // Pass 1. Dynamic LDS: kSlabWaves * E ints.
 __global__ __launch_bounds__(kUnionThreads) void union_count_kernel(
-    const int32_t* __restrict__ idx, int n, int E, int32_t* __restrict__ slab_cnt /* [S][E] */,
+    const int32_t* __restrict__ idx, int n, int E, int bits, int32_t* __restrict__ slab_cnt /* [S][E] */,
     int32_t* __restrict__ rank /* [n] */) {
     extern __shared__ int s_cnt[];               // [wave][E]: counts, then exclusive prefixes
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
@@ -58,16 +95,9 @@ __global__ __launch_bounds__(kUnionThreads) void union_count_kernel(
     __syncthreads();
     const int a = blockIdx.x * kSlab + t;
     const int e = valid_expert(idx, a, n, E);
-    int r = 0;
-    unsigned long long active = __ballot(e >= 0);
-    while (active) {
-        const int leader = __ffsll((long long)active) - 1;
-        const int v = __shfl(e, leader);
-        const unsigned long long m = __ballot(e == v) & active;
-        if (e == v) r = __popcll(m & ((1ull << lane) - 1ull));
-        if (lane == leader) s_cnt[wave * E + v] = __popcll(m);
-        active &= ~m;
-    }
+    const unsigned long long m = same_expert(e, bits);
+    const int r = __popcll(m & ((1ull << lane) - 1ull));
+    if (e >= 0 && r == 0) s_cnt[wave * E + e] = __popcll(m);
     __syncthreads();
     for (int x = t; x < E; x += kUnionThreads) {
         int c = 0;
@@ -135,30 +165,71 @@ __global__ __launch_bounds__(kUnionThreads) void union_scatter_kernel(
     if (inv != nullptr) inv[a] = at;
 }
 
+// Passes 2 and 3 for at most kFusedSlabs slabs: every workgroup sums the slabs'
+// counts (its own slab's prefix among them), the first one writes the results
+// of pass 2.
+__global__ __launch_bounds__(kUnionThreads) void union_scan_scatter_kernel(
+    const int32_t* __restrict__ idx, int n, int S, int E, const int32_t* __restrict__ slab_cnt,
+    const int32_t* __restrict__ rank, int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
+    int32_t* __restrict__ perm, int32_t* __restrict__ unique, int32_t* __restrict__ n_unique,
+    int32_t* __restrict__ inv /* [n] or nullptr */) {
+    __shared__ int s_at[kUnionThreads];
+    __shared__ uint64_t s_wave[kSlabWaves];
+    const int t = threadIdx.x, slab = blockIdx.x;
+    const int a = slab * kSlab + t;
+    const int e = valid_expert(idx, a, n, E);
+    const int r = e >= 0 ? rank[a] : 0;
+    int cnt = 0, prefix = 0;
+    if (t < E) {
+        for (int s = 0; s < S; s += 8) {
+            int v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = s + j < S ? slab_cnt[(int64_t)(s + j) * E + t] : 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (s + j < slab) prefix += v[j];
+                cnt += v[j];
+            }
+        }
+    }
+    uint64_t total;
+    const uint64_t excl = block_scan2(cnt | (uint64_t)(cnt > 0) << 32, s_wave, &total);
+    s_at[t] = (int)excl + prefix;
+    if (slab == 0) {
+        if (t < E) {
+            counts[t] = cnt;
+            offsets[t] = (int)excl;
+            if (cnt > 0) unique[excl >> 32] = t;
+        }
+        if (t == 0) {
+            offsets[E] = (int)total;
+            *n_unique = (int)(total >> 32);
+        }
+    }
+    __syncthreads();
+    if (e >= 0) {
+        perm[s_at[e] + r] = a;
+        if (inv != nullptr) inv[a] = s_at[e] + r;
+    } else if (inv != nullptr && a < n) {
+        inv[a] = -1;
+    }
+}
+
 // All three passes and the inverse for at most one slab, in one workgroup: the
-// counts stay in LDS, and one scan over the experts carries both the counts
-// (low half) and the number of experts used (high half; both at most 1024).
-// Dynamic LDS: kSlabWaves * E ints.
+// counts stay in LDS. Dynamic LDS: kSlabWaves * E ints.
 __global__ __launch_bounds__(kUnionThreads) void union_small_kernel(
-    const int32_t* __restrict__ idx, int n, int E, int32_t* __restrict__ counts,
+    const int32_t* __restrict__ idx, int n, int E, int bits, int32_t* __restrict__ counts,
     int32_t* __restrict__ offsets, int32_t* __restrict__ perm, int32_t* __restrict__ unique,
     int32_t* __restrict__ n_unique, int32_t* __restrict__ inv) {
     extern __shared__ int s_cnt[];               // [wave][E]: counts, then exclusive prefixes
-    __shared__ int s_wave[kSlabWaves];
+    __shared__ uint64_t s_wave[kSlabWaves];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int e = valid_expert(idx, t, n, E);
     for (int i = t; i < kSlabWaves * E; i += kUnionThreads) s_cnt[i] = 0;
     __syncthreads();
-    int r = 0;
-    unsigned long long active = __ballot(e >= 0);
-    while (active) {
-        const int leader = __ffsll((long long)active) - 1;
-        const int v = __shfl(e, leader);
-        const unsigned long long m = __ballot(e == v) & active;
-        if (e == v) r = __popcll(m & ((1ull << lane) - 1ull));
-        if (lane == leader) s_cnt[wave * E + v] = __popcll(m);
-        active &= ~m;
-    }
+    const unsigned long long m = same_expert(e, bits);
+    const int r = __popcll(m & ((1ull << lane) - 1ull));
+    if (e >= 0 && r == 0) s_cnt[wave * E + e] = __popcll(m);
     __syncthreads();
     int cnt = 0;
     if (t < E) {
@@ -170,32 +241,18 @@ __global__ __launch_bounds__(kUnionThreads) void union_small_kernel(
         }
         counts[t] = cnt;
     }
-    const int own = cnt | (cnt > 0 ? 1 << 16 : 0);
-    int incl = own;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int v = __shfl_up(incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 63) s_wave[wave] = incl;
-    __syncthreads();
-    int before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kSlabWaves; ++w) {
-        before += w < wave ? s_wave[w] : 0;
-        total += s_wave[w];
-    }
-    const int excl = before + incl - own;
+    uint64_t total;
+    const uint64_t excl = block_scan2(t < E ? cnt | (uint64_t)(cnt > 0) << 32 : 0, s_wave, &total);
     if (t < E) {
-        const int off = excl & 0xffff;
+        const int off = (int)excl;
         offsets[t] = off;
 #pragma unroll
         for (int w = 0; w < kSlabWaves; ++w) s_cnt[w * E + t] += off;
-        if (cnt > 0) unique[excl >> 16] = t;
+        if (cnt > 0) unique[excl >> 32] = t;
     }
     if (t == 0) {
-        offsets[E] = total & 0xffff;
-        *n_unique = total >> 16;
+        offsets[E] = (int)total;
+        *n_unique = (int)(total >> 32);
     }
     __syncthreads();
     if (e >= 0) {
@@ -284,9 +341,11 @@ coli_status launch_union(const int32_t* idx, int32_t T, int32_t k, int32_t E, in
                          int32_t* offsets, int32_t* perm, int32_t* unique, int32_t* n_unique,
                          void* ws, hipStream_t stream, int32_t* inv) {
     const int n = T * k;
+    int bits = 0;
+    while (1 << bits < E) ++bits;
     if (inv != nullptr && n <= kSlab && E <= kSmallExperts) {
         launch(union_small_kernel, dim3(1), dim3(kUnionThreads),
-               (size_t)kSlabWaves * E * 4, stream, idx, n, E, counts, offsets, perm, unique,
+               (size_t)kSlabWaves * E * 4, stream, idx, n, E, bits, counts, offsets, perm, unique,
                n_unique, inv);
         COLI_CHECK_LAUNCH("union small kernel launch");
         return COLI_OK;
@@ -296,8 +355,15 @@ coli_status launch_union(const int32_t* idx, int32_t T, int32_t k, int32_t E, in
     int32_t* rank = (int32_t*)((char*)ws + align256((size_t)S * E * 4));
     if (S > 0) {
         launch(union_count_kernel, dim3(S), dim3(kUnionThreads), (size_t)kSlabWaves * E * 4, stream,
-               idx, n, E, slab_cnt, rank);
+               idx, n, E, bits, slab_cnt, rank);
         COLI_CHECK_LAUNCH("union count kernel launch");
+    }
+    if (S > 0 && S <= kFusedSlabs) {
+        launch(union_scan_scatter_kernel, dim3(S), dim3(kUnionThreads), 0, stream, idx, n, S, E,
+               (const int32_t*)slab_cnt, (const int32_t*)rank, counts, offsets, perm, unique,
+               n_unique, inv);
+        COLI_CHECK_LAUNCH("union scan and scatter kernel launch");
+        return COLI_OK;
     }
     launch(union_scan_kernel, dim3(1), dim3(kUnionThreads), 0, stream, S, E, slab_cnt, counts,
            offsets, unique, n_unique);

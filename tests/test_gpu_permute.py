@@ -74,7 +74,7 @@ def test_union_inverse(coli, T, k, E, drop):
 # T, k, E, H, share of slots without a row, row padding
 CASES = [(1, 1, 1, 1, 0, 0), (1, 8, 16, 6144, 0, 0), (3, 2, 4, 7, 0.4, 0), (5, 3, 4, 33, 0.5, 3), (2, 4, 5, 64, 1.0, 0),
          (17, 5, 9, 2049, 0.2, 0), (40, 8, 32, 256, 0.1, 8), (9, 11, 16, 1000, 0.3, 1), (700, 4, 60, 96, 0.2, 0),
-         (6, 32, 40, 4104, 0.2, 0)]
+         (6, 32, 40, 4104, 0.2, 0), (11, 3, 6, 1002, 0.2, 0), (13, 6, 8, 514, 0.1, 2)]
 
 
 def _setup(rng, T, k, E, H, drop, pad, dtype, n_mats):
