@@ -32,65 +32,62 @@ __device__ __forceinline__ int64_t slot_row(const int32_t* inv, int64_t at, int6
     return p >= 0 && p < n ? p : -1;
 }
 
-// A thread's V columns of a workgroup's stretch of kThreads * V, from first_col on:
-// neighbours (WIDE: 16-byte accesses), or every kThreads-th one. Stores that
-// cross a 16-byte boundary are slow (2557 rows of 2049 f32: 19.5 us in 16-byte
-// stores, 8.6 in 4-byte ones), so rows that do not start on one are written
-// column by column, a wave's neighbours next to each other.
-template <int V, bool WIDE>
-__device__ __forceinline__ int first_col(int stretch) {
-    return stretch * kThreads * V + (WIDE ? (int)threadIdx.x * V : (int)threadIdx.x);
-}
-
-// The columns from c on (0 from H on).
-template <int V, bool WIDE, typename T>
+// The V columns from c on. FULL: all are below H, one access (wherever the row
+// starts: see Pack); otherwise one by one, columns from H on as 0, loaded from
+// the last column so that the loads need no branch and stay in flight together.
+template <int V, bool FULL, typename T>
 __device__ __forceinline__ void load_cols(const T* row, int c, int H, float (&v)[V]) {
-    if (WIDE && c + V <= H) {
+    if constexpr (FULL) {
         load_f32<T, V>(row + c, v);
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int x = c + (WIDE ? i : i * kThreads);
-        v[i] = x < H ? (float)row[x] : 0.f;
+        for (int i = 0; i < V; ++i) {
+            const float f = (float)row[min(c + i, H - 1)];
+            v[i] = c + i < H ? f : 0.f;
+        }
     }
 }
 
-template <int V, bool WIDE, typename T>
+template <int V, bool FULL, typename T>
 __device__ __forceinline__ void store_cols(T* row, int c, int H, const float (&v)[V]) {
-    if (WIDE && c + V <= H) {
+    if constexpr (FULL) {
         store_f32<T, V>(row + c, v);
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int x = c + (WIDE ? i : i * kThreads);
-        if (x < H) row[x] = (T)v[i];
+        for (int i = 0; i < V; ++i)
+            if (c + i < H) row[c + i] = (T)v[i];
     }
 }
 
 // ------------------------------------------------------------ dispatch
-// Workgroup (token, stretch of kThreads * PER units): rows of `units` units, the
-// widest type that divides both rows' starts and length. The copy keeps every
-// bit.
-template <typename U, int PER>
-__global__ __launch_bounds__(kThreads) void dispatch_kernel(const U* __restrict__ x, int64_t ld_x,
-                                                            int k, int units, int64_t n, int tiles,
+// Workgroup (token, stretch of kThreads * kVec columns). T is any type of the
+// element's size: the copy keeps every bit.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void dispatch_kernel(const T* __restrict__ x, int64_t ld_x,
+                                                            int k, int H, int64_t n, int tiles,
                                                             const int32_t* __restrict__ inv,
-                                                            U* __restrict__ rows, int64_t ld_rows) {
+                                                            T* __restrict__ rows, int64_t ld_rows) {
+    constexpr int V = kVec<T>;
     const int64_t t = blockIdx.x / (uint32_t)tiles;
-    const int c = (blockIdx.x % (uint32_t)tiles) * kThreads * PER + threadIdx.x;
-    U v[PER];
+    const int c = ((blockIdx.x % (uint32_t)tiles) * kThreads + threadIdx.x) * V;
+    const T* src = x + t * ld_x;
+    if (c + V <= H) {
+        const Pack<T, V> v = *reinterpret_cast<const Pack<T, V>*>(src + c);
+        for (int j = 0; j < k; ++j) {
+            const int64_t p = slot_row(inv, t * k + j, n);
+            if (p >= 0) *reinterpret_cast<Pack<T, V>*>(rows + p * ld_rows + c) = v;
+        }
+    } else if (c < H) {
+        T v[V];
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (c + i * kThreads < units) v[i] = x[t * ld_x + c + i * kThreads];
-    for (int j = 0; j < k; ++j) {
-        const int64_t p = slot_row(inv, t * k + j, n);
-        if (p < 0) continue;
-        U* dst = rows + p * ld_rows + c;
+        for (int i = 0; i < V; ++i) v[i] = src[min(c + i, H - 1)];
+        for (int j = 0; j < k; ++j) {
+            const int64_t p = slot_row(inv, t * k + j, n);
+            if (p < 0) continue;
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (c + i * kThreads < units) dst[i * kThreads] = v[i];
+            for (int i = 0; i < V; ++i)
+                if (c + i < H) rows[p * ld_rows + c + i] = v[i];
+        }
     }
 }
 
@@ -125,48 +122,53 @@ __global__ __launch_bounds__(kThreads) void dispatch_mxfp4_kernel(
 // groups of G whose rows are all loaded before the first is added; a slot
 // without a row re-reads the token's first row (in cache by then) and adds
 // nothing, so that the loads need no branch.
-template <typename Tin, typename Tout, int G, bool WIDE>
+template <typename Tin, typename Tout, int G>
 __global__ __launch_bounds__(kThreads) void gather_sum_kernel(
     const Tin* __restrict__ rows, int64_t ld_rows, int k, int H, int64_t n, int tiles,
     const int32_t* __restrict__ inv, const float* __restrict__ w, const Tout* shared,
     int64_t ld_shared, float scale, Tout* y, int64_t ld_y) {
     constexpr int V = kVec<Tin>;
     const int64_t t = blockIdx.x / (uint32_t)tiles;
-    const int c = first_col<V, WIDE>(blockIdx.x % (uint32_t)tiles);
+    const int c = ((blockIdx.x % (uint32_t)tiles) * kThreads + threadIdx.x) * V;
     if (c >= H) return;
     int64_t first = -1;
     for (int j = 0; j < k && first < 0; ++j) first = slot_row(inv, t * k + j, n);
-    float acc[V], sh[V];
+    auto sum = [&](auto full) {
+        constexpr bool FULL = decltype(full)::value;
+        float acc[V], sh[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = sh[i] = 0.f;
-    if (shared) load_cols<V, WIDE>(shared + t * ld_shared, c, H, sh);
-    if (first >= 0) {
-        for (int j0 = 0; j0 < k; j0 += G) {
-            float v[G][V], wj[G];
-            bool on[G];
+        for (int i = 0; i < V; ++i) acc[i] = sh[i] = 0.f;
+        if (shared) load_cols<V, FULL>(shared + t * ld_shared, c, H, sh);
+        if (first >= 0) {
+            for (int j0 = 0; j0 < k; j0 += G) {
+                float v[G][V], wj[G];
+                bool on[G];
 #pragma unroll
-            for (int j = 0; j < G; ++j) {
-                const int64_t p = j0 + j < k ? slot_row(inv, t * k + j0 + j, n) : -1;
-                on[j] = p >= 0;
-                wj[j] = on[j] && w ? w[t * k + j0 + j] : 1.f;
-                load_cols<V, WIDE>(rows + (on[j] ? p : first) * ld_rows, c, H, v[j]);
+                for (int j = 0; j < G; ++j) {
+                    const int64_t p = j0 + j < k ? slot_row(inv, t * k + j0 + j, n) : -1;
+                    on[j] = p >= 0;
+                    wj[j] = on[j] && w ? w[t * k + j0 + j] : 1.f;
+                    load_cols<V, FULL>(rows + (on[j] ? p : first) * ld_rows, c, H, v[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < G; ++j)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) acc[i] = on[j] ? fmaf(wj[j], v[j][i], acc[i]) : acc[i];
             }
-#pragma unroll
-            for (int j = 0; j < G; ++j)
-#pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] = on[j] ? fmaf(wj[j], v[j][i], acc[i]) : acc[i];
         }
-    }
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = fmaf(scale, acc[i], sh[i]);
-    store_cols<V, WIDE>(y + t * ld_y, c, H, acc);
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(scale, acc[i], sh[i]);
+        store_cols<V, FULL>(y + t * ld_y, c, H, acc);
+    };
+    if (c + V <= H) sum(std::true_type{});
+    else sum(std::false_type{});
 }
 
 // ------------------------------------------------------------ combine backward
 // Workgroup (token, group of up to G of its slots): one pass over H with the
 // group's dot products in registers, then one reduction over the workgroup
 // (lanes, then waves in order).
-template <typename Td, typename Tr, int G, bool WIDE>
+template <typename Td, typename Tr, int G>
 __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(
     const Td* __restrict__ dy, int64_t ld_dy, const Tr* __restrict__ rows, int64_t ld_rows, int k,
     int H, int64_t n, int groups, const int32_t* __restrict__ inv, const float* __restrict__ w,
@@ -183,21 +185,26 @@ __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(
         wj[j] = p[j] >= 0 ? scale * w[t * k + j0 + j] : 0.f;
         dot[j] = 0.f;
     }
-    for (int c = first_col<V, WIDE>(0); c < H; c += kThreads * V) {
+    auto columns = [&](auto full, int c) {
+        constexpr bool FULL = decltype(full)::value;
         float g[V];
-        load_cols<V, WIDE>(dy + t * ld_dy, c, H, g);
+        load_cols<V, FULL>(dy + t * ld_dy, c, H, g);
 #pragma unroll
         for (int j = 0; j < G; ++j) {
-            if (p[j] < 0) continue;
+            if (p[j] < 0) continue;               // uniform
             float v[V], out[V];
-            load_cols<V, WIDE>(rows + p[j] * ld_rows, c, H, v);
+            load_cols<V, FULL>(rows + p[j] * ld_rows, c, H, v);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 dot[j] = fmaf(g[i], v[i], dot[j]);
                 out[i] = wj[j] * g[i];
             }
-            store_cols<V, WIDE>(drows + p[j] * ld_drows, c, H, out);
+            store_cols<V, FULL>(drows + p[j] * ld_drows, c, H, out);
         }
+    };
+    for (int c = threadIdx.x * V; c < H; c += kThreads * V) {
+        if (c + V <= H) columns(std::true_type{}, c);
+        else columns(std::false_type{}, c);
     }
 #pragma unroll
     for (int j = 0; j < G; ++j) {
@@ -225,37 +232,23 @@ coli_status grid_of(int64_t T, int64_t per, uint32_t* grid) {
 
 int tiles_of(int H, int vec) { return (H + kThreads * vec - 1) / (kThreads * vec); }
 
-// Whether every row of the buffer starts on a multiple of `bytes`.
-bool rows_aligned(const void* p, int64_t ld, int elem, int bytes) {
-    return (uintptr_t)p % bytes == 0 && ld * elem % bytes == 0;
-}
-
-template <typename U, int PER>
-coli_status dispatch_as(const void* x, int es, int32_t T, int32_t k, int32_t H, int64_t ld_x,
-                        const int32_t* inv, void* rows, int64_t ld_rows, hipStream_t stream) {
-    const int units = (int)((int64_t)H * es / (int)sizeof(U)), tiles = tiles_of(units, PER);
-    uint32_t grid;
-    if (coli_status st = grid_of(T, tiles, &grid)) return st;
-    launch(dispatch_kernel<U, PER>, dim3(grid), dim3(kThreads), 0, stream, (const U*)x,
-           ld_x * es / (int)sizeof(U), k, units, (int64_t)T * k, tiles, inv, (U*)rows,
-           ld_rows * es / (int)sizeof(U));
-    COLI_CHECK_LAUNCH("dispatch kernel launch");
-    return COLI_OK;
-}
-
 }  // namespace
 
 coli_status launch_dispatch(const void* x, int32_t dtype, int32_t T, int32_t k, int32_t H,
                             int64_t ld_x, const int32_t* inv, void* rows, int64_t ld_rows,
                             hipStream_t stream) {
-    const int es = elem_bytes(dtype);
-    auto whole = [&](int bytes) {
-        return rows_aligned(x, ld_x, es, bytes) && rows_aligned(rows, ld_rows, es, bytes) &&
-               (int64_t)H * es % bytes == 0;
-    };
-    if (whole(16)) return dispatch_as<u32x4, 1>(x, es, T, k, H, ld_x, inv, rows, ld_rows, stream);
-    if (whole(4)) return dispatch_as<uint32_t, 4>(x, es, T, k, H, ld_x, inv, rows, ld_rows, stream);
-    return dispatch_as<uint16_t, 8>(x, es, T, k, H, ld_x, inv, rows, ld_rows, stream);
+    const int64_t n = (int64_t)T * k;
+    const int tiles = tiles_of(H, 16 / elem_bytes(dtype));
+    uint32_t grid;
+    if (coli_status st = grid_of(T, tiles, &grid)) return st;
+    if (elem_bytes(dtype) == 4)
+        launch(dispatch_kernel<uint32_t>, dim3(grid), dim3(kThreads), 0, stream, (const uint32_t*)x,
+               ld_x, k, H, n, tiles, inv, (uint32_t*)rows, ld_rows);
+    else
+        launch(dispatch_kernel<uint16_t>, dim3(grid), dim3(kThreads), 0, stream, (const uint16_t*)x,
+               ld_x, k, H, n, tiles, inv, (uint16_t*)rows, ld_rows);
+    COLI_CHECK_LAUNCH("dispatch kernel launch");
+    return COLI_OK;
 }
 
 coli_status launch_dispatch_mxfp4(const void* x, int32_t dtype, int32_t T, int32_t k, int32_t H,
@@ -290,10 +283,7 @@ static coli_status gather_sum(const void* rows, int32_t rows_dtype, int64_t ld_r
                 launch(kernel, dim3(grid), dim3(kThreads), 0, stream, (const Tin*)rows, ld_rows, k, H,
                        n, tiles, inv, w, (const Tout*)shared, ld_shared, scale, (Tout*)y, ld_y);
             };
-            if (rows_aligned(y, ld_y, sizeof(Tout), 16))
-                k > 4 ? go(gather_sum_kernel<Tin, Tout, 8, true>) : go(gather_sum_kernel<Tin, Tout, 4, true>);
-            else
-                go(gather_sum_kernel<Tin, Tout, 4, false>);
+            k > 4 ? go(gather_sum_kernel<Tin, Tout, 8>) : go(gather_sum_kernel<Tin, Tout, 4>);
             COLI_CHECK_LAUNCH("gather_sum kernel launch");
             return COLI_OK;
         });
@@ -327,13 +317,9 @@ coli_status launch_combine_bwd(const void* dy, int32_t dy_dtype, int64_t ld_dy, 
         using Td = decltype(e);
         return with_elem(rows_dtype, [&](auto f) -> coli_status {
             using Tr = decltype(f);
-            auto go = [&](auto kernel) {
-                launch(kernel, dim3(grid), dim3(kThreads), 0, stream, (const Td*)dy, ld_dy,
-                       (const Tr*)rows, ld_rows, k, H, n, groups, inv, w, scale, (Tr*)drows, ld_drows,
-                       dw);
-            };
-            rows_aligned(drows, ld_drows, sizeof(Tr), 16) ? go(combine_bwd_kernel<Td, Tr, G, true>)
-                                                          : go(combine_bwd_kernel<Td, Tr, G, false>);
+            launch(combine_bwd_kernel<Td, Tr, G>, dim3(grid), dim3(kThreads), 0, stream,
+                   (const Td*)dy, ld_dy, (const Tr*)rows, ld_rows, k, H, n, groups, inv, w, scale,
+                   (Tr*)drows, ld_drows, dw);
             COLI_CHECK_LAUNCH("combine_bwd kernel launch");
             return COLI_OK;
         });
