@@ -9,6 +9,7 @@
 // + 3 of one row m = l % 16, which is one wide store. Products are exact and
 // sums are f32.
 #include <algorithm>
+#include <cmath>
 
 #include "mxfp4.h"
 
@@ -22,6 +23,7 @@ constexpr int kFrag = 16;                    // rows of one operand of the instr
 constexpr int kStep = 128;                   // columns of one instruction
 constexpr int kStepBytes = kStep / 2;
 constexpr int kXcds = 8;
+constexpr uint32_t kCus = 256;
 
 // MXFP4 as an output type of the SwiGLU epilogue.
 struct MxOut {};
@@ -325,6 +327,40 @@ __global__ __launch_bounds__(64 * KS) void mx_few_rows_kernel(MxGemmArgs a, int 
     }
 }
 
+// ------------------------------------------------------------ a tile's outputs
+// A wave's outputs: L fragments of rows, STEP fragments apart (this lane's row of
+// the first one: m_wave of the unit), by NF fragments of matrix rows from n_wave on.
+template <typename Out, bool SWIGLU, int NF, int L, int STEP>
+__device__ __forceinline__ void write_tile(const MxGemmArgs& a, int m0, int rows, int m_wave, int n_wave,
+                                           const f32x4 (&acc)[L][NF]) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        const int at = m_wave + i * STEP * kFrag, m = m0 + at;
+        const bool live = at < rows;
+        if constexpr (!SWIGLU) {
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+                if (live) store4<Out>(a, m, n_wave + f * kFrag + 4 * g, a.N, acc[i][f]);
+        } else {
+            f32x4 h[NF / 2];
+#pragma unroll
+            for (int p = 0; p < NF / 2; ++p)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) h[p][x] = silu_mul(acc[i][2 * p][x], acc[i][2 * p + 1][x]);
+            const int n0 = n_wave / 2;
+            if constexpr (std::is_same<Out, MxOut>::value) {
+                static_assert(NF == 4, "a wave holds one block of h");
+                store_mx(a, m, n0, a.N / 2, live && n0 < a.N / 2, h[0], h[1]);
+            } else {
+#pragma unroll
+                for (int p = 0; p < NF / 2; ++p)
+                    if (live) store4<Out>(a, m, n0 + p * kFrag + 4 * g, a.N / 2, h[p]);
+            }
+        }
+    }
+}
+
 // ------------------------------------------------------------ many rows
 // Workgroup: 4 waves, each 64 matrix rows (4 fragments) by MT fragments of 16
 // rows. The matrix is the operand that has to come from HBM: each wave loads
@@ -381,23 +417,23 @@ struct TileLds {
     Scales<4 * CS> scale[2][BM], w_scale[2][BN];
 };
 
-// WM x WN waves, each MT fragments of rows by NF fragments of matrix rows;
-// chunks of CS steps.
-template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int CS>
+// WN waves, each MT fragments of rows by NF fragments of matrix rows; chunks of
+// CS steps.
+template <typename Out, bool SWIGLU, int MT, int NF, int WN, int CS>
 struct Tile {
-    static constexpr int BM = WM * MT * kFrag, BN = WN * NF * kFrag, kThreads = 64 * WM * WN;
+    static constexpr int BM = MT * kFrag, BN = WN * NF * kFrag, kThreads = 64 * WN;
     static constexpr int U = 4 * CS;                          // 16-byte units of a row's chunk
     static_assert(BM <= kThreads && BN <= kThreads, "a thread stages one row's scales");
     typedef TileLds<BM, BN, CS> Lds;
 
-    // L: the fragments of a wave that hold rows (all MT unless WM is 1).
+    // L: the fragments of a wave that hold rows.
     template <int L>
     static __device__ __forceinline__ void run(const MxGemmArgs& a, const Unit& u, Lds& lds) {
-        constexpr int LM = WM * L * kFrag;
+        constexpr int LM = L * kFrag;
         constexpr int kStage = LM * U / kThreads;             // 16-byte units a thread stages
         static_assert(LM * U % kThreads == 0, "whole units for every thread");
         const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
-        const int wn = (tid >> 6) % WN, wm = (tid >> 6) / WN;
+        const int wn = tid >> 6;
         const int KB = a.K / kMxBlock, chunks = (KB + U - 1) / U;
         const uint32_t row_bytes = KB * 16;
         const int n_tile = u.nt * BN, n_wave = n_tile + wn * NF * kFrag;
@@ -445,21 +481,20 @@ struct Tile {
             }
         };
 
-        f32x4 acc[NF][L];
+        f32x4 acc[L][NF];
 #pragma unroll
-        for (int f = 0; f < NF; ++f)
+        for (int i = 0; i < L; ++i)
 #pragma unroll
-            for (int i = 0; i < L; ++i) acc[f][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int f = 0; f < NF; ++f) acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
 
         stage_load(0);
 #pragma unroll
         for (int s = 0; s < CS; s += 2) w_pair(0, s);
         stage_store(0, 0);
         __syncthreads();
-        const int m_wave = wm * L * kFrag + r;
         for (int c = 0; c < chunks; ++c) {
             const int buf = c & 1, next = min(c + 1, chunks - 1);
-            const uint8_t* as_b = (const uint8_t*)lds.scale[buf] + m_wave * U + g;
+            const uint8_t* as_b = (const uint8_t*)lds.scale[buf] + r * U + g;
             const uint8_t* ws_b = (const uint8_t*)lds.w_scale[buf] + (wn * NF * kFrag + r) * U + g;
             stage_load(next);
 #pragma unroll
@@ -471,59 +506,308 @@ struct Tile {
 #pragma unroll
                 for (int i = 0; i < L; ++i) {
                     as[i] = as_b[i * kFrag * U + s * 4];
-                    av[i] = lds.code[buf][lds_unit<U>(m_wave + i * kFrag, s * 4 + g)];
+                    av[i] = lds.code[buf][lds_unit<U>(i * kFrag + r, s * 4 + g)];
                 }
 #pragma unroll
                 for (int f = 0; f < NF; ++f)
 #pragma unroll
-                    for (int i = 0; i < L; ++i) acc[f][i] = mx_mfma(w[s][f], ws[f], av[i], as[i], acc[f][i]);
+                    for (int i = 0; i < L; ++i) acc[i][f] = mx_mfma(w[s][f], ws[f], av[i], as[i], acc[i][f]);
 #pragma unroll
-                for (int f = 0; f < NF; ++f) hold(acc[f]);
+                for (int i = 0; i < L; ++i) hold(acc[i]);
                 if (s % 2 == 1) w_pair(next, s - 1);
                 sched_fence();
             }
             stage_store(next, buf ^ 1);
             __syncthreads();
         }
-        // outputs
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            const bool live = m_wave + i * kFrag < u.rows;
-            const int m = u.m0 + m_wave + i * kFrag;
-            if constexpr (!SWIGLU) {
-#pragma unroll
-                for (int f = 0; f < NF; ++f)
-                    if (live) store4<Out>(a, m, n_wave + f * kFrag + 4 * g, a.N, acc[f][i]);
-            } else {
-                f32x4 h[NF / 2];
-#pragma unroll
-                for (int p = 0; p < NF / 2; ++p)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) h[p][x] = silu_mul(acc[2 * p][i][x], acc[2 * p + 1][i][x]);
-                const int n0 = n_wave / 2;
-                if constexpr (std::is_same<Out, MxOut>::value) {
-                    static_assert(NF == 4, "a wave holds one block of h");
-                    store_mx(a, m, n0, a.N / 2, live && n0 < a.N / 2, h[0], h[1]);
-                } else {
-#pragma unroll
-                    for (int p = 0; p < NF / 2; ++p)
-                        if (live) store4<Out>(a, m, n0 + p * kFrag + 4 * g, a.N / 2, h[p]);
-                }
-            }
-        }
+        write_tile<Out, SWIGLU, NF, L, 1>(a, u.m0, u.rows, r, n_wave, acc);
     }
 };
 
-template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int CS>
-__global__ __launch_bounds__(64 * WM * WN, 2) void mx_tile_kernel(MxGemmArgs a, int NT) {
-    typedef Tile<Out, SWIGLU, MT, NF, WM, WN, CS> T;
+template <typename Out, bool SWIGLU, int MT, int NF, int WN, int CS>
+__global__ __launch_bounds__(64 * WN, 2) void mx_tile_kernel(MxGemmArgs a, int NT) {
+    typedef Tile<Out, SWIGLU, MT, NF, WN, CS> T;
     __shared__ typename T::Lds lds;
     Unit u;
     if (!find_unit<T::BM>(a, NT, &u)) return;
-    if constexpr (WM == 1 && MT >= 8) {
+    if constexpr (MT >= 8) {
         if (u.rows <= T::BM / 2) return T::template run<MT / 2>(a, u, lds);
     }
     T::template run<MT>(a, u, lds);
+}
+
+// ------------------------------------------------------------ both sides over LDS
+// Persistent workgroups of WM x WN waves, each MT fragments of rows (those with
+// number i * WM + wm, so that a short stretch of rows is shared evenly) by NF
+// fragments of matrix rows. Codes and scales of both operands go from memory
+// straight into LDS (no registers on the way), in chunks of 256 columns: a chunk
+// is one cache line of every row. The loads run STAGES chunks ahead and straight
+// on into the workgroup's next unit, so that its first chunks arrive while the
+// unit before is multiplied and written. A wave waits for its own loads of a chunk
+// by count and meets the others at one barrier a chunk, in its middle: by then
+// all have the chunk's second step in registers, so the slot can be filled again
+// and the next chunk's first step be read while the second step is multiplied.
+// Whole chunks only, at least STAGES of them, scales on 4-byte boundaries.
+constexpr int kLineBlocks = 8;               // 16-byte units of a row's chunk
+constexpr int kMaxExperts = 1024;
+constexpr uint32_t kBlockM = 8;
+
+typedef __attribute__((address_space(1))) const void global_void;
+typedef __attribute__((address_space(3))) void lds_void;
+
+// 16 or 4 bytes a lane, from p (per lane) to 64 consecutive units at dst (uniform).
+__device__ __forceinline__ void load_to_lds(const uint8_t* p, u32x4* dst) {
+    __builtin_amdgcn_global_load_lds((global_void*)p, (lds_void*)dst, 16, 0, 0);
+}
+__device__ __forceinline__ void load_to_lds(const uint8_t* p, uint32_t* dst) {
+    __builtin_amdgcn_global_load_lds((global_void*)p, (lds_void*)dst, 4, 0, 0);
+}
+
+// Waits until at most N of this wave's vector memory operations are in flight,
+// and for all of its LDS operations. One instruction that no memory access
+// crosses in either direction: the count says which loads are done only if they
+// were issued in program order. (Stores of results count too: with them in
+// flight the wait is longer than it has to be, never shorter.)
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(N < 64, "vmcnt has 6 bits");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int STAGES>
+struct LineTile {
+    static constexpr int BM = WM * MT * kFrag, BN = WN * NF * kFrag, kWaves = WM * WN, kThreads = 64 * kWaves;
+    static constexpr int U = kLineBlocks;
+    static constexpr int kLoads = (BM + BN) * U / kThreads;   // code loads of a wave and chunk
+    static constexpr int kARows = BM * U / kThreads;          // of them for the rows
+    static constexpr int kScaleLoads = (BM + BN) / 64;        // 64 rows each, one per wave
+    static_assert(BM * U % kThreads == 0 && BN * U % kThreads == 0, "whole loads for every wave");
+    static_assert(kScaleLoads <= kWaves && BM % 64 == 0, "one scale load a wave, of rows or matrix rows");
+    struct Lds {
+        u32x4 code[STAGES][(BM + BN) * U];                    // rows, then matrix rows
+        u32x4 scale[2][BM + BN];                              // the same order, a row's 16 bytes
+        uint32_t first[kMaxExperts];                          // first unit of every expert
+    };
+};
+
+// The first unit of every expert into first[0 .. E - 1], and the number of units,
+// for a workgroup of THREADS.
+template <int BM, int THREADS>
+__device__ __forceinline__ uint32_t scan_units(const MxGemmArgs& a, int NT, uint32_t* first, uint32_t* scratch) {
+    constexpr int kPer = kMaxExperts / THREADS;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    uint32_t n[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = tid * kPer + i;
+        n[i] = 0;
+        if (a.offsets == nullptr) {
+            n[i] = e == 0 ? (uint32_t)(a.rows + BM - 1) / BM * NT : 0;
+        } else if (e < a.E) {
+            const int lo = min(max(a.offsets[e], 0), a.rows), hi = min(max(a.offsets[e + 1], lo), a.rows);
+            n[i] = (uint32_t)(hi - lo + BM - 1) / BM * NT;
+        }
+        sum += n[i];
+    }
+    uint32_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const uint32_t v = __shfl_up(incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 63) scratch[wave] = incl;
+    __syncthreads();
+    uint32_t at = incl - sum, total = 0;
+    for (int w = 0; w < THREADS / 64; ++w) {
+        at += w < wave ? scratch[w] : 0;
+        total += scratch[w];
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (tid * kPer + i < a.E) first[tid * kPer + i] = at;
+        at += n[i];
+    }
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(total);
+}
+
+struct LineUnit {
+    const uint8_t* blob;
+    int m0, rows, nt;                        // rows 0: no unit
+};
+
+typedef __attribute__((address_space(4))) const int32_t const_i32;
+typedef __attribute__((address_space(4))) const uint64_t const_u64;
+
+// Unit w from the table of first units: a search in LDS, and scalar loads of the
+// expert's offsets and blob, which leave the vector loads in flight alone.
+template <int BM>
+__device__ __forceinline__ LineUnit line_unit(const MxGemmArgs& a, int NT, const uint32_t* first, uint32_t w, bool live) {
+    LineUnit u = {(const uint8_t*)((const_u64*)a.table)[0], 0, 0, 0};
+    const int lane = threadIdx.x & 63;
+    int e = -1;
+    for (int b = 0; b < a.E; b += 64) e += __popcll(__ballot(b + lane < a.E && first[min(b + lane, a.E - 1)] <= w));
+    if (!live || e < 0) return u;
+    int lo = 0, hi = a.rows;
+    if (a.offsets) {
+        lo = min(max(((const_i32*)a.offsets)[e], 0), a.rows);
+        hi = min(max(((const_i32*)a.offsets)[e + 1], lo), a.rows);
+    }
+    const uint32_t mt = (uint32_t)(hi - lo + BM - 1) / BM;
+    if (mt == 0) return u;                   // offsets that are not ascending
+    const uint32_t rest = w - __builtin_amdgcn_readfirstlane(first[e]);
+    u.blob = (const uint8_t*)((const_u64*)a.table)[e];
+    // blocks of kBlockM row tiles by all matrix tiles, row tiles first: the units that
+    // an XCD's workgroups are at together share rows and matrix rows evenly
+    const uint32_t block = min(rest / (kBlockM * NT), (mt - 1) / kBlockM), in = rest - block * kBlockM * NT;
+    const uint32_t wide = min(kBlockM, mt - block * kBlockM);
+    u.nt = min(in / wide, (uint32_t)NT - 1);
+    u.m0 = lo + (int)(block * kBlockM + in % wide) * BM;
+    u.rows = min(BM, hi - u.m0);
+    return u;
+}
+
+template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int STAGES>
+__global__ __launch_bounds__(64 * WM * WN, 2) void mx_line_kernel(MxGemmArgs a, int NT) {
+    typedef LineTile<Out, SWIGLU, MT, NF, WM, WN, STAGES> T;
+    constexpr int U = T::U;
+    __shared__ typename T::Lds lds;
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wn = wave % WN, wm = wave / WN;
+    const int KB = a.K / kMxBlock, chunks = KB / U;
+    const uint32_t row_bytes = KB * 16;
+
+    const uint32_t total = scan_units<T::BM, T::kThreads>(a, NT, lds.first, (uint32_t*)lds.scale[0]);
+    const uint32_t per = (total + kXcds - 1) / kXcds, xcd = blockIdx.x % kXcds, step = gridDim.x / kXcds;
+    uint32_t at = blockIdx.x / kXcds;        // this workgroup's units: at, at + step, ... of its XCD's `per`
+    auto unit_at = [&](uint32_t x) {
+        const uint32_t w = xcd * per + x;
+        return line_unit<T::BM>(a, NT, lds.first, w, x < per && w < total);
+    };
+    LineUnit u = unit_at(at);
+    if (u.rows <= 0) return;
+
+    // the unit that is being loaded
+    const uint8_t *w_base, *ws_base, *a_base, *as_base;
+    int m_last, n_last;                      // its last row and matrix row
+    int lc = 0;                              // its next chunk
+    bool loading = true;
+    auto set_unit = [&](const LineUnit& v) {
+        const int n_tile = v.nt * T::BN;
+        m_last = v.rows - 1, n_last = a.N - 1 - n_tile;
+        w_base = v.blob + a.q_off + (int64_t)n_tile * row_bytes;
+        ws_base = v.blob + a.s_off + (int64_t)n_tile * KB;
+        a_base = a.a + (int64_t)v.m0 * row_bytes;
+        as_base = a.as + (int64_t)v.m0 * KB;
+        lc = 0;
+    };
+    // Load i of this wave for the next chunk: 8 rows into a slot, lane l row l / 8,
+    // position l % 8. Behind the last unit the same number of loads goes out, so that
+    // the counts hold, each of one place and into a slot that is not read again.
+    const uint32_t unit16 = ((lane & 7) ^ (lane >> 3)) * 16;
+    auto load_codes = [&](int slot, int i) {
+        const bool rows = i < T::kARows;
+        const int x = (rows ? i : i - T::kARows) * T::kWaves + wave;
+        const uint32_t row = min(x * 8 + (lane >> 3), rows ? m_last : n_last);
+        load_to_lds((rows ? a_base : w_base) + (loading ? __umul24(row, row_bytes) + lc * U * 16 + unit16 : 0u),
+                    lds.code[slot] + (rows ? x : T::BM / 8 + x) * 64);
+    };
+    // With the first of two chunks, their scales: 64 rows a wave (two waves the same
+    // ones where there are fewer).
+    int scale_fill = 0;                      // the scale slot that is filled next
+    auto load_scales = [&]() {
+        const int x = min(wave, T::kScaleLoads - 1);
+        const bool rows = x * 64 < T::BM;
+        const uint32_t row = min(x * 64 - (rows ? 0 : T::BM) + lane, rows ? m_last : n_last);
+        load_to_lds((rows ? as_base : ws_base) + (loading ? __umul24(row, KB) + lc * U : 0u),
+                    lds.scale[scale_fill] + x * 64);
+        scale_fill ^= 1;
+    };
+
+    set_unit(u);
+    __syncthreads();                         // the scan's scratch is a scale slot
+#pragma unroll
+    for (int c = 0; c < STAGES; ++c, ++lc) {
+        if (c % 2 == 0) load_scales();
+#pragma unroll
+        for (int i = 0; i < T::kLoads; ++i) load_codes(c, i);
+    }
+
+    const int m_lds = wm * kFrag + r, n_lds = T::BM + wn * NF * kFrag + r;
+    auto code = [&](int slot, int row, int s) { return lds.code[slot][lds_unit<U>(row, s * 4 + g)]; };
+    // the scale byte of step s of the even (0) or odd (1) chunk of a scale slot
+    auto scale = [&](int from, int row, int odd, int s) {
+        return (uint32_t)((const uint8_t*)lds.scale[from])[row * 16 + odd * U + s * 4 + g];
+    };
+    u32x4 av[MT], w[NF], w_next[NF];
+    uint32_t as[MT], ws[NF], ws_next[NF];
+    f32x4 acc[MT][NF];
+    int slot = 0, scales = 0;                // of the chunk that is multiplied
+    wait_loads<(STAGES - 1) * T::kLoads>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int f = 0; f < NF; ++f) w[f] = code(0, n_lds + f * kFrag, 0), ws[f] = scale(0, n_lds + f * kFrag, 0, 0);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) av[i] = code(0, m_lds + i * WM * kFrag, 0), as[i] = scale(0, m_lds + i * WM * kFrag, 0, 0);
+    while (true) {
+        const int live = (u.rows - wm * kFrag + WM * kFrag - 1) / (WM * kFrag);   // fragments with rows
+        at += step;
+        const LineUnit next = unit_at(at);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int f = 0; f < NF; ++f) acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+        // Multiplies the step in the registers and reads step s of a chunk into those it
+        // leaves; between the products, a share of the loads into slot `fill` (-1: none).
+        auto multiply = [&](int from, int from_scales, int odd, int s, int fill) {
+#pragma unroll
+            for (int f = 0; f < NF; ++f) {
+                w_next[f] = code(from, n_lds + f * kFrag, s);
+                ws_next[f] = scale(from_scales, n_lds + f * kFrag, odd, s);
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                if (MT > 4 || i < live) {
+#pragma unroll
+                    for (int f = 0; f < NF; ++f) acc[i][f] = mx_mfma(w[f], ws[f], av[i], as[i], acc[i][f]);
+                    hold(acc[i]);
+                }
+                av[i] = code(from, m_lds + i * WM * kFrag, s);
+                as[i] = scale(from_scales, m_lds + i * WM * kFrag, odd, s);
+                if (fill >= 0) {
+#pragma unroll
+                    for (int x = i * T::kLoads / MT; x < (i + 1) * T::kLoads / MT; ++x) load_codes(fill, x);
+                }
+            }
+#pragma unroll
+            for (int f = 0; f < NF; ++f) w[f] = w_next[f], ws[f] = ws_next[f];
+        };
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+            const int odd = c & 1;
+            multiply(slot, scales, odd, 1, -1);
+            // The next chunk and its scales (issued before its codes) have arrived, the
+            // codes of the STAGES - 2 behind it may not have, and this one is read.
+            wait_loads<(STAGES - 2) * T::kLoads>();
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            if (lc == chunks) {
+                loading = next.rows > 0;
+                set_unit(loading ? next : u);
+            }
+            if (lc % 2 == 0) load_scales();
+            const int fill = slot;
+            slot = slot == STAGES - 1 ? 0 : slot + 1;
+            scales ^= odd;
+            multiply(slot, scales, odd ^ 1, 0, fill);
+            ++lc;
+        }
+        write_tile<Out, SWIGLU, NF, MT, WM>(a, u.m0, u.rows, m_lds, u.nt * T::BN + wn * NF * kFrag, acc);
+        if (next.rows <= 0) break;
+        u = next;
+    }
+    wait_loads<0>();                         // nothing lands in LDS after the workgroup
 }
 
 // Units of a launch at most: the rows fill rows / BM stretches, and each expert
@@ -550,34 +834,63 @@ coli_status few_rows(const MxGemmArgs& a, hipStream_t stream) {
     return COLI_OK;
 }
 
-template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int CS>
+template <typename Out, bool SWIGLU, int MT, int NF, int WN, int CS>
 coli_status tiles(const MxGemmArgs& a, hipStream_t stream) {
-    typedef Tile<Out, SWIGLU, MT, NF, WM, WN, CS> T;
+    typedef Tile<Out, SWIGLU, MT, NF, WN, CS> T;
     const int NT = (a.N + T::BN - 1) / T::BN;
     uint32_t grid;
     if (coli_status st = grid_of(a, T::BM, NT, T::kThreads, &grid)) return st;
-    launch(mx_tile_kernel<Out, SWIGLU, MT, NF, WM, WN, CS>, dim3(grid), dim3(T::kThreads), 0, stream, a, NT);
+    launch(mx_tile_kernel<Out, SWIGLU, MT, NF, WN, CS>, dim3(grid), dim3(T::kThreads), 0, stream, a, NT);
     COLI_CHECK_LAUNCH("mxfp4 product kernel launch");
     return COLI_OK;
 }
 
+template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int STAGES>
+coli_status lines(const MxGemmArgs& a, hipStream_t stream) {
+    typedef LineTile<Out, SWIGLU, MT, NF, WM, WN, STAGES> T;
+    const int NT = (a.N + T::BN - 1) / T::BN;
+    uint32_t grid;
+    if (coli_status st = grid_of(a, T::BM, NT, T::kThreads, &grid)) return st;
+    grid = std::min(grid, kCus);             // LDS holds one workgroup a CU
+    launch(mx_line_kernel<Out, SWIGLU, MT, NF, WM, WN, STAGES>, dim3(grid), dim3(T::kThreads), 0, stream, a, NT);
+    COLI_CHECK_LAUNCH("mxfp4 product kernel launch");
+    return COLI_OK;
+}
+
+// Which kernel, from the average rows of an expert (`per`) and the workgroups the
+// kernel would have. Times on one MI355X, us: SwiGLU K 6144, inter 2048 / product
+// K 2048, N 6144, over 256 experts unless noted.
+//  - few_rows keeps 16 rows a tile and reads the matrix once per tile. 2 rows an
+//    expert: 507 / 261 against 513 / 260 for lines; 4: 603 / 318 against 588 / 302.
+//    Where lines would not fill the CUs it wins for longer: one expert of 64 rows
+//    14.7 / 9.2 against 31.8 / 16.0, of 256 rows 42.6 / 25.6 against 37.0 / 19.4.
+//  - lines of 256 rows halve the traffic into LDS of lines of 128, once they fill
+//    the CUs: N 8192, K 8192, 2048 rows 75 against 94, 1024 rows 66 against 51.
+//  - tiles take what lines cannot (columns not in 512s, scales off 16 bytes):
+//    16384 rows over 256 experts 884 / 488 against 694 / 385 for lines.
 template <typename Out, bool SWIGLU>
 coli_status product(const MxGemmArgs& a, hipStream_t stream) {
     constexpr bool mx = std::is_same<Out, MxOut>::value;
-    const double per = (double)a.rows / (a.offsets ? std::min(a.E, a.rows) : 1);
-    if (per <= 8 || a.K < kChunkBlocks * kMxBlock) {
+    const int64_t experts = a.offsets ? std::min(a.E, a.rows) : 1;
+    const double per = (double)a.rows / experts;
+    auto units = [&](int bm, int bn) { return experts * (int64_t)std::ceil(per / bm) * ((a.N + bn - 1) / bn); };
+    const bool fits = a.K % 512 == 0 && a.K >= 1024 && a.s_off % 16 == 0 && (uintptr_t)a.as % 16 == 0;
+    const bool few = fits ? per <= 2 || (per <= 128 && units(128, 256) < kCus) : per <= 8 || a.K < 512;
+    if (few) {
         // a wave takes at least two chunks where there are that many: 11.4 us with 2
         // waves against 13.3 with 4 for 8 rows of 8 experts at K 2048, N 6144 (4
         // chunks), 22.6 with 4 against 23.7 with 2 at K 6144, inter 2048 (12)
         if (a.K >= 8 * kChunkBlocks * kMxBlock) return few_rows<Out, SWIGLU, mx ? 4 : 2, 4>(a, stream);
         return few_rows<Out, SWIGLU, mx ? 4 : 2, 2>(a, stream);
     }
-    // 64-row tiles read the matrix once for the rows of most experts up to here:
-    // 637 against 710 us for 4072 rows over 256 experts (K 6144, inter 2048), 884
-    // against 833 us for 16384
-    if (per <= 32) return tiles<Out, SWIGLU, 4, 4, 1, 4, 4>(a, stream);
-    if constexpr (mx) return tiles<Out, SWIGLU, 8, 4, 1, 4, 2>(a, stream);
-    else return tiles<Out, SWIGLU, 8, 2, 1, 8, 4>(a, stream);
+    if (fits) {
+        if (per >= 1024 && units(256, 256) >= kCus) return lines<Out, SWIGLU, 8, 4, 2, 4, 2>(a, stream);
+        return lines<Out, SWIGLU, 4, 4, 2, 4, 3>(a, stream);
+    }
+    // 64-row tiles leave two workgroups a CU: 637 against 711 us for 4072 rows over
+    // 256 experts (K 6144, inter 2048), 884 against 870 for 16384
+    if (per <= 32) return tiles<Out, SWIGLU, 4, 4, 4, 4>(a, stream);
+    return tiles<Out, SWIGLU, 8, 4, 4, 2>(a, stream);
 }
 
 }  // namespace

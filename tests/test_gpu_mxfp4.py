@@ -127,10 +127,11 @@ def test_quantize_past_32_bits(coli):
 
 
 class Mats:
-    """E random MXFP4 matrices as device buffers (codes, then scales at an odd offset) and in 64 bits."""
+    """E random MXFP4 matrices as device buffers (codes, then scales at an offset of 5 past 16 bytes, or
+    aligned to them) and in 64 bits."""
 
-    def __init__(self, coli, rng, E, N, K, lo=117, hi=130, keep=None, interleaved=False):
-        self.q_off, self.s_off = 32, 32 + N * K // 2 + 5
+    def __init__(self, coli, rng, E, N, K, lo=117, hi=130, aligned=False):
+        self.q_off, self.s_off = 32, 32 + N * K // 2 + (0 if aligned else 5)
         self.values, blobs = [], []
         for e in range(E):
             q = rng.integers(0, 256, (N, K // 2), dtype=np.uint8)
@@ -163,7 +164,7 @@ CASES = [
 ]
 
 
-def _case(coli, rng, counts, N, K, spare, **kw):
+def _case(coli, rng, counts, N, K, spare, aligned=False, **kw):
     if isinstance(counts, int):
         off, R, E = None, counts, 1
         off_np = np.array([0, counts])
@@ -171,19 +172,26 @@ def _case(coli, rng, counts, N, K, spare, **kw):
         off_np = _counts_to_offsets(counts)
         R, E = int(off_np[-1]) + spare, len(counts)
         off = _dev(off_np)
-    mats = Mats(coli, rng, E, N, K, **kw)
+    mats = Mats(coli, rng, E, N, K, aligned=aligned, **kw)
     q, s, a = _rows(rng, R, K, **kw)
     if spare:                                                   # rows of no expert hold NaN
         s[-spare:] = 255
     return mats, _dev(q), _dev(s), a, off, off_np, R
 
 
+# the same with scales on 16-byte boundaries and columns in 512s: rows per expert around the tiles of 128 and 256,
+# empty experts between them, more units than workgroups, one unit, matrix rows that end inside a tile
+LINES = [([3], 256, 1024, 0), ([5, 0, 4, 130, 128, 129, 0], 300, 1024, 2), ([0] * 9 + [200], 77, 1536, 1),
+         ([31, 33, 17, 16, 64, 65], 1000, 2048, 0), (257, 1030, 1024, 0), ([9] * 70, 1100, 1024, 5),
+         ([1025, 1030], 4100, 1024, 3), (2300, 8300, 1024, 0), ([300] + [0] * 1022 + [7], 520, 1024, 0)]
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("counts,N,K,spare", CASES)
-def test_matmul_matches_reference(coli, dtype, counts, N, K, spare):
+@pytest.mark.parametrize("counts,N,K,spare,aligned", [c + (False,) for c in CASES] + [c + (True,) for c in LINES])
+def test_matmul_matches_reference(coli, dtype, counts, N, K, spare, aligned):
     import torch
     rng = np.random.default_rng(N * 7919 + K)
-    mats, q, s, a, off, off_np, R = _case(coli, rng, counts, N, K, spare)
+    mats, q, s, a, off, off_np, R = _case(coli, rng, counts, N, K, spare, aligned=aligned)
     pad = 3
     buf = torch.full((R, N + pad), 7.0, dtype=_t(dtype), device="cuda")
     y = coli.mxfp4_matmul(q, s, mats.table, N, mats.q_off, mats.s_off, offsets=off, out=buf[:, :N])
@@ -198,14 +206,16 @@ def test_matmul_matches_reference(coli, dtype, counts, N, K, spare):
     assert bool((buf[:, N:] == 7.0).all()) and bool((buf[n:] == 7.0).all())
 
 
-@pytest.mark.parametrize("R,N,K", [(1, 64, 2048), (16, 48, 6144), (70, 256, 1024), (260, 256, 2048)])
+@pytest.mark.parametrize("R,N,K", [(1, 64, 2048), (16, 48, 6144), (70, 256, 1024), (260, 256, 2048), (130, 500, 2080),
+                                   (300, 300, 5152), (1100, 520, 1536), (2100, 8200, 1024), (9, 40, 1056)])
 def test_matmul_is_exact_where_f32_is(coli, R, N, K):
     """With scales within three binades on each side every partial sum has at most 24 bits."""
     rng = np.random.default_rng(R)
-    mats = Mats(coli, rng, 1, N, K, 119, 121)
-    q, s, a = _rows(rng, R, K, 126, 128)
-    y = coli.mxfp4_matmul(_dev(q), _dev(s), mats.table, N, mats.q_off, mats.s_off)
-    assert np.array_equal(_host(y), ref.product(a, mats.values, np.array([0, R]))[0])
+    for aligned in (False, True):
+        mats = Mats(coli, rng, 1, N, K, 119, 121, aligned)
+        q, s, a = _rows(rng, R, K, 126, 128)
+        y = coli.mxfp4_matmul(_dev(q), _dev(s), mats.table, N, mats.q_off, mats.s_off)
+        assert np.array_equal(_host(y), ref.product(a, mats.values, np.array([0, R]))[0])
 
 
 def test_product_special_scales(coli):
@@ -248,11 +258,13 @@ def _swiglu_ref(a, mats, off_np, K):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("counts,I,K,spare", [
     ([1], 32, 32, 0), ([0, 1, 2], 64, 96, 1), (5, 32, 544, 0), ([16, 17, 0, 1], 96, 640, 2),
-    ([64, 1, 70], 160, 512, 0), (130, 288, 1056, 0), ([1] * 9, 256, 2048, 0), (260, 128, 256, 0)])
-def test_swiglu_matches_reference(coli, dtype, counts, I, K, spare):
+    ([64, 1, 70], 160, 512, 0), (130, 288, 1056, 0), ([1] * 9, 256, 2048, 0), (260, 128, 256, 0),
+    ([5, 0, 4, 130, 128, 129], 160, 1024, 2), ([40] * 40, 1056, 1024, 0), (2300, 4128, 1024, 0)])
+@pytest.mark.parametrize("aligned", [False, True])
+def test_swiglu_matches_reference(coli, dtype, counts, I, K, spare, aligned):
     import torch
     rng = np.random.default_rng(I + K)
-    mats, q, s, a, off, off_np, R = _case(coli, rng, counts, 2 * I, K, spare, lo=120, hi=126)
+    mats, q, s, a, off, off_np, R = _case(coli, rng, counts, 2 * I, K, spare, aligned=aligned, lo=120, hi=126)
     buf = torch.full((R, I + 1), 7.0, dtype=_t(dtype), device="cuda")
     h = coli.mxfp4_swiglu(q, s, mats.table, I, mats.q_off, mats.s_off, offsets=off, out=buf[:, :I])
     want, bound = _swiglu_ref(a, mats, off_np, K)
@@ -265,12 +277,14 @@ def test_swiglu_matches_reference(coli, dtype, counts, I, K, spare):
 
 @pytest.mark.parametrize("counts,I,K,spare", [
     ([1], 32, 32, 0), ([0, 1, 2], 64, 96, 1), ([16, 17, 0, 1], 96, 640, 2), ([64, 1, 70], 160, 512, 0),
-    (130, 288, 1024, 0), ([1] * 9, 256, 2048, 0), (300, 64, 512, 0)])
-def test_swiglu_to_mxfp4(coli, counts, I, K, spare):
+    (130, 288, 1024, 0), ([1] * 9, 256, 2048, 0), (300, 64, 512, 0), ([5, 0, 4, 130, 128, 129], 160, 1024, 2),
+    ([40] * 40, 1056, 1024, 0), (2300, 4128, 1024, 0), ([150, 33], 96, 1056, 0)])
+@pytest.mark.parametrize("aligned", [False, True])
+def test_swiglu_to_mxfp4(coli, counts, I, K, spare, aligned):
     """The quantised output is the quantiser's answer to the f32 output (sums exact by the choice of scales)."""
     import torch
     rng = np.random.default_rng(I * 3 + K)
-    mats, q, s, a, off, off_np, R = _case(coli, rng, counts, 2 * I, K, spare, lo=119, hi=121)
+    mats, q, s, a, off, off_np, R = _case(coli, rng, counts, 2 * I, K, spare, aligned=aligned, lo=119, hi=121)
     h = torch.zeros(R, I, device="cuda")
     coli.mxfp4_swiglu(q, s, mats.table, I, mats.q_off, mats.s_off, offsets=off, out=h)
     hq = torch.full((R, I // 2), 0x5a, dtype=torch.uint8, device="cuda")
