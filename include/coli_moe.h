@@ -478,7 +478,8 @@ COLI_API coli_status coli_quantize_mxfp4_expert(const coli_moe_shape* shape, con
  * The buffers of experts without rows are not read. d_y: type dtype (f32, bf16 or
  * f16), row stride ld >= N. Products are exact, sums f32, the result rounded
  * once; a row's result does not depend on the other rows' values. E <= 1024, K <=
- * 2^22. */
+ * 2^22. K in multiples of 512, with d_as, s_off and the buffers on 16-byte
+ * boundaries, takes the faster kernel for many rows. */
 COLI_API coli_status coli_mxfp4_matmul(const uint8_t* d_a, const uint8_t* d_as, int32_t rows, int32_t K,
                                        const int32_t* d_offsets, int32_t E,
                                        const void* const* d_blob_table, size_t q_off, size_t s_off,

@@ -7,7 +7,15 @@
 // rows go from memory into the instruction without any unpacking. The matrix
 // rows are the first operand: result lane l then holds outputs n = 4 (l / 16) ..
 // + 3 of one row m = l % 16, which is one wide store. Products are exact and
-// sums are f32.
+// sums are f32. A step is one instruction's 128 columns; in registers alone the
+// instruction runs at 8.1 PFLOP/s on this card.
+//
+// Up to about 100 rows an expert the products are bound by reading the matrices
+// (17/32 byte a value): 256 experts' gate and up matrices of 2 x 2048 x 6144 are
+// 3.4 GB. Three kernels, chosen in product() below:
+//   few_rows  16 rows a tile, operands straight into registers: single tokens
+//   lines     128 or 256 rows a tile, both operands over LDS, persistent
+//   tiles     64 or 128 rows a tile, rows over LDS: any number of columns
 #include <algorithm>
 #include <cmath>
 
@@ -20,8 +28,6 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kFrag = 16;                    // rows of one operand of the instruction
-constexpr int kStep = 128;                   // columns of one instruction
-constexpr int kStepBytes = kStep / 2;
 constexpr int kXcds = 8;
 constexpr uint32_t kCus = 256;
 
@@ -361,14 +367,14 @@ __device__ __forceinline__ void write_tile(const MxGemmArgs& a, int m0, int rows
     }
 }
 
-// ------------------------------------------------------------ many rows
-// Workgroup: 4 waves, each 64 matrix rows (4 fragments) by MT fragments of 16
-// rows. The matrix is the operand that has to come from HBM: each wave loads
-// its own rows straight into the instruction's registers, one step's registers
-// refilled for the next chunk as soon as the step has used them, so that nearly
-// a chunk (16 KB a wave) is on the way all the time without a barrier. The rows
-// are shared by the waves and come (from L2) over LDS, two chunks deep, and so
-// do the scale bytes of both sides, which a wave then reads one per lane.
+// ------------------------------------------------------------ many rows, any columns
+// Workgroup: WN waves, each NF fragments of matrix rows by MT fragments of rows.
+// The matrix is the operand that has to come from HBM: each wave loads its own
+// rows straight into the instruction's registers, a cache line of every row (two
+// steps) refilled for the next chunk as soon as it is used, without a barrier. The
+// rows are shared by the waves and come (from L2) over LDS, two chunks deep, and
+// so do the scale bytes of both sides, which a wave then reads one per lane. Rows
+// that are no whole chunks long end in blocks of zeros.
 
 // Position of 16-byte unit b of row r in an LDS chunk of U units a row: the units
 // of a row are permuted by its number, so that the rows that a load reads at one
@@ -417,8 +423,7 @@ struct TileLds {
     Scales<4 * CS> scale[2][BM], w_scale[2][BN];
 };
 
-// WN waves, each MT fragments of rows by NF fragments of matrix rows; chunks of
-// CS steps.
+// Chunks of CS steps.
 template <typename Out, bool SWIGLU, int MT, int NF, int WN, int CS>
 struct Tile {
     static constexpr int BM = MT * kFrag, BN = WN * NF * kFrag, kThreads = 64 * WN;
@@ -540,14 +545,23 @@ __global__ __launch_bounds__(64 * WN, 2) void mx_tile_kernel(MxGemmArgs a, int N
 // Persistent workgroups of WM x WN waves, each MT fragments of rows (those with
 // number i * WM + wm, so that a short stretch of rows is shared evenly) by NF
 // fragments of matrix rows. Codes and scales of both operands go from memory
-// straight into LDS (no registers on the way), in chunks of 256 columns: a chunk
-// is one cache line of every row. The loads run STAGES chunks ahead and straight
-// on into the workgroup's next unit, so that its first chunks arrive while the
-// unit before is multiplied and written. A wave waits for its own loads of a chunk
-// by count and meets the others at one barrier a chunk, in its middle: by then
-// all have the chunk's second step in registers, so the slot can be filled again
-// and the next chunk's first step be read while the second step is multiplied.
-// Whole chunks only, at least STAGES of them, scales on 4-byte boundaries.
+// straight into LDS (no registers on the way), in chunks of two steps, one cache
+// line of every row. The loads run STAGES chunks ahead and straight on into the
+// workgroup's next unit, so that its first chunks arrive while the unit before is
+// multiplied and written. A wave waits for its own loads of a chunk by count and
+// meets the others at one barrier a chunk, in its middle: by then all have the
+// second step in registers, so the slot can be filled again and the next chunk's
+// first step be read while the second step is multiplied. Scales come 16 bytes a
+// row, for two chunks at once (4 bytes a row and chunk took more of the cache's
+// cycles than the codes: 800 in place of 694 us below). An even number of whole
+// chunks, at least STAGES, and scale rows on 16-byte boundaries.
+//
+// SwiGLU of 16384 rows over 256 experts, K 6144, inter 2048: 694 us, 5.1 TB/s; of
+// 4072 rows 590 us, 5.8 TB/s, what HBM gives. Dense 8191 x 8192 x 8192: 303 us, 3.6
+// PFLOP/s; there the matrix cores work 40% of the time and the loads into LDS
+// alone take 310 us (a chunk's 64 KB are on the way for as long as one chunk is
+// multiplied, which does not cover their latency; LDS has no room for a third
+// slot, and chunks of one step with four slots gave 331 us).
 constexpr int kLineBlocks = 8;               // 16-byte units of a row's chunk
 constexpr int kMaxExperts = 1024;
 constexpr uint32_t kBlockM = 8;
@@ -555,12 +569,9 @@ constexpr uint32_t kBlockM = 8;
 typedef __attribute__((address_space(1))) const void global_void;
 typedef __attribute__((address_space(3))) void lds_void;
 
-// 16 or 4 bytes a lane, from p (per lane) to 64 consecutive units at dst (uniform).
+// 16 bytes a lane, from p (per lane) to 64 consecutive units at dst (uniform).
 __device__ __forceinline__ void load_to_lds(const uint8_t* p, u32x4* dst) {
     __builtin_amdgcn_global_load_lds((global_void*)p, (lds_void*)dst, 16, 0, 0);
-}
-__device__ __forceinline__ void load_to_lds(const uint8_t* p, uint32_t* dst) {
-    __builtin_amdgcn_global_load_lds((global_void*)p, (lds_void*)dst, 4, 0, 0);
 }
 
 // Waits until at most N of this wave's vector memory operations are in flight,
@@ -583,6 +594,10 @@ struct LineTile {
     static constexpr int kScaleLoads = (BM + BN) / 64;        // 64 rows each, one per wave
     static_assert(BM * U % kThreads == 0 && BN * U % kThreads == 0, "whole loads for every wave");
     static_assert(kScaleLoads <= kWaves && BM % 64 == 0, "one scale load a wave, of rows or matrix rows");
+    // The scales of chunks t and t + 1 are loaded in chunk t - STAGES behind its
+    // barrier, into the slot whose last bytes, of chunk t - 3, are read before the
+    // barrier of that chunk.
+    static_assert(STAGES == 2 || STAGES == 3, "a scale slot is read before it is filled again");
     struct Lds {
         u32x4 code[STAGES][(BM + BN) * U];                    // rows, then matrix rows
         u32x4 scale[2][BM + BN];                              // the same order, a row's 16 bytes

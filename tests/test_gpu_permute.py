@@ -305,14 +305,14 @@ def test_expert_layer(coli, T, H, I, E, k, drop):
     assert np.median(err) <= 1e-5 and err.max() <= 1 / (3 * np.sqrt(I)), (float(np.median(err)), float(err.max()))
 
 
-def test_expert_layer_in_a_graph_and_on_streams(coli):
+@pytest.mark.parametrize("T,H,I", [(40, 256, 128), (600, 1024, 1024), (90, 288, 544)])
+def test_expert_layer_in_a_graph_and_on_streams(coli, T, H, I):
     """Captured calls replay to the eager result, with eager work between the replays; two graphs and a side stream
-    run the same calls at once on outputs of their own."""
+    run the same calls at once on outputs of their own. One case for each kernel of the products."""
     import torch
     rng = np.random.default_rng(3)
-    layer = Layer(coli, 3, 256, 128, 8, 2)
-    T = 40
-    xs = [_dev(rng.standard_normal((T, 256)).astype(np.float32)) for _ in range(3)]
+    layer = Layer(coli, 3, H, I, 8, 2)
+    xs = [_dev(rng.standard_normal((T, H)).astype(np.float32)) for _ in range(3)]
     routes = [coli.route(_dev(rng.standard_normal((T, 8)).astype(np.float32)), None, 2) for _ in range(3)]
     want = [layer.run(coli, x, *r) for x, r in zip(xs, routes)]
     torch.cuda.synchronize()
