@@ -1,26 +1,23 @@
 // MXFP4 rows: E2M1 codes with one E8M0 scale per 32 columns, and back.
 //
-// A lane takes 8 neighbouring columns, so a block is 4 lanes: the largest
-// |x| of the block is the largest of 8 in the lane and of 4 lanes (two DPP
-// exchanges inside the quad), and the codes are one 4-byte store per lane (256
-// contiguous bytes a wave). The conversion itself is the hardware's scaled
-// E2M1 convert (half to even, saturating).
+// Quantising, a lane takes 16 bytes (4 or 8 neighbouring columns), so that a wave
+// reads 1 KiB in one piece, and a block is 8 or 4 lanes: its largest |x| is the
+// largest in the lane and over the lanes by DPP exchanges. The conversion itself
+// is the hardware's scaled E2M1 convert (half to even, saturating).
 //
 // Both directions are bound by HBM: 4 (f32) or 2 bytes a value on one side,
 // 17/32 byte on the other.
-#include <algorithm>
-
 #include "mxfp4.h"
 
 namespace coli {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnit = 8;                          // columns per lane
+constexpr int kUnit = 8;                          // columns per lane, dequantising
 
-// Position of unit `u` (8 columns): its row and the unit's number within it.
-// Rows that follow each other without a gap are one long row (a block never
-// crosses a row end: columns come in 32s), which needs no division.
+// Position of unit `u`: its row and the unit's number within it. Rows that
+// follow each other without a gap are one long row (a block never crosses a
+// row end: columns come in 32s), which needs no division.
 struct UnitMap {
     int64_t units;       // units in all
     int64_t per_row;     // units of a row (all of them for gapless rows)
@@ -42,39 +39,50 @@ __device__ __forceinline__ void locate(const UnitMap& m, int64_t u, int64_t* row
     }
 }
 
-// U units per thread, kThreads apart, all loaded before the first is converted.
-template <typename T, int U>
+// 16 bytes of a row that is read once: past the caches. (98304 x 2048 f32: 157
+// us, 5.8 TB/s, against 200 us with cached loads of 8 columns a lane.)
+template <typename T, int N>
+__device__ __forceinline__ void load_once(const T* p, float (&out)[N]) {
+    typedef T V __attribute__((ext_vector_type(N), aligned(sizeof(T))));
+    const V v = __builtin_nontemporal_load(reinterpret_cast<const V*>(p));
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = (float)v[i];
+}
+
+// A unit a thread (two to eight, loaded before the first is converted, were 1 to 3%
+// slower).
+template <typename T>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(const T* __restrict__ x, UnitMap m,
                                                             uint8_t* __restrict__ q,
                                                             uint8_t* __restrict__ s) {
-    const int64_t u0 = (int64_t)blockIdx.x * (kThreads * U) + threadIdx.x;
-    float v[U][kUnit];
-    int64_t out[U];
+    constexpr int N = 16 / sizeof(T), kLanes = kMxBlock / N;      // columns a lane, lanes a block
+    const int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (u >= m.units) return;                     // whole blocks: their lanes come together
+    int64_t row, at;
+    locate(m, u, &row, &at);
+    float v[N];
+    load_once<T, N>(x + row * m.ld + at * N, v);
+    uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-        const int64_t u = u0 + i * kThreads;
-        out[i] = -1;
-        if (u < m.units) {
-            int64_t row, at;
-            locate(m, u, &row, &at);
-            load_f32<T, kUnit>(x + row * m.ld + at * kUnit, v[i]);
-            out[i] = (m.gu_base < 0 ? row : gu_row(row) + m.gu_base) * m.per_row + at;
-        }
+    for (int c = 0; c < N; ++c) top = max(top, abs_bits(v[c]));
+    top = mx_quad_max(top);
+    if constexpr (kLanes == 8)                    // the other quad of the eight
+        top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0x141, 0xf, 0xf, true));
+    const int code = mx_scale_code(top);
+    const float scale = mx_scale_value(code);
+    const int64_t out = (m.gu_base < 0 ? row : gu_row(row) + m.gu_base) * m.per_row + at;
+    if constexpr (N == 8) {
+        reinterpret_cast<uint32_t*>(q)[out] = code == 255 ? 0u : mx_codes8(v, scale);
+    } else {
+        uint32_t w = 0;
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], scale, 0);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], scale, 1);
+        reinterpret_cast<uint16_t*>(q)[out] = code == 255 ? 0 : (uint16_t)w;
     }
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-        if (out[i] < 0) continue;                 // whole quads: units come in 4s
-        uint32_t top = 0;
-#pragma unroll
-        for (int c = 0; c < kUnit; ++c) top = max(top, abs_bits(v[i][c]));
-        top = mx_quad_max(top);
-        const int code = mx_scale_code(top);
-        const uint32_t w = code == 255 ? 0u : mx_codes8(v[i], mx_scale_value(code));
-        reinterpret_cast<uint32_t*>(q)[out[i]] = w;
-        if ((threadIdx.x & 3) == 0) s[out[i] >> 2] = (uint8_t)code;
-    }
+    if (threadIdx.x % kLanes == 0) s[out / kLanes] = (uint8_t)code;
 }
 
+// U units per thread, kThreads apart.
 template <typename T, int U>
 __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __restrict__ q,
                                                               const uint8_t* __restrict__ s,
@@ -109,18 +117,15 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __r
     }
 }
 
-UnitMap unit_map(int64_t rows, int64_t cols, int64_t ld, int32_t gu_base) {
+UnitMap unit_map(int64_t rows, int64_t cols, int64_t ld, int32_t gu_base, int unit) {
     UnitMap m;
-    m.units = rows * (cols / kUnit);
-    m.per_row = (ld == cols && gu_base < 0) ? m.units : cols / kUnit;
+    m.units = rows * (cols / unit);
+    m.per_row = (ld == cols && gu_base < 0) ? m.units : cols / unit;
     m.ld = ld;
     m.gu_base = gu_base;
     return m;
 }
 
-// One unit per thread until the launch has a workgroup for every CU four
-// times over, then four, so that a thread has 64-128 bytes on the way.
-constexpr int64_t kManyUnits = 4 * 256 * 4 * kThreads;
 // A launch holds fewer than 2^32 threads.
 constexpr int64_t kMaxGrid = (int64_t(1) << 32) / kThreads - 1;
 
@@ -130,16 +135,12 @@ coli_status launch_quantize_mxfp4(const void* x, int32_t dtype, int64_t rows, in
                                   int64_t ld, uint8_t* q, uint8_t* s, int32_t gu_base,
                                   hipStream_t stream) {
     if (rows == 0) return COLI_OK;
-    const UnitMap m = unit_map(rows, cols, ld, gu_base);
     return with_elem(dtype, [&](auto e) -> coli_status {
         using T = decltype(e);
-        const int U = m.units >= kManyUnits ? 4 : 1;
-        const int64_t grid = (m.units + kThreads * U - 1) / (kThreads * U);
-        if (grid > kMaxGrid) return fail(COLI_EUNSUPPORTED, "quantize_mxfp4: 2^37 values or more");
-        if (U == 4)
-            launch(quantize_kernel<T, 4>, dim3((uint32_t)grid), dim3(kThreads), 0, stream, (const T*)x, m, q, s);
-        else
-            launch(quantize_kernel<T, 1>, dim3((uint32_t)grid), dim3(kThreads), 0, stream, (const T*)x, m, q, s);
+        const UnitMap m = unit_map(rows, cols, ld, gu_base, 16 / (int)sizeof(T));
+        const int64_t grid = (m.units + kThreads - 1) / kThreads;
+        if (grid > kMaxGrid) return fail(COLI_EUNSUPPORTED, "quantize_mxfp4: too many values for one launch");
+        launch(quantize_kernel<T>, dim3((uint32_t)grid), dim3(kThreads), 0, stream, (const T*)x, m, q, s);
         COLI_CHECK_LAUNCH("quantize_mxfp4 kernel launch");
         return COLI_OK;
     });
@@ -148,16 +149,13 @@ coli_status launch_quantize_mxfp4(const void* x, int32_t dtype, int64_t rows, in
 coli_status launch_dequantize_mxfp4(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t cols,
                                     void* x, int32_t dtype, int64_t ld, hipStream_t stream) {
     if (rows == 0) return COLI_OK;
-    const UnitMap m = unit_map(rows, cols, ld, -1);
+    const UnitMap m = unit_map(rows, cols, ld, -1, kUnit);
     return with_elem(dtype, [&](auto e) -> coli_status {
         using T = decltype(e);
-        const int U = m.units >= kManyUnits ? 4 : 1;
+        constexpr int U = 2;                      // 1: 4% slower, 4: 1%, 8: 5%
         const int64_t grid = (m.units + kThreads * U - 1) / (kThreads * U);
-        if (grid > kMaxGrid) return fail(COLI_EUNSUPPORTED, "dequantize_mxfp4: 2^37 values or more");
-        if (U == 4)
-            launch(dequantize_kernel<T, 4>, dim3((uint32_t)grid), dim3(kThreads), 0, stream, q, s, m, (T*)x);
-        else
-            launch(dequantize_kernel<T, 1>, dim3((uint32_t)grid), dim3(kThreads), 0, stream, q, s, m, (T*)x);
+        if (grid > kMaxGrid) return fail(COLI_EUNSUPPORTED, "dequantize_mxfp4: too many values for one launch");
+        launch(dequantize_kernel<T, U>, dim3((uint32_t)grid), dim3(kThreads), 0, stream, q, s, m, (T*)x);
         COLI_CHECK_LAUNCH("dequantize_mxfp4 kernel launch");
         return COLI_OK;
     });
