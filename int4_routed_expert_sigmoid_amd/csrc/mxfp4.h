@@ -41,6 +41,25 @@ __device__ __forceinline__ void store_f32(T* p, const float (&in)[N]) {
     *reinterpret_cast<Pack<T, N>*>(p) = r;
 }
 
+// The same past the caches, for what is read once, and for results that are more
+// than the caches hold.
+template <typename T, int N>
+__device__ __forceinline__ void load_f32_once(const T* p, float (&out)[N]) {
+    typedef T V __attribute__((ext_vector_type(N), aligned(sizeof(T))));
+    const V v = __builtin_nontemporal_load(reinterpret_cast<const V*>(p));
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = (float)v[i];
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void store_f32_once(T* p, const float (&in)[N]) {
+    typedef T V __attribute__((ext_vector_type(N), aligned(sizeof(T))));
+    V v;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = (T)in[i];
+    __builtin_nontemporal_store(v, reinterpret_cast<V*>(p));
+}
+
 // ------------------------------------------------------------ MXFP4 blocks
 constexpr int kMxBlock = 32;
 

