@@ -865,7 +865,7 @@ coli_status lines(const MxGemmArgs& a, hipStream_t stream) {
     typedef LineTile<Out, SWIGLU, MT, NF, WM, WN, STAGES> T;
     const int NT = (a.N + T::BN - 1) / T::BN;
     uint32_t grid;
-    if (coli_status st = grid_of(a, T::BM, NT, T::kThreads, &grid)) return st;
+    if (coli_status st = grid_of(a, T::BM, NT, 1, &grid)) return st;
     grid = std::min(grid, kCus);             // LDS holds one workgroup a CU
     launch(mx_line_kernel<Out, SWIGLU, MT, NF, WM, WN, STAGES>, dim3(grid), dim3(T::kThreads), 0, stream, a, NT);
     COLI_CHECK_LAUNCH("mxfp4 product kernel launch");
@@ -877,8 +877,10 @@ coli_status lines(const MxGemmArgs& a, hipStream_t stream) {
 // K 2048, N 6144, over 256 experts unless noted.
 //  - few_rows keeps 16 rows a tile and reads the matrix once per tile. 2 rows an
 //    expert: 507 / 261 against 513 / 260 for lines; 4: 603 / 318 against 588 / 302.
-//    Where lines would not fill the CUs it wins for longer: one expert of 64 rows
-//    14.7 / 9.2 against 31.8 / 16.0, of 256 rows 42.6 / 25.6 against 37.0 / 19.4.
+//    Where lines would not fill the CUs it wins for longer, until its reads, at 5.2
+//    TB/s, take longer than lines' chunks, 1.2 us each: one product of N 8192, K
+//    8192 and 64 rows 32 against 38, 96 rows 46 against 41; N 6144, K 2048 and 128
+//    rows 14 against 19, 192 rows 21 against 20.
 //  - lines of 256 rows halve the traffic into LDS of lines of 128, once they fill
 //    the CUs: N 8192, K 8192, 2048 rows 75 against 94, 1024 rows 66 against 51.
 //  - tiles take what lines cannot (columns not in 512s, scales off 16 bytes):
@@ -890,7 +892,9 @@ coli_status product(const MxGemmArgs& a, hipStream_t stream) {
     const double per = (double)a.rows / experts;
     auto units = [&](int bm, int bn) { return experts * (int64_t)std::ceil(per / bm) * ((a.N + bn - 1) / bn); };
     const bool fits = a.K % 512 == 0 && a.K >= 1024 && a.s_off % 16 == 0 && (uintptr_t)a.as % 16 == 0;
-    const bool few = fits ? per <= 2 || (per <= 128 && units(128, 256) < kCus) : per <= 8 || a.K < 512;
+    const double reads_us = std::ceil(per / kFrag) * experts * a.N * (a.K * (17 / 32.0)) / 5.2e6;
+    const double chunks_us = 1.2 * a.K / 256 + 5;
+    const bool few = fits ? per <= 2 || (units(128, 256) < kCus && reads_us < chunks_us) : per <= 8 || a.K < 512;
     if (few) {
         // a wave takes at least two chunks where there are that many: 11.4 us with 2
         // waves against 13.3 with 4 for 8 rows of 8 experts at K 2048, N 6144 (4

@@ -96,6 +96,9 @@ def test_quantize_extremes(coli, dtype):
     assert sr[0].tolist() == [255, 255] and sr[1, 0] == 255 and sr[1, 1] != 255
     v = coli.dequantize_mxfp4(q, s)
     assert np.array_equal(_host(v), ref.values(qr, sr), equal_nan=True)
+    for out in ("float16", "bfloat16"):                       # beyond float16's range: infinity
+        want = torch.from_numpy(ref.values(qr, sr)).to(_t(out))
+        assert torch.equal(coli.dequantize_mxfp4(q, s, dtype=_t(out)).cpu().nan_to_num(9.0), want.nan_to_num(9.0))
     buf = torch.zeros(8 * 64 + 1, dtype=_t(dtype), device="cuda")
     odd = buf[1:].view(8, 64)
     odd.copy_(x)
@@ -183,7 +186,8 @@ def _case(coli, rng, counts, N, K, spare, aligned=False, **kw):
 # empty experts between them, more units than workgroups, one unit, matrix rows that end inside a tile
 LINES = [([3], 256, 1024, 0), ([5, 0, 4, 130, 128, 129, 0], 300, 1024, 2), ([0] * 9 + [200], 77, 1536, 1),
          ([31, 33, 17, 16, 64, 65], 1000, 2048, 0), (257, 1030, 1024, 0), ([9] * 70, 1100, 1024, 5),
-         ([1025, 1030], 4100, 1024, 3), (2300, 8300, 1024, 0), ([300] + [0] * 1022 + [7], 520, 1024, 0)]
+         ([1025, 1030], 4100, 1024, 3), (2300, 8300, 1024, 0), ([300] + [0] * 1022 + [7], 520, 1024, 0),
+         ([0] * 300, 300, 1024, 700), ([0, 700] * 20, 1100, 1024, 0), ([2] * 500, 260, 1024, 0), ([3] * 500, 260, 1536, 0)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -207,7 +211,8 @@ def test_matmul_matches_reference(coli, dtype, counts, N, K, spare, aligned):
 
 
 @pytest.mark.parametrize("R,N,K", [(1, 64, 2048), (16, 48, 6144), (70, 256, 1024), (260, 256, 2048), (130, 500, 2080),
-                                   (300, 300, 5152), (1100, 520, 1536), (2100, 8200, 1024), (9, 40, 1056)])
+                                   (300, 300, 5152), (1100, 520, 1536), (2100, 8200, 1024), (9, 40, 1056),
+                                   (5, 70, 5152), (3, 33, 4096)])
 def test_matmul_is_exact_where_f32_is(coli, R, N, K):
     """With scales within three binades on each side every partial sum has at most 24 bits."""
     rng = np.random.default_rng(R)
@@ -278,7 +283,8 @@ def test_swiglu_matches_reference(coli, dtype, counts, I, K, spare, aligned):
 @pytest.mark.parametrize("counts,I,K,spare", [
     ([1], 32, 32, 0), ([0, 1, 2], 64, 96, 1), ([16, 17, 0, 1], 96, 640, 2), ([64, 1, 70], 160, 512, 0),
     (130, 288, 1024, 0), ([1] * 9, 256, 2048, 0), (300, 64, 512, 0), ([5, 0, 4, 130, 128, 129], 160, 1024, 2),
-    ([40] * 40, 1056, 1024, 0), (2300, 4128, 1024, 0), ([150, 33], 96, 1056, 0)])
+    ([40] * 40, 1056, 1024, 0), (2300, 4128, 1024, 0), ([150, 33], 96, 1056, 0), ([1, 0, 3], 64, 4640, 0),
+    ([2, 1], 64, 4096, 1)])
 @pytest.mark.parametrize("aligned", [False, True])
 def test_swiglu_to_mxfp4(coli, counts, I, K, spare, aligned):
     """The quantised output is the quantiser's answer to the f32 output (sums exact by the choice of scales)."""

@@ -52,7 +52,7 @@ def _idx(rng, T, k, E, drop=0.0, repeat=False):
 
 @pytest.mark.parametrize("T,k,E,drop", [(0, 2, 4, 0), (1, 1, 1, 0), (1, 8, 256, 0), (3, 4, 7, 0.5), (128, 8, 256, 0.1),
                                         (129, 8, 256, 0.1), (64, 16, 1024, 0.3), (1024, 1, 5, 0), (700, 3, 1024, 0.2),
-                                        (5, 3, 9, 1.0), (2500, 8, 64, 0.05)])
+                                        (5, 3, 9, 1.0), (2500, 8, 64, 0.05), (0, 2, 1020, 0), (9000, 8, 64, 0.05), (8192, 8, 1024, 0.01)])
 def test_union_inverse(coli, T, k, E, drop):
     import torch
     rng = np.random.default_rng(T + k + E)
