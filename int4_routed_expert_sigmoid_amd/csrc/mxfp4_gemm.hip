@@ -390,11 +390,17 @@ struct Scales {
 
 // The scale bytes of blocks b0 .. b0 + BYTES - 1 of a row in two steps, so that the
 // load can be on the way while other work runs: the bytes from b0 on, or the row's
-// last BYTES where fewer are left (no byte outside the row is touched; KB >= 16),
-// and then their shift into place, which leaves 0 (2^-127) for blocks from KB on;
-// their codes are 0 on one side of the product.
-template <int BYTES>
+// last BYTES where fewer are left (no byte outside the row is touched: KB >= BYTES,
+// or SHORT, a row of fewer, byte by byte), and then their shift into place, which
+// leaves 0 (2^-127) for blocks from KB on; their codes are 0 on one side of the
+// product.
+template <int BYTES, bool SHORT>
 __device__ __forceinline__ Scales<BYTES> load_scales(const uint8_t* row, int b0, int KB) {
+    if (SHORT && KB < BYTES) {
+        uint64_t v = 0;
+        for (int i = 0; i < KB; ++i) v |= (uint64_t)load1(row + i) << (8 * i);
+        return Scales<BYTES>{{(uint32_t)v, (uint32_t)(v >> 32)}};
+    }
     typedef __attribute__((address_space(1))) const Pack<uint8_t, BYTES> G;
     G* p = (G*)(row + min(b0, KB - BYTES));
     Scales<BYTES> v;
@@ -402,10 +408,10 @@ __device__ __forceinline__ Scales<BYTES> load_scales(const uint8_t* row, int b0,
     return v;
 }
 
-template <int BYTES>
+template <int BYTES, bool SHORT>
 __device__ __forceinline__ Scales<BYTES> place_scales(const Scales<BYTES>& v, int b0, int KB) {
     const int sh = 8 * (b0 + BYTES - KB);            // uniform
-    if (sh <= 0) return v;
+    if (sh <= 0 || (SHORT && KB < BYTES)) return v;
     uint64_t lo = v.w[0] | (uint64_t)v.w[1] << 32, hi = 0;
     if constexpr (BYTES == 16) hi = v.w[2] | (uint64_t)v.w[3] << 32;
     const uint64_t l = sh < 64 ? lo >> sh | (hi << 1) << (63 - sh) : hi >> (sh - 64);
@@ -424,11 +430,12 @@ struct TileLds {
 };
 
 // Chunks of CS steps.
-template <typename Out, bool SWIGLU, int MT, int NF, int WN, int CS>
+template <typename Out, bool SWIGLU, int MT, int NF, int WN, int CS, bool SHORT>
 struct Tile {
     static constexpr int BM = MT * kFrag, BN = WN * NF * kFrag, kThreads = 64 * WN;
     static constexpr int U = 4 * CS;                          // 16-byte units of a row's chunk
     static_assert(BM <= kThreads && BN <= kThreads, "a thread stages one row's scales");
+    static_assert(!SHORT || U == 8, "a short row's scales are gathered in 8 bytes");
     typedef TileLds<BM, BN, CS> Lds;
 
     // L: the fragments of a wave that hold rows.
@@ -461,8 +468,8 @@ struct Tile {
             const uint32_t b = min(c * U + tid % U, KB - 1) * 16;
 #pragma unroll
             for (int i = 0; i < kStage; ++i) stage[i] = load16(a_base + (s_off[i] + b));
-            stage_ws = load_scales<U>(ws_row, c * U, KB);
-            stage_s = load_scales<U>(as_row, c * U, KB);
+            stage_ws = load_scales<U, SHORT>(ws_row, c * U, KB);
+            stage_s = load_scales<U, SHORT>(as_row, c * U, KB);
         };
         auto stage_store = [&](int c, int buf) {
             const bool in = c * U + tid % U < KB;
@@ -471,8 +478,8 @@ struct Tile {
                 const int x = tid + i * kThreads;
                 lds.code[buf][lds_unit<U>(x / U, x % U)] = in ? stage[i] : u32x4{0, 0, 0, 0};
             }
-            if (tid < BN) lds.w_scale[buf][tid] = place_scales<U>(stage_ws, c * U, KB);
-            if (tid < LM) lds.scale[buf][tid] = place_scales<U>(stage_s, c * U, KB);
+            if (tid < BN) lds.w_scale[buf][tid] = place_scales<U, SHORT>(stage_ws, c * U, KB);
+            if (tid < LM) lds.scale[buf][tid] = place_scales<U, SHORT>(stage_s, c * U, KB);
         };
 
         u32x4 w[CS][NF];
@@ -529,9 +536,9 @@ struct Tile {
     }
 };
 
-template <typename Out, bool SWIGLU, int MT, int NF, int WN, int CS>
+template <typename Out, bool SWIGLU, int MT, int NF, int WN, int CS, bool SHORT>
 __global__ __launch_bounds__(64 * WN, 2) void mx_tile_kernel(MxGemmArgs a, int NT) {
-    typedef Tile<Out, SWIGLU, MT, NF, WN, CS> T;
+    typedef Tile<Out, SWIGLU, MT, NF, WN, CS, SHORT> T;
     __shared__ typename T::Lds lds;
     Unit u;
     if (!find_unit<T::BM>(a, NT, &u)) return;
@@ -849,13 +856,13 @@ coli_status few_rows(const MxGemmArgs& a, hipStream_t stream) {
     return COLI_OK;
 }
 
-template <typename Out, bool SWIGLU, int MT, int NF, int WN, int CS>
+template <typename Out, bool SWIGLU, int MT, int NF, int WN, int CS, bool SHORT>
 coli_status tiles(const MxGemmArgs& a, hipStream_t stream) {
-    typedef Tile<Out, SWIGLU, MT, NF, WN, CS> T;
+    typedef Tile<Out, SWIGLU, MT, NF, WN, CS, SHORT> T;
     const int NT = (a.N + T::BN - 1) / T::BN;
     uint32_t grid;
     if (coli_status st = grid_of(a, T::BM, NT, T::kThreads, &grid)) return st;
-    launch(mx_tile_kernel<Out, SWIGLU, MT, NF, WN, CS>, dim3(grid), dim3(T::kThreads), 0, stream, a, NT);
+    launch(mx_tile_kernel<Out, SWIGLU, MT, NF, WN, CS, SHORT>, dim3(grid), dim3(T::kThreads), 0, stream, a, NT);
     COLI_CHECK_LAUNCH("mxfp4 product kernel launch");
     return COLI_OK;
 }
@@ -883,8 +890,10 @@ coli_status lines(const MxGemmArgs& a, hipStream_t stream) {
 //    rows 14 against 19, 192 rows 21 against 20.
 //  - lines of 256 rows halve the traffic into LDS of lines of 128, once they fill
 //    the CUs: N 8192, K 8192, 2048 rows 75 against 94, 1024 rows 66 against 51.
-//  - tiles take what lines cannot (columns not in 512s, scales off 16 bytes):
-//    16384 rows over 256 experts 884 / 488 against 694 / 385 for lines.
+//  - tiles take what lines cannot (columns not in 512s, fewer than 1024, scales off
+//    16 bytes): 16384 rows over 256 experts 884 / 488 against 694 / 385 for lines.
+//    Against few_rows they win from more rows: 128 experts, K 2880, inter 2048, 8
+//    rows an expert 186 against 217; K 2080, N 2880, 108 against 120.
 template <typename Out, bool SWIGLU>
 coli_status product(const MxGemmArgs& a, hipStream_t stream) {
     constexpr bool mx = std::is_same<Out, MxOut>::value;
@@ -894,7 +903,7 @@ coli_status product(const MxGemmArgs& a, hipStream_t stream) {
     const bool fits = a.K % 512 == 0 && a.K >= 1024 && a.s_off % 16 == 0 && (uintptr_t)a.as % 16 == 0;
     const double reads_us = std::ceil(per / kFrag) * experts * a.N * (a.K * (17 / 32.0)) / 5.2e6;
     const double chunks_us = 1.2 * a.K / 256 + 5;
-    const bool few = fits ? per <= 2 || (units(128, 256) < kCus && reads_us < chunks_us) : per <= 8 || a.K < 512;
+    const bool few = per <= (fits ? 2 : 4) || (units(fits ? 128 : 64, 256) < kCus && reads_us < chunks_us);
     if (few) {
         // a wave takes at least two chunks where there are that many: 11.4 us with 2
         // waves against 13.3 with 4 for 8 rows of 8 experts at K 2048, N 6144 (4
@@ -906,10 +915,13 @@ coli_status product(const MxGemmArgs& a, hipStream_t stream) {
         if (per >= 1024 && units(256, 256) >= kCus) return lines<Out, SWIGLU, 8, 4, 2, 4, 2>(a, stream);
         return lines<Out, SWIGLU, 4, 4, 2, 4, 3>(a, stream);
     }
+    // the other two load 8 and 16 scales of a row at once (short rows: 8000 x 8000 x
+    // 224 73 us against 185 for few_rows, 4000 x 5000 x 96 26 against 57)
+    if (a.K < 512) return tiles<Out, SWIGLU, 8, 4, 4, 2, true>(a, stream);
     // 64-row tiles leave two workgroups a CU: 637 against 711 us for 4072 rows over
     // 256 experts (K 6144, inter 2048), 884 against 870 for 16384
-    if (per <= 32) return tiles<Out, SWIGLU, 4, 4, 4, 4>(a, stream);
-    return tiles<Out, SWIGLU, 8, 4, 4, 2>(a, stream);
+    if (per <= 32) return tiles<Out, SWIGLU, 4, 4, 4, 4, false>(a, stream);
+    return tiles<Out, SWIGLU, 8, 4, 4, 2, false>(a, stream);
 }
 
 }  // namespace

@@ -212,7 +212,8 @@ def test_matmul_matches_reference(coli, dtype, counts, N, K, spare, aligned):
 
 @pytest.mark.parametrize("R,N,K", [(1, 64, 2048), (16, 48, 6144), (70, 256, 1024), (260, 256, 2048), (130, 500, 2080),
                                    (300, 300, 5152), (1100, 520, 1536), (2100, 8200, 1024), (9, 40, 1056),
-                                   (5, 70, 5152), (3, 33, 4096)])
+                                   (5, 70, 5152), (3, 33, 4096), (700, 520, 32), (300, 300, 96), (400, 260, 224),
+                                   (500, 600, 480)])
 def test_matmul_is_exact_where_f32_is(coli, R, N, K):
     """With scales within three binades on each side every partial sum has at most 24 bits."""
     rng = np.random.default_rng(R)
@@ -284,7 +285,7 @@ def test_swiglu_matches_reference(coli, dtype, counts, I, K, spare, aligned):
     ([1], 32, 32, 0), ([0, 1, 2], 64, 96, 1), ([16, 17, 0, 1], 96, 640, 2), ([64, 1, 70], 160, 512, 0),
     (130, 288, 1024, 0), ([1] * 9, 256, 2048, 0), (300, 64, 512, 0), ([5, 0, 4, 130, 128, 129], 160, 1024, 2),
     ([40] * 40, 1056, 1024, 0), (2300, 4128, 1024, 0), ([150, 33], 96, 1056, 0), ([1, 0, 3], 64, 4640, 0),
-    ([2, 1], 64, 4096, 1)])
+    ([2, 1], 64, 4096, 1), ([700, 0, 9], 288, 96, 1), ([300, 600], 512, 224, 0)])
 @pytest.mark.parametrize("aligned", [False, True])
 def test_swiglu_to_mxfp4(coli, counts, I, K, spare, aligned):
     """The quantised output is the quantiser's answer to the f32 output (sums exact by the choice of scales)."""
