@@ -1,6 +1,7 @@
 // C ABI of libcoli_moe: argument checks, workspace carving and the launch
 // sequence of each call (include/coli_moe.h documents every entry point).
 #include <algorithm>
+#include <cmath>
 #include <exception>
 #include <initializer_list>
 #include <mutex>
@@ -592,8 +593,6 @@ coli_status coli_moe_dispatch_bwd(const void* d_g, int32_t g_dtype, int64_t ld_g
     COLI_GUARD_END
 }
 
-static bool finite_scale(float s) { return s == s && s <= 3.4e38f && s >= -3.4e38f; }
-
 coli_status coli_moe_combine(const void* d_rows, int32_t rows_dtype, int64_t ld_rows, int32_t T, int32_t k,
                              int32_t H, const int32_t* d_inv, const float* d_w, const void* d_shared,
                              int64_t ld_shared, float scale, void* d_y, int32_t dtype, int64_t ld_y,
@@ -602,7 +601,7 @@ coli_status coli_moe_combine(const void* d_rows, int32_t rows_dtype, int64_t ld_
     coli_status st = check_permute("combine", T, k, H, rows_dtype, dtype,
                                    {ld_rows, ld_y, d_shared ? ld_shared : ld_y});
     if (st) return st;
-    if (!finite_scale(scale)) return fail(COLI_EINVAL, "combine: scale must be finite");
+    if (!std::isfinite(scale)) return fail(COLI_EINVAL, "combine: scale must be finite");
     if (T == 0) return COLI_OK;
     if (!d_rows || !d_inv || !d_w || !d_y) return fail(COLI_EINVAL, "combine: NULL pointer");
     return launch_combine_rows(d_rows, rows_dtype, ld_rows, T, k, H, d_inv, d_w, d_shared, ld_shared, scale,
@@ -617,7 +616,7 @@ coli_status coli_moe_combine_bwd(const void* d_dy, int32_t dy_dtype, int64_t ld_
     COLI_GUARD_BEGIN
     coli_status st = check_permute("combine_bwd", T, k, H, dy_dtype, rows_dtype, {ld_dy, ld_rows, ld_drows});
     if (st) return st;
-    if (!finite_scale(scale)) return fail(COLI_EINVAL, "combine_bwd: scale must be finite");
+    if (!std::isfinite(scale)) return fail(COLI_EINVAL, "combine_bwd: scale must be finite");
     if (T == 0) return COLI_OK;
     if (!d_dy || !d_rows || !d_inv || !d_w || !d_drows || !d_dw) return fail(COLI_EINVAL, "combine_bwd: NULL pointer");
     return launch_combine_bwd(d_dy, dy_dtype, ld_dy, d_rows, rows_dtype, ld_rows, T, k, H, d_inv, d_w, scale,

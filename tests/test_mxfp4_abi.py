@@ -85,6 +85,9 @@ def test_permutation_refusals(L):
     assert L.coli_moe_combine(16, 0, 8, 2, 2, 8, 16, 16, None, 0, float("inf"), 16, 0, 8, None) == EINVAL
     assert L.coli_moe_combine(16, 0, 8, 2, 2, 8, 16, 16, 16, 4, 1.0, 16, 0, 8, None) == EINVAL
     assert L.coli_moe_combine_bwd(16, 0, 8, 16, 0, 8, 2, 2, 8, 16, 16, float("nan"), 16, 8, 16, None) == EINVAL
+    top = 3.4028234663852886e38                                 # the largest finite value is one
+    assert L.coli_moe_combine(16, 0, 8, 0, 2, 8, 16, 16, None, 0, top, 16, 0, 8, None) == OK
+    assert L.coli_moe_combine_bwd(16, 0, 8, 16, 0, 8, 0, 2, 8, 16, 16, -top, 16, 8, 16, None) == OK
     u = lambda T=2, k=2, E=4, inv=16, ws=1 << 20: L.coli_moe_union_inverse(16, T, k, E, 16, 16, 16, 16, 16, inv, 16, ws, None)
     assert u(T=-1) == EINVAL and u(E=2000) == EUNSUP and u(inv=None) == EINVAL and u(ws=0) == coli.COLI_ENOMEM
 
