@@ -612,12 +612,16 @@ def quantize_mxfp4_expert(shape: MoEShape, gate, up, down, blob=None, stream=Non
     return blob
 
 
-def _groups(table, offsets):
+def _groups(table, offsets, rows, n, q_off, s_off):
     import torch
     _need(table, torch.int64, "table")
     _need(offsets, torch.int32, "offsets")
     if offsets is not None and offsets.numel() != table.numel() + 1:
         raise ValueError("offsets must hold one more value than the table")
+    # what the C types would cut to other values
+    if rows >= 2 ** 31 or not 0 < n < 2 ** 31 or q_off < 0 or s_off < 0:
+        raise ValueError(f"rows {rows} and matrix rows {n} must be below 2^31, q_off {q_off} and s_off {s_off} "
+                         "not negative")
     return table.numel(), None if offsets is None else offsets.data_ptr()
 
 
@@ -628,7 +632,7 @@ def mxfp4_matmul(a, a_s, table, n, q_off=0, s_off=0, offsets=None, dtype=None, o
     gives it (None: one matrix for every row). out in `dtype` (default float32)."""
     import torch
     rows, K = _mx(a, a_s, "a")
-    E, off = _groups(table, offsets)
+    E, off = _groups(table, offsets, rows, n, q_off, s_off)
     if out is None:
         out = torch.empty((rows, n), dtype=dtype or torch.float32, device=a.device)
     code, ld = _rows(out, "out", rows, n, dtype)
@@ -644,8 +648,10 @@ def mxfp4_swiglu(a, a_s, table, inter, q_off=0, s_off=0, offsets=None, dtype=Non
     scales) pair): h as MXFP4 rows, returned as that pair."""
     import torch
     rows, K = _mx(a, a_s, "a")
-    E, off = _groups(table, offsets)
+    E, off = _groups(table, offsets, rows, inter, q_off, s_off)
     if dtype == "mxfp4" or isinstance(out, (tuple, list)):
+        if dtype not in (None, "mxfp4"):
+            raise ValueError(f"out is an MXFP4 pair, dtype {dtype}")
         q, s = _mx_out(*(out or (None, None)), rows, inter, a, "mxfp4_swiglu")
         out, h, hs, code, ld = (q, s), q, s.data_ptr(), MXFP4, inter
     else:
@@ -666,6 +672,8 @@ def union_inverse(idx, E, stream=None):
     _need(idx, torch.int32, "idx")
     T, k = idx.shape
     n = T * k
+    if n >= 2 ** 31:
+        raise ValueError("idx must have fewer than 2^31 values")
     nb = ctypes.c_size_t()
     _check(lib().coli_moe_union_workspace_size(T, k, E, ctypes.byref(nb)))
     buf = torch.empty(3 * E + 2 + 2 * n + (nb.value + 3) // 4, dtype=torch.int32, device=idx.device)
@@ -685,6 +693,8 @@ def _slots(inv, w=None):
     _need(w, torch.float32, "w")
     if inv.dim() != 2 or (w is not None and w.shape != inv.shape):
         raise ValueError("inv must be [T][k], and w of the same shape")
+    if inv.numel() >= 2 ** 31:
+        raise ValueError("inv must have fewer than 2^31 values")
     return inv.shape
 
 

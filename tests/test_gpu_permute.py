@@ -413,6 +413,11 @@ def test_binding_refuses_what_the_calls_cannot_take(coli):
     for f in (lambda: coli.mxfp4_matmul(q, s, table, 8, offsets=torch.zeros(2, dtype=torch.int32, device="cuda")),
               lambda: coli.mxfp4_matmul(q, s, table.int(), 8),
               lambda: coli.mxfp4_swiglu(q, s, table, 48, dtype="mxfp4"),
+              lambda: coli.mxfp4_swiglu(q, s, table[:1], 32, dtype=torch.float32,
+                                        out=coli.quantize_mxfp4(x[:, :32])),
+              lambda: coli.mxfp4_matmul(q, s, table[:1], 8, q_off=-16),
+              lambda: coli.mxfp4_matmul(q, s, table[:1], 8, s_off=-16),
+              lambda: coli.mxfp4_matmul(q, s, table[:1], 2 ** 32 + 8, out=torch.zeros(4, 8, device="cuda")),
               lambda: coli.mxfp4_matmul(q, s, table[:1], 8, out=torch.zeros(4, 9, device="cuda"))):
         with pytest.raises(ValueError):
             f()
