@@ -527,17 +527,27 @@ def _mx(q, s, name):
     raise ValueError(f"{name}: codes {tuple(q.shape)} and scales {tuple(s.shape)} do not match")
 
 
-def _mx_out(q, s, rows, cols, like, name):
+def _new(like, shape, dtype, stream):
+    """A new tensor on like's device that belongs to the stream the call runs on, so that its
+    memory is neither still in use on another stream nor reused there while the call runs."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    import torch
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _mx_out(q, s, rows, cols, like, name, stream):
     import torch
     if cols % 32:
         raise ValueError(f"{name}: the columns of MXFP4 rows must be a multiple of 32, got {cols}")
-    if q is None and s is None:
-        return (like.new_empty((rows, cols // 2), dtype=torch.uint8),
-                like.new_empty((rows, cols // 32), dtype=torch.uint8))
+    fresh = q is None and s is None
     if q is None:
-        q = like.new_empty((rows, cols // 2), dtype=torch.uint8)
+        q = _new(like, (rows, cols // 2), torch.uint8, stream)
     if s is None:
-        s = like.new_empty((rows, cols // 32), dtype=torch.uint8)
+        s = _new(like, (rows, cols // 32), torch.uint8, stream)
+    if fresh:
+        return q, s
     if _mx(q, s, name) != (rows, cols):
         raise ValueError(f"{name}: codes must have shape ({rows}, {cols // 2})")
     return q, s
@@ -545,13 +555,18 @@ def _mx_out(q, s, rows, cols, like, name):
 
 def _enqueue(tensors, stream, fn, *args):
     """The library's call `fn`(*args, stream) on the tensors' device, on its current stream unless
-    one is given. (The raw current stream costs 0.2 us of host time, a Stream object 2.)"""
+    one is given (which has to wait for the inputs, as for any work of another stream). (The raw current stream costs 0.2 us of host time, a Stream object 2.)"""
     import torch
     dev = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"tensors on devices {dev} and {t.get_device()}: one device is needed")
-    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        if stream.device_index != dev:
+            raise ValueError(f"tensors on device {dev}, stream on device {stream.device_index}")
+        raw = stream.cuda_stream
     call = getattr(_lib or lib(), fn)
     if dev == torch.cuda.current_device():
         rc = call(*args, raw)
@@ -567,7 +582,7 @@ def quantize_mxfp4(x, q=None, s=None, stream=None):
     [rows][cols/2], scales uint8 [rows][cols/32])."""
     code, ld = _rows(x, "x")
     rows, cols = x.shape
-    q, s = _mx_out(q, s, rows, cols, x, "quantize_mxfp4")
+    q, s = _mx_out(q, s, rows, cols, x, "quantize_mxfp4", stream)
     _enqueue((x, q, s), stream, "coli_quantize_mxfp4", x.data_ptr(), code, rows, cols, ld,
              q.data_ptr(), s.data_ptr())
     return q, s
@@ -578,7 +593,7 @@ def dequantize_mxfp4(q, s, dtype=None, out=None, stream=None):
     import torch
     rows, cols = _mx(q, s, "dequantize_mxfp4")
     if out is None:
-        out = q.new_empty((rows, cols), dtype=dtype or torch.float32)
+        out = _new(q, (rows, cols), dtype or torch.float32, stream)
     code, ld = _rows(out, "out", rows, cols, dtype)
     _enqueue((q, s, out), stream, "coli_dequantize_mxfp4", q.data_ptr(), s.data_ptr(), rows, cols,
              out.data_ptr(), code, ld)
@@ -603,7 +618,7 @@ def quantize_mxfp4_expert(shape: MoEShape, gate, up, down, blob=None, stream=Non
         if tuple(t.shape) != want:
             raise ValueError(f"{n} must have shape {want}")
     if blob is None:
-        blob = torch.empty(nbytes, dtype=torch.uint8, device=gate.device)
+        blob = _new(gate, (nbytes,), torch.uint8, stream)
     _need(blob, torch.uint8, "blob")
     if blob.numel() < nbytes:
         raise ValueError(f"blob must hold {nbytes} bytes")
@@ -634,7 +649,7 @@ def mxfp4_matmul(a, a_s, table, n, q_off=0, s_off=0, offsets=None, dtype=None, o
     rows, K = _mx(a, a_s, "a")
     E, off = _groups(table, offsets, rows, n, q_off, s_off)
     if out is None:
-        out = torch.empty((rows, n), dtype=dtype or torch.float32, device=a.device)
+        out = _new(a, (rows, n), dtype or torch.float32, stream)
     code, ld = _rows(out, "out", rows, n, dtype)
     _enqueue((a, a_s, table, offsets, out), stream, "coli_mxfp4_matmul", a.data_ptr(),
              a_s.data_ptr(), rows, K, off, E, table.data_ptr(), q_off, s_off, n, out.data_ptr(), code, ld)
@@ -652,11 +667,11 @@ def mxfp4_swiglu(a, a_s, table, inter, q_off=0, s_off=0, offsets=None, dtype=Non
     if dtype == "mxfp4" or isinstance(out, (tuple, list)):
         if dtype not in (None, "mxfp4"):
             raise ValueError(f"out is an MXFP4 pair, dtype {dtype}")
-        q, s = _mx_out(*(out or (None, None)), rows, inter, a, "mxfp4_swiglu")
+        q, s = _mx_out(*(out or (None, None)), rows, inter, a, "mxfp4_swiglu", stream)
         out, h, hs, code, ld = (q, s), q, s.data_ptr(), MXFP4, inter
     else:
         if out is None:
-            out = torch.empty((rows, inter), dtype=dtype or torch.float32, device=a.device)
+            out = _new(a, (rows, inter), dtype or torch.float32, stream)
         code, ld = _rows(out, "out", rows, inter, dtype)
         h, hs, s = out, None, None
     _enqueue((a, a_s, table, offsets, h, s), stream, "coli_mxfp4_swiglu", a.data_ptr(),
@@ -676,7 +691,7 @@ def union_inverse(idx, E, stream=None):
         raise ValueError("idx must have fewer than 2^31 values")
     nb = ctypes.c_size_t()
     _check(lib().coli_moe_union_workspace_size(T, k, E, ctypes.byref(nb)))
-    buf = torch.empty(3 * E + 2 + 2 * n + (nb.value + 3) // 4, dtype=torch.int32, device=idx.device)
+    buf = _new(idx, (3 * E + 2 + 2 * n + (nb.value + 3) // 4,), torch.int32, stream)
     counts, offsets, perm, unique, n_unique, inv, ws = buf.split(
         (E, E + 1, n, E, 1, n, (nb.value + 3) // 4))
     base = buf.data_ptr()
@@ -701,12 +716,11 @@ def _slots(inv, w=None):
 def dispatch(x, inv, out=None, stream=None):
     """out[inv[t, j]] = x[t]: the tokens' rows in the experts' order (rows of no
     slot are left as they are)."""
-    import torch
     T, k = _slots(inv)
     code, ld = _rows(x, "x", T)
     H = x.shape[1]
     if out is None:
-        out = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
+        out = _new(x, (T * k, H), x.dtype, stream)
     ld_out = _rows(out, "out", T * k, H, x.dtype)[1]
     _enqueue((x, inv, out), stream, "coli_moe_dispatch", x.data_ptr(), code, T, k, H, ld,
              inv.data_ptr(), out.data_ptr(), ld_out)
@@ -718,7 +732,7 @@ def dispatch_mxfp4(x, inv, q=None, s=None, stream=None):
     T, k = _slots(inv)
     code, ld = _rows(x, "x", T)
     H = x.shape[1]
-    q, s = _mx_out(q, s, T * k, H, x, "dispatch_mxfp4")
+    q, s = _mx_out(q, s, T * k, H, x, "dispatch_mxfp4", stream)
     _enqueue((x, inv, q, s), stream, "coli_moe_dispatch_mxfp4", x.data_ptr(), code, T, k, H, ld,
              inv.data_ptr(), q.data_ptr(), s.data_ptr())
     return q, s
@@ -726,12 +740,11 @@ def dispatch_mxfp4(x, inv, q=None, s=None, stream=None):
 
 def dispatch_bwd(grad, inv, dtype=None, out=None, stream=None):
     """dispatch's gradient: out[t] = sum_j grad[inv[t, j]], in `dtype` (default grad's)."""
-    import torch
     T, k = _slots(inv)
     g_code, ld_g = _rows(grad, "grad", T * k)
     H = grad.shape[1]
     if out is None:
-        out = torch.empty((T, H), dtype=dtype or grad.dtype, device=grad.device)
+        out = _new(grad, (T, H), dtype or grad.dtype, stream)
     code, ld = _rows(out, "out", T, H, dtype)
     _enqueue((grad, inv, out), stream, "coli_moe_dispatch_bwd", grad.data_ptr(), g_code, ld_g, T, k,
              H, inv.data_ptr(), out.data_ptr(), code, ld)
@@ -741,13 +754,11 @@ def dispatch_bwd(grad, inv, dtype=None, out=None, stream=None):
 def combine(rows, inv, w, shared=None, scale=1.0, dtype=None, out=None, stream=None):
     """out[t] = shared[t] + scale * sum_j w[t, j] * rows[inv[t, j]], in `dtype`
     (default: shared's type, else the rows'). out may be shared."""
-    import torch
     T, k = _slots(inv, w)
     r_code, ld_r = _rows(rows, "rows", T * k)
     H = rows.shape[1]
     if out is None:
-        out = torch.empty((T, H), dtype=dtype or (rows if shared is None else shared).dtype,
-                          device=rows.device)
+        out = _new(rows, (T, H), dtype or (rows if shared is None else shared).dtype, stream)
     code, ld = _rows(out, "out", T, H, dtype)
     ld_s = ld if shared is None else _rows(shared, "shared", T, H, out.dtype)[1]
     _enqueue((rows, inv, w, shared, out), stream, "coli_moe_combine", rows.data_ptr(), r_code, ld_r,
@@ -759,15 +770,14 @@ def combine(rows, inv, w, shared=None, scale=1.0, dtype=None, out=None, stream=N
 def combine_bwd(grad, rows, inv, w, scale=1.0, rows_grad=None, w_grad=None, stream=None):
     """combine's gradients for the output gradient `grad` (which is shared's own
     gradient): (rows_grad in the rows' type and order, w_grad [T][k])."""
-    import torch
     T, k = _slots(inv, w)
     r_code, ld_r = _rows(rows, "rows", T * k)
     H = rows.shape[1]
     g_code, ld_g = _rows(grad, "grad", T, H)
     if rows_grad is None:
-        rows_grad = torch.empty_like(rows, memory_format=torch.contiguous_format)
+        rows_grad = _new(rows, rows.shape, rows.dtype, stream)
     if w_grad is None:
-        w_grad = torch.empty_like(w)
+        w_grad = _new(w, w.shape, w.dtype, stream)
     _slots(inv, w_grad)
     ld_rg = _rows(rows_grad, "rows_grad", T * k, H, rows.dtype)[1]
     _enqueue((grad, rows, inv, w, rows_grad, w_grad), stream, "coli_moe_combine_bwd",

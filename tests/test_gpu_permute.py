@@ -370,6 +370,57 @@ def test_gradients_in_a_graph(coli):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_outputs_belong_to_the_given_stream(coli):
+    """An output that a call allocates is the given stream's: when it is dropped, the current stream does not get its
+    memory, where the call may still be writing. And the results are those of the current stream."""
+    import torch
+    rng = np.random.default_rng(6)
+    T, k, H = 64, 4, 2048
+    x, w = _dev(rng.standard_normal((T, H)).astype(np.float32)), _dev(rng.standard_normal((T, k)).astype(np.float32))
+    rows = _dev(rng.standard_normal((T * k, H)).astype(np.float32))
+    idx = _dev(np.stack([rng.permutation(16)[:k] for _ in range(T)]).astype(np.int32))   # every row is written
+    inv = coli.union_inverse(idx, 16)[5]
+    q, s = coli.quantize_mxfp4(rows)
+    layer = Layer(coli, 1, H, 512, 1, 1)
+    gu = layer.off[0], layer.off[2]
+    shape = coli.MoEShape(128, 128, 1, top_k=1)                          # a blob without gaps
+    gate = _dev(rng.standard_normal((128, 128)).astype(np.float32))
+    calls = [
+        lambda st: coli.quantize_mxfp4(x, stream=st), lambda st: coli.dequantize_mxfp4(q, s, stream=st),
+        lambda st: coli.quantize_mxfp4_expert(shape, gate, gate, gate, stream=st),
+        lambda st: coli.mxfp4_swiglu(q, s, layer.table, 512, *gu, stream=st),
+        lambda st: coli.mxfp4_swiglu(q, s, layer.table, 512, *gu, dtype="mxfp4", stream=st),
+        lambda st: coli.mxfp4_matmul(q, s, layer.table, 512, *gu, stream=st),
+        lambda st: coli.union_inverse(idx, 16, stream=st), lambda st: coli.dispatch(x, inv, stream=st),
+        lambda st: coli.dispatch_mxfp4(x, inv, stream=st), lambda st: coli.dispatch_bwd(rows, inv, stream=st),
+        lambda st: coli.combine(rows, inv, w, stream=st), lambda st: coli.combine_bwd(x, rows, inv, w, stream=st)]
+    side = torch.cuda.Stream()
+    as_tuple = lambda o: o if isinstance(o, tuple) else (o,)
+    for call in calls:
+        want = [o.clone() for o in as_tuple(call(None))]
+        torch.cuda.synchronize()
+        got = as_tuple(call(side))
+        torch.cuda.synchronize()
+        meta = [(o.data_ptr(), o.numel() * o.element_size()) for o in got]
+        for o, v in zip(got, want):
+            assert torch.equal(o, v)
+        del got, o
+        for at, n in meta:
+            held = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(8)]
+            assert all(not at <= h.data_ptr() < at + n for h in held)
+
+
+def test_stream_of_another_device_is_refused(coli):
+    import torch
+
+    class Other:
+        device_index, cuda_stream = 1, 0
+
+    x, out = torch.zeros(2, 64, device="cuda"), torch.zeros(4, 64, device="cuda")
+    with pytest.raises(ValueError, match="stream on device 1"):
+        coli.dispatch(x, torch.zeros(2, 2, dtype=torch.int32, device="cuda"), out=out, stream=Other())
+
+
 def test_places_outside_the_rows_are_skipped(coli):
     """Entries of inv below 0 or at least T*k mark slots without a row, whatever their value."""
     import torch
