@@ -432,7 +432,8 @@ COLI_API coli_status coli_debug_read_log(uint32_t* d_count, void* d_records, int
  * buffers are 16-byte aligned, scale buffers need no alignment.
  * The calls below are stateless, allocate nothing, use no workspace and may be
  * captured into a HIP graph. Where a buffer is both read and written the
- * comment says so; other buffers of a call must not overlap. */
+ * comment says so; other buffers of a call must not overlap. A call that would
+ * need 2^32 threads is refused (quantising: at 2^34 f32 or 2^35 16-bit values). */
 #define COLI_F32 0
 #define COLI_BF16 1
 #define COLI_F16 2
@@ -503,7 +504,8 @@ COLI_API coli_status coli_mxfp4_swiglu(const uint8_t* d_a, const uint8_t* d_as, 
  * coli_moe_union_inverse) mark slots without a row. No two slots may have the
  * same row. Row buffers have T*k rows; rows that no slot has are neither read
  * nor written. Every row stride is in elements and at least H. 1 <= k <= 1024,
- * T*k < 2^31, H positive. Sums run in slot order in f32. */
+ * T*k < 2^31, H positive, T * ceil(H / 1024) and T * ceil(k / 4) < 2^24. Sums run
+ * in slot order in f32. */
 
 /* coli_moe_union that also writes the inverse of d_perm: d_inv [T][k], d_inv[a]
  * = p where d_perm[p] = a, -1 where the entry belongs to no expert. The same
