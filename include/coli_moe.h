@@ -509,7 +509,7 @@ COLI_API coli_status coli_mxfp4_swiglu(const uint8_t* d_a, const uint8_t* d_as, 
 
 /* coli_moe_union that also writes the inverse of d_perm: d_inv [T][k], d_inv[a]
  * = p where d_perm[p] = a, -1 where the entry belongs to no expert. The same
- * arguments, limits and workspace otherwise; at most 1024 assignments take one
+ * arguments, limits and workspace otherwise; at most 2048 assignments take one
  * launch. */
 COLI_API coli_status coli_moe_union_inverse(const int32_t* d_idx, int32_t T, int32_t k, int32_t E,
                                             int32_t* d_counts, int32_t* d_offsets, int32_t* d_perm,

@@ -52,7 +52,9 @@ def _idx(rng, T, k, E, drop=0.0, repeat=False):
 
 @pytest.mark.parametrize("T,k,E,drop", [(0, 2, 4, 0), (1, 1, 1, 0), (1, 8, 256, 0), (3, 4, 7, 0.5), (128, 8, 256, 0.1),
                                         (129, 8, 256, 0.1), (64, 16, 1024, 0.3), (1024, 1, 5, 0), (700, 3, 1024, 0.2),
-                                        (5, 3, 9, 1.0), (2500, 8, 64, 0.05), (0, 2, 1020, 0), (9000, 8, 64, 0.05), (8192, 8, 1024, 0.01)])
+                                        (5, 3, 9, 1.0), (2500, 8, 64, 0.05), (0, 2, 1020, 0), (9000, 8, 64, 0.05), (8192, 8, 1024, 0.01),
+                                        (1023, 4, 256, 0.1), (512, 8, 470, 0.05), (512, 8, 480, 0.05), (4096, 1, 1, 0),
+                                        (1025, 1, 1024, 0.1), (513, 8, 256, 0.1)])
 def test_union_inverse(coli, T, k, E, drop):
     import torch
     rng = np.random.default_rng(T + k + E)
