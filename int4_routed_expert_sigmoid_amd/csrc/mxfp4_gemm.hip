@@ -603,12 +603,13 @@ __global__ __launch_bounds__(64 * WN, 2) void mx_tile_kernel(MxGemmArgs a, int N
 // cycles than the codes: 800 in place of 694 us below). An even number of whole
 // chunks, at least STAGES, and scale rows on 16-byte boundaries.
 //
-// SwiGLU of 16384 rows over 256 experts, K 6144, inter 2048: 694 us, 5.1 TB/s; of
-// 4072 rows 590 us, 5.8 TB/s, what HBM gives. Dense 8191 x 8192 x 8192: 303 us, 3.6
-// PFLOP/s; there the matrix cores work 40% of the time and the loads into LDS
-// alone take 310 us (a chunk's 64 KB are on the way for as long as one chunk is
-// multiplied, which does not cover their latency; LDS has no room for a third
-// slot, and chunks of one step with four slots gave 331 us).
+// SwiGLU of 16384 rows over 256 experts, K 6144, inter 2048: 681 us, 5.2 TB/s; of
+// 4072 rows 590 us, 5.8 TB/s, what HBM gives. Dense 8191 x 8192 x 8192: 282 us, 3.9
+// PFLOP/s (the matrix instructions alone 136). There a chunk's 64 KB are on the way
+// for as long as one chunk is multiplied, which does not cover their latency (LDS
+// has no room for a third slot, and chunks of one step with four slots gave 331 us
+// where this gave 306), and the loads behind a tile's stores wait for those (255 us
+// without stores).
 constexpr int kLineBlocks = 8;               // 16-byte units of a row's chunk
 constexpr int kMaxExperts = 1024;
 constexpr uint32_t kBlockM = 8;
