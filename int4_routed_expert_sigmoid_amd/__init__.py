@@ -627,17 +627,18 @@ def quantize_mxfp4_expert(shape: MoEShape, gate, up, down, blob=None, stream=Non
     return blob
 
 
-def _groups(table, offsets, rows, n, q_off, s_off):
+def _groups(table, offsets, rows, K, n, q_off, s_off):
     import torch
     _need(table, torch.int64, "table")
     _need(offsets, torch.int32, "offsets")
     if offsets is not None and offsets.numel() != table.numel() + 1:
         raise ValueError("offsets must hold one more value than the table")
     # what the C types would cut to other values
-    if rows >= 2 ** 31 or not 0 < n < 2 ** 31 or q_off < 0 or s_off < 0:
-        raise ValueError(f"rows {rows} and matrix rows {n} must be below 2^31, q_off {q_off} and s_off {s_off} "
-                         "not negative")
-    return table.numel(), None if offsets is None else offsets.data_ptr()
+    E = table.numel()
+    if max(rows, K, E) >= 2 ** 31 or not 0 < n < 2 ** 31 or q_off < 0 or s_off < 0:
+        raise ValueError(f"rows {rows}, columns {K}, matrices {E} and matrix rows {n} must be below 2^31, "
+                         f"q_off {q_off} and s_off {s_off} not negative")
+    return E, None if offsets is None else offsets.data_ptr()
 
 
 def mxfp4_matmul(a, a_s, table, n, q_off=0, s_off=0, offsets=None, dtype=None, out=None, stream=None):
@@ -647,7 +648,7 @@ def mxfp4_matmul(a, a_s, table, n, q_off=0, s_off=0, offsets=None, dtype=None, o
     gives it (None: one matrix for every row). out in `dtype` (default float32)."""
     import torch
     rows, K = _mx(a, a_s, "a")
-    E, off = _groups(table, offsets, rows, n, q_off, s_off)
+    E, off = _groups(table, offsets, rows, K, n, q_off, s_off)
     if out is None:
         out = _new(a, (rows, n), dtype or torch.float32, stream)
     code, ld = _rows(out, "out", rows, n, dtype)
@@ -663,7 +664,7 @@ def mxfp4_swiglu(a, a_s, table, inter, q_off=0, s_off=0, offsets=None, dtype=Non
     scales) pair): h as MXFP4 rows, returned as that pair."""
     import torch
     rows, K = _mx(a, a_s, "a")
-    E, off = _groups(table, offsets, rows, inter, q_off, s_off)
+    E, off = _groups(table, offsets, rows, K, inter, q_off, s_off)
     if dtype == "mxfp4" or isinstance(out, (tuple, list)):
         if dtype not in (None, "mxfp4"):
             raise ValueError(f"out is an MXFP4 pair, dtype {dtype}")
@@ -687,8 +688,8 @@ def union_inverse(idx, E, stream=None):
     _need(idx, torch.int32, "idx")
     T, k = idx.shape
     n = T * k
-    if n >= 2 ** 31:
-        raise ValueError("idx must have fewer than 2^31 values")
+    if n >= 2 ** 31 or E >= 2 ** 31:
+        raise ValueError(f"idx must have fewer than 2^31 values, and E, {E}, be below 2^31")
     nb = ctypes.c_size_t()
     _check(lib().coli_moe_union_workspace_size(T, k, E, ctypes.byref(nb)))
     buf = _new(idx, (3 * E + 2 + 2 * n + (nb.value + 3) // 4,), torch.int32, stream)

@@ -118,3 +118,57 @@ def test_reference_quantizer():
     assert s[0, 0] == 127 and (ref.values(q, s) == 6.0).all()   # saturated
     q, s = ref.quantize(np.full((1, 32), 2.0 ** -130))
     assert s[0, 0] == 0 and (q == 0).all()
+
+
+class _Device:
+    """What the binding looks at of a device tensor, without one (sizes that no test could allocate)."""
+    is_cuda = True
+
+    def __init__(self, *shape, dtype=None):
+        import torch
+        self.shape, self.dtype = shape, dtype or torch.uint8
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        n = 1
+        for d in self.shape:
+            n *= d
+        return n
+
+    def is_contiguous(self):
+        return True
+
+    def stride(self):
+        return tuple(int(np.prod(self.shape[i + 1:], dtype=object)) for i in range(self.dim()))
+
+    def data_ptr(self):
+        return 16
+
+    def new_empty(self, shape, dtype=None):
+        return _Device(*shape, dtype=dtype)
+
+
+def test_binding_refuses_sizes_that_the_c_types_would_cut(monkeypatch):
+    """A size of 2^32 + n would arrive as n, pass the library's checks and give the product of a part."""
+    import torch
+
+    def reached(*args):
+        raise AssertionError("the call went on to the library")
+
+    monkeypatch.setattr(coli, "_enqueue", reached)
+    K = 2 ** 32 + 32
+    one = _Device(1, dtype=torch.int64)
+    for a, a_s, table in ((_Device(1, K // 2), _Device(1, K // 32), one),
+                          (_Device(1, 16), _Device(1, 1), _Device(2 ** 32 + 1, dtype=torch.int64))):
+        with pytest.raises(ValueError, match="2\\^31"):
+            coli.mxfp4_matmul(a, a_s, table, 8)
+        with pytest.raises(ValueError, match="2\\^31"):
+            coli.mxfp4_swiglu(a, a_s, table, 32)
+        with pytest.raises(ValueError, match="2\\^31"):
+            coli.mxfp4_swiglu(a, a_s, table, 32, dtype="mxfp4")
+    with pytest.raises(ValueError, match="2\\^31"):
+        coli.union_inverse(_Device(1, 2, dtype=torch.int32), 2 ** 32 + 4)
+    with pytest.raises(AssertionError, match="library"):         # the largest K that the library takes is not refused
+        coli.mxfp4_matmul(_Device(1, 2 ** 21), _Device(1, 2 ** 17), one, 8)
