@@ -447,9 +447,20 @@ static MxBlobLayout mx_blob_layout(size_t H, size_t I) {
     return L;
 }
 
+// check_shape of the fields that MXFP4 blobs use.
+static coli_status check_mx_shape(const coli_moe_shape* shape) {
+    if (!shape) return check_shape(shape);
+    coli_moe_shape s = *shape;
+    s.group = 0;
+    s.topp = 0.f;
+    s.wbits = 0;
+    s.routed_scale = 1.f;
+    return check_shape(&s);
+}
+
 coli_status coli_mxfp4_blob_layout(const coli_moe_shape* shape, size_t off[4], size_t* blob_bytes) {
     COLI_GUARD_BEGIN
-    coli_status st = check_shape(shape);
+    coli_status st = check_mx_shape(shape);
     if (st) return st;
     if (!off || !blob_bytes) return fail(COLI_EINVAL, "off or blob_bytes is NULL");
     const MxBlobLayout L = mx_blob_layout(shape->hidden, shape->inter);
@@ -462,7 +473,7 @@ coli_status coli_mxfp4_blob_layout(const coli_moe_shape* shape, size_t off[4], s
 coli_status coli_quantize_mxfp4_expert(const coli_moe_shape* shape, const void* d_gate, const void* d_up,
                                        const void* d_down, int32_t dtype, void* d_blob, void* stream) {
     COLI_GUARD_BEGIN
-    coli_status st = check_shape(shape);
+    coli_status st = check_mx_shape(shape);
     if (st) return st;
     if (!elem_dtype(dtype)) return fail(COLI_EUNSUPPORTED, "quantize_mxfp4_expert: dtype must be f32, bf16 or f16");
     if (!d_gate || !d_up || !d_down || !d_blob) return fail(COLI_EINVAL, "quantize_mxfp4_expert: NULL pointer");

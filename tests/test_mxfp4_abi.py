@@ -172,3 +172,14 @@ def test_binding_refuses_sizes_that_the_c_types_would_cut(monkeypatch):
         coli.union_inverse(_Device(1, 2, dtype=torch.int32), 2 ** 32 + 4)
     with pytest.raises(AssertionError, match="library"):         # the largest K that the library takes is not refused
         coli.mxfp4_matmul(_Device(1, 2 ** 21), _Device(1, 2 ** 17), one, 8)
+
+
+@pytest.mark.parametrize("kw", [dict(group=64), dict(group=48), dict(topp=-1.0), dict(topp=float("nan")), dict(wbits=3),
+                                dict(routed_scale=float("inf")), dict(routed_scale=float("nan"))])
+def test_mxfp4_blobs_take_no_account_of_fields_they_do_not_use(L, kw):
+    want = coli.mxfp4_blob_layout(coli.MoEShape(96, 32, 4, top_k=2))
+    shape = coli.MoEShape(96, 32, 4, top_k=2, **kw)
+    assert coli.mxfp4_blob_layout(shape) == want
+    s = shape.c()                                               # past the shape, to the pointers' check
+    assert L.coli_quantize_mxfp4_expert(ctypes.byref(s), None, 16, 16, 0, 16, None) == EINVAL
+    assert b"NULL" in L.coli_last_error()
