@@ -527,14 +527,15 @@ def _mx(q, s, name):
     raise ValueError(f"{name}: codes {tuple(q.shape)} and scales {tuple(s.shape)} do not match")
 
 
-def _new(like, shape, dtype, stream):
+def _new(like, shape, dtype, stream, zero=False):
     """A new tensor on like's device that belongs to the stream the call runs on, so that its
     memory is neither still in use on another stream nor reused there while the call runs."""
+    make = like.new_zeros if zero else like.new_empty
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return make(shape, dtype=dtype)
     import torch
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return make(shape, dtype=dtype)
 
 
 def _mx_out(q, s, rows, cols, like, name, stream):
@@ -776,7 +777,7 @@ def combine_bwd(grad, rows, inv, w, scale=1.0, rows_grad=None, w_grad=None, stre
     H = rows.shape[1]
     g_code, ld_g = _rows(grad, "grad", T, H)
     if rows_grad is None:
-        rows_grad = _new(rows, rows.shape, rows.dtype, stream)
+        rows_grad = _new(rows, rows.shape, rows.dtype, stream, zero=True)
     if w_grad is None:
         w_grad = _new(w, w.shape, w.dtype, stream)
     _slots(inv, w_grad)

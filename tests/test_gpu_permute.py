@@ -476,3 +476,29 @@ def test_binding_refuses_what_the_calls_cannot_take(coli):
             f()
     with pytest.raises(coli.ColiError):
         coli.mxfp4_matmul(q, s, table, 8)                                # two matrices need offsets
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("extra", [0, 3])
+@pytest.mark.parametrize("side", [False, True])
+def test_combine_bwd_own_rows_grad_is_zero_where_no_slot_is(coli, dtype, extra, side):
+    """The rows' gradient that the call allocates itself: 0 in the rows that no slot has (whatever its memory held),
+    and what a given buffer gets in the others."""
+    import torch
+    rng = np.random.default_rng(12)
+    T, k, E, H = 19, 4, 9, 1026
+    inv = _dev(ref.sort(_idx(rng, T, k, E, 0.4), E)[2])
+    rows = _dev(rng.standard_normal((T * k + extra, H))).to(_t(dtype))
+    dy, w = _dev(rng.standard_normal((T, H))).to(_t(dtype)), _dev(rng.standard_normal((T, k)).astype(np.float32))
+    want, dw = coli.combine_bwd(dy, rows, inv, w, rows_grad=torch.zeros_like(rows))
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream() if side else None
+    with torch.cuda.stream(stream):
+        held = torch.full_like(rows, float("nan"))              # the memory that the next tensor of this size gets
+        del held
+    got, got_w = coli.combine_bwd(dy, rows, inv, w, stream=stream)
+    torch.cuda.synchronize()
+    used = torch.zeros(len(rows), dtype=torch.bool, device="cuda")
+    used[inv[inv >= 0].long()] = True
+    assert int((~used).sum()) > extra                            # some slots have no row
+    assert bool((got[~used] == 0).all()) and torch.equal(got, want) and torch.equal(got_w, dw)
