@@ -449,7 +449,9 @@ COLI_API coli_status coli_quantize_mxfp4(const void* d_x, int32_t dtype, int64_t
                                          int64_t ld, uint8_t* d_q, uint8_t* d_s, void* stream);
 
 /* The values of d_q, d_s as d_x [rows][cols] (row stride ld): exact in f32 and
- * bf16, rounded half to even (to infinity above its range) in f16. */
+ * bf16, rounded half to even in f16. Above a type's range, infinity: in f32 and
+ * bf16 only under scale codes 253 and 254, which the quantiser never gives (its
+ * largest is 252). */
 COLI_API coli_status coli_dequantize_mxfp4(const uint8_t* d_q, const uint8_t* d_s, int64_t rows,
                                            int64_t cols, void* d_x, int32_t dtype, int64_t ld,
                                            void* stream);

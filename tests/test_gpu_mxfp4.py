@@ -357,3 +357,19 @@ def test_row_results_do_not_depend_on_other_rows(coli):
     s2[4] = 255                                                 # a neighbour of the same expert is NaN
     y2 = coli.mxfp4_matmul(q, s2, *args, offsets=off)
     assert torch.equal(y2[:4], y[:4]) and torch.equal(y2[5:], y[5:]) and bool(y2[4].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_dequantize_every_scale(coli, dtype):
+    """All 256 scale codes with all 16 element codes, the scales beyond the quantiser's (252) among them: 253 and 254
+    pass f32 and bf16 from 2^128 on, to infinity."""
+    import torch
+    q = np.tile(np.arange(16, dtype=np.uint8) | np.arange(16, dtype=np.uint8) << 4, (256, 1))
+    s = np.arange(256, dtype=np.uint8)[:, None]
+    want = torch.from_numpy(ref.values(q, s)).to(_t(dtype))
+    got = coli.dequantize_mxfp4(_dev(q), _dev(s), dtype=_t(dtype)).cpu()
+    nan = want.isnan()
+    assert bool(nan[255].all()) and not bool(nan[:255].any())
+    assert torch.equal(got.isnan(), nan) and torch.equal(got[:255], want[:255])
+    assert torch.equal(torch.signbit(got[:255]), torch.signbit(want[:255]))
+    assert bool(got[254].isinf().any()) and bool(got[253].isinf().any())
