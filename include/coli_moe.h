@@ -500,6 +500,13 @@ COLI_API coli_status coli_mxfp4_swiglu(const uint8_t* d_a, const uint8_t* d_as, 
                                        int32_t inter, void* d_h, uint8_t* d_hs, int32_t dtype,
                                        int64_t ld, void* stream);
 
+/* Testing: which kernel a product of these sizes runs (N: rows of the matrix, 2 *
+ * inter for SwiGLU; grouped: with d_offsets; aligned: scales and buffers on 16-byte
+ * boundaries): 0, 1 few rows, 2 or 4 waves; 2 tiles for K < 512; 3, 4 tiles of 64
+ * or 128 rows; 5, 6 persistent tiles of 128 or 256 rows. Host-only arithmetic. */
+COLI_API coli_status coli_debug_mxfp4_kernel(int32_t rows, int32_t K, int32_t E, int32_t N,
+                                             int32_t grouped, int32_t aligned, int32_t* kernel);
+
 /* ------------------------------------------------------- token permutation
  * The T tokens' rows in the experts' order and back, with gradients. d_inv [T][k]
  * holds each assignment's row in that order; values outside [0, T*k) (-1 from

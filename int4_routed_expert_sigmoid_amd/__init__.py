@@ -35,7 +35,7 @@ EXPORTED = [
     "coli_profile_enable", "coli_profile_clear",
     "coli_profile_summary", "coli_profile_rerun", "coli_read_probe",
     "coli_quantize_mxfp4", "coli_dequantize_mxfp4", "coli_mxfp4_blob_layout",
-    "coli_quantize_mxfp4_expert", "coli_mxfp4_matmul", "coli_mxfp4_swiglu",
+    "coli_quantize_mxfp4_expert", "coli_mxfp4_matmul", "coli_mxfp4_swiglu", "coli_debug_mxfp4_kernel",
     "coli_moe_union_inverse", "coli_moe_dispatch", "coli_moe_dispatch_mxfp4",
     "coli_moe_dispatch_bwd", "coli_moe_combine", "coli_moe_combine_bwd",
 ]
@@ -137,6 +137,7 @@ def lib():
                                             vp]
             L.coli_mxfp4_swiglu.argtypes = [vp, vp, i32, i32, vp, i32, vp, sz, sz, i32, vp, vp, i32,
                                             i64, vp]
+            L.coli_debug_mxfp4_kernel.argtypes = [i32, i32, i32, i32, i32, i32, P(i32)]
             L.coli_moe_union_inverse.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
             L.coli_moe_dispatch.argtypes = [vp, i32, i32, i32, i32, i64, vp, vp, i64, vp]
             L.coli_moe_dispatch_mxfp4.argtypes = [vp, i32, i32, i32, i32, i64, vp, vp, vp, vp]
@@ -680,6 +681,16 @@ def mxfp4_swiglu(a, a_s, table, inter, q_off=0, s_off=0, offsets=None, dtype=Non
              a_s.data_ptr(), rows, K, off, E, table.data_ptr(), q_off, s_off, inter, h.data_ptr(), hs,
              code, ld)
     return out
+
+
+MXFP4_KERNELS = ("few_rows_2", "few_rows_4", "tiles_short", "tiles_64", "tiles_128", "lines_128", "lines_256")
+
+
+def debug_mxfp4_kernel(rows: int, K: int, E: int, N: int, grouped=True, aligned=True) -> str:
+    """coli_debug_mxfp4_kernel: the kernel that a product of these sizes runs."""
+    out = ctypes.c_int32()
+    _check(lib().coli_debug_mxfp4_kernel(rows, K, E, N, int(grouped), int(aligned), ctypes.byref(out)))
+    return MXFP4_KERNELS[out.value]
 
 
 def union_inverse(idx, E, stream=None):

@@ -538,6 +538,21 @@ coli_status coli_mxfp4_swiglu(const uint8_t* d_a, const uint8_t* d_as, int32_t r
     COLI_GUARD_END
 }
 
+coli_status coli_debug_mxfp4_kernel(int32_t rows, int32_t K, int32_t E, int32_t N, int32_t grouped,
+                                    int32_t aligned, int32_t* kernel) {
+    COLI_GUARD_BEGIN
+    if (rows <= 0 || K <= 0 || K % kMxBlock || E < 1 || N <= 0 || (!grouped && E != 1) || !kernel)
+        return fail(COLI_EINVAL, "debug_mxfp4_kernel: sizes that a product does not take, or NULL");
+    static const int32_t some = 0;
+    MxGemmArgs a = {};
+    a.rows = rows; a.K = K; a.E = E; a.N = N;
+    a.offsets = grouped ? &some : nullptr;      // asked for, not read
+    a.s_off = aligned ? 0 : 1;
+    *kernel = choose_mxfp4_kernel(a);
+    return COLI_OK;
+    COLI_GUARD_END
+}
+
 // ------------------------------------------------------- token permutation
 coli_status coli_moe_union_inverse(const int32_t* d_idx, int32_t T, int32_t k, int32_t E, int32_t* d_counts,
                                    int32_t* d_offsets, int32_t* d_perm, int32_t* d_unique,

@@ -122,6 +122,13 @@ struct MxGemmArgs {
     int32_t rows, K, E;
     int32_t N;                   // rows of the matrix (SwiGLU: 2 * inter)
 };
+// The kernel that a product runs: its rows, E, offsets, N, K, s_off and as decide.
+enum MxKernel : int32_t {
+    kMxFewRows2, kMxFewRows4,                    // by waves that share the columns
+    kMxTilesShort, kMxTiles64, kMxTiles128,      // fewer than 512 columns; by rows a tile
+    kMxLines128, kMxLines256,                    // by rows a tile
+};
+MxKernel choose_mxfp4_kernel(const MxGemmArgs& a);
 coli_status launch_mxfp4_gemm(const MxGemmArgs& a, bool swiglu, int32_t dtype, hipStream_t stream);
 
 // Token permutation (permute.hip).

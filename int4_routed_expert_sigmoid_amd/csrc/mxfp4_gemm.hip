@@ -12,7 +12,7 @@
 //
 // Up to about 100 rows an expert the products are bound by reading the matrices
 // (17/32 byte a value): 256 experts' gate and up matrices of 2 x 2048 x 6144 are
-// 3.4 GB. Three kernels, chosen in product() below:
+// 3.4 GB. Three kernels, chosen by choose_mxfp4_kernel below:
 //   few_rows  16 rows a tile, operands straight into registers: single tokens
 //   lines     128 or 256 rows a tile, both operands over LDS, persistent
 //   tiles     64 or 128 rows a tile, rows over LDS: any number of columns
@@ -920,6 +920,22 @@ coli_status lines(const MxGemmArgs& a, hipStream_t stream) {
     return COLI_OK;
 }
 
+template <typename Out, bool SWIGLU>
+coli_status product(const MxGemmArgs& a, hipStream_t stream) {
+    constexpr int kFew = std::is_same<Out, MxOut>::value ? 4 : 2;   // a block of h is four fragments
+    switch (choose_mxfp4_kernel(a)) {
+        case kMxFewRows2: return few_rows<Out, SWIGLU, kFew, 2>(a, stream);
+        case kMxFewRows4: return few_rows<Out, SWIGLU, kFew, 4>(a, stream);
+        case kMxTilesShort: return tiles<Out, SWIGLU, 8, 4, 4, 2, true>(a, stream);
+        case kMxTiles64: return tiles<Out, SWIGLU, 4, 4, 4, 4, false>(a, stream);
+        case kMxTiles128: return tiles<Out, SWIGLU, 8, 4, 4, 2, false>(a, stream);
+        case kMxLines128: return lines<Out, SWIGLU, 4, 4, 2, 4, 3>(a, stream);
+        default: return lines<Out, SWIGLU, 8, 4, 2, 4, 2>(a, stream);
+    }
+}
+
+}  // namespace
+
 // Which kernel, from the average rows of an expert (`per`) and the workgroups the
 // kernel would have. Times on one MI355X, us: SwiGLU K 6144, inter 2048 / product
 // K 2048, N 6144, over 256 experts unless noted.
@@ -935,9 +951,7 @@ coli_status lines(const MxGemmArgs& a, hipStream_t stream) {
 //    16 bytes): 16384 rows over 256 experts 884 / 488 against 694 / 385 for lines.
 //    Against few_rows they win from more rows: 128 experts, K 2880, inter 2048, 8
 //    rows an expert 186 against 217; K 2080, N 2880, 108 against 120.
-template <typename Out, bool SWIGLU>
-coli_status product(const MxGemmArgs& a, hipStream_t stream) {
-    constexpr bool mx = std::is_same<Out, MxOut>::value;
+MxKernel choose_mxfp4_kernel(const MxGemmArgs& a) {
     const int64_t experts = a.offsets ? std::min(a.E, a.rows) : 1;
     const double per = (double)a.rows / experts;
     auto units = [&](int bm, int bn) { return experts * (int64_t)std::ceil(per / bm) * ((a.N + bn - 1) / bn); };
@@ -945,27 +959,18 @@ coli_status product(const MxGemmArgs& a, hipStream_t stream) {
     const double reads_us = std::ceil(per / kFrag) * experts * a.N * (a.K * (17 / 32.0)) / 5.2e6;
     const double chunks_us = 1.2 * a.K / 256 + 5;
     const bool few = per <= (fits ? 2 : 4) || (units(fits ? 128 : 64, 256) < kCus && reads_us < chunks_us);
-    if (few) {
-        // a wave takes at least two chunks where there are that many: 11.4 us with 2
-        // waves against 13.3 with 4 for 8 rows of 8 experts at K 2048, N 6144 (4
-        // chunks), 22.6 with 4 against 23.7 with 2 at K 6144, inter 2048 (12)
-        if (a.K >= 8 * kChunkBlocks * kMxBlock) return few_rows<Out, SWIGLU, mx ? 4 : 2, 4>(a, stream);
-        return few_rows<Out, SWIGLU, mx ? 4 : 2, 2>(a, stream);
-    }
-    if (fits) {
-        if (per >= 1024 && units(256, 256) >= kCus) return lines<Out, SWIGLU, 8, 4, 2, 4, 2>(a, stream);
-        return lines<Out, SWIGLU, 4, 4, 2, 4, 3>(a, stream);
-    }
+    // a wave takes at least two chunks where there are that many: 11.4 us with 2
+    // waves against 13.3 with 4 for 8 rows of 8 experts at K 2048, N 6144 (4
+    // chunks), 22.6 with 4 against 23.7 with 2 at K 6144, inter 2048 (12)
+    if (few) return a.K >= 8 * kChunkBlocks * kMxBlock ? kMxFewRows4 : kMxFewRows2;
+    if (fits) return per >= 1024 && units(256, 256) >= kCus ? kMxLines256 : kMxLines128;
     // the other two load 8 and 16 scales of a row at once (short rows: 8000 x 8000 x
     // 224 73 us against 185 for few_rows, 4000 x 5000 x 96 26 against 57)
-    if (a.K < 512) return tiles<Out, SWIGLU, 8, 4, 4, 2, true>(a, stream);
+    if (a.K < 512) return kMxTilesShort;
     // 64-row tiles leave two workgroups a CU: 637 against 711 us for 4072 rows over
     // 256 experts (K 6144, inter 2048), 884 against 870 for 16384
-    if (per <= 32) return tiles<Out, SWIGLU, 4, 4, 4, 4, false>(a, stream);
-    return tiles<Out, SWIGLU, 8, 4, 4, 2, false>(a, stream);
+    return per <= 32 ? kMxTiles64 : kMxTiles128;
 }
-
-}  // namespace
 
 coli_status launch_mxfp4_gemm(const MxGemmArgs& a, bool swiglu, int32_t dtype, hipStream_t stream) {
     if (swiglu && dtype == COLI_MXFP4) return product<MxOut, true>(a, stream);
