@@ -942,9 +942,12 @@ coli_status product(const MxGemmArgs& a, hipStream_t stream) {
 //  - few_rows keeps 16 rows a tile and reads the matrix once per tile. 2 rows an
 //    expert: 507 / 261 against 513 / 260 for lines; 4: 603 / 318 against 588 / 302.
 //    Where lines would not fill the CUs it wins for longer, until its reads, at 5.2
-//    TB/s, take longer than lines' chunks, 1.2 us each: one product of N 8192, K
-//    8192 and 64 rows 32 against 38, 96 rows 46 against 41; N 6144, K 2048 and 128
-//    rows 14 against 19, 192 rows 21 against 20.
+//    TB/s, and 3 us of its own take longer than lines' chunks, 1.1 us each, and
+//    their 7.8: one product of N 8192, K 8192 and 64 rows 30.5 against 40.1, 96 rows
+//    44.1 against 42.9; N 6144, K 2048 and 128 rows 12.2 against 16.4, 192 rows 17.8
+//    against 16.3; eight of N 2048, K 2048 and 48 rows 14.2 against 15.6, 64 rows
+//    16.7 against 16.2. Against tiles it is given a little more: N 6144, K 2080 and
+//    128 rows 13.9 against 19.8, 192 rows 20.0 against 18.1.
 //  - lines of 256 rows halve the traffic into LDS of lines of 128, once they fill
 //    the CUs: N 8192, K 8192, 2048 rows 75 against 94, 1024 rows 66 against 51.
 //  - tiles take what lines cannot (columns not in 512s, fewer than 1024, scales off
@@ -957,7 +960,7 @@ MxKernel choose_mxfp4_kernel(const MxGemmArgs& a) {
     auto units = [&](int bm, int bn) { return experts * (int64_t)std::ceil(per / bm) * ((a.N + bn - 1) / bn); };
     const bool fits = a.K % 512 == 0 && a.K >= 1024 && a.s_off % 16 == 0 && (uintptr_t)a.as % 16 == 0;
     const double reads_us = std::ceil(per / kFrag) * experts * a.N * (a.K * (17 / 32.0)) / 5.2e6;
-    const double chunks_us = 1.2 * a.K / 256 + 5;
+    const double chunks_us = fits ? 1.1 * a.K / 256 + 4.8 : 1.2 * a.K / 256 + 5;   // less few_rows' own
     const bool few = per <= (fits ? 2 : 4) || (units(fits ? 128 : 64, 256) < kCus && reads_us < chunks_us);
     // a wave takes at least two chunks where there are that many: 11.4 us with 2
     // waves against 13.3 with 4 for 8 rows of 8 experts at K 2048, N 6144 (4
