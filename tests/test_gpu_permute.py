@@ -502,3 +502,49 @@ def test_combine_bwd_own_rows_grad_is_zero_where_no_slot_is(coli, dtype, extra, 
     used[inv[inv >= 0].long()] = True
     assert int((~used).sum()) > extra                            # some slots have no row
     assert bool((got[~used] == 0).all()) and torch.equal(got, want) and torch.equal(got_w, dw)
+
+
+def test_inputs_of_a_given_stream_are_kept_until_it_is_done(coli):
+    """A tensor that is dropped right after a call on another stream than its own: the current stream does not get its
+    memory while the call has still to read (or write) it."""
+    import torch
+    rng = np.random.default_rng(8)
+    T, k, H = 64, 4, 2048
+    f = lambda *s: _dev(rng.standard_normal(s).astype(np.float32))
+    x, rows, w, sh = f(T, H), f(T * k, H), f(T, k), f(T, H)
+    idx = _dev(np.stack([rng.permutation(16)[:k] for _ in range(T)]).astype(np.int32))
+    offsets, inv = coli.union_inverse(idx, 16)[1::4]
+    q, s = coli.quantize_mxfp4(rows)
+    layer = Layer(coli, 1, H, 128, 16, 1)
+    gu = layer.off[0], layer.off[2]
+    calls = [
+        ([x], lambda a, st: coli.quantize_mxfp4(a, stream=st)), ([q, s], lambda a, b, st: coli.dequantize_mxfp4(a, b, stream=st)),
+        ([q, s, layer.table, offsets], lambda a, b, c, d, st: coli.mxfp4_matmul(a, b, c, 128, *gu, offsets=d, stream=st)),
+        ([q, s, layer.table, offsets], lambda a, b, c, d, st: coli.mxfp4_swiglu(a, b, c, 128, *gu, offsets=d, dtype="mxfp4", stream=st)),
+        ([idx], lambda a, st: coli.union_inverse(a, 16, stream=st)), ([x, inv], lambda a, b, st: coli.dispatch(a, b, stream=st)),
+        ([x, inv], lambda a, b, st: coli.dispatch_mxfp4(a, b, stream=st)),
+        ([rows, inv], lambda a, b, st: coli.dispatch_bwd(a, b, stream=st)),
+        ([rows, inv, w, sh], lambda a, b, c, d, st: coli.combine(a, b, c, shared=d, stream=st)),
+        ([x, torch.zeros_like(x)], lambda a, o, st: (coli.dispatch(a, inv[:T // k], out=o, stream=st), ())[1]),   # a given output
+        ([x, rows, inv, w], lambda a, b, c, d, st: coli.combine_bwd(a, b, c, d, stream=st))]
+    side, square = torch.cuda.Stream(), torch.zeros(4096, 4096, device="cuda")
+    as_tuple = lambda o: o if isinstance(o, tuple) else (o,)
+    for tensors, call in calls:
+        want = [o.clone() for o in as_tuple(call(*tensors, None))]
+        own = [t.clone() for t in tensors]
+        spans = [(t.data_ptr(), t.numel() * t.element_size()) for t in own]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(20):                                  # some 20 ms of work in front of the call
+                square @ square
+        got = as_tuple(call(*own, side))
+        del own
+        held = [[torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(4)] for _, n in spans]
+        running = not side.query()
+        for at, n in spans:
+            for h in sum(held, []):
+                assert at + n <= h.data_ptr() or h.data_ptr() + h.numel() <= at
+        torch.cuda.synchronize()
+        assert running
+        for o, v in zip(got, want):
+            assert torch.equal(o, v)
