@@ -474,8 +474,8 @@ COLI_API coli_status coli_quantize_mxfp4_expert(const coli_moe_shape* shape, con
 /* Grouped product: d_y[r][n] = sum_k a[r][k] w[n][k], n < N, for MXFP4 rows d_a
  * [rows][K/2], d_as [rows][K/32] and the MXFP4 matrix w [N][K] of the row's
  * expert. d_offsets [E+1] (device, ascending, as coli_moe_union gives it): rows
- * d_offsets[e] .. d_offsets[e+1]-1 belong to expert e; rows from d_offsets[E] on
- * are neither read nor written. d_offsets NULL: E is 1 and has every row.
+ * d_offsets[e] .. d_offsets[e+1]-1 belong to expert e; rows before d_offsets[0] (of
+ * a share of the experts) and from d_offsets[E] on are neither read nor written. d_offsets NULL: E is 1 and has every row.
  * d_blob_table [E] (device): per expert the buffer that holds its matrix, codes
  * at q_off (a multiple of 16, as the buffer's address) and scales at s_off.
  * The buffers of experts without rows are not read. d_y: type dtype (f32, bf16 or

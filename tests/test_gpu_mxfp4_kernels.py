@@ -76,6 +76,29 @@ def test_swiglu(coli, kernel, counts, K, aligned, spare):
     assert bool((hq[n:] == 0x5a).all()) and bool((hs[n:] == 0x5a).all())
 
 
+GROUPED = {c[0]: c for c in cases.CASES if not isinstance(c[1], int)}.values()   # the last one of each kernel
+
+
+@pytest.mark.parametrize("kernel,counts,K,aligned,spare", GROUPED)
+def test_a_share_of_the_experts(coli, kernel, counts, K, aligned, spare):
+    """Offsets and table of some of the experts, as a rank that has them passes: the rows before the first offset and
+    behind the last are neither read (they hold NaN) nor written."""
+    import torch
+    N, I = cases.matrix_rows(kernel, counts, False), cases.matrix_rows(kernel, counts, True)
+    for n, swiglu in ((N, False), (2 * I, True)):
+        rng = np.random.default_rng(K)
+        mats, q, s, a, off, off_np, R = _case(coli, rng, [7] + counts + [11], n, K, 0, aligned=aligned, lo=119, hi=121)
+        assert coli.debug_mxfp4_kernel(R, K, len(counts), n, True, aligned) == kernel
+        lo, hi = int(off_np[1]), int(off_np[-2])
+        args = (n if not swiglu else I, mats.q_off, mats.s_off)
+        call = coli.mxfp4_swiglu if swiglu else coli.mxfp4_matmul
+        want = call(q, s, mats.table, *args, offsets=off)
+        s[:lo], s[hi:] = 255, 255
+        out = torch.full((R, args[0]), 7.0, device="cuda")
+        call(q, s, mats.table[1:-1], *args, offsets=off[1:-1], out=out)
+        assert torch.equal(out[lo:hi], want[lo:hi]) and bool((out[:lo] == 7.0).all()) and bool((out[hi:] == 7.0).all())
+
+
 @pytest.mark.parametrize("T,E,k,H,I,up,down", cases.LAYERS)
 def test_layer_in_graphs_and_on_streams(coli, T, E, k, H, I, up, down):
     """A layer whose two products run the named kernels: captured calls replay to the eager result, with eager work

@@ -548,3 +548,38 @@ def test_inputs_of_a_given_stream_are_kept_until_it_is_done(coli):
         assert running
         for o, v in zip(got, want):
             assert torch.equal(o, v)
+
+
+def test_given_stream_inside_a_capture(coli):
+    """A captured program that forks into a stream of its own, drops the input and joins again."""
+    import torch
+    rng = np.random.default_rng(10)
+    T, k, E, H = 50, 3, 8, 640
+    x = _dev(rng.standard_normal((T, H)).astype(np.float32))
+    inv = coli.union_inverse(_dev(_idx(rng, T, k, E, 0.0)), E)[5]
+    side = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        t = x * 2
+        side.wait_stream(here)
+        rows = coli.dispatch(t, inv, stream=side)
+        del t
+        other = x * 3                                            # would get t's memory
+        here.wait_stream(side)
+        return rows, other
+
+    want = [t.clone() for t in step()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        eager = step()
+        torch.cuda.synchronize()
+        assert torch.equal(eager[0], want[0]) and torch.equal(eager[1], want[1])
