@@ -141,3 +141,33 @@ def test_layer_in_graphs_and_on_streams(coli, T, E, k, H, I, up, down):
         torch.cuda.synchronize()
         assert all(torch.equal(o, want[i]) for o in outs) and torch.equal(eager, want[i])
         assert torch.equal(other, want[(i + 1) % 3])
+
+
+def _random_rows(g, rows, K, lo):
+    import torch
+    q = torch.empty(rows, K // 2, dtype=torch.uint8, device="cuda").random_(0, 256, generator=g)
+    return q, torch.randint(lo, lo + 2, (rows, K // 32), dtype=torch.uint8, device="cuda", generator=g)
+
+
+@pytest.mark.parametrize("kernel,R,N,K", [("lines_256", 1_060_000, 40, 8192), ("lines_128", 33, 1_060_003, 8192),
+                                          ("few_rows_4", 2, 1_060_003, 8192), ("tiles_128", 1_060_000, 40, 8160),
+                                          ("tiles_128", 33, 1_060_003, 8160), ("tiles_short", 2_100, 1_060_003, 224),
+                                          ("lines_256", 2_100, 1_060_003, 1024)])
+def test_products_past_32_bits(coli, kernel, R, N, K):
+    """Rows, matrices and outputs of more than 2^32 bytes: the last rows and columns are those of a call on them alone."""
+    import torch
+    assert coli.debug_mxfp4_kernel(R, K, 1, N, False) == kernel
+    assert max(R * K // 2, N * K // 2, 2 * R * N) > 2 ** 32
+    g = torch.Generator(device="cuda").manual_seed(N)
+    a, a_s = _random_rows(g, R, K, 126)
+    w, w_s = _random_rows(g, N, K, 119)
+    r, n = min(R, 30), min(N, 35)
+    blob = torch.cat([w.view(-1), w_s.view(-1)])
+    del w, w_s
+    table, s_off = coli.blob_table([blob]), N * K // 2
+    y = coli.mxfp4_matmul(a, a_s, table, N, 0, s_off, dtype=torch.bfloat16)
+    part = coli.mxfp4_matmul(a[-r:].clone(), a_s[-r:].clone(), table, n, (N - n) * (K // 2), s_off + (N - n) * (K // 32),
+                             dtype=torch.bfloat16)               # sums are exact: any kernel gives the same
+    assert torch.equal(y[-r:, -n:], part) and float(part.abs().max()) > 0
+    first = coli.mxfp4_matmul(a[:r].clone(), a_s[:r].clone(), table, n, 0, s_off, dtype=torch.bfloat16)
+    assert torch.equal(y[:r, :n], first) and not torch.equal(first, part)

@@ -583,3 +583,43 @@ def test_given_stream_inside_a_capture(coli):
         eager = step()
         torch.cuda.synchronize()
         assert torch.equal(eager[0], want[0]) and torch.equal(eager[1], want[1])
+
+
+def test_permutation_past_32_bits(coli):
+    """Rows of more than 2^32 elements (9 GB): tokens at either end and in the middle meet the definition."""
+    import torch
+    T, k, H = 70_000, 8, 8192
+    assert T * k * H > 2 ** 32 and T * k * H // 2 > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(5)
+    inv = torch.randperm(T * k, device="cuda", generator=g).to(torch.int32).view(T, k)
+    inv[T // 2, 3] = -1
+    at = torch.tensor([0, 1, T // 2, T - 2, T - 1], device="cuda")
+    x = torch.randn(T, H, device="cuda", generator=g).to(torch.bfloat16)
+    rows = coli.dispatch(x, inv)
+    for t in at.tolist():
+        for j in range(k):
+            p = int(inv[t, j])
+            assert p < 0 or torch.equal(rows[p], x[t])
+    far = int(inv.argmax())                                      # the last row
+    assert int(inv.view(-1)[far]) == T * k - 1 and torch.equal(rows[-1], x[far // k])
+    q, s = coli.dispatch_mxfp4(x, inv)
+    qt, st = coli.quantize_mxfp4(x[far // k][None])
+    assert torch.equal(q[-1], qt[0]) and torch.equal(s[-1], st[0])
+    del q, s
+    kept = (inv[at] >= 0).unsqueeze(2)
+    got = torch.where(kept, rows[inv[at].clamp_min(0).long()].double(), 0.0)             # [5][k][H]
+    dx = coli.dispatch_bwd(rows, inv, dtype=torch.float32)
+    assert ((dx[at].double() - got.sum(1)).abs() <= (k + 2) * U * got.abs().sum(1)).all()
+    w = torch.rand(T, k, device="cuda", generator=g)
+    y = coli.combine(rows, inv, w, dtype=torch.float32)
+    terms = w[at].double().unsqueeze(2) * got
+    assert ((y[at].double() - terms.sum(1)).abs() <= (k + 4) * U * terms.abs().sum(1)).all()
+    drows, dw = coli.combine_bwd(x, rows, inv, w)
+    for t in at.tolist():
+        for j in range(k):
+            p = int(inv[t, j])
+            assert p < 0 or torch.equal(drows[p], (w[t, j] * x[t].float()).to(torch.bfloat16))
+    slots = got * x[at].double().unsqueeze(1)
+    adds = -(-H // 1024) * 8 + 12
+    assert ((dw[at].double() - slots.sum(2)).abs() <= (adds + 2) * U * slots.abs().sum(2)).all()
+    assert float(dw[T // 2, 3]) == 0
