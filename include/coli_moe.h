@@ -480,8 +480,9 @@ COLI_API coli_status coli_quantize_mxfp4_expert(const coli_moe_shape* shape, con
  * at q_off (a multiple of 16, as the buffer's address) and scales at s_off.
  * The buffers of experts without rows are not read. d_y: type dtype (f32, bf16 or
  * f16), row stride ld >= N. Products are exact, sums f32, the result rounded
- * once; a row's result does not depend on the other rows' values. E <= 1024, K <=
- * 2^22. K in multiples of 512, with d_as, s_off and the buffers on 16-byte
+ * once; a row's result does not depend on the other rows' values. (It may on how
+ * many there are: sizes choose the kernel, and with it the order of the f32 sums.)
+ * E <= 1024, K <= 2^22. K in multiples of 512, with d_as, s_off and the buffers on 16-byte
  * boundaries, takes the faster kernel for many rows. */
 COLI_API coli_status coli_mxfp4_matmul(const uint8_t* d_a, const uint8_t* d_as, int32_t rows, int32_t K,
                                        const int32_t* d_offsets, int32_t E,
@@ -490,7 +491,8 @@ COLI_API coli_status coli_mxfp4_matmul(const uint8_t* d_a, const uint8_t* d_as, 
 
 /* The gate/up product with SwiGLU, arguments as coli_mxfp4_matmul: with the
  * expert's interleaved [2 inter][K] matrix, h[r][i] = silu(gate_i . a_r) *
- * (up_i . a_r), i < inter (a positive multiple of 32). dtype f32, bf16 or f16:
+ * (up_i . a_r), i < inter (a positive multiple of 32); silu of a gate below -88.7,
+ * less than 2.7e-37 in size, is 0. dtype f32, bf16 or f16:
  * d_h [rows][ld], d_hs NULL. COLI_MXFP4: the f32 h is quantised in the same
  * launch as coli_quantize_mxfp4 does, d_h [rows][inter/2] codes and d_hs
  * [rows][inter/32] scales (ld is ignored): the input of the down product. */
@@ -518,8 +520,8 @@ COLI_API coli_status coli_debug_mxfp4_kernel(int32_t rows, int32_t K, int32_t E,
 
 /* coli_moe_union that also writes the inverse of d_perm: d_inv [T][k], d_inv[a]
  * = p where d_perm[p] = a, -1 where the entry belongs to no expert. The same
- * arguments, limits and workspace otherwise; at most 2048 assignments take one
- * launch. */
+ * arguments, limits and workspace otherwise; at most 1024 assignments take one
+ * launch, and at most 2048 of up to 958 experts. */
 COLI_API coli_status coli_moe_union_inverse(const int32_t* d_idx, int32_t T, int32_t k, int32_t E,
                                             int32_t* d_counts, int32_t* d_offsets, int32_t* d_perm,
                                             int32_t* d_unique, int32_t* d_n_unique, int32_t* d_inv,

@@ -4,7 +4,9 @@ Argument marshalling only: every step of the layer runs in the library's HIP
 kernels (``csrc/``); this module turns torch tensors into device pointers and
 the current torch stream into a ``hipStream_t``. The names follow the C ABI in
 ``include/coli_moe.h``. There is no CPU fallback: if the library is missing,
-``lib()`` raises.
+``lib()`` raises. Autograd records none of the calls: results of tensors that
+require a gradient are detached, and the gradients that exist (``dispatch_bwd``,
+``combine_bwd``) are calls of their own.
 """
 from __future__ import annotations
 
@@ -652,7 +654,8 @@ def mxfp4_matmul(a, a_s, table, n, q_off=0, s_off=0, offsets=None, dtype=None, o
     """out[r] = W_e(r) a[r] for MXFP4 rows (a, a_s) sorted by expert. table: device
     array (int64) of pointers to the experts' buffers, each with an MXFP4
     [n][K] matrix: codes at q_off, scales at s_off. offsets [E + 1] as union
-    gives it (None: one matrix for every row). out in `dtype` (default float32)."""
+    gives it (None: one matrix for every row). out in `dtype` (default float32); its
+    rows outside the offsets are left as they are (undefined in a new one)."""
     import torch
     rows, K = _mx(a, a_s, "a")
     E, off = _groups(table, offsets, rows, K, n, q_off, s_off)
@@ -667,8 +670,8 @@ def mxfp4_matmul(a, a_s, table, n, q_off=0, s_off=0, offsets=None, dtype=None, o
 def mxfp4_swiglu(a, a_s, table, inter, q_off=0, s_off=0, offsets=None, dtype=None, out=None,
                  stream=None):
     """h[r] = silu(G_e(r) a[r]) * (U_e(r) a[r]), arguments as mxfp4_matmul with the
-    interleaved [2 inter][K] gate/up matrix. dtype "mxfp4" (or out a (codes,
-    scales) pair): h as MXFP4 rows, returned as that pair."""
+    interleaved [2 inter][K] gate/up matrix (rows outside the offsets too). dtype
+    "mxfp4" (or out a (codes, scales) pair): h as MXFP4 rows, returned as that pair."""
     import torch
     rows, K = _mx(a, a_s, "a")
     E, off = _groups(table, offsets, rows, K, inter, q_off, s_off)
@@ -733,7 +736,7 @@ def _slots(inv, w=None):
 
 def dispatch(x, inv, out=None, stream=None):
     """out[inv[t, j]] = x[t]: the tokens' rows in the experts' order (rows of no
-    slot are left as they are)."""
+    slot are left as they are, undefined in a new out)."""
     T, k = _slots(inv)
     code, ld = _rows(x, "x", T)
     H = x.shape[1]
@@ -746,7 +749,8 @@ def dispatch(x, inv, out=None, stream=None):
 
 
 def dispatch_mxfp4(x, inv, q=None, s=None, stream=None):
-    """dispatch with the rows quantised on the way: (codes, scales) of T*k MXFP4 rows."""
+    """dispatch with the rows quantised on the way: (codes, scales) of T*k MXFP4 rows (those
+    of no slot as there)."""
     T, k = _slots(inv)
     code, ld = _rows(x, "x", T)
     H = x.shape[1]

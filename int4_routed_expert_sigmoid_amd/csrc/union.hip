@@ -14,9 +14,10 @@
 //  3. per slab: perm[offsets[e] + slab_prefix[s][e] + rank] = a.
 // Up to kFusedSlabs slabs every workgroup of the third pass does the second for
 // itself (S loads a thread, which cost less than the launch between them). Up to
-// kSmallSlabs, where the inverse is wanted too, one launch does it all: 2048
-// assignments to 256 experts 5.9 us in a graph and 11.5 from the host against 6.2
-// and 14.1; of four slabs 8.9 and 11.3 against 6.5 and 13.9.
+// kSmallSlabs, where the inverse is wanted too and the counts fit the LDS (two
+// slabs: up to 958 experts), one launch does it all: 2048 assignments to 256
+// experts 5.9 us in a graph and 11.5 from the host against 6.2 and 14.1; of four
+// slabs 8.9 and 11.3 against 6.5 and 13.9.
 // The result is the stable counting sort of the assignments by expert.
 #include <algorithm>
 
