@@ -603,8 +603,8 @@ __global__ __launch_bounds__(64 * WN, 2) void mx_tile_kernel(MxGemmArgs a, int N
 // cycles than the codes: 800 in place of 694 us below). An even number of whole
 // chunks, at least STAGES, and scale rows on 16-byte boundaries.
 //
-// SwiGLU of 16384 rows over 256 experts, K 6144, inter 2048: 681 us, 5.2 TB/s; of
-// 4072 rows 590 us, 5.8 TB/s, what HBM gives. Dense 8191 x 8192 x 8192: 282 us, 3.9
+// SwiGLU of 16384 rows over 256 experts, K 6144, inter 2048: 674 us, 5.3 TB/s; of
+// 4072 rows 620 us, 5.6 TB/s, what HBM gives. Dense 8191 x 8192 x 8192: 274 us, 4.0
 // PFLOP/s (the matrix instructions alone 136). There a chunk's 64 KB are on the way
 // for as long as one chunk is multiplied, which does not cover their latency (LDS
 // has no room for a third slot, and chunks of one step with four slots gave 331 us
@@ -940,7 +940,7 @@ coli_status product(const MxGemmArgs& a, hipStream_t stream) {
 // kernel would have. Times on one MI355X, us: SwiGLU K 6144, inter 2048 / product
 // K 2048, N 6144, over 256 experts unless noted.
 //  - few_rows keeps 16 rows a tile and reads the matrix once per tile. 2 rows an
-//    expert: 507 / 261 against 513 / 260 for lines; 4: 603 / 318 against 588 / 302.
+//    expert: 497 / 262 against 498 / 265 for lines; 4: 598 / 321 against 587 / 312.
 //    Where lines would not fill the CUs it wins for longer, until its reads, at 5.2
 //    TB/s, and 3 us of its own take longer than lines' chunks, 1.1 us each, and
 //    their 7.8: one product of N 8192, K 8192 and 64 rows 30.5 against 40.1, 96 rows
@@ -949,11 +949,11 @@ coli_status product(const MxGemmArgs& a, hipStream_t stream) {
 //    16.7 against 16.2. Against tiles it is given a little more: N 6144, K 2080 and
 //    128 rows 13.9 against 19.8, 192 rows 20.0 against 18.1.
 //  - lines of 256 rows halve the traffic into LDS of lines of 128, once they fill
-//    the CUs: N 8192, K 8192, 2048 rows 75 against 94, 1024 rows 66 against 51.
+//    the CUs: N 8192, K 8192, 2048 rows 78 against 99, 1024 rows 68 against 52.
 //  - tiles take what lines cannot (columns not in 512s, fewer than 1024, scales off
-//    16 bytes): 16384 rows over 256 experts 884 / 488 against 694 / 385 for lines.
+//    16 bytes): 16384 rows over 256 experts 877 / 449 against 698 / 394 for lines.
 //    Against few_rows they win from more rows: 128 experts, K 2880, inter 2048, 8
-//    rows an expert 186 against 217; K 2080, N 2880, 108 against 120.
+//    rows an expert 186 against 217; K 2080, N 2880, 109 against 120.
 MxKernel choose_mxfp4_kernel(const MxGemmArgs& a) {
     const int64_t experts = a.offsets ? std::min(a.E, a.rows) : 1;
     const double per = (double)a.rows / experts;
@@ -962,16 +962,16 @@ MxKernel choose_mxfp4_kernel(const MxGemmArgs& a) {
     const double reads_us = std::ceil(per / kFrag) * experts * a.N * (a.K * (17 / 32.0)) / 5.2e6;
     const double chunks_us = fits ? 1.1 * a.K / 256 + 4.8 : 1.2 * a.K / 256 + 5;   // less few_rows' own
     const bool few = per <= (fits ? 2 : 4) || (units(fits ? 128 : 64, 256) < kCus && reads_us < chunks_us);
-    // a wave takes at least two chunks where there are that many: 11.4 us with 2
-    // waves against 13.3 with 4 for 8 rows of 8 experts at K 2048, N 6144 (4
-    // chunks), 22.6 with 4 against 23.7 with 2 at K 6144, inter 2048 (12)
+    // a wave takes at least two chunks where there are that many: 12.5 us with 2
+    // waves against 14.2 with 4 for 8 rows of 8 experts at K 2048, N 6144 (4
+    // chunks), 23.8 with 4 against 24.9 with 2 at K 6144, inter 2048 (12)
     if (few) return a.K >= 8 * kChunkBlocks * kMxBlock ? kMxFewRows4 : kMxFewRows2;
     if (fits) return per >= 1024 && units(256, 256) >= kCus ? kMxLines256 : kMxLines128;
     // the other two load 8 and 16 scales of a row at once (short rows: 8000 x 8000 x
-    // 224 73 us against 185 for few_rows, 4000 x 5000 x 96 26 against 57)
+    // 224 56 us against 184 for few_rows, 4000 x 5000 x 96 24 against 60)
     if (a.K < 512) return kMxTilesShort;
-    // 64-row tiles leave two workgroups a CU: 637 against 711 us for 4072 rows over
-    // 256 experts (K 6144, inter 2048), 884 against 870 for 16384
+    // 64-row tiles leave two workgroups a CU: 681 against 755 us for 4072 rows over
+    // 256 experts (K 6144, inter 2048), 908 against 865 for 16384
     return per <= 32 ? kMxTiles64 : kMxTiles128;
 }
 
