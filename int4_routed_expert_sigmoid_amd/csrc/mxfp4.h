@@ -4,6 +4,7 @@
 #pragma once
 
 #include "common.h"
+#include "row_groups.h"
 
 namespace coli {
 
@@ -110,16 +111,14 @@ coli_status launch_dequantize_mxfp4(const uint8_t* q, const uint8_t* s, int64_t 
                                     void* x, int32_t dtype, int64_t ld, hipStream_t stream);
 
 // Grouped product of MXFP4 rows with MXFP4 matrices; see mxfp4_gemm.hip.
-struct MxGemmArgs {
+struct MxGemmArgs : RowGroups {
     const uint8_t* a;            // [rows][K/2] codes
     const uint8_t* as;           // [rows][K/32] scales
-    const int32_t* offsets;      // [E + 1], or nullptr: every row belongs to matrix 0
-    const void* const* table;    // [E] blobs
     size_t q_off, s_off;         // codes and scales of the matrix in its blob
     void* y;                     // [rows][ld] output, or codes [rows][n_out / 2]
     uint8_t* ys;                 // scales [rows][n_out / 32] of an MXFP4 output
     int64_t ld;
-    int32_t rows, K, E;
+    int32_t K;
     int32_t N;                   // rows of the matrix (SwiGLU: 2 * inter)
 };
 // The kernel that a product runs: its rows, E, offsets, N, K, s_off and as decide.

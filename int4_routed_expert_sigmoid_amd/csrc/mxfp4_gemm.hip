@@ -19,136 +19,15 @@
 #include <algorithm>
 #include <cmath>
 
-#include "mxfp4.h"
+#include "mfma_tiles.h"
 
 namespace coli {
 namespace {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-constexpr int kFrag = 16;                    // rows of one operand of the instruction
-constexpr int kXcds = 8;
-constexpr uint32_t kCus = 256;
-
 // MXFP4 as an output type of the SwiGLU epilogue.
 struct MxOut {};
 
-// ------------------------------------------------------------ work units
-// Unit `w` of the launch: an expert, a stretch of its rows and a stretch of the
-// matrix' rows. Every wave finds its unit from the offsets by itself (a scan
-// over at most 1024 counts), so a product is one launch without a workspace. Up
-// to 256 experts a lane's four offsets and blob pointers are loaded together:
-// the search costs one memory latency. Consecutive workgroups run on different
-// XCDs; each XCD is given one contiguous eighth of the units, ordered by
-// expert, matrix rows, rows, so that units that read the same matrix rows
-// follow each other behind one L2.
-struct Unit {
-    const uint8_t* blob;
-    int m0, rows, nt;            // rows [m0, m0 + rows) (rows <= BM), n tile
-};
-
-constexpr int kLaneExperts = 4;
-
-// First row and row count of experts e0 .. e0 + 3, clamped to the R rows; 0 rows
-// from expert E on.
-__device__ __forceinline__ void expert_rows(const int32_t* offsets, int e0, int E, int R,
-                                            int (&lo)[kLaneExperts], int (&n)[kLaneExperts]) {
-    int o[kLaneExperts + 1];
-#pragma unroll
-    for (int c = 0; c <= kLaneExperts; ++c) o[c] = offsets[min(e0 + c, E)];
-#pragma unroll
-    for (int c = 0; c < kLaneExperts; ++c) {
-        lo[c] = min(max(o[c], 0), R);
-        n[c] = min(max(o[c + 1], lo[c]), R) - lo[c];
-    }
-}
-
-template <int BM>
-__device__ __forceinline__ bool find_unit(const MxGemmArgs& a, int NT, Unit* out) {
-    const int lane = threadIdx.x & 63, E = a.E, R = a.rows;
-    const uint32_t xcd = blockIdx.x % kXcds, at = blockIdx.x / kXcds;
-    if (a.offsets == nullptr) {
-        const uint32_t mt = (R + BM - 1) / BM, total = mt * NT, per = (total + kXcds - 1) / kXcds;
-        const uint32_t w = xcd * per + at;
-        if (at >= per || w >= total) return false;
-        out->blob = (const uint8_t*)a.table[0];
-        out->nt = w / mt;
-        out->m0 = (w % mt) * BM;
-        out->rows = min(BM, R - out->m0);
-        return true;
-    }
-    const int groups = (E + 64 * kLaneExperts - 1) / (64 * kLaneExperts);   // of 4 experts a lane
-    const int e0 = lane * groups * kLaneExperts;
-    int lo[kLaneExperts], n[kLaneExperts];
-    uint32_t tiles = 0;
-    for (int c = groups - 1; c >= 0; --c) {                  // ends with the lane's first group loaded
-        expert_rows(a.offsets, e0 + c * kLaneExperts, E, R, lo, n);
-#pragma unroll
-        for (int i = 0; i < kLaneExperts; ++i) tiles += (n[i] + BM - 1) / BM;
-    }
-    const uint8_t* ptr[kLaneExperts];
-#pragma unroll
-    for (int i = 0; i < kLaneExperts; ++i) ptr[i] = (const uint8_t*)a.table[min(e0 + i, E - 1)];
-    uint32_t incl = tiles;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const uint32_t v = __shfl_up(incl, o);
-        if (lane >= o) incl += v;
-    }
-    const uint32_t total = __builtin_amdgcn_readlane(incl, 63) * NT, per = (total + kXcds - 1) / kXcds;
-    const uint32_t w = xcd * per + at;
-    if (at >= per || w >= total) return false;
-    const uint32_t first = (incl - tiles) * NT;
-    const unsigned long long has = __ballot(w >= first && w < incl * NT);
-    if (has == 0) return false;                              // offsets that are not ascending
-    const int owner = __ffsll(has) - 1;
-    Unit u = {nullptr, 0, 0, 0};
-    if (lane == owner) {
-        uint32_t rest = w - first;
-        for (int c = 0; c < groups; ++c) {
-            if (c > 0) {
-                expert_rows(a.offsets, e0 + c * kLaneExperts, E, R, lo, n);
-#pragma unroll
-                for (int i = 0; i < kLaneExperts; ++i)
-                    ptr[i] = (const uint8_t*)a.table[min(e0 + c * kLaneExperts + i, E - 1)];
-            }
-#pragma unroll
-            for (int i = 0; i < kLaneExperts; ++i) {
-                const uint32_t mt = (n[i] + BM - 1) / BM;
-                if (u.rows == 0 && rest < mt * NT) {
-                    u.blob = ptr[i];
-                    u.nt = rest / mt;
-                    u.m0 = (int)(rest % mt) * BM;
-                    u.rows = min(BM, n[i] - u.m0);
-                    u.m0 += lo[i];
-                }
-                rest -= u.rows == 0 ? mt * NT : 0;
-            }
-        }
-    }
-    const uint64_t b = (uint64_t)u.blob;
-    const uint32_t b_lo = __builtin_amdgcn_readlane((uint32_t)b, owner);
-    const uint32_t b_hi = __builtin_amdgcn_readlane((uint32_t)(b >> 32), owner);
-    out->blob = (const uint8_t*)((uint64_t)b_hi << 32 | b_lo);
-    out->m0 = __builtin_amdgcn_readlane(u.m0, owner);
-    out->rows = __builtin_amdgcn_readlane(u.rows, owner);
-    out->nt = __builtin_amdgcn_readlane(u.nt, owner);
-    return out->rows > 0;
-}
-
 // ------------------------------------------------------------ operands
-struct __attribute__((packed, aligned(1))) Bytes16 {
-    uint32_t w[4];
-};
-// Blob pointers come from a table in memory: without the address space their
-// loads would be generic ones, which also count as LDS accesses.
-typedef __attribute__((address_space(1))) const uint8_t global_u8;
-typedef __attribute__((address_space(1))) const Bytes16 global_bytes16;
-
-__device__ __forceinline__ u32x4 load16(const uint8_t* p) { return *(global_u32x4*)(p); }
-__device__ __forceinline__ uint32_t load1(const uint8_t* p) { return *(global_u8*)(p); }
-
 __device__ __forceinline__ f32x4 mx_mfma(const u32x4& w, uint32_t ws, const u32x4& a, uint32_t as,
                                          f32x4 c) {
     const i32x8 W = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
@@ -165,71 +44,6 @@ constexpr int kChunkBlocks = 4 * kChunkSteps;          // 16 blocks: 512 columns
 __device__ __forceinline__ u32x4 load_scales16(const uint8_t* row, int b0) {
     global_bytes16* v = (global_bytes16*)(row + b0);
     return u32x4{v->w[0], v->w[1], v->w[2], v->w[3]};
-}
-
-// Everything above this point happens before everything below it: memory
-// accesses by the clobber, the instructions that feed `acc` (which the compiler
-// would otherwise collect at the end of the loop, with all their operands
-// live) by the operands. No instruction of its own.
-template <int N>
-__device__ __forceinline__ void hold(f32x4 (&acc)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(acc[i])::"memory");
-}
-
-// ------------------------------------------------------------ epilogues
-__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + expf(-g)) * u; }
-
-// Outputs n0 .. n0 + 3 (those below N) of row `m`.
-template <typename T>
-__device__ __forceinline__ void store4(const MxGemmArgs& a, int m, int n0, int N, const f32x4& v) {
-    T* p = (T*)a.y + (int64_t)m * a.ld + n0;
-    const float r[4] = {v.x, v.y, v.z, v.w};
-    if (n0 + 4 <= N) {
-        store_f32<T, 4>(p, r);
-    } else {
-        for (int i = 0; i < 4 && n0 + i < N; ++i) p[i] = (T)r[i];
-    }
-}
-
-// The four lanes of a row, g = lane / 16, hold quarter g of two 16-byte halves (x:
-// the first): afterwards lane 0 holds quarters 0 and 1 of the first half, lane 1
-// its quarters 2 and 3, lanes 2 and 3 the same of the second.
-__device__ __forceinline__ void swap_quarters(uint32_t& x, uint32_t& y) {
-    const auto a = __builtin_amdgcn_permlane32_swap(x, y, false, false);   // x of lanes 2, 3 with y of 0, 1
-    const auto b = __builtin_amdgcn_permlane16_swap(a[0], a[1], false, false);   // x of 1, 3 with y of 0, 2
-    x = b[0], y = b[1];
-}
-
-// Outputs n0 .. n0 + 31 (those below N) of row `m`, of which this lane holds n0 + 4 g
-// .. + 3 (lo) and n0 + 16 + 4 g .. + 3 (hi): for a 16-bit type one store of 16 bytes a
-// lane, 64 neighbouring bytes a row. Stores hold up the loads behind them, all of
-// which a wave counts in one order: half as many take the dense product of 8191 x
-// 8192 x 8192 from 302 to 283 us, 16384 rows of 256 experts (K 2048, N 6144) from
-// 398 to 391. (For SwiGLU, whose stores the activations space out, it is no gain:
-// 648 with store4, 667 with this; its MXFP4 codes 696 and 707.)
-template <typename T>
-__device__ __forceinline__ void store32(const MxGemmArgs& a, int m, int n0, int N, bool live,
-                                        const f32x4& lo, const f32x4& hi) {
-    const int g = (threadIdx.x & 63) >> 4;
-    if (sizeof(T) == 2 && n0 + 32 <= N) {         // uniform
-        union {
-            T v[4];
-            uint32_t w[2];
-        } x, y;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x.v[i] = (T)lo[i], y.v[i] = (T)hi[i];
-        swap_quarters(x.w[0], y.w[0]);
-        swap_quarters(x.w[1], y.w[1]);
-        if (!live) return;
-        Pack<T, 8> r;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r.v[i] = x.v[i], r.v[4 + i] = y.v[i];
-        *reinterpret_cast<Pack<T, 8>*>((T*)a.y + (int64_t)m * a.ld + n0 + 8 * g) = r;
-    } else if (live) {
-        store4<T>(a, m, n0 + 4 * g, N, lo);
-        store4<T>(a, m, n0 + kFrag + 4 * g, N, hi);
-    }
 }
 
 // One block of 32 h of row `m`, starting at column n0: this lane holds columns
@@ -415,12 +229,6 @@ __device__ __forceinline__ void write_tile(const MxGemmArgs& a, int m0, int rows
 // rows are shared by the waves and come (from L2) over LDS, two chunks deep, and
 // so do the scale bytes of both sides, which a wave then reads one per lane. Rows
 // that are no whole chunks long end in blocks of zeros.
-
-// Position of 16-byte unit b of row r in an LDS chunk of U units a row: the units
-// of a row are permuted by its number, so that the rows that a load reads at one
-// column fall into different banks.
-template <int U>
-__device__ __forceinline__ int lds_unit(int r, int b) { return r * U + (b ^ (r & (U - 1))); }
 
 // BYTES (8 or 16) scale bytes.
 template <int BYTES>
@@ -611,27 +419,6 @@ __global__ __launch_bounds__(64 * WN, 2) void mx_tile_kernel(MxGemmArgs a, int N
 // where this gave 306), and the loads behind a tile's stores wait for those (255 us
 // without stores).
 constexpr int kLineBlocks = 8;               // 16-byte units of a row's chunk
-constexpr int kMaxExperts = 1024;
-constexpr uint32_t kBlockM = 8;
-
-typedef __attribute__((address_space(1))) const void global_void;
-typedef __attribute__((address_space(3))) void lds_void;
-
-// 16 bytes a lane, from p (per lane) to 64 consecutive units at dst (uniform).
-__device__ __forceinline__ void load_to_lds(const uint8_t* p, u32x4* dst) {
-    __builtin_amdgcn_global_load_lds((global_void*)p, (lds_void*)dst, 16, 0, 0);
-}
-
-// Waits until at most N of this wave's vector memory operations are in flight,
-// and for all of its LDS operations. One instruction that no memory access
-// crosses in either direction: the count says which loads are done only if they
-// were issued in program order. (Stores of results count too: with them in
-// flight the wait is longer than it has to be, never shorter.)
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-    static_assert(N < 64, "vmcnt has 6 bits");
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
-}
 
 template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int STAGES>
 struct LineTile {
@@ -652,83 +439,6 @@ struct LineTile {
         uint32_t first[kMaxExperts];                          // first unit of every expert
     };
 };
-
-// The first unit of every expert into first[0 .. E - 1], and the number of units,
-// for a workgroup of THREADS.
-template <int BM, int THREADS>
-__device__ __forceinline__ uint32_t scan_units(const MxGemmArgs& a, int NT, uint32_t* first, uint32_t* scratch) {
-    constexpr int kPer = kMaxExperts / THREADS;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    uint32_t n[kPer], sum = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = tid * kPer + i;
-        n[i] = 0;
-        if (a.offsets == nullptr) {
-            n[i] = e == 0 ? (uint32_t)(a.rows + BM - 1) / BM * NT : 0;
-        } else if (e < a.E) {
-            const int lo = min(max(a.offsets[e], 0), a.rows), hi = min(max(a.offsets[e + 1], lo), a.rows);
-            n[i] = (uint32_t)(hi - lo + BM - 1) / BM * NT;
-        }
-        sum += n[i];
-    }
-    uint32_t incl = sum;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const uint32_t v = __shfl_up(incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 63) scratch[wave] = incl;
-    __syncthreads();
-    uint32_t at = incl - sum, total = 0;
-    for (int w = 0; w < THREADS / 64; ++w) {
-        at += w < wave ? scratch[w] : 0;
-        total += scratch[w];
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        if (tid * kPer + i < a.E) first[tid * kPer + i] = at;
-        at += n[i];
-    }
-    __syncthreads();
-    return __builtin_amdgcn_readfirstlane(total);
-}
-
-struct LineUnit {
-    const uint8_t* blob;
-    int m0, rows, nt;                        // rows 0: no unit
-};
-
-typedef __attribute__((address_space(4))) const int32_t const_i32;
-typedef __attribute__((address_space(4))) const uint64_t const_u64;
-
-// Unit w from the table of first units: a search in LDS, and scalar loads of the
-// expert's offsets and blob, which leave the vector loads in flight alone.
-template <int BM>
-__device__ __forceinline__ LineUnit line_unit(const MxGemmArgs& a, int NT, const uint32_t* first, uint32_t w, bool live) {
-    LineUnit u = {(const uint8_t*)((const_u64*)a.table)[0], 0, 0, 0};
-    const int lane = threadIdx.x & 63;
-    int e = -1;
-    for (int b = 0; b < a.E; b += 64) e += __popcll(__ballot(b + lane < a.E && first[min(b + lane, a.E - 1)] <= w));
-    if (!live || e < 0) return u;
-    int lo = 0, hi = a.rows;
-    if (a.offsets) {
-        lo = min(max(((const_i32*)a.offsets)[e], 0), a.rows);
-        hi = min(max(((const_i32*)a.offsets)[e + 1], lo), a.rows);
-    }
-    const uint32_t mt = (uint32_t)(hi - lo + BM - 1) / BM;
-    if (mt == 0) return u;                   // offsets that are not ascending
-    const uint32_t rest = w - __builtin_amdgcn_readfirstlane(first[e]);
-    u.blob = (const uint8_t*)((const_u64*)a.table)[e];
-    // blocks of kBlockM row tiles by all matrix tiles, row tiles first: the units that
-    // an XCD's workgroups are at together share rows and matrix rows evenly
-    const uint32_t block = min(rest / (kBlockM * NT), (mt - 1) / kBlockM), in = rest - block * kBlockM * NT;
-    const uint32_t wide = min(kBlockM, mt - block * kBlockM);
-    u.nt = min(in / wide, (uint32_t)NT - 1);
-    u.m0 = lo + (int)(block * kBlockM + in % wide) * BM;
-    u.rows = min(BM, hi - u.m0);
-    return u;
-}
 
 template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int STAGES>
 __global__ __launch_bounds__(64 * WM * WN, 2) void mx_line_kernel(MxGemmArgs a, int NT) {
@@ -873,22 +583,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx_line_kernel(MxGemmArgs a, 
     wait_loads<0>();                         // nothing lands in LDS after the workgroup
 }
 
-// Units of a launch at most: the rows fill rows / BM stretches, and each expert
-// with rows may add one that is not full.
-coli_status grid_of(const MxGemmArgs& a, int BM, int NT, int threads, uint32_t* grid) {
-    const int64_t stretches = a.offsets ? (int64_t)a.rows / BM + std::min(a.E, a.rows)
-                                        : ((int64_t)a.rows + BM - 1) / BM;
-    const int64_t g = (stretches * NT + kXcds - 1) / kXcds * kXcds;
-    if (g * threads > 0xffffffffll) return fail(COLI_EUNSUPPORTED, "mxfp4 product: more than 2^32 threads");
-    *grid = (uint32_t)g;
-    return COLI_OK;
-}
-
 template <typename Out, bool SWIGLU, int NF, int KS>
 coli_status few_rows(const MxGemmArgs& a, hipStream_t stream) {
     const int NT = (a.N + NF * kFrag - 1) / (NF * kFrag);
     uint32_t grid;
-    if (coli_status st = grid_of(a, kFrag, NT, 64 * KS, &grid)) return st;
+    if (coli_status st = grid_of(a, kFrag, NT, 64 * KS, "mxfp4 product", &grid)) return st;
     if (a.K % (kChunkBlocks * kMxBlock) == 0)
         launch(mx_few_rows_kernel<Out, SWIGLU, NF, KS, false>, dim3(grid), dim3(64 * KS), 0, stream, a, NT);
     else
@@ -902,7 +601,7 @@ coli_status tiles(const MxGemmArgs& a, hipStream_t stream) {
     typedef Tile<Out, SWIGLU, MT, NF, WN, CS, SHORT> T;
     const int NT = (a.N + T::BN - 1) / T::BN;
     uint32_t grid;
-    if (coli_status st = grid_of(a, T::BM, NT, T::kThreads, &grid)) return st;
+    if (coli_status st = grid_of(a, T::BM, NT, T::kThreads, "mxfp4 product", &grid)) return st;
     launch(mx_tile_kernel<Out, SWIGLU, MT, NF, WN, CS, SHORT>, dim3(grid), dim3(T::kThreads), 0, stream, a, NT);
     COLI_CHECK_LAUNCH("mxfp4 product kernel launch");
     return COLI_OK;
@@ -913,7 +612,7 @@ coli_status lines(const MxGemmArgs& a, hipStream_t stream) {
     typedef LineTile<Out, SWIGLU, MT, NF, WM, WN, STAGES> T;
     const int NT = (a.N + T::BN - 1) / T::BN;
     uint32_t grid;
-    if (coli_status st = grid_of(a, T::BM, NT, 1, &grid)) return st;
+    if (coli_status st = grid_of(a, T::BM, NT, 1, "mxfp4 product", &grid)) return st;
     grid = std::min(grid, kCus);             // LDS holds one workgroup a CU
     launch(mx_line_kernel<Out, SWIGLU, MT, NF, WM, WN, STAGES>, dim3(grid), dim3(T::kThreads), 0, stream, a, NT);
     COLI_CHECK_LAUNCH("mxfp4 product kernel launch");
