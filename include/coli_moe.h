@@ -174,6 +174,39 @@ COLI_API coli_status coli_moe_route_topp(const float* d_logits, const float* d_b
                                 int32_t E, int32_t k, float topp, int32_t* d_idx, float* d_w,
                                 void* stream);
 
+/* Routing with softmax or sigmoid scores and groups of experts, for logits d_logits [T][E]
+ * of type dtype (COLI_F32, COLI_BF16 or COLI_F16; E <= 1024, T < 2^26). score 0: sigmoid, 1: softmax
+ * over the row, in double, rounded once to f32 (d_scores [T][E], nullable, receives them).
+ * key = score + bias (f32; d_bias [E] nullable); an expert whose logit or bias is -infinity
+ * is never chosen. Group j holds experts j * E / n_groups on (n_groups <= 64, a divisor of E);
+ * its value is its largest key (group_top 1) or the f32 sum of its two largest (group_top 2;
+ * of one, where it has one); the groups_kept groups of the largest values stay, and of
+ * their experts the k (<= 32, and at most as many as those groups have) of the largest keys,
+ * in descending order, go to d_idx [T][k]. Equal values and keys go to the lower index.
+ * Slots for which no expert is left get d_idx -1 and d_w 0 (a row of -infinity has only
+ * those). d_w [T][k] = scale * score / (sum of the chosen scores, in slot order, double; all
+ * 0: equal shares), or scale * score with norm 0; rounded to f32. A NaN key counts as the
+ * largest, so that the weights of its token are NaN. scale must be finite. Uses no
+ * workspace, and may be captured. */
+#define COLI_SCORE_SIGMOID 0
+#define COLI_SCORE_SOFTMAX 1
+COLI_API coli_status coli_moe_route_groups(const void* d_logits, int32_t dtype, const float* d_bias,
+                                           int32_t T, int32_t E, int32_t k, int32_t score,
+                                           int32_t n_groups, int32_t groups_kept, int32_t group_top,
+                                           int32_t norm, float scale, int32_t* d_idx, float* d_w,
+                                           float* d_scores, void* stream);
+
+/* Its gradient: d_dlogits [T][E] of type grad_dtype from d_dw [T][k], the gradient of the
+ * weights (of slots whose d_idx is outside [0, E) not used), and d_dscores [T][E] (nullable),
+ * that of the scores. d_logits, d_idx, score, norm and scale as there; the choice itself and
+ * the bias have no gradient. Sums are f32. Weights that are equal shares of a sum of 0 have
+ * gradient 0. */
+COLI_API coli_status coli_moe_route_groups_bwd(const float* d_dw, const void* d_logits, int32_t dtype,
+                                               const int32_t* d_idx, int32_t T, int32_t E, int32_t k,
+                                               int32_t score, int32_t norm, float scale,
+                                               const float* d_dscores, void* d_dlogits,
+                                               int32_t grad_dtype, void* stream);
+
 /* Workspace bytes coli_moe_union needs for T tokens, k slots, E experts. */
 COLI_API coli_status coli_moe_union_workspace_size(int32_t T, int32_t k, int32_t E, size_t* bytes);
 
@@ -438,6 +471,7 @@ COLI_API coli_status coli_debug_read_log(uint32_t* d_count, void* d_records, int
 #define COLI_BF16 1
 #define COLI_F16 2
 #define COLI_MXFP4 3   /* as an output type of coli_mxfp4_swiglu */
+#define COLI_FP8 4     /* as an output type of coli_fp8_swiglu */
 
 /* Quantise d_x [rows][cols] of type dtype (COLI_F32, COLI_BF16 or COLI_F16; row
  * r starts ld elements after row r-1, ld >= cols) to d_q [rows][cols/2] and d_s
@@ -509,6 +543,103 @@ COLI_API coli_status coli_mxfp4_swiglu(const uint8_t* d_a, const uint8_t* d_as, 
 COLI_API coli_status coli_debug_mxfp4_kernel(int32_t rows, int32_t K, int32_t E, int32_t N,
                                              int32_t grouped, int32_t aligned, int32_t* kernel);
 
+/* -------------------------------------------------------------- FP8 experts
+ * 8-bit floating point with a scale for each block of 128: OCP e4m3 codes (as in
+ * coli_convert_fp8_int4; NaN codes stand for NaN) and f32 scales, value = code * scale. A
+ * row of K values (K a positive multiple of 16) is K bytes of codes and ceil(K / 128) scales,
+ * one per 128 columns (the last block may be short); a matrix [N][K] is N such rows of
+ * codes and [ceil(N / 128)][ceil(K / 128)] scales, one per 128 x 128 block: the checkpoint's
+ * own format. Code buffers are 16-byte aligned, scales 4. Unless said otherwise the calls
+ * allocate nothing, use no workspace, may be captured into a HIP graph, and their buffers do
+ * not overlap. A call that would need 2^32 threads is refused.
+ * The quantisers' scale is the smallest power of two (at least 2^-126) that brings the
+ * block's largest |x| to 448 or below, values are x / scale, which is exact, rounded half to
+ * even; a block that holds an infinity or a NaN gets scale NaN and codes 0. The products
+ * take any scales. A product sums the 128 columns of a block, then the blocks' sums times both
+ * scales (multiplied with each other first), in f32. For f32 results the products are exact; for
+ * 16-bit and FP8 results the matrix instruction adds 8 products at a time, cut off 2^-13 below
+ * the largest exponent among them (1.5e-5 of a sum of normal values). */
+
+/* Rows d_x [rows][cols] (type dtype, row stride ld elements) to d_q [rows][cols] and d_s
+ * [rows][ceil(cols / 128)]. */
+COLI_API coli_status coli_quantize_fp8(const void* d_x, int32_t dtype, int64_t rows, int64_t cols,
+                                       int64_t ld, uint8_t* d_q, float* d_s, void* stream);
+
+/* `count` matrices d_x [rows][cols] of type dtype, x_stride elements apart with row stride ld, by
+ * blocks of 128 x 128: to codes d_q [rows][cols] and scales d_s, q_stride and s_stride bytes
+ * apart (multiples of 16 and 4), and transposed to d_qt [cols][rows] and d_st
+ * [ceil(cols / 128)][ceil(rows / 128)] (the operand of the product's input gradient; rows a
+ * multiple of 16 too), qt_stride and st_stride apart. Either pair may be NULL. rows, cols below
+ * 2^30. */
+COLI_API coli_status coli_quantize_fp8_matrix(const void* d_x, int32_t dtype, int32_t count, int64_t rows,
+                                              int64_t cols, int64_t ld, int64_t x_stride, uint8_t* d_q,
+                                              int64_t q_stride, float* d_s, int64_t s_stride,
+                                              uint8_t* d_qt, int64_t qt_stride, float* d_st,
+                                              int64_t st_stride, void* stream);
+
+/* Rows d_x [rows][cols] sorted by expert (d_offsets [E + 1] as in coli_fp8_matmul; NULL: E is 1)
+ * for coli_fp8_wgrad: quantised over 128 of an expert's rows by one column, and laid out by columns.
+ * The experts' rows follow each other in d_qt [cols][ld_t], each expert's beginning at a multiple
+ * of 128, with codes 0 behind its last; d_st [ld_t / 128][cols] holds the scales' exponents, code c
+ * for 2^(c - 127), 255 for NaN. ld_t, a multiple of 128, is at least coli_fp8_columns_ld's. What lies
+ * behind the last expert's rows is left as it is. d_q, d_s (nullable, together): the same rows as
+ * coli_quantize_fp8 gives them, in the same pass (rows outside the offsets are left as they are). */
+COLI_API coli_status coli_quantize_fp8_columns(const void* d_x, int32_t dtype, int32_t rows, int32_t cols,
+                                               int64_t ld, const int32_t* d_offsets, int32_t E,
+                                               uint8_t* d_qt, int64_t ld_t, uint8_t* d_st, uint8_t* d_q,
+                                               float* d_s, void* stream);
+
+/* The least ld_t for `rows` rows over E experts: 128 * floor((rows + 127 min(E, rows)) / 128).
+ * Host-only arithmetic. */
+COLI_API coli_status coli_fp8_columns_ld(int32_t rows, int32_t E, int64_t* ld_t);
+
+/* The values of d_q [rows][cols] with scales for 128 columns of `block_rows` rows (1 or 128) as
+ * d_x [rows][cols] (type dtype, row stride ld): one f32 product, rounded to the type. */
+COLI_API coli_status coli_dequantize_fp8(const uint8_t* d_q, const float* d_s, int64_t rows, int64_t cols,
+                                         int32_t block_rows, void* d_x, int32_t dtype, int64_t ld,
+                                         void* stream);
+
+/* An expert as one buffer: byte offsets of gate, up and down codes, then of their scales, and the
+ * buffer's size (hidden and inter multiples of 32; group, topp, wbits and routed_scale are not
+ * used). Host-only arithmetic. */
+COLI_API coli_status coli_fp8_blob_layout(const coli_moe_shape* shape, size_t off[6], size_t* blob_bytes);
+
+/* Grouped product: d_y[r][n] = sum_k a[r][k] w[n][k], n < N, for FP8 rows d_a, d_as and the FP8
+ * matrix w [N][K] of the row's expert; arguments and rows outside the offsets as in
+ * coli_mxfp4_matmul, codes at q_off (a multiple of 16) and scales at s_off (of 4) of the expert's
+ * buffer (16-byte aligned). With the transposed matrices (coli_quantize_fp8_matrix) it is the input
+ * gradient. E <= 1024, K <= 2^22. */
+COLI_API coli_status coli_fp8_matmul(const uint8_t* d_a, const float* d_as, int32_t rows, int32_t K,
+                                     const int32_t* d_offsets, int32_t E, const void* const* d_blob_table,
+                                     size_t q_off, size_t s_off, int32_t N, void* d_y, int32_t dtype,
+                                     int64_t ld, void* stream);
+
+/* The gate/up product with SwiGLU: h[r][i] = silu(gate_i . a_r) * (up_i . a_r), i < inter, for the
+ * matrices gate [inter][K] at q_off, s_off and up [inter][K] at up_q_off, up_s_off. dtype f32, bf16 or
+ * f16: d_h [rows][ld], d_hs NULL. COLI_FP8 (inter a multiple of 16): the f32 h is quantised in the
+ * same launch as coli_quantize_fp8 does, d_h [rows][inter] codes and d_hs [rows][ceil(inter / 128)]
+ * scales (ld is ignored). silu as in coli_mxfp4_swiglu. */
+COLI_API coli_status coli_fp8_swiglu(const uint8_t* d_a, const float* d_as, int32_t rows, int32_t K,
+                                     const int32_t* d_offsets, int32_t E, const void* const* d_blob_table,
+                                     size_t q_off, size_t s_off, size_t up_q_off, size_t up_s_off,
+                                     int32_t inter, void* d_h, float* d_hs, int32_t dtype, int64_t ld,
+                                     void* stream);
+
+/* Every expert's matrix gradient: d_dw[e][n][k] = sum over the expert's rows r of g[r][n] x[r][k] (0
+ * without rows), for g [rows][N] and x [rows][K] (N, K multiples of 16) as coli_quantize_fp8_columns
+ * lays them out with the same rows, d_offsets, E and ld_t. d_dw [E][N][ld] of type dtype, ld >= K;
+ * accumulate: the sums are added to what it holds. Sums as the products'. */
+COLI_API coli_status coli_fp8_wgrad(const uint8_t* d_gt, const uint8_t* d_gs, const uint8_t* d_xt,
+                                    const uint8_t* d_xs, int64_t ld_t, int32_t rows,
+                                    const int32_t* d_offsets, int32_t E, int32_t N, int32_t K,
+                                    int32_t accumulate, void* d_dw, int32_t dtype, int64_t ld,
+                                    void* stream);
+
+/* Testing: which kernel a product of these sizes runs (grouped: with d_offsets). Host-only
+ * arithmetic. */
+COLI_API coli_status coli_debug_fp8_kernel(int32_t rows, int32_t K, int32_t E, int32_t N, int32_t grouped,
+                                           int32_t swiglu, int32_t* kernel);
+
 /* ------------------------------------------------------- token permutation
  * The T tokens' rows in the experts' order and back, with gradients. d_inv [T][k]
  * holds each assignment's row in that order; values outside [0, T*k) (-1 from
@@ -537,6 +668,12 @@ COLI_API coli_status coli_moe_dispatch(const void* d_x, int32_t dtype, int32_t T
 COLI_API coli_status coli_moe_dispatch_mxfp4(const void* d_x, int32_t dtype, int32_t T, int32_t k,
                                              int32_t H, int64_t ld_x, const int32_t* d_inv,
                                              uint8_t* d_q, uint8_t* d_s, void* stream);
+
+/* The same into FP8 rows d_q [T*k][H], d_s [T*k][ceil(H / 128)], each token quantised as by
+ * coli_quantize_fp8 (H a multiple of 16). */
+COLI_API coli_status coli_moe_dispatch_fp8(const void* d_x, int32_t dtype, int32_t T, int32_t k, int32_t H,
+                                           int64_t ld_x, const int32_t* d_inv, uint8_t* d_q, float* d_s,
+                                           void* stream);
 
 /* Gradient of coli_moe_dispatch: d_dx[t] = sum_j d_g[d_inv[t][j]] (0 for a token
  * without rows). d_g has type g_dtype, d_dx type dtype. */

@@ -6,7 +6,8 @@ the current torch stream into a ``hipStream_t``. The names follow the C ABI in
 ``include/coli_moe.h``. There is no CPU fallback: if the library is missing,
 ``lib()`` raises. Autograd records none of the calls: results of tensors that
 require a gradient are detached, and the gradients that exist (``dispatch_bwd``,
-``combine_bwd``) are calls of their own.
+``combine_bwd``, ``route_groups_bwd``, ``fp8_wgrad``, and ``fp8_matmul`` with transposed
+matrices) are calls of their own.
 """
 from __future__ import annotations
 
@@ -20,7 +21,7 @@ SO_PATH = os.path.join(HERE, "libcoli_moe.so")
 
 COLI_OK, COLI_EINVAL, COLI_EUNSUPPORTED, COLI_EHIP, COLI_ENOMEM, COLI_EBUSY = 0, -1, -2, -3, -4, -5
 PATH_AUTO, PATH_GEMV, PATH_MFMA = 0, 1, 2
-F32, BF16, F16, MXFP4 = 0, 1, 2, 3
+F32, BF16, F16, MXFP4, FP8 = 0, 1, 2, 3, 4
 
 EXPORTED = [
     "coli_last_error", "coli_version", "coli_expert_blob_layout", "coli_quantize_int4",
@@ -40,6 +41,10 @@ EXPORTED = [
     "coli_quantize_mxfp4_expert", "coli_mxfp4_matmul", "coli_mxfp4_swiglu", "coli_debug_mxfp4_kernel",
     "coli_moe_union_inverse", "coli_moe_dispatch", "coli_moe_dispatch_mxfp4",
     "coli_moe_dispatch_bwd", "coli_moe_combine", "coli_moe_combine_bwd",
+    "coli_moe_route_groups", "coli_moe_route_groups_bwd",
+    "coli_quantize_fp8", "coli_quantize_fp8_matrix", "coli_quantize_fp8_columns", "coli_fp8_columns_ld",
+    "coli_dequantize_fp8", "coli_fp8_blob_layout", "coli_fp8_matmul", "coli_fp8_swiglu", "coli_fp8_wgrad",
+    "coli_debug_fp8_kernel", "coli_moe_dispatch_fp8",
 ]
 
 
@@ -148,6 +153,23 @@ def lib():
                                            i64, vp]
             L.coli_moe_combine_bwd.argtypes = [vp, i32, i64, vp, i32, i64, i32, i32, i32, vp, vp, f32,
                                                vp, i64, vp, vp]
+            L.coli_moe_route_groups.argtypes = [vp, i32, vp, i32, i32, i32, i32, i32, i32, i32, i32, f32,
+                                                vp, vp, vp, vp]
+            L.coli_moe_route_groups_bwd.argtypes = [vp, vp, i32, vp, i32, i32, i32, i32, i32, f32, vp, vp,
+                                                    i32, vp]
+            L.coli_quantize_fp8.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
+            L.coli_quantize_fp8_matrix.argtypes = [vp, i32, i32, i64, i64, i64, i64, vp, i64, vp, i64, vp,
+                                                   i64, vp, i64, vp]
+            L.coli_quantize_fp8_columns.argtypes = [vp, i32, i32, i32, i64, vp, i32, vp, i64, vp, vp, vp, vp]
+            L.coli_fp8_columns_ld.argtypes = [i32, i32, P(i64)]
+            L.coli_dequantize_fp8.argtypes = [vp, vp, i64, i64, i32, vp, i32, i64, vp]
+            L.coli_fp8_blob_layout.argtypes = [P(Shape), P(sz), P(sz)]
+            L.coli_fp8_matmul.argtypes = [vp, vp, i32, i32, vp, i32, vp, sz, sz, i32, vp, i32, i64, vp]
+            L.coli_fp8_swiglu.argtypes = [vp, vp, i32, i32, vp, i32, vp, sz, sz, sz, sz, i32, vp, vp, i32,
+                                          i64, vp]
+            L.coli_fp8_wgrad.argtypes = [vp, vp, vp, vp, i64, i32, vp, i32, i32, i32, i32, vp, i32, i64, vp]
+            L.coli_debug_fp8_kernel.argtypes = [i32, i32, i32, i32, i32, i32, P(i32)]
+            L.coli_moe_dispatch_fp8.argtypes = [vp, i32, i32, i32, i32, i64, vp, vp, vp, vp]
             _lib = L
     return _lib
 
@@ -760,6 +782,18 @@ def dispatch_mxfp4(x, inv, q=None, s=None, stream=None):
     return q, s
 
 
+def dispatch_fp8(x, inv, q=None, s=None, stream=None):
+    """dispatch with the rows quantised on the way: (codes, scales) of T*k FP8 rows (those of no
+    slot as there)."""
+    T, k = _slots(inv)
+    code, ld = _rows(x, "x", T)
+    H = x.shape[1]
+    q, s = _fp8_out(q, s, T * k, H, x, "dispatch_fp8", stream)
+    _enqueue((x, inv, q, s), stream, "coli_moe_dispatch_fp8", x.data_ptr(), code, T, k, H, ld,
+             inv.data_ptr(), q.data_ptr(), s.data_ptr())
+    return q, s
+
+
 def dispatch_bwd(grad, inv, dtype=None, out=None, stream=None):
     """dispatch's gradient: out[t] = sum_j grad[inv[t, j]], in `dtype` (default grad's)."""
     T, k = _slots(inv)
@@ -806,6 +840,348 @@ def combine_bwd(grad, rows, inv, w, scale=1.0, rows_grad=None, w_grad=None, stre
              grad.data_ptr(), g_code, ld_g, rows.data_ptr(), r_code, ld_r, T, k, H, inv.data_ptr(),
              w.data_ptr(), scale, rows_grad.data_ptr(), ld_rg, w_grad.data_ptr())
     return rows_grad, w_grad
+
+
+# ---------------------------------------------------------------- routing with groups
+SCORES = {"sigmoid": 0, "softmax": 1}
+
+
+def _score(score) -> int:
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
+    return SCORES[score]
+
+
+def _token_rows(t, name, dtype=None, shape=None):
+    """Type code of a contiguous 2-d device tensor."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be 2-d and contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if max(t.shape) >= 2 ** 31:
+        raise ValueError(f"{name} must have fewer than 2^31 rows and columns")
+    return None if dtype is not None else _dtype_code(t.dtype)
+
+
+def route_groups(logits, bias, k, score="sigmoid", groups=1, groups_kept=None, group_top=2, norm=True,
+                 scale=1.0, with_scores=False, idx=None, w=None, scores=None, stream=None):
+    """The k experts of every token and their weights, (idx int32 [T][k], w float32 [T][k]), for logits
+    [T][E] (float32, bfloat16 or float16) and a selection bias float32 [E] (or None): sigmoid or softmax
+    scores; the `groups_kept` (default all) best of `groups` groups by their largest key or the sum of
+    their `group_top` = 2 largest; weights `scale` times the scores, which `norm` divides by their sum.
+    Slots for which no expert is left have idx -1. with_scores (or scores given): also the scores,
+    float32 [T][E]."""
+    import torch
+    code = _token_rows(logits, "logits")
+    T, E = logits.shape
+    _need(bias, torch.float32, "bias")
+    if bias is not None and bias.numel() != E:
+        raise ValueError(f"bias must have {E} values")
+    if idx is None:
+        idx = _new(logits, (T, k), torch.int32, stream)
+    if w is None:
+        w = _new(logits, (T, k), torch.float32, stream)
+    if scores is None and with_scores:
+        scores = _new(logits, (T, E), torch.float32, stream)
+    _token_rows(idx, "idx", torch.int32, (T, k))
+    _token_rows(w, "w", torch.float32, (T, k))
+    if scores is not None:
+        _token_rows(scores, "scores", torch.float32, (T, E))
+    _enqueue((logits, bias, idx, w, scores), stream, "coli_moe_route_groups", logits.data_ptr(), code,
+             None if bias is None else bias.data_ptr(), T, E, k, _score(score), groups,
+             groups if groups_kept is None else groups_kept, group_top, int(norm), scale, idx.data_ptr(),
+             w.data_ptr(), None if scores is None else scores.data_ptr())
+    return (idx, w) if scores is None else (idx, w, scores)
+
+
+def route_groups_bwd(w_grad, logits, idx, score="sigmoid", norm=True, scale=1.0, scores_grad=None,
+                     dtype=None, out=None, stream=None):
+    """route_groups' gradient to the logits, [T][E] in `dtype` (default the logits'), from that of its
+    weights and (optionally) that of its scores; score, norm and scale as there."""
+    import torch
+    code = _token_rows(logits, "logits")
+    T, E = logits.shape
+    _token_rows(idx, "idx", torch.int32)
+    k = idx.shape[1]
+    _token_rows(idx, "idx", torch.int32, (T, k))
+    _token_rows(w_grad, "w_grad", torch.float32, (T, k))
+    if scores_grad is not None:
+        _token_rows(scores_grad, "scores_grad", torch.float32, (T, E))
+    if out is None:
+        out = _new(logits, (T, E), dtype or logits.dtype, stream)
+    elif dtype is not None and out.dtype != dtype:
+        raise ValueError(f"out must be {dtype}, got {out.dtype}")
+    if tuple(out.shape) != (T, E):
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(T, E)}")
+    out_code = _token_rows(out, "out")
+    _enqueue((w_grad, logits, idx, scores_grad, out), stream, "coli_moe_route_groups_bwd", w_grad.data_ptr(),
+             logits.data_ptr(), code, idx.data_ptr(), T, E, k, _score(score), int(norm), scale,
+             None if scores_grad is None else scores_grad.data_ptr(), out.data_ptr(), out_code)
+    return out
+
+
+# ---------------------------------------------------------------- FP8 experts
+FP8_KERNELS = ("few_rows_2", "few_rows_4", "lines_128", "lines_256")
+
+
+def _blocks(n):
+    return -(-n // 128)
+
+
+def _fp8_rows(q, s, name):
+    """(rows, cols) of FP8 rows: codes uint8 [rows][cols], scales float32 [rows][ceil(cols / 128)]."""
+    import torch
+    _need(q, torch.uint8, f"{name} codes")
+    _need(s, torch.float32, f"{name} scales")
+    if q.dim() != 2 or tuple(s.shape) != (q.shape[0], _blocks(q.shape[1])):
+        raise ValueError(f"{name}: codes {tuple(q.shape)} and scales {tuple(s.shape)} do not match")
+    return tuple(q.shape)
+
+
+def _fp8_out(q, s, rows, cols, like, name, stream):
+    import torch
+    if q is None:
+        q = _new(like, (rows, cols), torch.uint8, stream)
+    if s is None:
+        s = _new(like, (rows, _blocks(cols)), torch.float32, stream)
+    if _fp8_rows(q, s, name) != (rows, cols):
+        raise ValueError(f"{name}: codes must have shape ({rows}, {cols})")
+    return q, s
+
+
+def quantize_fp8(x, q=None, s=None, stream=None):
+    """Rows x [rows][cols] (float32, bfloat16 or float16) -> (codes uint8 [rows][cols], scales float32
+    [rows][ceil(cols / 128)])."""
+    code, ld = _rows(x, "x")
+    rows, cols = x.shape
+    q, s = _fp8_out(q, s, rows, cols, x, "quantize_fp8", stream)
+    _enqueue((x, q, s), stream, "coli_quantize_fp8", x.data_ptr(), code, rows, cols, ld, q.data_ptr(),
+             s.data_ptr())
+    return q, s
+
+
+def _fp8_matrices(q, s, count, rows, cols, like, name, stream):
+    """Outputs [count][rows][cols] and [count][blocks][blocks], each matrix without gaps; their strides in bytes."""
+    import torch
+    shapes = (count, rows, cols), (count, _blocks(rows), _blocks(cols))
+    if q is None:
+        q = _new(like, shapes[0], torch.uint8, stream)
+    if s is None:
+        s = _new(like, shapes[1], torch.float32, stream)
+    for t, shape, dtype, part in ((q, shapes[0], torch.uint8, "codes"), (s, shapes[1], torch.float32, "scales")):
+        if t.dtype != dtype or not t.is_cuda or tuple(t.shape) != shape:
+            raise ValueError(f"{name}: {part} must be a {dtype} device tensor of shape {shape}")
+        if count and not t[0].is_contiguous():
+            raise ValueError(f"{name}: each matrix of the {part} must be contiguous")
+    return q, s, q.stride(0), 4 * s.stride(0)
+
+
+def quantize_fp8_matrix(x, transposed=False, q=None, s=None, qt=None, st=None, stream=None):
+    """Matrices x [rows][cols] or [count][rows][cols] (float32, bfloat16 or float16) by blocks of 128 x 128
+    -> (codes uint8 of x's shape, scales float32 [..][ceil(rows / 128)][ceil(cols / 128)]), with
+    `transposed` (or qt, st given) followed by those of the transposed matrices. Given outputs may be
+    views into experts' buffers: only a matrix itself has to be contiguous."""
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be [rows][cols] or [count][rows][cols]")
+    flat = x.dim() == 2
+    x3, outs = (x[None], [None if t is None else t[None] for t in (q, s, qt, st)]) if flat else (x, [q, s, qt, st])
+    count, rows, cols = x3.shape
+    code, ld = (_dtype_code(x.dtype), cols) if x3.numel() == 0 else _rows(x3[0], "x")
+    if not x.is_cuda:
+        raise ValueError("x must be a device tensor")
+    if count >= 2 ** 31:
+        raise ValueError("fewer than 2^31 matrices are needed")
+    if count > 1 and x3.numel() and x3.stride(0) < (rows - 1) * ld + cols:
+        raise ValueError("x has matrices that overlap")
+    both = transposed or qt is not None or st is not None
+    outs[:2], strides = [], outs[:2]
+    q3, s3, q_stride, s_stride = _fp8_matrices(*strides, count, rows, cols, x, "quantize_fp8_matrix", stream)
+    tensors, t_args = [x, q3, s3], (None, 0, None, 0)
+    if both:
+        qt3, st3, qt_stride, st_stride = _fp8_matrices(*outs, count, cols, rows, x, "quantize_fp8_matrix", stream)
+        tensors += [qt3, st3]
+        t_args = qt3.data_ptr(), qt_stride, st3.data_ptr(), st_stride
+    _enqueue(tensors, stream, "coli_quantize_fp8_matrix", x.data_ptr(), code, count, rows, cols, ld, x3.stride(0),
+             q3.data_ptr(), q_stride, s3.data_ptr(), s_stride, *t_args)
+    return tuple(t[0] if flat else t for t in tensors[1:])
+
+
+def fp8_columns_ld(rows: int, E: int) -> int:
+    """The columns (128 for each 128 rows of an expert) that quantize_fp8_columns' codes need."""
+    out = ctypes.c_int64()
+    _check(lib().coli_fp8_columns_ld(rows, E, ctypes.byref(out)))
+    return out.value
+
+
+def quantize_fp8_columns(x, offsets=None, rows=False, qt=None, st=None, q=None, s=None, stream=None):
+    """Rows x [rows][cols] sorted by expert -> (codes uint8 [cols][P], scale exponents uint8 [P / 128][cols])
+    over 128 of an expert's rows by one column, for fp8_wgrad; P is fp8_columns_ld's (or that of a given
+    qt). `rows` (or q, s given): also quantize_fp8's codes and scales, from the same pass."""
+    import torch
+    code, ld = _rows(x, "x")
+    n, cols = x.shape
+    _need(offsets, torch.int32, "offsets")
+    E = 1 if offsets is None else offsets.numel() - 1
+    if max(n, cols, E) >= 2 ** 31 or E < 1:
+        raise ValueError(f"rows {n}, columns {cols} and experts {E} must be below 2^31, experts at least 1")
+    P = fp8_columns_ld(n, E) if qt is None else qt.shape[-1]
+    if qt is None:
+        qt = _new(x, (cols, P), torch.uint8, stream)
+    if st is None:
+        st = _new(x, (P // 128, cols), torch.uint8, stream)
+    _fp8_columns(qt, st, "quantize_fp8_columns", cols)
+    if rows or q is not None or s is not None:
+        q, s = _fp8_out(q, s, n, cols, x, "quantize_fp8_columns", stream)
+    _enqueue((x, offsets, qt, st, q, s), stream, "coli_quantize_fp8_columns", x.data_ptr(), code, n, cols, ld,
+             None if offsets is None else offsets.data_ptr(), E, qt.data_ptr(), P, st.data_ptr(),
+             None if q is None else q.data_ptr(), None if s is None else s.data_ptr())
+    return (qt, st) if q is None else (qt, st, q, s)
+
+
+def _rows_of_ld(P, E):
+    """The most rows over E experts whose columns fit P."""
+    many = P + 127 - 127 * E
+    return many if many >= E else min(P // 128, E)
+
+
+def _fp8_columns(qt, st, name, cols=None):
+    """(cols, P) of columns: codes uint8 [cols][P], scale exponents uint8 [P / 128][cols]."""
+    import torch
+    _need(qt, torch.uint8, f"{name} codes")
+    _need(st, torch.uint8, f"{name} scales")
+    if qt.dim() != 2 or qt.shape[1] % 128 or tuple(st.shape) != (qt.shape[1] // 128, qt.shape[0]) or \
+            cols not in (None, qt.shape[0]):
+        raise ValueError(f"{name}: codes {tuple(qt.shape)} and scales {tuple(st.shape)} do not match")
+    return tuple(qt.shape)
+
+
+def dequantize_fp8(q, s, dtype=None, out=None, stream=None):
+    """The values of FP8 rows, or of matrices ([..][rows][cols] with a scale for each 128 x 128 block), in
+    `out`'s type, else `dtype` (default float32)."""
+    import torch
+    shape = tuple(q.shape)
+    if q.dim() not in (2, 3) or s.dim() != q.dim():
+        raise ValueError("codes must be [rows][cols] or [count][rows][cols], and scales have as many dimensions")
+    for t, kind, name in ((q, torch.uint8, "codes"), (s, torch.float32, "scales")):
+        _need(t if q.dim() == 2 or not len(t) else t[0], kind, name)
+    rows, cols = shape[-2:]
+    per_row, per_block = (*shape[:-1], _blocks(cols)), (*shape[:-2], _blocks(rows), _blocks(cols))
+    if tuple(s.shape) not in (per_row, per_block):
+        raise ValueError(f"codes {shape} and scales {tuple(s.shape)} do not match")
+    block_rows = 1 if tuple(s.shape) == per_row else 128
+    if out is None:
+        out = _new(q, shape, dtype or torch.float32, stream)
+    if tuple(out.shape) != shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {shape}")
+    if q.dim() == 2:
+        parts = [(q, s, out)]
+    elif all(t.is_contiguous() for t in (q, s, out)) and (block_rows == 1 or rows % 128 == 0):   # one long matrix
+        parts = [(q.view(-1, cols), s.view(-1, s.shape[-1]), out.view(-1, cols))]
+    else:
+        parts = zip(q, s, out)
+    for pq, ps, po in parts:
+        code, ld = _rows(po, "out", pq.shape[0], cols, dtype)
+        _enqueue((pq, ps, po), stream, "coli_dequantize_fp8", pq.data_ptr(), ps.data_ptr(), pq.shape[0], cols,
+                 block_rows, po.data_ptr(), code, ld)
+    return out
+
+
+def fp8_blob_layout(shape: MoEShape):
+    """(offsets of the gate, up and down codes, then of their scales; blob bytes)."""
+    off = (ctypes.c_size_t * 6)()
+    nb = ctypes.c_size_t()
+    _check(lib().coli_fp8_blob_layout(ctypes.byref(shape.c()), off, ctypes.byref(nb)))
+    return list(off), nb.value
+
+
+def fp8_matmul(a, a_s, table, n, q_off=0, s_off=0, offsets=None, dtype=None, out=None, stream=None):
+    """out[r] = W_e(r) a[r] for FP8 rows (a, a_s) sorted by expert. table: device array (int64) of pointers
+    to the experts' buffers, each with an FP8 [n][K] matrix: codes at q_off, scales at s_off. offsets [E + 1]
+    as union gives it (None: one matrix for every row). out in `dtype` (default float32); its rows outside
+    the offsets are left as they are (undefined in a new one). With the transposed matrices of
+    quantize_fp8_matrix it is the product's gradient to its rows."""
+    import torch
+    rows, K = _fp8_rows(a, a_s, "a")
+    E, off = _groups(table, offsets, rows, K, n, q_off, s_off)
+    if out is None:
+        out = _new(a, (rows, n), dtype or torch.float32, stream)
+    code, ld = _rows(out, "out", rows, n, dtype)
+    _enqueue((a, a_s, table, offsets, out), stream, "coli_fp8_matmul", a.data_ptr(), a_s.data_ptr(), rows, K,
+             off, E, table.data_ptr(), q_off, s_off, n, out.data_ptr(), code, ld)
+    return out
+
+
+def fp8_swiglu(a, a_s, table, inter, q_off=0, s_off=0, up_q_off=None, up_s_off=None, offsets=None, dtype=None,
+               out=None, stream=None):
+    """h[r] = silu(G_e(r) a[r]) * (U_e(r) a[r]), arguments as fp8_matmul: the gate matrix [inter][K] at q_off
+    and s_off, the up matrix at up_q_off and up_s_off (default: right behind gate's codes and scales).
+    dtype "fp8" (or out a (codes, scales) pair): h as FP8 rows, returned as that pair."""
+    import torch
+    rows, K = _fp8_rows(a, a_s, "a")
+    E, off = _groups(table, offsets, rows, K, inter, q_off, s_off)
+    if up_q_off is None:
+        up_q_off = q_off + inter * K
+    if up_s_off is None:
+        up_s_off = s_off + 4 * _blocks(inter) * _blocks(K)
+    if up_q_off < 0 or up_s_off < 0:
+        raise ValueError("up_q_off and up_s_off must not be negative")
+    if dtype == "fp8" or isinstance(out, (tuple, list)):
+        if dtype not in (None, "fp8"):
+            raise ValueError(f"out is an FP8 pair, dtype {dtype}")
+        q, s = _fp8_out(*(out or (None, None)), rows, inter, a, "fp8_swiglu", stream)
+        out, h, hs, code, ld = (q, s), q, s.data_ptr(), FP8, inter
+    else:
+        if out is None:
+            out = _new(a, (rows, inter), dtype or torch.float32, stream)
+        code, ld = _rows(out, "out", rows, inter, dtype)
+        h, hs, s = out, None, None
+    _enqueue((a, a_s, table, offsets, h, s), stream, "coli_fp8_swiglu", a.data_ptr(), a_s.data_ptr(), rows, K,
+             off, E, table.data_ptr(), q_off, s_off, up_q_off, up_s_off, inter, h.data_ptr(), hs, code, ld)
+    return out
+
+
+def fp8_wgrad(gt, gt_s, xt, xt_s, offsets=None, rows=None, dtype=None, out=None, accumulate=False, stream=None):
+    """fp8_matmul's gradient to its matrices, out[e] = sum over the expert's rows of grad[r] x[r]^T, [E][n][K]
+    in `dtype` (default float32), from quantize_fp8_columns of the output's gradient and of the rows, with
+    the same offsets. rows (needed only without offsets, for columns with room for more): how many rows
+    those had. accumulate: added to what `out` holds."""
+    import torch
+    n, P = _fp8_columns(gt, gt_s, "gt")
+    K, Px = _fp8_columns(xt, xt_s, "xt")
+    if P != Px:
+        raise ValueError(f"gt has {P} columns, xt {Px}")
+    _need(offsets, torch.int32, "offsets")
+    E = 1 if offsets is None else offsets.numel() - 1
+    if E < 1:
+        raise ValueError("offsets must hold at least two values")
+    if rows is None:
+        rows = _rows_of_ld(P, E)
+    if max(n, K, rows, E) >= 2 ** 31 or rows < 0:
+        raise ValueError("rows, columns and experts must be below 2^31")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = _new(gt, (E, n, K), dtype or torch.float32, stream)
+    if out.dim() != 3 or tuple(out.shape) != (E, n, K) or not out.is_cuda:
+        raise ValueError(f"out must be a device tensor of shape {(E, n, K)}")
+    if E > 1 and n and out.stride(0) != n * out.stride(1):
+        raise ValueError("out's matrices must follow each other without gaps")
+    code, ld = _rows(out.view(E * n, K) if out.is_contiguous() else out[0], "out", n, K, dtype)
+    _enqueue((gt, gt_s, xt, xt_s, offsets, out), stream, "coli_fp8_wgrad", gt.data_ptr(), gt_s.data_ptr(),
+             xt.data_ptr(), xt_s.data_ptr(), P, rows, None if offsets is None else offsets.data_ptr(), E, n, K,
+             int(accumulate), out.data_ptr(), code, ld)
+    return out
+
+
+def debug_fp8_kernel(rows: int, K: int, E: int, N: int, grouped=True, swiglu=False) -> str:
+    """coli_debug_fp8_kernel: the kernel that a product of these sizes runs."""
+    out = ctypes.c_int32()
+    _check(lib().coli_debug_fp8_kernel(rows, K, E, N, int(grouped), int(swiglu), ctypes.byref(out)))
+    return FP8_KERNELS[out.value]
 
 
 class ExpertCache:

@@ -15,7 +15,8 @@ ARCH = "gfx950"
 
 SOURCES = ["abi.hip", "layer.hip", "quant.hip", "route.hip", "union.hip", "gemv.hip", "gemm.hip",
            "cache.hip", "profile.hip", "gemv_gateup.hip", "gemv_down.hip", "probe.hip",
-           "mxfp4_quant.hip", "mxfp4_gemm.hip", "permute.hip"]
+           "mxfp4_quant.hip", "mxfp4_gemm.hip", "permute.hip", "fp8_quant.hip",
+           "fp8_gemm.hip", "fp8_wgrad.hip", "route_groups.hip"]
 
 FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-fPIC", "-std=c++17", "-Wall", "-Wno-unused-function",

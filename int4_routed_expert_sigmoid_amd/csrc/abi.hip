@@ -9,10 +9,12 @@
 #include <string>
 
 #include "common.h"
+#include "fp8.h"
 #include "gemm.h"
 #include "layer.h"
 #include "mxfp4.h"
 #include "quant.h"
+#include "route_groups.h"
 
 namespace coli {
 
@@ -247,6 +249,59 @@ coli_status coli_moe_route_topp(const float* d_logits, const float* d_bias, int3
                                 int32_t k, float topp, int32_t* d_idx, float* d_w, void* stream) {
     COLI_GUARD_BEGIN
     return route_call(d_logits, d_bias, T, E, k, topp, d_idx, d_w, stream);
+    COLI_GUARD_END
+}
+
+// ------------------------------------------------------- routing with groups
+static coli_status check_route_groups(const std::string& w, int32_t dtype, int32_t T, int32_t E, int32_t k,
+                                      int32_t score, float scale) {
+    if (T < 0 || E <= 0 || k <= 0 || k > E) return fail(COLI_EINVAL, w + ": need T >= 0 and 1 <= k <= E");
+    if (E > 1024 || k > 32) return fail(COLI_EUNSUPPORTED, w + ": E <= 1024 and k <= 32");
+    if (!elem_dtype(dtype)) return fail(COLI_EUNSUPPORTED, w + ": dtype must be f32, bf16 or f16");
+    if (score != COLI_SCORE_SIGMOID && score != COLI_SCORE_SOFTMAX)
+        return fail(COLI_EINVAL, w + ": score must be sigmoid or softmax");
+    if (!std::isfinite(scale)) return fail(COLI_EINVAL, w + ": scale must be finite");
+    if (T >= (1 << 26)) return fail(COLI_EUNSUPPORTED, w + ": T must be below 2^26");
+    return COLI_OK;
+}
+
+coli_status coli_moe_route_groups(const void* d_logits, int32_t dtype, const float* d_bias, int32_t T, int32_t E,
+                                  int32_t k, int32_t score, int32_t n_groups, int32_t groups_kept,
+                                  int32_t group_top, int32_t norm, float scale, int32_t* d_idx, float* d_w,
+                                  float* d_scores, void* stream) {
+    COLI_GUARD_BEGIN
+    coli_status st = check_route_groups("route_groups", dtype, T, E, k, score, scale);
+    if (st) return st;
+    if (n_groups < 1 || E % n_groups) return fail(COLI_EINVAL, "route_groups: n_groups must divide E");
+    if (n_groups > 64) return fail(COLI_EUNSUPPORTED, "route_groups: n_groups <= 64");
+    if (groups_kept < 1 || groups_kept > n_groups || k > groups_kept * (E / n_groups))
+        return fail(COLI_EINVAL, "route_groups: the groups kept must be at most n_groups and hold k experts");
+    if (group_top != 1 && group_top != 2) return fail(COLI_EINVAL, "route_groups: group_top must be 1 or 2");
+    if (T == 0) return COLI_OK;
+    if (!d_logits || !d_idx || !d_w) return fail(COLI_EINVAL, "route_groups: NULL pointer");
+    RouteArgs a;
+    a.logits = d_logits; a.bias = d_bias; a.T = T; a.E = E; a.k = k;
+    a.softmax = score == COLI_SCORE_SOFTMAX; a.norm = norm != 0;
+    a.groups = n_groups; a.kept = groups_kept; a.group_top = group_top; a.scale = scale;
+    a.idx = d_idx; a.w = d_w; a.scores = d_scores;
+    return launch_route_groups(a, dtype, (hipStream_t)stream);
+    COLI_GUARD_END
+}
+
+coli_status coli_moe_route_groups_bwd(const float* d_dw, const void* d_logits, int32_t dtype, const int32_t* d_idx,
+                                      int32_t T, int32_t E, int32_t k, int32_t score, int32_t norm, float scale,
+                                      const float* d_dscores, void* d_dlogits, int32_t grad_dtype, void* stream) {
+    COLI_GUARD_BEGIN
+    coli_status st = check_route_groups("route_groups_bwd", dtype, T, E, k, score, scale);
+    if (st) return st;
+    if (!elem_dtype(grad_dtype)) return fail(COLI_EUNSUPPORTED, "route_groups_bwd: grad_dtype must be f32, bf16 or f16");
+    if (T == 0) return COLI_OK;
+    if (!d_dw || !d_logits || !d_idx || !d_dlogits) return fail(COLI_EINVAL, "route_groups_bwd: NULL pointer");
+    RouteBwdArgs a;
+    a.dw = d_dw; a.logits = d_logits; a.idx = d_idx; a.T = T; a.E = E; a.k = k;
+    a.softmax = score == COLI_SCORE_SOFTMAX; a.norm = norm != 0; a.scale = scale;
+    a.dscores = d_dscores; a.dlogits = d_dlogits;
+    return launch_route_groups_bwd(a, dtype, grad_dtype, (hipStream_t)stream);
     COLI_GUARD_END
 }
 
@@ -553,6 +608,234 @@ coli_status coli_debug_mxfp4_kernel(int32_t rows, int32_t K, int32_t E, int32_t 
     COLI_GUARD_END
 }
 
+// -------------------------------------------------------------- FP8 experts
+static bool aligned4(const void* p) { return ((uintptr_t)p & 3) == 0; }
+
+static coli_status check_fp8_rows(const std::string& w, int64_t rows, int64_t cols, int32_t dtype, int64_t ld) {
+    if (rows < 0 || cols <= 0 || cols % kFp8Unit)
+        return fail(COLI_EINVAL, w + ": rows >= 0, cols a positive multiple of 16");
+    if (cols >= (1 << 30)) return fail(COLI_EUNSUPPORTED, w + ": cols must be below 2^30");
+    if (!elem_dtype(dtype)) return fail(COLI_EUNSUPPORTED, w + ": dtype must be f32, bf16 or f16");
+    if (ld < cols) return fail(COLI_EINVAL, w + ": ld below cols");
+    if (rows > 0 && ld > (int64_t(1) << 56) / rows) return fail(COLI_EUNSUPPORTED, w + ": too large");
+    return COLI_OK;
+}
+
+static coli_status check_fp8_pair(const std::string& w, const void* q, const void* s) {
+    if (!q || !s) return fail(COLI_EINVAL, w + ": NULL pointer");
+    if (!aligned16(q)) return fail(COLI_EINVAL, w + ": codes must be 16-byte aligned");
+    if (!aligned4(s)) return fail(COLI_EINVAL, w + ": scales must be 4-byte aligned");
+    return COLI_OK;
+}
+
+coli_status coli_quantize_fp8(const void* d_x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, uint8_t* d_q,
+                              float* d_s, void* stream) {
+    COLI_GUARD_BEGIN
+    coli_status st = check_fp8_rows("quantize_fp8", rows, cols, dtype, ld);
+    if (st || rows == 0) return st;
+    if (!d_x) return fail(COLI_EINVAL, "quantize_fp8: NULL pointer");
+    if ((st = check_fp8_pair("quantize_fp8", d_q, d_s))) return st;
+    return launch_quantize_fp8(d_x, dtype, rows, cols, ld, d_q, d_s, (hipStream_t)stream);
+    COLI_GUARD_END
+}
+
+coli_status coli_quantize_fp8_matrix(const void* d_x, int32_t dtype, int32_t count, int64_t rows, int64_t cols,
+                                     int64_t ld, int64_t x_stride, uint8_t* d_q, int64_t q_stride, float* d_s,
+                                     int64_t s_stride, uint8_t* d_qt, int64_t qt_stride, float* d_st,
+                                     int64_t st_stride, void* stream) {
+    COLI_GUARD_BEGIN
+    const char* w = "quantize_fp8_matrix";
+    coli_status st = check_fp8_rows(w, rows, cols, dtype, ld);
+    if (st) return st;
+    if (rows >= (1 << 30)) return fail(COLI_EUNSUPPORTED, "quantize_fp8_matrix: rows must be below 2^30");
+    if (count < 0) return fail(COLI_EINVAL, "quantize_fp8_matrix: count below 0");
+    const bool plain = d_q || d_s, transposed = d_qt || d_st;
+    if (!plain && !transposed) return fail(COLI_EINVAL, "quantize_fp8_matrix: no output");
+    if (transposed && rows % kFp8Unit)
+        return fail(COLI_EINVAL, "quantize_fp8_matrix: rows must be a multiple of 16 for the transposed form");
+    const int64_t n = rows * cols, ns = 4 * fp8_blocks(rows) * fp8_blocks(cols), far = (int64_t(1) << 60) / std::max(1, count);
+    if (count > 1 && rows > 0) {
+        if (x_stride < (rows - 1) * ld + cols || (plain && (q_stride < n || s_stride < ns)) ||
+            (transposed && (qt_stride < n || st_stride < ns)))
+            return fail(COLI_EINVAL, "quantize_fp8_matrix: matrices overlap");
+        if ((plain && (q_stride % 16 || s_stride % 4)) || (transposed && (qt_stride % 16 || st_stride % 4)))
+            return fail(COLI_EINVAL, "quantize_fp8_matrix: codes must be multiples of 16 bytes apart, scales of 4");
+        if (x_stride > far || (plain && (q_stride > far || s_stride > far)) || (transposed && (qt_stride > far || st_stride > far)))
+            return fail(COLI_EUNSUPPORTED, "quantize_fp8_matrix: too large");
+    }
+    if (count == 0 || rows == 0) return COLI_OK;
+    if (!d_x) return fail(COLI_EINVAL, "quantize_fp8_matrix: NULL pointer");
+    if (plain && (st = check_fp8_pair(w, d_q, d_s))) return st;
+    if (transposed && (st = check_fp8_pair(w, d_qt, d_st))) return st;
+    Fp8MatrixArgs a;
+    a.x = d_x; a.x_stride = x_stride; a.ld = ld;
+    a.q = d_q; a.s = d_s; a.qt = d_qt; a.st = d_st;
+    a.q_stride = q_stride; a.s_stride = s_stride; a.qt_stride = qt_stride; a.st_stride = st_stride;
+    a.rows = (int32_t)rows; a.cols = (int32_t)cols;
+    return launch_quantize_fp8_matrix(a, dtype, count, (hipStream_t)stream);
+    COLI_GUARD_END
+}
+
+static int64_t fp8_columns_ld(int64_t rows, int64_t E) {
+    return (rows + (kFp8Block - 1) * std::min(E, rows)) / kFp8Block * kFp8Block;
+}
+
+coli_status coli_fp8_columns_ld(int32_t rows, int32_t E, int64_t* ld_t) {
+    COLI_GUARD_BEGIN
+    if (rows < 0 || E < 1 || !ld_t) return fail(COLI_EINVAL, "fp8_columns_ld: rows >= 0, E at least 1");
+    *ld_t = fp8_columns_ld(rows, E);
+    return COLI_OK;
+    COLI_GUARD_END
+}
+
+static coli_status check_fp8_columns(const std::string& w, int32_t rows, const int32_t* d_offsets, int32_t E, int64_t ld_t) {
+    if (rows < 0 || E < 1) return fail(COLI_EINVAL, w + ": rows >= 0, E at least 1");
+    if (E > 1024) return fail(COLI_EUNSUPPORTED, w + ": E must be at most 1024");
+    if (!d_offsets && E != 1) return fail(COLI_EINVAL, w + ": without offsets E must be 1");
+    if (ld_t % kFp8Block || ld_t < fp8_columns_ld(rows, E))
+        return fail(COLI_EINVAL, w + ": ld_t must be a multiple of 128 and at least coli_fp8_columns_ld's");
+    if (ld_t > INT32_MAX) return fail(COLI_EUNSUPPORTED, w + ": ld_t must be below 2^31");
+    return COLI_OK;
+}
+
+coli_status coli_quantize_fp8_columns(const void* d_x, int32_t dtype, int32_t rows, int32_t cols, int64_t ld,
+                                      const int32_t* d_offsets, int32_t E, uint8_t* d_qt, int64_t ld_t,
+                                      uint8_t* d_st, uint8_t* d_q, float* d_s, void* stream) {
+    COLI_GUARD_BEGIN
+    const char* w = "quantize_fp8_columns";
+    coli_status st = check_fp8_rows(w, rows, cols, dtype, ld);
+    if (st || (st = check_fp8_columns(w, rows, d_offsets, E, ld_t)) || rows == 0) return st;
+    if (!d_x || !d_qt || !d_st) return fail(COLI_EINVAL, "quantize_fp8_columns: NULL pointer");
+    if (!aligned16(d_qt)) return fail(COLI_EINVAL, "quantize_fp8_columns: codes must be 16-byte aligned");
+    if ((d_q || d_s) && (st = check_fp8_pair(w, d_q, d_s))) return st;
+    Fp8ColumnArgs a;
+    a.x = d_x; a.ld = ld; a.ld_t = ld_t; a.offsets = d_offsets;
+    a.qt = d_qt; a.st = d_st; a.q = d_q; a.s = d_s;
+    a.rows = rows; a.cols = cols; a.E = E;
+    return launch_quantize_fp8_columns(a, dtype, (hipStream_t)stream);
+    COLI_GUARD_END
+}
+
+coli_status coli_dequantize_fp8(const uint8_t* d_q, const float* d_s, int64_t rows, int64_t cols, int32_t block_rows,
+                                void* d_x, int32_t dtype, int64_t ld, void* stream) {
+    COLI_GUARD_BEGIN
+    coli_status st = check_fp8_rows("dequantize_fp8", rows, cols, dtype, ld);
+    if (st) return st;
+    if (block_rows != 1 && block_rows != kFp8Block) return fail(COLI_EINVAL, "dequantize_fp8: block_rows must be 1 or 128");
+    if (rows == 0) return COLI_OK;
+    if (!d_x) return fail(COLI_EINVAL, "dequantize_fp8: NULL pointer");
+    if ((st = check_fp8_pair("dequantize_fp8", d_q, d_s))) return st;
+    return launch_dequantize_fp8(d_q, d_s, rows, cols, block_rows, d_x, dtype, ld, (hipStream_t)stream);
+    COLI_GUARD_END
+}
+
+coli_status coli_fp8_blob_layout(const coli_moe_shape* shape, size_t off[6], size_t* blob_bytes) {
+    COLI_GUARD_BEGIN
+    coli_status st = check_mx_shape(shape);
+    if (st) return st;
+    if (!off || !blob_bytes) return fail(COLI_EINVAL, "off or blob_bytes is NULL");
+    const size_t H = shape->hidden, I = shape->inter, n = 4 * (size_t)(fp8_blocks(H) * fp8_blocks(I));
+    size_t o = 0;
+    for (int i = 0; i < 6; ++i) {
+        off[i] = o;
+        o = align256(o + (i < 3 ? H * I : n));
+    }
+    *blob_bytes = o;
+    return COLI_OK;
+    COLI_GUARD_END
+}
+
+static coli_status check_fp8_product(const std::string& w, int32_t rows, int32_t K, int32_t E, int64_t N, bool grouped) {
+    if (rows < 0 || K <= 0 || K % kFp8Unit) return fail(COLI_EINVAL, w + ": rows >= 0, K a positive multiple of 16");
+    if (N <= 0) return fail(COLI_EINVAL, w + ": the matrix must have rows");
+    if (K > (1 << 22)) return fail(COLI_EUNSUPPORTED, w + ": K must be at most 2^22");
+    if (N > INT32_MAX / 2 - 4096) return fail(COLI_EUNSUPPORTED, w + ": matrix too large");
+    if (E < 1) return fail(COLI_EINVAL, w + ": E must be at least 1");
+    if (E > 1024) return fail(COLI_EUNSUPPORTED, w + ": E must be at most 1024");
+    if (!grouped && E != 1) return fail(COLI_EINVAL, w + ": without offsets E must be 1");
+    return COLI_OK;
+}
+
+static coli_status fp8_product(const char* what, Fp8GemmArgs& a, bool swiglu, int32_t dtype, void* stream) {
+    const std::string w(what);
+    coli_status st = check_fp8_product(w, a.rows, a.K, a.E, a.N, a.offsets != nullptr);
+    if (st) return st;
+    const bool fp8 = swiglu && dtype == COLI_FP8;
+    if (!fp8 && !elem_dtype(dtype)) return fail(COLI_EUNSUPPORTED, w + ": output type not supported");
+    if (fp8 && a.N % kFp8Unit) return fail(COLI_EINVAL, w + ": inter must be a multiple of 16 for FP8 rows");
+    if (!fp8 && a.ld < a.N) return fail(COLI_EINVAL, w + ": ld below the output's columns");
+    if (!fp8 && a.ld > (int64_t(1) << 56) / std::max(1, a.rows)) return fail(COLI_EUNSUPPORTED, w + ": ld too large");
+    if (a.q_off % 16 || a.up_q % 16) return fail(COLI_EINVAL, w + ": q_off must be a multiple of 16");
+    if (a.s_off % 4 || a.up_s % 4) return fail(COLI_EINVAL, w + ": s_off must be a multiple of 4");
+    if (a.rows == 0) return COLI_OK;
+    if (!a.table || !a.y) return fail(COLI_EINVAL, w + ": NULL pointer");
+    if ((st = check_fp8_pair(w, a.a, a.as))) return st;
+    if (fp8 && (st = check_fp8_pair(w, a.y, a.ys))) return st;
+    return launch_fp8_gemm(a, swiglu, dtype, (hipStream_t)stream);
+}
+
+coli_status coli_fp8_matmul(const uint8_t* d_a, const float* d_as, int32_t rows, int32_t K, const int32_t* d_offsets,
+                            int32_t E, const void* const* d_blob_table, size_t q_off, size_t s_off, int32_t N,
+                            void* d_y, int32_t dtype, int64_t ld, void* stream) {
+    COLI_GUARD_BEGIN
+    Fp8GemmArgs a = {};
+    a.offsets = d_offsets; a.table = d_blob_table; a.rows = rows; a.E = E;
+    a.a = d_a; a.as = d_as; a.q_off = q_off; a.s_off = s_off;
+    a.y = d_y; a.ld = ld; a.K = K; a.N = N;
+    return fp8_product("fp8_matmul", a, false, dtype, stream);
+    COLI_GUARD_END
+}
+
+coli_status coli_fp8_swiglu(const uint8_t* d_a, const float* d_as, int32_t rows, int32_t K, const int32_t* d_offsets,
+                            int32_t E, const void* const* d_blob_table, size_t q_off, size_t s_off, size_t up_q_off,
+                            size_t up_s_off, int32_t inter, void* d_h, float* d_hs, int32_t dtype, int64_t ld,
+                            void* stream) {
+    COLI_GUARD_BEGIN
+    Fp8GemmArgs a = {};
+    a.offsets = d_offsets; a.table = d_blob_table; a.rows = rows; a.E = E;
+    a.a = d_a; a.as = d_as; a.q_off = q_off; a.s_off = s_off; a.up_q = up_q_off; a.up_s = up_s_off;
+    a.y = d_h; a.ys = d_hs; a.ld = ld; a.K = K; a.N = inter;
+    return fp8_product("fp8_swiglu", a, true, dtype, stream);
+    COLI_GUARD_END
+}
+
+coli_status coli_fp8_wgrad(const uint8_t* d_gt, const uint8_t* d_gs, const uint8_t* d_xt, const uint8_t* d_xs,
+                           int64_t ld_t, int32_t rows, const int32_t* d_offsets, int32_t E, int32_t N, int32_t K,
+                           int32_t accumulate, void* d_dw, int32_t dtype, int64_t ld, void* stream) {
+    COLI_GUARD_BEGIN
+    coli_status st = check_fp8_columns("fp8_wgrad", rows, d_offsets, E, ld_t);
+    if (st) return st;
+    if (N <= 0 || K <= 0 || N % kFp8Unit || K % kFp8Unit)
+        return fail(COLI_EINVAL, "fp8_wgrad: N and K must be positive multiples of 16");
+    if (N >= (1 << 30) || K >= (1 << 30)) return fail(COLI_EUNSUPPORTED, "fp8_wgrad: N and K must be below 2^30");
+    if (!elem_dtype(dtype)) return fail(COLI_EUNSUPPORTED, "fp8_wgrad: dtype must be f32, bf16 or f16");
+    if (ld < K) return fail(COLI_EINVAL, "fp8_wgrad: ld below K");
+    if (ld > (int64_t(1) << 56) / N / E) return fail(COLI_EUNSUPPORTED, "fp8_wgrad: ld too large");
+    if (!d_dw || (rows > 0 && (!d_gt || !d_gs || !d_xt || !d_xs))) return fail(COLI_EINVAL, "fp8_wgrad: NULL pointer");
+    if (!aligned16(d_gt) || !aligned16(d_xt)) return fail(COLI_EINVAL, "fp8_wgrad: codes must be 16-byte aligned");
+    if (rows == 0 && accumulate) return COLI_OK;
+    Fp8WgradArgs a;
+    a.g = d_gt; a.gs = d_gs; a.x = d_xt; a.xs = d_xs; a.offsets = d_offsets; a.dw = d_dw;
+    a.ld_t = ld_t; a.ld = ld; a.rows = rows; a.E = E; a.N = N; a.K = K; a.accumulate = accumulate != 0;
+    return launch_fp8_wgrad(a, dtype, (hipStream_t)stream);
+    COLI_GUARD_END
+}
+
+coli_status coli_debug_fp8_kernel(int32_t rows, int32_t K, int32_t E, int32_t N, int32_t grouped, int32_t swiglu,
+                                  int32_t* kernel) {
+    COLI_GUARD_BEGIN
+    coli_status st = check_fp8_product("debug_fp8_kernel", rows, K, E, N, grouped != 0);
+    if (st) return st;
+    if (rows == 0 || !kernel) return fail(COLI_EINVAL, "debug_fp8_kernel: no rows, or NULL");
+    static const int32_t some = 0;
+    Fp8GemmArgs a = {};
+    a.rows = rows; a.K = K; a.E = E; a.N = N;
+    a.offsets = grouped ? &some : nullptr;      // asked for, not read
+    *kernel = choose_fp8_kernel(a, swiglu != 0);
+    return COLI_OK;
+    COLI_GUARD_END
+}
+
 // ------------------------------------------------------- token permutation
 coli_status coli_moe_union_inverse(const int32_t* d_idx, int32_t T, int32_t k, int32_t E, int32_t* d_counts,
                                    int32_t* d_offsets, int32_t* d_perm, int32_t* d_unique,
@@ -605,6 +888,19 @@ coli_status coli_moe_dispatch_mxfp4(const void* d_x, int32_t dtype, int32_t T, i
     if (!d_x || !d_inv || !d_q || !d_s) return fail(COLI_EINVAL, "dispatch_mxfp4: NULL pointer");
     if (!aligned16(d_q)) return fail(COLI_EINVAL, "dispatch_mxfp4: codes must be 16-byte aligned");
     return launch_dispatch_mxfp4(d_x, dtype, T, k, H, ld_x, d_inv, d_q, d_s, (hipStream_t)stream);
+    COLI_GUARD_END
+}
+
+coli_status coli_moe_dispatch_fp8(const void* d_x, int32_t dtype, int32_t T, int32_t k, int32_t H, int64_t ld_x,
+                                  const int32_t* d_inv, uint8_t* d_q, float* d_s, void* stream) {
+    COLI_GUARD_BEGIN
+    coli_status st = check_permute("dispatch_fp8", T, k, H, dtype, dtype, {ld_x});
+    if (st) return st;
+    if (H % kFp8Unit) return fail(COLI_EINVAL, "dispatch_fp8: H must be a multiple of 16");
+    if (T == 0) return COLI_OK;
+    if (!d_x || !d_inv) return fail(COLI_EINVAL, "dispatch_fp8: NULL pointer");
+    if ((st = check_fp8_pair("dispatch_fp8", d_q, d_s))) return st;
+    return launch_dispatch_fp8(d_x, dtype, T, k, H, ld_x, d_inv, d_q, d_s, (hipStream_t)stream);
     COLI_GUARD_END
 }
 

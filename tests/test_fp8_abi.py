@@ -1,0 +1,170 @@
+"""The FP8 and routing calls refuse bad arguments before anything is enqueued, and the reference forms
+that the GPU tests use are pinned (no device needed)."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import int4_routed_expert_sigmoid_amd as coli
+from tests import fp8_refs as ref
+
+EINVAL, EUNSUP, OK = coli.COLI_EINVAL, coli.COLI_EUNSUPPORTED, coli.COLI_OK
+
+
+@pytest.fixture(scope="module")
+def L():
+    return coli.lib()
+
+
+def test_route_refusals(L):
+    def fwd(l=16, dt=0, T=2, E=8, k=2, score=0, groups=2, kept=1, top=2, norm=1, scale=1.0, idx=16, w=16):
+        return L.coli_moe_route_groups(l, dt, None, T, E, k, score, groups, kept, top, norm, scale, idx, w, None, None)
+
+    def bwd(l=16, dt=0, T=2, E=8, k=2, score=0, scale=1.0, idx=16, w=16, dl=16, gdt=0):
+        return L.coli_moe_route_groups_bwd(w, l, dt, idx, T, E, k, score, 1, scale, None, dl, gdt, None)
+
+    for f in (fwd, bwd):
+        assert f(T=-1) == EINVAL and f(E=0) == EINVAL and f(k=0) == EINVAL and f(k=9) == EINVAL
+        assert f(E=1025) == EUNSUP and f(E=64, k=33) == EUNSUP and f(T=1 << 26) == EUNSUP
+        assert f(dt=3) == EUNSUP and f(dt=-1) == EUNSUP
+        assert f(score=2) == EINVAL and f(scale=float("nan")) == EINVAL and f(scale=float("inf")) == EINVAL
+        assert f(l=None) == EINVAL and f(idx=None) == EINVAL and f(w=None) == EINVAL
+        assert f(T=0, l=None, idx=None, w=None) == OK
+    assert fwd(groups=3) == EINVAL and fwd(groups=0) == EINVAL and fwd(E=130, groups=65, kept=65) == EUNSUP
+    assert fwd(kept=0) == EINVAL and fwd(kept=3) == EINVAL and fwd(k=5) == EINVAL     # one group of 4 experts
+    assert fwd(top=0) == EINVAL and fwd(top=3) == EINVAL
+    assert bwd(dl=None) == EINVAL and bwd(gdt=3) == EUNSUP
+
+
+def test_quantize_refusals(L):
+    def rows(x=16, dt=0, r=4, c=64, ld=64, q=16, s=16):
+        return L.coli_quantize_fp8(x, dt, r, c, ld, q, s, None)
+
+    def back(x=16, dt=0, r=4, c=64, ld=64, q=16, s=16):
+        return L.coli_dequantize_fp8(q, s, r, c, 1, x, dt, ld, None)
+
+    def matrix(x=16, dt=0, r=32, c=64, ld=64, q=16, s=16, n=2, xs=2048, qs=2048, ss=4, qt=None, st=None):
+        return L.coli_quantize_fp8_matrix(x, dt, n, r, c, ld, xs, q, qs, s, ss, qt, qs, st, ss, None)
+
+    def columns(x=16, dt=0, r=4, c=64, ld=64, qt=16, st=16, off=16, E=2, P=512, q=None, s=None):
+        return L.coli_quantize_fp8_columns(x, dt, r, c, ld, off, E, qt, P, st, q, s, None)
+
+    for f in (rows, back, matrix, columns):
+        assert f(c=40) == EINVAL and f(c=0) == EINVAL and f(r=-1) == EINVAL and f(ld=63) == EINVAL
+        assert f(dt=3) == EUNSUP and f(dt=-1) == EUNSUP and f(x=None) == EINVAL
+        assert f(c=1 << 30, ld=1 << 30) == EUNSUP if f is not columns else True
+        assert f(r=0, x=None) == OK
+    for f in (rows, back, matrix):
+        assert f(q=24) == EINVAL and f(s=18) == EINVAL and f(q=None) == EINVAL and f(s=None) == EINVAL
+    assert rows(r=1 << 40) == EUNSUP and back(r=1 << 40) == EUNSUP
+    assert L.coli_dequantize_fp8(16, 16, 4, 64, 2, 16, 0, 64, None) == EINVAL
+    assert matrix(q=None, s=None) == EINVAL                      # no output
+    assert matrix(n=-1) == EINVAL and matrix(n=0) == OK
+    assert matrix(xs=2047) == EINVAL and matrix(qs=2032) == EINVAL and matrix(ss=0) == EINVAL
+    assert matrix(qs=2056) == EINVAL and matrix(ss=6) == EINVAL
+    assert matrix(r=24, qt=16, st=16) == EINVAL                  # the transposed rows are no multiple of 16
+    assert matrix(qt=24, st=16) == EINVAL and matrix(qt=16) == EINVAL
+    assert matrix(r=1 << 30) == EUNSUP and matrix(r=1 << 24, c=1 << 20, ld=1 << 20, n=1) == EUNSUP
+    assert columns(P=500) == EINVAL and columns(P=128) == EINVAL and columns(P=1 << 31) == EUNSUP
+    assert columns(E=0) == EINVAL and columns(E=1025, P=1 << 20) == EUNSUP and columns(off=None) == EINVAL
+    assert columns(qt=None) == EINVAL and columns(st=None) == EINVAL and columns(qt=24) == EINVAL
+    assert columns(q=16) == EINVAL and columns(q=24, s=16) == EINVAL
+
+
+def test_product_refusals(L):
+    def mm(a=16, s=16, rows=4, K=64, off=16, E=2, table=16, q=0, so=256, n=8, y=16, dt=0, ld=8):
+        return L.coli_fp8_matmul(a, s, rows, K, off, E, table, q, so, n, y, dt, ld, None)
+
+    def sw(a=16, s=16, rows=4, K=64, off=16, E=2, table=16, q=0, so=256, n=16, y=16, ys=16, dt=0, ld=16, uq=1024, us=512):
+        return L.coli_fp8_swiglu(a, s, rows, K, off, E, table, q, so, uq, us, n, y, ys, dt, ld, None)
+
+    for f in (mm, sw):
+        assert f(rows=-1) == EINVAL and f(K=40) == EINVAL and f(K=0) == EINVAL and f(K=(1 << 22) + 16) == EUNSUP
+        assert f(n=0) == EINVAL and f(E=0) == EINVAL and f(E=1025) == EUNSUP and f(off=None) == EINVAL
+        assert f(ld=7) == EINVAL and f(dt=3) == EUNSUP and f(dt=-1) == EUNSUP
+        assert f(q=8) == EINVAL and f(so=6) == EINVAL and f(a=24) == EINVAL and f(s=18) == EINVAL
+        assert f(a=None) == EINVAL and f(table=None) == EINVAL and f(y=None) == EINVAL and f(s=None) == EINVAL
+        assert f(rows=0, a=None, table=None, y=None) == OK
+        assert f(n=(1 << 31) - 1, ld=1 << 31) == EUNSUP
+    assert mm(dt=coli.FP8) == EUNSUP                             # only the SwiGLU writes FP8
+    assert sw(n=24, ld=24, dt=coli.FP8) == EINVAL and sw(dt=coli.FP8, ys=None) == EINVAL and sw(dt=coli.FP8, y=24) == EINVAL
+    assert sw(uq=8) == EINVAL and sw(us=2) == EINVAL
+
+    def wg(g=16, gs=16, x=16, xs=16, P=512, rows=4, off=16, E=2, N=16, K=32, acc=0, dw=16, dt=0, ld=32):
+        return L.coli_fp8_wgrad(g, gs, x, xs, P, rows, off, E, N, K, acc, dw, dt, ld, None)
+
+    assert wg(rows=-1) == EINVAL and wg(P=500) == EINVAL and wg(P=128) == EINVAL and wg(P=1 << 31) == EUNSUP
+    assert wg(E=0) == EINVAL and wg(E=1025, P=1 << 20) == EUNSUP and wg(off=None) == EINVAL
+    assert wg(N=24) == EINVAL and wg(K=24) == EINVAL and wg(N=0) == EINVAL and wg(K=0) == EINVAL
+    assert wg(dt=3) == EUNSUP and wg(ld=31) == EINVAL and wg(ld=1 << 56) == EUNSUP and wg(N=1 << 30) == EUNSUP
+    assert wg(dw=None) == EINVAL and wg(g=None) == EINVAL and wg(xs=None) == EINVAL and wg(g=24) == EINVAL
+    assert wg(rows=0, acc=1, g=None, gs=None, x=None, xs=None) == OK
+    assert L.coli_moe_dispatch_fp8(16, 0, 2, 2, 40, 40, 16, 16, 16, None) == EINVAL
+    assert L.coli_moe_dispatch_fp8(16, 0, 2, 2, 32, 31, 16, 16, 16, None) == EINVAL
+    assert L.coli_moe_dispatch_fp8(16, 0, 2, 2, 32, 32, 16, 24, 16, None) == EINVAL
+    assert L.coli_moe_dispatch_fp8(None, 0, 2, 2, 32, 32, 16, 16, 16, None) == EINVAL
+    assert L.coli_moe_dispatch_fp8(None, 0, 0, 2, 32, 32, None, None, None, None) == OK
+
+
+def test_sizes(L):
+    assert coli.fp8_columns_ld(1, 256) == 128 and coli.fp8_columns_ld(128, 1) == 128 and coli.fp8_columns_ld(129, 1) == 256
+    assert coli.fp8_columns_ld(0, 4) == 0 and coli.fp8_columns_ld(300, 2) == 512      # 1 + 299, or 172 + 128
+    for rows in (1, 5, 127, 128, 129, 1000):
+        for E in (1, 3, 64):
+            P = coli.fp8_columns_ld(rows, E)
+            assert coli.fp8_columns_ld(coli._rows_of_ld(P, E), E) <= P and coli._rows_of_ld(P, E) >= rows
+    off, nbytes = coli.fp8_blob_layout(coli.MoEShape(6144, 2048, 256))
+    m, n = 6144 * 2048, 4 * 48 * 16
+    assert off == [0, m, 2 * m, 3 * m, 3 * m + n, 3 * m + 2 * n] and nbytes == 3 * (m + n)
+    off, nbytes = coli.fp8_blob_layout(coli.MoEShape(32, 64, 1, top_k=1))
+    m = 32 * 64
+    assert off == [0, m, 2 * m, 3 * m, 3 * m + 256, 3 * m + 512] and nbytes == 3 * m + 768
+    with pytest.raises(coli.ColiError):
+        coli.fp8_blob_layout(coli.MoEShape(48, 32, 1, top_k=1))
+
+
+def test_binding_refusals():
+    import torch
+    x, i = torch.zeros(4, 32), torch.zeros(4, 2, dtype=torch.int32)
+    for f in (lambda: coli.quantize_fp8(x), lambda: coli.quantize_fp8_matrix(x), lambda: coli.quantize_fp8_columns(x),
+              lambda: coli.route_groups(x, None, 2), lambda: coli.route_groups_bwd(x, x, i), lambda: coli.dispatch_fp8(x, i),
+              lambda: coli.dequantize_fp8(x.to(torch.uint8), x), lambda: coli.fp8_matmul(x.to(torch.uint8), x, i, 4),
+              lambda: coli.fp8_wgrad(x, x, x, x)):
+        with pytest.raises(ValueError, match="device tensor"):
+            f()
+    with pytest.raises(ValueError, match="score"):
+        coli._score("relu")
+
+
+def test_reference_codes():
+    """The codes against torch's type, the scale rule by its definition."""
+    import torch
+    t = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(t, ref.CODES, equal_nan=True)
+    x = np.concatenate([np.linspace(-448, 448, 40001), ref.CODES[:126], (ref.CODES[:126] + ref.CODES[1:127]) / 2])
+    assert np.array_equal(ref.encode(x), torch.from_numpy(x).float().to(torch.float8_e4m3fn).view(torch.uint8).numpy())
+    for top in (448.0, 448.0000305, 447.9, 1.0, 1.75, 1.7500001, 3e-39, 0.0, 3.4e38, 2.0 ** -118 * 1.75, 2.0 ** -118 * 1.76):
+        s = ref.scale_value(ref.scale_code(np.float32(top)))
+        assert float(np.float32(top)) <= 448 * s and (s == 2.0 ** -126 or float(np.float32(top)) > 224 * s)
+    assert ref.scale_code(np.inf) == 255 and ref.scale_code(np.nan) == 255
+
+
+def test_reference_route_gradient():
+    """The formula against central differences of the weights (and scores) for fixed choices."""
+    rng = np.random.default_rng(5)
+    logits = rng.standard_normal((5, 12))
+    logits[1, 3] = -np.inf
+    idx = np.stack([rng.permutation(12)[:4] for _ in range(5)]).astype(np.int32)
+    idx[2, 3] = -1
+    idx[4] = -1
+    gw, gs = rng.standard_normal((5, 4)), rng.standard_normal((5, 12))
+    for kind in ("sigmoid", "softmax"):
+        for norm in (True, False):
+            def f(l):
+                return (gw * ref.weights(l, idx, kind, norm, 2.5) * (idx >= 0)).sum(1) + (gs * ref.scores(l, kind)).sum(1)
+            got = ref.route_grad(gw, logits, idx, kind, norm, 2.5, gs)
+            for e in range(12):
+                d = np.zeros_like(logits)
+                d[:, e] = 1e-5
+                diff = (f(logits + d) - f(logits - d)) / 2e-5
+                assert np.abs(got[:, e] - diff).max() < 1e-8

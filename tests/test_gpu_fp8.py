@@ -1,0 +1,549 @@
+"""FP8 quantisers, grouped products and their gradients against plain 64-bit forms.
+
+Tolerances: the quantisers and their inverse are exact. Products: product_bound's argument for every value and norm_bound's
+for all together (fp8_refs), plus half a step of the output type. SwiGLU: the errors of both sums through the derivatives
+(|silu'| <= 1.1), 16 half-steps of f32 for exp, divide and the two products, plus the output's half step."""
+import numpy as np
+import pytest
+
+from tests import fp8_refs as ref
+from tests.fp8_cases import CASES
+
+pytestmark = pytest.mark.gpu
+DTYPES = ("float32", "bfloat16", "float16")
+
+
+@pytest.fixture(scope="module")
+def coli():
+    import int4_routed_expert_sigmoid_amd as c
+    c.lib()
+    return c
+
+
+def _dev(a):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a)).to("cuda")
+
+
+def _t(name):
+    import torch
+    return getattr(torch, name)
+
+
+def _half_step(name):
+    import torch
+    return torch.finfo(_t(name)).eps / 2
+
+
+def _rounding(name, y):
+    """Half a step of the type at y: relative to the value, and below the smallest normal number half of the fixed step that
+    subnormal numbers have (float16: 2^-25 below 2^-14)."""
+    import torch
+    return np.maximum(_half_step(name) * np.abs(y), torch.finfo(_t(name)).tiny * _half_step(name))
+
+
+def _within(err, tol):
+    return err.size == 0 or bool((err <= tol).all())
+
+
+def _host(t):
+    return t.double().cpu().numpy()
+
+
+def _hard(rng, rows, cols):
+    """Normal values of very different sizes, with ties between codes, exact ends of ranges, zeros and outliers."""
+    x = rng.standard_normal((rows, cols)) * np.exp2(rng.integers(-8, 9, (rows, -(-cols // 16)))).repeat(16, 1)[:, :cols]
+    mid = (ref.CODES[:126] + ref.CODES[1:127]) / 2
+    ties = rng.choice(np.concatenate([mid, ref.CODES[:127]]), (rows, cols)) * rng.choice([-1.0, 1.0], (rows, cols))
+    pick = rng.random((rows, -(-cols // 128))).repeat(128, 1)[:, :cols] < 0.4
+    scale = np.exp2(rng.integers(-4, 4, (rows, -(-cols // 128)))).repeat(128, 1)[:, :cols]
+    x = np.where(pick, ties * scale, x)
+    x[rng.random((rows, cols)) < 0.05] = -0.0
+    x[rng.random((rows, cols)) < 0.05] = 0.0
+    x[rng.random(rows) < 0.1] = 0.0
+    return x
+
+
+# ---------------------------------------------------------------- quantisers
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols,pad", [(1, 16, 0), (1, 128, 0), (3, 144, 0), (1, 6144, 0), (37, 2080, 0), (37, 2080, 5),
+                                           (1029, 1040, 0), (513, 2048, 8), (5, 240, 1)])
+def test_quantize_rows(coli, dtype, rows, cols, pad):
+    import torch
+    rng = np.random.default_rng(rows * 1000 + cols + pad)
+    full = torch.from_numpy(_hard(rng, rows, cols)).to(_t(dtype))
+    buf = torch.full((rows, cols + pad), float("nan"), dtype=_t(dtype))
+    buf[:, :cols] = full
+    q, s = coli.quantize_fp8(buf.to("cuda")[:, :cols])
+    qr, sr = ref.quantize_rows(_host(full))
+    assert np.array_equal(_host(s), ref.scale_value(sr))
+    assert np.array_equal(q.cpu().numpy(), qr)
+    for out in DTYPES:
+        out_buf = torch.full((rows, cols + pad), 7.0, dtype=_t(out), device="cuda")
+        v = coli.dequantize_fp8(q, s, out=out_buf[:, :cols])
+        assert torch.equal(v.cpu(), torch.from_numpy(ref.values(qr, ref.scale_value(sr))).to(_t(out)))
+        assert bool((out_buf[:, cols:] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_quantize_extremes(coli, dtype):
+    """Infinities, NaN, a type's largest and smallest values, every scale border, empty input, rows off a 16-byte boundary."""
+    import torch
+    info = torch.finfo(_t(dtype))
+    x = torch.zeros(10, 256, dtype=_t(dtype))
+    x[0, 3], x[0, 133] = float("inf"), float("-inf")
+    x[1, 31], x[1, 140] = float("nan"), 1.0
+    x[2], x[3] = info.max, info.min
+    x[4] = info.tiny
+    x[5, :32] = info.smallest_normal * info.eps                  # subnormal
+    x[6, 0], x[6, 1] = info.max, info.tiny
+    x[7, 0] = info.tiny / 4
+    x[8, 0], x[8, 130] = 448.0, 448.0 * (1 + info.eps)            # the largest of one scale, the smallest of the next
+    x[9, :128] = torch.linspace(-448, 448, 128)
+    q, s = coli.quantize_fp8(x.to("cuda"))
+    qr, sr = ref.quantize_rows(_host(x))
+    assert np.array_equal(_host(s), ref.scale_value(sr), equal_nan=True) and np.array_equal(q.cpu().numpy(), qr)
+    assert sr[0].tolist() == [255, 255] and sr[1, 0] == 255 and sr[1, 1] != 255 and sr[8].tolist() == [127, 128]
+    v = coli.dequantize_fp8(q, s)
+    assert np.array_equal(_host(v), ref.values(qr, ref.scale_value(sr)).astype(np.float32), equal_nan=True)
+    buf = torch.zeros(10 * 256 + 1, dtype=_t(dtype), device="cuda")
+    odd = buf[1:].view(10, 256)
+    odd.copy_(x)
+    q2, s2 = coli.quantize_fp8(odd)
+    assert torch.equal(q2, q) and torch.equal(s2.nan_to_num(7.0), s.nan_to_num(7.0))
+    q0, s0 = coli.quantize_fp8(torch.empty(0, 64, dtype=_t(dtype), device="cuda"))
+    assert q0.shape == (0, 64) and s0.shape == (0, 1) and coli.dequantize_fp8(q0, s0).shape == (0, 64)
+
+
+def test_all_codes_and_any_scale(coli):
+    """Every code under scales that are no powers of two, 0, NaN and infinity, of rows and of matrices."""
+    import torch
+    q = torch.arange(256, dtype=torch.uint8, device="cuda").repeat(130, 1)
+    for s in (torch.rand(130, 2, device="cuda") * 3, torch.rand(2, 2, device="cuda")):
+        s[1, 1], s[0, 1] = float("inf"), 0.0
+        block = 1 if s.shape[0] == 130 else 128
+        with np.errstate(invalid="ignore"):
+            want = ref.values(q.cpu().numpy(), _host(s), block).astype(np.float32)
+        for out in DTYPES:
+            got = coli.dequantize_fp8(q, s, dtype=_t(out)).cpu()
+            assert torch.equal(got.nan_to_num(9.0), torch.from_numpy(want).to(_t(out)).nan_to_num(9.0))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("count,rows,cols,pad", [(1, 16, 16, 0), (1, 128, 128, 0), (3, 144, 272, 0), (2, 256, 128, 3), (1, 1040, 96, 0),
+                                                 (5, 48, 384, 16)])
+def test_quantize_matrix(coli, dtype, count, rows, cols, pad):
+    import torch
+    rng = np.random.default_rng(count * 1000 + rows + cols + pad)
+    x = torch.from_numpy(np.stack([_hard(rng, rows, cols) for _ in range(count)])).to(_t(dtype))
+    buf = torch.full((count, rows + 1, cols + pad), float("nan"), dtype=_t(dtype), device="cuda")
+    buf[:, :rows, :cols] = x.cuda()
+    arena = torch.full((count, 3 * rows * cols + 512), 9, dtype=torch.uint8, device="cuda")
+    half, nb, nk = rows * cols, -(-rows // 128), -(-cols // 128)
+    places = dict(q=arena[:, :half].unflatten(1, (rows, cols)), qt=arena[:, half:2 * half].unflatten(1, (cols, rows)),
+                  s=arena[:, 2 * half:2 * half + 4 * nb * nk].view(torch.float32).unflatten(1, (nb, nk)))
+    for given in ({}, places):
+        q, s, qt, st = coli.quantize_fp8_matrix(buf[:, :rows, :cols], transposed=True, **given)
+        for i in range(count):
+            qr, sr = ref.quantize_matrix(_host(x[i]))
+            assert np.array_equal(q[i].cpu().numpy(), qr) and np.array_equal(_host(s[i]), ref.scale_value(sr))
+            assert np.array_equal(qt[i].cpu().numpy(), qr.T) and np.array_equal(_host(st[i]), ref.scale_value(sr).T)
+    assert bool((arena[:, 2 * half + 4 * nb * nk:] == 9).all())
+    one = coli.quantize_fp8_matrix(x[0].cuda())
+    assert len(one) == 2 and torch.equal(one[0], q[0]) and torch.equal(one[1], s[0])
+    v = coli.dequantize_fp8(q, s)
+    assert np.array_equal(_host(v[-1]), ref.values(q[-1].cpu().numpy(), _host(s[-1]), 128))
+    one = coli.quantize_fp8_matrix(torch.full((20, 32), float("inf"), device="cuda"))   # rows in no 16s: one way round
+    assert bool(one[1].isnan().all()) and int(one[0].sum()) == 0
+
+
+COUNTS = [[1], [0, 3, 0], [128, 129, 0, 1, 127, 256], [7] * 70, [0] * 5, [300], [0, 0, 500, 12]]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("case", range(len(COUNTS)))
+def test_quantize_columns(coli, dtype, case):
+    import torch
+    counts, cols = COUNTS[case], (16, 144, 272, 128, 32, 400, 96)[case]
+    rng = np.random.default_rng(case)
+    before, behind = (0, 3)[case % 2], (0, 0, 5)[case % 3]
+    off = np.concatenate([[before], before + np.cumsum(counts)]).astype(np.int32)
+    rows = int(off[-1]) + behind
+    x = torch.from_numpy(_hard(rng, rows, cols)).to(_t(dtype)) if rows else torch.zeros(0, cols, dtype=_t(dtype))
+    if rows > 4:
+        x[before, 3] = float("nan")
+    want_q, want_s = ref.quantize_columns(_host(x), off)
+    P = coli.fp8_columns_ld(rows, len(counts)) + 128
+    qt = torch.full((cols, P), 77, dtype=torch.uint8, device="cuda")
+    st = torch.full((P // 128, cols), 77, dtype=torch.uint8, device="cuda")
+    q = torch.full((rows, cols), 77, dtype=torch.uint8, device="cuda")
+    s = torch.full((rows, -(-cols // 128)), 77.0, device="cuda")
+    buf = torch.full((rows, cols + 3), 1.0, dtype=_t(dtype), device="cuda")
+    buf[:, :cols] = x.cuda()
+    coli.quantize_fp8_columns(buf[:, :cols], _dev(off), qt=qt, st=st, q=q, s=s)
+    n = want_q.shape[1]
+    assert np.array_equal(qt.cpu().numpy()[:, :n], want_q) and bool((qt[:, n:] == 77).all())
+    assert np.array_equal(st.cpu().numpy()[:n // 128], want_s) and bool((st[n // 128:] == 77).all())
+    lo, hi = before, int(off[-1])
+    if hi > lo:
+        qr, sr = ref.quantize_rows(_host(x[lo:hi]))
+        assert np.array_equal(q[lo:hi].cpu().numpy(), qr) and np.array_equal(_host(s[lo:hi]), ref.scale_value(sr), equal_nan=True)
+    assert bool((q[:lo] == 77).all()) and bool((q[hi:] == 77).all()) and bool((s[hi:] == 77.0).all())
+    if len(counts) == 1 and before + behind == 0:
+        a, b = coli.quantize_fp8_columns(x.cuda())
+        assert a.shape[1] == -(-rows // 128) * 128 and np.array_equal(a.cpu().numpy(), want_q) and np.array_equal(b.cpu().numpy(), want_s)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_dispatch(coli, dtype):
+    """A token's codes and scales in all of its rows, rows of no slot left as they are."""
+    import torch
+    rng = np.random.default_rng(2)
+    for T, k, H in ((1, 1, 16), (9, 4, 272), (70, 8, 2064), (3, 2, 6144)):
+        x = torch.from_numpy(_hard(rng, T, H)).to(_t(dtype))
+        inv = rng.permutation(T * k).reshape(T, k).astype(np.int32)
+        gone = rng.random((T, k)) < 0.3
+        want_q, want_s = ref.quantize_rows(_host(x))
+        q = torch.full((T * k, H), 7, dtype=torch.uint8, device="cuda")
+        s = torch.full((T * k, -(-H // 128)), 7.0, device="cuda")
+        coli.dispatch_fp8(x.cuda(), _dev(np.where(gone, rng.choice([-1, T * k], (T, k)), inv).astype(np.int32)), q=q, s=s)
+        for t in range(T):
+            for j in range(k):
+                p = inv[t, j]
+                if gone[t, j]:
+                    assert bool((q[p] == 7).all()) and bool((s[p] == 7.0).all())
+                else:
+                    assert np.array_equal(q[p].cpu().numpy(), want_q[t]) and np.array_equal(_host(s[p]), ref.scale_value(want_s[t]))
+
+
+def test_quantize_past_32_bits(coli):
+    import torch
+    rows, cols = 1 << 18, 8208                                    # 2.15e9 bf16 values
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[-1, -16:] = 3.0
+    x[rows // 2, 128] = -1.0
+    for src in (x, x[:, :8192]):
+        q, s = coli.quantize_fp8(src)
+        assert int((q != 0).sum()) == (17 if src is x else 1) and q[rows // 2, 128].item() == 0xF8
+        v = coli.dequantize_fp8(q, s, dtype=torch.bfloat16)
+        assert v[rows // 2, 128].item() == -1.0 and (src is not x or bool((v[-1, -16:] == 3.0).all()))
+        del q, s, v
+    q, s, qt, st = coli.quantize_fp8_matrix(x, transposed=True)
+    assert q[-1, -1].item() == qt[-1, -1].item() == 0x7C and int((qt != 0).sum()) == 17 and st[-1, -1] == s[-1, -1]
+    del q, s
+    a, b = coli.quantize_fp8_columns(x)
+    assert int((a != 0).sum()) == 17 and a[-1, -1].item() == 0x7C and a[128, rows // 2].item() == 0xF8
+    assert b[-1, -1].item() == 120
+
+
+# ---------------------------------------------------------------- products
+def _weights(rng, E, n, K, parts=1):
+    """Blobs of `parts` FP8 matrices each with any scales, 16 bytes of something before them; (blobs, table, matrices, offsets)."""
+    import torch
+    nb, nk = -(-n // 128), -(-K // 128)
+    s_off = 16 + parts * n * K + (-parts * n * K) % 4 + 4
+    size = -(-(s_off + 4 * parts * nb * nk) // 16) * 16
+    blobs = np.full((E, size), 0x7F, np.uint8)                    # NaN wherever a product should not read
+    mats = []
+    for e in range(E):
+        q = ref.encode(np.clip(110 * rng.standard_normal((parts, n, K)), -448, 448))
+        s = (2e-3 * (0.5 + rng.random((parts, nb, nk)))).astype(np.float32)
+        blobs[e, 16:16 + q.size] = q.reshape(-1)
+        blobs[e, s_off:s_off + 4 * s.size] = s.reshape(-1).view(np.uint8)
+        mats.append([ref.values(q[p], s[p], 128) for p in range(parts)])
+    dev = _dev(blobs)
+    table = dev.data_ptr() + size * torch.arange(E, dtype=torch.int64)
+    return dev, table.cuda(), mats, dict(q_off=16, s_off=s_off)
+
+
+def _rows(rng, rows, K):
+    q = ref.encode(np.clip(110 * rng.standard_normal((rows, K)), -448, 448))
+    s = (0.01 * (0.5 + rng.random((rows, -(-K // 128))))).astype(np.float32)
+    return _dev(q), _dev(s), ref.values(q, s)
+
+
+def _groups(counts, before, behind):
+    if isinstance(counts, int):
+        return None, np.array([0, counts]), counts
+    off = np.concatenate([[before], before + np.cumsum(counts)]).astype(np.int32)
+    return _dev(off), off, int(off[-1]) + behind
+
+
+def _case_id(c):
+    return f"{c[0]}-{c[1] if isinstance(c[1], int) else len(c[1])}-{c[2]}-{c[3]}"
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("case", CASES, ids=_case_id)
+def test_matmul(coli, case, dtype):
+    import torch
+    kernel, counts, K, n, before, behind = case
+    offsets, off, rows = _groups(counts, before, behind)
+    E = len(off) - 1
+    assert kernel == "" or rows == 0 or coli.debug_fp8_kernel(rows, K, E, n, grouped=offsets is not None) == kernel
+    rng = np.random.default_rng(K + n)
+    _keep, table, mats, at = _weights(rng, E, n, K)
+    a, a_s, va = _rows(rng, rows, K)
+    out = torch.full((rows, n + 3), 7.0, dtype=_t(dtype), device="cuda")
+    coli.fp8_matmul(a, a_s, table, n, offsets=offsets, out=out[:, :n], **at)
+    y, terms = ref.product(va, [m[0] for m in mats], off)
+    got, lo, hi = _host(out), int(off[0]), int(off[-1])
+    assert (got[:, n:] == 7.0).all() and (got[:lo] == 7.0).all() and (got[hi:] == 7.0).all()
+    err = np.abs(got[lo:hi, :n] - y[lo:hi])
+    assert _within(err, ref.product_bound(K, terms[lo:hi], dtype == "float32") * (1 + _half_step(dtype)) + _rounding(dtype, y[lo:hi]))
+    if hi > lo:
+        assert np.linalg.norm(err) <= (ref.norm_bound(K, dtype == "float32") + _half_step(dtype)) * np.linalg.norm(y[lo:hi])
+    again = coli.fp8_matmul(a, a_s, table, n, offsets=offsets, dtype=_t(dtype), **at)
+    assert torch.equal(again[lo:hi], out[lo:hi, :n])
+
+
+@pytest.mark.parametrize("dtype", DTYPES + ("fp8",))
+@pytest.mark.parametrize("case", CASES, ids=_case_id)
+def test_swiglu(coli, case, dtype):
+    import torch
+    _, counts, K, n, before, behind = case
+    n = -(-n // 16) * 16 if dtype == "fp8" else n
+    offsets, off, rows = _groups(counts, before, behind)
+    E = len(off) - 1
+    rng = np.random.default_rng(K + n + 1)
+    _keep, table, mats, at = _weights(rng, E, n, K, parts=2)
+    a, a_s, va = _rows(rng, rows, K)
+    va, a_s = va * (8 / np.sqrt(K)), a_s * np.float32(8 / np.sqrt(K))
+    va = ref.values(a.cpu().numpy(), _host(a_s))
+    exact = dtype == "float32"
+    g, tg = ref.product(va, [m[0] for m in mats], off)
+    u, tu = ref.product(va, [m[1] for m in mats], off)
+    eg, eu = ref.product_bound(K, tg, exact), ref.product_bound(K, tu, exact)
+    h = ref.silu(g) * u
+    err = 1.1 * eg * (np.abs(u) + eu) + (np.abs(ref.silu(g))) * eu + 16 * 2.0 ** -24 * np.abs(h)
+    lo, hi = int(off[0]), int(off[-1])
+    if dtype != "fp8":
+        out = torch.full((rows, n + 3), 7.0, dtype=_t(dtype), device="cuda")
+        coli.fp8_swiglu(a, a_s, table, n, offsets=offsets, out=out[:, :n], **at)
+        got = _host(out)
+        assert (got[:, n:] == 7.0).all() and (got[:lo] == 7.0).all() and (got[hi:] == 7.0).all()
+        assert _within(np.abs(got[:, :n] - h)[lo:hi], (err * (1 + _half_step(dtype)) + _rounding(dtype, h))[lo:hi])
+        return
+    q = torch.full((rows, n), 77, dtype=torch.uint8, device="cuda")
+    s = torch.full((rows, -(-n // 128)), 77.0, device="cuda")
+    coli.fp8_swiglu(a, a_s, table, n, offsets=offsets, out=(q, s), **at)
+    assert bool((q[:lo] == 77).all()) and bool((q[hi:] == 77).all()) and bool((s[:lo] == 77.0).all()) and bool((s[hi:] == 77.0).all())
+    s = _host(s)
+    for b in range(s.shape[1] if hi > lo else 0):
+        cols = slice(b * 128, (b + 1) * 128)
+        low = ref.scale_value(ref.scale_code(np.maximum(np.abs(h[lo:hi, cols]) - err[lo:hi, cols], 0).max(1)))
+        high = ref.scale_value(ref.scale_code((np.abs(h[lo:hi, cols]) + err[lo:hi, cols]).max(1)))
+        assert (low <= s[lo:hi, b]).all() and (s[lo:hi, b] <= high).all()
+    v = ref.values(q.cpu().numpy(), s)
+    step = np.maximum(2.0 ** -4 * (np.abs(h) + err), 2.0 ** -10 * s.repeat(128, 1)[:, :n])
+    assert _within(np.abs(v - h)[lo:hi], (err + step)[lo:hi])
+    new = coli.fp8_swiglu(a, a_s, table, n, offsets=offsets, dtype="fp8", **at)
+    assert torch.equal(new[0][lo:hi], q[lo:hi])
+
+
+def test_separate_gate_and_up(coli):
+    """Gate and up anywhere in the buffer: up before gate, scales before codes."""
+    import torch
+    rng = np.random.default_rng(8)
+    K, n = 272, 48
+    a, a_s, _ = _rows(rng, 3, K)
+    keep, table, _, at = _weights(rng, 1, n, K, parts=2)
+    want = coli.fp8_swiglu(a, a_s, table, n, **at)
+    b = keep[0].cpu().numpy()
+    q, s = b[16:16 + 2 * n * K].reshape(2, -1), b[at["s_off"]:at["s_off"] + 24].reshape(2, -1)
+    blob = _dev(np.concatenate([s[1], s[0], np.zeros(8, np.uint8), q[1], q[0]]))
+    t = torch.tensor([blob.data_ptr()], device="cuda")
+    got = coli.fp8_swiglu(a, a_s, t, n, q_off=32 + n * K, s_off=12, up_q_off=32, up_s_off=0)
+    assert torch.equal(got, want)
+
+
+def test_not_finite(coli):
+    """NaN codes and scales reach the results that they belong to and no other, in tails too."""
+    import torch
+    rng = np.random.default_rng(9)
+    for K in (144, 512):
+        a, a_s, _ = _rows(rng, 40, K)
+        keep, table, _, at = _weights(rng, 1, 33, K)
+        a[3, K - 1] = 0x7F
+        a_s[5, -1] = float("nan")
+        keep[0, 16 + 7 * K] = 0xFF
+        for dtype in DTYPES:
+            y = coli.fp8_matmul(a, a_s, table, 33, dtype=_t(dtype), **at).isnan()
+            want = torch.zeros(40, 33, dtype=torch.bool, device="cuda")
+            want[3], want[5], want[:, 7] = True, True, True
+            assert torch.equal(y, want)
+
+
+# ---------------------------------------------------------------- gradients
+WGRAD = [([3], 16, 16), ([128, 0, 129, 1], 144, 272), ([5, 40, 0, 260, 17], 64, 528), ([0, 0], 32, 16), ([1] * 9, 128, 128), (300, 272, 144),
+         ([700], 528, 400)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("counts,n,K", WGRAD, ids=lambda v: str(v).replace(" ", ""))
+def test_wgrad(coli, counts, n, K, dtype):
+    import torch
+    before, behind = (0, 0) if isinstance(counts, int) else (2, 3)
+    offsets, off, rows = _groups(counts, before, behind)
+    E = len(off) - 1
+    rng = np.random.default_rng(n + K)
+    g, x = 0.05 * rng.standard_normal((rows, n)), rng.standard_normal((rows, K)) * np.exp2(rng.integers(-6, 6, K))
+    g, x = _dev(g).to(torch.bfloat16), _dev(x).to(torch.bfloat16)
+    cols = [(coli.quantize_fp8_columns(t, offsets)) for t in (g, x)]
+    want, terms = np.zeros((E, n, K)), np.zeros((E, n, K))
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        vals = []
+        for t in (g, x):
+            q, s = ref.quantize_columns(_host(t)[lo:hi], [0, hi - lo])
+            vals.append(ref.CODES[q] * ref.scale_value(s).T.repeat(128, 1))
+        want[e], terms[e] = vals[0] @ vals[1].T, np.abs(vals[0]) @ np.abs(vals[1]).T
+    most = max(1, int((off[1:] - off[:-1]).max()))
+    tol = ref.product_bound(most, terms, dtype == "float32")
+    got = coli.fp8_wgrad(*cols[0], *cols[1], offsets, dtype=_t(dtype))
+    assert got.shape == (E, n, K)
+    err = np.abs(_host(got) - want)
+    assert _within(err, tol * (1 + _half_step(dtype)) + _rounding(dtype, want))
+    assert np.linalg.norm(err) <= (ref.norm_bound(most, dtype == "float32") + _half_step(dtype)) * np.linalg.norm(want)
+    # added to what is there, into rows with a gap
+    buf = torch.full((E, n, K + 3), 2.0, dtype=_t(dtype), device="cuda")
+    coli.fp8_wgrad(*cols[0], *cols[1], offsets, out=buf[..., :K], accumulate=True)
+    assert bool((buf[..., K:] == 2.0).all())
+    err = np.abs(_host(buf[..., :K]) - want - 2.0)
+    assert _within(err, tol * 1.01 + (_half_step(dtype) + 2.0 ** -24) * (np.abs(want) + 2.0))
+    coli.fp8_wgrad(*cols[0], *cols[1], offsets, out=buf[..., :K])
+    assert torch.equal(buf[..., :K], got)
+
+
+def test_wgrad_not_finite_and_no_rows(coli):
+    import torch
+    off = _dev(np.array([0, 0, 5], np.int32))
+    g, x = torch.ones(5, 16, device="cuda"), torch.ones(5, 32, device="cuda")
+    g[2, 3], x[1, 7] = float("nan"), float("inf")
+    for dtype in DTYPES:
+        dw = coli.fp8_wgrad(*coli.quantize_fp8_columns(g, off), *coli.quantize_fp8_columns(x, off), off, dtype=_t(dtype))
+        assert bool((dw[0] == 0).all())
+        bad = torch.zeros(16, 32, dtype=torch.bool, device="cuda")
+        bad[3], bad[:, 7] = True, True
+        assert torch.equal(dw[1].isnan(), bad) and bool((dw[1][~bad] == 5.0).all())
+        none = torch.zeros(3, dtype=torch.int32, device="cuda")
+        cols = coli.quantize_fp8_columns(g[:0], none), coli.quantize_fp8_columns(x[:0], none)
+        out = torch.full((2, 16, 32), 3.0, dtype=_t(dtype), device="cuda")
+        coli.fp8_wgrad(*cols[0], *cols[1], none, out=out, accumulate=True)
+        assert bool((out == 3.0).all())
+        assert bool((coli.fp8_wgrad(*cols[0], *cols[1], none, out=out) == 0).all())
+
+
+def test_layer_forward_and_backward(coli):
+    """The operators as a training step runs them, against the same steps in 64 bits from the same choices and
+    quantised values; the matrices' gradient also against differences."""
+    import torch
+    rng = np.random.default_rng(11)
+    T, k, E, H, I = 70, 3, 8, 272, 144
+    x = _dev(rng.standard_normal((T, H))).to(torch.bfloat16)
+    logits, bias = _dev(rng.standard_normal((T, E)).astype(np.float32)), _dev(0.1 * rng.standard_normal(E).astype(np.float32))
+    logits[4] = -float("inf")                                     # a padded token
+    W = _dev(0.05 * rng.standard_normal((E, I, H))).to(torch.bfloat16)
+    q, s, qt, st = coli.quantize_fp8_matrix(W, transposed=True)
+
+    def table(q, s):
+        n = q[0].numel()
+        blobs = torch.zeros(E, -(-(n + 4 * s[0].numel()) // 16) * 16, dtype=torch.uint8, device="cuda")
+        blobs[:, :n] = q.flatten(1)
+        blobs[:, n:n + 4 * s[0].numel()] = s.flatten(1).contiguous().view(torch.uint8)
+        return blobs, blobs.data_ptr() + blobs.shape[1] * torch.arange(E, device="cuda"), n
+
+    keep, tab, s_off = table(q, s)
+    keep_t, tab_t, s_off_t = table(qt, st)
+    idx, w = coli.route_groups(logits, bias, k, groups=4, groups_kept=2, scale=2.0)
+    _, offsets, _, _, _, inv = coli.union_inverse(idx, E)
+    a, a_s = coli.dispatch_fp8(x, inv)
+    rows = coli.fp8_matmul(a, a_s, tab, I, s_off=s_off, offsets=offsets)
+    y = coli.combine(rows, inv, w)
+    dy = _dev(rng.standard_normal((T, I)).astype(np.float32))
+    d_rows, d_w = coli.combine_bwd(dy, rows, inv, w)
+    gt, gt_s, g, g_s = coli.quantize_fp8_columns(d_rows, offsets, rows=True)
+    d_a = coli.fp8_matmul(g, g_s, tab_t, H, s_off=s_off_t, offsets=offsets)
+    xr = coli.dispatch(x, inv)
+    dW = coli.fp8_wgrad(gt, gt_s, *coli.quantize_fp8_columns(xr, offsets), offsets)
+    dx = coli.dispatch_bwd(d_a, inv)
+    dl = coli.route_groups_bwd(d_w, logits, idx, scale=2.0)
+    # the same in 64 bits
+    vx = ref.values(*[f(t) for f, t in zip((lambda t: t, ref.scale_value), ref.quantize_rows(_host(x)))])
+    vW = _host(coli.dequantize_fp8(q, s))
+    ii, ww = idx.cpu().numpy(), _host(w)
+    off, place = offsets.cpu().numpy(), inv.cpu().numpy()
+    assert (place[4] == -1).all() and int(off[-1]) == (T - 1) * k and (ii[4] == -1).all()
+    yr, drows = np.zeros((T, I)), np.zeros((T * k, I))
+    dwr, xrow = np.zeros((T, k)), np.zeros((T * k, H))
+    for t in range(T):
+        for j in range(k):
+            if ii[t, j] >= 0:
+                r = vW[ii[t, j]] @ vx[t]
+                yr[t] += ww[t, j] * r
+                dwr[t, j] = _host(dy)[t] @ r
+                drows[place[t, j]] = ww[t, j] * _host(dy)[t]
+                xrow[place[t, j]] = _host(x)[t]
+    assert np.linalg.norm(_host(y) - yr) <= 1e-5 * np.linalg.norm(yr)
+    assert np.linalg.norm(_host(d_w) - dwr) <= 1e-5 * np.linalg.norm(dwr)
+    assert np.linalg.norm(_host(dl) - ref.route_grad(dwr, _host(logits), ii, "sigmoid", True, 2.0)) <= 1e-4 * np.linalg.norm(_host(dl))
+    assert bool((dl[4] == 0).all()) and bool((dx[4] == 0).all())
+    used = int(off[-1])
+    dr = _host(d_rows)[:used]                                     # the quantisers' own inputs
+    qg, sg = ref.quantize_rows(dr)
+    vg, da = ref.values(qg, ref.scale_value(sg)), np.zeros((T * k, H))
+    for e in range(E):
+        da[off[e]:off[e + 1]] = vg[off[e]:off[e + 1]] @ vW[e]
+    dxr = np.stack([sum((da[p] for p in place[t] if p >= 0), np.zeros(H)) for t in range(T)])
+    assert np.linalg.norm(_host(dx) - dxr) <= 1e-5 * np.linalg.norm(dxr)
+    vals = []
+    for t in (dr, xrow[:used]):
+        qc, sc = ref.quantize_columns(t, off)
+        vals.append(ref.CODES[qc] * ref.scale_value(sc).T.repeat(128, 1))
+    first = np.concatenate([[0], np.cumsum(-(-(off[1:] - off[:-1]) // 128) * 128)])
+    for e in range(E):
+        gv, xv = vals[0][:, first[e]:first[e + 1]], vals[1][:, first[e]:first[e + 1]]
+        assert np.linalg.norm(_host(dW[e]) - gv @ xv.T) <= 1e-5 * np.linalg.norm(gv @ xv.T)
+        D = rng.standard_normal((I, H))                           # f(W) = sum of g . W x is linear: its difference is <dW, D>
+        diff = ((gv * ((vW[e] + D) @ xv)).sum() - (gv * ((vW[e] - D) @ xv)).sum()) / 2
+        assert abs((_host(dW[e]) * D).sum() - diff) <= 1e-4 * np.linalg.norm(gv @ xv.T) * np.linalg.norm(D) / np.sqrt(D.size) * 40
+
+
+def test_graph_and_streams(coli):
+    """A layer, forward and backward, in a graph that is replayed with new inputs, and on a given stream."""
+    import torch
+    rng = np.random.default_rng(12)
+    K, n, E, rows = 640, 256, 3, 30
+    keep, table, _, at = _weights(rng, E, n, K, parts=2)
+    off = _dev(np.array([0, 9, 9, 30], np.int32))
+    x = torch.randn(rows, K, device="cuda").to(torch.bfloat16)
+    keep2, table2, _, at2 = _weights(rng, E, K, n)
+    P = coli.fp8_columns_ld(rows, E)
+    e = torch.empty
+    out = dict(q=e(rows, K, dtype=torch.uint8, device="cuda"), s=e(rows, 5, device="cuda"), h=e(rows, n, dtype=torch.uint8, device="cuda"),
+               hs=e(rows, 2, device="cuda"), y=e(rows, K, device="cuda"), qt=e(K, P, dtype=torch.uint8, device="cuda"),
+               st=e(P // 128, K, dtype=torch.uint8, device="cuda"), dw=e(E, K, K, device="cuda"), v=e(rows, K, device="cuda"))
+
+    def step(o, stream=None):
+        coli.quantize_fp8_columns(x, off, qt=o["qt"], st=o["st"], q=o["q"], s=o["s"], stream=stream)
+        coli.fp8_swiglu(o["q"], o["s"], table, n, offsets=off, out=(o["h"], o["hs"]), stream=stream, **at)
+        coli.fp8_matmul(o["h"], o["hs"], table2, K, offsets=off, out=o["y"], stream=stream, **at2)
+        coli.fp8_wgrad(o["qt"], o["st"], o["qt"], o["st"], off, out=o["dw"], stream=stream)
+        coli.dequantize_fp8(o["q"], o["s"], out=o["v"], stream=stream)
+
+    step(out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(out)
+    side = torch.cuda.Stream()
+    for seed in range(3):
+        x.copy_(torch.randn(rows, K, generator=torch.Generator().manual_seed(seed)))
+        graph.replay()
+        torch.cuda.synchronize()
+        other = {k: torch.zeros_like(v) for k, v in out.items()}
+        side.wait_stream(torch.cuda.current_stream())
+        step(other, side)
+        side.synchronize()
+        assert torch.equal(out["y"], other["y"]) and torch.equal(out["dw"], other["dw"]) and torch.equal(out["v"], other["v"])
+        assert torch.equal(out["h"], other["h"])
