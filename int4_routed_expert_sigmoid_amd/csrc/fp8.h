@@ -96,6 +96,15 @@ __device__ __forceinline__ f32x4 wide_mfma(const Wide& w, const Wide& a, f32x4 c
 // sum's. Results of 32 bits (EXACT) therefore take bf16 products, which are exact and summed in f32 (1e-8),
 // at half the instruction's rate.
 
+constexpr int kBlockUnits = kFp8Block / kFp8Unit;       // 16-byte units of a row's block
+
+// What lanes behind the last column load into LDS.
+__device__ const u32x4 kZeroUnit = {0, 0, 0, 0};
+
+__device__ __forceinline__ void load4_to_lds(const uint8_t* p, uint32_t* dst) {
+    __builtin_amdgcn_global_load_lds((global_void*)p, (lds_void*)dst, 4, 0, 0);
+}
+
 // ------------------------------------------------------------ launchers
 coli_status launch_quantize_fp8(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
                                 uint8_t* q, float* s, hipStream_t stream);

@@ -196,43 +196,41 @@ __global__ __launch_bounds__(64 * WN * KS) void fp8_few_rows_kernel(Fp8GemmArgs 
 // LDS, a block of 128 columns (one cache line of every row) at a time, STAGES blocks ahead and on into the
 // workgroup's next unit. A wave waits for its own loads of a block by count and meets the others at one
 // barrier a block, once it has the block's last fragments in registers: from there on the slot is filled
-// again while the last two rows of fragments are multiplied and the next block's first ones are read.
-// Scales come 16 bytes, four blocks, a row where rows of scales are on 16-byte boundaries (wide).
-constexpr int kBlockUnits = kFp8Block / kFp8Unit;       // 16-byte units of a row's block
-
-// What lanes behind the last column load (TAIL).
-__device__ const u32x4 kZeroUnit = {0, 0, 0, 0};
-
-__device__ __forceinline__ void load4_to_lds(const uint8_t* p, uint32_t* dst) {
-    __builtin_amdgcn_global_load_lds((global_void*)p, (lds_void*)dst, 4, 0, 0);
-}
-
-template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int STAGES>
+// again while the last row of fragments is multiplied and the next block's first ones are read.
+// A product is scaled into its sum while the next row's are in the matrix unit: the four multiply-adds of one
+// product take half of its time there.
+// FAST: K in multiples of 512 and rows of scales on 16-byte boundaries: scales come 16 bytes, four blocks, a
+// row, and every unit is whole. Otherwise one block's at a time, and zeros behind the last column.
+template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int STAGES, bool FAST>
 struct LineTile {
+    static constexpr bool kFp8 = std::is_same<Out, Fp8Out>::value;
     static constexpr int BM = WM * MT * kFrag, BN = WN * NF * kFrag, kWaves = WM * WN, kThreads = 64 * kWaves;
     static constexpr int U = kBlockUnits;
     static constexpr int kCols = SWIGLU ? BN / 2 : BN;        // outputs of a tile
     static constexpr int kLoads = (BM + BN) * U / kThreads;   // code loads of a wave and block
     static constexpr int kARows = BM * U / kThreads;          // of them for the rows
     static constexpr int kScaleLoads = BM / 64 + 1;           // 64 rows each, and the matrix' blocks
+    static constexpr int kGroup = FAST ? 4 : 1;               // blocks whose scales come together
+    static constexpr int kStores = kFp8 ? MT : SWIGLU ? MT * NF / 2 : MT * (int)sizeof(Out);   // of a wave and whole tile
     static_assert(BM * U % kThreads == 0 && BN * U % kThreads == 0, "whole loads for every wave");
     static_assert(kScaleLoads <= kWaves && BM % 64 == 0, "one scale load a wave");
-    static_assert(MT % 4 == 0 && kLoads % 2 == 0, "the ring of row fragments; two shares of loads");
+    static_assert((MT == 4 || MT == 8) && NF == 4 && kWaves == 8, "the ring of row fragments; 64 columns and 8 rows a wave");
+    static_assert(STAGES == 2 || STAGES == 3, "the stores that a wait may leave in flight");
     static_assert(kCols % kFp8Block == 0 && NF * kFrag <= kFp8Block, "a wave's fragments share their scales");
     struct Lds {
         u32x4 code[STAGES][(BM + BN) * U];                    // rows, then matrix rows
-        // The scales of a group of blocks (4, or 1): rows, then the matrix' blocks. A slot is filled again
-        // STAGES groups later, for a block at least STAGES behind the last one that reads it.
-        u32x4 scale[STAGES][BM + 64];
+        // The scales of a group of blocks: rows, then the matrix' blocks. A slot is filled again STAGES groups
+        // later, for a block at least STAGES behind the last one that reads it.
+        float scale[STAGES][(BM + 64) * kGroup];
         uint32_t first[kMaxExperts];                          // first unit of every expert
-        uint32_t top[std::is_same<Out, Fp8Out>::value ? WN * BM : 1];
+        uint32_t top[kFp8 ? WN * BM : 1];
     };
 };
 
-template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int STAGES, bool TAIL>
-__global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a, int NT, int wide) {
-    typedef LineTile<Out, SWIGLU, MT, NF, WM, WN, STAGES> T;
-    constexpr int U = T::U;
+template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int STAGES, bool FAST>
+__global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a, int NT) {
+    typedef LineTile<Out, SWIGLU, MT, NF, WM, WN, STAGES, FAST> T;
+    constexpr int U = T::U, kGroup = T::kGroup, kW = SWIGLU ? 2 : 1;
     constexpr bool EXACT = std::is_same<Out, float>::value;
     __shared__ typename T::Lds lds;
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
@@ -252,16 +250,26 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a
 
     // the unit that is being loaded
     uint32_t load_at = at;
-    const uint8_t *w_base[SWIGLU ? 2 : 1], *a_base, *scale_base;
-    int m_last, n_last, scale_last;          // its last row and matrix row; of the scales that this wave loads
+    const uint8_t *w_base, *a_base, *scale_base;
     int lc = 0;                              // its next block
     bool loading = true;
+    uint32_t a_max, w_max;                   // a lane's place in the last row, and in the last matrix row
     const int sx = min(wave, T::kScaleLoads - 1);
+    // A load takes 8 rows, lane l row l / 8, position l % 8; of a wave's loads i each is kStep rows below the
+    // one before. SwiGLU: the tile's fragments are gate's and up's in turn, two loads each, and as there are 8
+    // waves, all of a wave's are of one matrix.
+    const int unit = (lane & 7) ^ (lane >> 3);
+    constexpr int kStepA = 8 * T::kWaves, kStepW = SWIGLU ? kStepA / 2 : kStepA;
+    const int a_row = wave * 8 + (lane >> 3);
+    const int w_row = SWIGLU ? wave / 4 * kFrag + wave % 2 * 8 + (lane >> 3) : a_row;
+    const bool up = SWIGLU && wave / 2 % 2 == 1;
+    const uint32_t a_lane = a_row * row_bytes + unit * 16, w_lane = w_row * row_bytes + unit * 16;
     auto set_unit = [&](const LineUnit& v) {
         const int n_tile = v.nt * T::kCols;
-        m_last = v.rows - 1, n_last = a.N - 1 - n_tile;
-        w_base[0] = v.blob + a.q_off + (int64_t)n_tile * row_bytes;
-        if constexpr (SWIGLU) w_base[1] = v.blob + a.up_q + (int64_t)n_tile * row_bytes;
+        const int m_last = v.rows - 1, n_last = a.N - 1 - n_tile;
+        a_max = m_last * row_bytes + unit * 16;
+        w_max = min(n_last, T::BN) * row_bytes + unit * 16;
+        w_base = v.blob + (up ? a.up_q : a.q_off) + (int64_t)n_tile * row_bytes;
         a_base = a.a + (int64_t)v.m0 * row_bytes;
         // rows' scales: 64 rows from sx * 64 on; the matrix': lane 0 and 1 its two blocks, or gate's and up's
         if (sx < T::BM / 64) {
@@ -274,37 +282,28 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a
         }
         lc = 0;
     };
-    // Load i of this wave for the block: 8 rows into a slot, lane l row l / 8, position l % 8. Behind the last
-    // unit the same number of loads goes out, so that the counts hold, into slots that are not read again.
-    const int unit = (lane & 7) ^ (lane >> 3);
+    // Load i of this wave for the block. Behind the last unit the same number of loads goes out, so that the
+    // counts hold, of its first block again and into slots that are not read.
     auto load_codes = [&](int slot, int i) {
         const bool rows = i < T::kARows;
-        const int x = (rows ? i : i - T::kARows) * T::kWaves + wave;         // 8 rows of the tile
-        const uint8_t* base;
-        uint32_t row;
-        if (rows) {
-            base = a_base;
-            row = min(x * 8 + (lane >> 3), m_last);
-        } else if constexpr (SWIGLU) {                                      // fragments of gate and up in turn
-            base = w_base[x / 2 % 2];
-            row = min(x / 4 * kFrag + x % 2 * 8 + (lane >> 3), n_last);
-        } else {
-            base = w_base[0];
-            row = min(x * 8 + (lane >> 3), n_last);
-        }
-        const uint8_t* p = base + (loading ? __umul24(row, row_bytes) + (uint32_t)(lc * U + unit) * 16 : 0u);
-        if (TAIL && lc * U + unit >= KU) p = (const uint8_t*)&kZeroUnit;
-        load_to_lds(p, lds.code[slot] + (rows ? x : T::BM / 8 + x) * 64);
+        const int j = rows ? i : i - T::kARows, below = j * (rows ? kStepA : kStepW);
+        // (rows behind the last are the last)
+        const uint32_t off = min((rows ? a_lane : w_lane) + (uint32_t)below * row_bytes, rows ? a_max : w_max);
+        const uint8_t* p = (rows ? a_base : w_base) + (uint32_t)lc * kFp8Block + off;
+        if (!FAST && lc * U + unit >= KU) p = (const uint8_t*)&kZeroUnit;
+        load_to_lds(p, lds.code[slot] + ((rows ? 0 : T::BM / 8) + j * T::kWaves + wave) * 64);
     };
     int fill_scale = 0;                      // the scale slot that is filled next
     auto load_scales = [&]() {
-        if (!loading || (wide && lc % 4 != 0)) return;
-        if (wide) load_to_lds(scale_base + lc * 4, lds.scale[fill_scale] + sx * 64);
-        else load4_to_lds(scale_base + lc * 4, (uint32_t*)lds.scale[fill_scale] + sx * 64);
+        if (!loading || lc % kGroup != 0) return;
+        float* dst = lds.scale[fill_scale] + sx * 64 * kGroup;
+        if constexpr (FAST) load_to_lds(scale_base + lc * 4, (u32x4*)dst);
+        else load4_to_lds(scale_base + lc * 4, (uint32_t*)dst);
         fill_scale = fill_scale == STAGES - 1 ? 0 : fill_scale + 1;
     };
     auto advance = [&]() {                   // to the block that is loaded next
-        if (++lc < KB || !loading) return;
+        if (!loading || ++lc < KB) return;
+        lc = 0;
         load_at += step;
         const LineUnit v = unit_at(load_at);
         loading = v.rows > 0;
@@ -321,95 +320,96 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a
         advance();
     }
 
+    // fragments: rows 16 apart have the same place in their unit's permutation
     const int m_lds = wm * kFrag + r, n_lds = T::BM + wn * NF * kFrag + r;
-    auto code = [&](int slot, int row) {
-        return Frag{lds.code[slot][lds_unit<U>(row, g)], lds.code[slot][lds_unit<U>(row, g + 4)]};
-    };
-    const int per_row = wide ? 4 : 1;
-    auto scale = [&](int from, int row, int b) {                // block b of the group's
-        return ((const float*)lds.scale[from])[row * per_row + (wide ? b % 4 : 0)];
-    };
-    constexpr int kW = SWIGLU ? 2 : 1;
-    const int ws_row = T::BM + (SWIGLU ? 0 : wn * NF * kFrag / kFp8Block);
-    Frag w[NF], av[4];
-    float as[4], ws[kW];
-    f32x4 acc[MT][NF];
+    const int lo = g ^ (r & 7), hi = (g + 4) ^ (r & 7);
     int slot = 0, scales = 0;                // of the block that is multiplied
+    auto code = [&](int row, int below) {
+        const u32x4* p = lds.code[slot] + below * U;
+        return Frag{p[row * U + lo], p[row * U + hi]};
+    };
+    const int ws_row = T::BM + (SWIGLU ? 0 : wn * NF * kFrag / kFp8Block);
+    // Tiles of 4 row fragments have registers for all of them, so that the waves meet, and the next loads go out,
+    // in the middle of a block; otherwise before its last row.
+    constexpr int kRing = MT == 4 ? 4 : 2, kMeet = MT == 4 ? 2 : MT - 1;
+    Frag w[NF], av[kRing];
+    float as[kRing], ws[kW];
+    f32x4 acc[MT][NF], p[NF];
+    float ps[kW] = {};                       // the scale of the products in p
     auto read_scales = [&](int b) {
 #pragma unroll
-        for (int x = 0; x < kW; ++x) ws[x] = scale(scales, ws_row + x, b);
+        for (int x = 0; x < kW; ++x) ws[x] = lds.scale[scales][(ws_row + x) * kGroup + b % kGroup];
     };
     auto read_row = [&](int i, int b) {
-        av[i % 4] = code(slot, m_lds + i * WM * kFrag);
-        as[i % 4] = scale(scales, m_lds + i * WM * kFrag, b);
+        av[i % kRing] = code(m_lds, i * WM * kFrag);
+        as[i % kRing] = lds.scale[scales][m_lds * kGroup + b % kGroup + i * WM * kFrag * kGroup];
     };
+    // How many tiles' stores may be in flight behind the loads of the block that is waited for next: those of
+    // the last STAGES - 1 blocks' units.
+    int stores[2] = {0, 0};
     wait_loads<(STAGES - 1) * T::kLoads>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 #pragma unroll
-    for (int f = 0; f < NF; ++f) w[f] = code(0, n_lds + f * kFrag);
+    for (int f = 0; f < NF; ++f) w[f] = code(n_lds, f * kFrag);
     read_scales(0);
     read_row(0, 0);
-    read_row(1, 0);
+    if constexpr (kRing == 4) read_row(1, 0);
     while (true) {
-        const int live = (u.rows - wm * kFrag + WM * kFrag - 1) / (WM * kFrag);   // fragments with rows
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int f = 0; f < NF; ++f) acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int f = 0; f < NF; ++f) p[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < kW; ++x) ps[x] = 0.f;
 #pragma unroll 1
         for (int c = 0; c < KB; ++c) {
-            auto multiply = [&](int i) {
-                if (MT > 4 || i < live) {
-                    f32x4 p[NF];
-#pragma unroll
-                    for (int f = 0; f < NF; ++f) p[f] = block_sum<EXACT>(w[f], av[i % 4]);
-#pragma unroll
-                    for (int f = 0; f < NF; ++f) add_scaled(acc[i][f], p[f], as[i % 4] * ws[SWIGLU ? f % 2 : 0]);
-                    hold(acc[i]);
-                }
-            };
-#pragma unroll
-            for (int i = 0; i < MT - 2; ++i) {
-                read_row(i + 2, c);
-                multiply(i);
-            }
-            // The next block and its scales (issued before its codes) have arrived, the codes of the
-            // STAGES - 2 behind it may not have, and this one is read.
-            wait_loads<(STAGES - 2) * T::kLoads>();
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
             const int fill = slot, next = c + 1 == KB ? 0 : c + 1;
-            slot = slot == STAGES - 1 ? 0 : slot + 1;
-            const float ws_old[2] = {ws[0], ws[kW - 1]}, as_old[2] = {as[2], as[3]};
-            if (!wide || next % 4 == 0) scales = scales == STAGES - 1 ? 0 : scales + 1;
-            load_scales();
-            // the last two rows, matrix fragment by matrix fragment, the one before scaled meanwhile
-            const bool last = MT > 4 || MT - 2 < live;
-            f32x4 p[2][2];
-            auto add_last = [&](int f) {
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    add_scaled(acc[MT - 2 + x][f], p[x][f % 2], as_old[x] * ws_old[SWIGLU ? f % 2 : 0]);
-                asm volatile("" : "+v"(acc[MT - 2][f]), "+v"(acc[MT - 1][f])::"memory");
-            };
+            for (int i = 0; i < MT; ++i) {
+                const int before = (i + MT - 1) % MT;
+                float s[kW];
 #pragma unroll
-            for (int f = 0; f < NF; ++f) {
-                if (last) {
-                    p[0][f % 2] = block_sum<EXACT>(w[f], av[2]);
-                    p[1][f % 2] = block_sum<EXACT>(w[f], av[3]);
-                    if (f > 0) add_last(f - 1);
+                for (int x = 0; x < kW; ++x) s[x] = as[i % kRing] * ws[x];
+                if (i == kMeet) {
+                    // The next block and its scales (issued before its codes) have arrived, the codes of the
+                    // STAGES - 2 behind it may not have, and this one is read.
+                    wait_behind_stores<(STAGES - 2) * T::kLoads, T::kStores>(STAGES == 3 ? stores[0] + stores[1] : stores[0]);
+                    if constexpr (STAGES == 3) stores[1] = stores[0];
+                    stores[0] = 0;
+                    __builtin_amdgcn_s_barrier();
+                    asm volatile("" ::: "memory");
+                    slot = slot == STAGES - 1 ? 0 : slot + 1;
+                    if (next % kGroup == 0) scales = scales == STAGES - 1 ? 0 : scales + 1;
+                    load_scales();
                 }
-                w[f] = code(slot, n_lds + f * kFrag);
-                if (f == 0) read_row(0, next);
-                if (f == 1) read_row(1, next);
-                if (f == 2) read_scales(next);
+                if constexpr (kRing == 4) {
+                    if (i == 0) read_row(2, c), read_row(3, c);
+                    if (i == kMeet) read_row(0, next), read_row(1, next);
+                } else {
+                    read_row((i + 1) % MT, i == kMeet ? next : c);
+                }
+                if (i == MT - 1) read_scales(next);
 #pragma unroll
-                for (int x = f * T::kLoads / NF; x < (f + 1) * T::kLoads / NF; ++x) load_codes(fill, x);
+                for (int f = 0; f < NF; ++f) {
+                    add_scaled(acc[before][f], p[f], ps[SWIGLU ? f % 2 : 0]);
+                    p[f] = block_sum<EXACT>(w[f], av[i % kRing]);
+                    if (i == MT - 1) w[f] = code(n_lds, f * kFrag);
+                    if (i == kMeet) {
+#pragma unroll
+                        for (int x = f * T::kLoads / NF; x < (f + 1) * T::kLoads / NF; ++x) load_codes(fill, x);
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < kW; ++x) ps[x] = s[x];
+                hold(acc[before]);
             }
-            if (last) add_last(NF - 1);
             advance();
         }
+#pragma unroll
+        for (int f = 0; f < NF; ++f) add_scaled(acc[MT - 1][f], p[f], ps[SWIGLU ? f % 2 : 0]);
         // outputs
         const int n_wave = u.nt * T::kCols + wn * (SWIGLU ? NF / 2 : NF) * kFrag;
 #pragma unroll
@@ -417,30 +417,39 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a
             const int row = m_lds + i * WM * kFrag, m = u.m0 + row;
             const bool there = row < u.rows;
             if constexpr (!SWIGLU) {
+                const int m0 = (i * WM + wm) * kFrag;
+                if (n_wave + NF * kFrag <= a.N) {         // uniform
+                    store64<Out, false>((Out*)a.y + (int64_t)(u.m0 + m0) * a.ld + n_wave, a.ld, u.rows - m0, acc[i][0], acc[i][1],
+                                        acc[i][2], acc[i][3]);
+                } else if (there) {
 #pragma unroll
-                for (int f = 0; f < NF; f += 2) store32<Out>(a, m, n_wave + f * kFrag, a.N, there, acc[i][f], acc[i][f + 1]);
+                    for (int f = 0; f < NF; ++f) {
+                        const int n0 = n_wave + f * kFrag + 4 * g;
+                        if (n0 < a.N) store4<Out>(a, m, n0, a.N, acc[i][f]);
+                    }
+                }
             } else {
 #pragma unroll
-                for (int p = 0; p < NF / 2; ++p) {
+                for (int x = 0; x < NF / 2; ++x) {
                     f32x4 h;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) h[x] = silu_mul(acc[i][2 * p][x], acc[i][2 * p + 1][x]);
-                    acc[i][2 * p] = h;
-                    const int n0 = n_wave + p * kFrag + 4 * g;
-                    if constexpr (!std::is_same<Out, Fp8Out>::value) {
+                    for (int y = 0; y < 4; ++y) h[y] = silu_mul(acc[i][2 * x][y], acc[i][2 * x + 1][y]);
+                    acc[i][2 * x] = h;
+                    const int n0 = n_wave + x * kFrag + 4 * g;
+                    if constexpr (!T::kFp8) {
                         if (there && n0 < a.N) store4<Out>(a, m, n0, a.N, h);
                     }
                 }
             }
         }
-        if constexpr (std::is_same<Out, Fp8Out>::value) {
+        if constexpr (T::kFp8) {
             // a row's largest |h| of the tile's 128, a wave's 32 of them at a time
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
                 uint32_t top = 0;
 #pragma unroll
-                for (int p = 0; p < NF / 2; ++p)
-                    if (n_wave + p * kFrag + 4 * g < a.N) top = max(top, top4(acc[i][2 * p]));
+                for (int x = 0; x < NF / 2; ++x)
+                    if (n_wave + x * kFrag + 4 * g < a.N) top = max(top, top4(acc[i][2 * x]));
                 top = umax_step<16>(top);
                 top = umax_step<32>(top);
                 if (g == 0) lds.top[wn * T::BM + m_lds + i * WM * kFrag] = top;
@@ -455,17 +464,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a
 #pragma unroll
                 for (int x = 0; x < WN; ++x) top = max(top, lds.top[x * T::BM + row]);
                 const int code = fp8_scale_code(top);
+                const float inv = fp8_scale_inverse(code);
+                // 8 neighbouring codes a lane
+                uint32_t q[2] = {codes4(acc[i][0], inv), codes4(acc[i][2], inv)};
+                swap_quarters(q[0], q[1]);
                 if (row >= u.rows) continue;
-#pragma unroll
-                for (int p = 0; p < NF / 2; ++p) {
-                    const int n0 = n_wave + p * kFrag + 4 * g;
-                    if (n0 < a.N) *(uint32_t*)((uint8_t*)a.y + (int64_t)m * a.N + n0) = codes4(acc[i][2 * p], fp8_scale_inverse(code));
-                }
+                typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+                uint8_t* y = (uint8_t*)a.y + (int64_t)m * a.N + n_wave + 8 * g;
+                if (n_wave + 8 * g < a.N) *(u32x2*)y = u32x2{q[0], q[1]};          // N comes in multiples of 16
                 if (wn == 0 && g == 0) a.ys[(int64_t)m * fp8_blocks(a.N) + u.nt] = fp8_scale_value(code);
             }
         }
-        at += step;
-        u = unit_at(at);
+        // Of a whole tile every lane's stores have gone out: at least as many as are counted.
+        if (u.rows == T::BM && (u.nt + 1) * T::kCols <= a.N) stores[0] = 1;
+        u = unit_at(at += step);
         if (u.rows <= 0) break;
     }
     wait_loads<0>();                         // nothing lands in LDS after the workgroup
@@ -473,16 +485,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a
 
 template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int STAGES>
 coli_status lines(const Fp8GemmArgs& a, hipStream_t stream) {
-    typedef LineTile<Out, SWIGLU, MT, NF, WM, WN, STAGES> T;
+    typedef LineTile<Out, SWIGLU, MT, NF, WM, WN, STAGES, true> T;
     const int NT = (a.N + T::kCols - 1) / T::kCols;
     uint32_t grid;
     if (coli_status st = grid_of(a, T::BM, NT, 1, "fp8 product", &grid)) return st;
     grid = std::min(grid, kCus);             // LDS holds one workgroup a CU
-    const int wide = fp8_blocks(a.K) % 4 == 0 && (uintptr_t)a.as % 16 == 0 && a.s_off % 16 == 0 && (!SWIGLU || a.up_s % 16 == 0);
-    if (a.K % kFp8Block == 0)
-        launch(fp8_line_kernel<Out, SWIGLU, MT, NF, WM, WN, STAGES, false>, dim3(grid), dim3(T::kThreads), 0, stream, a, NT, wide);
-    else
-        launch(fp8_line_kernel<Out, SWIGLU, MT, NF, WM, WN, STAGES, true>, dim3(grid), dim3(T::kThreads), 0, stream, a, NT, wide);
+    const bool fast = a.K % (4 * kFp8Block) == 0 && (uintptr_t)a.as % 16 == 0 && a.s_off % 16 == 0 && (!SWIGLU || a.up_s % 16 == 0);
+    if (fast) launch(fp8_line_kernel<Out, SWIGLU, MT, NF, WM, WN, STAGES, true>, dim3(grid), dim3(T::kThreads), 0, stream, a, NT);
+    else launch(fp8_line_kernel<Out, SWIGLU, MT, NF, WM, WN, STAGES, false>, dim3(grid), dim3(T::kThreads), 0, stream, a, NT);
     COLI_CHECK_LAUNCH("fp8 product kernel launch");
     return COLI_OK;
 }

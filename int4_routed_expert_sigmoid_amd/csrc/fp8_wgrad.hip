@@ -12,115 +12,255 @@
 namespace coli {
 namespace {
 
-// The first block of expert e and how many it has, by a wave.
-__device__ __forceinline__ void expert_blocks(const Fp8WgradArgs& a, int e, int* first, int* count) {
-    if (a.offsets == nullptr) {
-        *first = 0;
-        *count = (int)fp8_blocks(a.rows);
-        return;
-    }
-    const int lane = threadIdx.x & 63;
-    int before = 0;
-    for (int i = lane; i < e; i += 64) {
-        const int lo = min(max(a.offsets[i], 0), a.rows), hi = min(max(a.offsets[i + 1], lo), a.rows);
-        before += (int)fp8_blocks(hi - lo);
-    }
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) before += __shfl_xor(before, o);
-    const int lo = min(max(a.offsets[e], 0), a.rows), hi = min(max(a.offsets[e + 1], lo), a.rows);
-    *first = __builtin_amdgcn_readfirstlane(before);
-    *count = __builtin_amdgcn_readfirstlane((int)fp8_blocks(hi - lo));
-    // offsets that are not ascending may count more blocks than there are
+// Persistent workgroups of WM x WN waves, each MT fragments of g's columns (n) by NF fragments of x's (k), as
+// fp8_gemm.hip's lines: codes and scales straight into LDS, a block of 128 rows at a time, STAGES blocks
+// ahead and on into the workgroup's next unit (a tile of one expert's gradient, whose sum has as many
+// blocks as the expert has rows for, none where it has no rows). x is the first operand: a lane's four
+// results are four neighbouring k.
+template <typename T, int MT, int NF, int WM, int WN, int STAGES>
+struct WgradTile {
+    static constexpr int BM = WM * MT * kFrag, BN = WN * NF * kFrag, kWaves = WM * WN, kThreads = 64 * kWaves;
+    static constexpr int U = kBlockUnits;
+    static constexpr int kLoads = (BM + BN) * U / kThreads;   // code loads of a wave and block
+    static constexpr int kARows = BM * U / kThreads;          // of them for g
+    static constexpr int kStores = MT * sizeof(T);            // of a wave and whole tile (store64)
+    static_assert(STAGES == 2 || STAGES == 3, "the stores that a wait may leave in flight");
+    static_assert(BM * U % kThreads == 0 && BN * U % kThreads == 0, "whole loads for every wave");
+    static_assert(NF == 4, "a wave's columns are one store64");
+    static_assert(BM <= 256 && BN <= 256 && MT % 4 == 0, "a wave loads 256 scales; the ring of fragments");
+    struct Lds {
+        u32x4 code[STAGES][(BM + BN) * U];                    // g's columns, then x's
+        uint32_t scale[STAGES][2][64];                        // 256 bytes of each
+        uint32_t first[kMaxExperts];                          // first block of every expert
+    };
+};
+
+struct WgradUnit {
+    int e, n_tile, k_tile, first, count;     // count -1: no unit
+};
+
+template <typename T, int MT, int NF, int WM, int WN, int STAGES>
+__global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(Fp8WgradArgs a, int NT, int KT) {
+    typedef WgradTile<T, MT, NF, WM, WN, STAGES> W;
+    constexpr int U = W::U;
+    constexpr bool EXACT = std::is_same<T, float>::value;
+    __shared__ typename W::Lds lds;
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wn = wave % WN, wm = wave / WN;
+
+    const RowGroups groups = {a.offsets, nullptr, a.rows, a.E};
     const int all = (int)(a.ld_t / kFp8Block);
-    *first = min(*first, all);
-    *count = min(*count, all - *first);
+    const int blocks = min((int)scan_units<kFp8Block, W::kThreads>(groups, 1, lds.first, lds.scale[0][0]), all);
+    const uint32_t per_expert = (uint32_t)NT * KT, total = per_expert * a.E, per = (total + kXcds - 1) / kXcds;
+    const uint32_t xcd = blockIdx.x % kXcds, step = gridDim.x / kXcds;
+    auto unit_at = [&](uint32_t x) {
+        const uint32_t w = xcd * per + x;
+        WgradUnit u = {0, 0, 0, 0, -1};
+        if (x >= per || w >= total) return u;
+        u.e = w / per_expert;
+        const uint32_t rest = w - u.e * per_expert;
+        // blocks of kBlockM tiles of n by all of k, n first
+        const uint32_t block = rest / (kBlockM * KT), in = rest - block * kBlockM * KT;
+        const uint32_t tall = min(kBlockM, NT - block * kBlockM);
+        u.k_tile = in / tall * W::BN;
+        u.n_tile = (block * kBlockM + in % tall) * W::BM;
+        // (offsets that are not ascending may count more blocks than there are)
+        u.first = min(__builtin_amdgcn_readfirstlane((int)lds.first[u.e]), blocks);
+        u.count = (u.e + 1 < a.E ? min(__builtin_amdgcn_readfirstlane((int)lds.first[min(u.e + 1, a.E - 1)]), blocks) : blocks) - u.first;
+        return u;
+    };
+    uint32_t at = blockIdx.x / kXcds;        // this workgroup's units: at, at + step, ... of its XCD's `per`
+    WgradUnit u = unit_at(at);
+    if (u.count < 0) return;
+
+    // the block that is loaded next
+    uint32_t load_at = at;
+    const uint8_t *g_base = nullptr, *x_base = nullptr, *scale_base = nullptr;
+    int g_last = 0, x_last = 0, lc = 0, load_count = 0;
+    bool loading = true;
+    uint32_t scale_step = 0;
+    auto set_unit = [&](const WgradUnit& v) {
+        g_last = a.N - 1 - v.n_tile, x_last = a.K - 1 - v.k_tile;
+        g_base = a.g + (int64_t)v.n_tile * a.ld_t + (int64_t)v.first * kFp8Block;
+        x_base = a.x + (int64_t)v.k_tile * a.ld_t + (int64_t)v.first * kFp8Block;
+        // wave 0: g's scales, the others: x's; four a lane
+        scale_base = wave == 0 ? a.gs + (int64_t)v.first * a.N + v.n_tile + min(lane * 4, g_last - 3)
+                               : a.xs + (int64_t)v.first * a.K + v.k_tile + min(lane * 4, x_last - 3);
+        scale_step = wave == 0 ? a.N : a.K;
+        load_count = v.count;
+        lc = 0;
+    };
+    auto find = [&](WgradUnit v) {           // from unit v (load_at) on, the next that has blocks
+        while (v.count == 0) v = unit_at(load_at += step);
+        loading = v.count > 0;
+        if (loading) set_unit(v);
+    };
+    const int unit16 = ((lane & 7) ^ (lane >> 3)) * 16;
+    // Load i of this wave: 8 columns into a slot, lane l column l / 8, position l % 8. Behind the last unit the
+    // same number of loads goes out, so that the counts hold.
+    auto load_codes = [&](int slot, int i) {
+        const bool of_g = i < W::kARows;
+        const int x = (of_g ? i : i - W::kARows) * W::kWaves + wave;
+        const int row = min(x * 8 + (lane >> 3), of_g ? g_last : x_last);
+        const uint8_t* p = (of_g ? g_base : x_base) + row * a.ld_t + (lc * kFp8Block + unit16);
+        load_to_lds(loading ? p : (const uint8_t*)&kZeroUnit, lds.code[slot] + (of_g ? x : W::BM / 8 + x) * 64);
+    };
+    auto load_scales = [&](int slot) {
+        load4_to_lds(loading ? scale_base + (int64_t)lc * scale_step : (const uint8_t*)&kZeroUnit, lds.scale[slot][min(wave, 1)]);
+    };
+    auto advance = [&]() {
+        if (!loading || ++lc < load_count) return;
+        find(unit_at(load_at += step));
+    };
+
+    find(u);
+    __syncthreads();                         // the scan's scratch is a scale slot
+#pragma unroll
+    for (int c = 0; c < STAGES; ++c) {
+        load_scales(c);
+#pragma unroll
+        for (int i = 0; i < W::kLoads; ++i) load_codes(c, i);
+        advance();
+    }
+
+    const int m_lds = wm * kFrag + r, n_lds = wn * NF * kFrag + r;
+    auto code = [&](int slot, int row) {
+        return Frag{lds.code[slot][lds_unit<U>(row, g)], lds.code[slot][lds_unit<U>(row, g + 4)]};
+    };
+    auto scale = [&](int slot, int which, int row) { return (int)((const uint8_t*)lds.scale[slot][which])[row]; };
+    typedef typename std::conditional<EXACT, Wide, Frag>::type Operand;
+    Frag w[NF], av[4];
+    int ws[NF], as[4];
+    f32x4 acc[MT][NF];
+    int slot = 0;                            // of the block that is multiplied
+    // How many tiles' stores may be in flight behind the loads of the block that is waited for next: those
+    // of the last STAGES - 1 blocks' units (of units without blocks, whose stores follow each other, one).
+    int stores[2] = {0, 0};
+    auto read_x = [&](int f) {
+        w[f] = code(slot, W::BM + n_lds + f * kFrag);
+        ws[f] = scale(slot, 1, n_lds + f * kFrag);
+    };
+    auto read_g = [&](int i) {
+        av[i % 4] = code(slot, m_lds + i * WM * kFrag);
+        as[i % 4] = scale(slot, 0, m_lds + i * WM * kFrag);
+    };
+    wait_loads<(STAGES - 1) * W::kLoads>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int f = 0; f < NF; ++f) read_x(f);
+    read_g(0);
+    read_g(1);
+    while (true) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int f = 0; f < NF; ++f) acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int c = 0; c < u.count; ++c) {
+            Wide ww[EXACT ? NF : 1];
+            if constexpr (EXACT) {
+#pragma unroll
+                for (int f = 0; f < NF; ++f) ww[f] = widen(w[f], fp8_scale_value(ws[f]));
+            }
+            // row i of fragments, from a value of g that is in registers
+            auto product = [&](int i, int f, const Operand& gv, int gs) {
+                if constexpr (EXACT) acc[i][f] = wide_mfma(ww[f], gv, acc[i][f]);
+                else acc[i][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(words8(w[f]), words8(gv), acc[i][f], 0, 0,
+                                                                                  0, ws[f], 0, gs);
+            };
+            auto operand = [&](const Frag& v, int s) {
+                if constexpr (EXACT) return widen(v, fp8_scale_value(s));
+                else return v;
+            };
+#pragma unroll
+            for (int i = 0; i < MT - 2; ++i) {
+                read_g(i + 2);
+                const Operand gv = operand(av[i % 4], as[i % 4]);
+#pragma unroll
+                for (int f = 0; f < NF; ++f) product(i, f, gv, as[i % 4]);
+                hold(acc[i]);
+            }
+            // The next block and its scales (issued before its codes) have arrived, the codes of the
+            // STAGES - 2 behind it may not have, and this one is read.
+            wait_behind_stores<(STAGES - 2) * W::kLoads, W::kStores>(STAGES == 3 ? stores[0] + stores[1] : stores[0]);
+            if constexpr (STAGES == 3) stores[1] = stores[0];
+            stores[0] = 0;
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            const int fill = slot;
+            slot = slot == STAGES - 1 ? 0 : slot + 1;
+            load_scales(fill);
+            const Operand g2 = operand(av[2], as[2]), g3 = operand(av[3], as[3]);
+            const int s2 = as[2], s3 = as[3];
+#pragma unroll
+            for (int f = 0; f < NF; ++f) {
+                product(MT - 2, f, g2, s2);
+                product(MT - 1, f, g3, s3);
+                asm volatile("" : "+v"(acc[MT - 2][f]), "+v"(acc[MT - 1][f])::"memory");
+                read_x(f);
+                if (f < 2) read_g(f);
+#pragma unroll
+                for (int x = f * W::kLoads / NF; x < (f + 1) * W::kLoads / NF; ++x) load_codes(fill, x);
+            }
+            advance();
+        }
+        const int k_wave = u.k_tile + wn * NF * kFrag;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int n0 = u.n_tile + (i * WM + wm) * kFrag, n = n0 + r;
+            T* row = (T*)a.dw + ((int64_t)u.e * a.N + n0) * a.ld + k_wave;
+            if ((EXACT || !a.accumulate) && k_wave + NF * kFrag <= a.K) {     // uniform
+                if (a.accumulate) store64<T, EXACT>(row, a.ld, a.N - n0, acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+                else store64<T, false>(row, a.ld, a.N - n0, acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+                continue;
+            }
+            if (n >= a.N) continue;
+#pragma unroll
+            for (int f = 0; f < NF; ++f) {
+                if (k_wave + f * kFrag + 4 * g >= a.K) continue;              // K comes in multiples of 16
+                T* p = row + r * a.ld + f * kFrag + 4 * g;
+                float v[4] = {acc[i][f][0], acc[i][f][1], acc[i][f][2], acc[i][f][3]};
+                if (a.accumulate) {
+                    float o[4];
+                    load_f32<T, 4>(p, o);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) v[x] += o[x];
+                }
+                store_f32<T, 4>(p, v);
+            }
+        }
+        // Of a whole tile every lane's stores have gone out: as many as are counted.
+        if (u.n_tile + W::BM <= a.N && u.k_tile + W::BN <= a.K) stores[0] = 1;
+        u = unit_at(at += step);
+        if (u.count < 0) break;
+    }
+    wait_loads<0>();                         // nothing lands in LDS after the workgroup
 }
 
-// A workgroup of 4 waves: 128 x 128 of one expert's gradient, a wave 64 x 64 of it.
-template <typename T>
-__global__ __launch_bounds__(256) void wgrad_kernel(Fp8WgradArgs a, int tiles_n, int tiles_k) {
-    constexpr int NF = 4;
-    const uint32_t per = (uint32_t)tiles_n * tiles_k, e = blockIdx.x / per, at = blockIdx.x % per;
-    const int n_tile = at / tiles_k * 128, k_tile = at % tiles_k * 128;
-    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, wave = threadIdx.x >> 6;
-    const int n_wave = n_tile + (wave >> 1) * 64, k_wave = k_tile + (wave & 1) * 64;
-    int first, count;
-    expert_blocks(a, e, &first, &count);
-    f32x4 acc[NF][NF];
-#pragma unroll
-    for (int i = 0; i < NF; ++i)
-#pragma unroll
-        for (int j = 0; j < NF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // x is the first operand: a lane's four results are four neighbouring k
-    const uint8_t *xp[NF], *gp[NF], *xsp[NF], *gsp[NF];
-#pragma unroll
-    for (int i = 0; i < NF; ++i) {
-        const int k = min(k_wave + i * kFrag + r, a.K - 1), n = min(n_wave + i * kFrag + r, a.N - 1);
-        xp[i] = a.x + k * a.ld_t + (int64_t)first * kFp8Block + g * 16;
-        gp[i] = a.g + n * a.ld_t + (int64_t)first * kFp8Block + g * 16;
-        xsp[i] = a.xs + (int64_t)first * a.K + k;
-        gsp[i] = a.gs + (int64_t)first * a.N + n;
-    }
-    for (int b = 0; b < count; ++b) {
-        Frag xv[NF], gv[NF];
-        int xs[NF], gs[NF];
-#pragma unroll
-        for (int i = 0; i < NF; ++i) {
-            xv[i] = Frag{load16(xp[i]), load16(xp[i] + 64)};
-            gv[i] = Frag{load16(gp[i]), load16(gp[i] + 64)};
-            xs[i] = load1(xsp[i]), gs[i] = load1(gsp[i]);
-            xp[i] += kFp8Block, gp[i] += kFp8Block, xsp[i] += a.K, gsp[i] += a.N;
-        }
-        if constexpr (std::is_same<T, float>::value) {
-            Wide xw[NF];
-#pragma unroll
-            for (int j = 0; j < NF; ++j) xw[j] = widen(xv[j], fp8_scale_value(xs[j]));
-#pragma unroll
-            for (int i = 0; i < NF; ++i) {
-                const Wide gw = widen(gv[i], fp8_scale_value(gs[i]));
-#pragma unroll
-                for (int j = 0; j < NF; ++j) acc[i][j] = wide_mfma(xw[j], gw, acc[i][j]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < NF; ++i)
-#pragma unroll
-                for (int j = 0; j < NF; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(words8(xv[j]), words8(gv[i]), acc[i][j], 0, 0,
-                                                                                 0, xs[j], 0, gs[i]);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < NF; ++i) {
-        const int n = n_wave + i * kFrag + r;
-        if (n >= a.N) continue;
-        T* row = (T*)a.dw + ((int64_t)e * a.N + n) * a.ld;
-#pragma unroll
-        for (int j = 0; j < NF; ++j) {
-            const int k = k_wave + j * kFrag + 4 * g;
-            if (k >= a.K) continue;              // K comes in multiples of 16
-            float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-            if (a.accumulate) {
-                float o[4];
-                load_f32<T, 4>(row + k, o);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) v[x] += o[x];
-            }
-            store_f32<T, 4>(row + k, v);
-        }
-    }
+template <typename T, int MT, int NF, int WM, int WN, int STAGES>
+coli_status wgrad(const Fp8WgradArgs& a, hipStream_t stream) {
+    typedef WgradTile<T, MT, NF, WM, WN, STAGES> W;
+    const int64_t NT = (a.N + W::BM - 1) / W::BM, KT = (a.K + W::BN - 1) / W::BN;
+    if (NT * KT > INT32_MAX / a.E) return fail(COLI_EUNSUPPORTED, "fp8_wgrad: more than 2^31 tiles");
+    constexpr int64_t kPerCu = 163840 / sizeof(typename W::Lds);
+    const uint32_t grid = (uint32_t)std::min<int64_t>(kCus * kPerCu, (NT * KT * a.E + kXcds - 1) / kXcds * kXcds);
+    launch(wgrad_kernel<T, MT, NF, WM, WN, STAGES>, dim3(grid), dim3(W::kThreads), 0, stream, a, (int)NT, (int)KT);
+    COLI_CHECK_LAUNCH("fp8_wgrad kernel launch");
+    return COLI_OK;
 }
 
 }  // namespace
 
 coli_status launch_fp8_wgrad(const Fp8WgradArgs& a, int32_t dtype, hipStream_t stream) {
-    const int64_t tn = (a.N + 127) / 128, tk = (a.K + 127) / 128;
-    if (tn * tk * a.E > (int64_t(1) << 32) / 256 - 1) return fail(COLI_EUNSUPPORTED, "fp8_wgrad: more than 2^32 threads");
     return with_elem(dtype, [&](auto e) -> coli_status {
         using T = decltype(e);
-        launch(wgrad_kernel<T>, dim3((uint32_t)(tn * tk * a.E)), dim3(256), 0, stream, a, (int)tn, (int)tk);
-        COLI_CHECK_LAUNCH("fp8_wgrad kernel launch");
-        return COLI_OK;
+        const char* v = getenv("WG");
+        if (v && v[0] == '1') return wgrad<T, 8, 4, 2, 4, 2>(a, stream);
+        if (v && v[0] == '2') return wgrad<T, 4, 4, 4, 2, 2>(a, stream);
+        if (v && v[0] == '3') return wgrad<T, 4, 4, 4, 2, 3>(a, stream);
+        if constexpr (std::is_same<T, float>::value) return wgrad<T, 4, 4, 2, 4, 3>(a, stream);
+        else return wgrad<T, 8, 4, 2, 4, 2>(a, stream);
     });
 }
 

@@ -89,6 +89,74 @@ __device__ __forceinline__ void store32(const Args& a, int m, int n0, int N, boo
     }
 }
 
+// x where a lane's number within 16 is below 8, y of the lane 8 further down where it is not (EVEN); or x of the
+// lane 8 further up where it is below, y where it is not.
+template <bool EVEN>
+__device__ __forceinline__ uint32_t merge_halves(uint32_t x, uint32_t y) {
+    // row_ror:8 into the upper, or the lower, two banks of four lanes
+    if constexpr (EVEN) return (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)y, 0x128, 0xf, 0xc, false);
+    else return (uint32_t)__builtin_amdgcn_update_dpp((int)y, (int)x, 0x128, 0xf, 0x3, false);
+}
+
+// Four fragments of results, columns 0 .. 63 of a row behind `out` (its row 0 and first column), in whole cache lines: of
+// a fragment's 16 rows, a store takes 8 rows by 128 bytes, so that no line is written in parts. A lane holds
+// row lane % 16; rows from `rows` on are left out. (16 stores of 16 rows by 64 bytes a tile: 3.2 GB of f32 took 696 us;
+// by whole lines, LINES.) Two stores for a 16-bit type, four for f32; ADD: to what is there.
+template <typename T, bool ADD>
+__device__ __forceinline__ void store64(T* out, int64_t ld, int rows, const f32x4& v0, const f32x4& v1, const f32x4& v2,
+                                        const f32x4& v3) {
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, row = r & 7;
+    if constexpr (sizeof(T) == 2) {
+        union Words {
+            T v[4];
+            uint32_t w[2];
+        } x[4];
+        const f32x4* v[4] = {&v0, &v1, &v2, &v3};
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[f].v[i] = (T)(*v[f])[i];
+#pragma unroll
+        for (int f = 0; f < 4; f += 2)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) swap_quarters(x[f].w[i], x[f + 1].w[i]);
+        Pack<uint32_t, 4> lo, hi;            // columns 8 g of the first 32, of the second
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t a = x[i / 2].w[i % 2], b = x[2 + i / 2].w[i % 2];
+            lo.v[i] = merge_halves<true>(a, b);
+            hi.v[i] = merge_halves<false>(a, b);
+        }
+        typedef Pack<T, 8> P;
+        T* p = out + row * ld + (r >= 8 ? 32 : 0) + 8 * g;
+        typedef uint32_t V __attribute__((ext_vector_type(4), aligned(2)));
+        if (row < rows) __builtin_nontemporal_store(__builtin_bit_cast(V, lo), reinterpret_cast<V*>(p));
+        if (row + 8 < rows) __builtin_nontemporal_store(__builtin_bit_cast(V, hi), reinterpret_cast<V*>(p + 8 * ld));
+    } else {
+        const f32x4* v[4] = {&v0, &v1, &v2, &v3};
+        T* p = out + row * ld + (r >= 8 ? 16 : 0) + 4 * g;
+#pragma unroll
+        for (int f = 0; f < 4; f += 2) {
+            float lo[4], hi[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t a = __float_as_uint((*v[f])[i]), b = __float_as_uint((*v[f + 1])[i]);
+                lo[i] = __uint_as_float(merge_halves<true>(a, b));
+                hi[i] = __uint_as_float(merge_halves<false>(a, b));
+            }
+            if constexpr (ADD) {
+                float o[4] = {}, q[4] = {};
+                if (row < rows) load_f32<T, 4>(p + 16 * f, o);
+                if (row + 8 < rows) load_f32<T, 4>(p + 16 * f + 8 * ld, q);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) lo[i] += o[i], hi[i] += q[i];
+            }
+            if (row < rows) store_f32_once<T, 4>(p + 16 * f, lo);
+            if (row + 8 < rows) store_f32_once<T, 4>(p + 16 * f + 8 * ld, hi);
+        }
+    }
+}
+
 // Position of 16-byte unit b of row r in an LDS chunk of U units a row: the units
 // of a row are permuted by its number, so that the rows that a load reads at one
 // column fall into different banks.
@@ -112,6 +180,16 @@ template <int N>
 __device__ __forceinline__ void wait_loads() {
     static_assert(N < 64, "vmcnt has 6 bits");
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+// The same with the stores of up to `tiles` (0, 1 or 2) tiles, STORES each, allowed to be in flight besides: they
+// were issued behind the loads that are waited for. (Fewer than were issued only make the wait longer.)
+template <int N, int STORES>
+__device__ __forceinline__ void wait_behind_stores(int tiles) {
+    static_assert(N + STORES < 64, "vmcnt has 6 bits");
+    if (tiles == 0) wait_loads<N>();
+    else if (tiles == 1) wait_loads<N + STORES>();
+    else wait_loads<(N + 2 * STORES < 64 ? N + 2 * STORES : N + STORES)>();
 }
 
 }  // namespace coli
