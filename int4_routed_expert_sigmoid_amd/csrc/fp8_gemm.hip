@@ -329,20 +329,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a
         return Frag{p[row * U + lo], p[row * U + hi]};
     };
     const int ws_row = T::BM + (SWIGLU ? 0 : wn * NF * kFrag / kFp8Block);
-    // Tiles of 4 row fragments have registers for all of them, so that the waves meet, and the next loads go out,
-    // in the middle of a block; otherwise before its last row.
-    constexpr int kRing = MT == 4 ? 4 : 2, kMeet = MT == 4 ? 2 : MT - 1;
+    // The steps of a block, a product each: row by row, and of the last two rows, from step kMeet on, both with one
+    // matrix fragment after the other, so that the next block's can be read one by one meanwhile. The row
+    // fragments take turns in a few registers.
+    constexpr int kMeet = (MT - 2) * NF;
+    auto row_of = [](int n) constexpr { return n < kMeet ? n / NF : MT - 2 + (n - kMeet) % 2; };
+    auto frag_of = [](int n) constexpr { return n < kMeet ? n % NF : (n - kMeet) / 2; };
+    auto ring = [](int i) constexpr { return MT == 4 || i < 2 ? i : i < 4 ? i - 2 : i == 4 ? 2 : i - 5; };   // 0 1 0 1 2 0 1 2
+    constexpr int kRing = MT == 4 ? 4 : 3;
     Frag w[NF], av[kRing];
-    float as[kRing], ws[kW];
-    f32x4 acc[MT][NF], p[NF];
-    float ps[kW] = {};                       // the scale of the products in p
+    float as[kRing], ws[kW], s_last[2 * kW];  // s_last: the scales of the block before, rows MT - 2 and MT - 1
+    f32x4 acc[MT][NF], p[4];
     auto read_scales = [&](int b) {
 #pragma unroll
         for (int x = 0; x < kW; ++x) ws[x] = lds.scale[scales][(ws_row + x) * kGroup + b % kGroup];
     };
     auto read_row = [&](int i, int b) {
-        av[i % kRing] = code(m_lds, i * WM * kFrag);
-        as[i % kRing] = lds.scale[scales][m_lds * kGroup + b % kGroup + i * WM * kFrag * kGroup];
+        av[ring(i)] = code(m_lds, i * WM * kFrag);
+        as[ring(i)] = lds.scale[scales][m_lds * kGroup + b % kGroup + i * WM * kFrag * kGroup];
     };
     // How many tiles' stores may be in flight behind the loads of the block that is waited for next: those of
     // the last STAGES - 1 blocks' units.
@@ -354,26 +358,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a
     for (int f = 0; f < NF; ++f) w[f] = code(n_lds, f * kFrag);
     read_scales(0);
     read_row(0, 0);
-    if constexpr (kRing == 4) read_row(1, 0);
+    if constexpr (MT == 4) read_row(1, 0);
     while (true) {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int f = 0; f < NF; ++f) acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int f = 0; f < NF; ++f) p[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int x = 0; x < 4; ++x) p[x] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int x = 0; x < kW; ++x) ps[x] = 0.f;
+        for (int x = 0; x < 2 * kW; ++x) s_last[x] = 0.f;
 #pragma unroll 1
         for (int c = 0; c < KB; ++c) {
             const int fill = slot, next = c + 1 == KB ? 0 : c + 1;
+            float s[MT][kW];
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const int before = (i + MT - 1) % MT;
-                float s[kW];
-#pragma unroll
-                for (int x = 0; x < kW; ++x) s[x] = as[i % kRing] * ws[x];
-                if (i == kMeet) {
+            for (int n = 0; n < MT * NF; ++n) {
+                const int i = row_of(n), f = frag_of(n);
+                if (n == kMeet) {
                     // The next block and its scales (issued before its codes) have arrived, the codes of the
                     // STAGES - 2 behind it may not have, and this one is read.
                     wait_behind_stores<(STAGES - 2) * T::kLoads, T::kStores>(STAGES == 3 ? stores[0] + stores[1] : stores[0]);
@@ -385,31 +387,39 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a
                     if (next % kGroup == 0) scales = scales == STAGES - 1 ? 0 : scales + 1;
                     load_scales();
                 }
-                if constexpr (kRing == 4) {
-                    if (i == 0) read_row(2, c), read_row(3, c);
-                    if (i == kMeet) read_row(0, next), read_row(1, next);
-                } else {
-                    read_row((i + 1) % MT, i == kMeet ? next : c);
-                }
-                if (i == MT - 1) read_scales(next);
+                if (f == 0) {
 #pragma unroll
-                for (int f = 0; f < NF; ++f) {
-                    add_scaled(acc[before][f], p[f], ps[SWIGLU ? f % 2 : 0]);
-                    p[f] = block_sum<EXACT>(w[f], av[i % kRing]);
+                    for (int x = 0; x < kW; ++x) s[i][x] = as[ring(i)] * ws[x];
+                }
+                if (n < kMeet && f == 0) {               // rows of this block
+                    if (MT == 4 && i == 0) read_row(2, c), read_row(3, c);
+                    if (MT == 8) read_row(i + 1, c);
+                    if (MT == 8 && i == MT - 3) read_row(MT - 1, c);
+                }
+                if (n == kMeet + 1) read_row(0, next);   // of the next
+                if (n == kMeet + 3 && MT == 4) read_row(1, next);
+                // the product of four steps before into its sum
+                const int m = (n + MT * NF - 4) % (MT * NF), mi = row_of(m), mf = frag_of(m), mx = SWIGLU ? mf % 2 : 0;
+                add_scaled(acc[mi][mf], p[n % 4], n < 4 ? s_last[(mi - (MT - 2)) * kW + mx] : s[mi][mx]);
+                p[n % 4] = block_sum<EXACT>(w[f], av[ring(i)]);
+                asm volatile("" : "+v"(acc[mi][mf])::"memory");
+                if (n >= kMeet) {
                     if (i == MT - 1) w[f] = code(n_lds, f * kFrag);
-                    if (i == kMeet) {
+                    const int q = n - kMeet;
 #pragma unroll
-                        for (int x = f * T::kLoads / NF; x < (f + 1) * T::kLoads / NF; ++x) load_codes(fill, x);
-                    }
+                    for (int x = q * T::kLoads / 8; x < (q + 1) * T::kLoads / 8; ++x) load_codes(fill, x);
                 }
-#pragma unroll
-                for (int x = 0; x < kW; ++x) ps[x] = s[x];
-                hold(acc[before]);
+                if (n == kMeet + 2) read_scales(next);   // (those of this block's last rows are multiplied)
             }
+#pragma unroll
+            for (int x = 0; x < 2 * kW; ++x) s_last[x] = s[MT - 2 + x / kW][x % kW];
             advance();
         }
 #pragma unroll
-        for (int f = 0; f < NF; ++f) add_scaled(acc[MT - 1][f], p[f], ps[SWIGLU ? f % 2 : 0]);
+        for (int n = MT * NF - 4; n < MT * NF; ++n) {
+            const int i = row_of(n), f = frag_of(n);
+            add_scaled(acc[i][f], p[n % 4], s_last[(i - (MT - 2)) * kW + (SWIGLU ? f % 2 : 0)]);
+        }
         // outputs
         const int n_wave = u.nt * T::kCols + wn * (SWIGLU ? NF / 2 : NF) * kFrag;
 #pragma unroll
