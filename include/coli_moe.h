@@ -579,19 +579,20 @@ COLI_API coli_status coli_quantize_fp8_matrix(const void* d_x, int32_t dtype, in
 
 /* Rows d_x [rows][cols] sorted by expert (d_offsets [E + 1] as in coli_fp8_matmul; NULL: E is 1)
  * for coli_fp8_wgrad: quantised over 128 of an expert's rows by one column, and laid out by columns.
- * The experts' rows follow each other in d_qt [cols][ld_t], each expert's beginning at a multiple
- * of 128, with codes 0 behind its last; d_st [ld_t / 128][cols] holds the scales' exponents, code c
- * for 2^(c - 127), 255 for NaN. ld_t, a multiple of 128, is at least coli_fp8_columns_ld's. What lies
- * behind the last expert's rows is left as it is. d_q, d_s (nullable, together): the same rows as
- * coli_quantize_fp8 gives them, in the same pass (rows outside the offsets are left as they are). */
+ * The blocks of 128 rows follow each other, each expert's beginning with its first row: d_qt
+ * [blocks][cols][128] holds a block's codes column by column, 0 behind an expert's last row, and d_st
+ * [blocks][cols] the scales' exponents, code c for 2^(c - 127), 255 for NaN. blocks is at least
+ * coli_fp8_column_blocks'; those behind the last expert's are left as they are. d_q, d_s (nullable,
+ * together): the same rows as coli_quantize_fp8 gives them, in the same pass (rows outside the
+ * offsets are left as they are). */
 COLI_API coli_status coli_quantize_fp8_columns(const void* d_x, int32_t dtype, int32_t rows, int32_t cols,
                                                int64_t ld, const int32_t* d_offsets, int32_t E,
-                                               uint8_t* d_qt, int64_t ld_t, uint8_t* d_st, uint8_t* d_q,
+                                               uint8_t* d_qt, int64_t blocks, uint8_t* d_st, uint8_t* d_q,
                                                float* d_s, void* stream);
 
-/* The least ld_t for `rows` rows over E experts: 128 * floor((rows + 127 min(E, rows)) / 128).
+/* The blocks that `rows` rows over E experts may need: floor((rows + 127 min(E, rows)) / 128).
  * Host-only arithmetic. */
-COLI_API coli_status coli_fp8_columns_ld(int32_t rows, int32_t E, int64_t* ld_t);
+COLI_API coli_status coli_fp8_column_blocks(int32_t rows, int32_t E, int64_t* blocks);
 
 /* The values of d_q [rows][cols] with scales for 128 columns of `block_rows` rows (1 or 128) as
  * d_x [rows][cols] (type dtype, row stride ld): one f32 product, rounded to the type. */
@@ -627,10 +628,10 @@ COLI_API coli_status coli_fp8_swiglu(const uint8_t* d_a, const float* d_as, int3
 
 /* Every expert's matrix gradient: d_dw[e][n][k] = sum over the expert's rows r of g[r][n] x[r][k] (0
  * without rows), for g [rows][N] and x [rows][K] (N, K multiples of 16) as coli_quantize_fp8_columns
- * lays them out with the same rows, d_offsets, E and ld_t. d_dw [E][N][ld] of type dtype, ld >= K;
+ * lays them out with the same rows, d_offsets, E and blocks. d_dw [E][N][ld] of type dtype, ld >= K;
  * accumulate: the sums are added to what it holds. Sums as the products'. */
 COLI_API coli_status coli_fp8_wgrad(const uint8_t* d_gt, const uint8_t* d_gs, const uint8_t* d_xt,
-                                    const uint8_t* d_xs, int64_t ld_t, int32_t rows,
+                                    const uint8_t* d_xs, int64_t blocks, int32_t rows,
                                     const int32_t* d_offsets, int32_t E, int32_t N, int32_t K,
                                     int32_t accumulate, void* d_dw, int32_t dtype, int64_t ld,
                                     void* stream);

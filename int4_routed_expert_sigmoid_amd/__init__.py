@@ -42,7 +42,7 @@ EXPORTED = [
     "coli_moe_union_inverse", "coli_moe_dispatch", "coli_moe_dispatch_mxfp4",
     "coli_moe_dispatch_bwd", "coli_moe_combine", "coli_moe_combine_bwd",
     "coli_moe_route_groups", "coli_moe_route_groups_bwd",
-    "coli_quantize_fp8", "coli_quantize_fp8_matrix", "coli_quantize_fp8_columns", "coli_fp8_columns_ld",
+    "coli_quantize_fp8", "coli_quantize_fp8_matrix", "coli_quantize_fp8_columns", "coli_fp8_column_blocks",
     "coli_dequantize_fp8", "coli_fp8_blob_layout", "coli_fp8_matmul", "coli_fp8_swiglu", "coli_fp8_wgrad",
     "coli_debug_fp8_kernel", "coli_moe_dispatch_fp8",
 ]
@@ -161,7 +161,7 @@ def lib():
             L.coli_quantize_fp8_matrix.argtypes = [vp, i32, i32, i64, i64, i64, i64, vp, i64, vp, i64, vp,
                                                    i64, vp, i64, vp]
             L.coli_quantize_fp8_columns.argtypes = [vp, i32, i32, i32, i64, vp, i32, vp, i64, vp, vp, vp, vp]
-            L.coli_fp8_columns_ld.argtypes = [i32, i32, P(i64)]
+            L.coli_fp8_column_blocks.argtypes = [i32, i32, P(i64)]
             L.coli_dequantize_fp8.argtypes = [vp, vp, i64, i64, i32, vp, i32, i64, vp]
             L.coli_fp8_blob_layout.argtypes = [P(Shape), P(sz), P(sz)]
             L.coli_fp8_matmul.argtypes = [vp, vp, i32, i32, vp, i32, vp, sz, sz, i32, vp, i32, i64, vp]
@@ -1010,17 +1010,18 @@ def quantize_fp8_matrix(x, transposed=False, q=None, s=None, qt=None, st=None, s
     return tuple(t[0] if flat else t for t in tensors[1:])
 
 
-def fp8_columns_ld(rows: int, E: int) -> int:
-    """The columns (128 for each 128 rows of an expert) that quantize_fp8_columns' codes need."""
+def fp8_column_blocks(rows: int, E: int) -> int:
+    """The blocks of 128 rows of an expert that quantize_fp8_columns may need."""
     out = ctypes.c_int64()
-    _check(lib().coli_fp8_columns_ld(rows, E, ctypes.byref(out)))
+    _check(lib().coli_fp8_column_blocks(rows, E, ctypes.byref(out)))
     return out.value
 
 
 def quantize_fp8_columns(x, offsets=None, rows=False, qt=None, st=None, q=None, s=None, stream=None):
-    """Rows x [rows][cols] sorted by expert -> (codes uint8 [cols][P], scale exponents uint8 [P / 128][cols])
-    over 128 of an expert's rows by one column, for fp8_wgrad; P is fp8_columns_ld's (or that of a given
-    qt). `rows` (or q, s given): also quantize_fp8's codes and scales, from the same pass."""
+    """Rows x [rows][cols] sorted by expert -> (codes uint8 [blocks][cols][128], scale exponents uint8
+    [blocks][cols]) over 128 of an expert's rows by one column, for fp8_wgrad; as many blocks as
+    fp8_column_blocks says (or a given qt has). `rows` (or q, s given): also quantize_fp8's codes and
+    scales, from the same pass."""
     import torch
     code, ld = _rows(x, "x")
     n, cols = x.shape
@@ -1028,35 +1029,34 @@ def quantize_fp8_columns(x, offsets=None, rows=False, qt=None, st=None, q=None, 
     E = 1 if offsets is None else offsets.numel() - 1
     if max(n, cols, E) >= 2 ** 31 or E < 1:
         raise ValueError(f"rows {n}, columns {cols} and experts {E} must be below 2^31, experts at least 1")
-    P = fp8_columns_ld(n, E) if qt is None else qt.shape[-1]
+    blocks = fp8_column_blocks(n, E) if qt is None else qt.shape[0]
     if qt is None:
-        qt = _new(x, (cols, P), torch.uint8, stream)
+        qt = _new(x, (blocks, cols, 128), torch.uint8, stream)
     if st is None:
-        st = _new(x, (P // 128, cols), torch.uint8, stream)
+        st = _new(x, (blocks, cols), torch.uint8, stream)
     _fp8_columns(qt, st, "quantize_fp8_columns", cols)
     if rows or q is not None or s is not None:
         q, s = _fp8_out(q, s, n, cols, x, "quantize_fp8_columns", stream)
     _enqueue((x, offsets, qt, st, q, s), stream, "coli_quantize_fp8_columns", x.data_ptr(), code, n, cols, ld,
-             None if offsets is None else offsets.data_ptr(), E, qt.data_ptr(), P, st.data_ptr(),
+             None if offsets is None else offsets.data_ptr(), E, qt.data_ptr(), blocks, st.data_ptr(),
              None if q is None else q.data_ptr(), None if s is None else s.data_ptr())
     return (qt, st) if q is None else (qt, st, q, s)
 
 
-def _rows_of_ld(P, E):
-    """The most rows over E experts whose columns fit P."""
-    many = P + 127 - 127 * E
-    return many if many >= E else min(P // 128, E)
+def _rows_of_blocks(blocks, E):
+    """The most rows over E experts that fit the blocks."""
+    many = 128 * blocks + 127 - 127 * E
+    return many if many >= E else min(blocks, E)
 
 
 def _fp8_columns(qt, st, name, cols=None):
-    """(cols, P) of columns: codes uint8 [cols][P], scale exponents uint8 [P / 128][cols]."""
+    """(blocks, cols) of columns: codes uint8 [blocks][cols][128], scale exponents uint8 [blocks][cols]."""
     import torch
     _need(qt, torch.uint8, f"{name} codes")
     _need(st, torch.uint8, f"{name} scales")
-    if qt.dim() != 2 or qt.shape[1] % 128 or tuple(st.shape) != (qt.shape[1] // 128, qt.shape[0]) or \
-            cols not in (None, qt.shape[0]):
+    if qt.dim() != 3 or qt.shape[2] != 128 or tuple(st.shape) != tuple(qt.shape[:2]) or cols not in (None, qt.shape[1]):
         raise ValueError(f"{name}: codes {tuple(qt.shape)} and scales {tuple(st.shape)} do not match")
-    return tuple(qt.shape)
+    return tuple(qt.shape[:2])
 
 
 def dequantize_fp8(q, s, dtype=None, out=None, stream=None):
@@ -1147,19 +1147,19 @@ def fp8_swiglu(a, a_s, table, inter, q_off=0, s_off=0, up_q_off=None, up_s_off=N
 def fp8_wgrad(gt, gt_s, xt, xt_s, offsets=None, rows=None, dtype=None, out=None, accumulate=False, stream=None):
     """fp8_matmul's gradient to its matrices, out[e] = sum over the expert's rows of grad[r] x[r]^T, [E][n][K]
     in `dtype` (default float32), from quantize_fp8_columns of the output's gradient and of the rows, with
-    the same offsets. rows (needed only without offsets, for columns with room for more): how many rows
-    those had. accumulate: added to what `out` holds."""
+    the same offsets. rows (needed only without offsets, where there are more blocks than it takes): how
+    many rows those had. accumulate: added to what `out` holds."""
     import torch
-    n, P = _fp8_columns(gt, gt_s, "gt")
-    K, Px = _fp8_columns(xt, xt_s, "xt")
-    if P != Px:
-        raise ValueError(f"gt has {P} columns, xt {Px}")
+    blocks, n = _fp8_columns(gt, gt_s, "gt")
+    x_blocks, K = _fp8_columns(xt, xt_s, "xt")
+    if blocks != x_blocks:
+        raise ValueError(f"gt has {blocks} blocks, xt {x_blocks}")
     _need(offsets, torch.int32, "offsets")
     E = 1 if offsets is None else offsets.numel() - 1
     if E < 1:
         raise ValueError("offsets must hold at least two values")
     if rows is None:
-        rows = _rows_of_ld(P, E)
+        rows = _rows_of_blocks(blocks, E)
     if max(n, K, rows, E) >= 2 ** 31 or rows < 0:
         raise ValueError("rows, columns and experts must be below 2^31")
     if out is None:
@@ -1172,7 +1172,7 @@ def fp8_wgrad(gt, gt_s, xt, xt_s, offsets=None, rows=None, dtype=None, out=None,
         raise ValueError("out's matrices must follow each other without gaps")
     code, ld = _rows(out.view(E * n, K) if out.is_contiguous() else out[0], "out", n, K, dtype)
     _enqueue((gt, gt_s, xt, xt_s, offsets, out), stream, "coli_fp8_wgrad", gt.data_ptr(), gt_s.data_ptr(),
-             xt.data_ptr(), xt_s.data_ptr(), P, rows, None if offsets is None else offsets.data_ptr(), E, n, K,
+             xt.data_ptr(), xt_s.data_ptr(), blocks, rows, None if offsets is None else offsets.data_ptr(), E, n, K,
              int(accumulate), out.data_ptr(), code, ld)
     return out
 

@@ -676,40 +676,38 @@ coli_status coli_quantize_fp8_matrix(const void* d_x, int32_t dtype, int32_t cou
     COLI_GUARD_END
 }
 
-static int64_t fp8_columns_ld(int64_t rows, int64_t E) {
-    return (rows + (kFp8Block - 1) * std::min(E, rows)) / kFp8Block * kFp8Block;
+static int64_t fp8_column_blocks(int64_t rows, int64_t E) {
+    return (rows + (kFp8Block - 1) * std::min(E, rows)) / kFp8Block;
 }
 
-coli_status coli_fp8_columns_ld(int32_t rows, int32_t E, int64_t* ld_t) {
+coli_status coli_fp8_column_blocks(int32_t rows, int32_t E, int64_t* blocks) {
     COLI_GUARD_BEGIN
-    if (rows < 0 || E < 1 || !ld_t) return fail(COLI_EINVAL, "fp8_columns_ld: rows >= 0, E at least 1");
-    *ld_t = fp8_columns_ld(rows, E);
+    if (rows < 0 || E < 1 || !blocks) return fail(COLI_EINVAL, "fp8_column_blocks: rows >= 0, E at least 1");
+    *blocks = fp8_column_blocks(rows, E);
     return COLI_OK;
     COLI_GUARD_END
 }
 
-static coli_status check_fp8_columns(const std::string& w, int32_t rows, const int32_t* d_offsets, int32_t E, int64_t ld_t) {
+static coli_status check_fp8_columns(const std::string& w, int32_t rows, const int32_t* d_offsets, int32_t E, int64_t blocks) {
     if (rows < 0 || E < 1) return fail(COLI_EINVAL, w + ": rows >= 0, E at least 1");
     if (E > 1024) return fail(COLI_EUNSUPPORTED, w + ": E must be at most 1024");
     if (!d_offsets && E != 1) return fail(COLI_EINVAL, w + ": without offsets E must be 1");
-    if (ld_t % kFp8Block || ld_t < fp8_columns_ld(rows, E))
-        return fail(COLI_EINVAL, w + ": ld_t must be a multiple of 128 and at least coli_fp8_columns_ld's");
-    if (ld_t > INT32_MAX) return fail(COLI_EUNSUPPORTED, w + ": ld_t must be below 2^31");
+    if (blocks < fp8_column_blocks(rows, E)) return fail(COLI_EINVAL, w + ": fewer blocks than coli_fp8_column_blocks says");
+    if (blocks >= (1 << 24)) return fail(COLI_EUNSUPPORTED, w + ": blocks must be below 2^24");
     return COLI_OK;
 }
 
 coli_status coli_quantize_fp8_columns(const void* d_x, int32_t dtype, int32_t rows, int32_t cols, int64_t ld,
-                                      const int32_t* d_offsets, int32_t E, uint8_t* d_qt, int64_t ld_t,
-                                      uint8_t* d_st, uint8_t* d_q, float* d_s, void* stream) {
+                                      const int32_t* d_offsets, int32_t E, uint8_t* d_qt, int64_t blocks, uint8_t* d_st, uint8_t* d_q, float* d_s, void* stream) {
     COLI_GUARD_BEGIN
     const char* w = "quantize_fp8_columns";
     coli_status st = check_fp8_rows(w, rows, cols, dtype, ld);
-    if (st || (st = check_fp8_columns(w, rows, d_offsets, E, ld_t)) || rows == 0) return st;
+    if (st || (st = check_fp8_columns(w, rows, d_offsets, E, blocks)) || rows == 0) return st;
     if (!d_x || !d_qt || !d_st) return fail(COLI_EINVAL, "quantize_fp8_columns: NULL pointer");
     if (!aligned16(d_qt)) return fail(COLI_EINVAL, "quantize_fp8_columns: codes must be 16-byte aligned");
     if ((d_q || d_s) && (st = check_fp8_pair(w, d_q, d_s))) return st;
     Fp8ColumnArgs a;
-    a.x = d_x; a.ld = ld; a.ld_t = ld_t; a.offsets = d_offsets;
+    a.x = d_x; a.ld = ld; a.blocks = (int32_t)blocks; a.offsets = d_offsets;
     a.qt = d_qt; a.st = d_st; a.q = d_q; a.s = d_s;
     a.rows = rows; a.cols = cols; a.E = E;
     return launch_quantize_fp8_columns(a, dtype, (hipStream_t)stream);
@@ -800,10 +798,10 @@ coli_status coli_fp8_swiglu(const uint8_t* d_a, const float* d_as, int32_t rows,
 }
 
 coli_status coli_fp8_wgrad(const uint8_t* d_gt, const uint8_t* d_gs, const uint8_t* d_xt, const uint8_t* d_xs,
-                           int64_t ld_t, int32_t rows, const int32_t* d_offsets, int32_t E, int32_t N, int32_t K,
+                           int64_t blocks, int32_t rows, const int32_t* d_offsets, int32_t E, int32_t N, int32_t K,
                            int32_t accumulate, void* d_dw, int32_t dtype, int64_t ld, void* stream) {
     COLI_GUARD_BEGIN
-    coli_status st = check_fp8_columns("fp8_wgrad", rows, d_offsets, E, ld_t);
+    coli_status st = check_fp8_columns("fp8_wgrad", rows, d_offsets, E, blocks);
     if (st) return st;
     if (N <= 0 || K <= 0 || N % kFp8Unit || K % kFp8Unit)
         return fail(COLI_EINVAL, "fp8_wgrad: N and K must be positive multiples of 16");
@@ -816,7 +814,7 @@ coli_status coli_fp8_wgrad(const uint8_t* d_gt, const uint8_t* d_gs, const uint8
     if (rows == 0 && accumulate) return COLI_OK;
     Fp8WgradArgs a;
     a.g = d_gt; a.gs = d_gs; a.x = d_xt; a.xs = d_xs; a.offsets = d_offsets; a.dw = d_dw;
-    a.ld_t = ld_t; a.ld = ld; a.rows = rows; a.E = E; a.N = N; a.K = K; a.accumulate = accumulate != 0;
+    a.blocks = (int32_t)blocks; a.ld = ld; a.rows = rows; a.E = E; a.N = N; a.K = K; a.accumulate = accumulate != 0;
     return launch_fp8_wgrad(a, dtype, (hipStream_t)stream);
     COLI_GUARD_END
 }

@@ -121,17 +121,16 @@ struct Fp8MatrixArgs {
 };
 coli_status launch_quantize_fp8_matrix(const Fp8MatrixArgs& a, int32_t dtype, int32_t count, hipStream_t stream);
 
-// Rows sorted by expert into codes qt [cols][ld_t] of 128 rows of an expert by one column
-// (each expert's from a multiple of 128 on, zeros behind its last row) with the scales'
-// exponent codes st [ld_t / 128][cols]; q, s (nullptr: not wanted): the rows as
-// launch_quantize_fp8 quantises them.
+// Rows sorted by expert into codes qt [blocks][cols][128] of 128 rows of an expert by one column
+// (zeros behind its last row) with the scales' exponent codes st [blocks][cols]; q, s (nullptr:
+// not wanted): the rows as launch_quantize_fp8 quantises them.
 struct Fp8ColumnArgs {
     const void* x;
-    int64_t ld, ld_t;
+    int64_t ld;
     const int32_t* offsets;
     uint8_t *qt, *st, *q;
     float* s;
-    int32_t rows, cols, E;
+    int32_t rows, cols, E, blocks;
 };
 coli_status launch_quantize_fp8_columns(const Fp8ColumnArgs& a, int32_t dtype, hipStream_t stream);
 
@@ -160,12 +159,12 @@ coli_status launch_fp8_gemm(const Fp8GemmArgs& a, bool swiglu, int32_t dtype, hi
 
 // dw[e][n][k] = sum over the expert's rows (+ dw[e][n][k]); see fp8_wgrad.hip.
 struct Fp8WgradArgs {
-    const uint8_t *g, *gs;       // [N][ld_t], [ld_t / 128][N]
-    const uint8_t *x, *xs;       // [K][ld_t], [ld_t / 128][K]
+    const uint8_t *g, *gs;       // [blocks][N][128], [blocks][N]
+    const uint8_t *x, *xs;       // [blocks][K][128], [blocks][K]
     const int32_t* offsets;
     void* dw;                    // [E][N][ld]
-    int64_t ld_t, ld;
-    int32_t rows, E, N, K;
+    int64_t ld;
+    int32_t blocks, rows, E, N, K;
     bool accumulate;
 };
 coli_status launch_fp8_wgrad(const Fp8WgradArgs& a, int32_t dtype, hipStream_t stream);

@@ -372,6 +372,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a
         for (int c = 0; c < KB; ++c) {
             const int fill = slot, next = c + 1 == KB ? 0 : c + 1;
             float s[MT][kW];
+            Wide ww[EXACT ? NF : 1], aw[EXACT ? 2 : 1];
+            if constexpr (EXACT) {
+#pragma unroll
+                for (int f = 0; f < NF; ++f) ww[f] = widen(w[f], 1.f);
+            }
+            // four steps by bf16 in turn, as the four instructions of one wait for each other
+            auto wide_steps = [&](int n) {
+                if (n <= kMeet) aw[0] = widen(av[ring(row_of(n))], 1.f);
+                if (n == kMeet) aw[EXACT] = widen(av[ring(MT - 1)], 1.f);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) p[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        p[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ww[EXACT ? frag_of(n + x) : 0].v[k],
+                                                                       aw[EXACT && row_of(n + x) == MT - 1].v[k], p[x], 0, 0, 0);
+            };
 #pragma unroll
             for (int n = 0; n < MT * NF; ++n) {
                 const int i = row_of(n), f = frag_of(n);
@@ -401,7 +419,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a
                 // the product of four steps before into its sum
                 const int m = (n + MT * NF - 4) % (MT * NF), mi = row_of(m), mf = frag_of(m), mx = SWIGLU ? mf % 2 : 0;
                 add_scaled(acc[mi][mf], p[n % 4], n < 4 ? s_last[(mi - (MT - 2)) * kW + mx] : s[mi][mx]);
-                p[n % 4] = block_sum<EXACT>(w[f], av[ring(i)]);
+                if constexpr (!EXACT) p[n % 4] = block_sum<false>(w[f], av[ring(i)]);
+                else if (n % 4 == 3) wide_steps(n - 3);
                 asm volatile("" : "+v"(acc[mi][mf])::"memory");
                 if (n >= kMeet) {
                     if (i == MT - 1) w[f] = code(n_lds, f * kFrag);

@@ -336,7 +336,7 @@ __global__ __launch_bounds__(kThreads) void quantize_columns_kernel(Fp8ColumnArg
         }
     }
     __syncthreads();
-    store_columns(lds, a.qt + (int64_t)tc * kFp8Block * a.ld_t + (int64_t)b * kFp8Block, a.ld_t, kFp8Block, cols);
+    store_columns(lds, a.qt + ((int64_t)b * a.cols + tc * kFp8Block) * kFp8Block, kFp8Block, kFp8Block, cols);
 }
 
 coli_status check_grid(int64_t grid, const char* what) {
@@ -412,9 +412,9 @@ coli_status launch_quantize_fp8_matrix(const Fp8MatrixArgs& a, int32_t dtype, in
 
 coli_status launch_quantize_fp8_columns(const Fp8ColumnArgs& a, int32_t dtype, hipStream_t stream) {
     if (a.rows == 0) return COLI_OK;
-    const int64_t tc = fp8_blocks(a.cols), blocks = a.ld_t / kFp8Block;
+    const int64_t tc = fp8_blocks(a.cols);
     const int64_t most = a.offsets ? (a.rows + (int64_t)(kFp8Block - 1) * std::min(a.E, a.rows)) / kFp8Block : fp8_blocks(a.rows);
-    const int64_t grid = tc * std::min(blocks, most);
+    const int64_t grid = tc * std::min<int64_t>(a.blocks, most);
     if (coli_status st = check_grid(grid, "quantize_fp8_columns")) return st;
     return with_elem(dtype, [&](auto e) -> coli_status {
         using T = decltype(e);

@@ -27,13 +27,15 @@ struct WgradTile {
     static_assert(STAGES == 2 || STAGES == 3, "the stores that a wait may leave in flight");
     static_assert(BM * U % kThreads == 0 && BN * U % kThreads == 0, "whole loads for every wave");
     static_assert(NF == 4, "a wave's columns are one store64");
-    static_assert(BM <= 256 && BN <= 256 && MT % 4 == 0, "a wave loads 256 scales; the ring of fragments");
+    static_assert(BM <= 256 && BN <= 256 && (MT == 4 || MT == 8), "a wave loads 256 scales; the ring of fragments");
     struct Lds {
         u32x4 code[STAGES][(BM + BN) * U];                    // g's columns, then x's
         uint32_t scale[STAGES][2][64];                        // 256 bytes of each
         uint32_t first[kMaxExperts];                          // first block of every expert
     };
 };
+
+constexpr uint32_t kTall = 2;
 
 struct WgradUnit {
     int e, n_tile, k_tile, first, count;     // count -1: no unit
@@ -49,8 +51,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(Fp8WgradArgs a, 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wn = wave % WN, wm = wave / WN;
 
     const RowGroups groups = {a.offsets, nullptr, a.rows, a.E};
-    const int all = (int)(a.ld_t / kFp8Block);
-    const int blocks = min((int)scan_units<kFp8Block, W::kThreads>(groups, 1, lds.first, lds.scale[0][0]), all);
+    const int blocks = min((int)scan_units<kFp8Block, W::kThreads>(groups, 1, lds.first, lds.scale[0][0]), a.blocks);
     const uint32_t per_expert = (uint32_t)NT * KT, total = per_expert * a.E, per = (total + kXcds - 1) / kXcds;
     const uint32_t xcd = blockIdx.x % kXcds, step = gridDim.x / kXcds;
     auto unit_at = [&](uint32_t x) {
@@ -59,11 +60,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(Fp8WgradArgs a, 
         if (x >= per || w >= total) return u;
         u.e = w / per_expert;
         const uint32_t rest = w - u.e * per_expert;
-        // blocks of kBlockM tiles of n by all of k, n first
-        const uint32_t block = rest / (kBlockM * KT), in = rest - block * kBlockM * KT;
-        const uint32_t tall = min(kBlockM, NT - block * kBlockM);
+        // blocks of kTall tiles of n by all of k, n first: neighbouring units write neighbouring columns
+        const uint32_t block = rest / (kTall * KT), in = rest - block * kTall * KT;
+        const uint32_t tall = min(kTall, NT - block * kTall);
         u.k_tile = in / tall * W::BN;
-        u.n_tile = (block * kBlockM + in % tall) * W::BM;
+        u.n_tile = (block * kTall + in % tall) * W::BM;
         // (offsets that are not ascending may count more blocks than there are)
         u.first = min(__builtin_amdgcn_readfirstlane((int)lds.first[u.e]), blocks);
         u.count = (u.e + 1 < a.E ? min(__builtin_amdgcn_readfirstlane((int)lds.first[min(u.e + 1, a.E - 1)]), blocks) : blocks) - u.first;
@@ -76,13 +77,17 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(Fp8WgradArgs a, 
     // the block that is loaded next
     uint32_t load_at = at;
     const uint8_t *g_base = nullptr, *x_base = nullptr, *scale_base = nullptr;
-    int g_last = 0, x_last = 0, lc = 0, load_count = 0;
+    int lc = 0, load_count = 0;
+    const uint32_t unit16 = ((lane & 7) ^ (lane >> 3)) * 16, lane_off = (wave * 8 + (lane >> 3)) * kFp8Block + unit16;
+    uint32_t g_max = 0, x_max = 0;           // a lane's place in the last column of each
     bool loading = true;
     uint32_t scale_step = 0;
     auto set_unit = [&](const WgradUnit& v) {
-        g_last = a.N - 1 - v.n_tile, x_last = a.K - 1 - v.k_tile;
-        g_base = a.g + (int64_t)v.n_tile * a.ld_t + (int64_t)v.first * kFp8Block;
-        x_base = a.x + (int64_t)v.k_tile * a.ld_t + (int64_t)v.first * kFp8Block;
+        const int g_last = a.N - 1 - v.n_tile, x_last = a.K - 1 - v.k_tile;
+        g_max = min(g_last, W::BM) * kFp8Block + unit16;
+        x_max = min(x_last, W::BN) * kFp8Block + unit16;
+        g_base = a.g + ((int64_t)v.first * a.N + v.n_tile) * kFp8Block;
+        x_base = a.x + ((int64_t)v.first * a.K + v.k_tile) * kFp8Block;
         // wave 0: g's scales, the others: x's; four a lane
         scale_base = wave == 0 ? a.gs + (int64_t)v.first * a.N + v.n_tile + min(lane * 4, g_last - 3)
                                : a.xs + (int64_t)v.first * a.K + v.k_tile + min(lane * 4, x_last - 3);
@@ -95,15 +100,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(Fp8WgradArgs a, 
         loading = v.count > 0;
         if (loading) set_unit(v);
     };
-    const int unit16 = ((lane & 7) ^ (lane >> 3)) * 16;
-    // Load i of this wave: 8 columns into a slot, lane l column l / 8, position l % 8. Behind the last unit the
-    // same number of loads goes out, so that the counts hold.
+    // Load i of this wave: 8 columns into a slot, lane l column l / 8, position l % 8, kStep columns below the one
+    // before. Behind the last unit the same number of loads goes out, so that the counts hold.
     auto load_codes = [&](int slot, int i) {
         const bool of_g = i < W::kARows;
-        const int x = (of_g ? i : i - W::kARows) * W::kWaves + wave;
-        const int row = min(x * 8 + (lane >> 3), of_g ? g_last : x_last);
-        const uint8_t* p = (of_g ? g_base : x_base) + row * a.ld_t + (lc * kFp8Block + unit16);
-        load_to_lds(loading ? p : (const uint8_t*)&kZeroUnit, lds.code[slot] + (of_g ? x : W::BM / 8 + x) * 64);
+        const int j = of_g ? i : i - W::kARows;
+        const uint32_t off = min(lane_off + j * 8 * W::kWaves * kFp8Block, of_g ? g_max : x_max);   // (behind the last column: the last)
+        const uint8_t* p = (of_g ? g_base + (int64_t)lc * a.N * kFp8Block : x_base + (int64_t)lc * a.K * kFp8Block) + off;
+        load_to_lds(loading ? p : (const uint8_t*)&kZeroUnit, lds.code[slot] + ((of_g ? 0 : W::BM / 8) + j * W::kWaves + wave) * 64);
     };
     auto load_scales = [&](int slot) {
         load4_to_lds(loading ? scale_base + (int64_t)lc * scale_step : (const uint8_t*)&kZeroUnit, lds.scale[slot][min(wave, 1)]);
@@ -123,26 +127,34 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(Fp8WgradArgs a, 
         advance();
     }
 
+    // fragments: columns 16 apart have the same place in their unit's permutation
     const int m_lds = wm * kFrag + r, n_lds = wn * NF * kFrag + r;
-    auto code = [&](int slot, int row) {
-        return Frag{lds.code[slot][lds_unit<U>(row, g)], lds.code[slot][lds_unit<U>(row, g + 4)]};
-    };
-    auto scale = [&](int slot, int which, int row) { return (int)((const uint8_t*)lds.scale[slot][which])[row]; };
-    typedef typename std::conditional<EXACT, Wide, Frag>::type Operand;
-    Frag w[NF], av[4];
-    int ws[NF], as[4];
-    f32x4 acc[MT][NF];
+    const int lo = g ^ (r & 7), hi = (g + 4) ^ (r & 7);
     int slot = 0;                            // of the block that is multiplied
+    auto code = [&](int row, int below) {
+        const u32x4* p = lds.code[slot] + below * U;
+        return Frag{p[row * U + lo], p[row * U + hi]};
+    };
+    auto scale = [&](int which, int row) { return (int)((const uint8_t*)lds.scale[slot][which])[row]; };
+    // The steps of a block as in fp8_gemm.hip: row by row, the last two rows, from step kMeet on, together.
+    constexpr int kMeet = (MT - 2) * NF;
+    auto row_of = [](int n) constexpr { return n < kMeet ? n / NF : MT - 2 + (n - kMeet) % 2; };
+    auto frag_of = [](int n) constexpr { return n < kMeet ? n % NF : (n - kMeet) / 2; };
+    auto ring = [](int i) constexpr { return MT == 4 || i < 2 ? i : i < 4 ? i - 2 : i == 4 ? 2 : i - 5; };   // 0 1 0 1 2 0 1 2
+    constexpr int kRing = MT == 4 ? 4 : 3;
+    Frag w[NF], av[kRing];
+    int ws[NF], as[kRing];
+    f32x4 acc[MT][NF];
     // How many tiles' stores may be in flight behind the loads of the block that is waited for next: those
     // of the last STAGES - 1 blocks' units (of units without blocks, whose stores follow each other, one).
     int stores[2] = {0, 0};
     auto read_x = [&](int f) {
-        w[f] = code(slot, W::BM + n_lds + f * kFrag);
-        ws[f] = scale(slot, 1, n_lds + f * kFrag);
+        w[f] = code(n_lds, W::BM + f * kFrag);
+        ws[f] = scale(1, n_lds + f * kFrag);
     };
     auto read_g = [&](int i) {
-        av[i % 4] = code(slot, m_lds + i * WM * kFrag);
-        as[i % 4] = scale(slot, 0, m_lds + i * WM * kFrag);
+        av[ring(i)] = code(m_lds, i * WM * kFrag);
+        as[ring(i)] = scale(0, m_lds + i * WM * kFrag);
     };
     wait_loads<(STAGES - 1) * W::kLoads>();
     __builtin_amdgcn_s_barrier();
@@ -150,7 +162,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(Fp8WgradArgs a, 
 #pragma unroll
     for (int f = 0; f < NF; ++f) read_x(f);
     read_g(0);
-    read_g(1);
+    if constexpr (MT == 4) read_g(1);
     while (true) {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
@@ -158,50 +170,59 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(Fp8WgradArgs a, 
             for (int f = 0; f < NF; ++f) acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
         for (int c = 0; c < u.count; ++c) {
-            Wide ww[EXACT ? NF : 1];
+            Wide ww[EXACT ? NF : 1], gw[EXACT ? 2 : 1];
             if constexpr (EXACT) {
 #pragma unroll
                 for (int f = 0; f < NF; ++f) ww[f] = widen(w[f], fp8_scale_value(ws[f]));
             }
-            // row i of fragments, from a value of g that is in registers
-            auto product = [&](int i, int f, const Operand& gv, int gs) {
-                if constexpr (EXACT) acc[i][f] = wide_mfma(ww[f], gv, acc[i][f]);
-                else acc[i][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(words8(w[f]), words8(gv), acc[i][f], 0, 0,
-                                                                                  0, ws[f], 0, gs);
-            };
-            auto operand = [&](const Frag& v, int s) {
-                if constexpr (EXACT) return widen(v, fp8_scale_value(s));
-                else return v;
-            };
+            // four steps by bf16 in turn, as the four instructions of one wait for each other
+            auto wide_steps = [&](int n) {
+                if (n <= kMeet) gw[0] = widen(av[ring(row_of(n))], fp8_scale_value(as[ring(row_of(n))]));
+                if (n == kMeet) gw[EXACT] = widen(av[ring(MT - 1)], fp8_scale_value(as[ring(MT - 1)]));
 #pragma unroll
-            for (int i = 0; i < MT - 2; ++i) {
-                read_g(i + 2);
-                const Operand gv = operand(av[i % 4], as[i % 4]);
+                for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int f = 0; f < NF; ++f) product(i, f, gv, as[i % 4]);
-                hold(acc[i]);
-            }
-            // The next block and its scales (issued before its codes) have arrived, the codes of the
-            // STAGES - 2 behind it may not have, and this one is read.
-            wait_behind_stores<(STAGES - 2) * W::kLoads, W::kStores>(STAGES == 3 ? stores[0] + stores[1] : stores[0]);
-            if constexpr (STAGES == 3) stores[1] = stores[0];
-            stores[0] = 0;
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
+                    for (int x = n; x < n + 4; ++x) {
+                        f32x4& y = acc[row_of(x)][frag_of(x)];
+                        y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ww[EXACT ? frag_of(x) : 0].v[k],
+                                                                    gw[EXACT && row_of(x) == MT - 1].v[k], y, 0, 0, 0);
+                    }
+            };
             const int fill = slot;
-            slot = slot == STAGES - 1 ? 0 : slot + 1;
-            load_scales(fill);
-            const Operand g2 = operand(av[2], as[2]), g3 = operand(av[3], as[3]);
-            const int s2 = as[2], s3 = as[3];
 #pragma unroll
-            for (int f = 0; f < NF; ++f) {
-                product(MT - 2, f, g2, s2);
-                product(MT - 1, f, g3, s3);
-                asm volatile("" : "+v"(acc[MT - 2][f]), "+v"(acc[MT - 1][f])::"memory");
-                read_x(f);
-                if (f < 2) read_g(f);
+            for (int n = 0; n < MT * NF; ++n) {
+                const int i = row_of(n), f = frag_of(n);
+                if (n < kMeet && f == 0) {               // rows of this block
+                    if (MT == 4 && i == 0) read_g(2), read_g(3);
+                    if (MT == 8) read_g(i + 1);
+                    if (MT == 8 && i == MT - 3) read_g(MT - 1);
+                }
+                if (n == kMeet) {
+                    // The next block and its scales (issued before its codes) have arrived, the codes of the
+                    // STAGES - 2 behind it may not have, and this one is read.
+                    wait_behind_stores<(STAGES - 2) * W::kLoads, W::kStores>(STAGES == 3 ? stores[0] + stores[1] : stores[0]);
+                    if constexpr (STAGES == 3) stores[1] = stores[0];
+                    stores[0] = 0;
+                    __builtin_amdgcn_s_barrier();
+                    asm volatile("" ::: "memory");
+                    slot = slot == STAGES - 1 ? 0 : slot + 1;
+                    load_scales(fill);
+                }
+                if constexpr (EXACT) {
+                    if (n % 4 == 0) wide_steps(n);
+                } else {
+                    acc[i][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(words8(w[f]), words8(av[ring(i)]), acc[i][f],
+                                                                                 0, 0, 0, ws[f], 0, as[ring(i)]);
+                }
+                asm volatile("" : "+v"(acc[i][f])::"memory");
+                if (n >= kMeet) {
+                    if (n == kMeet + 1) read_g(0);       // of the next block
+                    if (n == kMeet + 3 && MT == 4) read_g(1);
+                    if (i == MT - 1) read_x(f);
+                    const int q = n - kMeet;
 #pragma unroll
-                for (int x = f * W::kLoads / NF; x < (f + 1) * W::kLoads / NF; ++x) load_codes(fill, x);
+                    for (int x = q * W::kLoads / 8; x < (q + 1) * W::kLoads / 8; ++x) load_codes(fill, x);
+                }
             }
             advance();
         }
@@ -255,10 +276,6 @@ coli_status wgrad(const Fp8WgradArgs& a, hipStream_t stream) {
 coli_status launch_fp8_wgrad(const Fp8WgradArgs& a, int32_t dtype, hipStream_t stream) {
     return with_elem(dtype, [&](auto e) -> coli_status {
         using T = decltype(e);
-        const char* v = getenv("WG");
-        if (v && v[0] == '1') return wgrad<T, 8, 4, 2, 4, 2>(a, stream);
-        if (v && v[0] == '2') return wgrad<T, 4, 4, 4, 2, 2>(a, stream);
-        if (v && v[0] == '3') return wgrad<T, 4, 4, 4, 2, 3>(a, stream);
         if constexpr (std::is_same<T, float>::value) return wgrad<T, 4, 4, 2, 4, 3>(a, stream);
         else return wgrad<T, 8, 4, 2, 4, 2>(a, stream);
     });

@@ -74,15 +74,20 @@ def quantize_matrix(x):
 
 
 def quantize_columns(x, offsets):
-    """(codes [cols][P], scale codes [P / 128][cols]) of the experts' rows, P as many as they fill."""
+    """(codes [blocks][cols][128], scale codes [blocks][cols]) of the experts' rows, as many blocks as they fill."""
     x = np.asarray(x, dtype=np.float64)
-    codes, scales = [np.zeros((x.shape[1], 0), np.uint8)], [np.zeros((0, x.shape[1]), np.int64)]
+    codes, scales = [np.zeros((0, x.shape[1], BLOCK), np.uint8)], [np.zeros((0, x.shape[1]), np.int64)]
     for lo, hi in zip(offsets[:-1], offsets[1:]):
         if hi > lo:
             q, s = quantize_rows(np.pad(x[lo:hi], ((0, -(hi - lo) % BLOCK), (0, 0))).T)
-            codes.append(q)
+            codes.append(q.reshape(x.shape[1], -1, BLOCK).transpose(1, 0, 2))
             scales.append(s.T)
-    return np.concatenate(codes, 1), np.concatenate(scales)
+    return np.concatenate(codes), np.concatenate(scales)
+
+
+def column_values(q, s):
+    """The values of such blocks, [cols][rows]."""
+    return (CODES[q] * scale_value(s)[..., None]).transpose(1, 0, 2).reshape(q.shape[1], -1)
 
 
 def values(q, s, block_rows=1):

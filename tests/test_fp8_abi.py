@@ -46,7 +46,7 @@ def test_quantize_refusals(L):
     def matrix(x=16, dt=0, r=32, c=64, ld=64, q=16, s=16, n=2, xs=2048, qs=2048, ss=4, qt=None, st=None):
         return L.coli_quantize_fp8_matrix(x, dt, n, r, c, ld, xs, q, qs, s, ss, qt, qs, st, ss, None)
 
-    def columns(x=16, dt=0, r=4, c=64, ld=64, qt=16, st=16, off=16, E=2, P=512, q=None, s=None):
+    def columns(x=16, dt=0, r=4, c=64, ld=64, qt=16, st=16, off=16, E=2, P=4, q=None, s=None):
         return L.coli_quantize_fp8_columns(x, dt, r, c, ld, off, E, qt, P, st, q, s, None)
 
     for f in (rows, back, matrix, columns):
@@ -65,7 +65,7 @@ def test_quantize_refusals(L):
     assert matrix(r=24, qt=16, st=16) == EINVAL                  # the transposed rows are no multiple of 16
     assert matrix(qt=24, st=16) == EINVAL and matrix(qt=16) == EINVAL
     assert matrix(r=1 << 30) == EUNSUP and matrix(r=1 << 24, c=1 << 20, ld=1 << 20, n=1) == EUNSUP
-    assert columns(P=500) == EINVAL and columns(P=128) == EINVAL and columns(P=1 << 31) == EUNSUP
+    assert columns(P=1) == EINVAL and columns(P=-1) == EINVAL and columns(P=1 << 24) == EUNSUP
     assert columns(E=0) == EINVAL and columns(E=1025, P=1 << 20) == EUNSUP and columns(off=None) == EINVAL
     assert columns(qt=None) == EINVAL and columns(st=None) == EINVAL and columns(qt=24) == EINVAL
     assert columns(q=16) == EINVAL and columns(q=24, s=16) == EINVAL
@@ -90,10 +90,10 @@ def test_product_refusals(L):
     assert sw(n=24, ld=24, dt=coli.FP8) == EINVAL and sw(dt=coli.FP8, ys=None) == EINVAL and sw(dt=coli.FP8, y=24) == EINVAL
     assert sw(uq=8) == EINVAL and sw(us=2) == EINVAL
 
-    def wg(g=16, gs=16, x=16, xs=16, P=512, rows=4, off=16, E=2, N=16, K=32, acc=0, dw=16, dt=0, ld=32):
+    def wg(g=16, gs=16, x=16, xs=16, P=4, rows=4, off=16, E=2, N=16, K=32, acc=0, dw=16, dt=0, ld=32):
         return L.coli_fp8_wgrad(g, gs, x, xs, P, rows, off, E, N, K, acc, dw, dt, ld, None)
 
-    assert wg(rows=-1) == EINVAL and wg(P=500) == EINVAL and wg(P=128) == EINVAL and wg(P=1 << 31) == EUNSUP
+    assert wg(rows=-1) == EINVAL and wg(P=1) == EINVAL and wg(P=-1) == EINVAL and wg(P=1 << 24) == EUNSUP
     assert wg(E=0) == EINVAL and wg(E=1025, P=1 << 20) == EUNSUP and wg(off=None) == EINVAL
     assert wg(N=24) == EINVAL and wg(K=24) == EINVAL and wg(N=0) == EINVAL and wg(K=0) == EINVAL
     assert wg(dt=3) == EUNSUP and wg(ld=31) == EINVAL and wg(ld=1 << 56) == EUNSUP and wg(N=1 << 30) == EUNSUP
@@ -107,12 +107,12 @@ def test_product_refusals(L):
 
 
 def test_sizes(L):
-    assert coli.fp8_columns_ld(1, 256) == 128 and coli.fp8_columns_ld(128, 1) == 128 and coli.fp8_columns_ld(129, 1) == 256
-    assert coli.fp8_columns_ld(0, 4) == 0 and coli.fp8_columns_ld(300, 2) == 512      # 1 + 299, or 172 + 128
+    assert coli.fp8_column_blocks(1, 256) == 1 and coli.fp8_column_blocks(128, 1) == 1 and coli.fp8_column_blocks(129, 1) == 2
+    assert coli.fp8_column_blocks(0, 4) == 0 and coli.fp8_column_blocks(300, 2) == 4       # 1 + 299 rows
     for rows in (1, 5, 127, 128, 129, 1000):
         for E in (1, 3, 64):
-            P = coli.fp8_columns_ld(rows, E)
-            assert coli.fp8_columns_ld(coli._rows_of_ld(P, E), E) <= P and coli._rows_of_ld(P, E) >= rows
+            n = coli.fp8_column_blocks(rows, E)
+            assert coli.fp8_column_blocks(coli._rows_of_blocks(n, E), E) <= n and coli._rows_of_blocks(n, E) >= rows
     off, nbytes = coli.fp8_blob_layout(coli.MoEShape(6144, 2048, 256))
     m, n = 6144 * 2048, 4 * 48 * 16
     assert off == [0, m, 2 * m, 3 * m, 3 * m + n, 3 * m + 2 * n] and nbytes == 3 * (m + n)

@@ -173,17 +173,17 @@ def test_quantize_columns(coli, dtype, case):
     if rows > 4:
         x[before, 3] = float("nan")
     want_q, want_s = ref.quantize_columns(_host(x), off)
-    P = coli.fp8_columns_ld(rows, len(counts)) + 128
-    qt = torch.full((cols, P), 77, dtype=torch.uint8, device="cuda")
-    st = torch.full((P // 128, cols), 77, dtype=torch.uint8, device="cuda")
+    B = coli.fp8_column_blocks(rows, len(counts)) + 1
+    qt = torch.full((B, cols, 128), 77, dtype=torch.uint8, device="cuda")
+    st = torch.full((B, cols), 77, dtype=torch.uint8, device="cuda")
     q = torch.full((rows, cols), 77, dtype=torch.uint8, device="cuda")
     s = torch.full((rows, -(-cols // 128)), 77.0, device="cuda")
     buf = torch.full((rows, cols + 3), 1.0, dtype=_t(dtype), device="cuda")
     buf[:, :cols] = x.cuda()
     coli.quantize_fp8_columns(buf[:, :cols], _dev(off), qt=qt, st=st, q=q, s=s)
-    n = want_q.shape[1]
-    assert np.array_equal(qt.cpu().numpy()[:, :n], want_q) and bool((qt[:, n:] == 77).all())
-    assert np.array_equal(st.cpu().numpy()[:n // 128], want_s) and bool((st[n // 128:] == 77).all())
+    n = len(want_q)
+    assert np.array_equal(qt.cpu().numpy()[:n], want_q) and bool((qt[n:] == 77).all())
+    assert np.array_equal(st.cpu().numpy()[:n], want_s) and bool((st[n:] == 77).all())
     lo, hi = before, int(off[-1])
     if hi > lo:
         qr, sr = ref.quantize_rows(_host(x[lo:hi]))
@@ -191,7 +191,7 @@ def test_quantize_columns(coli, dtype, case):
     assert bool((q[:lo] == 77).all()) and bool((q[hi:] == 77).all()) and bool((s[hi:] == 77.0).all())
     if len(counts) == 1 and before + behind == 0:
         a, b = coli.quantize_fp8_columns(x.cuda())
-        assert a.shape[1] == -(-rows // 128) * 128 and np.array_equal(a.cpu().numpy(), want_q) and np.array_equal(b.cpu().numpy(), want_s)
+        assert len(a) == -(-rows // 128) and np.array_equal(a.cpu().numpy(), want_q) and np.array_equal(b.cpu().numpy(), want_s)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -232,7 +232,7 @@ def test_quantize_past_32_bits(coli):
     assert q[-1, -1].item() == qt[-1, -1].item() == 0x7C and int((qt != 0).sum()) == 17 and st[-1, -1] == s[-1, -1]
     del q, s
     a, b = coli.quantize_fp8_columns(x)
-    assert int((a != 0).sum()) == 17 and a[-1, -1].item() == 0x7C and a[128, rows // 2].item() == 0xF8
+    assert int((a != 0).sum()) == 17 and a[-1, -1, -1].item() == 0x7C and a[rows // 256, 128, 0].item() == 0xF8
     assert b[-1, -1].item() == 120
 
 
@@ -396,7 +396,7 @@ def test_wgrad(coli, counts, n, K, dtype):
         vals = []
         for t in (g, x):
             q, s = ref.quantize_columns(_host(t)[lo:hi], [0, hi - lo])
-            vals.append(ref.CODES[q] * ref.scale_value(s).T.repeat(128, 1))
+            vals.append(ref.column_values(q, s))
         want[e], terms[e] = vals[0] @ vals[1].T, np.abs(vals[0]) @ np.abs(vals[1]).T
     most = max(1, int((off[1:] - off[:-1]).max()))
     tol = ref.product_bound(most, terms, dtype == "float32")
@@ -499,7 +499,7 @@ def test_layer_forward_and_backward(coli):
     vals = []
     for t in (dr, xrow[:used]):
         qc, sc = ref.quantize_columns(t, off)
-        vals.append(ref.CODES[qc] * ref.scale_value(sc).T.repeat(128, 1))
+        vals.append(ref.column_values(qc, sc))
     first = np.concatenate([[0], np.cumsum(-(-(off[1:] - off[:-1]) // 128) * 128)])
     for e in range(E):
         gv, xv = vals[0][:, first[e]:first[e + 1]], vals[1][:, first[e]:first[e + 1]]
@@ -518,11 +518,11 @@ def test_graph_and_streams(coli):
     off = _dev(np.array([0, 9, 9, 30], np.int32))
     x = torch.randn(rows, K, device="cuda").to(torch.bfloat16)
     keep2, table2, _, at2 = _weights(rng, E, K, n)
-    P = coli.fp8_columns_ld(rows, E)
+    B = coli.fp8_column_blocks(rows, E)
     e = torch.empty
     out = dict(q=e(rows, K, dtype=torch.uint8, device="cuda"), s=e(rows, 5, device="cuda"), h=e(rows, n, dtype=torch.uint8, device="cuda"),
-               hs=e(rows, 2, device="cuda"), y=e(rows, K, device="cuda"), qt=e(K, P, dtype=torch.uint8, device="cuda"),
-               st=e(P // 128, K, dtype=torch.uint8, device="cuda"), dw=e(E, K, K, device="cuda"), v=e(rows, K, device="cuda"))
+               hs=e(rows, 2, device="cuda"), y=e(rows, K, device="cuda"), qt=e(B, K, 128, dtype=torch.uint8, device="cuda"),
+               st=e(B, K, dtype=torch.uint8, device="cuda"), dw=e(E, K, K, device="cuda"), v=e(rows, K, device="cuda"))
 
     def step(o, stream=None):
         coli.quantize_fp8_columns(x, off, qt=o["qt"], st=o["st"], q=o["q"], s=o["s"], stream=stream)
