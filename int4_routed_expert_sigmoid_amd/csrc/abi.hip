@@ -754,7 +754,7 @@ static coli_status check_fp8_product(const std::string& w, int32_t rows, int32_t
     return COLI_OK;
 }
 
-static coli_status fp8_product(const char* what, Fp8GemmArgs& a, bool swiglu, int32_t dtype, void* stream) {
+static coli_status fp8_product(const char* what, Fp8GemmArgs& a, bool swiglu, int32_t dtype, size_t ws_bytes, void* stream) {
     const std::string w(what);
     coli_status st = check_fp8_product(w, a.rows, a.K, a.E, a.N, a.offsets != nullptr);
     if (st) return st;
@@ -769,6 +769,8 @@ static coli_status fp8_product(const char* what, Fp8GemmArgs& a, bool swiglu, in
     if (!a.table || !a.y) return fail(COLI_EINVAL, w + ": NULL pointer");
     if ((st = check_fp8_pair(w, a.a, a.as))) return st;
     if (fp8 && (st = check_fp8_pair(w, a.y, a.ys))) return st;
+    if (fp8 && a.ws && !aligned16(a.ws)) return fail(COLI_EINVAL, w + ": the workspace must be 16-byte aligned");
+    if (fp8 && ws_bytes < fp8_swiglu_ws(a)) a.ws = nullptr;
     return launch_fp8_gemm(a, swiglu, dtype, (hipStream_t)stream);
 }
 
@@ -780,20 +782,34 @@ coli_status coli_fp8_matmul(const uint8_t* d_a, const float* d_as, int32_t rows,
     a.offsets = d_offsets; a.table = d_blob_table; a.rows = rows; a.E = E;
     a.a = d_a; a.as = d_as; a.q_off = q_off; a.s_off = s_off;
     a.y = d_y; a.ld = ld; a.K = K; a.N = N;
-    return fp8_product("fp8_matmul", a, false, dtype, stream);
+    return fp8_product("fp8_matmul", a, false, dtype, 0, stream);
     COLI_GUARD_END
 }
 
 coli_status coli_fp8_swiglu(const uint8_t* d_a, const float* d_as, int32_t rows, int32_t K, const int32_t* d_offsets,
                             int32_t E, const void* const* d_blob_table, size_t q_off, size_t s_off, size_t up_q_off,
-                            size_t up_s_off, int32_t inter, void* d_h, float* d_hs, int32_t dtype, int64_t ld,
-                            void* stream) {
+                            size_t up_s_off, int32_t inter, void* d_h, float* d_hs, int32_t dtype, int64_t ld, void* d_ws, size_t ws_bytes, void* stream) {
     COLI_GUARD_BEGIN
     Fp8GemmArgs a = {};
     a.offsets = d_offsets; a.table = d_blob_table; a.rows = rows; a.E = E;
     a.a = d_a; a.as = d_as; a.q_off = q_off; a.s_off = s_off; a.up_q = up_q_off; a.up_s = up_s_off;
-    a.y = d_h; a.ys = d_hs; a.ld = ld; a.K = K; a.N = inter;
-    return fp8_product("fp8_swiglu", a, true, dtype, stream);
+    a.y = d_h; a.ys = d_hs; a.ld = ld; a.K = K; a.N = inter; a.ws = d_ws;
+    return fp8_product("fp8_swiglu", a, true, dtype, ws_bytes, stream);
+    COLI_GUARD_END
+}
+
+coli_status coli_fp8_swiglu_workspace_size(int32_t rows, int32_t K, int32_t E, int32_t inter, int32_t grouped,
+                                           size_t* bytes) {
+    COLI_GUARD_BEGIN
+    coli_status st = check_fp8_product("fp8_swiglu_workspace_size", rows, K, E, inter, grouped != 0);
+    if (st) return st;
+    if (!bytes) return fail(COLI_EINVAL, "fp8_swiglu_workspace_size: NULL pointer");
+    static const int32_t some = 0;
+    Fp8GemmArgs a = {};
+    a.rows = rows; a.K = K; a.E = E; a.N = inter;
+    a.offsets = grouped ? &some : nullptr;      // asked for, not read
+    *bytes = rows == 0 ? 0 : fp8_swiglu_ws(a);
+    return COLI_OK;
     COLI_GUARD_END
 }
 

@@ -106,8 +106,10 @@ __device__ __forceinline__ void load4_to_lds(const uint8_t* p, uint32_t* dst) {
 }
 
 // ------------------------------------------------------------ launchers
+// With offsets [E + 1] (device), of the rows in [offsets[0], offsets[E]) alone.
 coli_status launch_quantize_fp8(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
-                                uint8_t* q, float* s, hipStream_t stream);
+                                uint8_t* q, float* s, hipStream_t stream, const int32_t* offsets = nullptr,
+                                int32_t E = 0);
 
 // `count` matrices [rows][cols], x_stride elements apart, into codes and scales (of either way
 // round, nullptr: not wanted) that lie q_stride, ... bytes apart.
@@ -149,6 +151,7 @@ struct Fp8GemmArgs : RowGroups {
     size_t up_q, up_s;           // SwiGLU: those of up
     void* y;                     // [rows][ld] output, or codes [rows][N]
     float* ys;                   // scales [rows][ceil(N / 128)] of an FP8 output
+    void* ws;                    // fp8_swiglu_ws bytes for one, or nullptr
     int64_t ld;
     int32_t K, N;                // N: rows of the matrix, of gate and of up alone
 };
@@ -156,6 +159,8 @@ struct Fp8GemmArgs : RowGroups {
 enum Fp8Kernel : int32_t { kFp8FewRows2, kFp8FewRows4, kFp8Lines128, kFp8Lines256 };
 Fp8Kernel choose_fp8_kernel(const Fp8GemmArgs& a, bool swiglu);
 coli_status launch_fp8_gemm(const Fp8GemmArgs& a, bool swiglu, int32_t dtype, hipStream_t stream);
+// The workspace that a SwiGLU product into FP8 rows makes use of.
+size_t fp8_swiglu_ws(const Fp8GemmArgs& a);
 
 // dw[e][n][k] = sum over the expert's rows (+ dw[e][n][k]); see fp8_wgrad.hip.
 struct Fp8WgradArgs {

@@ -16,8 +16,18 @@
 namespace coli {
 namespace {
 
-// FP8 rows as an output type of the SwiGLU epilogue.
+// FP8 rows as an output type of the SwiGLU epilogue, and f32 rows on their way there.
 struct Fp8Out {};
+struct RawOut {};
+
+template <typename Out>
+struct StoredAs {
+    typedef Out type;
+};
+template <>
+struct StoredAs<RawOut> {
+    typedef float type;
+};
 
 typedef __attribute__((address_space(4))) const float const_f32;
 typedef __attribute__((address_space(1))) const float global_float;
@@ -170,7 +180,7 @@ __global__ __launch_bounds__(64 * WN * KS) void fp8_few_rows_kernel(Fp8GemmArgs 
                 top = umax_step<32>(top);
                 if (g == 0) tops[o][r] = top;
             } else {
-                if (live && n0 < a.N) store4<Out>(a, m, n0, a.N, h[i]);
+                if (live && n0 < a.N) store4<typename StoredAs<Out>::type>(a, m, n0, a.N, h[i]);
             }
         }
         if constexpr (kFp8) {
@@ -540,13 +550,31 @@ coli_status few_rows(const Fp8GemmArgs& a, hipStream_t stream) {
     return COLI_OK;
 }
 
+// SwiGLU of few rows into FP8. A block of 128 h is one workgroup's, whose CU takes in about 35 GB/s, so that fewer
+// workgroups than CUs leave the device idle: then, with a workspace for h in f32, it is formed 16 columns a
+// workgroup and quantised by a launch of its own (8 rows of 8 of 256 experts, K 6144, inter 2048: TWO us against 58;
+// one row 13 against 51; from 256 workgroups on, of 40 experts, 186 for the one launch).
+int64_t few_rows_blocks(const Fp8GemmArgs& a) {
+    const int64_t experts = a.offsets ? std::min(a.E, a.rows) : 1;
+    return experts * ((a.rows + experts * kFrag - 1) / (experts * kFrag)) * fp8_blocks(a.N);
+}
+
+coli_status few_rows_fp8(const Fp8GemmArgs& a, hipStream_t stream) {
+    if (a.ws == nullptr || fp8_swiglu_ws(a) == 0) return few_rows<Fp8Out, true, 2, 8, 1, 4>(a, stream);
+    Fp8GemmArgs h = a;
+    h.y = a.ws;
+    h.ld = a.N;
+    if (coli_status st = few_rows<RawOut, true, 2, 1, 4, 4>(h, stream)) return st;
+    return launch_quantize_fp8(a.ws, COLI_F32, a.rows, a.N, a.N, (uint8_t*)a.y, a.ys, stream, a.offsets, a.E);
+}
+
 template <typename Out, bool SWIGLU>
 coli_status product(const Fp8GemmArgs& a, hipStream_t stream) {
     constexpr bool kFp8 = std::is_same<Out, Fp8Out>::value, kWide = std::is_same<Out, float>::value;
     switch (choose_fp8_kernel(a, SWIGLU)) {
         case kFp8FewRows2:
         case kFp8FewRows4:
-            if constexpr (kFp8) return few_rows<Out, SWIGLU, 4, 4, 2, 4>(a, stream);
+            if constexpr (kFp8) return few_rows_fp8(a, stream);
             else return few_rows<Out, SWIGLU, 2, 1, 4, 4>(a, stream);
         case kFp8Lines256:
             // (32-bit results have no registers for it: operands are twice as wide)
@@ -564,6 +592,12 @@ Fp8Kernel choose_fp8_kernel(const Fp8GemmArgs& a, bool swiglu) {
     auto units = [&](int bm) { return experts * (int64_t)std::ceil(per / bm) * ((a.N + cols - 1) / cols); };
     if (per <= 4 || (per <= 32 && units(128) < kCus)) return kFp8FewRows4;
     return per >= 512 ? kFp8Lines256 : kFp8Lines128;
+}
+
+size_t fp8_swiglu_ws(const Fp8GemmArgs& a) {
+    const Fp8Kernel k = choose_fp8_kernel(a, true);
+    const bool two = (k == kFp8FewRows2 || k == kFp8FewRows4) && few_rows_blocks(a) < kCus;
+    return two ? (size_t)a.rows * a.N * 4 : 0;
 }
 
 coli_status launch_fp8_gemm(const Fp8GemmArgs& a, bool swiglu, int32_t dtype, hipStream_t stream) {

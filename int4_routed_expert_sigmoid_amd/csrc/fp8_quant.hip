@@ -58,22 +58,24 @@ __device__ __forceinline__ void locate(const UnitMap& m, int64_t u, int64_t* row
 }
 
 // ------------------------------------------------------------ rows
-template <typename T>
+template <typename T, bool BOUNDED>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const T* __restrict__ x, UnitMap m,
                                                                  uint8_t* __restrict__ q,
-                                                                 float* __restrict__ s) {
+                                                                 float* __restrict__ s,
+                                                                 const int32_t* __restrict__ offsets, int E) {
     constexpr int N = kVec<T>;
     const int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (u >= m.units) return;                     // whole blocks: their lanes come together
     int64_t row, at;
     locate(m, u, &row, &at);
     const int64_t c = at * N;
-    const bool in = c < m.cols;
+    const bool mine = !BOUNDED || (row >= offsets[0] && row < offsets[E]);      // alike in a block's lanes
+    const bool in = c < m.cols && mine;
     float v[N] = {};
     if (in) load_f32_once<T, N>(x + row * m.ld + c, v);
     const int code = fp8_scale_code(lanes_umax<kLanes<T>>(top_bits(v)));
     if (in) store_codes(q + row * m.cols + c, v, fp8_scale_inverse(code));
-    if (threadIdx.x % kLanes<T> == 0) s[u / kLanes<T>] = fp8_scale_value(code);
+    if (threadIdx.x % kLanes<T> == 0 && mine) s[u / kLanes<T>] = fp8_scale_value(code);
 }
 
 // The same into the experts' order: a token is read and converted once, its codes and scales go to
@@ -347,7 +349,7 @@ coli_status check_grid(int64_t grid, const char* what) {
 }  // namespace
 
 coli_status launch_quantize_fp8(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
-                                uint8_t* q, float* s, hipStream_t stream) {
+                                uint8_t* q, float* s, hipStream_t stream, const int32_t* offsets, int32_t E) {
     if (rows == 0) return COLI_OK;
     return with_elem(dtype, [&](auto e) -> coli_status {
         using T = decltype(e);
@@ -358,7 +360,8 @@ coli_status launch_quantize_fp8(const void* x, int32_t dtype, int64_t rows, int6
         m.cols = (int32_t)cols;
         const int64_t grid = (m.units + kThreads - 1) / kThreads;
         if (coli_status st = check_grid(grid, "quantize_fp8")) return st;
-        launch(quantize_rows_kernel<T>, dim3((uint32_t)grid), dim3(kThreads), 0, stream, (const T*)x, m, q, s);
+        if (offsets) launch(quantize_rows_kernel<T, true>, dim3((uint32_t)grid), dim3(kThreads), 0, stream, (const T*)x, m, q, s, offsets, E);
+        else launch(quantize_rows_kernel<T, false>, dim3((uint32_t)grid), dim3(kThreads), 0, stream, (const T*)x, m, q, s, offsets, E);
         COLI_CHECK_LAUNCH("quantize_fp8 kernel launch");
         return COLI_OK;
     });

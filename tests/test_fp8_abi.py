@@ -75,8 +75,8 @@ def test_product_refusals(L):
     def mm(a=16, s=16, rows=4, K=64, off=16, E=2, table=16, q=0, so=256, n=8, y=16, dt=0, ld=8):
         return L.coli_fp8_matmul(a, s, rows, K, off, E, table, q, so, n, y, dt, ld, None)
 
-    def sw(a=16, s=16, rows=4, K=64, off=16, E=2, table=16, q=0, so=256, n=16, y=16, ys=16, dt=0, ld=16, uq=1024, us=512):
-        return L.coli_fp8_swiglu(a, s, rows, K, off, E, table, q, so, uq, us, n, y, ys, dt, ld, None)
+    def sw(a=16, s=16, rows=4, K=64, off=16, E=2, table=16, q=0, so=256, n=16, y=16, ys=16, dt=0, ld=16, uq=1024, us=512, ws=None):
+        return L.coli_fp8_swiglu(a, s, rows, K, off, E, table, q, so, uq, us, n, y, ys, dt, ld, ws, 1 << 20, None)
 
     for f in (mm, sw):
         assert f(rows=-1) == EINVAL and f(K=40) == EINVAL and f(K=0) == EINVAL and f(K=(1 << 22) + 16) == EUNSUP
@@ -88,7 +88,7 @@ def test_product_refusals(L):
         assert f(n=(1 << 31) - 1, ld=1 << 31) == EUNSUP
     assert mm(dt=coli.FP8) == EUNSUP                             # only the SwiGLU writes FP8
     assert sw(n=24, ld=24, dt=coli.FP8) == EINVAL and sw(dt=coli.FP8, ys=None) == EINVAL and sw(dt=coli.FP8, y=24) == EINVAL
-    assert sw(uq=8) == EINVAL and sw(us=2) == EINVAL
+    assert sw(uq=8) == EINVAL and sw(us=2) == EINVAL and sw(dt=coli.FP8, ws=24) == EINVAL
 
     def wg(g=16, gs=16, x=16, xs=16, P=4, rows=4, off=16, E=2, N=16, K=32, acc=0, dw=16, dt=0, ld=32):
         return L.coli_fp8_wgrad(g, gs, x, xs, P, rows, off, E, N, K, acc, dw, dt, ld, None)
@@ -113,6 +113,13 @@ def test_sizes(L):
         for E in (1, 3, 64):
             n = coli.fp8_column_blocks(rows, E)
             assert coli.fp8_column_blocks(coli._rows_of_blocks(n, E), E) <= n and coli._rows_of_blocks(n, E) >= rows
+    nb = ctypes.c_size_t()
+    size = coli.lib().coli_fp8_swiglu_workspace_size
+    for rows, K, E, inter, grouped, want in ((8, 6144, 256, 2048, 1, 8 * 2048 * 4), (1, 272, 1, 144, 0, 144 * 4), (64, 6144, 40, 2048, 1, 0),
+                                             (4096, 6144, 256, 2048, 1, 0), (0, 64, 4, 64, 1, 0)):
+        assert size(rows, K, E, inter, grouped, ctypes.byref(nb)) == OK and nb.value == want
+    assert size(4, 40, 1, 16, 0, ctypes.byref(nb)) == EINVAL and size(4, 48, 2, 16, 0, ctypes.byref(nb)) == EINVAL
+    assert size(4, 48, 1, 16, 0, None) == EINVAL
     off, nbytes = coli.fp8_blob_layout(coli.MoEShape(6144, 2048, 256))
     m, n = 6144 * 2048, 4 * 48 * 16
     assert off == [0, m, 2 * m, 3 * m, 3 * m + n, 3 * m + 2 * n] and nbytes == 3 * (m + n)
