@@ -42,6 +42,22 @@ __device__ __forceinline__ void load_logits(const T* row, int E, int e0, float (
     }
 }
 
+// The wave's largest, uniform: rows of 16 by shifts, then from row to row; lane 63 ends with it. Lanes without a
+// source take 0.
+__device__ __forceinline__ uint32_t wave_top(uint32_t v) {
+    auto step = [&](auto ctrl, auto rows) {
+        v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value, decltype(rows)::value, 0xf, false));
+    };
+    typedef std::integral_constant<int, 0xf> all;
+    step(std::integral_constant<int, 0x111>{}, all{});                               // row_shr:1
+    step(std::integral_constant<int, 0x112>{}, all{});
+    step(std::integral_constant<int, 0x114>{}, all{});
+    step(std::integral_constant<int, 0x118>{}, all{});
+    step(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xa>{});  // row_bcast:15
+    step(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xc>{});  // row_bcast:31
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
 // The code by which a key is chosen; a NaN key comes first, so that it shows in the weights.
 __device__ __forceinline__ uint64_t key_code(float key, int e) {
     return selection_code(key != key ? __uint_as_float(0x7fc00000u) : key, e);
@@ -100,78 +116,109 @@ __global__ __launch_bounds__(kThreads) void route_groups_kernel(RouteArgs a) {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) key[i] = l[i] == none || b[i] == none || e0 + i >= E ? none : s[i] + b[i];
 
-    // open: the groups whose experts can be chosen
-    uint64_t open = ~0ull;
-    const uint32_t size = E / a.groups, div = ((1u << 21) + size - 1) / size;    // e / size = e div >> 21, e < 1024
-    if (a.kept < a.groups) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) lds[wave][e0 + i] = key[i];
-        __builtin_amdgcn_wave_barrier();
-        float first = none, second = none;
-        bool nan = false;
-        if (lane < a.groups) {
-            for (uint32_t i = 0; i < size; ++i) {
-                const float v = lds[wave][lane * size + i];
-                nan |= v != v;
-                second = fmaxf(second, fminf(first, v));
-                first = fmaxf(first, v);
-            }
-        }
-        float value = a.group_top == 2 && second != none ? first + second : first;
-        if (nan) value = __uint_as_float(0x7fc00000u);
-        const uint64_t code = lane < a.groups && value != none ? key_code(value, lane) : 0;
-        int rank = 0;
-        for (int j = 0; j < a.groups; ++j) {
-            const uint64_t other = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(code >> 32), j) << 32 |
-                                   (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)code, j);
-            rank += other > code;
-        }
-        open = __ballot(code != 0 && rank < a.kept);
-    }
+    // the groups whose experts can be chosen
     uint64_t c[EPL];
-    float sc[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        const bool there = key[i] != none && (open >> (((uint32_t)(e0 + i) * div) >> 21 & 63) & 1);
-        c[i] = there ? key_code(key[i], e0 + i) : 0;
-        sc[i] = s[i];
+    for (int i = 0; i < EPL; ++i) c[i] = key[i] != none ? key_code(key[i], e0 + i) : 0;
+    if (a.kept < a.groups) {
+        const uint32_t size = E / a.groups, wide = size / EPL;
+        if (size % EPL == 0 && (wide & (wide - 1)) == 0) {
+            // a group is 1, 2, 4, .. 64 whole lanes: its two largest by exchanges among them
+            float first = none, second = none;
+            uint32_t nan = 0;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                nan |= key[i] != key[i];
+                second = fmaxf(second, fminf(first, key[i]));
+                first = fmaxf(first, key[i]);
+            }
+            auto join = [&](auto s) {
+                constexpr int S = decltype(s)::value;
+                if (wide <= S) return;                // uniform
+                merge2(first, second, __int_as_float(lane_xchg<S>(__float_as_int(first))),
+                       __int_as_float(lane_xchg<S>(__float_as_int(second))));
+                nan |= (uint32_t)lane_xchg<S>((int)nan);
+            };
+            join(std::integral_constant<int, 1>{});
+            join(std::integral_constant<int, 2>{});
+            join(std::integral_constant<int, 4>{});
+            join(std::integral_constant<int, 8>{});
+            join(std::integral_constant<int, 16>{});
+            join(std::integral_constant<int, 32>{});
+            const float value = nan ? __uint_as_float(0x7fc00000u) : a.group_top == 2 && second != none ? first + second : first;
+            const uint64_t code = value != none ? key_code(value, lane / wide) : 0;
+            int rank = 0;
+            for (int j = 0; j < a.groups; ++j) {
+                const int from = j * wide;
+                const uint64_t other = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(code >> 32), from) << 32 |
+                                       (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)code, from);
+                rank += other > code;
+            }
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) c[i] = rank < a.kept ? c[i] : 0;
+        } else {
+            const uint32_t div = ((1u << 21) + size - 1) / size;                     // e / size = e div >> 21, e < 1024
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) lds[wave][e0 + i] = key[i];
+            __builtin_amdgcn_wave_barrier();
+            float first = none, second = none;
+            bool nan = false;
+            if (lane < a.groups) {
+                for (uint32_t i = 0; i < size; ++i) {
+                    const float v = lds[wave][lane * size + i];
+                    nan |= v != v;
+                    second = fmaxf(second, fminf(first, v));
+                    first = fmaxf(first, v);
+                }
+            }
+            const float value = nan ? __uint_as_float(0x7fc00000u) : a.group_top == 2 && second != none ? first + second : first;
+            const uint64_t code = lane < a.groups && value != none ? key_code(value, lane) : 0;
+            int rank = 0;
+            for (int j = 0; j < a.groups; ++j) {
+                const uint64_t other = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(code >> 32), j) << 32 |
+                                       (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)code, j);
+                rank += other > code;
+            }
+            const uint64_t open = __ballot(code != 0 && rank < a.kept);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) c[i] = open >> (((uint32_t)(e0 + i) * div) >> 21 & 63) & 1 ? c[i] : 0;
+            __builtin_amdgcn_wave_barrier();
+        }
     }
-    // each lane's codes in descending order, then k times the largest of the lanes' first codes
+    // The scores where a slot finds them by its expert. Each lane's codes in descending order, then k times the
+    // largest of the lanes' first codes, which that lane drops.
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) lds[wave][e0 + i] = s[i];
 #pragma unroll
     for (int pass = 0; pass < EPL; ++pass)
 #pragma unroll
         for (int i = pass & 1; i + 1 < EPL; i += 2) {
             const bool sw = c[i + 1] > c[i];
             const uint64_t x = c[i], y = c[i + 1];
-            const float fx = sc[i], fy = sc[i + 1];
             c[i] = sw ? y : x;
             c[i + 1] = sw ? x : y;
-            sc[i] = sw ? fy : fx;
-            sc[i + 1] = sw ? fx : fy;
         }
-    double sum = 0.0;
-    float mine = 0.f;
     int my_idx = -1, found = 0;
     for (; found < a.k; ++found) {
         const uint32_t hi = (uint32_t)(c[0] >> 32), lo = (uint32_t)c[0];
-        const uint32_t mh = wave_umax(hi);
+        const uint32_t mh = wave_top(hi);
         if (mh == 0) break;                           // no expert is left
         uint64_t top = __ballot(hi == mh);
         if (__popcll(top) > 1) {                      // equal keys: the lower expert
-            const uint32_t ml = wave_umax(hi == mh ? lo : 0u);
+            const uint32_t ml = wave_top(hi == mh ? lo : 0u);
             top = __ballot(hi == mh && lo == ml);
         }
         const int src = (int)__builtin_ctzll(top);
-        const int e = (int)~(uint32_t)__builtin_amdgcn_readlane((int)lo, src);
-        const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sc[0]), src));
-        if (lane == src) {
+        my_idx = lane == found ? (int)~(uint32_t)__builtin_amdgcn_readlane((int)lo, src) : my_idx;
+        const bool taken = lane == src;
 #pragma unroll
-            for (int i = 0; i + 1 < EPL; ++i) c[i] = c[i + 1], sc[i] = sc[i + 1];
-            c[EPL - 1] = 0;
-        }
-        if (lane == found) mine = v, my_idx = e;
-        sum += (double)v;
+        for (int i = 0; i + 1 < EPL; ++i) c[i] = taken ? c[i + 1] : c[i];
+        c[EPL - 1] = taken ? 0 : c[EPL - 1];
     }
+    __builtin_amdgcn_wave_barrier();
+    const float mine = my_idx < 0 ? 0.f : lds[wave][my_idx];
+    double sum = 0.0;
+    for (int j = 0; j < found; ++j) sum += (double)__int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), j));
     if (lane < a.k) {
         double w = mine;
         if (a.norm && my_idx >= 0) w = sum == 0.0 ? 1.0 / found : w / sum;
