@@ -636,7 +636,7 @@ COLI_API coli_status coli_fp8_swiglu_workspace_size(int32_t rows, int32_t K, int
 
 /* Every expert's matrix gradient: d_dw[e][n][k] = sum over the expert's rows r of g[r][n] x[r][k] (0
  * without rows), for g [rows][N] and x [rows][K] (N, K multiples of 16) as coli_quantize_fp8_columns
- * lays them out with the same rows, d_offsets, E and blocks. d_dw [E][N][ld] of type dtype, ld >= K;
+ * lays them out with the same rows, d_offsets, E and blocks (scales 4-byte aligned). d_dw [E][N][ld] of type dtype, ld >= K;
  * accumulate: the sums are added to what it holds. Sums as the products'. */
 COLI_API coli_status coli_fp8_wgrad(const uint8_t* d_gt, const uint8_t* d_gs, const uint8_t* d_xt,
                                     const uint8_t* d_xs, int64_t blocks, int32_t rows,
@@ -644,10 +644,11 @@ COLI_API coli_status coli_fp8_wgrad(const uint8_t* d_gt, const uint8_t* d_gs, co
                                     int32_t accumulate, void* d_dw, int32_t dtype, int64_t ld,
                                     void* stream);
 
-/* Testing: which kernel a product of these sizes runs (grouped: with d_offsets). Host-only
+/* Testing: which kernel a product of these sizes runs (grouped: with d_offsets; wide: f32 results): 0, 1
+ * few rows, 16 or 32 matrix rows a workgroup; 2, 3 persistent tiles of 128 or 256 rows. Host-only
  * arithmetic. */
 COLI_API coli_status coli_debug_fp8_kernel(int32_t rows, int32_t K, int32_t E, int32_t N, int32_t grouped,
-                                           int32_t swiglu, int32_t* kernel);
+                                           int32_t swiglu, int32_t wide, int32_t* kernel);
 
 /* ------------------------------------------------------- token permutation
  * The T tokens' rows in the experts' order and back, with gradients. d_inv [T][k]

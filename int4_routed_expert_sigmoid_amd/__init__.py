@@ -170,7 +170,7 @@ def lib():
                                           i64, vp, sz, vp]
             L.coli_fp8_swiglu_workspace_size.argtypes = [i32, i32, i32, i32, i32, P(sz)]
             L.coli_fp8_wgrad.argtypes = [vp, vp, vp, vp, i64, i32, vp, i32, i32, i32, i32, vp, i32, i64, vp]
-            L.coli_debug_fp8_kernel.argtypes = [i32, i32, i32, i32, i32, i32, P(i32)]
+            L.coli_debug_fp8_kernel.argtypes = [i32, i32, i32, i32, i32, i32, i32, P(i32)]
             L.coli_moe_dispatch_fp8.argtypes = [vp, i32, i32, i32, i32, i64, vp, vp, vp, vp]
             _lib = L
     return _lib
@@ -927,7 +927,7 @@ def route_groups_bwd(w_grad, logits, idx, score="sigmoid", norm=True, scale=1.0,
 
 
 # ---------------------------------------------------------------- FP8 experts
-FP8_KERNELS = ("few_rows_2", "few_rows_4", "lines_128", "lines_256")
+FP8_KERNELS = ("few_rows_16", "few_rows_32", "lines_128", "lines_256")
 
 
 def _blocks(n):
@@ -1185,10 +1185,10 @@ def fp8_wgrad(gt, gt_s, xt, xt_s, offsets=None, rows=None, dtype=None, out=None,
     return out
 
 
-def debug_fp8_kernel(rows: int, K: int, E: int, N: int, grouped=True, swiglu=False) -> str:
+def debug_fp8_kernel(rows: int, K: int, E: int, N: int, grouped=True, swiglu=False, wide=False) -> str:
     """coli_debug_fp8_kernel: the kernel that a product of these sizes runs."""
     out = ctypes.c_int32()
-    _check(lib().coli_debug_fp8_kernel(rows, K, E, N, int(grouped), int(swiglu), ctypes.byref(out)))
+    _check(lib().coli_debug_fp8_kernel(rows, K, E, N, int(grouped), int(swiglu), int(wide), ctypes.byref(out)))
     return FP8_KERNELS[out.value]
 
 

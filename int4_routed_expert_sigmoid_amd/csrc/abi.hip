@@ -827,6 +827,7 @@ coli_status coli_fp8_wgrad(const uint8_t* d_gt, const uint8_t* d_gs, const uint8
     if (ld > (int64_t(1) << 56) / N / E) return fail(COLI_EUNSUPPORTED, "fp8_wgrad: ld too large");
     if (!d_dw || (rows > 0 && (!d_gt || !d_gs || !d_xt || !d_xs))) return fail(COLI_EINVAL, "fp8_wgrad: NULL pointer");
     if (!aligned16(d_gt) || !aligned16(d_xt)) return fail(COLI_EINVAL, "fp8_wgrad: codes must be 16-byte aligned");
+    if (!aligned4(d_gs) || !aligned4(d_xs)) return fail(COLI_EINVAL, "fp8_wgrad: scales must be 4-byte aligned");
     if (rows == 0 && accumulate) return COLI_OK;
     Fp8WgradArgs a;
     a.g = d_gt; a.gs = d_gs; a.x = d_xt; a.xs = d_xs; a.offsets = d_offsets; a.dw = d_dw;
@@ -836,7 +837,7 @@ coli_status coli_fp8_wgrad(const uint8_t* d_gt, const uint8_t* d_gs, const uint8
 }
 
 coli_status coli_debug_fp8_kernel(int32_t rows, int32_t K, int32_t E, int32_t N, int32_t grouped, int32_t swiglu,
-                                  int32_t* kernel) {
+                                  int32_t wide, int32_t* kernel) {
     COLI_GUARD_BEGIN
     coli_status st = check_fp8_product("debug_fp8_kernel", rows, K, E, N, grouped != 0);
     if (st) return st;
@@ -845,7 +846,7 @@ coli_status coli_debug_fp8_kernel(int32_t rows, int32_t K, int32_t E, int32_t N,
     Fp8GemmArgs a = {};
     a.rows = rows; a.K = K; a.E = E; a.N = N;
     a.offsets = grouped ? &some : nullptr;      // asked for, not read
-    *kernel = choose_fp8_kernel(a, swiglu != 0);
+    *kernel = choose_fp8_kernel(a, swiglu != 0, wide != 0);
     return COLI_OK;
     COLI_GUARD_END
 }

@@ -155,9 +155,12 @@ struct Fp8GemmArgs : RowGroups {
     int64_t ld;
     int32_t K, N;                // N: rows of the matrix, of gate and of up alone
 };
-// The kernel that a product runs: its rows, E, offsets, N and K decide.
-enum Fp8Kernel : int32_t { kFp8FewRows2, kFp8FewRows4, kFp8Lines128, kFp8Lines256 };
-Fp8Kernel choose_fp8_kernel(const Fp8GemmArgs& a, bool swiglu);
+// The kernel that a product runs: its rows, E, offsets, N and K decide, and whether its results have 32 bits (wide).
+enum Fp8Kernel : int32_t {
+    kFp8FewRows16, kFp8FewRows32,                // by matrix rows a workgroup
+    kFp8Lines128, kFp8Lines256,                  // by rows a tile
+};
+Fp8Kernel choose_fp8_kernel(const Fp8GemmArgs& a, bool swiglu, bool wide);
 coli_status launch_fp8_gemm(const Fp8GemmArgs& a, bool swiglu, int32_t dtype, hipStream_t stream);
 // The workspace that a SwiGLU product into FP8 rows makes use of.
 size_t fp8_swiglu_ws(const Fp8GemmArgs& a);

@@ -3,11 +3,20 @@
 //
 // v_mfma_f32_16x16x128_f8f6f4 multiplies 16 rows by 16 rows over one block: a lane holds 32 of the
 // block's 128 columns of row l % 16, here the 16-byte units l / 16 and l / 16 + 4 (a block's columns
-// may be taken in any order, as long as both sides take the same). The block's sum, exact products
-// summed in f32, starts from 0 and enters the row's f32 sum by one multiplication: scales are any f32
+// may be taken in any order, as long as both sides take the same). The block's sum (for its accuracy, and
+// what results of 32 bits take in its place, see fp8.h) starts from 0 and enters the row's f32 sum by one multiplication: scales are any f32
 // numbers, so they cannot go into the instruction, which takes powers of two. The matrix rows are the
 // first operand: result lane l then holds outputs n = 4 (l / 16) .. + 3 of one row m = l % 16, whose
 // scale for the block is one number a lane, as the 16 matrix rows have one together.
+//
+// Bounds and times on one MI355X, where a copy moves 4.7 TB/s and a CU takes in about 35 GB/s from beyond its LDS:
+//  - few rows: the matrices' bytes. 8192 x 8192, one to 16 rows, 67 MB: 17 us (4.0 TB/s); SwiGLU of 8 of 256 experts
+//    of 2048 x 6144, 201 MB: 41 (4.9).
+//  - many rows: the matrix unit, in which a block of a tile takes 1.2 us of the 1.73 that it takes altogether. What
+//    keeps the rest: a tile of 256 by 256 brings in 64 KB a block, 1.8 us at a CU's rate if nothing hits a cache near
+//    by; and the four scalings of a product share the issue slots with the matrix instructions. 8191 x 8192 x 8192
+//    into bf16: 450 us, 2.44 PFLOP/s; of these 16 go if every load hits the L2 cache, 60 with no loads.
+//  - SwiGLU of all of 256 experts of 2048 x 6144, 6.4 GB: 1.19 ms (5.6 TB/s) for 1 to 8 rows an expert and more.
 #include <algorithm>
 #include <cmath>
 
@@ -209,6 +218,8 @@ __global__ __launch_bounds__(64 * WN * KS) void fp8_few_rows_kernel(Fp8GemmArgs 
 // again while the last row of fragments is multiplied and the next block's first ones are read.
 // A product is scaled into its sum while the next row's are in the matrix unit: the four multiply-adds of one
 // product take half of its time there.
+// Tiles of 256 rows in two stages of 64 KB and tiles of 128 in three of 48: two workgroups a CU would leave each half
+// of the rows and read everything twice (8191 x 8192 x 8192: 534 us by tiles of 128).
 // FAST: K in multiples of 512 and rows of scales on 16-byte boundaries: scales come 16 bytes, four blocks, a
 // row, and every unit is whole. Otherwise one block's at a time, and zeros behind the last column.
 template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int STAGES, bool FAST>
@@ -552,8 +563,8 @@ coli_status few_rows(const Fp8GemmArgs& a, hipStream_t stream) {
 
 // SwiGLU of few rows into FP8. A block of 128 h is one workgroup's, whose CU takes in about 35 GB/s, so that fewer
 // workgroups than CUs leave the device idle: then, with a workspace for h in f32, it is formed 16 columns a
-// workgroup and quantised by a launch of its own (8 rows of 8 of 256 experts, K 6144, inter 2048: TWO us against 58;
-// one row 13 against 51; from 256 workgroups on, of 40 experts, 186 for the one launch).
+// workgroup and quantised by a launch of its own (K 6144, inter 2048: 8 rows of 8 of 256 experts 41 us against 58, one
+// row 11 against 51; from 256 workgroups on, 40 rows of 40 experts, 188 against the one launch's 186).
 int64_t few_rows_blocks(const Fp8GemmArgs& a) {
     const int64_t experts = a.offsets ? std::min(a.E, a.rows) : 1;
     return experts * ((a.rows + experts * kFrag - 1) / (experts * kFrag)) * fp8_blocks(a.N);
@@ -571,13 +582,14 @@ coli_status few_rows_fp8(const Fp8GemmArgs& a, hipStream_t stream) {
 template <typename Out, bool SWIGLU>
 coli_status product(const Fp8GemmArgs& a, hipStream_t stream) {
     constexpr bool kFp8 = std::is_same<Out, Fp8Out>::value, kWide = std::is_same<Out, float>::value;
-    switch (choose_fp8_kernel(a, SWIGLU)) {
-        case kFp8FewRows2:
-        case kFp8FewRows4:
+    switch (choose_fp8_kernel(a, SWIGLU, kWide)) {
+        case kFp8FewRows16:                  // (not of SwiGLU's)
+            if constexpr (!SWIGLU) return few_rows<Out, SWIGLU, 1, 1, 4, 4>(a, stream);
+        case kFp8FewRows32:
             if constexpr (kFp8) return few_rows_fp8(a, stream);
             else return few_rows<Out, SWIGLU, 2, 1, 4, 4>(a, stream);
         case kFp8Lines256:
-            // (32-bit results have no registers for it: operands are twice as wide)
+            // (32-bit results have no registers for it, as their operands are twice as wide, and are not sent here)
             if constexpr (!kWide) return lines<Out, SWIGLU, 8, 4, 2, 4, 2>(a, stream);
         default: return lines<Out, SWIGLU, 4, 4, 2, 4, 3>(a, stream);
     }
@@ -585,18 +597,42 @@ coli_status product(const Fp8GemmArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-Fp8Kernel choose_fp8_kernel(const Fp8GemmArgs& a, bool swiglu) {
+// Which kernel, by estimates of each one's time in us, from times on one MI355X (graphs, warm caches):
+//  - few_rows reads a matrix once per 16 rows, 5.5 TB/s the first time and 6 from the caches, and a workgroup takes
+//    in its rows no faster than about 35 GB/s: 1.3 us per 1024 columns; 1024 workgroups take 3 at least. One matrix
+//    of 8192 x 8192, 17 / 64 / 128 / 256 rows 25.7 / 47 / 90 / 176; 2048 x 6144 (N, K), 64 / 256 rows 11.4 / 35; 64 of
+//    2048 x 2048, 1024 rows 71; SwiGLU of 256 of 2048 x 6144, 512 / 2048 rows 928 / 1166.
+//  - lines takes 2 for a unit's ends and a time a block of columns: tiles of 128 rows 0.78 while they leave half of
+//    the CUs idle, 1.03 where they do not, of 256 rows 1.8, for 32-bit results 1.5 to 1.85; and 5.4 TB/s. 8192 x 8192:
+//    17 to 512 rows 56 (f32 103 to 108), 1024 rows 72 against 103 for tiles of 256, 2048 rows 135 against 121, 8192
+//    rows 534 against 453; 2048 x 6144, 17 to 256 rows 43; 64 of 2048 x 2048, 1024 rows 49; the SwiGLU of 256 988 /
+//    1102.
+// few_rows with 16 matrix rows a workgroup in place of 32 where that leaves no more workgroups than CUs.
+Fp8Kernel choose_fp8_kernel(const Fp8GemmArgs& a, bool swiglu, bool wide) {
     const int64_t experts = a.offsets ? std::min(a.E, a.rows) : 1;
-    const double per = (double)a.rows / experts;
-    const int cols = swiglu ? 128 : 256;
-    auto units = [&](int bm) { return experts * (int64_t)std::ceil(per / bm) * ((a.N + cols - 1) / cols); };
-    if (per <= 4 || (per <= 32 && units(128) < kCus)) return kFp8FewRows4;
-    return per >= 512 ? kFp8Lines256 : kFp8Lines128;
+    const double per = (double)a.rows / experts, KB = (double)fp8_blocks(a.K);
+    const double bytes = (double)experts * a.N * a.K * (swiglu ? 2 : 1);
+    // (an expert's last tile is half full on average)
+    auto tiles = [&](int rows) { return a.offsets ? std::max(1.0, per / rows + 0.5) : std::ceil(per / rows); };
+    auto units = [&](int rows) { return experts * tiles(rows) * std::ceil(a.N / (swiglu ? 128.0 : 256.0)); };
+    auto line_us = [&](int rows, double block, double idle) {
+        const double u = units(rows);
+        return 4 + std::max((2 + KB * (u <= kCus / 2 ? idle : block)) * std::ceil(u / kCus), bytes / 5.4e6);
+    };
+    const double again = a.offsets ? std::max(0.0, per / kFrag - 0.4) : tiles(kFrag) - 1;
+    const double groups = experts * (1 + again) * std::ceil(a.N / (swiglu ? 16.0 : 32.0));
+    const double few = 3 + std::max({1.3 * a.K / 1024, bytes / 5.5e6 + again * bytes / 6e6, 3 * groups / 1024});
+    const double l128 = wide ? line_us(128, 1.85, 1.5) : line_us(128, 1.03, 0.78);
+    const double l256 = wide ? l128 : line_us(256, 1.8, 1.7);
+    if (few < std::min(l128, l256)) {
+        const bool half = !swiglu && experts * tiles(kFrag) * std::ceil(a.N / 16.0) <= kCus;
+        return half ? kFp8FewRows16 : kFp8FewRows32;
+    }
+    return l256 < l128 ? kFp8Lines256 : kFp8Lines128;
 }
 
 size_t fp8_swiglu_ws(const Fp8GemmArgs& a) {
-    const Fp8Kernel k = choose_fp8_kernel(a, true);
-    const bool two = (k == kFp8FewRows2 || k == kFp8FewRows4) && few_rows_blocks(a) < kCus;
+    const bool two = choose_fp8_kernel(a, true, false) == kFp8FewRows32 && few_rows_blocks(a) < kCus;
     return two ? (size_t)a.rows * a.N * 4 : 0;
 }
 

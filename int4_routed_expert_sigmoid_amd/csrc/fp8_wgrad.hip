@@ -5,6 +5,10 @@
 // The scales are powers of two and go into the matrix instruction (one E8M0 byte for each row of an
 // operand and block), or into the conversion to bf16 for 32-bit results (fp8.h), so that sums stay in
 // the instruction's registers from block to block.
+//
+// What bounds it: the gradients that it writes where experts have few rows (64 experts of 2048 x 6144, 256 rows each,
+// one MI355X: 3.2 GB of f32 in 828 us, 3.9 TB/s; bf16 417), the bf16 matrix instructions where there are many and results have 32
+// bits (6144 x 8192 from 4095 rows, 0.41 TFLOP: 343 us, 1.2 PFLOP/s, where a large bf16 product reaches 1.34).
 #include <algorithm>
 
 #include "fp8.h"
@@ -16,7 +20,8 @@ namespace {
 // fp8_gemm.hip's lines: codes and scales straight into LDS, a block of 128 rows at a time, STAGES blocks
 // ahead and on into the workgroup's next unit (a tile of one expert's gradient, whose sum has as many
 // blocks as the expert has rows for, none where it has no rows). x is the first operand: a lane's four
-// results are four neighbouring k.
+// results are four neighbouring k. Results of 32 bits have tiles of 128 n in three stages (256 would leave the operands'
+// bf16 form no registers), the others of 256 in two.
 template <typename T, int MT, int NF, int WM, int WN, int STAGES>
 struct WgradTile {
     static constexpr int BM = WM * MT * kFrag, BN = WN * NF * kFrag, kWaves = WM * WN, kThreads = 64 * kWaves;
@@ -60,7 +65,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(Fp8WgradArgs a, 
         if (x >= per || w >= total) return u;
         u.e = w / per_expert;
         const uint32_t rest = w - u.e * per_expert;
-        // blocks of kTall tiles of n by all of k, n first: neighbouring units write neighbouring columns
+        // blocks of kTall tiles of n by all of k, n first: neighbouring units write neighbouring columns (the pass of
+        // 64 experts' gradients, input gradients included: 1234 us; 1299 for one tile after the other)
         const uint32_t block = rest / (kTall * KT), in = rest - block * kTall * KT;
         const uint32_t tall = min(kTall, NT - block * kTall);
         u.k_tile = in / tall * W::BN;

@@ -98,6 +98,7 @@ def test_product_refusals(L):
     assert wg(N=24) == EINVAL and wg(K=24) == EINVAL and wg(N=0) == EINVAL and wg(K=0) == EINVAL
     assert wg(dt=3) == EUNSUP and wg(ld=31) == EINVAL and wg(ld=1 << 56) == EUNSUP and wg(N=1 << 30) == EUNSUP
     assert wg(dw=None) == EINVAL and wg(g=None) == EINVAL and wg(xs=None) == EINVAL and wg(g=24) == EINVAL
+    assert wg(gs=18) == EINVAL and wg(xs=17) == EINVAL
     assert wg(rows=0, acc=1, g=None, gs=None, x=None, xs=None) == OK
     assert L.coli_moe_dispatch_fp8(16, 0, 2, 2, 40, 40, 16, 16, 16, None) == EINVAL
     assert L.coli_moe_dispatch_fp8(16, 0, 2, 2, 32, 31, 16, 16, 16, None) == EINVAL
@@ -175,3 +176,39 @@ def test_reference_route_gradient():
                 d[:, e] = 1e-5
                 diff = (f(logits + d) - f(logits - d)) / 2e-5
                 assert np.abs(got[:, e] - diff).max() < 1e-8
+
+
+def test_cases_reach_every_kernel():
+    """The sizes of the products' tests run the kernels that they are named after, SwiGLU's reach all but the first too."""
+    from tests.fp8_cases import CASES
+    reached = {False: set(), True: set()}
+    for kernel, wide, counts, K, N, before, behind in CASES:
+        one = isinstance(counts, int)
+        rows, E = (counts, 1) if one else (sum(counts) + before + behind, len(counts))
+        assert coli.debug_fp8_kernel(rows, K, E, N, grouped=not one) == kernel
+        assert coli.debug_fp8_kernel(rows, K, E, N, grouped=not one, wide=True) == wide
+        for w in (False, True):
+            reached[w].add(coli.debug_fp8_kernel(rows, K, E, N, grouped=not one, swiglu=True, wide=w))
+    assert {c[0] for c in CASES} == set(coli.FP8_KERNELS) and {c[1] for c in CASES} == set(coli.FP8_KERNELS[:3])
+    assert reached[False] == set(coli.FP8_KERNELS[1:]) and reached[True] == set(coli.FP8_KERNELS[1:3])
+
+
+def test_kernel_choice():
+    """The choice follows times measured on both sides (graphs, warm caches; us)."""
+    def pick(rows, K, E, N, **how):
+        return coli.debug_fp8_kernel(rows, K, E, N, grouped=E > 1, **how)
+
+    assert pick(64, 8192, 1, 8192) == "few_rows_32"                 # 47 against 56
+    assert pick(128, 8192, 1, 8192) == "lines_128"                  # 56 against 90
+    assert pick(128, 8192, 1, 8192, wide=True) == "few_rows_32"     # 91 against 105
+    assert pick(192, 8192, 1, 8192, wide=True) == "lines_128"       # 107 against 134
+    assert pick(1024, 8192, 1, 8192) == "lines_128"                 # 72 against 103 for tiles of 256
+    assert pick(2048, 8192, 1, 8192) == "lines_256"                 # 121 against 135 for tiles of 128
+    assert pick(8192, 8192, 1, 8192) == "lines_256"                 # 453 against 534
+    assert pick(256, 2048, 1, 6144) == "lines_128"                  # 20 against 36
+    assert pick(256, 6144, 1, 2048) == "few_rows_32"                # 35 against 43
+    assert pick(512, 6144, 1, 2048) == "lines_128"                  # 45 against 68
+    assert pick(1024, 2048, 64, 2048) == "lines_128"                # 49 against 71
+    assert pick(256, 2048, 16, 1024, wide=True) == "few_rows_32"    # 14 against 33
+    assert pick(512, 6144, 256, 2048, swiglu=True) == "few_rows_32"     # 928 against 988
+    assert pick(2048, 6144, 256, 2048, swiglu=True) == "lines_128"      # 1102 against 1166

@@ -237,29 +237,57 @@ def test_quantize_past_32_bits(coli):
 
 
 # ---------------------------------------------------------------- products
+# (Their 64-bit forms are elementary torch operations on the device: sizes that reach every kernel are large for numpy.)
+def _codes(rng, *shape):
+    """Codes of normal values near the end of the range, as a block's quantised ones are."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(int(rng.integers(1 << 31)))
+    x = 110 * torch.randn(*shape, device="cuda", generator=g)
+    return x.clamp_(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+
+
+def _values(q, s, block_rows=1):
+    import torch
+    v = torch.from_numpy(ref.CODES).cuda()[q.long()]
+    s = s.double().repeat_interleave(128, -1)[..., :q.shape[-1]]
+    return v * (s if block_rows == 1 else s.repeat_interleave(128, -2)[..., :q.shape[-2], :])
+
+
+def _scales(rng, mean, *shape):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(int(rng.integers(1 << 31)))
+    return mean * (0.5 + torch.rand(*shape, device="cuda", generator=g))
+
+
 def _weights(rng, E, n, K, parts=1):
-    """Blobs of `parts` FP8 matrices each with any scales, 16 bytes of something before them; (blobs, table, matrices, offsets)."""
+    """Blobs of `parts` FP8 matrices each with any scales, 16 bytes of something before them; (blobs, table, a function of the
+    matrix' values, offsets)."""
     import torch
     nb, nk = -(-n // 128), -(-K // 128)
     s_off = 16 + parts * n * K + (-parts * n * K) % 4 + 4
     size = -(-(s_off + 4 * parts * nb * nk) // 16) * 16
-    blobs = np.full((E, size), 0x7F, np.uint8)                    # NaN wherever a product should not read
-    mats = []
-    for e in range(E):
-        q = ref.encode(np.clip(110 * rng.standard_normal((parts, n, K)), -448, 448))
-        s = (2e-3 * (0.5 + rng.random((parts, nb, nk)))).astype(np.float32)
-        blobs[e, 16:16 + q.size] = q.reshape(-1)
-        blobs[e, s_off:s_off + 4 * s.size] = s.reshape(-1).view(np.uint8)
-        mats.append([ref.values(q[p], s[p], 128) for p in range(parts)])
-    dev = _dev(blobs)
-    table = dev.data_ptr() + size * torch.arange(E, dtype=torch.int64)
-    return dev, table.cuda(), mats, dict(q_off=16, s_off=s_off)
+    blobs = torch.full((E, size), 0x7F, dtype=torch.uint8, device="cuda")    # NaN wherever a product should not read
+    q, s = _codes(rng, E, parts, n, K), _scales(rng, 2e-3, E, parts, nb, nk)
+    blobs[:, 16:16 + parts * n * K] = q.flatten(1)
+    blobs[:, s_off:s_off + 4 * parts * nb * nk] = s.flatten(1).view(torch.uint8)
+    table = blobs.data_ptr() + size * torch.arange(E, dtype=torch.int64)
+    return blobs, table.cuda(), lambda e, p=0: _values(q[e, p], s[e, p], 128), dict(q_off=16, s_off=s_off)
 
 
-def _rows(rng, rows, K):
-    q = ref.encode(np.clip(110 * rng.standard_normal((rows, K)), -448, 448))
-    s = (0.01 * (0.5 + rng.random((rows, -(-K // 128))))).astype(np.float32)
-    return _dev(q), _dev(s), ref.values(q, s)
+def _rows(rng, rows, K, mean=0.01):
+    q, s = _codes(rng, rows, K), _scales(rng, mean, rows, -(-K // 128))
+    return q, s, _values(q, s)
+
+
+def _product(a, matrix, off, n, p=0):
+    """(y, sum of |terms|) [rows][n]; rows outside the offsets are 0."""
+    y = a.new_zeros(a.shape[0], n)
+    t = a.new_zeros(a.shape[0], n)
+    for e, (lo, hi) in enumerate(zip(off[:-1], off[1:])):
+        if hi > lo:
+            m = matrix(e, p).t().contiguous()
+            y[lo:hi], t[lo:hi] = a[lo:hi] @ m, a[lo:hi].abs() @ m.abs()
+    return y, t
 
 
 def _groups(counts, before, behind):
@@ -270,75 +298,87 @@ def _groups(counts, before, behind):
 
 
 def _case_id(c):
-    return f"{c[0]}-{c[1] if isinstance(c[1], int) else len(c[1])}-{c[2]}-{c[3]}"
+    return f"{c[0]}-{c[2] if isinstance(c[2], int) else len(c[2])}-{c[3]}-{c[4]}"
+
+
+def _half(dtype, y):
+    """_rounding of a tensor."""
+    import torch
+    return (_half_step(dtype) * y.abs()).clamp_min(torch.finfo(_t(dtype)).tiny * _half_step(dtype))
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("case", CASES, ids=_case_id)
 def test_matmul(coli, case, dtype):
     import torch
-    kernel, counts, K, n, before, behind = case
+    kernel, wide, counts, K, n, before, behind = case
     offsets, off, rows = _groups(counts, before, behind)
-    E = len(off) - 1
-    assert kernel == "" or rows == 0 or coli.debug_fp8_kernel(rows, K, E, n, grouped=offsets is not None) == kernel
+    E, exact = len(off) - 1, dtype == "float32"
+    assert coli.debug_fp8_kernel(rows, K, E, n, grouped=offsets is not None, wide=exact) == (wide if exact else kernel)
     rng = np.random.default_rng(K + n)
-    _keep, table, mats, at = _weights(rng, E, n, K)
+    _keep, table, matrix, at = _weights(rng, E, n, K)
     a, a_s, va = _rows(rng, rows, K)
     out = torch.full((rows, n + 3), 7.0, dtype=_t(dtype), device="cuda")
     coli.fp8_matmul(a, a_s, table, n, offsets=offsets, out=out[:, :n], **at)
-    y, terms = ref.product(va, [m[0] for m in mats], off)
-    got, lo, hi = _host(out), int(off[0]), int(off[-1])
-    assert (got[:, n:] == 7.0).all() and (got[:lo] == 7.0).all() and (got[hi:] == 7.0).all()
-    err = np.abs(got[lo:hi, :n] - y[lo:hi])
-    assert _within(err, ref.product_bound(K, terms[lo:hi], dtype == "float32") * (1 + _half_step(dtype)) + _rounding(dtype, y[lo:hi]))
-    if hi > lo:
-        assert np.linalg.norm(err) <= (ref.norm_bound(K, dtype == "float32") + _half_step(dtype)) * np.linalg.norm(y[lo:hi])
+    y, terms = _product(va, matrix, off, n)
+    lo, hi = int(off[0]), int(off[-1])
+    assert bool((out[:, n:] == 7.0).all()) and bool((out[:lo] == 7.0).all()) and bool((out[hi:] == 7.0).all())
+    err, y = (out[lo:hi, :n].double() - y[lo:hi]).abs(), y[lo:hi]
+    assert bool((err <= ref.product_bound(K, terms[lo:hi], exact) * (1 + _half_step(dtype)) + _half(dtype, y)).all())
+    assert float(err.norm()) <= (ref.norm_bound(K, exact) + _half_step(dtype)) * float(y.norm())
     again = coli.fp8_matmul(a, a_s, table, n, offsets=offsets, dtype=_t(dtype), **at)
     assert torch.equal(again[lo:hi], out[lo:hi, :n])
+
+
+def _scale_of(top):
+    """The quantiser's scale for a block whose largest is `top` (64 bits)."""
+    import torch
+    return torch.from_numpy(ref.scale_value(ref.scale_code(top.cpu().numpy()))).cuda()
 
 
 @pytest.mark.parametrize("dtype", DTYPES + ("fp8",))
 @pytest.mark.parametrize("case", CASES, ids=_case_id)
 def test_swiglu(coli, case, dtype):
     import torch
-    _, counts, K, n, before, behind = case
+    _, _, counts, K, n, before, behind = case
     n = -(-n // 16) * 16 if dtype == "fp8" else n
     offsets, off, rows = _groups(counts, before, behind)
-    E = len(off) - 1
+    E, exact = len(off) - 1, dtype == "float32"
     rng = np.random.default_rng(K + n + 1)
-    _keep, table, mats, at = _weights(rng, E, n, K, parts=2)
-    a, a_s, va = _rows(rng, rows, K)
-    va, a_s = va * (8 / np.sqrt(K)), a_s * np.float32(8 / np.sqrt(K))
-    va = ref.values(a.cpu().numpy(), _host(a_s))
-    exact = dtype == "float32"
-    g, tg = ref.product(va, [m[0] for m in mats], off)
-    u, tu = ref.product(va, [m[1] for m in mats], off)
+    _keep, table, matrix, at = _weights(rng, E, n, K, parts=2)
+    a, a_s, va = _rows(rng, rows, K, 0.08 / np.sqrt(K))
+    g, tg = _product(va, matrix, off, n, 0)
+    u, tu = _product(va, matrix, off, n, 1)
     eg, eu = ref.product_bound(K, tg, exact), ref.product_bound(K, tu, exact)
-    h = ref.silu(g) * u
-    err = 1.1 * eg * (np.abs(u) + eu) + (np.abs(ref.silu(g))) * eu + 16 * 2.0 ** -24 * np.abs(h)
+    silu = g / (1 + torch.exp(-g))
+    h = silu * u
+    err = 1.1 * eg * (u.abs() + eu) + silu.abs() * eu + 16 * 2.0 ** -24 * h.abs()
     lo, hi = int(off[0]), int(off[-1])
     if dtype != "fp8":
         out = torch.full((rows, n + 3), 7.0, dtype=_t(dtype), device="cuda")
         coli.fp8_swiglu(a, a_s, table, n, offsets=offsets, out=out[:, :n], **at)
-        got = _host(out)
-        assert (got[:, n:] == 7.0).all() and (got[:lo] == 7.0).all() and (got[hi:] == 7.0).all()
-        assert _within(np.abs(got[:, :n] - h)[lo:hi], (err * (1 + _half_step(dtype)) + _rounding(dtype, h))[lo:hi])
+        assert bool((out[:, n:] == 7.0).all()) and bool((out[:lo] == 7.0).all()) and bool((out[hi:] == 7.0).all())
+        assert bool(((out[:, :n].double() - h).abs() <= err * (1 + _half_step(dtype)) + _half(dtype, h))[lo:hi].all())
         return
-    q = torch.full((rows, n), 77, dtype=torch.uint8, device="cuda")
-    s = torch.full((rows, -(-n // 128)), 77.0, device="cuda")
-    coli.fp8_swiglu(a, a_s, table, n, offsets=offsets, out=(q, s), **at)
-    assert bool((q[:lo] == 77).all()) and bool((q[hi:] == 77).all()) and bool((s[:lo] == 77.0).all()) and bool((s[hi:] == 77.0).all())
-    s = _host(s)
-    for b in range(s.shape[1] if hi > lo else 0):
-        cols = slice(b * 128, (b + 1) * 128)
-        low = ref.scale_value(ref.scale_code(np.maximum(np.abs(h[lo:hi, cols]) - err[lo:hi, cols], 0).max(1)))
-        high = ref.scale_value(ref.scale_code((np.abs(h[lo:hi, cols]) + err[lo:hi, cols]).max(1)))
-        assert (low <= s[lo:hi, b]).all() and (s[lo:hi, b] <= high).all()
-    v = ref.values(q.cpu().numpy(), s)
-    step = np.maximum(2.0 ** -4 * (np.abs(h) + err), 2.0 ** -10 * s.repeat(128, 1)[:, :n])
-    assert _within(np.abs(v - h)[lo:hi], (err + step)[lo:hi])
     new = coli.fp8_swiglu(a, a_s, table, n, offsets=offsets, dtype="fp8", **at)
-    assert torch.equal(new[0][lo:hi], q[lo:hi])
+    up = (at["q_off"] + n * K, at["s_off"] + 4 * -(-n // 128) * -(-K // 128))
+    for workspace in (True, False):                               # without the one that few rows may use: one launch, sums in another order
+        q = torch.full((rows, n), 77, dtype=torch.uint8, device="cuda")
+        s = torch.full((rows, -(-n // 128)), 77.0, device="cuda")
+        if workspace:
+            coli.fp8_swiglu(a, a_s, table, n, offsets=offsets, out=(q, s), **at)
+            assert torch.equal(new[0][lo:hi], q[lo:hi]) and torch.equal(new[1][lo:hi], s[lo:hi])
+        elif rows:
+            assert coli.lib().coli_fp8_swiglu(a.data_ptr(), a_s.data_ptr(), rows, K, None if offsets is None else offsets.data_ptr(), E,
+                                              table.data_ptr(), at["q_off"], at["s_off"], *up, n, q.data_ptr(), s.data_ptr(), coli.FP8,
+                                              n, None, 0, coli._stream()) == 0
+        assert bool((q[:lo] == 77).all()) and bool((q[hi:] == 77).all()) and bool((s[:lo] == 77.0).all()) and bool((s[hi:] == 77.0).all())
+        for b in range(s.shape[1] if hi > lo else 0):
+            part, e = h[lo:hi, b * 128:(b + 1) * 128].abs(), err[lo:hi, b * 128:(b + 1) * 128]
+            sb = s[lo:hi, b].double()
+            assert bool((_scale_of((part - e).clamp_min(0).amax(1)) <= sb).all()) and bool((sb <= _scale_of((part + e).amax(1))).all())
+        step = torch.maximum(2.0 ** -4 * (h.abs() + err), 2.0 ** -10 * s.double().repeat_interleave(128, 1)[:, :n])
+        assert bool(((_values(q, s) - h).abs() <= err + step)[lo:hi].all())
 
 
 def test_separate_gate_and_up(coli):
@@ -372,6 +412,61 @@ def test_not_finite(coli):
             want = torch.zeros(40, 33, dtype=torch.bool, device="cuda")
             want[3], want[5], want[:, 7] = True, True, True
             assert torch.equal(y, want)
+
+
+def test_products_past_32_bits(coli):
+    """Rows, matrices and outputs that lie beyond 2^32 bytes or 2^31 values: codes 1, scales 1 and 2, so that sums are whole."""
+    import torch
+    one = 0x38
+    rows, n = 40000, 65552                                        # 2.6e9 outputs
+    a = torch.full((rows, 16), one, dtype=torch.uint8, device="cuda")
+    a_s = torch.ones(rows, 1, device="cuda")
+    a_s[-1] = 2.0
+    blob = torch.full((n * 16 + 4 * 513,), one, dtype=torch.uint8, device="cuda")
+    blob[n * 16:] = torch.ones(513, device="cuda").view(torch.uint8)
+    table = torch.tensor([blob.data_ptr()], device="cuda")
+    for dtype in (torch.bfloat16, torch.float32):
+        y = coli.fp8_matmul(a, a_s, table, n, s_off=n * 16, dtype=dtype)
+        assert y.max().item() == 32.0 and bool((y[-1] == 32.0).all()) and bool((y[:-1:997] == 16.0).all()) and y[-2].min().item() == 16.0
+        del y
+    rows, K, n = 70000, 65536, 144                                # 4.6e9 codes of rows
+    a = torch.zeros(rows, K, dtype=torch.uint8, device="cuda")
+    a[-1], a[-2, -1] = one, one
+    a_s = torch.ones(rows, 512, device="cuda")
+    w = torch.full((n * K + 4 * 1024,), one, dtype=torch.uint8, device="cuda")
+    w[n * K:] = torch.ones(1024, device="cuda").view(torch.uint8)
+    table = torch.tensor([w.data_ptr()], device="cuda")
+    off = torch.tensor([0, rows - 3, rows], dtype=torch.int32, device="cuda")
+    for kw in (dict(), dict(offsets=off)):
+        y = coli.fp8_matmul(a, a_s, table.repeat(2) if kw else table, n, s_off=n * K, dtype=torch.bfloat16, **kw)
+        assert bool((y[-1] == 65536.0).all()) and bool((y[-2] == 1.0).all()) and bool((y[:-2] == 0).all())
+    del a, y
+    n = 70000                                                     # 4.6e9 codes of a matrix, and one row
+    w = torch.zeros(n * K + 4 * 547 * 512, dtype=torch.uint8, device="cuda")
+    w[(n - 1) * K:n * K] = one
+    w[n * K:].view(torch.float32).fill_(2.0)
+    table = torch.tensor([w.data_ptr()], device="cuda")
+    for rows in (1, 300):
+        a, a_s = torch.full((rows, K), one, dtype=torch.uint8, device="cuda"), torch.ones(rows, 512, device="cuda")
+        y = coli.fp8_matmul(a, a_s, table, n, s_off=n * K)
+        assert bool((y[:, -1] == 131072.0).all()) and bool((y[:, :-1] == 0).all())
+
+
+def test_wgrad_past_32_bits(coli):
+    import torch
+    E, n, K = 3, 30016, 30000                                     # 2.7e9 gradients
+    g, x = torch.zeros(4, n, device="cuda"), torch.ones(4, K, device="cuda")
+    g[-1, -1] = 2.0
+    off = torch.tensor([0, 1, 1, 4], dtype=torch.int32, device="cuda")
+    for dtype in (torch.bfloat16, torch.float32):
+        dw = coli.fp8_wgrad(*coli.quantize_fp8_columns(g, off), *coli.quantize_fp8_columns(x, off), off, dtype=dtype)
+        assert bool((dw[2, -1] == 2.0).all()) and bool((dw[2, :-1] == 0).all()) and bool((dw[:2] == 0).all())
+        del dw
+    rows, n, K = 40000, 65552, 16                                 # 2.6e9 codes of columns, 16-bit: 2^32 bytes of values
+    g, x = torch.zeros(rows, n, dtype=torch.bfloat16, device="cuda"), torch.ones(rows, K, device="cuda")
+    g[-1, -1], g[0, 0] = 2.0, 3.0
+    dw = coli.fp8_wgrad(*coli.quantize_fp8_columns(g), *coli.quantize_fp8_columns(x), rows=rows)
+    assert bool((dw[0, -1] == 2.0).all()) and bool((dw[0, 0] == 3.0).all()) and bool((dw[0, 1:-1] == 0).all())
 
 
 # ---------------------------------------------------------------- gradients
