@@ -612,14 +612,14 @@ Fp8Kernel choose_fp8_kernel(const Fp8GemmArgs& a, bool swiglu, bool wide) {
     const int64_t experts = a.offsets ? std::min(a.E, a.rows) : 1;
     const double per = (double)a.rows / experts, KB = (double)fp8_blocks(a.K);
     const double bytes = (double)experts * a.N * a.K * (swiglu ? 2 : 1);
-    // (an expert's last tile is half full on average)
-    auto tiles = [&](int rows) { return a.offsets ? std::max(1.0, per / rows + 0.5) : std::ceil(per / rows); };
+    // (of several experts, the last tile of each is half full on average)
+    auto tiles = [&](int rows) { return experts > 1 ? std::max(1.0, per / rows + 0.5) : std::ceil(per / rows); };
     auto units = [&](int rows) { return experts * tiles(rows) * std::ceil(a.N / (swiglu ? 128.0 : 256.0)); };
     auto line_us = [&](int rows, double block, double idle) {
         const double u = units(rows);
         return 4 + std::max((2 + KB * (u <= kCus / 2 ? idle : block)) * std::ceil(u / kCus), bytes / 5.4e6);
     };
-    const double again = a.offsets ? std::max(0.0, per / kFrag - 0.4) : tiles(kFrag) - 1;
+    const double again = experts > 1 ? std::max(0.0, per / kFrag - 0.4) : tiles(kFrag) - 1;
     const double groups = experts * (1 + again) * std::ceil(a.N / (swiglu ? 16.0 : 32.0));
     const double few = 3 + std::max({1.3 * a.K / 1024, bytes / 5.5e6 + again * bytes / 6e6, 3 * groups / 1024});
     const double l128 = wide ? line_us(128, 1.85, 1.5) : line_us(128, 1.03, 0.78);
