@@ -469,7 +469,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a
             if constexpr (!SWIGLU) {
                 const int m0 = (i * WM + wm) * kFrag;
                 if (n_wave + NF * kFrag <= a.N) {         // uniform
-                    store64<Out, false>((Out*)a.y + (int64_t)(u.m0 + m0) * a.ld + n_wave, a.ld, u.rows - m0, acc[i][0], acc[i][1],
+                    store64<Out>((Out*)a.y + (int64_t)(u.m0 + m0) * a.ld + n_wave, a.ld, u.rows - m0, acc[i][0], acc[i][1],
                                         acc[i][2], acc[i][3]);
                 } else if (there) {
 #pragma unroll

@@ -7,8 +7,9 @@
 // the instruction's registers from block to block.
 //
 // What bounds it: the gradients that it writes where experts have few rows (64 experts of 2048 x 6144, 256 rows each,
-// one MI355X: 3.2 GB of f32 in 828 us, 3.9 TB/s; bf16 417), the bf16 matrix instructions where there are many and results have 32
-// bits (6144 x 8192 from 4095 rows, 0.41 TFLOP: 343 us, 1.2 PFLOP/s, where a large bf16 product reaches 1.34).
+// one MI355X: 3.2 GB of f32 in 780 us, 4.1 TB/s, added to what is there 1244, 5.2 TB/s; bf16 417 and 782), the bf16 matrix
+// instructions where there are many and results have 32 bits (6144 x 8192 from 4095 rows, 0.41 TFLOP: 337 us, 1.22
+// PFLOP/s, where a large bf16 product reaches 1.34; bf16 162, 2.5 PFLOP/s).
 #include <algorithm>
 
 #include "fp8.h"
@@ -21,7 +22,8 @@ namespace {
 // ahead and on into the workgroup's next unit (a tile of one expert's gradient, whose sum has as many
 // blocks as the expert has rows for, none where it has no rows). x is the first operand: a lane's four
 // results are four neighbouring k. Results of 32 bits have tiles of 128 n in three stages (256 would leave the operands'
-// bf16 form no registers), the others of 256 in two.
+// bf16 form no registers), the others of 256 in two. Where they are added to what is there (ADD), which is loaded at a
+// tile's end all at once (row by row: 1880 us for the 1244 above), all have 128.
 template <typename T, int MT, int NF, int WM, int WN, int STAGES>
 struct WgradTile {
     static constexpr int BM = WM * MT * kFrag, BN = WN * NF * kFrag, kWaves = WM * WN, kThreads = 64 * kWaves;
@@ -40,13 +42,11 @@ struct WgradTile {
     };
 };
 
-constexpr uint32_t kTall = 2;
-
 struct WgradUnit {
     int e, n_tile, k_tile, first, count;     // count -1: no unit
 };
 
-template <typename T, int MT, int NF, int WM, int WN, int STAGES>
+template <typename T, int MT, int NF, int WM, int WN, int STAGES, bool ADD>
 __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(Fp8WgradArgs a, int NT, int KT) {
     typedef WgradTile<T, MT, NF, WM, WN, STAGES> W;
     constexpr int U = W::U;
@@ -57,26 +57,28 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(Fp8WgradArgs a, 
 
     const RowGroups groups = {a.offsets, nullptr, a.rows, a.E};
     const int blocks = min((int)scan_units<kFp8Block, W::kThreads>(groups, 1, lds.first, lds.scale[0][0]), a.blocks);
-    const uint32_t per_expert = (uint32_t)NT * KT, total = per_expert * a.E, per = (total + kXcds - 1) / kXcds;
-    const uint32_t xcd = blockIdx.x % kXcds, step = gridDim.x / kXcds;
-    auto unit_at = [&](uint32_t x) {
-        const uint32_t w = xcd * per + x;
+    const uint32_t per_expert = (uint32_t)NT * KT, total = per_expert * a.E;
+    // Units in order of expert, stretches of `tall` tiles of n, k, n, round all workgroups, and with them round the XCDs: the
+    // device writes neighbouring tiles at a time. With KT a multiple of 4 and tall 1 an XCD reads an eighth or a
+    // quarter of x's columns, with tall 8 a stretch of its own of g's. (An eighth of the units for each XCD in place of
+    // it: 64 experts' 2048 x 6144 in f32 799 us in place of 780, 16 of 2048 x 6400 326 in place of 298, 4 of 5008 x 1280
+    // in bf16 251 in place of 213; tall 1 where KT is 7 184 in place of 177, tall 8 where it is 32 367 in place of 349.)
+    const uint32_t tall = KT % 4 == 0 ? 1 : 8;
+    auto unit_at = [&](uint32_t w) {
         WgradUnit u = {0, 0, 0, 0, -1};
-        if (x >= per || w >= total) return u;
+        if (w >= total) return u;
         u.e = w / per_expert;
         const uint32_t rest = w - u.e * per_expert;
-        // blocks of kTall tiles of n by all of k, n first: neighbouring units write neighbouring columns (the pass of
-        // 64 experts' gradients, input gradients included: 1234 us; 1299 for one tile after the other)
-        const uint32_t block = rest / (kTall * KT), in = rest - block * kTall * KT;
-        const uint32_t tall = min(kTall, NT - block * kTall);
-        u.k_tile = in / tall * W::BN;
-        u.n_tile = (block * kTall + in % tall) * W::BM;
+        const uint32_t block = rest / (tall * KT), in = rest - block * tall * KT, high = min(tall, NT - block * tall);
+        u.n_tile = (block * tall + in % high) * W::BM;
+        u.k_tile = in / high * W::BN;
         // (offsets that are not ascending may count more blocks than there are)
         u.first = min(__builtin_amdgcn_readfirstlane((int)lds.first[u.e]), blocks);
         u.count = (u.e + 1 < a.E ? min(__builtin_amdgcn_readfirstlane((int)lds.first[min(u.e + 1, a.E - 1)]), blocks) : blocks) - u.first;
         return u;
     };
-    uint32_t at = blockIdx.x / kXcds;        // this workgroup's units: at, at + step, ... of its XCD's `per`
+    uint32_t at = blockIdx.x;                // this workgroup's units: at, at + step, ...
+    const uint32_t step = gridDim.x;
     WgradUnit u = unit_at(at);
     if (u.count < 0) return;
 
@@ -233,13 +235,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(Fp8WgradArgs a, 
             advance();
         }
         const int k_wave = u.k_tile + wn * NF * kFrag;
+        const bool whole = k_wave + NF * kFrag <= a.K;                        // uniform
+        auto row_at = [&](int i) { return (T*)a.dw + ((int64_t)u.e * a.N + u.n_tile + (i * WM + wm) * kFrag) * a.ld + k_wave; };
+        if (ADD && whole) {                  // all loads before the first is waited for
+            Old64<T> old[MT];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) old[i].load(row_at(i), a.ld, a.N - u.n_tile - (i * WM + wm) * kFrag);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                old[i].add_to(acc[i]);
+                if constexpr (!EXACT) hold(acc[i]);      // (one after the other: fewer registers)
+            }
+        }
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             const int n0 = u.n_tile + (i * WM + wm) * kFrag, n = n0 + r;
-            T* row = (T*)a.dw + ((int64_t)u.e * a.N + n0) * a.ld + k_wave;
-            if ((EXACT || !a.accumulate) && k_wave + NF * kFrag <= a.K) {     // uniform
-                if (a.accumulate) store64<T, EXACT>(row, a.ld, a.N - n0, acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-                else store64<T, false>(row, a.ld, a.N - n0, acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+            T* row = row_at(i);
+            if (whole) {
+                store64<T>(row, a.ld, a.N - n0, acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
                 continue;
             }
             if (n >= a.N) continue;
@@ -248,7 +261,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(Fp8WgradArgs a, 
                 if (k_wave + f * kFrag + 4 * g >= a.K) continue;              // K comes in multiples of 16
                 T* p = row + r * a.ld + f * kFrag + 4 * g;
                 float v[4] = {acc[i][f][0], acc[i][f][1], acc[i][f][2], acc[i][f][3]};
-                if (a.accumulate) {
+                if (ADD) {
                     float o[4];
                     load_f32<T, 4>(p, o);
 #pragma unroll
@@ -265,14 +278,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(Fp8WgradArgs a, 
     wait_loads<0>();                         // nothing lands in LDS after the workgroup
 }
 
-template <typename T, int MT, int NF, int WM, int WN, int STAGES>
+template <typename T, int MT, int NF, int WM, int WN, int STAGES, bool ADD>
 coli_status wgrad(const Fp8WgradArgs& a, hipStream_t stream) {
     typedef WgradTile<T, MT, NF, WM, WN, STAGES> W;
     const int64_t NT = (a.N + W::BM - 1) / W::BM, KT = (a.K + W::BN - 1) / W::BN;
     if (NT * KT > INT32_MAX / a.E) return fail(COLI_EUNSUPPORTED, "fp8_wgrad: more than 2^31 tiles");
     constexpr int64_t kPerCu = 163840 / sizeof(typename W::Lds);
-    const uint32_t grid = (uint32_t)std::min<int64_t>(kCus * kPerCu, (NT * KT * a.E + kXcds - 1) / kXcds * kXcds);
-    launch(wgrad_kernel<T, MT, NF, WM, WN, STAGES>, dim3(grid), dim3(W::kThreads), 0, stream, a, (int)NT, (int)KT);
+    const uint32_t grid = (uint32_t)std::min<int64_t>(kCus * kPerCu, NT * KT * a.E);
+    launch(wgrad_kernel<T, MT, NF, WM, WN, STAGES, ADD>, dim3(grid), dim3(W::kThreads), 0, stream, a, (int)NT, (int)KT);
     COLI_CHECK_LAUNCH("fp8_wgrad kernel launch");
     return COLI_OK;
 }
@@ -282,8 +295,9 @@ coli_status wgrad(const Fp8WgradArgs& a, hipStream_t stream) {
 coli_status launch_fp8_wgrad(const Fp8WgradArgs& a, int32_t dtype, hipStream_t stream) {
     return with_elem(dtype, [&](auto e) -> coli_status {
         using T = decltype(e);
-        if constexpr (std::is_same<T, float>::value) return wgrad<T, 4, 4, 2, 4, 3>(a, stream);
-        else return wgrad<T, 8, 4, 2, 4, 2>(a, stream);
+        constexpr int MT = std::is_same<T, float>::value ? 4 : 8;
+        if (a.accumulate) return wgrad<T, 4, 4, 2, 4, 3, true>(a, stream);
+        return wgrad<T, MT, 4, 2, 4, MT == 4 ? 3 : 2, false>(a, stream);
     });
 }
 

@@ -58,6 +58,12 @@ __device__ __forceinline__ void swap_quarters(uint32_t& x, uint32_t& y) {
     x = b[0], y = b[1];
 }
 
+__device__ __forceinline__ void swap_quarters_back(uint32_t& x, uint32_t& y) {
+    const auto a = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(a[0], a[1], false, false);
+    x = b[0], y = b[1];
+}
+
 // Outputs n0 .. n0 + 31 (those below N) of row `m`, of which this lane holds n0 + 4 g
 // .. + 3 (lo) and n0 + 16 + 4 g .. + 3 (hi): for a 16-bit type one store of 16 bytes a
 // lane, 64 neighbouring bytes a row. Stores hold up the loads behind them, all of
@@ -102,9 +108,8 @@ __device__ __forceinline__ uint32_t merge_halves(uint32_t x, uint32_t y) {
 // a fragment's 16 rows, a store takes 8 rows by 128 bytes, so that no line is written in parts. A lane holds
 // row lane % 16; rows from `rows` on are left out. (3.2 GB of f32 by 16 rows of 64 bytes a store took 696 us, by whole
 // lines 624.) They go past the caches, which hold the operands (gradients of 64 experts' 2048 x 6144 matrices, 256 rows
-// each: 1136 us through them, 828 past them; in bf16 646 and 417). Two stores for a 16-bit type, four for f32; ADD: to
-// what is there.
-template <typename T, bool ADD>
+// each: 1136 us through them, 828 past them; in bf16 646 and 417). Two stores for a 16-bit type, four for f32.
+template <typename T>
 __device__ __forceinline__ void store64(T* out, int64_t ld, int rows, const f32x4& v0, const f32x4& v1, const f32x4& v2,
                                         const f32x4& v3) {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, row = r & 7;
@@ -146,18 +151,61 @@ __device__ __forceinline__ void store64(T* out, int64_t ld, int rows, const f32x
                 lo[i] = __uint_as_float(merge_halves<true>(a, b));
                 hi[i] = __uint_as_float(merge_halves<false>(a, b));
             }
-            if constexpr (ADD) {
-                float o[4] = {}, q[4] = {};
-                if (row < rows) load_f32<T, 4>(p + 16 * f, o);
-                if (row + 8 < rows) load_f32<T, 4>(p + 16 * f + 8 * ld, q);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) lo[i] += o[i], hi[i] += q[i];
-            }
             if (row < rows) store_f32_once<T, 4>(p + 16 * f, lo);
             if (row + 8 < rows) store_f32_once<T, 4>(p + 16 * f + 8 * ld, hi);
         }
     }
 }
+
+// What store64 would replace: loaded the same way, and added to the fragments (merge_halves is its own inverse).
+template <typename T>
+struct Old64 {
+    typedef uint32_t V __attribute__((ext_vector_type(4), aligned(2)));
+    V v[sizeof(T)];
+
+    __device__ __forceinline__ void load(const T* out, int64_t ld, int rows) {
+        constexpr int kStep = 16 / sizeof(T);        // of a lane, and columns of a store's half / 4
+        const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, row = r & 7;
+        const T* p = out + row * ld + (r >= 8 ? 4 * kStep : 0) + kStep * g;
+#pragma unroll
+        for (int x = 0; x < (int)sizeof(T); x += 2) {
+            v[x] = V{0, 0, 0, 0};
+            v[x + 1] = V{0, 0, 0, 0};
+            if (row < rows) v[x] = __builtin_nontemporal_load(reinterpret_cast<const V*>(p + 16 * x));
+            if (row + 8 < rows) v[x + 1] = __builtin_nontemporal_load(reinterpret_cast<const V*>(p + 16 * x + 8 * ld));
+        }
+    }
+
+    __device__ __forceinline__ void add_to(f32x4 (&acc)[4]) const {
+        if constexpr (sizeof(T) == 2) {
+            union Words {
+                T v[4];
+                uint32_t w[2];
+            } x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i / 2].w[i % 2] = merge_halves<true>(v[0][i], v[1][i]);
+                x[2 + i / 2].w[i % 2] = merge_halves<false>(v[0][i], v[1][i]);
+            }
+#pragma unroll
+            for (int f = 0; f < 4; f += 2)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) swap_quarters_back(x[f].w[i], x[f + 1].w[i]);
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[f][i] += (float)x[f].v[i];
+        } else {
+#pragma unroll
+            for (int f = 0; f < 4; f += 2)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc[f][i] += __uint_as_float(merge_halves<true>(v[f][i], v[f + 1][i]));
+                    acc[f + 1][i] += __uint_as_float(merge_halves<false>(v[f][i], v[f + 1][i]));
+                }
+        }
+    }
+};
 
 // Position of 16-byte unit b of row r in an LDS chunk of U units a row: the units
 // of a row are permuted by its number, so that the rows that a load reads at one

@@ -471,7 +471,7 @@ def test_wgrad_past_32_bits(coli):
 
 # ---------------------------------------------------------------- gradients
 WGRAD = [([3], 16, 16), ([128, 0, 129, 1], 144, 272), ([5, 40, 0, 260, 17], 64, 528), ([0, 0], 32, 16), ([1] * 9, 128, 128), (300, 272, 144),
-         ([700], 528, 400)]
+         ([700], 528, 400), ([5, 0, 130], 1168, 272), ([40, 3], 144, 1024)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
