@@ -4,9 +4,10 @@
 // A lane takes 16 bytes of values (4 or 8 columns), so that a block of a row is 32 or 16 lanes and
 // its largest |x| is theirs by DPP exchanges. Scales are powers of two (fp8.h): x / scale is exact
 // and e4m3's rounding (the hardware convert, half to even) is the only one. All of these are bound
-// by HBM. On one MI355X (a copy: 4.7 TB/s): 8191 rows of 6144 bf16, 153 MB, 22 us (out of the caches, in part); 16 matrices of
-// 6144 x 2048 f32 both ways round, 1.2 GB, 190 us (6.4 TB/s), and back from either, 103; the columns of 16381 rows
-// of 2048 in bf16, with the rows, 39.
+// by HBM. On one MI355X (a copy: 4.7 TB/s): 8191 rows of 6144 bf16, 153 MB, 22 us (out of the caches, in part);
+// 16 matrices of 6144 x 2048 f32 both ways round, 1.2 GB, 190 us (6.4 TB/s), and back from either, 103; the columns of
+// 16384 rows of 2048 bf16 by 64 experts, with the rows, 134 MB, 37, of 6144 without, 302 MB, 71 (48 and 98 with the
+// tile in f32, which leaves room for three workgroups a CU in place of six).
 #include "fp8.h"
 
 namespace coli {
@@ -141,22 +142,33 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __r
 }
 
 // ------------------------------------------------------------ tiles of 128 x 128
-// A workgroup holds a tile in registers: pass p of a thread is row p * kRows + tid / kLanes, columns
+// A workgroup holds a tile in registers, in its own type: pass p of a thread is row p * kRows + tid / kLanes, columns
 // kVec (tid % kLanes) on; what lies outside the matrix is 0.
 template <typename T>
 struct TileIn {
     static constexpr int N = kVec<T>, L = kLanes<T>, kRows = kThreads / L, kPasses = kFp8Block / kRows;
-    float v[kPasses][N];
+    typedef T V __attribute__((ext_vector_type(N), aligned(sizeof(T))));
+    u32x4 raw[kPasses];
     int c, r;
 
     __device__ __forceinline__ void load(const T* x, int64_t ld, int rows, int cols) {
         c = threadIdx.x % L * N, r = threadIdx.x / L;
 #pragma unroll
         for (int p = 0; p < kPasses; ++p) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[p][i] = 0.f;
-            if (p * kRows + r < rows && c < cols) load_f32_once<T, N>(x + (p * kRows + r) * ld + c, v[p]);
+            raw[p] = u32x4{0, 0, 0, 0};
+            if (p * kRows + r < rows && c < cols)
+                raw[p] = __builtin_bit_cast(u32x4, __builtin_nontemporal_load(reinterpret_cast<const V*>(x + (p * kRows + r) * ld + c)));
         }
+    }
+    __device__ __forceinline__ void get(int p, float (&v)[N]) const {
+        const Pack<T, N> t = __builtin_bit_cast(Pack<T, N>, raw[p]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = (float)t.v[i];
+    }
+    // Nothing formed from the values is kept from here on (the compiler would keep them all as f32).
+    __device__ __forceinline__ void forget() {
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) asm volatile("" : "+v"(raw[p]));
     }
 };
 
@@ -207,7 +219,12 @@ __global__ __launch_bounds__(kThreads) void quantize_matrix_kernel(Fp8MatrixArgs
     in.load((const T*)a.x + mat * a.x_stride + (int64_t)tr * kFp8Block * a.ld + tc * kFp8Block, a.ld, rows, cols);
     uint32_t top = 0;
 #pragma unroll
-    for (int p = 0; p < In::kPasses; ++p) top = max(top, top_bits(in.v[p]));
+    for (int p = 0; p < In::kPasses; ++p) {
+        float v[In::N];
+        in.get(p, v);
+        top = max(top, top_bits(v));
+    }
+    in.forget();
     top = wave_umax(top);
     if (tid % 64 == 0) lds.top[0][tid / 64] = top;
     __syncthreads();
@@ -219,9 +236,10 @@ __global__ __launch_bounds__(kThreads) void quantize_matrix_kernel(Fp8MatrixArgs
     for (int p = 0; p < In::kPasses; ++p) {
         const int r = p * In::kRows + in.r;
         uint32_t w[In::N / 4];
+        float v[In::N];
+        in.get(p, v);
 #pragma unroll
-        for (int i = 0; i < In::N / 4; ++i)
-            w[i] = fp8_codes4(in.v[p][4 * i], in.v[p][4 * i + 1], in.v[p][4 * i + 2], in.v[p][4 * i + 3], inv);
+        for (int i = 0; i < In::N / 4; ++i) w[i] = fp8_codes4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], inv);
         if (q && r < rows && in.c < cols) {
             Pack<uint32_t, In::N / 4> o;
 #pragma unroll
@@ -297,10 +315,17 @@ __global__ __launch_bounds__(kThreads) void quantize_columns_kernel(Fp8ColumnArg
     // a column's largest: over the thread's rows, over the lanes of its columns, over the waves
     uint32_t top[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        top[i] = 0;
+    for (int i = 0; i < N; ++i) top[i] = 0;
 #pragma unroll
-        for (int p = 0; p < In::kPasses; ++p) top[i] = max(top[i], abs_bits(in.v[p][i]));
+    for (int p = 0; p < In::kPasses; ++p) {
+        float v[N];
+        in.get(p, v);
+#pragma unroll
+        for (int i = 0; i < N; ++i) top[i] = max(top[i], abs_bits(v[i]));
+    }
+    in.forget();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
         if constexpr (In::L == 16) top[i] = umax_step<16>(top[i]);
         top[i] = umax_step<32>(top[i]);
     }
@@ -321,21 +346,20 @@ __global__ __launch_bounds__(kThreads) void quantize_columns_kernel(Fp8ColumnArg
 #pragma unroll
     for (int p = 0; p < In::kPasses; ++p) {
         const int r = p * In::kRows + in.r;
+        float x[N];
+        in.get(p, x);
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             float v[4];
-            bool bad[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                bad[j] = inv[4 * i + j] == 0.f;          // a column with an infinity or a NaN
-                v[j] = bad[j] ? 0.f : in.v[p][4 * i + j] * inv[4 * i + j];
-            }
+            for (int j = 0; j < 4; ++j)                  // (0: a column with an infinity or a NaN)
+                v[j] = inv[4 * i + j] == 0.f ? 0.f : x[4 * i + j] * inv[4 * i + j];
             lds.code[r * kTileWords + in.c / 4 + i] = fp8_codes4(v[0], v[1], v[2], v[3], 1.f);
         }
         if (a.q) {
-            const int code = fp8_scale_code(lanes_umax<In::L>(top_bits(in.v[p])));
+            const int code = fp8_scale_code(lanes_umax<In::L>(top_bits(x)));
             if (r < rows && in.c < cols)
-                store_codes(a.q + (int64_t)(m0 + r) * a.cols + tc * kFp8Block + in.c, in.v[p], fp8_scale_inverse(code));
+                store_codes(a.q + (int64_t)(m0 + r) * a.cols + tc * kFp8Block + in.c, x, fp8_scale_inverse(code));
             if (r < rows && tid % In::L == 0) a.s[(int64_t)(m0 + r) * SB + tc] = fp8_scale_value(code);
         }
     }
