@@ -880,19 +880,22 @@ def route_groups(logits, bias, k, score="sigmoid", groups=1, groups_kept=None, g
     import torch
     code = _token_rows(logits, "logits")
     T, E = logits.shape
-    _need(bias, torch.float32, "bias")
-    if bias is not None and bias.numel() != E:
-        raise ValueError(f"bias must have {E} values")
+    if bias is not None:
+        _need(bias, torch.float32, "bias")
+        if bias.numel() != E:
+            raise ValueError(f"bias must have {E} values")
     if idx is None:
         idx = _new(logits, (T, k), torch.int32, stream)
+    else:
+        _token_rows(idx, "idx", torch.int32, (T, k))
     if w is None:
         w = _new(logits, (T, k), torch.float32, stream)
-    if scores is None and with_scores:
-        scores = _new(logits, (T, E), torch.float32, stream)
-    _token_rows(idx, "idx", torch.int32, (T, k))
-    _token_rows(w, "w", torch.float32, (T, k))
+    else:
+        _token_rows(w, "w", torch.float32, (T, k))
     if scores is not None:
         _token_rows(scores, "scores", torch.float32, (T, E))
+    elif with_scores:
+        scores = _new(logits, (T, E), torch.float32, stream)
     _enqueue((logits, bias, idx, w, scores), stream, "coli_moe_route_groups", logits.data_ptr(), code,
              None if bias is None else bias.data_ptr(), T, E, k, _score(score), groups,
              groups if groups_kept is None else groups_kept, group_top, int(norm), scale, idx.data_ptr(),
@@ -946,11 +949,12 @@ def _fp8_rows(q, s, name):
 
 def _fp8_out(q, s, rows, cols, like, name, stream):
     import torch
+    fresh = q is None and s is None
     if q is None:
         q = _new(like, (rows, cols), torch.uint8, stream)
     if s is None:
         s = _new(like, (rows, _blocks(cols)), torch.float32, stream)
-    if _fp8_rows(q, s, name) != (rows, cols):
+    if not fresh and _fp8_rows(q, s, name) != (rows, cols):
         raise ValueError(f"{name}: codes must have shape ({rows}, {cols})")
     return q, s
 
