@@ -609,7 +609,7 @@ COLI_API coli_status coli_fp8_blob_layout(const coli_moe_shape* shape, size_t of
  * matrix w [N][K] of the row's expert; arguments and rows outside the offsets as in
  * coli_mxfp4_matmul, codes at q_off (a multiple of 16) and scales at s_off (of 4) of the expert's
  * buffer (16-byte aligned). With the transposed matrices (coli_quantize_fp8_matrix) it is the input
- * gradient. E <= 1024, K <= 2^22. */
+ * gradient. E <= 1024, K <= 2^22, rows below 2^31 - 4096, N below 2^30 - 4096. */
 COLI_API coli_status coli_fp8_matmul(const uint8_t* d_a, const float* d_as, int32_t rows, int32_t K,
                                      const int32_t* d_offsets, int32_t E, const void* const* d_blob_table,
                                      size_t q_off, size_t s_off, int32_t N, void* d_y, int32_t dtype,

@@ -748,6 +748,7 @@ static coli_status check_fp8_product(const std::string& w, int32_t rows, int32_t
     if (N <= 0) return fail(COLI_EINVAL, w + ": the matrix must have rows");
     if (K > (1 << 22)) return fail(COLI_EUNSUPPORTED, w + ": K must be at most 2^22");
     if (N > INT32_MAX / 2 - 4096) return fail(COLI_EUNSUPPORTED, w + ": matrix too large");
+    if (rows > INT32_MAX - 4096) return fail(COLI_EUNSUPPORTED, w + ": too many rows");
     if (E < 1) return fail(COLI_EINVAL, w + ": E must be at least 1");
     if (E > 1024) return fail(COLI_EUNSUPPORTED, w + ": E must be at most 1024");
     if (!grouped && E != 1) return fail(COLI_EINVAL, w + ": without offsets E must be 1");

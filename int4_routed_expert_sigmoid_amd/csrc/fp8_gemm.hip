@@ -624,7 +624,10 @@ Fp8Kernel choose_fp8_kernel(const Fp8GemmArgs& a, bool swiglu, bool wide) {
     const double few = 3 + std::max({1.3 * a.K / 1024, bytes / 5.5e6 + again * bytes / 6e6, 3 * groups / 1024});
     const double l128 = wide ? line_us(128, 1.85, 1.5) : line_us(128, 1.03, 0.78);
     const double l256 = wide ? l128 : line_us(256, 1.8, 1.7);
-    if (few < std::min(l128, l256)) {
+    // (as many workgroups as few_rows may need must fit a launch)
+    const int64_t stretches = a.offsets ? (int64_t)a.rows / kFrag + std::min(a.E, a.rows) : ((int64_t)a.rows + kFrag - 1) / kFrag;
+    const bool fits = stretches * ((a.N + 15) / 16) < int64_t(1) << 23;
+    if (fits && few < std::min(l128, l256)) {
         const bool half = !swiglu && experts * tiles(kFrag) * std::ceil(a.N / 16.0) <= kCus;
         return half ? kFp8FewRows16 : kFp8FewRows32;
     }

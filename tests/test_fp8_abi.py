@@ -85,7 +85,7 @@ def test_product_refusals(L):
         assert f(q=8) == EINVAL and f(so=6) == EINVAL and f(a=24) == EINVAL and f(s=18) == EINVAL
         assert f(a=None) == EINVAL and f(table=None) == EINVAL and f(y=None) == EINVAL and f(s=None) == EINVAL
         assert f(rows=0, a=None, table=None, y=None) == OK
-        assert f(n=(1 << 31) - 1, ld=1 << 31) == EUNSUP
+        assert f(n=(1 << 31) - 1, ld=1 << 31) == EUNSUP and f(rows=(1 << 31) - 1) == EUNSUP
     assert mm(dt=coli.FP8) == EUNSUP                             # only the SwiGLU writes FP8
     assert sw(n=24, ld=24, dt=coli.FP8) == EINVAL and sw(dt=coli.FP8, ys=None) == EINVAL and sw(dt=coli.FP8, y=24) == EINVAL
     assert sw(uq=8) == EINVAL and sw(us=2) == EINVAL and sw(dt=coli.FP8, ws=24) == EINVAL
@@ -212,3 +212,4 @@ def test_kernel_choice():
     assert pick(256, 2048, 16, 1024, wide=True) == "few_rows_32"    # 14 against 33
     assert pick(512, 6144, 256, 2048, swiglu=True) == "few_rows_32"     # 928 against 988
     assert pick(2048, 6144, 256, 2048, swiglu=True) == "lines_128"      # 1102 against 1166
+    assert pick(1, 16, 1, 1 << 27) == "lines_128"                   # more workgroups than a launch may have

@@ -441,6 +441,15 @@ def test_products_past_32_bits(coli):
         y = coli.fp8_matmul(a, a_s, table.repeat(2) if kw else table, n, s_off=n * K, dtype=torch.bfloat16, **kw)
         assert bool((y[-1] == 65536.0).all()) and bool((y[-2] == 1.0).all()) and bool((y[:-2] == 0).all())
     del a, y
+    n = (1 << 29) + 16                                            # more matrix rows than few_rows' launches take
+    w = torch.full((16 * n + 4 * (n // 128 + 1),), one, dtype=torch.uint8, device="cuda")
+    w[16 * n:].view(torch.float32).fill_(0.5)
+    w[16 * (n - 1):16 * n] = 0x40
+    for dtype in (torch.bfloat16, torch.float32):
+        y = coli.fp8_matmul(torch.full((1, 16), one, dtype=torch.uint8, device="cuda"), torch.ones(1, 1, device="cuda"),
+                            torch.tensor([w.data_ptr()], device="cuda"), n, s_off=16 * n, dtype=dtype)
+        assert y[0, -1].item() == 16.0 and bool((y[0, :-1] == 8.0).all())
+    del w, y
     n = 70000                                                     # 4.6e9 codes of a matrix, and one row
     w = torch.zeros(n * K + 4 * 547 * 512, dtype=torch.uint8, device="cuda")
     w[(n - 1) * K:n * K] = one
