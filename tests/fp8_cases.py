@@ -24,4 +24,9 @@ CASES = [
     ("lines_256", "lines_128", 9000, 16, 1300, 0, 0), ("lines_256", "lines_128", _FULL * 3, 128, 2056, 1, 2),
     ("lines_256", "lines_128", 8200, 272, 1313, 0, 0), ("lines_256", "lines_128", [2300, 0, 3700], 512, 2049, 0, 0),
     ("lines_256", "lines_128", 4500, 1152, 2060, 0, 0), ("lines_256", "lines_128", [2000, 3001, 1000], 656, 2040, 2, 1),
+    # several groups of scales (four blocks each) a unit
+    ("lines_128", "lines_128", _MANY, 1024, 640, 1, 0), ("lines_128", "lines_128", _MANY * 2, 1536, 300, 0, 2),
+    ("lines_128", "few_rows_32", [70] * 40, 2560, 264, 0, 0), ("lines_128", "lines_128", 1500, 2048, 1100, 0, 0),
+    ("lines_128", "lines_128", _FULL * 2, 1024, 2056, 1, 1), ("lines_256", "lines_128", 9000, 1536, 1300, 0, 0),
+    ("lines_256", "lines_128", [2300, 0, 3700], 2048, 2049, 0, 0), ("lines_256", "lines_128", [256] * 40, 2560, 520, 0, 0),
 ]

@@ -259,12 +259,12 @@ def _scales(rng, mean, *shape):
     return mean * (0.5 + torch.rand(*shape, device="cuda", generator=g))
 
 
-def _weights(rng, E, n, K, parts=1):
+def _weights(rng, E, n, K, parts=1, odd=4):
     """Blobs of `parts` FP8 matrices each with any scales, 16 bytes of something before them; (blobs, table, a function of the
-    matrix' values, offsets)."""
+    matrix' values, offsets). odd: where the scales lie behind a multiple of 16 bytes."""
     import torch
     nb, nk = -(-n // 128), -(-K // 128)
-    s_off = 16 + parts * n * K + (-parts * n * K) % 4 + 4
+    s_off = 16 + parts * n * K + odd
     size = -(-(s_off + 4 * parts * nb * nk) // 16) * 16
     blobs = torch.full((E, size), 0x7F, dtype=torch.uint8, device="cuda")    # NaN wherever a product should not read
     q, s = _codes(rng, E, parts, n, K), _scales(rng, 2e-3, E, parts, nb, nk)
@@ -307,16 +307,17 @@ def _half(dtype, y):
     return (_half_step(dtype) * y.abs()).clamp_min(torch.finfo(_t(dtype)).tiny * _half_step(dtype))
 
 
+@pytest.mark.parametrize("odd", (0, 4))                             # (0: scales come 16 bytes at a time)
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("case", CASES, ids=_case_id)
-def test_matmul(coli, case, dtype):
+def test_matmul(coli, case, dtype, odd):
     import torch
     kernel, wide, counts, K, n, before, behind = case
     offsets, off, rows = _groups(counts, before, behind)
     E, exact = len(off) - 1, dtype == "float32"
     assert coli.debug_fp8_kernel(rows, K, E, n, grouped=offsets is not None, wide=exact) == (wide if exact else kernel)
     rng = np.random.default_rng(K + n)
-    _keep, table, matrix, at = _weights(rng, E, n, K)
+    _keep, table, matrix, at = _weights(rng, E, n, K, odd=odd)
     a, a_s, va = _rows(rng, rows, K)
     out = torch.full((rows, n + 3), 7.0, dtype=_t(dtype), device="cuda")
     coli.fp8_matmul(a, a_s, table, n, offsets=offsets, out=out[:, :n], **at)
@@ -336,16 +337,17 @@ def _scale_of(top):
     return torch.from_numpy(ref.scale_value(ref.scale_code(top.cpu().numpy()))).cuda()
 
 
+@pytest.mark.parametrize("odd", (0, 4))
 @pytest.mark.parametrize("dtype", DTYPES + ("fp8",))
 @pytest.mark.parametrize("case", CASES, ids=_case_id)
-def test_swiglu(coli, case, dtype):
+def test_swiglu(coli, case, dtype, odd):
     import torch
     _, _, counts, K, n, before, behind = case
     n = -(-n // 16) * 16 if dtype == "fp8" else n
     offsets, off, rows = _groups(counts, before, behind)
     E, exact = len(off) - 1, dtype == "float32"
     rng = np.random.default_rng(K + n + 1)
-    _keep, table, matrix, at = _weights(rng, E, n, K, parts=2)
+    _keep, table, matrix, at = _weights(rng, E, n, K, parts=2, odd=odd)
     a, a_s, va = _rows(rng, rows, K, 0.08 / np.sqrt(K))
     g, tg = _product(va, matrix, off, n, 0)
     u, tu = _product(va, matrix, off, n, 1)
@@ -651,3 +653,38 @@ def test_graph_and_streams(coli):
         side.synchronize()
         assert torch.equal(out["y"], other["y"]) and torch.equal(out["dw"], other["dw"]) and torch.equal(out["v"], other["v"])
         assert torch.equal(out["h"], other["h"])
+
+
+def test_two_graphs_at_once(coli):
+    """Two captured layers of few rows, whose SwiGLU takes a workspace, replayed at the same time on two streams."""
+    import torch
+    rng = np.random.default_rng(13)
+    K, n, E, rows = 1536, 640, 4, 4
+    off = _dev(np.array([0, 1, 1, 3, 4], np.int32))
+    runs = []
+    for i in range(2):
+        keep, table, _, at = _weights(rng, E, n, K, parts=2, odd=0)
+        x = torch.randn(rows, K, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+
+        def layer(x=x, table=table, at=at):
+            q, s = coli.quantize_fp8(x)
+            return coli.fp8_swiglu(q, s, table, n, offsets=off, dtype="fp8", **at)
+
+        layer()
+        with torch.cuda.graph(graph):
+            out = layer()
+        runs.append((keep, layer, x, graph, out, torch.cuda.Stream()))
+    assert coli.debug_fp8_kernel(rows, K, E, n, grouped=True, swiglu=True) == "few_rows_32"
+    for seed in range(4):
+        for i, (_, _, x, _, _, stream) in enumerate(runs):
+            x.copy_(torch.randn(rows, K, generator=torch.Generator().manual_seed(2 * seed + i)))
+            stream.wait_stream(torch.cuda.current_stream())
+        for _ in range(5):
+            for _, _, _, graph, _, stream in runs:
+                with torch.cuda.stream(stream):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for _, layer, _, _, out, _ in runs:
+            want = layer()
+            assert torch.equal(want[0], out[0]) and torch.equal(want[1], out[1])
