@@ -600,6 +600,14 @@ COLI_API coli_status coli_dequantize_fp8(const uint8_t* d_q, const float* d_s, i
                                          int32_t block_rows, void* d_x, int32_t dtype, int64_t ld,
                                          void* stream);
 
+/* The values of `count` matrices as coli_quantize_fp8_matrix lays them out (codes q_stride bytes apart, a
+ * multiple of 16, scales s_stride, a multiple of 4; rows any number) as d_x, each [rows][ld] and x_stride
+ * elements apart. rows below 2^30. */
+COLI_API coli_status coli_dequantize_fp8_matrix(const uint8_t* d_q, int64_t q_stride, const float* d_s,
+                                                int64_t s_stride, int32_t count, int64_t rows, int64_t cols,
+                                                void* d_x, int32_t dtype, int64_t ld, int64_t x_stride,
+                                                void* stream);
+
 /* An expert as one buffer: byte offsets of gate, up and down codes, then of their scales, and the
  * buffer's size (hidden and inter multiples of 32; group, topp, wbits and routed_scale are not
  * used). Host-only arithmetic. */

@@ -43,7 +43,7 @@ EXPORTED = [
     "coli_moe_dispatch_bwd", "coli_moe_combine", "coli_moe_combine_bwd",
     "coli_moe_route_groups", "coli_moe_route_groups_bwd",
     "coli_quantize_fp8", "coli_quantize_fp8_matrix", "coli_quantize_fp8_columns", "coli_fp8_column_blocks",
-    "coli_dequantize_fp8", "coli_fp8_blob_layout", "coli_fp8_matmul", "coli_fp8_swiglu",
+    "coli_dequantize_fp8", "coli_dequantize_fp8_matrix", "coli_fp8_blob_layout", "coli_fp8_matmul", "coli_fp8_swiglu",
     "coli_fp8_swiglu_workspace_size", "coli_fp8_wgrad",
     "coli_debug_fp8_kernel", "coli_moe_dispatch_fp8",
 ]
@@ -164,6 +164,7 @@ def lib():
             L.coli_quantize_fp8_columns.argtypes = [vp, i32, i32, i32, i64, vp, i32, vp, i64, vp, vp, vp, vp]
             L.coli_fp8_column_blocks.argtypes = [i32, i32, P(i64)]
             L.coli_dequantize_fp8.argtypes = [vp, vp, i64, i64, i32, vp, i32, i64, vp]
+            L.coli_dequantize_fp8_matrix.argtypes = [vp, i64, vp, i64, i32, i64, i64, vp, i32, i64, i64, vp]
             L.coli_fp8_blob_layout.argtypes = [P(Shape), P(sz), P(sz)]
             L.coli_fp8_matmul.argtypes = [vp, vp, i32, i32, vp, i32, vp, sz, sz, i32, vp, i32, i64, vp]
             L.coli_fp8_swiglu.argtypes = [vp, vp, i32, i32, vp, i32, vp, sz, sz, sz, sz, i32, vp, vp, i32,
@@ -1085,8 +1086,14 @@ def dequantize_fp8(q, s, dtype=None, out=None, stream=None):
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {shape}")
     if q.dim() == 2:
         parts = [(q, s, out)]
-    elif all(t.is_contiguous() for t in (q, s, out)) and (block_rows == 1 or rows % 128 == 0):   # one long matrix
+    elif block_rows == 1 and all(t.is_contiguous() for t in (q, s, out)):       # the rows of one long matrix
         parts = [(q.view(-1, cols), s.view(-1, s.shape[-1]), out.view(-1, cols))]
+    elif block_rows == 128 and 0 < len(q) < 2 ** 31 and (
+            len(q) == 1 or (q.stride(0) % 16 == 0 and out.stride(0) >= (rows - 1) * out.stride(1) + cols)):
+        code, ld = _rows(out[0], "out", rows, cols, dtype)
+        _enqueue((q, s, out), stream, "coli_dequantize_fp8_matrix", q.data_ptr(), q.stride(0), s.data_ptr(),
+                 4 * s.stride(0), len(q), rows, cols, out.data_ptr(), code, ld, out.stride(0))
+        return out
     else:
         parts = zip(q, s, out)
     for pq, ps, po in parts:

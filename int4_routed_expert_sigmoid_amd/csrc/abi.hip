@@ -727,6 +727,31 @@ coli_status coli_dequantize_fp8(const uint8_t* d_q, const float* d_s, int64_t ro
     COLI_GUARD_END
 }
 
+coli_status coli_dequantize_fp8_matrix(const uint8_t* d_q, int64_t q_stride, const float* d_s, int64_t s_stride, int32_t count,
+                                       int64_t rows, int64_t cols, void* d_x, int32_t dtype, int64_t ld, int64_t x_stride,
+                                       void* stream) {
+    COLI_GUARD_BEGIN
+    const char* w = "dequantize_fp8_matrix";
+    coli_status st = check_fp8_rows(w, rows, cols, dtype, ld);
+    if (st) return st;
+    if (rows >= (1 << 30)) return fail(COLI_EUNSUPPORTED, "dequantize_fp8_matrix: rows must be below 2^30");
+    if (count < 0) return fail(COLI_EINVAL, "dequantize_fp8_matrix: count below 0");
+    if (count > 1 && rows > 0) {
+        if (x_stride < (rows - 1) * ld + cols || q_stride < 0 || s_stride < 0)
+            return fail(COLI_EINVAL, "dequantize_fp8_matrix: matrices overlap");
+        if (q_stride % 16 || s_stride % 4)
+            return fail(COLI_EINVAL, "dequantize_fp8_matrix: codes must be multiples of 16 bytes apart, scales of 4");
+        if (std::max({x_stride, q_stride, s_stride}) > (int64_t(1) << 60) / count)
+            return fail(COLI_EUNSUPPORTED, "dequantize_fp8_matrix: too large");
+    }
+    if (count == 0 || rows == 0) return COLI_OK;
+    if (!d_x) return fail(COLI_EINVAL, "dequantize_fp8_matrix: NULL pointer");
+    if ((st = check_fp8_pair(w, d_q, d_s))) return st;
+    return launch_dequantize_fp8(d_q, d_s, rows, cols, kFp8Block, d_x, dtype, ld, (hipStream_t)stream, count, q_stride, s_stride,
+                                 x_stride);
+    COLI_GUARD_END
+}
+
 coli_status coli_fp8_blob_layout(const coli_moe_shape* shape, size_t off[6], size_t* blob_bytes) {
     COLI_GUARD_BEGIN
     coli_status st = check_mx_shape(shape);

@@ -105,13 +105,18 @@ __global__ __launch_bounds__(kThreads) void dispatch_fp8_kernel(
     }
 }
 
-// A thread takes U units of kVec columns, kThreads apart.
+// A thread takes U units of kVec columns, kThreads apart; `per` workgroups a matrix.
 template <typename T, int U>
 __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __restrict__ q,
                                                               const float* __restrict__ s, UnitMap m,
-                                                              int block_rows, T* __restrict__ x) {
+                                                              int block_rows, T* __restrict__ x, uint32_t per,
+                                                              int64_t q_stride, int64_t s_stride, int64_t x_stride) {
     constexpr int N = kVec<T>, W = N / 4;
-    const int64_t u0 = (int64_t)blockIdx.x * (kThreads * U) + threadIdx.x;
+    const uint32_t mat = blockIdx.x / per;
+    q += mat * q_stride;
+    s = (const float*)((const uint8_t*)s + mat * s_stride);
+    x += mat * x_stride;
+    const int64_t u0 = (int64_t)(blockIdx.x - mat * per) * (kThreads * U) + threadIdx.x;
     const int64_t SB = fp8_blocks(m.cols);
     Pack<uint32_t, W> w[U];
     float sc[U];
@@ -409,8 +414,8 @@ coli_status launch_dispatch_fp8(const void* x, int32_t dtype, int32_t T, int32_t
 
 coli_status launch_dequantize_fp8(const uint8_t* q, const float* s, int64_t rows, int64_t cols,
                                   int32_t block_rows, void* x, int32_t dtype, int64_t ld,
-                                  hipStream_t stream) {
-    if (rows == 0) return COLI_OK;
+                                  hipStream_t stream, int32_t count, int64_t q_stride, int64_t s_stride, int64_t x_stride) {
+    if (rows == 0 || count == 0) return COLI_OK;
     return with_elem(dtype, [&](auto e) -> coli_status {
         using T = decltype(e);
         constexpr int U = 2;
@@ -419,9 +424,10 @@ coli_status launch_dequantize_fp8(const uint8_t* q, const float* s, int64_t rows
         m.units = rows * m.per_row;
         m.ld = ld;
         m.cols = (int32_t)cols;
-        const int64_t grid = (m.units + kThreads * U - 1) / (kThreads * U);
-        if (coli_status st = check_grid(grid, "dequantize_fp8")) return st;
-        launch(dequantize_kernel<T, U>, dim3((uint32_t)grid), dim3(kThreads), 0, stream, q, s, m, (int)block_rows, (T*)x);
+        const int64_t per = (m.units + kThreads * U - 1) / (kThreads * U);
+        if (coli_status st = check_grid(per > kMaxGrid ? per : per * count, "dequantize_fp8")) return st;
+        launch(dequantize_kernel<T, U>, dim3((uint32_t)(per * count)), dim3(kThreads), 0, stream, q, s, m, (int)block_rows, (T*)x,
+               (uint32_t)per, q_stride, s_stride, x_stride);
         COLI_CHECK_LAUNCH("dequantize_fp8 kernel launch");
         return COLI_OK;
     });

@@ -58,6 +58,16 @@ def test_quantize_refusals(L):
         assert f(q=24) == EINVAL and f(s=18) == EINVAL and f(q=None) == EINVAL and f(s=None) == EINVAL
     assert rows(r=1 << 40) == EUNSUP and back(r=1 << 40) == EUNSUP
     assert L.coli_dequantize_fp8(16, 16, 4, 64, 2, 16, 0, 64, None) == EINVAL
+
+    def many(q=16, qs=2048, s=16, ss=4, n=2, r=20, c=64, x=16, dt=0, ld=64, xs=2048):
+        return L.coli_dequantize_fp8_matrix(q, qs, s, ss, n, r, c, x, dt, ld, xs, None)
+
+    assert many(c=40) == EINVAL and many(c=0) == EINVAL and many(r=-1) == EINVAL and many(ld=63) == EINVAL and many(n=-1) == EINVAL
+    assert many(dt=3) == EUNSUP and many(r=1 << 30, n=1) == EUNSUP and many(xs=1 << 60) == EUNSUP and many(n=1 << 30) == EUNSUP
+    assert many(qs=24) == EINVAL and many(qs=-16) == EINVAL and many(ss=6) == EINVAL and many(ss=-4) == EINVAL
+    assert many(xs=20 * 64 - 1) == EINVAL and many(q=24) == EINVAL and many(s=18) == EINVAL
+    assert many(q=None) == EINVAL and many(s=None) == EINVAL and many(x=None) == EINVAL
+    assert many(n=0, q=None, s=None, x=None) == OK and many(r=0, q=None, s=None, x=None) == OK
     assert matrix(q=None, s=None) == EINVAL                      # no output
     assert matrix(n=-1) == EINVAL and matrix(n=0) == OK
     assert matrix(xs=2047) == EINVAL and matrix(qs=2032) == EINVAL and matrix(ss=0) == EINVAL

@@ -153,6 +153,13 @@ def test_quantize_matrix(coli, dtype, count, rows, cols, pad):
     assert len(one) == 2 and torch.equal(one[0], q[0]) and torch.equal(one[1], s[0])
     v = coli.dequantize_fp8(q, s)
     assert np.array_equal(_host(v[-1]), ref.values(q[-1].cpu().numpy(), _host(s[-1]), 128))
+    for a, b in ((q, s), (qt, st), (places["q"], places["s"])):      # dense, transposed, in buffers with gaps
+        back = torch.full((count, a.shape[1] + 1, a.shape[2] + 5), 9.0, dtype=_t(dtype), device="cuda")
+        coli.dequantize_fp8(a, b, out=back[:, :-1, :-5])
+        for i in range(count):
+            want = torch.from_numpy(ref.values(a[i].cpu().numpy(), _host(b[i]), 128)).float().to(_t(dtype))
+            assert torch.equal(back[i, :-1, :-5].cpu().nan_to_num(7.0), want.nan_to_num(7.0))
+        assert bool((back[:, -1] == 9).all()) and bool((back[..., -5:] == 9).all())
     one = coli.quantize_fp8_matrix(torch.full((20, 32), float("inf"), device="cuda"))   # rows in no 16s: one way round
     assert bool(one[1].isnan().all()) and int(one[0].sum()) == 0
 
