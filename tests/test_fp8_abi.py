@@ -126,7 +126,7 @@ def test_sizes(L):
             assert coli.fp8_column_blocks(coli._rows_of_blocks(n, E), E) <= n and coli._rows_of_blocks(n, E) >= rows
     nb = ctypes.c_size_t()
     size = coli.lib().coli_fp8_swiglu_workspace_size
-    for rows, K, E, inter, grouped, want in ((8, 6144, 256, 2048, 1, 8 * 2048 * 4), (1, 272, 1, 144, 0, 144 * 4), (64, 6144, 40, 2048, 1, 0),
+    for rows, K, E, inter, grouped, want in ((8, 6144, 256, 2048, 1, 8 * 2048 * 4), (1, 2064, 1, 144, 0, 144 * 4), (1, 1024, 1, 144, 0, 0), (64, 6144, 40, 2048, 1, 0),
                                              (4096, 6144, 256, 2048, 1, 0), (0, 64, 4, 64, 1, 0)):
         assert size(rows, K, E, inter, grouped, ctypes.byref(nb)) == OK and nb.value == want
     assert size(4, 40, 1, 16, 0, ctypes.byref(nb)) == EINVAL and size(4, 48, 2, 16, 0, ctypes.byref(nb)) == EINVAL

@@ -666,7 +666,7 @@ def test_two_graphs_at_once(coli):
     """Two captured layers of few rows, whose SwiGLU takes a workspace, replayed at the same time on two streams."""
     import torch
     rng = np.random.default_rng(13)
-    K, n, E, rows = 1536, 640, 4, 4
+    K, n, E, rows = 2048, 640, 4, 4
     off = _dev(np.array([0, 1, 1, 3, 4], np.int32))
     runs = []
     for i in range(2):
