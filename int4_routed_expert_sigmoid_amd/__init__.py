@@ -973,20 +973,21 @@ def quantize_fp8(x, q=None, s=None, stream=None):
     return q, s
 
 
-def _fp8_matrices(q, s, count, rows, cols, like, name, stream):
-    """Outputs [count][rows][cols] and [count][blocks][blocks], each matrix without gaps; their strides in bytes."""
+def _fp8_matrices(q, s, lead, rows, cols, like, name, stream):
+    """Outputs [..lead][rows][cols] and [..lead][blocks][blocks], each matrix without gaps; their strides in bytes."""
     import torch
-    shapes = (count, rows, cols), (count, _blocks(rows), _blocks(cols))
-    if q is None:
-        q = _new(like, shapes[0], torch.uint8, stream)
-    if s is None:
-        s = _new(like, shapes[1], torch.float32, stream)
-    for t, shape, dtype, part in ((q, shapes[0], torch.uint8, "codes"), (s, shapes[1], torch.float32, "scales")):
-        if t.dtype != dtype or not t.is_cuda or tuple(t.shape) != shape:
-            raise ValueError(f"{name}: {part} must be a {dtype} device tensor of shape {shape}")
-        if count and not t[0].is_contiguous():
+    blocks = _blocks(rows), _blocks(cols)
+    made = []
+    for t, shape, dtype, part in ((q, (rows, cols), torch.uint8, "codes"), (s, blocks, torch.float32, "scales")):
+        if t is None:
+            made += _new(like, (*lead, *shape), dtype, stream), shape[0] * shape[1]
+            continue
+        if t.dtype != dtype or not t.is_cuda or t.shape != (*lead, *shape):
+            raise ValueError(f"{name}: {part} must be a {dtype} device tensor of shape {(*lead, *shape)}")
+        if not t.is_contiguous() and not (lead and t[0].is_contiguous()):
             raise ValueError(f"{name}: each matrix of the {part} must be contiguous")
-    return q, s, q.stride(0), 4 * s.stride(0)
+        made += t, t.stride(0) if lead else shape[0] * shape[1]
+    return made[0], made[2], made[1], 4 * made[3]
 
 
 def quantize_fp8_matrix(x, transposed=False, q=None, s=None, qt=None, st=None, stream=None):
@@ -994,29 +995,28 @@ def quantize_fp8_matrix(x, transposed=False, q=None, s=None, qt=None, st=None, s
     -> (codes uint8 of x's shape, scales float32 [..][ceil(rows / 128)][ceil(cols / 128)]), with
     `transposed` (or qt, st given) followed by those of the transposed matrices. Given outputs may be
     views into experts' buffers: only a matrix itself has to be contiguous."""
-    if x.dim() not in (2, 3):
+    shape = x.shape
+    if len(shape) not in (2, 3):
         raise ValueError("x must be [rows][cols] or [count][rows][cols]")
-    flat = x.dim() == 2
-    x3, outs = (x[None], [None if t is None else t[None] for t in (q, s, qt, st)]) if flat else (x, [q, s, qt, st])
-    count, rows, cols = x3.shape
-    code, ld = (_dtype_code(x.dtype), cols) if x3.numel() == 0 else _rows(x3[0], "x")
     if not x.is_cuda:
         raise ValueError("x must be a device tensor")
+    lead, (rows, cols) = shape[:-2], shape[-2:]
+    count, x_stride = (lead[0], x.stride(0)) if lead else (1, 0)
+    code, ld = (_dtype_code(x.dtype), cols) if x.numel() == 0 else _rows(x[0] if lead else x, "x")
     if count >= 2 ** 31:
         raise ValueError("fewer than 2^31 matrices are needed")
-    if count > 1 and x3.numel() and x3.stride(0) < (rows - 1) * ld + cols:
+    if count > 1 and x.numel() and x_stride < (rows - 1) * ld + cols:
         raise ValueError("x has matrices that overlap")
-    both = transposed or qt is not None or st is not None
-    outs[:2], strides = [], outs[:2]
-    q3, s3, q_stride, s_stride = _fp8_matrices(*strides, count, rows, cols, x, "quantize_fp8_matrix", stream)
-    tensors, t_args = [x, q3, s3], (None, 0, None, 0)
-    if both:
-        qt3, st3, qt_stride, st_stride = _fp8_matrices(*outs, count, cols, rows, x, "quantize_fp8_matrix", stream)
-        tensors += [qt3, st3]
-        t_args = qt3.data_ptr(), qt_stride, st3.data_ptr(), st_stride
-    _enqueue(tensors, stream, "coli_quantize_fp8_matrix", x.data_ptr(), code, count, rows, cols, ld, x3.stride(0),
-             q3.data_ptr(), q_stride, s3.data_ptr(), s_stride, *t_args)
-    return tuple(t[0] if flat else t for t in tensors[1:])
+    name = "quantize_fp8_matrix"
+    q, s, q_stride, s_stride = _fp8_matrices(q, s, lead, rows, cols, x, name, stream)
+    if not transposed and qt is None and st is None:
+        _enqueue((x, q, s), stream, "coli_quantize_fp8_matrix", x.data_ptr(), code, count, rows, cols, ld, x_stride,
+                 q.data_ptr(), q_stride, s.data_ptr(), s_stride, None, 0, None, 0)
+        return q, s
+    qt, st, qt_stride, st_stride = _fp8_matrices(qt, st, lead, cols, rows, x, name, stream)
+    _enqueue((x, q, s, qt, st), stream, "coli_quantize_fp8_matrix", x.data_ptr(), code, count, rows, cols, ld, x_stride,
+             q.data_ptr(), q_stride, s.data_ptr(), s_stride, qt.data_ptr(), qt_stride, st.data_ptr(), st_stride)
+    return q, s, qt, st
 
 
 @functools.lru_cache(4096)
@@ -1076,27 +1076,27 @@ def dequantize_fp8(q, s, dtype=None, out=None, stream=None):
     """The values of FP8 rows, or of matrices ([..][rows][cols] with a scale for each 128 x 128 block), in
     `out`'s type, else `dtype` (default float32)."""
     import torch
-    shape = tuple(q.shape)
-    if q.dim() not in (2, 3) or s.dim() != q.dim():
+    shape, many = q.shape, q.dim() == 3
+    if len(shape) not in (2, 3) or s.dim() != len(shape):
         raise ValueError("codes must be [rows][cols] or [count][rows][cols], and scales have as many dimensions")
     for t, kind, name in ((q, torch.uint8, "codes"), (s, torch.float32, "scales")):
-        _need(t if q.dim() == 2 or not len(t) else t[0], kind, name)
-    rows, cols = shape[-2:]
-    per_row, per_block = (*shape[:-1], _blocks(cols)), (*shape[:-2], _blocks(rows), _blocks(cols))
-    if tuple(s.shape) not in (per_row, per_block):
-        raise ValueError(f"codes {shape} and scales {tuple(s.shape)} do not match")
-    block_rows = 1 if tuple(s.shape) == per_row else 128
-    if out is None:
+        _need(t[0] if many and len(t) and not t.is_contiguous() else t, kind, name)
+    lead, (rows, cols) = shape[:-2], shape[-2:]
+    per_row = s.shape == (*lead, rows, _blocks(cols))
+    if not per_row and s.shape != (*lead, _blocks(rows), _blocks(cols)):
+        raise ValueError(f"codes {tuple(shape)} and scales {tuple(s.shape)} do not match")
+    fresh = out is None
+    if fresh:
         out = _new(q, shape, dtype or torch.float32, stream)
-    if tuple(out.shape) != shape:
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {shape}")
-    if q.dim() == 2:
+    elif out.shape != shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(shape)}")
+    if not many:
         parts = [(q, s, out)]
-    elif block_rows == 1 and all(t.is_contiguous() for t in (q, s, out)):       # the rows of one long matrix
+    elif per_row and q.is_contiguous() and s.is_contiguous() and out.is_contiguous():       # the rows of one long matrix
         parts = [(q.view(-1, cols), s.view(-1, s.shape[-1]), out.view(-1, cols))]
-    elif block_rows == 128 and 0 < len(q) < 2 ** 31 and (
-            len(q) == 1 or (q.stride(0) % 16 == 0 and out.stride(0) >= (rows - 1) * out.stride(1) + cols)):
-        code, ld = _rows(out[0], "out", rows, cols, dtype)
+    elif not per_row and 0 < len(q) < 2 ** 31 and (fresh or len(q) == 1 or out.stride(0) >= (rows - 1) * out.stride(1) + cols) and (
+            len(q) == 1 or q.stride(0) % 16 == 0):
+        code, ld = (_dtype_code(out.dtype), cols) if fresh else _rows(out[0], "out", rows, cols, dtype)
         _enqueue((q, s, out), stream, "coli_dequantize_fp8_matrix", q.data_ptr(), q.stride(0), s.data_ptr(),
                  4 * s.stride(0), len(q), rows, cols, out.data_ptr(), code, ld, out.stride(0))
         return out
@@ -1105,7 +1105,7 @@ def dequantize_fp8(q, s, dtype=None, out=None, stream=None):
     for pq, ps, po in parts:
         code, ld = _rows(po, "out", pq.shape[0], cols, dtype)
         _enqueue((pq, ps, po), stream, "coli_dequantize_fp8", pq.data_ptr(), ps.data_ptr(), pq.shape[0], cols,
-                 block_rows, po.data_ptr(), code, ld)
+                 1 if per_row else 128, po.data_ptr(), code, ld)
     return out
 
 
