@@ -727,6 +727,13 @@ def debug_mxfp4_kernel(rows: int, K: int, E: int, N: int, grouped=True, aligned=
     return MXFP4_KERNELS[out.value]
 
 
+@functools.lru_cache(4096)
+def _union_ws(T, k, E):
+    nb = ctypes.c_size_t()
+    _check(lib().coli_moe_union_workspace_size(T, k, E, ctypes.byref(nb)))
+    return nb.value
+
+
 def union_inverse(idx, E, stream=None):
     """union, with each assignment's place in the experts' order: (counts, offsets,
     perm, unique, n_unique, inv [T][k])."""
@@ -736,16 +743,15 @@ def union_inverse(idx, E, stream=None):
     n = T * k
     if n >= 2 ** 31 or E >= 2 ** 31:
         raise ValueError(f"idx must have fewer than 2^31 values, and E, {E}, be below 2^31")
-    nb = ctypes.c_size_t()
-    _check(lib().coli_moe_union_workspace_size(T, k, E, ctypes.byref(nb)))
-    buf = _new(idx, (3 * E + 2 + 2 * n + (nb.value + 3) // 4,), torch.int32, stream)
-    counts, offsets, perm, unique, n_unique, inv, ws = buf.split(
-        (E, E + 1, n, E, 1, n, (nb.value + 3) // 4))
+    nb = _union_ws(T, k, E)
+    buf = _new(idx, (3 * E + 2 + 2 * n + (nb + 3) // 4,), torch.int32, stream)
+    counts, offsets, perm, unique, n_unique, inv, ws = buf.split_with_sizes(
+        (E, E + 1, n, E, 1, n, (nb + 3) // 4))
     base = buf.data_ptr()
     at = [base + 4 * i for i in (0, E, 2 * E + 1, 2 * E + 1 + n, 3 * E + 1 + n, 3 * E + 2 + n,
                                  3 * E + 2 + 2 * n)]
     _enqueue((idx, buf), stream, "coli_moe_union_inverse", idx.data_ptr(), T, k, E, *at[:6], at[6],
-             nb.value)
+             nb)
     return counts, offsets, perm, unique, n_unique, inv.view(T, k)
 
 
