@@ -645,12 +645,18 @@ COLI_API coli_status coli_fp8_swiglu_workspace_size(int32_t rows, int32_t K, int
 /* Every expert's matrix gradient: d_dw[e][n][k] = sum over the expert's rows r of g[r][n] x[r][k] (0
  * without rows), for g [rows][N] and x [rows][K] (N, K multiples of 16) as coli_quantize_fp8_columns
  * lays them out with the same rows, d_offsets, E and blocks (scales 4-byte aligned). d_dw [E][N][ld] of type dtype, ld >= K;
- * accumulate: the sums are added to what it holds. Sums as the products'. */
+ * accumulate: the sums are added to what it holds. Sums as the products'. d_ws (nullable, 16-byte aligned): a
+ * workspace of coli_fp8_wgrad_workspace_size's bytes, with which many rows of few small matrices are several times
+ * as fast (parts of the rows are summed by themselves, in f32, and then together); smaller ones are not used. It needs no
+ * initialisation, and calls that run at the same time (two graphs' too) need one each. */
 COLI_API coli_status coli_fp8_wgrad(const uint8_t* d_gt, const uint8_t* d_gs, const uint8_t* d_xt,
                                     const uint8_t* d_xs, int64_t blocks, int32_t rows,
                                     const int32_t* d_offsets, int32_t E, int32_t N, int32_t K,
                                     int32_t accumulate, void* d_dw, int32_t dtype, int64_t ld,
-                                    void* stream);
+                                    void* d_ws, size_t ws_bytes, void* stream);
+
+/* The workspace that coli_fp8_wgrad makes use of for these sizes, 0 where it needs none. Host-only arithmetic. */
+COLI_API coli_status coli_fp8_wgrad_workspace_size(int32_t rows, int32_t E, int32_t N, int32_t K, size_t* bytes);
 
 /* Testing: which kernel a product of these sizes runs (grouped: with d_offsets; wide: f32 results): 0, 1
  * few rows, 16 or 32 matrix rows a workgroup; 2, 3 persistent tiles of 128 or 256 rows. Host-only

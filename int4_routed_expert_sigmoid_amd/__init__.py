@@ -45,7 +45,7 @@ EXPORTED = [
     "coli_moe_route_groups", "coli_moe_route_groups_bwd",
     "coli_quantize_fp8", "coli_quantize_fp8_matrix", "coli_quantize_fp8_columns", "coli_fp8_column_blocks",
     "coli_dequantize_fp8", "coli_dequantize_fp8_matrix", "coli_fp8_blob_layout", "coli_fp8_matmul", "coli_fp8_swiglu",
-    "coli_fp8_swiglu_workspace_size", "coli_fp8_wgrad",
+    "coli_fp8_swiglu_workspace_size", "coli_fp8_wgrad", "coli_fp8_wgrad_workspace_size",
     "coli_debug_fp8_kernel", "coli_moe_dispatch_fp8",
 ]
 
@@ -171,7 +171,8 @@ def lib():
             L.coli_fp8_swiglu.argtypes = [vp, vp, i32, i32, vp, i32, vp, sz, sz, sz, sz, i32, vp, vp, i32,
                                           i64, vp, sz, vp]
             L.coli_fp8_swiglu_workspace_size.argtypes = [i32, i32, i32, i32, i32, P(sz)]
-            L.coli_fp8_wgrad.argtypes = [vp, vp, vp, vp, i64, i32, vp, i32, i32, i32, i32, vp, i32, i64, vp]
+            L.coli_fp8_wgrad.argtypes = [vp, vp, vp, vp, i64, i32, vp, i32, i32, i32, i32, vp, i32, i64, vp, sz, vp]
+            L.coli_fp8_wgrad_workspace_size.argtypes = [i32, i32, i32, i32, P(sz)]
             L.coli_debug_fp8_kernel.argtypes = [i32, i32, i32, i32, i32, i32, i32, P(i32)]
             L.coli_moe_dispatch_fp8.argtypes = [vp, i32, i32, i32, i32, i64, vp, vp, vp, vp]
             _lib = L
@@ -1181,6 +1182,13 @@ def fp8_swiglu(a, a_s, table, inter, q_off=0, s_off=0, up_q_off=None, up_s_off=N
     return out
 
 
+@functools.lru_cache(4096)
+def _fp8_wgrad_ws(rows, E, n, K):
+    nb = ctypes.c_size_t()
+    _check(lib().coli_fp8_wgrad_workspace_size(rows, E, n, K, ctypes.byref(nb)))
+    return nb.value
+
+
 def fp8_wgrad(gt, gt_s, xt, xt_s, offsets=None, rows=None, dtype=None, out=None, accumulate=False, stream=None):
     """fp8_matmul's gradient to its matrices, out[e] = sum over the expert's rows of grad[r] x[r]^T, [E][n][K]
     in `dtype` (default float32), from quantize_fp8_columns of the output's gradient and of the rows, with
@@ -1210,9 +1218,11 @@ def fp8_wgrad(gt, gt_s, xt, xt_s, offsets=None, rows=None, dtype=None, out=None,
         if E > 1 and n and out.stride(0) != n * out.stride(1):
             raise ValueError("out's matrices must follow each other without gaps")
         code, ld = _rows(out.view(E * n, K) if out.is_contiguous() else out[0], "out", n, K, dtype)
-    _enqueue((gt, gt_s, xt, xt_s, offsets, out), stream, "coli_fp8_wgrad", gt.data_ptr(), gt_s.data_ptr(),
+    nb = _fp8_wgrad_ws(rows, E, n, K)
+    ws = _new(gt, (nb,), torch.uint8, stream) if nb else None
+    _enqueue((gt, gt_s, xt, xt_s, offsets, out, ws), stream, "coli_fp8_wgrad", gt.data_ptr(), gt_s.data_ptr(),
              xt.data_ptr(), xt_s.data_ptr(), blocks, rows, None if offsets is None else offsets.data_ptr(), E, n, K,
-             int(accumulate), out.data_ptr(), code, ld)
+             int(accumulate), out.data_ptr(), code, ld, None if ws is None else ws.data_ptr(), nb)
     return out
 
 

@@ -841,7 +841,8 @@ coli_status coli_fp8_swiglu_workspace_size(int32_t rows, int32_t K, int32_t E, i
 
 coli_status coli_fp8_wgrad(const uint8_t* d_gt, const uint8_t* d_gs, const uint8_t* d_xt, const uint8_t* d_xs,
                            int64_t blocks, int32_t rows, const int32_t* d_offsets, int32_t E, int32_t N, int32_t K,
-                           int32_t accumulate, void* d_dw, int32_t dtype, int64_t ld, void* stream) {
+                           int32_t accumulate, void* d_dw, int32_t dtype, int64_t ld, void* d_ws, size_t ws_bytes,
+                           void* stream) {
     COLI_GUARD_BEGIN
     coli_status st = check_fp8_columns("fp8_wgrad", rows, d_offsets, E, blocks);
     if (st) return st;
@@ -854,11 +855,26 @@ coli_status coli_fp8_wgrad(const uint8_t* d_gt, const uint8_t* d_gs, const uint8
     if (!d_dw || (rows > 0 && (!d_gt || !d_gs || !d_xt || !d_xs))) return fail(COLI_EINVAL, "fp8_wgrad: NULL pointer");
     if (!aligned16(d_gt) || !aligned16(d_xt)) return fail(COLI_EINVAL, "fp8_wgrad: codes must be 16-byte aligned");
     if (!aligned4(d_gs) || !aligned4(d_xs)) return fail(COLI_EINVAL, "fp8_wgrad: scales must be 4-byte aligned");
+    if (d_ws && !aligned16(d_ws)) return fail(COLI_EINVAL, "fp8_wgrad: the workspace must be 16-byte aligned");
     if (rows == 0 && accumulate) return COLI_OK;
-    Fp8WgradArgs a;
+    Fp8WgradArgs a = {};
     a.g = d_gt; a.gs = d_gs; a.x = d_xt; a.xs = d_xs; a.offsets = d_offsets; a.dw = d_dw;
     a.blocks = (int32_t)blocks; a.ld = ld; a.rows = rows; a.E = E; a.N = N; a.K = K; a.accumulate = accumulate != 0;
+    const size_t need = fp8_wgrad_ws(a);
+    a.ws = need > 0 && ws_bytes >= need ? d_ws : nullptr;
     return launch_fp8_wgrad(a, dtype, (hipStream_t)stream);
+    COLI_GUARD_END
+}
+
+coli_status coli_fp8_wgrad_workspace_size(int32_t rows, int32_t E, int32_t N, int32_t K, size_t* bytes) {
+    COLI_GUARD_BEGIN
+    if (rows < 0 || E < 1 || N <= 0 || K <= 0 || N % kFp8Unit || K % kFp8Unit || !bytes)
+        return fail(COLI_EINVAL, "fp8_wgrad_workspace_size: rows >= 0, E at least 1, N and K positive multiples of 16");
+    if (E > 1024) return fail(COLI_EUNSUPPORTED, "fp8_wgrad_workspace_size: E must be at most 1024");
+    Fp8WgradArgs a = {};
+    a.rows = rows; a.E = E; a.N = N; a.K = K;
+    *bytes = fp8_wgrad_ws(a);
+    return COLI_OK;
     COLI_GUARD_END
 }
 

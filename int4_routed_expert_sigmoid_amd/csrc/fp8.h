@@ -176,7 +176,11 @@ struct Fp8WgradArgs {
     int64_t ld;
     int32_t blocks, rows, E, N, K;
     bool accumulate;
+    void* ws;                    // fp8_wgrad_ws bytes, or nullptr
+    int32_t splits;              // parts of an expert's rows, each into a gradient of its own (the launcher's)
 };
 coli_status launch_fp8_wgrad(const Fp8WgradArgs& a, int32_t dtype, hipStream_t stream);
+// The workspace that the gradients make use of.
+size_t fp8_wgrad_ws(const Fp8WgradArgs& a);
 
 }  // namespace coli

@@ -43,7 +43,7 @@ struct WgradTile {
 };
 
 struct WgradUnit {
-    int e, n_tile, k_tile, first, count;     // count -1: no unit
+    int e, n_tile, k_tile, first, count;     // e: of the outputs, expert + E * part; count -1: no unit
 };
 
 template <typename T, int MT, int NF, int WM, int WN, int STAGES, bool ADD>
@@ -57,7 +57,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(Fp8WgradArgs a, 
 
     const RowGroups groups = {a.offsets, nullptr, a.rows, a.E};
     const int blocks = min((int)scan_units<kFp8Block, W::kThreads>(groups, 1, lds.first, lds.scale[0][0]), a.blocks);
-    const uint32_t per_expert = (uint32_t)NT * KT, total = per_expert * a.E;
+    const uint32_t per_expert = (uint32_t)NT * KT, total = per_expert * a.E * a.splits;
     // Units in order of expert, stretches of `tall` tiles of n, k, n, round all workgroups, and with them round the XCDs: the
     // device writes neighbouring tiles at a time. With KT a multiple of 4 and tall 1 an XCD reads an eighth or a
     // quarter of x's columns, with tall 8 a stretch of its own of g's. (An eighth of the units for each XCD in place of
@@ -73,8 +73,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(Fp8WgradArgs a, 
         u.n_tile = (block * tall + in % high) * W::BM;
         u.k_tile = in / high * W::BN;
         // (offsets that are not ascending may count more blocks than there are)
-        u.first = min(__builtin_amdgcn_readfirstlane((int)lds.first[u.e]), blocks);
-        u.count = (u.e + 1 < a.E ? min(__builtin_amdgcn_readfirstlane((int)lds.first[min(u.e + 1, a.E - 1)]), blocks) : blocks) - u.first;
+        const int part = u.e / a.E, e = u.e - part * a.E;
+        u.first = min(__builtin_amdgcn_readfirstlane((int)lds.first[e]), blocks);
+        u.count = (e + 1 < a.E ? min(__builtin_amdgcn_readfirstlane((int)lds.first[min(e + 1, a.E - 1)]), blocks) : blocks) - u.first;
+        if (a.splits > 1 && u.count > 0) {
+            const int lo = (int)((int64_t)u.count * part / a.splits), hi = (int)((int64_t)u.count * (part + 1) / a.splits);
+            u.first += lo;
+            u.count = hi - lo;
+        }
         return u;
     };
     uint32_t at = blockIdx.x;                // this workgroup's units: at, at + step, ...
@@ -282,17 +288,73 @@ template <typename T, int MT, int NF, int WM, int WN, int STAGES, bool ADD>
 coli_status wgrad(const Fp8WgradArgs& a, hipStream_t stream) {
     typedef WgradTile<T, MT, NF, WM, WN, STAGES> W;
     const int64_t NT = (a.N + W::BM - 1) / W::BM, KT = (a.K + W::BN - 1) / W::BN;
-    if (NT * KT > INT32_MAX / a.E) return fail(COLI_EUNSUPPORTED, "fp8_wgrad: more than 2^31 tiles");
+    if (NT * KT > INT32_MAX / a.E / a.splits) return fail(COLI_EUNSUPPORTED, "fp8_wgrad: more than 2^31 tiles");
     constexpr int64_t kPerCu = 163840 / sizeof(typename W::Lds);
-    const uint32_t grid = (uint32_t)std::min<int64_t>(kCus * kPerCu, NT * KT * a.E);
+    const uint32_t grid = (uint32_t)std::min<int64_t>(kCus * kPerCu, NT * KT * a.E * a.splits);
     launch(wgrad_kernel<T, MT, NF, WM, WN, STAGES, ADD>, dim3(grid), dim3(W::kThreads), 0, stream, a, (int)NT, (int)KT);
     COLI_CHECK_LAUNCH("fp8_wgrad kernel launch");
     return COLI_OK;
 }
 
+// dw = the sum of the parts, in their order (+ dw); 4 neighbouring columns a thread.
+template <typename T>
+__global__ __launch_bounds__(256) void wgrad_sum_kernel(const float* __restrict__ part, int64_t rows, int K, int splits, bool add,
+                                                        T* __restrict__ dw, int64_t ld) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= rows * K) return;
+    f32x4 v = *(const f32x4*)(part + i);
+#pragma unroll 4
+    for (int s = 1; s < splits; ++s) v += *(const f32x4*)(part + s * rows * K + i);
+    T* p = dw + i / K * ld + i % K;
+    float x[4] = {v[0], v[1], v[2], v[3]};
+    if (add) {
+        float o[4];
+        load_f32<T, 4>(p, o);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] += o[j];
+    }
+    store_f32<T, 4>(p, x);
+}
+
+// Into how many parts an expert's rows are divided: a tile takes about 1.5 us a block of rows, however few tiles there
+// are, and the parts' sum a launch (5) and its bytes. (One gradient of 1024 x 256 from 65536 rows: 732 us in one part, 55
+// in 32; 2048 x 2048 from 16384 192 and 129 in 2; 256 x 1168 from 3274 44 and 19 in 8; 48 x 80 from 1400 21 and 12 in 5.)
+int wgrad_splits(const Fp8WgradArgs& a) {
+    const int64_t units = (int64_t)((a.N + 127) / 128) * ((a.K + 255) / 256) * a.E;
+    const double blocks = (double)a.rows / kFp8Block / a.E, one = 1.6 * blocks;
+    int best = 1;
+    double least = one - 4;                      // (what the second launch costs the host)
+    for (int s = 2; s <= 32 && s * units <= kCus && 2 * s <= blocks + 1; ++s) {
+        const double us = one / s + 5 + (double)s * a.E * a.N * a.K * 8 / 4e6;
+        if (us < least) best = s, least = us;
+    }
+    return best;
+}
+
 }  // namespace
 
-coli_status launch_fp8_wgrad(const Fp8WgradArgs& a, int32_t dtype, hipStream_t stream) {
+size_t fp8_wgrad_ws(const Fp8WgradArgs& a) {
+    const int splits = wgrad_splits(a);
+    return splits > 1 ? (size_t)splits * a.E * a.N * a.K * 4 : 0;
+}
+
+coli_status launch_fp8_wgrad(const Fp8WgradArgs& args, int32_t dtype, hipStream_t stream) {
+    Fp8WgradArgs a = args;
+    a.splits = 1;
+    if (a.ws) {
+        a.splits = wgrad_splits(a);
+        a.dw = a.ws;
+        a.ld = a.K;
+        if (coli_status st = wgrad<float, 4, 4, 2, 4, 3, false>(a, stream)) return st;
+        return with_elem(dtype, [&](auto e) -> coli_status {
+            using T = decltype(e);
+            const int64_t rows = (int64_t)a.E * a.N;
+            launch(wgrad_sum_kernel<T>, dim3((uint32_t)((rows * a.K / 4 + 255) / 256)), dim3(256), 0, stream, (const float*)a.ws, rows,
+                   (int)a.K, (int)a.splits, args.accumulate, (T*)args.dw, args.ld);
+            COLI_CHECK_LAUNCH("fp8_wgrad kernel launch");
+            return COLI_OK;
+        });
+    }
     return with_elem(dtype, [&](auto e) -> coli_status {
         using T = decltype(e);
         constexpr int MT = std::is_same<T, float>::value ? 4 : 8;

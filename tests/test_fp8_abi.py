@@ -100,15 +100,15 @@ def test_product_refusals(L):
     assert sw(n=24, ld=24, dt=coli.FP8) == EINVAL and sw(dt=coli.FP8, ys=None) == EINVAL and sw(dt=coli.FP8, y=24) == EINVAL
     assert sw(uq=8) == EINVAL and sw(us=2) == EINVAL and sw(dt=coli.FP8, ws=24) == EINVAL
 
-    def wg(g=16, gs=16, x=16, xs=16, P=4, rows=4, off=16, E=2, N=16, K=32, acc=0, dw=16, dt=0, ld=32):
-        return L.coli_fp8_wgrad(g, gs, x, xs, P, rows, off, E, N, K, acc, dw, dt, ld, None)
+    def wg(g=16, gs=16, x=16, xs=16, P=4, rows=4, off=16, E=2, N=16, K=32, acc=0, dw=16, dt=0, ld=32, ws=None):
+        return L.coli_fp8_wgrad(g, gs, x, xs, P, rows, off, E, N, K, acc, dw, dt, ld, ws, 1 << 20, None)
 
     assert wg(rows=-1) == EINVAL and wg(P=1) == EINVAL and wg(P=-1) == EINVAL and wg(P=1 << 24) == EUNSUP
     assert wg(E=0) == EINVAL and wg(E=1025, P=1 << 20) == EUNSUP and wg(off=None) == EINVAL
     assert wg(N=24) == EINVAL and wg(K=24) == EINVAL and wg(N=0) == EINVAL and wg(K=0) == EINVAL
     assert wg(dt=3) == EUNSUP and wg(ld=31) == EINVAL and wg(ld=1 << 56) == EUNSUP and wg(N=1 << 30) == EUNSUP
     assert wg(dw=None) == EINVAL and wg(g=None) == EINVAL and wg(xs=None) == EINVAL and wg(g=24) == EINVAL
-    assert wg(gs=18) == EINVAL and wg(xs=17) == EINVAL
+    assert wg(gs=18) == EINVAL and wg(xs=17) == EINVAL and wg(ws=24) == EINVAL
     assert wg(rows=0, acc=1, g=None, gs=None, x=None, xs=None) == OK
     assert L.coli_moe_dispatch_fp8(16, 0, 2, 2, 40, 40, 16, 16, 16, None) == EINVAL
     assert L.coli_moe_dispatch_fp8(16, 0, 2, 2, 32, 31, 16, 16, 16, None) == EINVAL
@@ -131,6 +131,14 @@ def test_sizes(L):
         assert size(rows, K, E, inter, grouped, ctypes.byref(nb)) == OK and nb.value == want
     assert size(4, 40, 1, 16, 0, ctypes.byref(nb)) == EINVAL and size(4, 48, 2, 16, 0, ctypes.byref(nb)) == EINVAL
     assert size(4, 48, 1, 16, 0, None) == EINVAL
+    size = coli.lib().coli_fp8_wgrad_workspace_size
+    for rows, E, n, K, parts in ((4095, 1, 6144, 8192, 1), (16384, 64, 2048, 6144, 1), (500, 1, 128, 128, 1), (0, 1, 16, 16, 1),
+                                 (4096, 1, 128, 256, 16), (8082, 1, 2384, 1024, 3), (1400, 1, 48, 80, 5),
+                                 (4096, 4, 128, 256, 1), (16000, 4, 144, 272, 13)):
+        assert size(rows, E, n, K, ctypes.byref(nb)) == OK and nb.value == (parts * E * n * K * 4 if parts > 1 else 0)
+    assert size(-1, 1, 16, 16, ctypes.byref(nb)) == EINVAL and size(4, 0, 16, 16, ctypes.byref(nb)) == EINVAL
+    assert size(4, 1, 24, 16, ctypes.byref(nb)) == EINVAL and size(4, 1, 16, 0, ctypes.byref(nb)) == EINVAL
+    assert size(4, 1, 16, 16, None) == EINVAL and size(4, 1025, 16, 16, ctypes.byref(nb)) == EUNSUP
     off, nbytes = coli.fp8_blob_layout(coli.MoEShape(6144, 2048, 256))
     m, n = 6144 * 2048, 4 * 48 * 16
     assert off == [0, m, 2 * m, 3 * m, 3 * m + n, 3 * m + 2 * n] and nbytes == 3 * (m + n)

@@ -489,7 +489,8 @@ def test_wgrad_past_32_bits(coli):
 
 # ---------------------------------------------------------------- gradients
 WGRAD = [([3], 16, 16), ([128, 0, 129, 1], 144, 272), ([5, 40, 0, 260, 17], 64, 528), ([0, 0], 32, 16), ([1] * 9, 128, 128), (300, 272, 144),
-         ([700], 528, 400), ([5, 0, 130], 1168, 272), ([40, 3], 144, 1024)]
+         ([700], 528, 400), ([5, 0, 130], 1168, 272), ([40, 3], 144, 1024), (1400, 48, 80),
+         ([6000, 0, 1500, 20], 48, 272), ([3, 8100], 272, 64)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -526,6 +527,32 @@ def test_wgrad(coli, counts, n, K, dtype):
     assert _within(err, tol * 1.01 + (_half_step(dtype) + 2.0 ** -24) * (np.abs(want) + 2.0))
     coli.fp8_wgrad(*cols[0], *cols[1], offsets, out=buf[..., :K])
     assert torch.equal(buf[..., :K], got)
+
+
+def test_wgrad_parts(coli):
+    """Rows summed in parts (with a workspace) and at once (without) agree, NaN included, and repeat bit for bit. f32: about
+    160 additions of 32 products each round by 2^-25 of sums that do not exceed the largest result by much, 13 * 2^-25 as
+    independent errors on each side, and 2^5 to spare; bf16: one rounding on each side, 2^-8 each."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for counts, n, K in (([2900, 1], 144, 272), (5000, 16, 1040)):
+        offsets, off, rows = _groups(counts, 0, 0)
+        E = len(off) - 1
+        a, b = torch.randn(rows, n, device="cuda", generator=g), torch.randn(rows, K, device="cuda", generator=g)
+        a[17, 3], b[rows - 1, 5] = float("nan"), float("inf")
+        (ga, gs), (xa, xs) = coli.quantize_fp8_columns(a, offsets), coli.quantize_fp8_columns(b, offsets)
+        assert coli._fp8_wgrad_ws(rows, E, n, K) > 0
+        for dtype, code in ((torch.float32, 0), (torch.bfloat16, 1)):
+            got = coli.fp8_wgrad(ga, gs, xa, xs, offsets, rows=rows, dtype=dtype)
+            one = torch.empty_like(got)
+            assert coli.lib().coli_fp8_wgrad(ga.data_ptr(), gs.data_ptr(), xa.data_ptr(), xs.data_ptr(), ga.shape[0], rows,
+                                             None if offsets is None else offsets.data_ptr(), E, n, K, 0, one.data_ptr(), code, K,
+                                             None, 0, coli._stream()) == 0
+            assert torch.equal(got.isnan(), one.isnan()) and bool(got[0, 3].isnan().all())
+            scale = float(one.nan_to_num(0.0).double().abs().max())
+            assert float((got - one).nan_to_num(0.0).double().abs().max()) <= (2.0 ** -15 if code == 0 else 2.0 ** -7) * scale
+            again = coli.fp8_wgrad(ga, gs, xa, xs, offsets, rows=rows, dtype=dtype)
+            assert torch.equal(again.nan_to_num(7.0), got.nan_to_num(7.0))
 
 
 def test_wgrad_not_finite_and_no_rows(coli):
