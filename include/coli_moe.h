@@ -617,11 +617,20 @@ COLI_API coli_status coli_fp8_blob_layout(const coli_moe_shape* shape, size_t of
  * matrix w [N][K] of the row's expert; arguments and rows outside the offsets as in
  * coli_mxfp4_matmul, codes at q_off (a multiple of 16) and scales at s_off (of 4) of the expert's
  * buffer (16-byte aligned). With the transposed matrices (coli_quantize_fp8_matrix) it is the input
- * gradient. E <= 1024, K <= 2^22, rows below 2^31 - 4096, N below 2^30 - 4096. */
+ * gradient. E <= 1024, K <= 2^22, rows below 2^31 - 4096, N below 2^30 - 4096. d_ws (nullable, 16-byte
+ * aligned): a workspace of coli_fp8_matmul_workspace_size's bytes, with which a product of some hundreds of
+ * rows, too few tiles for the device, is up to twice as fast (parts of the columns are summed by themselves, in
+ * f32, and then together); smaller ones are not used. It needs no initialisation, and calls that run at the
+ * same time (two graphs' too) need one each. */
 COLI_API coli_status coli_fp8_matmul(const uint8_t* d_a, const float* d_as, int32_t rows, int32_t K,
                                      const int32_t* d_offsets, int32_t E, const void* const* d_blob_table,
                                      size_t q_off, size_t s_off, int32_t N, void* d_y, int32_t dtype,
-                                     int64_t ld, void* stream);
+                                     int64_t ld, void* d_ws, size_t ws_bytes, void* stream);
+
+/* The workspace that coli_fp8_matmul makes use of for these sizes (grouped: with d_offsets) and output type, 0 where
+ * it needs none. Host-only arithmetic. */
+COLI_API coli_status coli_fp8_matmul_workspace_size(int32_t rows, int32_t K, int32_t E, int32_t N,
+                                                    int32_t grouped, int32_t dtype, size_t* bytes);
 
 /* The gate/up product with SwiGLU: h[r][i] = silu(gate_i . a_r) * (up_i . a_r), i < inter, for the
  * matrices gate [inter][K] at q_off, s_off and up [inter][K] at up_q_off, up_s_off. dtype f32, bf16 or

@@ -44,7 +44,7 @@ EXPORTED = [
     "coli_moe_dispatch_bwd", "coli_moe_combine", "coli_moe_combine_bwd",
     "coli_moe_route_groups", "coli_moe_route_groups_bwd",
     "coli_quantize_fp8", "coli_quantize_fp8_matrix", "coli_quantize_fp8_columns", "coli_fp8_column_blocks",
-    "coli_dequantize_fp8", "coli_dequantize_fp8_matrix", "coli_fp8_blob_layout", "coli_fp8_matmul", "coli_fp8_swiglu",
+    "coli_dequantize_fp8", "coli_dequantize_fp8_matrix", "coli_fp8_blob_layout", "coli_fp8_matmul", "coli_fp8_matmul_workspace_size", "coli_fp8_swiglu",
     "coli_fp8_swiglu_workspace_size", "coli_fp8_wgrad", "coli_fp8_wgrad_workspace_size",
     "coli_debug_fp8_kernel", "coli_moe_dispatch_fp8",
 ]
@@ -167,7 +167,8 @@ def lib():
             L.coli_dequantize_fp8.argtypes = [vp, vp, i64, i64, i32, vp, i32, i64, vp]
             L.coli_dequantize_fp8_matrix.argtypes = [vp, i64, vp, i64, i32, i64, i64, vp, i32, i64, i64, vp]
             L.coli_fp8_blob_layout.argtypes = [P(Shape), P(sz), P(sz)]
-            L.coli_fp8_matmul.argtypes = [vp, vp, i32, i32, vp, i32, vp, sz, sz, i32, vp, i32, i64, vp]
+            L.coli_fp8_matmul.argtypes = [vp, vp, i32, i32, vp, i32, vp, sz, sz, i32, vp, i32, i64, vp, sz, vp]
+            L.coli_fp8_matmul_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, P(sz)]
             L.coli_fp8_swiglu.argtypes = [vp, vp, i32, i32, vp, i32, vp, sz, sz, sz, sz, i32, vp, vp, i32,
                                           i64, vp, sz, vp]
             L.coli_fp8_swiglu_workspace_size.argtypes = [i32, i32, i32, i32, i32, P(sz)]
@@ -1124,6 +1125,13 @@ def fp8_blob_layout(shape: MoEShape):
     return list(off), nb.value
 
 
+@functools.lru_cache(4096)
+def _fp8_matmul_ws(rows, K, E, n, grouped, code):
+    nb = ctypes.c_size_t()
+    _check(lib().coli_fp8_matmul_workspace_size(rows, K, E, n, int(grouped), code, ctypes.byref(nb)))
+    return nb.value
+
+
 def fp8_matmul(a, a_s, table, n, q_off=0, s_off=0, offsets=None, dtype=None, out=None, stream=None):
     """out[r] = W_e(r) a[r] for FP8 rows (a, a_s) sorted by expert. table: device array (int64) of pointers
     to the experts' buffers, each with an FP8 [n][K] matrix: codes at q_off, scales at s_off. offsets [E + 1]
@@ -1136,8 +1144,10 @@ def fp8_matmul(a, a_s, table, n, q_off=0, s_off=0, offsets=None, dtype=None, out
     if out is None:
         out = _new(a, (rows, n), dtype or torch.float32, stream)
     code, ld = _rows(out, "out", rows, n, dtype)
-    _enqueue((a, a_s, table, offsets, out), stream, "coli_fp8_matmul", a.data_ptr(), a_s.data_ptr(), rows, K,
-             off, E, table.data_ptr(), q_off, s_off, n, out.data_ptr(), code, ld)
+    nb = _fp8_matmul_ws(rows, K, E, n, off is not None, code)
+    ws = _new(a, (nb,), torch.uint8, stream) if nb else None
+    _enqueue((a, a_s, table, offsets, out, ws), stream, "coli_fp8_matmul", a.data_ptr(), a_s.data_ptr(), rows, K,
+             off, E, table.data_ptr(), q_off, s_off, n, out.data_ptr(), code, ld, None if ws is None else ws.data_ptr(), nb)
     return out
 
 

@@ -795,20 +795,41 @@ static coli_status fp8_product(const char* what, Fp8GemmArgs& a, bool swiglu, in
     if (!a.table || !a.y) return fail(COLI_EINVAL, w + ": NULL pointer");
     if ((st = check_fp8_pair(w, a.a, a.as))) return st;
     if (fp8 && (st = check_fp8_pair(w, a.y, a.ys))) return st;
-    if (fp8 && a.ws && !aligned16(a.ws)) return fail(COLI_EINVAL, w + ": the workspace must be 16-byte aligned");
+    if ((fp8 || !swiglu) && a.ws && !aligned16(a.ws)) return fail(COLI_EINVAL, w + ": the workspace must be 16-byte aligned");
     if (fp8 && ws_bytes < fp8_swiglu_ws(a)) a.ws = nullptr;
+    if (!swiglu && a.ws) {
+        a.parts = fp8_matmul_parts(a, dtype == COLI_F32);
+        if (a.parts > 1 && ws_bytes < fp8_matmul_ws(a)) a.parts = 0;
+    }
     return launch_fp8_gemm(a, swiglu, dtype, (hipStream_t)stream);
 }
 
 coli_status coli_fp8_matmul(const uint8_t* d_a, const float* d_as, int32_t rows, int32_t K, const int32_t* d_offsets,
                             int32_t E, const void* const* d_blob_table, size_t q_off, size_t s_off, int32_t N,
-                            void* d_y, int32_t dtype, int64_t ld, void* stream) {
+                            void* d_y, int32_t dtype, int64_t ld, void* d_ws, size_t ws_bytes, void* stream) {
     COLI_GUARD_BEGIN
     Fp8GemmArgs a = {};
     a.offsets = d_offsets; a.table = d_blob_table; a.rows = rows; a.E = E;
     a.a = d_a; a.as = d_as; a.q_off = q_off; a.s_off = s_off;
-    a.y = d_y; a.ld = ld; a.K = K; a.N = N;
-    return fp8_product("fp8_matmul", a, false, dtype, 0, stream);
+    a.y = d_y; a.ld = ld; a.K = K; a.N = N; a.ws = d_ws;
+    return fp8_product("fp8_matmul", a, false, dtype, ws_bytes, stream);
+    COLI_GUARD_END
+}
+
+coli_status coli_fp8_matmul_workspace_size(int32_t rows, int32_t K, int32_t E, int32_t N, int32_t grouped, int32_t dtype,
+                                           size_t* bytes) {
+    COLI_GUARD_BEGIN
+    coli_status st = check_fp8_product("fp8_matmul_workspace_size", rows, K, E, N, grouped != 0);
+    if (st) return st;
+    if (!elem_dtype(dtype)) return fail(COLI_EUNSUPPORTED, "fp8_matmul_workspace_size: output type not supported");
+    if (!bytes) return fail(COLI_EINVAL, "fp8_matmul_workspace_size: NULL pointer");
+    static const int32_t some = 0;
+    Fp8GemmArgs a = {};
+    a.rows = rows; a.K = K; a.E = E; a.N = N;
+    a.offsets = grouped ? &some : nullptr;      // asked for, not read
+    a.parts = rows == 0 ? 1 : fp8_matmul_parts(a, dtype == COLI_F32);
+    *bytes = a.parts > 1 ? fp8_matmul_ws(a) : 0;
+    return COLI_OK;
     COLI_GUARD_END
 }
 

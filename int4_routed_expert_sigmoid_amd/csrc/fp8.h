@@ -156,6 +156,7 @@ struct Fp8GemmArgs : RowGroups {
     void* ws;                    // fp8_swiglu_ws bytes for one, or nullptr
     int64_t ld;
     int32_t K, N;                // N: rows of the matrix, of gate and of up alone
+    int32_t parts;               // of the columns (a product with a workspace of parts * rows * N f32 sums), or 0
 };
 // The kernel that a product runs: its rows, E, offsets, N and K decide, and whether its results have 32 bits (wide).
 enum Fp8Kernel : int32_t {
@@ -166,6 +167,9 @@ Fp8Kernel choose_fp8_kernel(const Fp8GemmArgs& a, bool swiglu, bool wide);
 coli_status launch_fp8_gemm(const Fp8GemmArgs& a, bool swiglu, int32_t dtype, hipStream_t stream);
 // The workspace that a SwiGLU product into FP8 rows makes use of.
 size_t fp8_swiglu_ws(const Fp8GemmArgs& a);
+// Into how many parts of its columns a product is best divided, 1: into none.
+int fp8_matmul_parts(const Fp8GemmArgs& a, bool wide);
+inline size_t fp8_matmul_ws(const Fp8GemmArgs& a) { return (size_t)a.parts * a.rows * a.N * 4; }
 
 // dw[e][n][k] = sum over the expert's rows (+ dw[e][n][k]); see fp8_wgrad.hip.
 struct Fp8WgradArgs {

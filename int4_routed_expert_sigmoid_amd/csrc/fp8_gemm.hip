@@ -25,7 +25,8 @@
 namespace coli {
 namespace {
 
-// FP8 rows as an output type of the SwiGLU epilogue, and f32 rows on their way there.
+// FP8 rows as an output type of the SwiGLU epilogue, and f32 rows on their way there, or parts of sums on their way to 16
+// bits (products by the FP8 instruction, as the results').
 struct Fp8Out {};
 struct RawOut {};
 
@@ -222,6 +223,7 @@ __global__ __launch_bounds__(64 * WN * KS) void fp8_few_rows_kernel(Fp8GemmArgs 
 // of the rows and read everything twice (8191 x 8192 x 8192: 534 us by tiles of 128).
 // FAST: K in multiples of 512 and rows of scales on 16-byte boundaries: scales come 16 bytes, four blocks, a
 // row, and every unit is whole. Otherwise one block's at a time, and zeros behind the last column.
+// PARTS: each unit once for every part of the columns, into an output of its own (product_parts).
 template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int STAGES, bool FAST>
 struct LineTile {
     static constexpr bool kFp8 = std::is_same<Out, Fp8Out>::value;
@@ -232,7 +234,7 @@ struct LineTile {
     static constexpr int kARows = BM * U / kThreads;          // of them for the rows
     static constexpr int kScaleLoads = BM / 64 + 1;           // 64 rows each, and the matrix' blocks
     static constexpr int kGroup = FAST ? 4 : 1;               // blocks whose scales come together
-    static constexpr int kStores = kFp8 ? MT : SWIGLU ? MT * NF / 2 : MT * (int)sizeof(Out);   // of a wave and whole tile
+    static constexpr int kStores = kFp8 ? MT : SWIGLU ? MT * NF / 2 : MT * (int)sizeof(typename StoredAs<Out>::type);   // of a wave and whole tile
     static_assert(BM * U % kThreads == 0 && BN * U % kThreads == 0, "whole loads for every wave");
     static_assert(kScaleLoads <= kWaves && BM % 64 == 0, "one scale load a wave");
     static_assert((MT == 4 || MT == 8) && NF == 4 && kWaves == 8, "the ring of row fragments; 64 columns and 8 rows a wave");
@@ -248,8 +250,19 @@ struct LineTile {
     };
 };
 
-template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int STAGES, bool FAST>
+struct Place {
+    void* y;
+    int64_t ld;
+};
+
+struct PartUnit : LineUnit {
+    int lo, hi, part;                        // blocks of columns
+};
+
+template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int STAGES, bool FAST, bool PARTS>
 __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a, int NT) {
+    static_assert(!PARTS || !SWIGLU, "SwiGLU takes whole sums");
+    typedef typename StoredAs<Out>::type Stored;
     typedef LineTile<Out, SWIGLU, MT, NF, WM, WN, STAGES, FAST> T;
     constexpr int U = T::U, kGroup = T::kGroup, kW = SWIGLU ? 2 : 1;
     constexpr bool EXACT = std::is_same<Out, float>::value;
@@ -259,20 +272,28 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a
     const int KB = (a.K + kFp8Block - 1) / kFp8Block, KU = a.K / kFp8Unit;
     const uint32_t row_bytes = a.K;
 
-    const uint32_t total = scan_units<T::BM, T::kThreads>(a, NT, lds.first, (uint32_t*)lds.scale[0]);
+    const uint32_t units = scan_units<T::BM, T::kThreads>(a, NT, lds.first, (uint32_t*)lds.scale[0]);
+    const uint32_t total = PARTS ? units * a.parts : units;
     const uint32_t per = (total + kXcds - 1) / kXcds, xcd = blockIdx.x % kXcds, step = gridDim.x / kXcds;
     auto unit_at = [&](uint32_t x) {
         const uint32_t w = xcd * per + x;
-        return line_unit<T::BM>(a, NT, lds.first, w, x < per && w < total);
+        const bool live = x < per && w < total;
+        PartUnit u;
+        u.part = PARTS && live ? w / units : 0;
+        (LineUnit&)u = line_unit<T::BM>(a, NT, lds.first, w - u.part * units, live);
+        const int groups = (KB + 3) / 4;     // whole groups of scales to a part
+        u.lo = PARTS ? groups * u.part / a.parts * 4 : 0;
+        u.hi = PARTS ? min(groups * (u.part + 1) / a.parts * 4, KB) : KB;
+        return u;
     };
     uint32_t at = blockIdx.x / kXcds;        // this workgroup's units: at, at + step, ... of its XCD's `per`
-    LineUnit u = unit_at(at);
+    PartUnit u = unit_at(at);
     if (u.rows <= 0) return;
 
     // the unit that is being loaded
     uint32_t load_at = at;
     const uint8_t *w_base, *a_base, *scale_base;
-    int lc = 0;                              // its next block
+    int lc = 0, load_hi = 0;                 // its next block, and the one behind its last
     bool loading = true;
     uint32_t a_max, w_max;                   // a lane's place in the last row, and in the last matrix row
     const int sx = min(wave, T::kScaleLoads - 1);
@@ -285,7 +306,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a
     const int w_row = SWIGLU ? wave / 4 * kFrag + wave % 2 * 8 + (lane >> 3) : a_row;
     const bool up = SWIGLU && wave / 2 % 2 == 1;
     const uint32_t a_lane = a_row * row_bytes + unit * 16, w_lane = w_row * row_bytes + unit * 16;
-    auto set_unit = [&](const LineUnit& v) {
+    auto set_unit = [&](const PartUnit& v) {
         const int n_tile = v.nt * T::kCols;
         const int m_last = v.rows - 1, n_last = a.N - 1 - n_tile;
         a_max = m_last * row_bytes + unit * 16;
@@ -301,7 +322,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a
             const int b = SWIGLU ? block : min(block + min(lane, T::BN / kFp8Block - 1), last);
             scale_base = v.blob + off + (int64_t)b * KB * 4;
         }
-        lc = 0;
+        lc = v.lo;
+        load_hi = v.hi;
     };
     // Load i of this wave for the block. Behind the last unit the same number of loads goes out, so that the
     // counts hold, of its first block again and into slots that are not read.
@@ -323,10 +345,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a
         fill_scale = fill_scale == STAGES - 1 ? 0 : fill_scale + 1;
     };
     auto advance = [&]() {                   // to the block that is loaded next
-        if (!loading || ++lc < KB) return;
+        if (!loading || ++lc < (PARTS ? load_hi : KB)) return;
         lc = 0;
         load_at += step;
-        const LineUnit v = unit_at(load_at);
+        const PartUnit v = unit_at(load_at);
         loading = v.rows > 0;
         if (loading) set_unit(v);
     };
@@ -390,8 +412,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a
 #pragma unroll
         for (int x = 0; x < 2 * kW; ++x) s_last[x] = 0.f;
 #pragma unroll 1
-        for (int c = 0; c < KB; ++c) {
-            const int fill = slot, next = c + 1 == KB ? 0 : c + 1;
+        for (int c = PARTS ? u.lo : 0; c < (PARTS ? u.hi : KB); ++c) {
+            const int fill = slot, next = c + 1 == (PARTS ? u.hi : KB) ? 0 : c + 1;   // (a part begins with a group of scales)
             float s[MT][kW];
             Wide ww[EXACT ? NF : 1], aw[EXACT ? 2 : 1];
             if constexpr (EXACT) {
@@ -468,14 +490,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a
             const bool there = row < u.rows;
             if constexpr (!SWIGLU) {
                 const int m0 = (i * WM + wm) * kFrag;
+                Stored* y = (Stored*)a.y + (PARTS ? (int64_t)u.part * a.rows * a.ld : 0);
                 if (n_wave + NF * kFrag <= a.N) {         // uniform
-                    store64<Out>((Out*)a.y + (int64_t)(u.m0 + m0) * a.ld + n_wave, a.ld, u.rows - m0, acc[i][0], acc[i][1],
-                                        acc[i][2], acc[i][3]);
+                    store64<Stored>(y + (int64_t)(u.m0 + m0) * a.ld + n_wave, a.ld, u.rows - m0, acc[i][0], acc[i][1], acc[i][2],
+                                    acc[i][3]);
                 } else if (there) {
 #pragma unroll
                     for (int f = 0; f < NF; ++f) {
                         const int n0 = n_wave + f * kFrag + 4 * g;
-                        if (n0 < a.N) store4<Out>(a, m, n0, a.N, acc[i][f]);
+                        if (n0 < a.N) store4<Stored>(Place{y, a.ld}, m, n0, a.N, acc[i][f]);
                     }
                 }
             } else {
@@ -533,16 +556,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a
     wait_loads<0>();                         // nothing lands in LDS after the workgroup
 }
 
-template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int STAGES>
+template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int STAGES, bool PARTS = false>
 coli_status lines(const Fp8GemmArgs& a, hipStream_t stream) {
     typedef LineTile<Out, SWIGLU, MT, NF, WM, WN, STAGES, true> T;
     const int NT = (a.N + T::kCols - 1) / T::kCols;
     uint32_t grid;
-    if (coli_status st = grid_of(a, T::BM, NT, 1, "fp8 product", &grid)) return st;
+    if (coli_status st = grid_of(a, T::BM, NT * (PARTS ? a.parts : 1), 1, "fp8 product", &grid)) return st;
     grid = std::min(grid, kCus);             // LDS holds one workgroup a CU
     const bool fast = a.K % (4 * kFp8Block) == 0 && (uintptr_t)a.as % 16 == 0 && a.s_off % 16 == 0 && (!SWIGLU || a.up_s % 16 == 0);
-    if (fast) launch(fp8_line_kernel<Out, SWIGLU, MT, NF, WM, WN, STAGES, true>, dim3(grid), dim3(T::kThreads), 0, stream, a, NT);
-    else launch(fp8_line_kernel<Out, SWIGLU, MT, NF, WM, WN, STAGES, false>, dim3(grid), dim3(T::kThreads), 0, stream, a, NT);
+    if (fast) launch(fp8_line_kernel<Out, SWIGLU, MT, NF, WM, WN, STAGES, true, PARTS>, dim3(grid), dim3(T::kThreads), 0, stream, a, NT);
+    else launch(fp8_line_kernel<Out, SWIGLU, MT, NF, WM, WN, STAGES, false, PARTS>, dim3(grid), dim3(T::kThreads), 0, stream, a, NT);
     COLI_CHECK_LAUNCH("fp8 product kernel launch");
     return COLI_OK;
 }
@@ -579,9 +602,55 @@ coli_status few_rows_fp8(const Fp8GemmArgs& a, hipStream_t stream) {
     return launch_quantize_fp8(a.ws, COLI_F32, a.rows, a.N, a.N, (uint8_t*)a.y, a.ys, stream, a.offsets, a.E);
 }
 
+// y = the sum of the parts, in their order; a thread has 4 neighbouring columns of a row. Rows outside the offsets stay.
+template <typename T>
+__global__ __launch_bounds__(256) void part_sum_kernel(const float* __restrict__ part, Fp8GemmArgs a, uint32_t per_row) {
+    const uint32_t i = blockIdx.x * 256 + threadIdx.x, m = i / per_row;
+    const int n0 = (int)(i - m * per_row) * 4;
+    if (m >= (uint32_t)a.rows || (a.offsets && ((int)m < a.offsets[0] || (int)m >= a.offsets[a.E]))) return;
+    const int64_t all = (int64_t)a.rows * a.N;
+    const float* p = part + (int64_t)m * a.N + n0;
+    T* y = (T*)a.y + (int64_t)m * a.ld + n0;
+    if (n0 + 4 <= a.N) {
+        float v[4], x[4];
+        load_f32<float, 4>(p, v);
+#pragma unroll 4
+        for (int s = 1; s < a.parts; ++s) {
+            load_f32<float, 4>(p + s * all, x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] += x[j];
+        }
+        store_f32<T, 4>(y, v);
+    } else {
+        for (int j = 0; n0 + j < a.N; ++j) {
+            float v = p[j];
+            for (int s = 1; s < a.parts; ++s) v += p[s * all + j];
+            y[j] = (T)v;
+        }
+    }
+}
+
+// The product in a.parts parts of its columns, f32 sums in the workspace, and their sum.
+template <typename Out>
+coli_status product_parts(const Fp8GemmArgs& a, hipStream_t stream) {
+    constexpr bool kWide = std::is_same<Out, float>::value;
+    Fp8GemmArgs p = a;
+    p.y = a.ws;
+    p.ld = a.N;
+    if (coli_status st = lines<std::conditional_t<kWide, float, RawOut>, false, 4, 4, 2, 4, 3, true>(p, stream)) return st;
+    const uint32_t per_row = ((uint32_t)a.N + 3) / 4;
+    launch(part_sum_kernel<Out>, dim3((uint32_t)(((int64_t)a.rows * per_row + 255) / 256)), dim3(256), 0, stream, (const float*)a.ws, a,
+           per_row);
+    COLI_CHECK_LAUNCH("fp8 product kernel launch");
+    return COLI_OK;
+}
+
 template <typename Out, bool SWIGLU>
 coli_status product(const Fp8GemmArgs& a, hipStream_t stream) {
     constexpr bool kFp8 = std::is_same<Out, Fp8Out>::value, kWide = std::is_same<Out, float>::value;
+    if constexpr (!SWIGLU) {
+        if (a.parts > 1) return product_parts<Out>(a, stream);
+    }
     switch (choose_fp8_kernel(a, SWIGLU, kWide)) {
         case kFp8FewRows16:                  // (not of SwiGLU's)
             if constexpr (!SWIGLU) return few_rows<Out, SWIGLU, 1, 1, 4, 4>(a, stream);
@@ -608,7 +677,12 @@ coli_status product(const Fp8GemmArgs& a, hipStream_t stream) {
 //    rows 534 against 453; 2048 x 6144, 17 to 256 rows 43; 64 of 2048 x 2048, 1024 rows 49; the SwiGLU of 256 988 /
 //    1102.
 // few_rows with 16 matrix rows a workgroup in place of 32 where that leaves no more workgroups than CUs.
-Fp8Kernel choose_fp8_kernel(const Fp8GemmArgs& a, bool swiglu, bool wide) {
+struct Fp8Estimate {
+    Fp8Kernel kernel;
+    int parts;                               // with a workspace, if more than 1
+};
+
+Fp8Estimate estimate_fp8(const Fp8GemmArgs& a, bool swiglu, bool wide) {
     const int64_t experts = a.offsets ? std::min(a.E, a.rows) : 1;
     const double per = (double)a.rows / experts, KB = (double)fp8_blocks(a.K);
     const double bytes = (double)experts * a.N * a.K * (swiglu ? 2 : 1);
@@ -627,12 +701,28 @@ Fp8Kernel choose_fp8_kernel(const Fp8GemmArgs& a, bool swiglu, bool wide) {
     // (as many workgroups as few_rows may need must fit a launch)
     const int64_t stretches = a.offsets ? (int64_t)a.rows / kFrag + std::min(a.E, a.rows) : ((int64_t)a.rows + kFrag - 1) / kFrag;
     const bool fits = stretches * ((a.N + 15) / 16) < int64_t(1) << 23;
-    if (fits && few < std::min(l128, l256)) {
+    Fp8Estimate best = {l256 < l128 ? kFp8Lines256 : kFp8Lines128, 1};
+    double least = std::min(l128, l256);
+    if (fits && few < least) {
         const bool half = !swiglu && experts * tiles(kFrag) * std::ceil(a.N / 16.0) <= kCus;
-        return half ? kFp8FewRows16 : kFp8FewRows32;
+        best.kernel = half ? kFp8FewRows16 : kFp8FewRows32;
+        least = few;
     }
-    return l256 < l128 ? kFp8Lines256 : kFp8Lines128;
+    // Tiles of 128 rows that leave CUs idle, in parts of the columns: as many blocks less, a second launch (5) and the
+    // sums' way through the caches. One matrix of 8192 x 8192 into 16 bits: 64 rows 24 in place of 46, 128 28 / 55, 256
+    // 33 / 54; into f32 64 rows 31 / 48, 256 49 / 105, 512 77 / 105; 512 rows of 2048 x 6144 25 / 43.
+    least -= 5;                              // (what the second launch and the workspace cost the host)
+    const double u = swiglu ? kCus : units(128), block = wide ? 1.85 : 1.03;
+    for (int s = 2; s <= 16 && s * u <= kCus && 4 * s <= KB; ++s) {
+        const double us = 4 + std::max(2 + (std::ceil(KB / 4 / s) * 4) * block, bytes / 5.4e6) + 5 + (double)s * a.rows * a.N * 8 / 8e6;
+        if (us < least) best.parts = s, least = us;
+    }
+    return best;
 }
+
+Fp8Kernel choose_fp8_kernel(const Fp8GemmArgs& a, bool swiglu, bool wide) { return estimate_fp8(a, swiglu, wide).kernel; }
+
+int fp8_matmul_parts(const Fp8GemmArgs& a, bool wide) { return estimate_fp8(a, false, wide).parts; }
 
 size_t fp8_swiglu_ws(const Fp8GemmArgs& a) {
     // (One row, inter 2048, K 512 / 1024 / 1536 / 4096: 6.9 / 11.0 / 15.0 / 34.4 us in one launch, 4.7 / 5.1 / 5.8 / 8.1 in

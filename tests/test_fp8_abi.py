@@ -82,8 +82,8 @@ def test_quantize_refusals(L):
 
 
 def test_product_refusals(L):
-    def mm(a=16, s=16, rows=4, K=64, off=16, E=2, table=16, q=0, so=256, n=8, y=16, dt=0, ld=8):
-        return L.coli_fp8_matmul(a, s, rows, K, off, E, table, q, so, n, y, dt, ld, None)
+    def mm(a=16, s=16, rows=4, K=64, off=16, E=2, table=16, q=0, so=256, n=8, y=16, dt=0, ld=8, ws=None):
+        return L.coli_fp8_matmul(a, s, rows, K, off, E, table, q, so, n, y, dt, ld, ws, 1 << 20, None)
 
     def sw(a=16, s=16, rows=4, K=64, off=16, E=2, table=16, q=0, so=256, n=16, y=16, ys=16, dt=0, ld=16, uq=1024, us=512, ws=None):
         return L.coli_fp8_swiglu(a, s, rows, K, off, E, table, q, so, uq, us, n, y, ys, dt, ld, ws, 1 << 20, None)
@@ -96,6 +96,7 @@ def test_product_refusals(L):
         assert f(a=None) == EINVAL and f(table=None) == EINVAL and f(y=None) == EINVAL and f(s=None) == EINVAL
         assert f(rows=0, a=None, table=None, y=None) == OK
         assert f(n=(1 << 31) - 1, ld=1 << 31) == EUNSUP and f(rows=(1 << 31) - 1) == EUNSUP
+    assert mm(ws=24) == EINVAL
     assert mm(dt=coli.FP8) == EUNSUP                             # only the SwiGLU writes FP8
     assert sw(n=24, ld=24, dt=coli.FP8) == EINVAL and sw(dt=coli.FP8, ys=None) == EINVAL and sw(dt=coli.FP8, y=24) == EINVAL
     assert sw(uq=8) == EINVAL and sw(us=2) == EINVAL and sw(dt=coli.FP8, ws=24) == EINVAL
@@ -131,6 +132,12 @@ def test_sizes(L):
         assert size(rows, K, E, inter, grouped, ctypes.byref(nb)) == OK and nb.value == want
     assert size(4, 40, 1, 16, 0, ctypes.byref(nb)) == EINVAL and size(4, 48, 2, 16, 0, ctypes.byref(nb)) == EINVAL
     assert size(4, 48, 1, 16, 0, None) == EINVAL
+    size = coli.lib().coli_fp8_matmul_workspace_size
+    for rows, K, E, n, dtype, parts in ((8, 8192, 1, 8192, 1, 0), (64, 8192, 1, 8192, 1, 8), (128, 8192, 1, 8192, 1, 6), (8191, 8192, 1, 8192, 0, 0),
+                                        (512, 8192, 1, 8192, 0, 2), (16384, 2048, 256, 6144, 1, 0), (0, 64, 1, 64, 0, 0)):
+        assert size(rows, K, E, n, int(E > 1), dtype, ctypes.byref(nb)) == OK and nb.value == 4 * parts * rows * n
+    assert size(4, 40, 1, 16, 0, 0, ctypes.byref(nb)) == EINVAL and size(4, 48, 2, 16, 0, 0, ctypes.byref(nb)) == EINVAL
+    assert size(4, 48, 1, 16, 0, 3, ctypes.byref(nb)) == EUNSUP and size(4, 48, 1, 16, 0, 0, None) == EINVAL
     size = coli.lib().coli_fp8_wgrad_workspace_size
     for rows, E, n, K, parts in ((4095, 1, 6144, 8192, 1), (16384, 64, 2048, 6144, 1), (500, 1, 128, 128, 1), (0, 1, 16, 16, 1),
                                  (4096, 1, 128, 256, 16), (8082, 1, 2384, 1024, 3), (1400, 1, 48, 80, 5),

@@ -323,6 +323,7 @@ def test_matmul(coli, case, dtype, odd):
     offsets, off, rows = _groups(counts, before, behind)
     E, exact = len(off) - 1, dtype == "float32"
     assert coli.debug_fp8_kernel(rows, K, E, n, grouped=offsets is not None, wide=exact) == (wide if exact else kernel)
+    assert coli._fp8_matmul_ws(rows, K, E, n, offsets is not None, 0 if exact else 1) == 0
     rng = np.random.default_rng(K + n)
     _keep, table, matrix, at = _weights(rng, E, n, K, odd=odd)
     a, a_s, va = _rows(rng, rows, K)
@@ -421,6 +422,35 @@ def test_not_finite(coli):
             want = torch.zeros(40, 33, dtype=torch.bool, device="cuda")
             want[3], want[5], want[:, 7] = True, True, True
             assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("odd", (0, 4))
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("counts,K,n,before,behind", [(150, 5136, 4100, 0, 0), ([130, 0, 123], 8192, 1030, 3, 4),
+                                                      (64, 8192, 8192, 0, 0), ([1, 257, 0, 40], 8208, 777, 0, 2)],
+                         ids=lambda v: str(v).replace(" ", ""))
+def test_matmul_parts(coli, counts, K, n, before, behind, dtype, odd):
+    """Columns summed in parts, in a workspace: another order of the same sums; rows outside the offsets stay."""
+    import torch
+    offsets, off, rows = _groups(counts, before, behind)
+    E, exact = len(off) - 1, dtype == "float32"
+    assert coli._fp8_matmul_ws(rows, K, E, n, offsets is not None, 1) > 0 or n == 777
+    rng = np.random.default_rng(K + n + 2)
+    _keep, table, matrix, at = _weights(rng, E, n, K, odd=odd)
+    a, a_s, va = _rows(rng, rows, K)
+    y, terms = _product(va, matrix, off, n)
+    out = torch.full((rows, n + 3), 7.0, dtype=_t(dtype), device="cuda")
+    coli.fp8_matmul(a, a_s, table, n, offsets=offsets, out=out[:, :n], **at)
+    lo, hi = int(off[0]), int(off[-1])
+    assert bool((out[:, n:] == 7.0).all()) and bool((out[:lo] == 7.0).all()) and bool((out[hi:] == 7.0).all())
+    err, y = (out[lo:hi, :n].double() - y[lo:hi]).abs(), y[lo:hi]
+    assert bool((err <= ref.product_bound(K, terms[lo:hi], exact) * (1 + _half_step(dtype)) + _half(dtype, y)).all())
+    assert float(err.norm()) <= (ref.norm_bound(K, exact) + _half_step(dtype)) * float(y.norm())
+    again = coli.fp8_matmul(a, a_s, table, n, offsets=offsets, dtype=_t(dtype), **at)
+    assert torch.equal(again[lo:hi], out[lo:hi, :n])
+    a[lo + 1, K - 1] = 0x7F                                       # a NaN in one part
+    bad = coli.fp8_matmul(a, a_s, table, n, offsets=offsets, dtype=_t(dtype), **at)[lo:hi].isnan()
+    assert bool(bad[1].all()) and int(bad.sum()) == n
 
 
 def test_products_past_32_bits(coli):
