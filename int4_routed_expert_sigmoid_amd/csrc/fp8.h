@@ -136,8 +136,8 @@ struct Fp8ColumnArgs {
 };
 coli_status launch_quantize_fp8_columns(const Fp8ColumnArgs& a, int32_t dtype, hipStream_t stream);
 
-// block_rows: rows that share a scale, 1 or 128. `count` matrices: codes and scales q_stride and s_stride bytes apart,
-// outputs x_stride elements.
+// block_rows: rows that share a scale, 1 or 128. `count` matrices: codes and scales q_stride and s_stride bytes
+// apart, outputs x_stride elements.
 coli_status launch_dequantize_fp8(const uint8_t* q, const float* s, int64_t rows, int64_t cols,
                                   int32_t block_rows, void* x, int32_t dtype, int64_t ld,
                                   hipStream_t stream, int32_t count = 1, int64_t q_stride = 0, int64_t s_stride = 0,

@@ -1,21 +1,21 @@
 // Grouped products of FP8 rows with FP8 matrices: y[r][n] = sum over blocks b of 128 columns of
 // sa[r][b] sw[n / 128][b] <a[r], w_e(r)[n]>_b, rows sorted by expert.
 //
-// v_mfma_f32_16x16x128_f8f6f4 multiplies 16 rows by 16 rows over one block: a lane holds 32 of the
-// block's 128 columns of row l % 16, here the 16-byte units l / 16 and l / 16 + 4 (a block's columns
-// may be taken in any order, as long as both sides take the same). The block's sum (for its accuracy, and
-// what results of 32 bits take in its place, see fp8.h) starts from 0 and enters the row's f32 sum by one multiplication: scales are any f32
-// numbers, so they cannot go into the instruction, which takes powers of two. The matrix rows are the
-// first operand: result lane l then holds outputs n = 4 (l / 16) .. + 3 of one row m = l % 16, whose
-// scale for the block is one number a lane, as the 16 matrix rows have one together.
+// v_mfma_f32_16x16x128_f8f6f4 multiplies 16 rows by 16 rows over one block: a lane holds 32 of the block's 128
+// columns of row l % 16, here the 16-byte units l / 16 and l / 16 + 4 (a block's columns may be taken in any order,
+// as long as both sides take the same). The block's sum (for its accuracy, and what results of 32 bits take in its
+// place, see fp8.h) starts from 0 and enters the row's f32 sum by one multiplication: scales are any f32 numbers,
+// so they cannot go into the instruction, which takes powers of two. The matrix rows are the first operand: result
+// lane l then holds outputs n = 4 (l / 16) .. + 3 of one row m = l % 16, whose scale for the block is one number a
+// lane, as the 16 matrix rows have one together.
 //
 // Bounds and times on one MI355X, where a copy moves 4.7 TB/s and a CU takes in about 35 GB/s from beyond its LDS:
-//  - few rows: the matrices' bytes. 8192 x 8192, one to 16 rows, 67 MB: 17 us (4.0 TB/s); SwiGLU of 8 of 256 experts
-//    of 2048 x 6144, 201 MB: 41 (4.9).
+//  - few rows: the matrices' bytes. 8192 x 8192, one to 16 rows, 67 MB: 17 us (4.0 TB/s); SwiGLU of 8 of 256
+//    experts of 2048 x 6144, 201 MB: 41 (4.9).
 //  - many rows: the matrix unit, in which a block of a tile takes 1.2 us of the 1.73 that it takes altogether. What
-//    keeps the rest: a tile of 256 by 256 brings in 64 KB a block, 1.8 us at a CU's rate if nothing hits a cache near
-//    by; and the four scalings of a product share the issue slots with the matrix instructions. 8191 x 8192 x 8192
-//    into bf16: 450 us, 2.44 PFLOP/s; of these 16 go if every load hits the L2 cache, 60 with no loads.
+//    keeps the rest: a tile of 256 by 256 brings in 64 KB a block, 1.8 us at a CU's rate if nothing hits a cache
+//    near by; and the four scalings of a product share the issue slots with the matrix instructions. 8191 x 8192 x
+//    8192 into bf16: 450 us, 2.44 PFLOP/s; of these 16 go if every load hits the L2 cache, 60 with no loads.
 //  - SwiGLU of all of 256 experts of 2048 x 6144, 6.4 GB: 1.19 ms (5.6 TB/s) for 1 to 8 rows an expert and more.
 #include <algorithm>
 #include <cmath>
@@ -25,8 +25,8 @@
 namespace coli {
 namespace {
 
-// FP8 rows as an output type of the SwiGLU epilogue, and f32 rows on their way there, or parts of sums on their way to 16
-// bits (products by the FP8 instruction, as the results').
+// FP8 rows as an output type of the SwiGLU epilogue, and f32 rows on their way there, or parts of sums on their way
+// to 16 bits (products by the FP8 instruction, as the results').
 struct Fp8Out {};
 struct RawOut {};
 
@@ -586,8 +586,8 @@ coli_status few_rows(const Fp8GemmArgs& a, hipStream_t stream) {
 
 // SwiGLU of few rows into FP8. A block of 128 h is one workgroup's, whose CU takes in about 35 GB/s, so that fewer
 // workgroups than CUs leave the device idle: then, with a workspace for h in f32, it is formed 16 columns a
-// workgroup and quantised by a launch of its own (K 6144, inter 2048: 8 rows of 8 of 256 experts 41 us against 58, one
-// row 11 against 51; from 256 workgroups on, 40 rows of 40 experts, 188 against the one launch's 186).
+// workgroup and quantised by a launch of its own (K 6144, inter 2048: 8 rows of 8 of 256 experts 41 us against 58,
+// one row 11 against 51; from 256 workgroups on, 40 rows of 40 experts, 188 against the one launch's 186).
 int64_t few_rows_blocks(const Fp8GemmArgs& a) {
     const int64_t experts = a.offsets ? std::min(a.E, a.rows) : 1;
     return experts * ((a.rows + experts * kFrag - 1) / (experts * kFrag)) * fp8_blocks(a.N);
@@ -602,7 +602,8 @@ coli_status few_rows_fp8(const Fp8GemmArgs& a, hipStream_t stream) {
     return launch_quantize_fp8(a.ws, COLI_F32, a.rows, a.N, a.N, (uint8_t*)a.y, a.ys, stream, a.offsets, a.E);
 }
 
-// y = the sum of the parts, in their order; a thread has 4 neighbouring columns of a row. Rows outside the offsets stay.
+// y = the sum of the parts, in their order; a thread has 4 neighbouring columns of a row. Rows outside the offsets
+// stay.
 template <typename T>
 __global__ __launch_bounds__(256) void part_sum_kernel(const float* __restrict__ part, Fp8GemmArgs a, uint32_t per_row) {
     const uint32_t i = blockIdx.x * 256 + threadIdx.x, m = i / per_row;
@@ -669,13 +670,13 @@ coli_status product(const Fp8GemmArgs& a, hipStream_t stream) {
 // Which kernel, by estimates of each one's time in us, from times on one MI355X (graphs, warm caches):
 //  - few_rows reads a matrix once per 16 rows, 5.5 TB/s the first time and 6 from the caches, and a workgroup takes
 //    in its rows no faster than about 35 GB/s: 1.3 us per 1024 columns; 1024 workgroups take 3 at least. One matrix
-//    of 8192 x 8192, 17 / 64 / 128 / 256 rows 25.7 / 47 / 90 / 176; 2048 x 6144 (N, K), 64 / 256 rows 11.4 / 35; 64 of
-//    2048 x 2048, 1024 rows 71; SwiGLU of 256 of 2048 x 6144, 512 / 2048 rows 928 / 1166.
+//    of 8192 x 8192, 17 / 64 / 128 / 256 rows 25.7 / 47 / 90 / 176; 2048 x 6144 (N, K), 64 / 256 rows 11.4 / 35; 64
+//    of 2048 x 2048, 1024 rows 71; SwiGLU of 256 of 2048 x 6144, 512 / 2048 rows 928 / 1166.
 //  - lines takes 2 for a unit's ends and a time a block of columns: tiles of 128 rows 0.78 while they leave half of
-//    the CUs idle, 1.03 where they do not, of 256 rows 1.8, for 32-bit results 1.5 to 1.85; and 5.4 TB/s. 8192 x 8192:
-//    17 to 512 rows 56 (f32 103 to 108), 1024 rows 72 against 103 for tiles of 256, 2048 rows 135 against 121, 8192
-//    rows 534 against 453; 2048 x 6144, 17 to 256 rows 43; 64 of 2048 x 2048, 1024 rows 49; the SwiGLU of 256 988 /
-//    1102.
+//    the CUs idle, 1.03 where they do not, of 256 rows 1.8, for 32-bit results 1.5 to 1.85; and 5.4 TB/s. 8192 x
+//    8192: 17 to 512 rows 56 (f32 103 to 108), 1024 rows 72 against 103 for tiles of 256, 2048 rows 135 against
+//    121, 8192 rows 534 against 453; 2048 x 6144, 17 to 256 rows 43; 64 of 2048 x 2048, 1024 rows 49; the SwiGLU of
+//    256 988 / 1102.
 // few_rows with 16 matrix rows a workgroup in place of 32 where that leaves no more workgroups than CUs.
 struct Fp8Estimate {
     Fp8Kernel kernel;
@@ -708,9 +709,9 @@ Fp8Estimate estimate_fp8(const Fp8GemmArgs& a, bool swiglu, bool wide) {
         best.kernel = half ? kFp8FewRows16 : kFp8FewRows32;
         least = few;
     }
-    // Tiles of 128 rows that leave CUs idle, in parts of the columns: as many blocks less, a second launch (5) and the
-    // sums' way through the caches. One matrix of 8192 x 8192 into 16 bits: 64 rows 24 in place of 46, 128 28 / 55, 256
-    // 33 / 54; into f32 64 rows 31 / 48, 256 49 / 105, 512 77 / 105; 512 rows of 2048 x 6144 25 / 43.
+    // Tiles of 128 rows that leave CUs idle, in parts of the columns: as many blocks less, a second launch (5) and
+    // the sums' way through the caches. One matrix of 8192 x 8192 into 16 bits: 64 rows 24 in place of 46, 128 28 /
+    // 55, 256 33 / 54; into f32 64 rows 31 / 48, 256 49 / 105, 512 77 / 105; 512 rows of 2048 x 6144 25 / 43.
     least -= 5;                              // (what the second launch and the workspace cost the host)
     const double u = swiglu ? kCus : units(128), block = wide ? 1.85 : 1.03;
     for (int s = 2; s <= 16 && s * u <= kCus && 4 * s <= KB; ++s) {
@@ -725,8 +726,8 @@ Fp8Kernel choose_fp8_kernel(const Fp8GemmArgs& a, bool swiglu, bool wide) { retu
 int fp8_matmul_parts(const Fp8GemmArgs& a, bool wide) { return estimate_fp8(a, false, wide).parts; }
 
 size_t fp8_swiglu_ws(const Fp8GemmArgs& a) {
-    // (One row, inter 2048, K 512 / 1024 / 1536 / 4096: 6.9 / 11.0 / 15.0 / 34.4 us in one launch, 4.7 / 5.1 / 5.8 / 8.1 in
-    // two, which cost the host 4.5 more.)
+    // (One row, inter 2048, K 512 / 1024 / 1536 / 4096: 6.9 / 11.0 / 15.0 / 34.4 us in one launch, 4.7 / 5.1 / 5.8
+    // / 8.1 in two, which cost the host 4.5 more.)
     const bool two = fp8_blocks(a.K) > 8 && few_rows_blocks(a) < kCus && choose_fp8_kernel(a, true, false) == kFp8FewRows32;
     return two ? (size_t)a.rows * a.N * 4 : 0;
 }

@@ -1,13 +1,13 @@
-// FP8 rows and matrices: e4m3 codes with a scale for each block of 128 columns (of one row, or
-// of 128 rows of a matrix), the same by columns for a product over rows, and back.
+// FP8 rows and matrices: e4m3 codes with a scale for each block of 128 columns (of one row, or of 128 rows of a
+// matrix), the same by columns for a product over rows, and back.
 //
-// A lane takes 16 bytes of values (4 or 8 columns), so that a block of a row is 32 or 16 lanes and
-// its largest |x| is theirs by DPP exchanges. Scales are powers of two (fp8.h): x / scale is exact
-// and e4m3's rounding (the hardware convert, half to even) is the only one. All of these are bound
-// by HBM. On one MI355X (a copy: 4.7 TB/s): 16383 rows of 2048 bf16, 102 MB, 21 us, and back 15 (out of the caches, in part);
-// 16 matrices of 6144 x 2048 f32 both ways round, 1.2 GB, 190 us (6.4 TB/s), and back from either, 103; the columns of
-// 16384 rows of 2048 bf16 by 64 experts, with the rows, 134 MB, 37, of 6144 without, 302 MB, 71 (48 and 98 with the
-// tile in f32, which leaves room for three workgroups a CU in place of six).
+// A lane takes 16 bytes of values (4 or 8 columns), so that a block of a row is 32 or 16 lanes and its largest |x|
+// is theirs by DPP exchanges. Scales are powers of two (fp8.h): x / scale is exact and e4m3's rounding (the
+// hardware convert, half to even) is the only one. All of these are bound by HBM. On one MI355X (a copy: 4.7 TB/s):
+// 16383 rows of 2048 bf16, 102 MB, 21 us, and back 15 (out of the caches, in part); 16 matrices of 6144 x 2048 f32
+// both ways round, 1.2 GB, 190 us (6.4 TB/s), and back from either, 103; the columns of 16384 rows of 2048 bf16 by
+// 64 experts, with the rows, 134 MB, 37, of 6144 without, 302 MB, 71 (48 and 98 with the tile in f32, which leaves
+// room for three workgroups a CU in place of six).
 #include "fp8.h"
 
 namespace coli {

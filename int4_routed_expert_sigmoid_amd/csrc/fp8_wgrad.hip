@@ -1,15 +1,15 @@
-// Every expert's matrix gradient from FP8 rows and output gradients: dw_e[n][k] = sum over the expert's
-// rows r of g[r][n] x[r][k], both quantised over 128 of its rows (a block of the sum) by one column and
-// laid out by columns, so that the sum runs along the rows of both operands.
+// Every expert's matrix gradient from FP8 rows and output gradients: dw_e[n][k] = sum over the expert's rows r of
+// g[r][n] x[r][k], both quantised over 128 of its rows (a block of the sum) by one column and laid out by columns,
+// so that the sum runs along the rows of both operands.
 //
-// The scales are powers of two and go into the matrix instruction (one E8M0 byte for each row of an
-// operand and block), or into the conversion to bf16 for 32-bit results (fp8.h), so that sums stay in
-// the instruction's registers from block to block.
+// The scales are powers of two and go into the matrix instruction (one E8M0 byte for each row of an operand and
+// block), or into the conversion to bf16 for 32-bit results (fp8.h), so that sums stay in the instruction's
+// registers from block to block.
 //
-// What bounds it: the gradients that it writes where experts have few rows (64 experts of 2048 x 6144, 256 rows each,
-// one MI355X: 3.2 GB of f32 in 780 us, 4.1 TB/s, added to what is there 1244, 5.2 TB/s; bf16 417 and 782), the bf16 matrix
-// instructions where there are many and results have 32 bits (6144 x 8192 from 4095 rows, 0.41 TFLOP: 337 us, 1.22
-// PFLOP/s, where a large bf16 product reaches 1.34; bf16 162, 2.5 PFLOP/s).
+// What bounds it: the gradients that it writes where experts have few rows (64 experts of 2048 x 6144, 256 rows
+// each, one MI355X: 3.2 GB of f32 in 780 us, 4.1 TB/s, added to what is there 1244, 5.2 TB/s; bf16 417 and 782),
+// the bf16 matrix instructions where there are many and results have 32 bits (6144 x 8192 from 4095 rows, 0.41
+// TFLOP: 337 us, 1.22 PFLOP/s, where a large bf16 product reaches 1.34; bf16 162, 2.5 PFLOP/s).
 #include <algorithm>
 
 #include "fp8.h"
@@ -18,12 +18,12 @@ namespace coli {
 namespace {
 
 // Persistent workgroups of WM x WN waves, each MT fragments of g's columns (n) by NF fragments of x's (k), as
-// fp8_gemm.hip's lines: codes and scales straight into LDS, a block of 128 rows at a time, STAGES blocks
-// ahead and on into the workgroup's next unit (a tile of one expert's gradient, whose sum has as many
-// blocks as the expert has rows for, none where it has no rows). x is the first operand: a lane's four
-// results are four neighbouring k. Results of 32 bits have tiles of 128 n in three stages (256 would leave the operands'
-// bf16 form no registers), the others of 256 in two. Where they are added to what is there (ADD), which is loaded at a
-// tile's end all at once (row by row: 1880 us for the 1244 above), all have 128.
+// fp8_gemm.hip's lines: codes and scales straight into LDS, a block of 128 rows at a time, STAGES blocks ahead and
+// on into the workgroup's next unit (a tile of one expert's gradient, whose sum has as many blocks as the expert
+// has rows for, none where it has no rows). x is the first operand: a lane's four results are four neighbouring k.
+// Results of 32 bits have tiles of 128 n in three stages (256 would leave the operands' bf16 form no registers),
+// the others of 256 in two. Where they are added to what is there (ADD), which is loaded at a tile's end all at
+// once (row by row: 1880 us for the 1244 above), all have 128.
 template <typename T, int MT, int NF, int WM, int WN, int STAGES>
 struct WgradTile {
     static constexpr int BM = WM * MT * kFrag, BN = WN * NF * kFrag, kWaves = WM * WN, kThreads = 64 * kWaves;
@@ -58,11 +58,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(Fp8WgradArgs a, 
     const RowGroups groups = {a.offsets, nullptr, a.rows, a.E};
     const int blocks = min((int)scan_units<kFp8Block, W::kThreads>(groups, 1, lds.first, lds.scale[0][0]), a.blocks);
     const uint32_t per_expert = (uint32_t)NT * KT, total = per_expert * a.E * a.splits;
-    // Units in order of expert, stretches of `tall` tiles of n, k, n, round all workgroups, and with them round the XCDs: the
-    // device writes neighbouring tiles at a time. With KT a multiple of 4 and tall 1 an XCD reads an eighth or a
-    // quarter of x's columns, with tall 8 a stretch of its own of g's. (An eighth of the units for each XCD in place of
-    // it: 64 experts' 2048 x 6144 in f32 799 us in place of 780, 16 of 2048 x 6400 326 in place of 298, 4 of 5008 x 1280
-    // in bf16 251 in place of 213; tall 1 where KT is 7 184 in place of 177, tall 8 where it is 32 367 in place of 349.)
+    // Units in order of expert, stretches of `tall` tiles of n, k, n, round all workgroups, and with them round the
+    // XCDs: the device writes neighbouring tiles at a time. With KT a multiple of 4 and tall 1 an XCD reads an
+    // eighth or a quarter of x's columns, with tall 8 a stretch of its own of g's. (An eighth of the units for each
+    // XCD in place of it: 64 experts' 2048 x 6144 in f32 799 us in place of 780, 16 of 2048 x 6400 326 in place of
+    // 298, 4 of 5008 x 1280 in bf16 251 in place of 213; tall 1 where KT is 7 184 in place of 177, tall 8 where it
+    // is 32 367 in place of 349.)
     const uint32_t tall = KT % 4 == 0 ? 1 : 8;
     auto unit_at = [&](uint32_t w) {
         WgradUnit u = {0, 0, 0, 0, -1};
@@ -316,9 +317,10 @@ __global__ __launch_bounds__(256) void wgrad_sum_kernel(const float* __restrict_
     store_f32<T, 4>(p, x);
 }
 
-// Into how many parts an expert's rows are divided: a tile takes about 1.5 us a block of rows, however few tiles there
-// are, and the parts' sum a launch (5) and its bytes. (One gradient of 1024 x 256 from 65536 rows: 732 us in one part, 55
-// in 32; 2048 x 2048 from 16384 192 and 129 in 2; 256 x 1168 from 3274 44 and 19 in 8; 48 x 80 from 1400 21 and 12 in 5.)
+// Into how many parts an expert's rows are divided: a tile takes about 1.5 us a block of rows, however few tiles
+// there are, and the parts' sum a launch (5) and its bytes. (One gradient of 1024 x 256 from 65536 rows: 732 us in
+// one part, 55 in 32; 2048 x 2048 from 16384 192 and 129 in 2; 256 x 1168 from 3274 44 and 19 in 8; 48 x 80 from
+// 1400 21 and 12 in 5.)
 int wgrad_splits(const Fp8WgradArgs& a) {
     const int64_t units = (int64_t)((a.N + 127) / 128) * ((a.K + 255) / 256) * a.E;
     const double blocks = (double)a.rows / kFp8Block / a.E, one = 1.6 * blocks;

@@ -104,11 +104,12 @@ __device__ __forceinline__ uint32_t merge_halves(uint32_t x, uint32_t y) {
     else return (uint32_t)__builtin_amdgcn_update_dpp((int)y, (int)x, 0x128, 0xf, 0x3, false);
 }
 
-// Four fragments of results, columns 0 .. 63 of a row behind `out` (its row 0 and first column), in whole cache lines: of
-// a fragment's 16 rows, a store takes 8 rows by 128 bytes, so that no line is written in parts. A lane holds
-// row lane % 16; rows from `rows` on are left out. (3.2 GB of f32 by 16 rows of 64 bytes a store took 696 us, by whole
-// lines 624.) They go past the caches, which hold the operands (gradients of 64 experts' 2048 x 6144 matrices, 256 rows
-// each: 1136 us through them, 828 past them; in bf16 646 and 417). Two stores for a 16-bit type, four for f32.
+// Four fragments of results, columns 0 .. 63 of a row behind `out` (its row 0 and first column), in whole cache
+// lines: of a fragment's 16 rows, a store takes 8 rows by 128 bytes, so that no line is written in parts. A lane
+// holds row lane % 16; rows from `rows` on are left out. (3.2 GB of f32 by 16 rows of 64 bytes a store took 696 us,
+// by whole lines 624.) They go past the caches, which hold the operands (gradients of 64 experts' 2048 x 6144
+// matrices, 256 rows each: 1136 us through them, 828 past them; in bf16 646 and 417). Two stores for a 16-bit type,
+// four for f32.
 template <typename T>
 __device__ __forceinline__ void store64(T* out, int64_t ld, int rows, const f32x4& v0, const f32x4& v1, const f32x4& v2,
                                         const f32x4& v3) {
