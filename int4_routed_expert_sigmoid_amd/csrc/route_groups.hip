@@ -12,10 +12,10 @@
 // the whole choice, does not hang on how an exponential was computed; gradients are f32. A wave has one
 // token; lane l holds experts l * EPL .. + EPL - 1.
 //
-// What bounds them: the forward, instructions, 777 a token: 16384 tokens of 256 experts, softmax, 4 of 8 groups, k 8
-// take 28 us (the bytes alone 8), of which the k rounds of a maximum over the wave are 10, the groups 4, the
-// exponentials in 64 bits 2.5. (Four tokens a wave, 16 lanes each, are slower: 34.) The backward, HBM: 12. One token
-// takes a launch, 5.
+// What bounds them: the forward, instructions: 16384 tokens of 256 experts, softmax, 4 of 8 groups, k 8 take 25 us
+// (the bytes alone 8), of which the k rounds of a maximum over the wave are about 8, the groups 3, the exponentials in
+// 64 bits 2.5. (28 with keys and experts in one 64-bit code; four tokens a wave, 16 lanes each, are slower: 34.) The
+// backward, HBM: 12. One token takes a launch, 4.
 #include "mxfp4.h"
 #include "route_groups.h"
 
@@ -63,9 +63,9 @@ __device__ __forceinline__ uint32_t wave_top(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// The code by which a key is chosen; a NaN key comes first, so that it shows in the weights.
-__device__ __forceinline__ uint64_t key_code(float key, int e) {
-    return selection_code(key != key ? __uint_as_float(0x7fc00000u) : key, e);
+// The code by which a key is chosen, above 0; a NaN key comes first, so that it shows in the weights.
+__device__ __forceinline__ uint32_t key_code(float key) {
+    return (uint32_t)(selection_code(key != key ? __uint_as_float(0x7fc00000u) : key, 0) >> 32);
 }
 
 // The two largest of four, each pair in order.
@@ -73,6 +73,15 @@ __device__ __forceinline__ void merge2(float& a0, float& a1, float b0, float b1)
     const float hi = fmaxf(a0, b0), lo = fminf(a0, b0);
     a1 = fmaxf(lo, fmaxf(a1, b1));
     a0 = hi;
+}
+
+// How many of the groups, whose codes the lanes 0, step, 2 step, .. hold, come before group `mine`.
+__device__ __forceinline__ int group_rank(uint32_t code, uint32_t mine, int groups, uint32_t step) {
+    const uint64_t self = (uint64_t)code << 32 | ~mine;
+    int rank = 0;
+    for (uint32_t j = 0; j < (uint32_t)groups; ++j)
+        rank += ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)code, j * step) << 32 | ~j) > self;
+    return rank;
 }
 
 template <typename T, int EPL>
@@ -122,9 +131,9 @@ __global__ __launch_bounds__(kThreads) void route_groups_kernel(RouteArgs a) {
     for (int i = 0; i < EPL; ++i) key[i] = l[i] == none || b[i] == none || e0 + i >= E ? none : s[i] + b[i];
 
     // the groups whose experts can be chosen
-    uint64_t c[EPL];
+    uint32_t c[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) c[i] = key[i] != none ? key_code(key[i], e0 + i) : 0;
+    for (int i = 0; i < EPL; ++i) c[i] = key[i] != none ? key_code(key[i]) : 0;
     if (a.kept < a.groups) {
         const uint32_t size = E / a.groups, wide = size / EPL;
         if (size % EPL == 0 && (wide & (wide - 1)) == 0) {
@@ -151,14 +160,8 @@ __global__ __launch_bounds__(kThreads) void route_groups_kernel(RouteArgs a) {
             join(std::integral_constant<int, 16>{});
             join(std::integral_constant<int, 32>{});
             const float value = nan ? __uint_as_float(0x7fc00000u) : a.group_top == 2 && second != none ? first + second : first;
-            const uint64_t code = value != none ? key_code(value, lane / wide) : 0;
-            int rank = 0;
-            for (int j = 0; j < a.groups; ++j) {
-                const int from = j * wide;
-                const uint64_t other = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(code >> 32), from) << 32 |
-                                       (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)code, from);
-                rank += other > code;
-            }
+            const uint32_t code = value != none ? key_code(value) : 0;
+            const int rank = group_rank(code, lane / wide, a.groups, wide);
 #pragma unroll
             for (int i = 0; i < EPL; ++i) c[i] = rank < a.kept ? c[i] : 0;
         } else {
@@ -177,48 +180,50 @@ __global__ __launch_bounds__(kThreads) void route_groups_kernel(RouteArgs a) {
                 }
             }
             const float value = nan ? __uint_as_float(0x7fc00000u) : a.group_top == 2 && second != none ? first + second : first;
-            const uint64_t code = lane < a.groups && value != none ? key_code(value, lane) : 0;
-            int rank = 0;
-            for (int j = 0; j < a.groups; ++j) {
-                const uint64_t other = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(code >> 32), j) << 32 |
-                                       (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)code, j);
-                rank += other > code;
-            }
+            const uint32_t code = lane < a.groups && value != none ? key_code(value) : 0;
+            const int rank = group_rank(code, lane, a.groups, 1);
             const uint64_t open = __ballot(code != 0 && rank < a.kept);
 #pragma unroll
             for (int i = 0; i < EPL; ++i) c[i] = open >> (((uint32_t)(e0 + i) * div) >> 21 & 63) & 1 ? c[i] : 0;
             __builtin_amdgcn_wave_barrier();
         }
     }
-    // The scores where a slot finds them by its expert. Each lane's codes in descending order, then k times the
-    // largest of the lanes' first codes, which that lane drops.
+    // The scores where a slot finds them by its expert. Each lane's codes in descending order (equal ones as they
+    // are), with their places among its experts, 4 bits each; then k times the largest of the lanes' first codes, which
+    // that lane drops; of equal ones the lowest lane's, whose experts come first.
+    uint32_t place[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) lds[wave][e0 + i] = s[i];
+    for (int i = 0; i < EPL; ++i) {
+        lds[wave][e0 + i] = s[i];
+        place[i] = i;
+    }
 #pragma unroll
     for (int pass = 0; pass < EPL; ++pass)
 #pragma unroll
         for (int i = pass & 1; i + 1 < EPL; i += 2) {
             const bool sw = c[i + 1] > c[i];
-            const uint64_t x = c[i], y = c[i + 1];
+            const uint32_t x = c[i], y = c[i + 1], p = place[i], q = place[i + 1];
             c[i] = sw ? y : x;
             c[i + 1] = sw ? x : y;
+            place[i] = sw ? q : p;
+            place[i + 1] = sw ? p : q;
         }
+    typedef std::conditional_t<EPL == 16, uint64_t, uint32_t> Places;
+    Places places = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) places |= (Places)place[i] << (4 * i);
     int my_idx = -1, found = 0;
     for (; found < a.k; ++found) {
-        const uint32_t hi = (uint32_t)(c[0] >> 32), lo = (uint32_t)c[0];
-        const uint32_t mh = wave_top(hi);
-        if (mh == 0) break;                           // no expert is left
-        uint64_t top = __ballot(hi == mh);
-        if (__popcll(top) > 1) {                      // equal keys: the lower expert
-            const uint32_t ml = wave_top(hi == mh ? lo : 0u);
-            top = __ballot(hi == mh && lo == ml);
-        }
-        const int src = (int)__builtin_ctzll(top);
-        my_idx = lane == found ? (int)~(uint32_t)__builtin_amdgcn_readlane((int)lo, src) : my_idx;
+        const uint32_t top = wave_top(c[0]);
+        if (top == 0) break;                          // no expert is left
+        const int src = (int)__builtin_ctzll(__ballot(c[0] == top));
+        const int e = src * EPL + (__builtin_amdgcn_readlane((int)(uint32_t)places, src) & 15);
+        my_idx = lane == found ? e : my_idx;
         const bool taken = lane == src;
 #pragma unroll
         for (int i = 0; i + 1 < EPL; ++i) c[i] = taken ? c[i + 1] : c[i];
         c[EPL - 1] = taken ? 0 : c[EPL - 1];
+        places = taken ? places >> 4 : places;
     }
     __builtin_amdgcn_wave_barrier();
     const float mine = my_idx < 0 ? 0.f : lds[wave][my_idx];
