@@ -752,3 +752,38 @@ def test_two_graphs_at_once(coli):
         for _, layer, _, _, out, _ in runs:
             want = layer()
             assert torch.equal(want[0], out[0]) and torch.equal(want[1], out[1])
+
+
+def test_parts_in_graphs(coli):
+    """Products and gradients in parts, in two graphs with workspaces of their own, replayed at the same time."""
+    import torch
+    rng = np.random.default_rng(14)
+    rows, K, n = 150, 5136, 4100
+    assert coli._fp8_matmul_ws(rows, K, 1, n, False, 1) > 0 and coli._fp8_wgrad_ws(3000, 1, 48, 80) > 0
+    runs = []
+    for _ in range(2):
+        keep, table, _, at = _weights(rng, 1, n, K, odd=0)
+        x, g, y = (torch.randn(*s, device="cuda") for s in ((rows, K), (3000, 48), (3000, 80)))
+
+        def step(x=x, g=g, y=y, table=table, at=at):
+            out = coli.fp8_matmul(*coli.quantize_fp8(x), table, n, dtype=torch.bfloat16, **at)
+            return out, coli.fp8_wgrad(*coli.quantize_fp8_columns(g), *coli.quantize_fp8_columns(y), rows=3000)
+
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        runs.append((keep, step, (x, g, y), graph, out, torch.cuda.Stream()))
+    for seed in range(3):
+        for i, (_, _, inputs, _, _, stream) in enumerate(runs):
+            for t in inputs:
+                t.copy_(torch.randn(*t.shape, generator=torch.Generator().manual_seed(2 * seed + i)))
+            stream.wait_stream(torch.cuda.current_stream())
+        for _ in range(3):
+            for _, _, _, graph, _, stream in runs:
+                with torch.cuda.stream(stream):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for _, step, _, _, out, _ in runs:
+            want = step()
+            assert torch.equal(want[0], out[0]) and torch.equal(want[1], out[1])
