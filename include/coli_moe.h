@@ -636,20 +636,20 @@ COLI_API coli_status coli_fp8_matmul_workspace_size(int32_t rows, int32_t K, int
  * matrices gate [inter][K] at q_off, s_off and up [inter][K] at up_q_off, up_s_off. dtype f32, bf16 or
  * f16: d_h [rows][ld], d_hs NULL. COLI_FP8 (inter a multiple of 16): the f32 h is quantised in the
  * same call as coli_quantize_fp8 does, d_h [rows][inter] codes and d_hs [rows][ceil(inter / 128)]
- * scales (ld is ignored). silu as in coli_mxfp4_swiglu. d_ws (nullable, 16-byte aligned): for FP8
- * rows, a workspace of coli_fp8_swiglu_workspace_size's bytes, with which few rows are about twice as
- * fast; smaller ones are not used. It needs no initialisation, and calls that run at the same time
- * (two graphs' too) need one each. */
+ * scales (ld is ignored). silu as in coli_mxfp4_swiglu. d_ws (nullable, 16-byte aligned): a
+ * workspace of coli_fp8_swiglu_workspace_size's bytes, with which few rows into FP8, and some hundreds of rows
+ * into any type, are about twice as fast; smaller ones are not used. It needs no initialisation, and calls
+ * that run at the same time (two graphs' too) need one each. */
 COLI_API coli_status coli_fp8_swiglu(const uint8_t* d_a, const float* d_as, int32_t rows, int32_t K,
                                      const int32_t* d_offsets, int32_t E, const void* const* d_blob_table,
                                      size_t q_off, size_t s_off, size_t up_q_off, size_t up_s_off,
                                      int32_t inter, void* d_h, float* d_hs, int32_t dtype, int64_t ld,
                                      void* d_ws, size_t ws_bytes, void* stream);
 
-/* The workspace that coli_fp8_swiglu makes use of for these sizes (grouped: with d_offsets) and FP8
- * rows, 0 where it needs none. Host-only arithmetic. */
+/* The workspace that coli_fp8_swiglu makes use of for these sizes (grouped: with d_offsets) and output type, 0
+ * where it needs none. Host-only arithmetic. */
 COLI_API coli_status coli_fp8_swiglu_workspace_size(int32_t rows, int32_t K, int32_t E, int32_t inter,
-                                                    int32_t grouped, size_t* bytes);
+                                                    int32_t grouped, int32_t dtype, size_t* bytes);
 
 /* Every expert's matrix gradient: d_dw[e][n][k] = sum over the expert's rows r of g[r][n] x[r][k] (0
  * without rows), for g [rows][N] and x [rows][K] (N, K multiples of 16) as coli_quantize_fp8_columns

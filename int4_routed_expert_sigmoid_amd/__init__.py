@@ -171,7 +171,7 @@ def lib():
             L.coli_fp8_matmul_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, P(sz)]
             L.coli_fp8_swiglu.argtypes = [vp, vp, i32, i32, vp, i32, vp, sz, sz, sz, sz, i32, vp, vp, i32,
                                           i64, vp, sz, vp]
-            L.coli_fp8_swiglu_workspace_size.argtypes = [i32, i32, i32, i32, i32, P(sz)]
+            L.coli_fp8_swiglu_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, P(sz)]
             L.coli_fp8_wgrad.argtypes = [vp, vp, vp, vp, i64, i32, vp, i32, i32, i32, i32, vp, i32, i64, vp, sz, vp]
             L.coli_fp8_wgrad_workspace_size.argtypes = [i32, i32, i32, i32, P(sz)]
             L.coli_debug_fp8_kernel.argtypes = [i32, i32, i32, i32, i32, i32, i32, P(i32)]
@@ -1152,9 +1152,9 @@ def fp8_matmul(a, a_s, table, n, q_off=0, s_off=0, offsets=None, dtype=None, out
 
 
 @functools.lru_cache(4096)
-def _fp8_swiglu_ws(rows, K, E, inter, grouped):
+def _fp8_swiglu_ws(rows, K, E, inter, grouped, code):
     nb = ctypes.c_size_t()
-    _check(lib().coli_fp8_swiglu_workspace_size(rows, K, E, inter, int(grouped), ctypes.byref(nb)))
+    _check(lib().coli_fp8_swiglu_workspace_size(rows, K, E, inter, int(grouped), code, ctypes.byref(nb)))
     return nb.value
 
 
@@ -1172,23 +1172,21 @@ def fp8_swiglu(a, a_s, table, inter, q_off=0, s_off=0, up_q_off=None, up_s_off=N
         up_s_off = s_off + 4 * _blocks(inter) * _blocks(K)
     if up_q_off < 0 or up_s_off < 0:
         raise ValueError("up_q_off and up_s_off must not be negative")
-    ws = None
     if dtype == "fp8" or isinstance(out, (tuple, list)):
         if dtype not in (None, "fp8"):
             raise ValueError(f"out is an FP8 pair, dtype {dtype}")
         q, s = _fp8_out(*(out or (None, None)), rows, inter, a, "fp8_swiglu", stream)
         out, h, hs, code, ld = (q, s), q, s.data_ptr(), FP8, inter
-        nb = _fp8_swiglu_ws(rows, K, E, inter, off is not None)
-        if nb:
-            ws = _new(a, (nb,), torch.uint8, stream)
     else:
         if out is None:
             out = _new(a, (rows, inter), dtype or torch.float32, stream)
         code, ld = _rows(out, "out", rows, inter, dtype)
         h, hs, s = out, None, None
+    nb = _fp8_swiglu_ws(rows, K, E, inter, off is not None, code)
+    ws = _new(a, (nb,), torch.uint8, stream) if nb else None
     _enqueue((a, a_s, table, offsets, h, s, ws), stream, "coli_fp8_swiglu", a.data_ptr(), a_s.data_ptr(), rows, K,
              off, E, table.data_ptr(), q_off, s_off, up_q_off, up_s_off, inter, h.data_ptr(), hs, code, ld,
-             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
+             None if ws is None else ws.data_ptr(), nb)
     return out
 
 

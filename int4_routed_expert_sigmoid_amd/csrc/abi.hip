@@ -795,11 +795,10 @@ static coli_status fp8_product(const char* what, Fp8GemmArgs& a, bool swiglu, in
     if (!a.table || !a.y) return fail(COLI_EINVAL, w + ": NULL pointer");
     if ((st = check_fp8_pair(w, a.a, a.as))) return st;
     if (fp8 && (st = check_fp8_pair(w, a.y, a.ys))) return st;
-    if ((fp8 || !swiglu) && a.ws && !aligned16(a.ws)) return fail(COLI_EINVAL, w + ": the workspace must be 16-byte aligned");
-    if (fp8 && ws_bytes < fp8_swiglu_ws(a)) a.ws = nullptr;
-    if (!swiglu && a.ws) {
-        a.parts = fp8_matmul_parts(a, dtype == COLI_F32);
-        if (a.parts > 1 && ws_bytes < fp8_matmul_ws(a)) a.parts = 0;
+    if (a.ws && !aligned16(a.ws)) return fail(COLI_EINVAL, w + ": the workspace must be 16-byte aligned");
+    if (a.ws) {
+        const size_t need = plan_fp8_ws(a, swiglu, dtype);
+        if (need == 0 || ws_bytes < need) a.ws = nullptr, a.parts = 0;
     }
     return launch_fp8_gemm(a, swiglu, dtype, (hipStream_t)stream);
 }
@@ -816,20 +815,25 @@ coli_status coli_fp8_matmul(const uint8_t* d_a, const float* d_as, int32_t rows,
     COLI_GUARD_END
 }
 
-coli_status coli_fp8_matmul_workspace_size(int32_t rows, int32_t K, int32_t E, int32_t N, int32_t grouped, int32_t dtype,
-                                           size_t* bytes) {
-    COLI_GUARD_BEGIN
-    coli_status st = check_fp8_product("fp8_matmul_workspace_size", rows, K, E, N, grouped != 0);
+static coli_status fp8_workspace_size(const char* what, bool swiglu, int32_t rows, int32_t K, int32_t E, int32_t N, int32_t grouped,
+                                      int32_t dtype, size_t* bytes) {
+    const std::string w(what);
+    coli_status st = check_fp8_product(w, rows, K, E, N, grouped != 0);
     if (st) return st;
-    if (!elem_dtype(dtype)) return fail(COLI_EUNSUPPORTED, "fp8_matmul_workspace_size: output type not supported");
-    if (!bytes) return fail(COLI_EINVAL, "fp8_matmul_workspace_size: NULL pointer");
+    if (!elem_dtype(dtype) && !(swiglu && dtype == COLI_FP8)) return fail(COLI_EUNSUPPORTED, w + ": output type not supported");
+    if (!bytes) return fail(COLI_EINVAL, w + ": NULL pointer");
     static const int32_t some = 0;
     Fp8GemmArgs a = {};
     a.rows = rows; a.K = K; a.E = E; a.N = N;
     a.offsets = grouped ? &some : nullptr;      // asked for, not read
-    a.parts = rows == 0 ? 1 : fp8_matmul_parts(a, dtype == COLI_F32);
-    *bytes = a.parts > 1 ? fp8_matmul_ws(a) : 0;
+    *bytes = plan_fp8_ws(a, swiglu, dtype);
     return COLI_OK;
+}
+
+coli_status coli_fp8_matmul_workspace_size(int32_t rows, int32_t K, int32_t E, int32_t N, int32_t grouped, int32_t dtype,
+                                           size_t* bytes) {
+    COLI_GUARD_BEGIN
+    return fp8_workspace_size("fp8_matmul_workspace_size", false, rows, K, E, N, grouped, dtype, bytes);
     COLI_GUARD_END
 }
 
@@ -845,18 +849,10 @@ coli_status coli_fp8_swiglu(const uint8_t* d_a, const float* d_as, int32_t rows,
     COLI_GUARD_END
 }
 
-coli_status coli_fp8_swiglu_workspace_size(int32_t rows, int32_t K, int32_t E, int32_t inter, int32_t grouped,
+coli_status coli_fp8_swiglu_workspace_size(int32_t rows, int32_t K, int32_t E, int32_t inter, int32_t grouped, int32_t dtype,
                                            size_t* bytes) {
     COLI_GUARD_BEGIN
-    coli_status st = check_fp8_product("fp8_swiglu_workspace_size", rows, K, E, inter, grouped != 0);
-    if (st) return st;
-    if (!bytes) return fail(COLI_EINVAL, "fp8_swiglu_workspace_size: NULL pointer");
-    static const int32_t some = 0;
-    Fp8GemmArgs a = {};
-    a.rows = rows; a.K = K; a.E = E; a.N = inter;
-    a.offsets = grouped ? &some : nullptr;      // asked for, not read
-    *bytes = rows == 0 ? 0 : fp8_swiglu_ws(a);
-    return COLI_OK;
+    return fp8_workspace_size("fp8_swiglu_workspace_size", true, rows, K, E, inter, grouped, dtype, bytes);
     COLI_GUARD_END
 }
 

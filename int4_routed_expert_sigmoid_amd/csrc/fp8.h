@@ -153,10 +153,10 @@ struct Fp8GemmArgs : RowGroups {
     size_t up_q, up_s;           // SwiGLU: those of up
     void* y;                     // [rows][ld] output, or codes [rows][N]
     float* ys;                   // scales [rows][ceil(N / 128)] of an FP8 output
-    void* ws;                    // fp8_swiglu_ws bytes for one, or nullptr
+    void* ws;                    // plan_fp8_ws bytes, or nullptr
     int64_t ld;
     int32_t K, N;                // N: rows of the matrix, of gate and of up alone
-    int32_t parts;               // of the columns (a product with a workspace of parts * rows * N f32 sums), or 0
+    int32_t parts;               // of the columns, whose f32 sums the workspace holds, or 0
 };
 // The kernel that a product runs: its rows, E, offsets, N and K decide, and whether its results have 32 bits (wide).
 enum Fp8Kernel : int32_t {
@@ -165,11 +165,8 @@ enum Fp8Kernel : int32_t {
 };
 Fp8Kernel choose_fp8_kernel(const Fp8GemmArgs& a, bool swiglu, bool wide);
 coli_status launch_fp8_gemm(const Fp8GemmArgs& a, bool swiglu, int32_t dtype, hipStream_t stream);
-// The workspace that a SwiGLU product into FP8 rows makes use of.
-size_t fp8_swiglu_ws(const Fp8GemmArgs& a);
-// Into how many parts of its columns a product is best divided, 1: into none.
-int fp8_matmul_parts(const Fp8GemmArgs& a, bool wide);
-inline size_t fp8_matmul_ws(const Fp8GemmArgs& a) { return (size_t)a.parts * a.rows * a.N * 4; }
+// The bytes of workspace that a product makes use of, with a.parts for it.
+size_t plan_fp8_ws(Fp8GemmArgs& a, bool swiglu, int32_t dtype);
 
 // dw[e][n][k] = sum over the expert's rows (+ dw[e][n][k]); see fp8_wgrad.hip.
 struct Fp8WgradArgs {

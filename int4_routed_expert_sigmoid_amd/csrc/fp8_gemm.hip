@@ -261,7 +261,6 @@ struct PartUnit : LineUnit {
 
 template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int STAGES, bool FAST, bool PARTS>
 __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a, int NT) {
-    static_assert(!PARTS || !SWIGLU, "SwiGLU takes whole sums");
     typedef typename StoredAs<Out>::type Stored;
     typedef LineTile<Out, SWIGLU, MT, NF, WM, WN, STAGES, FAST> T;
     constexpr int U = T::U, kGroup = T::kGroup, kW = SWIGLU ? 2 : 1;
@@ -501,6 +500,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a
                         if (n0 < a.N) store4<Stored>(Place{y, a.ld}, m, n0, a.N, acc[i][f]);
                     }
                 }
+            } else if constexpr (PARTS) {                 // gate's sums and up's, N each a row
+                float* y = (float*)a.y + (int64_t)u.part * a.rows * a.ld;
+#pragma unroll
+                for (int f = 0; f < NF; ++f) {
+                    const int n0 = n_wave + f / 2 * kFrag + 4 * g;
+                    if (there && n0 < a.N) store4<float>(Place{y + (f % 2 ? a.N : 0), a.ld}, m, n0, a.N, acc[i][f]);
+                }
             } else {
 #pragma unroll
                 for (int x = 0; x < NF / 2; ++x) {
@@ -594,7 +600,7 @@ int64_t few_rows_blocks(const Fp8GemmArgs& a) {
 }
 
 coli_status few_rows_fp8(const Fp8GemmArgs& a, hipStream_t stream) {
-    if (a.ws == nullptr || fp8_swiglu_ws(a) == 0) return few_rows<Fp8Out, true, 2, 8, 1, 4>(a, stream);
+    if (a.ws == nullptr) return few_rows<Fp8Out, true, 2, 8, 1, 4>(a, stream);
     Fp8GemmArgs h = a;
     h.y = a.ws;
     h.ld = a.N;
@@ -631,17 +637,61 @@ __global__ __launch_bounds__(256) void part_sum_kernel(const float* __restrict__
     }
 }
 
-// The product in a.parts parts of its columns, f32 sums in the workspace, and their sum.
+// The same for gate's sums and up's (N each a row) and SwiGLU; 32 lanes have a block of 128 h.
 template <typename Out>
+__global__ __launch_bounds__(256) void part_swiglu_kernel(const float* __restrict__ part, Fp8GemmArgs a, uint32_t per_row) {
+    constexpr bool kFp8 = std::is_same<Out, Fp8Out>::value;
+    const uint32_t i = blockIdx.x * 256 + threadIdx.x, m = i / per_row;
+    const int n0 = (int)(i - m * per_row) * 4;
+    if (m >= (uint32_t)a.rows || (a.offsets && ((int)m < a.offsets[0] || (int)m >= a.offsets[a.E]))) return;   // 32 lanes alike
+    const int64_t ld = 2 * (int64_t)a.N, all = a.rows * ld;
+    const float* p = part + m * ld + n0;
+    f32x4 h = {0.f, 0.f, 0.f, 0.f};
+    if (n0 + 4 <= a.N) {
+        float g[4], u[4], x[4];
+        load_f32<float, 4>(p, g);
+        load_f32<float, 4>(p + a.N, u);
+#pragma unroll 4
+        for (int s = 1; s < a.parts; ++s) {
+            load_f32<float, 4>(p + s * all, x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) g[j] += x[j];
+            load_f32<float, 4>(p + s * all + a.N, x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[j] += x[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = silu_mul(g[j], u[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            if (n0 + j >= a.N) break;
+            float g = p[j], u = p[a.N + j];
+            for (int s = 1; s < a.parts; ++s) g += p[s * all + j], u += p[s * all + a.N + j];
+            h[j] = silu_mul(g, u);
+        }
+    }
+    if constexpr (kFp8) {
+        const int code = fp8_scale_code(lanes_umax<32>(top4(h)));
+        if (n0 < a.N) *(uint32_t*)((uint8_t*)a.y + (int64_t)m * a.N + n0) = codes4(h, fp8_scale_inverse(code));
+        if (threadIdx.x % 32 == 0) a.ys[(int64_t)m * fp8_blocks(a.N) + n0 / kFp8Block] = fp8_scale_value(code);
+    } else {
+        if (n0 < a.N) store4<Out>(a, (int)m, n0, a.N, h);
+    }
+}
+
+// The product in a.parts parts of its columns, f32 sums in the workspace, and their sum.
+template <typename Out, bool SWIGLU>
 coli_status product_parts(const Fp8GemmArgs& a, hipStream_t stream) {
     constexpr bool kWide = std::is_same<Out, float>::value;
     Fp8GemmArgs p = a;
     p.y = a.ws;
-    p.ld = a.N;
-    if (coli_status st = lines<std::conditional_t<kWide, float, RawOut>, false, 4, 4, 2, 4, 3, true>(p, stream)) return st;
-    const uint32_t per_row = ((uint32_t)a.N + 3) / 4;
-    launch(part_sum_kernel<Out>, dim3((uint32_t)(((int64_t)a.rows * per_row + 255) / 256)), dim3(256), 0, stream, (const float*)a.ws, a,
-           per_row);
+    p.ld = (SWIGLU ? 2 : 1) * (int64_t)a.N;
+    if (coli_status st = lines<std::conditional_t<kWide, float, RawOut>, SWIGLU, 4, 4, 2, 4, 3, true>(p, stream)) return st;
+    const uint32_t per_row = SWIGLU ? (uint32_t)fp8_blocks(a.N) * 32 : ((uint32_t)a.N + 3) / 4;
+    const dim3 grid((uint32_t)(((int64_t)a.rows * per_row + 255) / 256));
+    if constexpr (SWIGLU) launch(part_swiglu_kernel<Out>, grid, dim3(256), 0, stream, (const float*)a.ws, a, per_row);
+    else launch(part_sum_kernel<Out>, grid, dim3(256), 0, stream, (const float*)a.ws, a, per_row);
     COLI_CHECK_LAUNCH("fp8 product kernel launch");
     return COLI_OK;
 }
@@ -649,9 +699,7 @@ coli_status product_parts(const Fp8GemmArgs& a, hipStream_t stream) {
 template <typename Out, bool SWIGLU>
 coli_status product(const Fp8GemmArgs& a, hipStream_t stream) {
     constexpr bool kFp8 = std::is_same<Out, Fp8Out>::value, kWide = std::is_same<Out, float>::value;
-    if constexpr (!SWIGLU) {
-        if (a.parts > 1) return product_parts<Out>(a, stream);
-    }
+    if (a.parts > 1) return product_parts<Out, SWIGLU>(a, stream);
     switch (choose_fp8_kernel(a, SWIGLU, kWide)) {
         case kFp8FewRows16:                  // (not of SwiGLU's)
             if constexpr (!SWIGLU) return few_rows<Out, SWIGLU, 1, 1, 4, 4>(a, stream);
@@ -712,10 +760,11 @@ Fp8Estimate estimate_fp8(const Fp8GemmArgs& a, bool swiglu, bool wide) {
     // Tiles of 128 rows that leave CUs idle, in parts of the columns: as many blocks less, a second launch (5) and
     // the sums' way through the caches. One matrix of 8192 x 8192 into 16 bits: 64 rows 24 in place of 46, 128 28 /
     // 55, 256 33 / 54; into f32 64 rows 31 / 48, 256 49 / 105, 512 77 / 105; 512 rows of 2048 x 6144 25 / 43.
+    // SwiGLU of two of 2048 x 6144, 128 / 256 / 512 rows 22 / 24 / 30 in place of 35 / 46 / 46.
     least -= 5;                              // (what the second launch and the workspace cost the host)
-    const double u = swiglu ? kCus : units(128), block = wide ? 1.85 : 1.03;
+    const double u = units(128), block = wide ? 1.85 : 1.03, sums = (swiglu ? 2.0 : 1.0) * a.rows * a.N;
     for (int s = 2; s <= 16 && s * u <= kCus && 4 * s <= KB; ++s) {
-        const double us = 4 + std::max(2 + (std::ceil(KB / 4 / s) * 4) * block, bytes / 5.4e6) + 5 + (double)s * a.rows * a.N * 8 / 8e6;
+        const double us = 4 + std::max(2 + (std::ceil(KB / 4 / s) * 4) * block, bytes / 5.4e6) + 5 + s * sums * 8 / 8e6;
         if (us < least) best.parts = s, least = us;
     }
     return best;
@@ -723,12 +772,14 @@ Fp8Estimate estimate_fp8(const Fp8GemmArgs& a, bool swiglu, bool wide) {
 
 Fp8Kernel choose_fp8_kernel(const Fp8GemmArgs& a, bool swiglu, bool wide) { return estimate_fp8(a, swiglu, wide).kernel; }
 
-int fp8_matmul_parts(const Fp8GemmArgs& a, bool wide) { return estimate_fp8(a, false, wide).parts; }
-
-size_t fp8_swiglu_ws(const Fp8GemmArgs& a) {
-    // (One row, inter 2048, K 512 / 1024 / 1536 / 4096: 6.9 / 11.0 / 15.0 / 34.4 us in one launch, 4.7 / 5.1 / 5.8
-    // / 8.1 in two, which cost the host 4.5 more.)
-    const bool two = fp8_blocks(a.K) > 8 && few_rows_blocks(a) < kCus && choose_fp8_kernel(a, true, false) == kFp8FewRows32;
+size_t plan_fp8_ws(Fp8GemmArgs& a, bool swiglu, int32_t dtype) {
+    if (a.rows == 0) return 0;
+    const Fp8Estimate e = estimate_fp8(a, swiglu, dtype == COLI_F32);
+    a.parts = e.parts;
+    if (e.parts > 1) return (size_t)e.parts * a.rows * a.N * (swiglu ? 8 : 4);
+    // SwiGLU of few rows into FP8 in two launches. (One row, inter 2048, K 512 / 1024 / 1536 / 4096: 6.9 / 11.0 / 15.0
+    // / 34.4 us in one launch, 4.7 / 5.1 / 5.8 / 8.1 in two, which cost the host 4.5 more.)
+    const bool two = swiglu && dtype == COLI_FP8 && e.kernel == kFp8FewRows32 && fp8_blocks(a.K) > 8 && few_rows_blocks(a) < kCus;
     return two ? (size_t)a.rows * a.N * 4 : 0;
 }
 

@@ -127,11 +127,14 @@ def test_sizes(L):
             assert coli.fp8_column_blocks(coli._rows_of_blocks(n, E), E) <= n and coli._rows_of_blocks(n, E) >= rows
     nb = ctypes.c_size_t()
     size = coli.lib().coli_fp8_swiglu_workspace_size
-    for rows, K, E, inter, grouped, want in ((8, 6144, 256, 2048, 1, 8 * 2048 * 4), (1, 2064, 1, 144, 0, 144 * 4), (1, 1024, 1, 144, 0, 0), (64, 6144, 40, 2048, 1, 0),
+    for rows, K, E, inter, grouped, want in (  # into FP8
+            (8, 6144, 256, 2048, 1, 8 * 2048 * 4), (1, 2064, 1, 144, 0, 144 * 4), (1, 1024, 1, 144, 0, 0), (64, 6144, 40, 2048, 1, 0),
                                              (4096, 6144, 256, 2048, 1, 0), (0, 64, 4, 64, 1, 0)):
-        assert size(rows, K, E, inter, grouped, ctypes.byref(nb)) == OK and nb.value == want
-    assert size(4, 40, 1, 16, 0, ctypes.byref(nb)) == EINVAL and size(4, 48, 2, 16, 0, ctypes.byref(nb)) == EINVAL
-    assert size(4, 48, 1, 16, 0, None) == EINVAL
+        assert size(rows, K, E, inter, grouped, coli.FP8, ctypes.byref(nb)) == OK and nb.value == want
+    assert size(8, 6144, 256, 2048, 1, 1, ctypes.byref(nb)) == OK and nb.value == 0
+    assert size(256, 6144, 1, 2048, 0, 1, ctypes.byref(nb)) == OK and nb.value == 6 * 256 * 2048 * 2 * 4
+    assert size(4, 40, 1, 16, 0, 0, ctypes.byref(nb)) == EINVAL and size(4, 48, 2, 16, 0, 0, ctypes.byref(nb)) == EINVAL
+    assert size(4, 48, 1, 16, 0, 0, None) == EINVAL and size(4, 48, 1, 16, 0, 3, ctypes.byref(nb)) == EUNSUP
     size = coli.lib().coli_fp8_matmul_workspace_size
     for rows, K, E, n, dtype, parts in ((8, 8192, 1, 8192, 1, 0), (64, 8192, 1, 8192, 1, 8), (128, 8192, 1, 8192, 1, 6), (8191, 8192, 1, 8192, 0, 0),
                                         (512, 8192, 1, 8192, 0, 2), (16384, 2048, 256, 6144, 1, 0), (0, 64, 1, 64, 0, 0)):

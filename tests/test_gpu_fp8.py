@@ -345,15 +345,21 @@ def _scale_of(top):
     return torch.from_numpy(ref.scale_value(ref.scale_code(top.cpu().numpy()))).cuda()
 
 
+# SwiGLU's columns summed in parts, gate's and up's apart
+PARTS = [("", "", 150, 5136, 2051, 0, 0), ("", "", [130, 0, 123], 8192, 528, 3, 4), ("", "", 64, 8192, 8192, 0, 0)]
+
+
 @pytest.mark.parametrize("odd", (0, 4))
 @pytest.mark.parametrize("dtype", DTYPES + ("fp8",))
-@pytest.mark.parametrize("case", CASES, ids=_case_id)
+@pytest.mark.parametrize("case", CASES + PARTS, ids=_case_id)
 def test_swiglu(coli, case, dtype, odd):
     import torch
     _, _, counts, K, n, before, behind = case
     n = -(-n // 16) * 16 if dtype == "fp8" else n
     offsets, off, rows = _groups(counts, before, behind)
     E, exact = len(off) - 1, dtype == "float32"
+    code = {"float32": 0, "bfloat16": 1, "float16": 2, "fp8": coli.FP8}[dtype]
+    assert case not in PARTS or (exact and E > 1) or coli._fp8_swiglu_ws(rows, K, E, n, offsets is not None, code) >= 2 * 8 * rows * n
     rng = np.random.default_rng(K + n + 1)
     _keep, table, matrix, at = _weights(rng, E, n, K, parts=2, odd=odd)
     a, a_s, va = _rows(rng, rows, K, 0.08 / np.sqrt(K))
