@@ -30,6 +30,15 @@ namespace {
 struct Fp8Out {};
 struct RawOut {};
 
+// FP8 rows from exact products (fp8.h). A sum decides a code, and one that falls to the other side of a rounding border
+// moves its value by up to an eighth: of the FP8 instruction's sums one in about 4000 does. Over a million values that
+// is 1e-3 of a layer's output (509 tokens of 256 experts: 2.6e-3 off the 64-bit form, with exact sums 2.4e-3, bf16's own
+// rounding), but of a few thousand a single large one can show (26 tokens, inter 288: 6.3e-3). Below kFewValues, and
+// wherever few_rows runs (whose time is the matrices' bytes), FP8 rows therefore take exact products; above, the
+// tiles' blocks would take 1.85 us in place of 1.03.
+struct ExactFp8Out {};
+constexpr int64_t kFewValues = 1 << 20;
+
 template <typename Out>
 struct StoredAs {
     typedef Out type;
@@ -71,6 +80,7 @@ __device__ __forceinline__ uint32_t top4(const f32x4& h) {
 template <typename Out, bool SWIGLU, int NF, int WN, int KS, int CB, bool TAIL>
 __global__ __launch_bounds__(64 * WN * KS) void fp8_few_rows_kernel(Fp8GemmArgs a, int NT) {
     constexpr bool kFp8 = std::is_same<Out, Fp8Out>::value;
+    constexpr bool EXACT = kFp8 || std::is_same<Out, RawOut>::value || std::is_same<Out, float>::value;
     constexpr int kWaves = WN * KS, kCols = (SWIGLU ? NF / 2 : NF) * WN * kFrag;   // outputs of a tile
     static_assert(!kFp8 || kCols == kFp8Block, "a tile holds one block of h");
     __shared__ f32x4 part[KS][WN * NF][64];
@@ -149,7 +159,7 @@ __global__ __launch_bounds__(64 * WN * KS) void fp8_few_rows_kernel(Fp8GemmArgs 
             }
             f32x4 p[NF];
 #pragma unroll
-            for (int f = 0; f < NF; ++f) p[f] = block_sum<std::is_same<Out, float>::value>(w[s][f], x);
+            for (int f = 0; f < NF; ++f) p[f] = block_sum<EXACT>(w[s][f], x);
 #pragma unroll
             for (int f = 0; f < NF; ++f) add_scaled(acc[f], p[f], as_c[s] * ws_c[s][f]);
             hold(acc);
@@ -226,7 +236,7 @@ __global__ __launch_bounds__(64 * WN * KS) void fp8_few_rows_kernel(Fp8GemmArgs 
 // PARTS: each unit once for every part of the columns, into an output of its own (product_parts).
 template <typename Out, bool SWIGLU, int MT, int NF, int WM, int WN, int STAGES, bool FAST>
 struct LineTile {
-    static constexpr bool kFp8 = std::is_same<Out, Fp8Out>::value;
+    static constexpr bool kFp8 = std::is_same<Out, Fp8Out>::value || std::is_same<Out, ExactFp8Out>::value;
     static constexpr int BM = WM * MT * kFrag, BN = WN * NF * kFrag, kWaves = WM * WN, kThreads = 64 * kWaves;
     static constexpr int U = kBlockUnits;
     static constexpr int kCols = SWIGLU ? BN / 2 : BN;        // outputs of a tile
@@ -264,7 +274,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_line_kernel(Fp8GemmArgs a
     typedef typename StoredAs<Out>::type Stored;
     typedef LineTile<Out, SWIGLU, MT, NF, WM, WN, STAGES, FAST> T;
     constexpr int U = T::U, kGroup = T::kGroup, kW = SWIGLU ? 2 : 1;
-    constexpr bool EXACT = std::is_same<Out, float>::value;
+    constexpr bool EXACT = std::is_same<Out, float>::value || std::is_same<Out, ExactFp8Out>::value;
     __shared__ typename T::Lds lds;
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wn = wave % WN, wm = wave / WN;
@@ -680,14 +690,17 @@ __global__ __launch_bounds__(256) void part_swiglu_kernel(const float* __restric
     }
 }
 
+bool exact_products(const Fp8GemmArgs& a, bool f32, bool fp8) { return f32 || (fp8 && a.rows * (int64_t)a.N < kFewValues); }
+
 // The product in a.parts parts of its columns, f32 sums in the workspace, and their sum.
 template <typename Out, bool SWIGLU>
 coli_status product_parts(const Fp8GemmArgs& a, hipStream_t stream) {
-    constexpr bool kWide = std::is_same<Out, float>::value;
     Fp8GemmArgs p = a;
     p.y = a.ws;
     p.ld = (SWIGLU ? 2 : 1) * (int64_t)a.N;
-    if (coli_status st = lines<std::conditional_t<kWide, float, RawOut>, SWIGLU, 4, 4, 2, 4, 3, true>(p, stream)) return st;
+    const bool exact = exact_products(a, std::is_same<Out, float>::value, std::is_same<Out, Fp8Out>::value);
+    if (coli_status st = exact ? lines<float, SWIGLU, 4, 4, 2, 4, 3, true>(p, stream) : lines<RawOut, SWIGLU, 4, 4, 2, 4, 3, true>(p, stream))
+        return st;
     const uint32_t per_row = SWIGLU ? (uint32_t)fp8_blocks(a.N) * 32 : ((uint32_t)a.N + 3) / 4;
     const dim3 grid((uint32_t)(((int64_t)a.rows * per_row + 255) / 256));
     if constexpr (SWIGLU) launch(part_swiglu_kernel<Out>, grid, dim3(256), 0, stream, (const float*)a.ws, a, per_row);
@@ -700,7 +713,8 @@ template <typename Out, bool SWIGLU>
 coli_status product(const Fp8GemmArgs& a, hipStream_t stream) {
     constexpr bool kFp8 = std::is_same<Out, Fp8Out>::value, kWide = std::is_same<Out, float>::value;
     if (a.parts > 1) return product_parts<Out, SWIGLU>(a, stream);
-    switch (choose_fp8_kernel(a, SWIGLU, kWide)) {
+    const bool exact = exact_products(a, kWide, kFp8);
+    switch (choose_fp8_kernel(a, SWIGLU, exact)) {
         case kFp8FewRows16:                  // (not of SwiGLU's)
             if constexpr (!SWIGLU) return few_rows<Out, SWIGLU, 1, 1, 4, 4>(a, stream);
         case kFp8FewRows32:
@@ -709,7 +723,11 @@ coli_status product(const Fp8GemmArgs& a, hipStream_t stream) {
         case kFp8Lines256:
             // (32-bit results have no registers for it, as their operands are twice as wide, and are not sent here)
             if constexpr (!kWide) return lines<Out, SWIGLU, 8, 4, 2, 4, 2>(a, stream);
-        default: return lines<Out, SWIGLU, 4, 4, 2, 4, 3>(a, stream);
+        default:
+            if constexpr (kFp8) {
+                if (exact) return lines<ExactFp8Out, SWIGLU, 4, 4, 2, 4, 3>(a, stream);
+            }
+            return lines<Out, SWIGLU, 4, 4, 2, 4, 3>(a, stream);
     }
 }
 
@@ -774,7 +792,7 @@ Fp8Kernel choose_fp8_kernel(const Fp8GemmArgs& a, bool swiglu, bool wide) { retu
 
 size_t plan_fp8_ws(Fp8GemmArgs& a, bool swiglu, int32_t dtype) {
     if (a.rows == 0) return 0;
-    const Fp8Estimate e = estimate_fp8(a, swiglu, dtype == COLI_F32);
+    const Fp8Estimate e = estimate_fp8(a, swiglu, exact_products(a, dtype == COLI_F32, dtype == COLI_FP8));
     a.parts = e.parts;
     if (e.parts > 1) return (size_t)e.parts * a.rows * a.N * (swiglu ? 8 : 4);
     // SwiGLU of few rows into FP8 in two launches. (One row, inter 2048, K 512 / 1024 / 1536 / 4096: 6.9 / 11.0 / 15.0
