@@ -30,12 +30,12 @@ namespace {
 struct Fp8Out {};
 struct RawOut {};
 
-// FP8 rows from exact products (fp8.h). A sum decides a code, and one that falls to the other side of a rounding border
-// moves its value by up to an eighth: of the FP8 instruction's sums one in about 4000 does. Over a million values that
-// is 1e-3 of a layer's output (509 tokens of 256 experts: 2.6e-3 off the 64-bit form, with exact sums 2.4e-3, bf16's own
-// rounding), but of a few thousand a single large one can show (26 tokens, inter 288: 6.3e-3). Below kFewValues, and
-// wherever few_rows runs (whose time is the matrices' bytes), FP8 rows therefore take exact products; above, the
-// tiles' blocks would take 1.85 us in place of 1.03.
+// FP8 rows from exact products (fp8.h). A sum decides a code, and one that falls to the other side of a rounding
+// border moves its value by up to an eighth: of the FP8 instruction's sums one in about 4000 does. Over a million
+// values that is 1e-3 of a layer's output (509 tokens of 256 experts: 2.6e-3 off the 64-bit form, with exact sums
+// 2.4e-3, bf16's own rounding), but of a few thousand a single large one can show (26 tokens, inter 288: 6.3e-3).
+// Below kFewValues, and wherever few_rows runs (whose time is the matrices' bytes), FP8 rows therefore take exact
+// products; above, the tiles' blocks would take 1.85 us in place of 1.03.
 struct ExactFp8Out {};
 constexpr int64_t kFewValues = 1 << 20;
 
@@ -795,8 +795,8 @@ size_t plan_fp8_ws(Fp8GemmArgs& a, bool swiglu, int32_t dtype) {
     const Fp8Estimate e = estimate_fp8(a, swiglu, exact_products(a, dtype == COLI_F32, dtype == COLI_FP8));
     a.parts = e.parts;
     if (e.parts > 1) return (size_t)e.parts * a.rows * a.N * (swiglu ? 8 : 4);
-    // SwiGLU of few rows into FP8 in two launches. (One row, inter 2048, K 512 / 1024 / 1536 / 4096: 6.9 / 11.0 / 15.0
-    // / 34.4 us in one launch, 4.7 / 5.1 / 5.8 / 8.1 in two, which cost the host 4.5 more.)
+    // SwiGLU of few rows into FP8 in two launches. (One row, inter 2048, K 512 / 1024 / 1536 / 4096: 6.9 / 11.0 /
+    // 15.0 / 34.4 us in one launch, 4.7 / 5.1 / 5.8 / 8.1 in two, which cost the host 4.5 more.)
     const bool two = swiglu && dtype == COLI_FP8 && e.kernel == kFp8FewRows32 && fp8_blocks(a.K) > 8 && few_rows_blocks(a) < kCus;
     return two ? (size_t)a.rows * a.N * 4 : 0;
 }
