@@ -36,6 +36,10 @@ __device__ __forceinline__ float wave_fsum(float v) {
     return plain_stage<1>(plain_stage<2>(plain_stage<4>(plain_stage<8>(plain_stage<16>(plain_stage<32>(v))))));
 }
 
+// What a softmax subtracts from its logits: their largest, 0 where all are -inf (which has no difference to itself). A
+// finite one is taken as it is, so that logits which all have the type's lowest value are equal ones.
+__device__ __forceinline__ float softmax_top(float top) { return top == -__builtin_inff() ? 0.f : top; }
+
 // The logits of a lane's experts, -inf behind the last.
 template <typename T, int EPL>
 __device__ __forceinline__ void load_logits(const T* row, int E, int e0, float (&l)[EPL]) {
@@ -101,7 +105,7 @@ __global__ __launch_bounds__(kThreads) void route_groups_kernel(RouteArgs a) {
         float top = l[0];
 #pragma unroll
         for (int i = 1; i < EPL; ++i) top = fmaxf(top, l[i]);
-        const double m = fmaxf(wave_fmax(top), -3.4e38f);
+        const double m = softmax_top(wave_fmax(top));
         double x[EPL], sum = 0;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
@@ -276,7 +280,7 @@ __global__ __launch_bounds__(kThreads) void route_groups_bwd_kernel(RouteBwdArgs
         float top = l[0];
 #pragma unroll
         for (int i = 1; i < EPL; ++i) top = fmaxf(top, l[i]);
-        const float m = fmaxf(wave_fmax(top), -3.4e38f);
+        const float m = softmax_top(wave_fmax(top));
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {

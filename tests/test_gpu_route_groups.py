@@ -127,6 +127,41 @@ def test_gradient_matches_formula(coli, T, E, k, groups, kept, top, kind):
             assert (np.abs(got - want) <= bound).all()
 
 
+@pytest.mark.parametrize("kind", ("sigmoid", "softmax"))
+@pytest.mark.parametrize("E", (5, 96, 256, 320, 1024))
+def test_masks_of_the_lowest_value(coli, E, kind):
+    """Rows masked by their type's lowest finite value: all of them (softmax: equal scores), all but one place, together with
+    -infinity, and values next to the lowest. Tolerances as for other rows."""
+    import torch
+    k = 4
+    for dtype in DTYPES:
+        low = torch.finfo(_t(dtype)).min
+        l = _inputs(8, E, dtype, E, False)[0]
+        l[0] = low
+        l[1] = low
+        l[1, E // 2] = 0.5
+        l[2] = low
+        l[2, ::2] = -float("inf")
+        l[3] = low * 0.9995
+        l[4, : E - 1] = low
+        l[5, 1:] = low
+        l[6] = -float("inf")
+        gw, gs = torch.randn(8, k, generator=torch.Generator().manual_seed(E)), torch.randn(8, E, generator=torch.Generator().manual_seed(E + 1))
+        for norm in (True, False):
+            want_idx, want_w, s = ref.route(l.double().numpy(), None, k, kind, 1, 1, 1, norm, 2.5)
+            idx, w, scores = coli.route_groups(l.cuda(), None, k, score=kind, norm=norm, scale=2.5, with_scores=True)
+            assert np.array_equal(idx.cpu().numpy(), want_idx)
+            assert np.abs(scores.cpu().numpy().astype(np.float64) - s).max() <= 2.0 ** -24
+            assert (np.abs(w.cpu().numpy() - want_w) <= 3 * 2.0 ** -24 * np.abs(want_w)).all()
+            if kind == "softmax":
+                assert abs(scores[0, 0].item() * E - 1) < 1e-6
+            want = ref.route_grad(gw.numpy(), l.double().numpy(), want_idx, kind, norm, 2.5, gs.numpy())
+            got = coli.route_groups_bwd(gw.cuda(), l.cuda(), idx, score=kind, norm=norm, scale=2.5, scores_grad=gs.cuda(),
+                                        dtype=torch.float32).double().cpu().numpy()
+            most = 2.5 * np.abs(gw.numpy()).max(1, keepdims=True) + np.abs(gs.numpy()).max(1, keepdims=True)
+            assert (np.abs(got - want) <= 2.0 ** -18 * most + 2.0 ** -24 * np.abs(want)).all()
+
+
 def test_gradient_of_small_scores_and_repeated_experts(coli):
     """Scores whose sum is near the smallest numbers keep the gradient of their shares; an expert named twice has both slots'."""
     import torch
