@@ -180,7 +180,8 @@ COLI_API coli_status coli_moe_route_topp(const float* d_logits, const float* d_b
  * key = score + bias (f32; d_bias [E] nullable); an expert whose logit or bias is -infinity
  * is never chosen. Group j holds experts j * E / n_groups on (n_groups <= 64, a divisor of E);
  * its value is its largest key (group_top 1) or the f32 sum of its two largest (group_top 2;
- * of one, where it has one); the groups_kept groups of the largest values stay, and of
+ * of one, where it has one; no finite keys' sum is below the lowest f32 value, so that a group
+ * with experts comes before one without); the groups_kept groups of the largest values stay, and of
  * their experts the k (<= 32, and at most as many as those groups have) of the largest keys,
  * in descending order, go to d_idx [T][k]. Equal values and keys go to the lower index.
  * Slots for which no expert is left get d_idx -1 and d_w 0 (a row of -infinity has only

@@ -79,6 +79,13 @@ __device__ __forceinline__ void merge2(float& a0, float& a1, float b0, float b1)
     a0 = hi;
 }
 
+// A group's value from its two largest keys (-inf: it has none, or only one). A sum that passes the lowest f32 value
+// (biases that switch whole groups off do) stays there, so that the group comes before those without any expert.
+__device__ __forceinline__ float group_value(float first, float second, bool nan, int top) {
+    if (nan) return __uint_as_float(0x7fc00000u);
+    return top == 2 && second != -__builtin_inff() ? fmaxf(first + second, -__FLT_MAX__) : first;
+}
+
 // How many of the groups, whose codes the lanes 0, step, 2 step, .. hold, come before group `mine`.
 __device__ __forceinline__ int group_rank(uint32_t code, uint32_t mine, int groups, uint32_t step) {
     const uint64_t self = (uint64_t)code << 32 | ~mine;
@@ -163,7 +170,7 @@ __global__ __launch_bounds__(kThreads) void route_groups_kernel(RouteArgs a) {
             join(std::integral_constant<int, 8>{});
             join(std::integral_constant<int, 16>{});
             join(std::integral_constant<int, 32>{});
-            const float value = nan ? __uint_as_float(0x7fc00000u) : a.group_top == 2 && second != none ? first + second : first;
+            const float value = group_value(first, second, nan != 0, a.group_top);
             const uint32_t code = value != none ? key_code(value) : 0;
             const int rank = group_rank(code, lane / wide, a.groups, wide);
 #pragma unroll
@@ -183,7 +190,7 @@ __global__ __launch_bounds__(kThreads) void route_groups_kernel(RouteArgs a) {
                     first = fmaxf(first, v);
                 }
             }
-            const float value = nan ? __uint_as_float(0x7fc00000u) : a.group_top == 2 && second != none ? first + second : first;
+            const float value = group_value(first, second, nan, a.group_top);
             const uint32_t code = lane < a.groups && value != none ? key_code(value) : 0;
             const int rank = group_rank(code, lane, a.groups, 1);
             const uint64_t open = __ballot(code != 0 && rank < a.kept);

@@ -162,6 +162,33 @@ def test_masks_of_the_lowest_value(coli, E, kind):
             assert (np.abs(got - want) <= 2.0 ** -18 * most + 2.0 ** -24 * np.abs(want)).all()
 
 
+# (64 of 8, 320 of 5, 512 of 16: a group is a power of two of whole lanes; the others': not)
+@pytest.mark.parametrize("top", (1, 2))
+@pytest.mark.parametrize("E,groups", ((64, 8), (320, 5), (512, 16), (60, 6), (72, 8), (336, 7)))
+def test_groups_whose_keys_add_up_past_the_lowest(coli, E, groups, top):
+    """A bias of f32's lowest value switches whole groups off, whose two keys together lie below it: they come after the
+    others and before groups without any expert, and fill the slots that the others leave."""
+    import torch
+    size = E // groups
+    k = min(32, size + 4)
+    l = _inputs(9, E, "float32", E, False)[0]
+    b = torch.full((E,), torch.finfo(torch.float32).min)
+    b[:size] = -float("inf")                                      # no expert
+    live = [size + 1, size + 3]
+    b[size:2 * size] = -float("inf")
+    b[live] = 0.0
+    s = ref.scores(l.double().numpy(), "sigmoid").astype(np.float32)
+    for norm in (True, False):
+        idx, w = coli.route_groups(l.cuda(), b.cuda(), k, groups=groups, groups_kept=3, group_top=top, norm=norm)
+        for t in range(9):
+            first = sorted(live, key=lambda e: (-s[t, e], e))
+            want = first + list(range(2 * size, 2 * size + k - 2))   # equal keys: the lower expert, and the lower group
+            assert idx[t].tolist() == want
+            got = s[t, want].astype(np.float64)
+            got = got / got.sum() if norm else got
+            assert (np.abs(w[t].cpu().numpy() - got) <= 3 * 2.0 ** -24 * got).all()
+
+
 def test_gradient_of_small_scores_and_repeated_experts(coli):
     """Scores whose sum is near the smallest numbers keep the gradient of their shares; an expert named twice has both slots'."""
     import torch
