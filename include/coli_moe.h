@@ -186,9 +186,9 @@ COLI_API coli_status coli_moe_route_topp(const float* d_logits, const float* d_b
  * in descending order, go to d_idx [T][k]. Equal values and keys go to the lower index.
  * Slots for which no expert is left get d_idx -1 and d_w 0 (a row of -infinity has only
  * those). d_w [T][k] = scale * score / (sum of the chosen scores, in slot order, double; all
- * 0: equal shares), or scale * score with norm 0; rounded to f32. A NaN key counts as the
- * largest, so that the weights of its token are NaN. scale must be finite. Uses no
- * workspace, and may be captured. */
+ * 0: equal shares), or scale * score with norm 0; rounded to f32. A NaN key (of a NaN logit or
+ * bias) counts as the largest and makes its slot's weight NaN, with norm all of the token's.
+ * scale must be finite. Uses no workspace, and may be captured. */
 #define COLI_SCORE_SIGMOID 0
 #define COLI_SCORE_SOFTMAX 1
 COLI_API coli_status coli_moe_route_groups(const void* d_logits, int32_t dtype, const float* d_bias,

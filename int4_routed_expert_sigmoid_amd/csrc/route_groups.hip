@@ -139,7 +139,10 @@ __global__ __launch_bounds__(kThreads) void route_groups_kernel(RouteArgs a) {
     }
     const float none = -__builtin_inff();
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) key[i] = l[i] == none || b[i] == none || e0 + i >= E ? none : s[i] + b[i];
+    for (int i = 0; i < EPL; ++i) {
+        key[i] = l[i] == none || b[i] == none || e0 + i >= E ? none : s[i] + b[i];
+        s[i] = key[i] != key[i] ? key[i] : s[i];      // a NaN bias shows in the weight, as a NaN score does
+    }
 
     // the groups whose experts can be chosen
     uint32_t c[EPL];

@@ -189,6 +189,25 @@ def test_groups_whose_keys_add_up_past_the_lowest(coli, E, groups, top):
             assert (np.abs(w[t].cpu().numpy() - got) <= 3 * 2.0 ** -24 * got).all()
 
 
+@pytest.mark.parametrize("kind", ("sigmoid", "softmax"))
+@pytest.mark.parametrize("E,groups", ((8, 1), (64, 8), (72, 8), (320, 5)))
+def test_a_bias_that_is_not_a_number(coli, E, groups, kind):
+    """It comes first and shows in its slot's weight, with norm in all of the token's; a -infinity logit still takes its expert out."""
+    import torch
+    l = _inputs(6, E, "float32", E, False)[0]
+    l[5, 3] = -float("inf")
+    b = torch.zeros(E)
+    b[3] = float("nan")
+    plain = coli.route_groups(l.cuda(), None, 3, score=kind, with_scores=True)[2]
+    for norm in (True, False):
+        idx, w, scores = coli.route_groups(l.cuda(), b.cuda(), 3, score=kind, groups=groups, groups_kept=groups // 2 or 1, norm=norm,
+                                           with_scores=True)
+        assert idx[:5, 0].tolist() == [3] * 5 and bool(w[:5, 0].isnan().all())
+        assert bool(w[:5, 1:].isnan().all()) if norm else bool(torch.isfinite(w[:5, 1:]).all())
+        assert 3 not in idx[5].tolist() and bool(torch.isfinite(w[5]).all())
+        assert torch.equal(scores, plain)
+
+
 def test_gradient_of_small_scores_and_repeated_experts(coli):
     """Scores whose sum is near the smallest numbers keep the gradient of their shares; an expert named twice has both slots'."""
     import torch
