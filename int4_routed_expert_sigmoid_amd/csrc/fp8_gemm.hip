@@ -144,9 +144,10 @@ __global__ __launch_bounds__(64 * WN * KS) void fp8_few_rows_kernel(Fp8GemmArgs 
         float as_c[CB], ws_c[CB][NF];
 #pragma unroll
         for (int s = 0; s < CB; ++s) {
-            as_c[s] = TAIL && c * CB + s >= KB ? 0.f : as[s];
+            const bool behind = TAIL && c * CB + s >= KB;     // (0 on both sides: the other may be infinite)
+            as_c[s] = behind ? 0.f : as[s];
 #pragma unroll
-            for (int f = 0; f < NF; ++f) ws_c[s][f] = ws[s][f];
+            for (int f = 0; f < NF; ++f) ws_c[s][f] = behind ? 0.f : ws[s][f];
         }
         if (more) load_scales(c + KS);
 #pragma unroll

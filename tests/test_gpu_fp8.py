@@ -430,6 +430,41 @@ def test_not_finite(coli):
             assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,K,n", [(40, 144, 33), (40, 512, 33), (5, 640, 4100), (40, 656, 161), (9000, 16, 1300), (700, 640, 1500),
+                                      (4500, 1152, 2060), (64, 8208, 8192)])
+def test_infinite_scales(coli, rows, K, n, dtype):
+    """An infinite scale of the last block, of a row and of the matrix, gives infinities of the products' signs (codes above 0 on
+    both sides, one row's below) and nothing else, SwiGLU's too."""
+    import torch
+    rng = np.random.default_rng(rows + K)
+    q, blocks = _codes(rng, n, K) & 0x7F, -(-K // 128)
+    s = _scales(rng, 2e-3, -(-n // 128), blocks)
+    s[-1, -1] = float("inf")                                      # of the last matrix rows
+    at = (n - 1) // 128 * 128
+    size = -(-(n * K + 4 * s.numel()) // 16) * 16
+    blob = torch.zeros(2 * size, dtype=torch.uint8, device="cuda")
+    blob[:n * K] = q.flatten()
+    blob[n * K:n * K + 4 * s.numel()] = s.flatten().view(torch.uint8)
+    blob[size:size + n * K] = q.flatten()                          # up: the same with finite scales
+    blob[size + n * K:size + n * K + 4 * s.numel()] = s.nan_to_num(posinf=1e-3).flatten().view(torch.uint8)
+    table = torch.tensor([blob.data_ptr()], device="cuda")
+    a, a_s, _ = _rows(rng, rows, K, 1e-4)
+    a &= 0x7F
+    want = torch.zeros(rows, n, dtype=torch.bool, device="cuda")
+    want[:, at:] = True
+    y = coli.fp8_matmul(a, a_s, table, n, s_off=n * K, dtype=_t(dtype))
+    assert not bool(y.isnan().any()) and torch.equal(y.isinf(), want) and bool((y > 0).all())
+    h = coli.fp8_swiglu(a, a_s, table, n, s_off=n * K, up_q_off=size, up_s_off=size + n * K, dtype=_t(dtype))
+    assert not bool(h.isnan().any()) and torch.equal(h.isinf(), want)
+    a_s[1, -1] = float("inf")
+    a[1] |= 0x80
+    want[1] = True
+    y = coli.fp8_matmul(a, a_s, table, n, s_off=n * K, dtype=_t(dtype))
+    assert not bool(y.isnan().any()) and torch.equal(y.isinf(), want)
+    assert bool((y[1] < 0).all()) and bool((y[torch.arange(rows, device="cuda") != 1] > 0).all())
+
+
 @pytest.mark.parametrize("odd", (0, 4))
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("counts,K,n,before,behind", [(150, 5136, 4100, 0, 0), ([130, 0, 123], 8192, 1030, 3, 4),
