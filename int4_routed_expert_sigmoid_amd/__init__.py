@@ -672,9 +672,9 @@ def _groups(table, offsets, rows, K, n, q_off, s_off):
         raise ValueError("offsets must hold one more value than the table")
     # what the C types would cut to other values
     E = table.numel()
-    if max(rows, K, E) >= 2 ** 31 or not 0 < n < 2 ** 31 or q_off < 0 or s_off < 0:
+    if max(rows, K, E) >= 2 ** 31 or not 0 < n < 2 ** 31 or (q_off | s_off) >> 63:
         raise ValueError(f"rows {rows}, columns {K}, matrices {E} and matrix rows {n} must be below 2^31, "
-                         f"q_off {q_off} and s_off {s_off} not negative")
+                         f"q_off {q_off} and s_off {s_off} below 2^63 and not negative")
     return E, None if offsets is None else offsets.data_ptr()
 
 
@@ -879,6 +879,13 @@ def _token_rows(t, name, dtype=None, shape=None):
     return None if dtype is not None else _dtype_code(t.dtype)
 
 
+def _small(*numbers):
+    """Refuses what a C int would cut to another value."""
+    for n in numbers:
+        if n >> 31 not in (0, -1):
+            raise ValueError(f"{n} is no number of 32 bits")
+
+
 def route_groups(logits, bias, k, score="sigmoid", groups=1, groups_kept=None, group_top=2, norm=True,
                  scale=1.0, with_scores=False, idx=None, w=None, scores=None, stream=None):
     """The k experts of every token and their weights, (idx int32 [T][k], w float32 [T][k]), for logits
@@ -888,6 +895,10 @@ def route_groups(logits, bias, k, score="sigmoid", groups=1, groups_kept=None, g
     Slots for which no expert is left have idx -1. with_scores (or scores given): also the scores,
     float32 [T][E]."""
     import torch
+    if groups_kept is None:
+        groups_kept = groups
+    if (k | groups | groups_kept | group_top) >> 31:
+        _small(k, groups, groups_kept, group_top)
     code = _token_rows(logits, "logits")
     T, E = logits.shape
     if bias is not None:
@@ -907,9 +918,8 @@ def route_groups(logits, bias, k, score="sigmoid", groups=1, groups_kept=None, g
     elif with_scores:
         scores = _new(logits, (T, E), torch.float32, stream)
     _enqueue((logits, bias, idx, w, scores), stream, "coli_moe_route_groups", logits.data_ptr(), code,
-             None if bias is None else bias.data_ptr(), T, E, k, _score(score), groups,
-             groups if groups_kept is None else groups_kept, group_top, int(norm), scale, idx.data_ptr(),
-             w.data_ptr(), None if scores is None else scores.data_ptr())
+             None if bias is None else bias.data_ptr(), T, E, k, _score(score), groups, groups_kept, group_top,
+             1 if norm else 0, scale, idx.data_ptr(), w.data_ptr(), None if scores is None else scores.data_ptr())
     return (idx, w) if scores is None else (idx, w, scores)
 
 
@@ -934,7 +944,7 @@ def route_groups_bwd(w_grad, logits, idx, score="sigmoid", norm=True, scale=1.0,
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {(T, E)}")
     out_code = _token_rows(out, "out")
     _enqueue((w_grad, logits, idx, scores_grad, out), stream, "coli_moe_route_groups_bwd", w_grad.data_ptr(),
-             logits.data_ptr(), code, idx.data_ptr(), T, E, k, _score(score), int(norm), scale,
+             logits.data_ptr(), code, idx.data_ptr(), T, E, k, _score(score), 1 if norm else 0, scale,
              None if scores_grad is None else scores_grad.data_ptr(), out.data_ptr(), out_code)
     return out
 
@@ -1030,6 +1040,7 @@ def quantize_fp8_matrix(x, transposed=False, q=None, s=None, qt=None, st=None, s
 @functools.lru_cache(4096)
 def fp8_column_blocks(rows: int, E: int) -> int:
     """The blocks of 128 rows of an expert that quantize_fp8_columns may need."""
+    _small(rows, E)
     out = ctypes.c_int64()
     _check(lib().coli_fp8_column_blocks(rows, E, ctypes.byref(out)))
     return out.value
@@ -1170,8 +1181,8 @@ def fp8_swiglu(a, a_s, table, inter, q_off=0, s_off=0, up_q_off=None, up_s_off=N
         up_q_off = q_off + inter * K
     if up_s_off is None:
         up_s_off = s_off + 4 * _blocks(inter) * _blocks(K)
-    if up_q_off < 0 or up_s_off < 0:
-        raise ValueError("up_q_off and up_s_off must not be negative")
+    if (up_q_off | up_s_off) >> 63:
+        raise ValueError(f"up_q_off {up_q_off} and up_s_off {up_s_off} must be below 2^63 and not negative")
     if dtype == "fp8" or isinstance(out, (tuple, list)):
         if dtype not in (None, "fp8"):
             raise ValueError(f"out is an FP8 pair, dtype {dtype}")
@@ -1230,14 +1241,15 @@ def fp8_wgrad(gt, gt_s, xt, xt_s, offsets=None, rows=None, dtype=None, out=None,
     ws = _new(gt, (nb,), torch.uint8, stream) if nb else None
     _enqueue((gt, gt_s, xt, xt_s, offsets, out, ws), stream, "coli_fp8_wgrad", gt.data_ptr(), gt_s.data_ptr(),
              xt.data_ptr(), xt_s.data_ptr(), blocks, rows, None if offsets is None else offsets.data_ptr(), E, n, K,
-             int(accumulate), out.data_ptr(), code, ld, None if ws is None else ws.data_ptr(), nb)
+             1 if accumulate else 0, out.data_ptr(), code, ld, None if ws is None else ws.data_ptr(), nb)
     return out
 
 
 def debug_fp8_kernel(rows: int, K: int, E: int, N: int, grouped=True, swiglu=False, wide=False) -> str:
     """coli_debug_fp8_kernel: the kernel that a product of these sizes runs."""
+    _small(rows, K, E, N)
     out = ctypes.c_int32()
-    _check(lib().coli_debug_fp8_kernel(rows, K, E, N, int(grouped), int(swiglu), int(wide), ctypes.byref(out)))
+    _check(lib().coli_debug_fp8_kernel(rows, K, E, N, bool(grouped), bool(swiglu), bool(wide), ctypes.byref(out)))
     return FP8_KERNELS[out.value]
 
 

@@ -172,6 +172,26 @@ def test_binding_refusals():
         coli._score("relu")
 
 
+def test_numbers_that_a_c_int_would_cut():
+    """Refused, not taken as their lower 32 (or 64) bits."""
+    import torch
+    x, far = torch.zeros(4, 32), 2 ** 32
+    for how in (dict(groups=far + 2), dict(groups=2, groups_kept=far + 1), dict(group_top=far + 2), dict(groups=2 - far),
+                dict(group_top=-far + 1)):
+        with pytest.raises(ValueError, match="32 bits"):
+            coli.route_groups(x, None, 2, **how)
+    with pytest.raises(ValueError, match="32 bits"):
+        coli.route_groups(x[:0], None, far + 2)
+    with pytest.raises(ValueError, match="32 bits"):
+        coli.fp8_column_blocks(far + 5, 1)
+    with pytest.raises(ValueError, match="32 bits"):
+        coli.fp8_column_blocks(5, far + 1)
+    for sizes in ((far + 8, 64, 1, 64), (8, far + 64, 1, 64), (8, 64, far + 1, 64), (8, 64, 1, far + 64)):
+        with pytest.raises(ValueError, match="32 bits"):
+            coli.debug_fp8_kernel(*sizes, grouped=sizes[2] > 1)
+    assert coli.debug_fp8_kernel(64, 8192, 1, 8192, grouped=far) == coli.debug_fp8_kernel(64, 8192, 1, 8192, grouped=True)
+
+
 def test_reference_codes():
     """The codes against torch's type, the scale rule by its definition."""
     import torch

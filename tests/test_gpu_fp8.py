@@ -430,6 +430,26 @@ def test_not_finite(coli):
             assert torch.equal(y, want)
 
 
+def test_offsets_that_c_would_cut(coli):
+    """Byte offsets and truth values of more bits than the C types have."""
+    import torch
+    rng = np.random.default_rng(10)
+    a, a_s, _ = _rows(rng, 3, 144)
+    _keep, table, _, at = _weights(rng, 1, 32, 144, parts=2)
+    for how in (dict(q_off=2 ** 64 + 16), dict(s_off=2 ** 64 + at["s_off"]), dict(q_off=-16), dict(s_off=-4)):
+        for call in (coli.fp8_matmul, coli.fp8_swiglu):
+            with pytest.raises(ValueError, match="2\\^63"):
+                call(a, a_s, table, 32, **{**at, **how})
+    for how in (dict(up_q_off=2 ** 64), dict(up_s_off=2 ** 64), dict(up_q_off=-16)):
+        with pytest.raises(ValueError, match="2\\^63"):
+            coli.fp8_swiglu(a, a_s, table, 32, **at, **how)
+    gt, gs = coli.quantize_fp8_columns(torch.ones(5, 16, device="cuda"))
+    out = torch.ones(1, 16, 16, device="cuda")
+    assert bool((coli.fp8_wgrad(gt, gs, gt, gs, out=out, accumulate=2 ** 32) == 6.0).all())
+    l = torch.randn(3, 8, device="cuda")
+    assert torch.equal(coli.route_groups(l, None, 2, norm=2 ** 32)[1], coli.route_groups(l, None, 2)[1])
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("rows,K,n", [(40, 144, 33), (40, 512, 33), (5, 640, 4100), (40, 656, 161), (9000, 16, 1300), (700, 640, 1500),
                                       (4500, 1152, 2060), (64, 8208, 8192)])
