@@ -172,6 +172,17 @@ def test_binding_refusals():
         coli._score("relu")
 
 
+def test_current_device_without_torchs_inner_call(monkeypatch):
+    """The calls find the current device with a torch that lacks the inner function."""
+    import torch
+    monkeypatch.delattr(torch._C, "_cuda_getDevice", raising=False)
+    coli._device_call.cache_clear()
+    try:
+        assert coli._device_call() is torch.cuda.current_device
+    finally:
+        coli._device_call.cache_clear()
+
+
 def test_numbers_that_a_c_int_would_cut():
     """Refused, not taken as their lower 32 (or 64) bits."""
     import torch
