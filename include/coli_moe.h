@@ -668,9 +668,12 @@ COLI_API coli_status coli_fp8_wgrad(const uint8_t* d_gt, const uint8_t* d_gs, co
 /* The workspace that coli_fp8_wgrad makes use of for these sizes, 0 where it needs none. Host-only arithmetic. */
 COLI_API coli_status coli_fp8_wgrad_workspace_size(int32_t rows, int32_t E, int32_t N, int32_t K, size_t* bytes);
 
-/* Testing: which kernel a product of these sizes runs (grouped: with d_offsets; wide: f32 results): 0, 1
- * few rows, 16 or 32 matrix rows a workgroup; 2, 3 persistent tiles of 128 or 256 rows. Host-only
- * arithmetic. */
+/* Testing: which kernel a product of these sizes runs without a workspace (grouped: with d_offsets;
+ * wide: exact products, those of f32 results and of FP8 rows below 2^20 values): 0, 1 few rows, 16 or 32
+ * matrix rows a workgroup; 2, 3 persistent tiles of 128 or 256 rows. Where the call makes use of a
+ * workspace it runs tiles of 128 rows over parts of the columns (two parts or more of 4 bytes for each sum
+ * in the workspace's size, 8 of SwiGLU), or few rows as f32 and then a quantiser (4 bytes for each h).
+ * Host-only arithmetic. */
 COLI_API coli_status coli_debug_fp8_kernel(int32_t rows, int32_t K, int32_t E, int32_t N, int32_t grouped,
                                            int32_t swiglu, int32_t wide, int32_t* kernel);
 

@@ -1253,7 +1253,8 @@ def fp8_wgrad(gt, gt_s, xt, xt_s, offsets=None, rows=None, dtype=None, out=None,
 
 
 def debug_fp8_kernel(rows: int, K: int, E: int, N: int, grouped=True, swiglu=False, wide=False) -> str:
-    """coli_debug_fp8_kernel: the kernel that a product of these sizes runs."""
+    """coli_debug_fp8_kernel: the kernel that a product of these sizes runs without a workspace (wide: exact products,
+    of float32 results and of FP8 rows below 2^20 values)."""
     _small(rows, K, E, N)
     out = ctypes.c_int32()
     _check(lib().coli_debug_fp8_kernel(rows, K, E, N, bool(grouped), bool(swiglu), bool(wide), ctypes.byref(out)))

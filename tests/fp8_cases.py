@@ -30,3 +30,15 @@ CASES = [
     ("lines_128", "lines_128", _FULL * 2, 1024, 2056, 1, 1), ("lines_256", "lines_128", 9000, 1536, 1300, 0, 0),
     ("lines_256", "lines_128", [2300, 0, 3700], 2048, 2049, 0, 0), ("lines_256", "lines_128", [256] * 40, 2560, 520, 0, 0),
 ]
+
+# SwiGLU into FP8 rows, by how the sums are formed: (form, rows of every expert, K, inter, rows before and behind). "exact":
+# fewer than 2^20 values, whose tiles take exact products; "parts": columns in parts, with a workspace, whose sums the FP8
+# rows are formed from. K ends inside a block and after one, with one group of scales, several, and a short last one.
+FP8_ROWS = [
+    ("exact tiles", _MANY * 4, 16, 48, 0, 0), ("exact tiles", _FULL, 128, 160, 1, 0), ("exact tiles", _MANY * 2, 144, 144, 0, 0),
+    ("exact tiles", 9000, 384, 112, 0, 0), ("exact tiles", _MANY, 512, 400, 0, 1), ("exact tiles", _MANY * 4, 1040, 80, 2, 3),
+    ("exact tiles", _MANY * 2, 1536, 144, 0, 0), ("exact tiles", [70] * 40, 2576, 272, 0, 0),
+    ("exact parts", 150, 5136, 2064, 0, 0), ("exact parts", [130, 0, 123, 1], 8192, 2064, 3, 4),
+    ("parts", 256, 5136, 4096, 0, 0), ("parts", 256, 8208, 4112, 0, 0), ("parts", 300, 8192, 4112, 0, 0),
+    ("parts", [300, 0, 250], 8192, 2048, 1, 2),
+]

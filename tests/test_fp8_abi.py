@@ -252,6 +252,37 @@ def test_cases_reach_every_kernel():
     assert reached[False] == set(coli.FP8_KERNELS[1:]) and reached[True] == set(coli.FP8_KERNELS[1:3])
 
 
+def test_cases_reach_every_form_of_fp8_rows():
+    """FP8_ROWS reaches the forms that it names, with a K that is a multiple of 512 (scales 16 bytes at a time), one that ends
+    after a block and one that ends inside it; what the workspace is for tells the parts."""
+    from tests.fp8_cases import FP8_ROWS
+    reached = set()
+    for form, counts, K, inter, before, behind in FP8_ROWS:
+        one = isinstance(counts, int)
+        rows, E = (counts, 1) if one else (sum(counts) + before + behind, len(counts))
+        exact = rows * inter < 1 << 20
+        parts, rest = divmod(coli._fp8_swiglu_ws(rows, K, E, inter, not one, coli.FP8), 8 * rows * inter)
+        assert rest == 0 and (form.startswith("exact")) == exact and ("parts" in form) == (parts >= 2)
+        if not parts:
+            assert coli.debug_fp8_kernel(rows, K, E, inter, grouped=not one, swiglu=True, wide=exact) == "lines_128"
+        reached.add((form, "groups" if K % 512 == 0 else "blocks" if K % 128 == 0 else "units"))
+    assert reached >= {(f, k) for f in ("exact tiles", "exact parts", "parts") for k in ("groups", "units")} | {("exact tiles", "blocks")}
+
+
+def test_workspaces_beside_the_named_kernel():
+    """debug_fp8_kernel names the kernel without a workspace, `wide` are exact products; the workspace's size tells what runs
+    with one: parts of the columns, or (few rows into FP8) f32 rows between two launches."""
+    def run(rows, K, E, n, code):
+        wide = code == 0 or (code == coli.FP8 and rows * n < 1 << 20)
+        ws = (coli._fp8_swiglu_ws if code == coli.FP8 else coli._fp8_matmul_ws)(rows, K, E, n, E > 1, code)
+        return coli.debug_fp8_kernel(rows, K, E, n, grouped=E > 1, swiglu=code == coli.FP8, wide=wide), ws // (4 * rows * n)
+
+    assert run(64, 8192, 1, 8192, 1) == ("few_rows_32", 8) and run(256, 6144, 1, 2048, 1)[0] == "few_rows_32"
+    assert run(256, 6144, 1, 2048, 1)[1] >= 2 and run(8, 8192, 1, 8192, 1)[1] == 0
+    assert run(4, 2048, 4, 640, coli.FP8) == ("few_rows_32", 1)          # two launches
+    assert run(127, 8192, 1, 8192, coli.FP8)[1] >= 2 and run(128, 8192, 1, 8192, coli.FP8)[1] >= 2
+
+
 def test_kernel_choice():
     """The choice follows times measured on both sides (graphs, warm caches; us)."""
     def pick(rows, K, E, N, **how):

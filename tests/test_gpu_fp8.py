@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 
 from tests import fp8_refs as ref
-from tests.fp8_cases import CASES
+from tests.fp8_cases import CASES, FP8_ROWS
 
 pytestmark = pytest.mark.gpu
 DTYPES = ("float32", "bfloat16", "float16")
@@ -395,6 +395,12 @@ def test_swiglu(coli, case, dtype, odd):
             assert bool((_scale_of((part - e).clamp_min(0).amax(1)) <= sb).all()) and bool((sb <= _scale_of((part + e).amax(1))).all())
         step = torch.maximum(2.0 ** -4 * (h.abs() + err), 2.0 ** -10 * s.double().repeat_interleave(128, 1)[:, :n])
         assert bool(((_values(q, s) - h).abs() <= err + step)[lo:hi].all())
+
+
+@pytest.mark.parametrize("odd", (0, 4))
+@pytest.mark.parametrize("case", FP8_ROWS, ids=lambda c: f"{c[0].replace(' ', '_')}-{c[2]}-{c[3]}")
+def test_swiglu_forms_of_fp8_rows(coli, case, odd):
+    test_swiglu(coli, ("", "", *case[1:]), "fp8", odd)
 
 
 def test_separate_gate_and_up(coli):
