@@ -557,9 +557,13 @@ COLI_API coli_status coli_debug_mxfp4_kernel(int32_t rows, int32_t K, int32_t E,
  * block's largest |x| to 448 or below, values are x / scale, which is exact, rounded half to
  * even; a block that holds an infinity or a NaN gets scale NaN and codes 0. The products
  * take any scales. A product sums the 128 columns of a block, then the blocks' sums times both
- * scales (multiplied with each other first), in f32. For f32 results the products are exact; for
- * 16-bit and FP8 results the matrix instruction adds 8 products at a time, cut off 2^-13 below
- * the largest exponent among them (1.5e-5 of a sum of normal values). */
+ * scales (multiplied with each other first), in f32. For f32 results the products are exact, and so
+ * they are for FP8 rows where the few-rows kernels run and below 2^20 values (rows * inter). For
+ * 16-bit results and other FP8 rows the matrix instruction adds 8 products at a time, cut off 2^-13
+ * below the largest exponent among them (1.5e-5 of a sum of normal values), parts of sums (with a
+ * workspace) included; one FP8 code in about 4000 differs for it, so that a row's codes may hang on
+ * how many rows there are beside it. 16-bit matrix gradients take the instruction's sums without a
+ * workspace and exact products with one. */
 
 /* Rows d_x [rows][cols] (type dtype, row stride ld elements) to d_q [rows][cols] and d_s
  * [rows][ceil(cols / 128)]. */

@@ -343,7 +343,7 @@ size_t fp8_wgrad_ws(const Fp8WgradArgs& a) {
 coli_status launch_fp8_wgrad(const Fp8WgradArgs& args, int32_t dtype, hipStream_t stream) {
     Fp8WgradArgs a = args;
     a.splits = 1;
-    if (a.ws) {
+    if (a.ws) {                                  // (f32 sums of exact products whatever the type, as they are stored)
         a.splits = wgrad_splits(a);
         a.dw = a.ws;
         a.ld = a.K;
