@@ -659,7 +659,9 @@ COLI_API coli_status coli_fp8_swiglu_workspace_size(int32_t rows, int32_t K, int
 /* Every expert's matrix gradient: d_dw[e][n][k] = sum over the expert's rows r of g[r][n] x[r][k] (0
  * without rows), for g [rows][N] and x [rows][K] (N, K multiples of 16) as coli_quantize_fp8_columns
  * lays them out with the same rows, d_offsets, E and blocks (scales 4-byte aligned). d_dw [E][N][ld] of type dtype, ld >= K;
- * accumulate: the sums are added to what it holds. Sums as the products'. d_ws (nullable, 16-byte aligned): a
+ * accumulate: the sums are added to what it holds. Sums as the products'; for exact ones the values are
+ * rounded to multiples of 2^-133, which all are already but those of the two smallest scales, 2^-126 and
+ * 2^-125 (a block of nothing above 1e-35). d_ws (nullable, 16-byte aligned): a
  * workspace of coli_fp8_wgrad_workspace_size's bytes, with which many rows of few small matrices are several times
  * as fast (parts of the rows are summed by themselves, in f32, and then together); smaller ones are not used. It needs no
  * initialisation, and calls that run at the same time (two graphs' too) need one each. */

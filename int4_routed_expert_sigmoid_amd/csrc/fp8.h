@@ -65,7 +65,8 @@ __device__ __forceinline__ i32x8 words8(const Frag& f) {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-// The values of 8 codes times a power of two: exact in bf16.
+// The values of 8 codes times a power of two: exact in bf16 from 2^-124 on. Below, the two smallest scales that there are
+// (values whose block has nothing above 1e-35) go past bf16's smallest step, 2^-133, to which they are rounded.
 __device__ __forceinline__ bf16x8 bf16_of(uint32_t a, uint32_t b, float scale) {
     const bf16x2 x = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, false);
     const bf16x2 y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, true);

@@ -626,6 +626,28 @@ def test_wgrad(coli, counts, n, K, dtype):
     assert torch.equal(buf[..., :K], got)
 
 
+@pytest.mark.parametrize("size", (1e-30, 1e-35, 1e-36, 1e-38, 1e-39))
+def test_wgrad_of_the_smallest_scales(coli, size):
+    """Gradients next to the smallest numbers: exact from a scale of 2^-124 on, below rounded to multiples of 2^-133 in f32
+    results, half of that off at most, times the other operand; the FP8 instruction takes the scales as they are."""
+    import torch
+    rng = np.random.default_rng(15)
+    rows, n, K = 300, 32, 144
+    x = 1e8 * rng.standard_normal((rows, K))
+    g = size * rng.standard_normal((rows, n))
+    cols = [coli.quantize_fp8_columns(_dev(t.astype(np.float32))) for t in (g, x)]
+    vals = [ref.column_values(q.cpu().numpy(), s.cpu().numpy().astype(np.int64)) for q, s in cols]
+    want, terms = vals[0] @ vals[1].T, np.abs(vals[0]) @ np.abs(vals[1]).T
+    code = cols[0][1].cpu().numpy()
+    assert code.max() < 3 if size < 5e-36 else code.min() >= 3
+    lost = 0.0 if size >= 5e-36 else 2.0 ** -134 * np.abs(vals[1]).sum(1)
+    for dtype in ("float32", "bfloat16"):
+        exact = dtype == "float32"
+        got = _host(coli.fp8_wgrad(*cols[0], *cols[1], rows=rows, dtype=_t(dtype))[0])
+        tol = ref.product_bound(rows, terms, exact) + (lost if exact else 0.0)
+        assert (np.abs(got - want) <= tol * (1 + _half_step(dtype)) + _rounding(dtype, want)).all()
+
+
 def test_wgrad_parts(coli):
     """Rows summed in parts (with a workspace) and at once (without) agree, NaN included, and repeat bit for bit. f32: about
     160 additions of 32 products each round by 2^-25 of sums that do not exceed the largest result by much, 13 * 2^-25 as
