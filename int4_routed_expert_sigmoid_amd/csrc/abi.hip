@@ -256,7 +256,7 @@ coli_status coli_moe_route_topp(const float* d_logits, const float* d_bias, int3
 static coli_status check_route_groups(const std::string& w, int32_t dtype, int32_t T, int32_t E, int32_t k,
                                       int32_t score, float scale) {
     if (T < 0 || E <= 0 || k <= 0 || k > E) return fail(COLI_EINVAL, w + ": need T >= 0 and 1 <= k <= E");
-    if (E > 1024 || k > 32) return fail(COLI_EUNSUPPORTED, w + ": E <= 1024 and k <= 32");
+    if (E > kRouteMaxExperts || k > kRouteMaxSlots) return fail(COLI_EUNSUPPORTED, w + ": E <= 1024 and k <= 32");
     if (!elem_dtype(dtype)) return fail(COLI_EUNSUPPORTED, w + ": dtype must be f32, bf16 or f16");
     if (score != COLI_SCORE_SIGMOID && score != COLI_SCORE_SOFTMAX)
         return fail(COLI_EINVAL, w + ": score must be sigmoid or softmax");
@@ -273,7 +273,7 @@ coli_status coli_moe_route_groups(const void* d_logits, int32_t dtype, const flo
     coli_status st = check_route_groups("route_groups", dtype, T, E, k, score, scale);
     if (st) return st;
     if (n_groups < 1 || E % n_groups) return fail(COLI_EINVAL, "route_groups: n_groups must divide E");
-    if (n_groups > 64) return fail(COLI_EUNSUPPORTED, "route_groups: n_groups <= 64");
+    if (n_groups > kRouteMaxGroups) return fail(COLI_EUNSUPPORTED, "route_groups: n_groups <= 64");
     if (groups_kept < 1 || groups_kept > n_groups || k > groups_kept * (E / n_groups))
         return fail(COLI_EINVAL, "route_groups: the groups kept must be at most n_groups and hold k experts");
     if (group_top != 1 && group_top != 2) return fail(COLI_EINVAL, "route_groups: group_top must be 1 or 2");

@@ -23,8 +23,8 @@ __device__ __forceinline__ int fp8_scale_code(uint32_t top_bits) {
     return max((int)(top_bits >> 23) - 8 + ((top_bits & 0x7fffffu) > 0x600000u ? 1 : 0), 1);
 }
 
-// The scale and its inverse: NaN, and 0 (which turns every value but the infinities and NaNs
-// into code 0; those need fp8_codes' `bad`), for code 255.
+// The scale and its inverse: NaN, and 0 (for which fp8_codes4 gives codes 0, also of infinities and NaNs), for
+// code 255.
 __device__ __forceinline__ float fp8_scale_value(int code) {
     return __uint_as_float(code == 255 ? 0x7fc00000u : (uint32_t)code << 23);
 }

@@ -5,6 +5,10 @@
 
 namespace coli {
 
+constexpr int kRouteMaxExperts = 1024;           // 16 a lane
+constexpr int kRouteMaxSlots = 32;
+constexpr int kRouteMaxGroups = 64;              // one a lane, a bit each in a 64-bit word
+
 struct RouteArgs {
     const void* logits;          // [T][E]
     const float* bias;           // [E] or nullptr

@@ -23,7 +23,6 @@ namespace coli {
 namespace {
 
 constexpr int kThreads = 256, kTokens = kThreads / 64;
-constexpr int kMaxGroups = 64;
 
 template <int S>
 __device__ __forceinline__ float fmax_step(float v) { return fmaxf(v, __int_as_float(lane_xchg<S>(__float_as_int(v)))); }
