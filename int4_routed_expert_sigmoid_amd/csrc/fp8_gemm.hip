@@ -15,7 +15,8 @@
 //  - many rows: the matrix unit, in which a block of a tile takes 1.2 us of the 1.73 that it takes altogether. What
 //    keeps the rest: a tile of 256 by 256 brings in 64 KB a block, 1.8 us at a CU's rate if nothing hits a cache
 //    near by; and the four scalings of a product share the issue slots with the matrix instructions. 8191 x 8192 x
-//    8192 into bf16: 450 us, 2.44 PFLOP/s; of these 16 go if every load hits the L2 cache, 60 with no loads.
+//    8192 into bf16: 446 to 474 us on several cards, 2.3 to 2.5 PFLOP/s; of 460 on one of them 16 go if every load
+//    hits the L2 cache, 63 with no loads.
 //  - SwiGLU of all of 256 experts of 2048 x 6144, 6.4 GB: 1.19 ms (5.6 TB/s) for 1 to 8 rows an expert and more.
 #include <algorithm>
 #include <cmath>
@@ -25,8 +26,8 @@
 namespace coli {
 namespace {
 
-// FP8 rows as an output type of the SwiGLU epilogue, and f32 rows on their way there, or parts of sums on their way
-// to 16 bits (products by the FP8 instruction, as the results').
+// FP8 rows as an output type of the SwiGLU epilogue; f32 rows on their way there (few_rows: exact products), or parts
+// of sums on their way to 16 bits or to kFewValues FP8 values and more (tiles: the FP8 instruction's, as without parts).
 struct Fp8Out {};
 struct RawOut {};
 
