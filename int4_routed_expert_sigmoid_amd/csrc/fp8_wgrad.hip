@@ -7,7 +7,7 @@
 // registers from block to block.
 //
 // What bounds it: the gradients that it writes where experts have few rows (64 experts of 2048 x 6144, 256 rows
-// each, one MI355X, repeated by itself: 3.2 GB of f32 in 710 to 780 us, 4.1 to 4.5 TB/s, added to what is there 1206
+// each, one MI355X, repeated by itself: 3.2 GB of f32 in 710 to 820 us, 3.9 to 4.5 TB/s, added to what is there 1206
 // to 1244, 5.2 TB/s; bf16 384 to 417 and 773 to 782; in a pass behind the rows' gradient the f32 one takes 940),
 // the bf16 matrix instructions where there are many and results have 32 bits (6144 x 8192 from 4095 rows, 0.41
 // TFLOP: 337 us, 1.22 PFLOP/s, where a large bf16 product reaches 1.34; bf16 162, 2.5 PFLOP/s).
