@@ -36,7 +36,8 @@ struct RawOut {};
 // values that is 1e-3 of a layer's output (509 tokens of 256 experts: 2.6e-3 off the 64-bit form, with exact sums
 // 2.4e-3, bf16's own rounding), but of a few thousand a single large one can show (26 tokens, inter 288: 6.3e-3).
 // Below kFewValues, and wherever few_rows runs (whose time is the matrices' bytes), FP8 rows therefore take exact
-// products; above, the tiles' blocks would take 1.85 us in place of 1.03.
+// products; above, the tiles' blocks would take 1.85 us in place of 1.03 (SwiGLU of 256 of 2048 x 6144, 16384 rows 1690
+// in place of 1180, 8192 rows of one 349 / 185, the layer of 509 tokens 1373 / 1050).
 struct ExactFp8Out {};
 constexpr int64_t kFewValues = 1 << 20;
 
